@@ -20,7 +20,7 @@ own = False
 
 NQ, NKV, HD, BLK = 16, 8, 128, 64
 QKV = (NQ + 2 * NKV) * HD
-TILE = BLK * HD // 2 + BLK * 8          # 4-bit codes of 64 tokens, then (scale, middle) of 2 groups a token
+TILE = BLK * HD // 2 + BLK * 8          # 4-bit codes of 64 tokens, then (scale, offset) of 2 groups a token
 IO = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
@@ -116,37 +116,39 @@ def work(case):
 
 # ------------------------------------------------------------------ the 4-bit cache's format
 def _unpack(pool):
-    """uint8 [..., TILE] tiles -> codes [..., 64 tokens, 2 groups, 64] (float32), scale and middle [..., 64, 2] (float32).
+    """uint8 [..., TILE] tiles -> the values they stand for, float32 [..., 64 tokens, 128].
 
     A token's 64 code bytes are 16 words; word w holds 8 dims of group w & 1, dims 64 (w & 1) + 8 (w >> 1) + i in
-    nibble i; its parameters are two (fp16 scale, fp16 middle) pairs behind the tile's codes."""
+    nibble i. Behind the tile's codes stand two (bf16 scale, bf16 offset) pairs a token, one for each group of 64
+    dims; a value is scale * (code + offset + 128)."""
     head = pool.shape[:-1]
     codes = pool[..., : BLK * HD // 2].reshape(*head, BLK, 8, 2, 4)
     codes = torch.stack((codes & 15, codes >> 4), -1).reshape(*head, BLK, 8, 2, 8)
     codes = codes.transpose(-3, -2).reshape(*head, BLK, 2, HD // 2)
-    par = pool[..., BLK * HD // 2 :].contiguous().view(torch.float16).reshape(*head, BLK, 2, 2).float()
-    return codes.float(), par[..., 0], par[..., 1]
+    par = pool[..., BLK * HD // 2 :].contiguous().view(torch.bfloat16).reshape(*head, BLK, 2, 2, 1).float()
+    return (par[..., 0, :] * (codes.float() + (par[..., 1, :] + 128))).flatten(-2)
 
 
 def _quantise(x):
-    """[..., 128] -> codes 0..15 [..., 2, 64], scale and middle [..., 2, 1], all in x's type: the scale is 1/15 of a
-    group's range and the middle the value of code 8, both rounded to fp16."""
+    """[..., 128] -> whole numbers 0..15 [..., 2, 64], scale and offset [..., 2, 1], all in x's type: the scale is a
+    15th of a group's range (at least a 120th of its largest magnitude), rounded to bf16; codes count scales upward
+    from the whole number next to the group's lowest value, and the offset is that number less 128."""
     x = x.reshape(*x.shape[:-1], 2, HD // 2)
     lo, hi = x.amin(-1, keepdim=True), x.amax(-1, keepdim=True)
-    scale = ((hi - lo) / 15).half().to(x.dtype)
-    mid = (lo + 8 * scale).half().to(x.dtype)
-    code = torch.where(scale > 0, torch.round((x - mid) / scale.clamp(min=1e-30)) + 8, torch.full_like(x, 8.0)).clamp(0, 15)
-    return code, scale, mid
+    scale = torch.maximum((hi - lo) / 15, torch.maximum(hi, -lo) / 120).float().bfloat16().to(x.dtype)
+    safe = torch.where(scale > 0, scale, torch.ones_like(scale))
+    zero = torch.round(lo / safe)
+    return (torch.round(x / safe) - zero).clamp(0, 15), scale, zero - 128
 
 
 def _tiles(x):
     """float [..., 64 tokens, 128] -> uint8 [..., TILE]."""
-    code, scale, mid = _quantise(x)
+    code, scale, offset = _quantise(x)
     head = x.shape[:-2]
     c = code.to(torch.uint8).reshape(*head, BLK, 2, 8, 8).transpose(-3, -2)
     c = c.reshape(*head, BLK, 8, 2, 4, 2)
     c = (c[..., 0] | (c[..., 1] << 4)).reshape(*head, BLK * HD // 2)
-    par = torch.cat((scale, mid), -1).half().contiguous().view(torch.uint8).reshape(*head, BLK * 8)
+    par = torch.cat((scale, offset), -1).bfloat16().contiguous().view(torch.uint8).reshape(*head, BLK * 8)
     return torch.cat((c, par), -1)
 
 
@@ -265,8 +267,8 @@ def _plain_append(s):
     v = x[:, NQ + NKV :].double()
     held = []
     for y in (k, v):
-        code, scale, mid = _quantise(y)
-        held.append((mid.float() + scale.float() * (code.float() - 8)).reshape(T, NKV, HD))
+        code, scale, offset = _quantise(y)
+        held.append((scale * (code + (offset + 128))).reshape(T, NKV, HD))
     rows = on[:, None, None]
     q, k, v = (torch.where(rows, y, torch.zeros_like(y)) for y in (q, *held))
     return {"q": q.to(s["q"].dtype), "k": k.bfloat16(), "v": v.bfloat16()}
@@ -274,9 +276,7 @@ def _plain_append(s):
 
 def _plain_attend(s):
     B, S = s["seqs"], s["tokens"]
-    codes, scale, mid = _unpack(s["pool"][s["table"].long()])      # [B, nb, 2, 8, 64, 2, 64]
-    x = (mid[..., None] + scale[..., None] * (codes - 8)).flatten(-2)
-    del codes
+    x = _unpack(s["pool"][s["table"].long()])                       # [B, nb, 2, 8, 64, 128]
     x = x.permute(2, 0, 3, 1, 4, 5).reshape(2, B, NKV, -1, HD)      # [2, B, 8, L, 128]
     q = s["q"].float().reshape(B, S, NKV, 2, HD).transpose(1, 2).reshape(B, NKV, S * 2, HD)
     z = q @ x[0].transpose(-1, -2) / math.sqrt(HD)                  # [B, 8, S * 2, L]
@@ -384,12 +384,11 @@ def _exact_append(s):
         out = torch.empty_like(y)
         for half in (slice(0, HD // 2), slice(HD // 2, HD)):
             p = y[..., half]
-            low = p.min(-1).values
-            step = ((p.max(-1).values - low) / 15).to(torch.float16).double()
-            middle = (low + 8 * step).to(torch.float16).double()
-            safe = torch.where(step == 0, torch.ones_like(step), step)
-            c = torch.clamp(torch.round((p - middle[..., None]) / safe[..., None]), -8, 7)
-            out[..., half] = middle[..., None] + step[..., None] * c
+            low, high = p.min(-1).values, p.max(-1).values
+            step = torch.max((high - low) / 15, p.abs().max(-1).values / 120).to(torch.float32).to(torch.bfloat16).double()
+            safe = torch.where(step == 0, torch.ones_like(step), step)[..., None]
+            first = torch.round(low[..., None] / safe)
+            out[..., half] = step[..., None] * torch.minimum(torch.round(p / safe), first + 15)
         return out
 
     q[live] = rotate(x[:, : NQ * HD].view(-1, NQ, HD), s["gq"])
@@ -405,15 +404,15 @@ def _exact_attend(s):
     for b, n in enumerate(s["lens"].tolist()):
         blocks = s["pool"][s["table"][b, : -(-n // BLK)].long()]
         words = blocks[..., : BLK * HD // 2].reshape(-1, 2, NKV, BLK, HD // 2)
-        par = blocks[..., BLK * HD // 2 :].contiguous().view(torch.float16).reshape(-1, 2, NKV, BLK, 2, 2).double()
+        par = blocks[..., BLK * HD // 2 :].contiguous().view(torch.bfloat16).reshape(-1, 2, NKV, BLK, 2, 2).double()
         kv = torch.empty(2, NKV, len(blocks) * BLK, HD, dtype=torch.float64, device="cuda")
         for byte in range(HD // 2):
             w, t = byte // 4, byte % 4
-            scale, mid = (par[..., w % 2, j].permute(1, 2, 0, 3).reshape(2, NKV, -1) for j in (0, 1))
+            scale, off = (par[..., w % 2, j].permute(1, 2, 0, 3).reshape(2, NKV, -1) for j in (0, 1))
             col = words[..., byte].permute(1, 2, 0, 3).reshape(2, NKV, -1)
             d = 64 * (w % 2) + 8 * (w // 2) + 2 * t
-            kv[..., d] = mid + scale * ((col % 16).double() - 8)
-            kv[..., d + 1] = mid + scale * ((col // 16).double() - 8)
+            kv[..., d] = scale * ((col % 16).double() + off + 128)
+            kv[..., d + 1] = scale * ((col // 16).double() + off + 128)
         for i in range(S):
             see = n - (S - 1 - i)
             if see > 0:
