@@ -47,6 +47,11 @@ class tts_bb_opts(C.Structure):
     _fields_ = [("embeds", C.c_void_p), ("hidden_out", C.c_void_p), ("argmax_stride", C.c_int)]
 
 
+class tts_bb_kv4(C.Structure):
+    _fields_ = [("pool", C.c_void_p), ("page_table", C.c_void_p), ("err", C.c_void_p), ("n_blocks", C.c_int),
+                ("n_seqs", C.c_int), ("blocks_per_seq", C.c_int)]
+
+
 class TtsBbError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {msg}")
@@ -107,6 +112,16 @@ def _load() -> C.CDLL:
         "tts_bb_dac_decode": (I, [P, I, I, P, P]),
         "tts_bb_dac_sync": (I, [P]),
         "tts_bb_dac_free": (V, [P]),
+        "tts_bb_rope_tables": (I, [C.c_double, I, P, P]),
+        "tts_bb_kv4_append": (I, [C.POINTER(tts_bb_kv4), I, P, I, C.c_int64, P, P, C.c_float, P, P, I, P, P, P, I, P]),
+        "tts_bb_kv4_read": (I, [C.POINTER(tts_bb_kv4), I, P, P, P, P, P]),
+        "tts_bb_kv4_attention_workspace": (C.c_size_t, [I, I, I]),
+        "tts_bb_kv4_attention": (I, [C.POINTER(tts_bb_kv4), I, I, P, I, P, P, I, P, P, C.c_size_t, P]),
+        "tts_bb_w4_packed_bytes": (C.c_size_t, [I, I, I]),
+        "tts_bb_w4_pack": (I, [I, I, I, P, P, P, P, P]),
+        "tts_bb_w4_linear": (I, [I, I, I, I, P, I, C.c_int64, P, P, P]),
+        "tts_bb_token_logprobs_workspace": (C.c_size_t, [I, I, I]),
+        "tts_bb_token_logprobs": (I, [I, I, P, I, C.c_int64, P, P, C.c_int64, I, P, P, P, P, P, P, C.c_size_t, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -124,7 +139,9 @@ EXPORTED = ("tts_bb_default_config", "tts_bb_create", "tts_bb_free", "tts_bb_pre
             "tts_bb_maskgit_schedule", "tts_bb_frame_step", "tts_bb_rvq_create", "tts_bb_rvq_decode",
             "tts_bb_rvq_sync", "tts_bb_rvq_free", "tts_bb_dac_create", "tts_bb_dac_decode", "tts_bb_dac_sync", "tts_bb_dac_free",
             "tts_bb_decode_step_host", "tts_bb_quantizer_create", "tts_bb_quantizer_decode",
-            "tts_bb_quantizer_sync", "tts_bb_quantizer_free")
+            "tts_bb_quantizer_sync", "tts_bb_quantizer_free", "tts_bb_rope_tables", "tts_bb_kv4_append",
+            "tts_bb_kv4_read", "tts_bb_kv4_attention_workspace", "tts_bb_kv4_attention", "tts_bb_w4_packed_bytes",
+            "tts_bb_w4_pack", "tts_bb_w4_linear", "tts_bb_token_logprobs_workspace", "tts_bb_token_logprobs")
 
 
 def _ptr(x) -> Optional[int]:
@@ -404,3 +421,142 @@ def tts_bb_gqa_decode_attention_static(q, kv_pool, page_table, blocks_per_seq: i
     return lib.tts_bb_gqa_decode_attention_static(_ptr(q), _ptr(kv_pool), _ptr(page_table), blocks_per_seq,
                                                   _ptr(positions), B, max_position, _ptr(out),
                                                   C.c_void_p(stream or None))
+
+
+# ---------------------------------------------------------------- low-bit decode operators
+# Device tensors with a dtype and strides (torch CUDA tensors); each call returns its status, or raises TtsBbError
+# with check=True. Shapes, types and strides are checked here, values by the library.
+T_F32, T_BF16, T_F16 = 0, 1, 2
+_TYPES = {"torch.float32": T_F32, "torch.bfloat16": T_BF16, "torch.float16": T_F16}
+KV4_TILE_BYTES, KV4_BLOCK_BYTES, KV4_MAX_QUERIES, W4_MAX_TOKENS, LOGPROBS_MAX_TOP = 4608, 73728, 64, 64, 32
+KV4_ERR_PAGE, KV4_ERR_RANGE = 1, 2
+
+
+def _arg(x, name: str, types, n: int, rows: bool = False):
+    """Address of a device tensor of at least n elements of one of the types; contiguous unless rows (then only
+    its last dimension has to be)."""
+    if x is None:
+        return None
+    if str(x.dtype) not in types or not x.is_cuda:
+        raise TypeError(f"{name}: a CUDA tensor of {' or '.join(types)} is wanted, not {x.dtype} on {x.device}")
+    if not (x.is_contiguous() or (rows and x.dim() == 2 and x.stride(1) == 1)):
+        raise ValueError(f"{name}: strides {tuple(x.stride())} of shape {tuple(x.shape)} are not supported")
+    if x.numel() < n:
+        raise ValueError(f"{name}: {n} elements are wanted, not {x.numel()}")
+    return x.data_ptr()
+
+
+_I32, _F32, _BF16, _U8 = ("torch.int32",), ("torch.float32",), ("torch.bfloat16",), ("torch.uint8",)
+_IO = ("torch.float32", "torch.bfloat16")
+
+
+def _status(st: int, name: str, check: bool) -> int:
+    if check and st != OK:
+        raise TtsBbError(st, name)
+    return st
+
+
+class Kv4Cache:
+    """A paged 4-bit KV cache on the caller's tensors (kept alive): pool uint8 of n_blocks * KV4_BLOCK_BYTES,
+    page_table int32 [n_seqs][blocks_per_seq], err an int32 word for device-side errors, or None."""
+
+    def __init__(self, pool, page_table, err=None):
+        self.pool, self.page_table, self.err = pool, page_table, err
+        if page_table.dim() != 2:
+            raise ValueError("page_table: two dimensions are wanted")
+        n = pool.numel() // KV4_BLOCK_BYTES
+        self.struct = tts_bb_kv4(_arg(pool, "pool", _U8, KV4_BLOCK_BYTES), _arg(page_table, "page_table", _I32, 1),
+                                 _arg(err, "err", _I32, 1), n, *page_table.shape)
+        self.ref = C.byref(self.struct)
+
+
+def tts_bb_rope_tables(theta: float, n_pos: int):
+    """Host (cos, sin) tables, float32 [n_pos][64]."""
+    c, s = (np.zeros((max(n_pos, 0), 64), np.float32) for _ in range(2))
+    st = lib.tts_bb_rope_tables(theta, n_pos, _ptr(c), _ptr(s))
+    if st != OK:
+        raise TtsBbError(st, "tts_bb_rope_tables: bad arguments")
+    return c, s
+
+
+def tts_bb_kv4_append(cache: Kv4Cache, T: int, qkv, q_norm, k_norm, cos_table, sin_table, n_pos: int, seqs, positions,
+                      q_out=None, eps: float = 1e-6, stream: int = 0, check: bool = True) -> int:
+    """qkv: [T][4096] fp32 or bf16 (rows may be strided); q_out: [T][16][128] fp32 or bf16, or None."""
+    stride = qkv.stride(0) if qkv.dim() == 2 and T > 1 else 4096
+    st = lib.tts_bb_kv4_append(
+        cache.ref, T, _arg(qkv, "qkv", _IO, T * 4096, True), _TYPES[str(qkv.dtype)], stride,
+        _arg(q_norm, "q_norm", _BF16, 128), _arg(k_norm, "k_norm", _BF16, 128), eps,
+        _arg(cos_table, "cos_table", _F32, n_pos * 64), _arg(sin_table, "sin_table", _F32, n_pos * 64), n_pos,
+        _arg(seqs, "seqs", _I32, T), _arg(positions, "positions", _I32, T), _arg(q_out, "q_out", _IO, T * 2048),
+        T_F32 if q_out is None else _TYPES[str(q_out.dtype)], stream or None)
+    return _status(st, "tts_bb_kv4_append", check)
+
+
+def tts_bb_kv4_read(cache: Kv4Cache, T: int, seqs, positions, k_out, v_out, stream: int = 0, check: bool = True) -> int:
+    """k_out, v_out: bf16 [T][8][128]."""
+    st = lib.tts_bb_kv4_read(cache.ref, T, _arg(seqs, "seqs", _I32, T), _arg(positions, "positions", _I32, T),
+                             _arg(k_out, "k_out", _BF16, T * 1024), _arg(v_out, "v_out", _BF16, T * 1024), stream or None)
+    return _status(st, "tts_bb_kv4_read", check)
+
+
+def tts_bb_kv4_attention_workspace(B: int, S: int, max_len: int) -> int:
+    return lib.tts_bb_kv4_attention_workspace(B, S, max_len)
+
+
+def tts_bb_kv4_attention(cache: Kv4Cache, B: int, S: int, q, kv_lens, max_len: int, out, workspace=None, seqs=None,
+                         stream: int = 0, check: bool = True) -> int:
+    """q, out: [B][S][16][128], both fp32 or both bf16; workspace: a uint8 tensor, or None where none is needed."""
+    if q.dtype != out.dtype:
+        raise TypeError(f"q and out have to be of one type, not {q.dtype} and {out.dtype}")
+    st = lib.tts_bb_kv4_attention(
+        cache.ref, B, S, _arg(q, "q", _IO, B * S * 2048), _TYPES[str(q.dtype)], _arg(seqs, "seqs", _I32, B),
+        _arg(kv_lens, "kv_lens", _I32, B), max_len, _arg(out, "out", _IO, B * S * 2048),
+        _arg(workspace, "workspace", _U8, 0), 0 if workspace is None else workspace.numel(), stream or None)
+    return _status(st, "tts_bb_kv4_attention", check)
+
+
+def tts_bb_w4_packed_bytes(N: int, K: int, group: int) -> int:
+    return lib.tts_bb_w4_packed_bytes(N, K, group)
+
+
+def tts_bb_w4_pack(N: int, K: int, group: int, codes, scales, zeros, packed, stream: int = 0, check: bool = True) -> int:
+    """codes uint8 [N][K / 2], scales bf16 [N][K / group], zeros uint8 [N][K / group] or None -> packed uint8."""
+    n = N * (K // group) if group > 0 else 0
+    st = lib.tts_bb_w4_pack(N, K, group, _arg(codes, "codes", _U8, N * K // 2), _arg(scales, "scales", _BF16, n),
+                            _arg(zeros, "zeros", _U8, n),
+                            _arg(packed, "packed", _U8, tts_bb_w4_packed_bytes(N, K, group)), stream or None)
+    return _status(st, "tts_bb_w4_pack", check)
+
+
+def tts_bb_w4_linear(T: int, N: int, K: int, group: int, x, packed, y, stream: int = 0, check: bool = True) -> int:
+    """x: [T][K] (rows may be strided), y: [T][N], both fp32 or both bf16."""
+    if x.dtype != y.dtype:
+        raise TypeError(f"x and y have to be of one type, not {x.dtype} and {y.dtype}")
+    st = lib.tts_bb_w4_linear(T, N, K, group, _arg(x, "x", _IO, T * K, True), _TYPES[str(x.dtype)],
+                              x.stride(0) if x.dim() == 2 and T > 1 else K,
+                              _arg(packed, "packed", _U8, tts_bb_w4_packed_bytes(N, K, group)), _arg(y, "y", _IO, T * N),
+                              stream or None)
+    return _status(st, "tts_bb_w4_linear", check)
+
+
+def tts_bb_token_logprobs_workspace(R: int, V: int, n_top: int) -> int:
+    return lib.tts_bb_token_logprobs_workspace(R, V, n_top)
+
+
+def tts_bb_token_logprobs(R: int, V: int, logits, targets=None, n_top: int = 0, logprob=None, entropy=None, lse=None,
+                          top_ids=None, top_logprobs=None, allowed=None, workspace=None, stream: int = 0,
+                          check: bool = True) -> int:
+    """logits: [R][>= V] fp32, bf16 or fp16 (rows may be strided); allowed: uint32 or int32 words, [words] for all
+    rows or [R][words]."""
+    stride = logits.stride(0) if logits.dim() == 2 and R > 1 else V
+    words = (V + 31) // 32
+    a_rows = allowed is not None and allowed.dim() == 2
+    st = lib.tts_bb_token_logprobs(
+        R, V, _arg(logits, "logits", tuple(_TYPES), R * V, True), _TYPES[str(logits.dtype)], stride,
+        _arg(targets, "targets", _I32, R),
+        _arg(allowed, "allowed", ("torch.uint32", "torch.int32"), words * (R if a_rows else 1), True),
+        allowed.stride(0) if a_rows and R > 1 else 0, n_top, _arg(logprob, "logprob", _F32, R), _arg(entropy, "entropy", _F32, R),
+        _arg(lse, "lse", _F32, R), _arg(top_ids, "top_ids", _I32, R * n_top),
+        _arg(top_logprobs, "top_logprobs", _F32, R * n_top), _arg(workspace, "workspace", _U8, 0),
+        0 if workspace is None else workspace.numel(), stream or None)
+    return _status(st, "tts_bb_token_logprobs", check)

@@ -1,0 +1,467 @@
+// Paged KV cache held in 4 bits: append (q/k RMSNorm, half-rotate RoPE, quantisation), read-back and
+// grouped-query attention (16 query heads, 8 KV heads of 128), all on the caller's buffers.
+//
+// Format. A cache block holds K then V of 64 tokens for the 8 KV heads as 16 tiles of 4608 bytes. A
+// tile: 64 code rows of 64 bytes, then 64 parameter rows of 8 bytes. The 128 dims of a token's head are
+// two groups of 64 (dims 0..63 and 64..127, the two halves that RoPE pairs). Word w of a code row holds
+// dims 64 (w & 1) + 8 (w >> 1) + i in nibble i, so that both 8-byte pieces (V: one piece a lane) and
+// 16-byte pieces (K: one piece a lane) carry both groups. A parameter row: (bf16 scale, bf16 offset) of
+// each group, value = scale * (code + 128 + offset). The offset is a whole number, -249 .. -7, so code +
+// 128 + offset is a whole number below 256 in magnitude: exact in bf16, which is what the tensor cores
+// of the attention take.
+//
+// Quantisation of a group x[64]: scale = bf16(max((hi - lo) / 15, max|x| / 120)), zero = rint(lo / scale),
+// code = clamp(rint(x / scale) - zero, 0, 15), offset = zero - 128. The second term bounds zero by 121.
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "../../include/tts_bb.h"
+
+#define TTS_API extern "C" __attribute__((visibility("default")))
+
+using namespace ttsbb;
+
+namespace {
+
+constexpr int TILE = TTS_BB_KV4_TILE_BYTES;
+constexpr size_t BLOCK = TTS_BB_KV4_BLOCK_BYTES;
+constexpr int PAR = KVB * HD / 2;  // byte offset of a tile's parameter rows
+static_assert(TILE == PAR + KVB * 8 && BLOCK == (size_t)2 * NKV * TILE, "tile layout");
+constexpr float LOG2E = 1.4426950408889634f;
+
+struct Cache {
+    uint8_t* pool;
+    const int32_t* table;
+    int32_t* err;
+    int n_blocks, n_seqs, bps;
+};
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const bf16* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store4(float* p, const float* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store4(bf16* p, const float* x) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// The block of (sequence row, position), or -1 with the reason in *err.
+__device__ __forceinline__ int find_block(const Cache& c, int seq, int pos, bool report) {
+    if (seq >= c.n_seqs || pos < 0 || pos / KVB >= c.bps) {
+        if (report) set_err(c.err, TTS_BB_KV4_ERR_RANGE);
+        return -1;
+    }
+    const int p = c.table[(size_t)seq * c.bps + pos / KVB];
+    if (p < 0 || p >= c.n_blocks) {
+        if (report) set_err(c.err, TTS_BB_KV4_ERR_PAGE);
+        return -1;
+    }
+    return p;
+}
+
+// ---------------------------------------------------------------- append
+// Codes and parameters of one head of one token; lane l holds dims 4l .. 4l + 3 (lanes 0..15 group 0).
+struct Quant {
+    uint32_t codes;  // 4 nibbles
+    uint32_t par;    // bf16 scale | bf16 offset << 16
+};
+
+template <typename F>
+__device__ __forceinline__ F half_min(F v) {
+#pragma unroll
+    for (int o = 8; o; o >>= 1) { const F w = __shfl_xor_sync(0xffffffffu, v, o); v = w < v ? w : v; }
+    return v;
+}
+template <typename F>
+__device__ __forceinline__ F half_max(F v) {
+#pragma unroll
+    for (int o = 8; o; o >>= 1) { const F w = __shfl_xor_sync(0xffffffffu, v, o); v = w > v ? w : v; }
+    return v;
+}
+__device__ __forceinline__ uint32_t bf_bits(float x) { return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+
+// The definition in 64 bits.
+__device__ __noinline__ Quant quant64(const double* x) {
+    const double lo = half_min(fmin(fmin(x[0], x[1]), fmin(x[2], x[3])));
+    const double hi = half_max(fmax(fmax(x[0], x[1]), fmax(x[2], x[3])));
+    const uint32_t sb = bf_bits((float)fmax((hi - lo) / 15.0, fmax(hi, -lo) / 120.0));
+    const double s = (double)__uint_as_float(sb << 16);
+    Quant q{0u, sb};
+    double zero = 0.0;
+    if (s > 0.0) {
+        zero = rint(lo / s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q.codes |= (uint32_t)(int)fmin(fmax(rint(x[e] / s) - zero, 0.0), 15.0) << (4 * e);
+    }
+    q.par |= bf_bits((float)zero - 128.f) << 16;
+    return q;
+}
+
+// The same in 32 bits, where x is known to within delta: false where a rounding could fall either way,
+// or where a group is not finite or too small for the arithmetic (quant64 and poison decide there).
+__device__ __forceinline__ bool quant32(const float* x, float delta, Quant& q) {
+    const float lo = half_min(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])));
+    const float hi = half_max(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+    const float amax = fmaxf(hi, -lo);
+    const float s0 = fmaxf((hi - lo) * (1.f / 15.f), amax * (1.f / 120.f));
+    const float es = 0.15f * delta + s0 * 0x1p-21f;
+    const uint32_t sb = bf_bits(s0 - es);
+    bool sure = sb == bf_bits(s0 + es) && s0 > 1e-30f;
+    const float s = __uint_as_float(sb << 16);
+    const float inv = 1.f / s;
+    const float rel = 0x1p-21f * amax * inv + delta * inv;  // bound of the error of x / s
+    const float tz = lo * inv, zero = rintf(tz);
+    sure = sure && rintf(tz - rel) == rintf(tz + rel);
+    q.codes = 0u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float t = x[e] * inv;
+        const float a = fminf(fmaxf(rintf(t - rel) - zero, 0.f), 15.f), b = fminf(fmaxf(rintf(t + rel) - zero, 0.f), 15.f);
+        sure = sure && a == b;
+        q.codes |= (uint32_t)(int)a << (4 * e);
+    }
+    q.par = sb | bf_bits(zero - 128.f) << 16;
+    return sure;
+}
+
+// grid T, 256 threads: token t's 16 q, 8 k and 8 v heads, four for each warp. q and k: RMSNorm over the
+// head with its gain, then the pairs (i, i + 64) rotated by the token's row of the cos / sin tables.
+// Bound by memory (8 or 16 KB read, 4 or 8 KB + 1152 B written for a token).
+//
+// A code next to a border between two would fall either way on the rounding of a 32-bit norm, and one
+// code off is a whole scale: 2e-5 of the values sit so near that quant32 is not sure, and their heads are
+// done again in 64 bits (about 1 % of the k heads), so that the codes are those of the definition.
+// delta bounds the 32-bit error of a rotated key: relative to |x_i cos| + |x_j sin|, 2^-24 times 4 (half of
+// the sum of squares' 8 roundings) + 4 (rsqrtf, 2 units) + 2 (norm and gain) + 2 (rotation) is below 16 * 2^-24.
+template <typename TI, typename TQ>
+__global__ void __launch_bounds__(256) k_kv4_append(const TI* __restrict__ qkv, long long stride,
+                                                    const bf16* __restrict__ gq, const bf16* __restrict__ gk, float eps,
+                                                    const float* __restrict__ cos_t, const float* __restrict__ sin_t,
+                                                    int n_pos, const int32_t* __restrict__ seqs,
+                                                    const int32_t* __restrict__ positions, Cache c, TQ* __restrict__ q_out) {
+    pdl_wait();  // upstream results are read below
+    pdl_trigger();
+    const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int seq = seqs[t], pos = positions[t];
+    if (seq < 0) return;
+    if (pos >= n_pos) {
+        if (threadIdx.x == 0) set_err(c.err, TTS_BB_KV4_ERR_RANGE);
+        return;
+    }
+    const int phys = find_block(c, seq, pos, threadIdx.x == 0);
+    if (phys < 0) return;
+    uint8_t* const base = c.pool + (size_t)phys * BLOCK;
+    const int tok = pos % KVB;
+    const TI* row = qkv + (size_t)t * stride + lane * 4;
+    const int i0 = (lane & 15) * 4;
+    const float4 cs4 = load4(cos_t + (size_t)pos * (HD / 2) + i0), sn4 = load4(sin_t + (size_t)pos * (HD / 2) + i0);
+    const float cs[4] = {cs4.x, cs4.y, cs4.z, cs4.w};
+    const float sgn = lane < 16 ? -1.f : 1.f;
+    const float sn[4] = {sgn * sn4.x, sgn * sn4.y, sgn * sn4.z, sgn * sn4.w};
+    float4 in[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) in[u] = load4(row + (warp + 8 * u) * HD);
+    const float4 gq4 = load4(gq + lane * 4), gk4 = load4(gk + lane * 4);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const float x[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
+        float y[4];
+        float delta = 0.f;
+        const float4 g4 = u < 2 ? gq4 : gk4;
+        const float g[4] = {g4.x, g4.y, g4.z, g4.w};
+        if (u < 3) {
+            const float r = rsqrtf(warp_sum(x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3]) * (1.f / HD) + eps);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float v = x[e] * r * g[e], a = v * cs[e], b = __shfl_xor_sync(0xffffffffu, v, 16) * sn[e];
+                y[e] = a + b;
+                delta = fmaxf(delta, fabsf(a) + fabsf(b));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = x[e];
+        }
+        if (u < 2) {
+            if (q_out) store4(q_out + ((size_t)t * NQ + warp + 8 * u) * HD + lane * 4, y);
+            continue;
+        }
+        bool finite = true;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) finite = finite && fabsf(y[e]) < INFINITY;
+        delta = u == 2 ? 0x1p-20f * warp_max(delta) : 0.f;
+        Quant q;
+        const bool sure = quant32(y, delta, q);
+        const unsigned bad = __ballot_sync(0xffffffffu, !finite);
+        if (!bad && __any_sync(0xffffffffu, !sure)) {
+            double z[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = (double)x[e];
+            if (u == 2) {
+                double ss = z[0] * z[0] + z[1] * z[1] + z[2] * z[2] + z[3] * z[3];
+#pragma unroll
+                for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const double r = 1.0 / sqrt(ss / HD + (double)eps);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const double v = z[e] * r * (double)g[e];
+                    z[e] = v * (double)cs[e] + __shfl_xor_sync(0xffffffffu, v, 16) * (double)sn[e];
+                }
+            }
+            q = quant64(z);
+        }
+        // a group with a value that is not finite is held as NaN
+        if (bad >> (lane & 16) & 0xffffu) q = Quant{0u, 0xC3007FC0u};
+        uint8_t* const tile = base + (size_t)((u - 2) * NKV + warp) * TILE;
+        const int group = lane >> 4, w = ((lane & 15) >> 1) * 2 + group;
+        *reinterpret_cast<uint16_t*>(tile + tok * (HD / 2) + w * 4 + (lane & 1) * 2) = (uint16_t)q.codes;
+        if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(tile + PAR + tok * 8 + group * 4) = q.par;
+    }
+}
+
+// ---------------------------------------------------------------- read
+// grid T, 256 threads: thread (head half, word) unpacks one word (8 dims) of K or V.
+__global__ void __launch_bounds__(256) k_kv4_read(const int32_t* __restrict__ seqs, const int32_t* __restrict__ positions,
+                                                  Cache c, bf16* __restrict__ k_out, bf16* __restrict__ v_out) {
+    pdl_wait();  // upstream results are read below
+    pdl_trigger();
+    const int t = blockIdx.x;
+    const int seq = seqs[t], pos = positions[t];
+    if (seq < 0) return;
+    const int phys = find_block(c, seq, pos, threadIdx.x == 0);
+    if (phys < 0) return;
+    const int unit = threadIdx.x >> 4, w = threadIdx.x & 15, tok = pos % KVB;  // unit: which * 8 + head
+    const uint8_t* tile = c.pool + (size_t)phys * BLOCK + (size_t)unit * TILE;
+    const uint32_t word = *reinterpret_cast<const uint32_t*>(tile + tok * (HD / 2) + w * 4);
+    const uint32_t par = *reinterpret_cast<const uint32_t*>(tile + PAR + tok * 8 + (w & 1) * 4);
+    const float s = __uint_as_float(par << 16), z = __uint_as_float(par & 0xFFFF0000u) + 128.f;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = s * ((float)(word >> (4 * i) & 15u) + z);
+    bf16* out = (unit < NKV ? k_out : v_out) + ((size_t)t * NKV + (unit & 7)) * HD + 64 * (w & 1) + 8 * (w >> 1);
+    store4(out, x);
+    store4(out + 4, x + 4);
+}
+
+// ---------------------------------------------------------------- attention
+struct AttnArgs {
+    const int32_t* seqs;
+    const int32_t* kv_lens;
+    int S, max_len, n_splits, bps;  // bps: cache blocks of one split
+    float* part;                    // [rows][16][n_splits][130]: output sums, running max, running sum
+};
+
+// Row r = (b, s): the cache row it reads and the keys it sees; false where the row is left as it was.
+__device__ __forceinline__ bool attn_row(const Cache& c, const AttnArgs& a, int r, bool report, int& seq, int& seen) {
+    const int b = r / a.S, s = r - b * a.S;
+    seq = a.seqs ? a.seqs[b] : b;
+    if (seq < 0) return false;
+    int len = a.kv_lens[b];
+    if (seq >= c.n_seqs || len < 0 || len > a.max_len) {
+        if (report) set_err(c.err, TTS_BB_KV4_ERR_RANGE);
+        return false;
+    }
+    seen = max(0, len - (a.S - 1 - s));
+    return true;
+}
+
+// grid (splits, 8, rows), 128 threads. Warp w takes keys w, w + 4, ...; lane l holds dims 4l .. 4l + 3.
+template <typename T>
+__global__ void __launch_bounds__(128) k_kv4_attn(const T* __restrict__ q, Cache c, AttnArgs a, T* __restrict__ out) {
+    pdl_wait();  // upstream results are read below
+    pdl_trigger();
+    const int split = blockIdx.x, g = blockIdx.y, row = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int seq, seen;
+    if (!attn_row(c, a, row, threadIdx.x == 0 && split == 0 && g == 0, seq, seen)) return;
+    const int k0 = split * a.bps * KVB, k1 = min(seen, k0 + a.bps * KVB);
+    const float sc = rsqrtf((float)HD) * LOG2E;
+    float4 q0 = load4(q + ((size_t)row * NQ + 2 * g) * HD + lane * 4);
+    float4 q1 = load4(q + ((size_t)row * NQ + 2 * g + 1) * HD + lane * 4);
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][4] = {};
+    const int group = lane >> 4, at = ((lane & 15) >> 1) * 8 + group * 4 + (lane & 1) * 2;
+    for (int j = k0 + warp; j < k1; j += 4) {
+        const int phys = find_block(c, seq, j, lane == 0);
+        if (phys < 0) continue;
+        float x[2][4];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const uint8_t* tile = c.pool + (size_t)phys * BLOCK + (size_t)(w * NKV + g) * TILE;
+            const uint32_t par = *reinterpret_cast<const uint32_t*>(tile + PAR + (j % KVB) * 8 + group * 4);
+            const uint32_t code = *reinterpret_cast<const uint16_t*>(tile + (j % KVB) * (HD / 2) + at);
+            const float s = __uint_as_float(par << 16), z = __uint_as_float(par & 0xFFFF0000u) + 128.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[w][e] = s * ((float)(code >> (4 * e) & 15u) + z);
+        }
+        float d[2] = {q0.x * x[0][0] + q0.y * x[0][1] + q0.z * x[0][2] + q0.w * x[0][3],
+                      q1.x * x[0][0] + q1.y * x[0][1] + q1.z * x[0][2] + q1.w * x[0][3]};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float z = warp_sum(d[h]) * sc, mn = fmaxf(m[h], z);
+            const float f = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn), p = exp2f(z - mn);
+            m[h] = mn;
+            l[h] = l[h] * f + p;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[h][e] = o[h][e] * f + p * x[1][e];
+        }
+    }
+    __shared__ float sm[4][2], sl[4][2], so[4][2][HD];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (lane == 0) { sm[warp][h] = m[h]; sl[warp][h] = l[h]; }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) so[warp][h][lane * 4 + e] = o[h][e];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * HD; i += 128) {
+        const int h = i / HD, d = i % HD;
+        float M = -INFINITY, L = 0.f, O = 0.f;
+        for (int w = 0; w < 4; ++w) M = fmaxf(M, sm[w][h]);
+        for (int w = 0; w < 4; ++w) {
+            const float f = sm[w][h] == -INFINITY ? 0.f : exp2f(sm[w][h] - M);
+            L += f * sl[w][h];
+            O += f * so[w][h][d];
+        }
+        if (a.n_splits == 1) {
+            out[((size_t)row * NQ + 2 * g + h) * HD + d] = (T)(L == 0.f ? 0.f : O / L);
+        } else {
+            float* dst = a.part + (((size_t)row * NQ + 2 * g + h) * a.n_splits + split) * (HD + 2);
+            dst[d] = O;
+            if (d == 0) { dst[HD] = M; dst[HD + 1] = L; }
+        }
+    }
+}
+
+// grid rows x 16, 128 threads: the splits of one (row, head) merged in split order.
+template <typename T>
+__global__ void __launch_bounds__(128) k_kv4_combine(Cache c, AttnArgs a, T* __restrict__ out) {
+    pdl_wait();  // upstream results are read below
+    pdl_trigger();
+    const int rh = blockIdx.x, d = threadIdx.x;
+    int seq, seen;
+    if (!attn_row(c, a, rh / NQ, false, seq, seen)) return;
+    const float* p = a.part + (size_t)rh * a.n_splits * (HD + 2);
+    float M = -INFINITY, L = 0.f, O = 0.f;
+    for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, p[s * (HD + 2) + HD]);
+    for (int s = 0; s < a.n_splits; ++s) {
+        const float ms = p[s * (HD + 2) + HD];
+        const float f = ms == -INFINITY ? 0.f : exp2f(ms - M);
+        L += f * p[s * (HD + 2) + HD + 1];
+        O += f * p[s * (HD + 2) + d];
+    }
+    out[(size_t)rh * HD + d] = (T)(L == 0.f ? 0.f : O / L);
+}
+
+struct Plan {
+    int splits, bps;
+};
+Plan attn_plan(long long rows, int max_len) {
+    const int nblk = (max_len + KVB - 1) / KVB;
+    const long long want = (32ll * 152 + rows * NKV - 1) / (rows * NKV);
+    const int splits = (int)std::max(1ll, std::min({want, (long long)nblk, 64ll}));
+    const int bps = (nblk + splits - 1) / splits;
+    return {(nblk + bps - 1) / bps, bps};
+}
+
+bool cache_ok(const tts_bb_kv4* c) {
+    return c && c->pool && c->page_table && c->n_blocks >= 1 && c->n_seqs >= 1 && c->blocks_per_seq >= 1 &&
+           (uintptr_t)c->pool % 16 == 0;
+}
+Cache cache_of(const tts_bb_kv4* c) {
+    return Cache{static_cast<uint8_t*>(c->pool), c->page_table, c->err, c->n_blocks, c->n_seqs, c->blocks_per_seq};
+}
+bool type_ok(int t) { return t == TTS_BB_T_F32 || t == TTS_BB_T_BF16; }
+bool aligned(const void* p, int type) { return (uintptr_t)p % (type == TTS_BB_T_F32 ? 16 : 8) == 0; }
+tts_bb_status status() { return cudaPeekAtLastError() == cudaSuccess ? TTS_BB_OK : TTS_BB_E_CUDA; }
+
+template <typename TI, typename TQ>
+void append(int T, const void* qkv, int64_t stride, const void* gq, const void* gk, float eps, const float* cos_t,
+            const float* sin_t, int n_pos, const int32_t* seqs, const int32_t* positions, const tts_bb_kv4* c, void* q_out,
+            cudaStream_t st) {
+    launch_pdl(k_kv4_append<TI, TQ>, T, 256, 0, st, static_cast<const TI*>(qkv), (long long)stride,
+               static_cast<const bf16*>(gq), static_cast<const bf16*>(gk), eps, cos_t, sin_t, n_pos, seqs, positions,
+               cache_of(c), static_cast<TQ*>(q_out));
+}
+
+}  // namespace
+
+TTS_API tts_bb_status tts_bb_rope_tables(double theta, int n_pos, float* cos_table, float* sin_table) {
+    if (n_pos < 1 || !(theta > 0.0) || !cos_table || !sin_table) return TTS_BB_E_INVALID;
+    for (int i = 0; i < HD / 2; ++i) {
+        const double f = std::pow(theta, -2.0 * i / HD);
+        for (int p = 0; p < n_pos; ++p) {
+            cos_table[(size_t)p * (HD / 2) + i] = (float)std::cos(p * f);
+            sin_table[(size_t)p * (HD / 2) + i] = (float)std::sin(p * f);
+        }
+    }
+    return TTS_BB_OK;
+}
+
+TTS_API tts_bb_status tts_bb_kv4_append(const tts_bb_kv4* cache, int T, const void* qkv, int qkv_type, int64_t qkv_stride,
+                                        const void* q_norm, const void* k_norm, float eps, const float* cos_table,
+                                        const float* sin_table, int n_pos, const int32_t* seqs, const int32_t* positions,
+                                        void* q_out, int q_type, void* stream) {
+    if (!cache_ok(cache) || T < 1 || !qkv || !q_norm || !k_norm || !cos_table || !sin_table || n_pos < 1 || !seqs ||
+        !positions || !type_ok(qkv_type) || !type_ok(q_type) || !(eps >= 0.f) || qkv_stride < QKV || qkv_stride % 4 ||
+        !aligned(qkv, qkv_type) || !aligned(q_out, q_type) || (uintptr_t)q_norm % 8 || (uintptr_t)k_norm % 8 ||
+        (uintptr_t)cos_table % 16 || (uintptr_t)sin_table % 16)
+        return TTS_BB_E_INVALID;
+    if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool fi = qkv_type == TTS_BB_T_F32, fq = q_type == TTS_BB_T_F32;
+    auto go = [&](auto f) {
+        f(T, qkv, qkv_stride, q_norm, k_norm, eps, cos_table, sin_table, n_pos, seqs, positions, cache, q_out, st);
+    };
+    if (fi && fq) go(append<float, float>);
+    else if (fi) go(append<float, bf16>);
+    else if (fq) go(append<bf16, float>);
+    else go(append<bf16, bf16>);
+    return status();
+}
+
+TTS_API tts_bb_status tts_bb_kv4_read(const tts_bb_kv4* cache, int T, const int32_t* seqs, const int32_t* positions,
+                                      void* k_out, void* v_out, void* stream) {
+    if (!cache_ok(cache) || T < 1 || !seqs || !positions || !k_out || !v_out || (uintptr_t)k_out % 8 || (uintptr_t)v_out % 8)
+        return TTS_BB_E_INVALID;
+    if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
+    launch_pdl(k_kv4_read, T, 256, 0, static_cast<cudaStream_t>(stream), seqs, positions, cache_of(cache),
+               static_cast<bf16*>(k_out), static_cast<bf16*>(v_out));
+    return status();
+}
+
+TTS_API size_t tts_bb_kv4_attention_workspace(int B, int S, int max_len) {
+    if (B < 1 || S < 1 || S > TTS_BB_KV4_MAX_QUERIES || max_len < 1 || (long long)B * S > 65535) return 0;
+    const Plan p = attn_plan((long long)B * S, max_len);
+    return p.splits == 1 ? 0 : (size_t)B * S * NQ * p.splits * (HD + 2) * sizeof(float);
+}
+
+TTS_API tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S, const void* q, int type,
+                                           const int32_t* seqs, const int32_t* kv_lens, int max_len, void* out,
+                                           void* workspace, size_t workspace_bytes, void* stream) {
+    if (!cache_ok(cache) || B < 1 || S < 1 || S > TTS_BB_KV4_MAX_QUERIES || (long long)B * S > 65535 || !q || !kv_lens ||
+        !out || !type_ok(type) || !aligned(q, type) || !aligned(out, type) || max_len < 1 ||
+        (long long)max_len > (long long)cache->blocks_per_seq * KVB || (!seqs && B > cache->n_seqs))
+        return TTS_BB_E_INVALID;
+    const size_t need = tts_bb_kv4_attention_workspace(B, S, max_len);
+    if (need && (!workspace || workspace_bytes < need || (uintptr_t)workspace % 16)) return TTS_BB_E_INVALID;
+    if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const Plan p = attn_plan((long long)B * S, max_len);
+    const Cache c = cache_of(cache);
+    const AttnArgs a{seqs, kv_lens, S, max_len, p.splits, p.bps, static_cast<float*>(workspace)};
+    const dim3 grid(p.splits, NKV, B * S);
+    auto go = [&](auto t) {
+        typedef decltype(t) T;
+        launch_pdl(k_kv4_attn<T>, grid, 128, 0, st, static_cast<const T*>(q), c, a, static_cast<T*>(out));
+        if (p.splits > 1) launch_pdl(k_kv4_combine<T>, B * S * NQ, 128, 0, st, c, a, static_cast<T*>(out));
+    };
+    if (type == TTS_BB_T_F32) go(float{});
+    else go(bf16{});
+    return status();
+}

@@ -487,6 +487,144 @@ tts_bb_status tts_bb_gqa_decode_attention_static(const void* q, const void* kv_p
                                                  int blocks_per_seq, const int32_t* positions, int B,
                                                  int max_position, void* out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Low-bit decode operators: a paged KV cache held in 4 bits, products with
+ * 4-bit weights, and log probabilities of the answers. Like
+ * tts_bb_gqa_decode_attention_static they work on the caller's buffers alone:
+ * every array is device memory of the current device, every call is
+ * asynchronous on `stream` (a cudaStream_t of that device, NULL = legacy
+ * default stream), allocates nothing, keeps nothing between calls and may be
+ * captured into a CUDA graph. Calls on several streams or threads at once are
+ * independent as long as what they write (outputs, workspaces, the same cache
+ * rows) is not shared. Host-side argument errors return TTS_BB_E_INVALID before
+ * anything is enqueued; TTS_BB_E_CUDA: a CUDA error was already pending (it
+ * is left pending) or a launch failed. */
+
+/* Element types of arrays that may have several. */
+enum { TTS_BB_T_F32 = 0, TTS_BB_T_BF16 = 1, TTS_BB_T_F16 = 2 };
+
+/* A paged KV cache in 4 bits: 4.5 bits a value. One block holds 64 tokens (the
+ * positions 64 j .. 64 j + 63 of a sequence) as K then V tiles of the 8 KV heads:
+ *   pool[block][2][8] tiles of TTS_BB_KV4_TILE_BYTES: 64 code rows of 64 bytes,
+ *   then 64 parameter rows of 8 bytes, one of each for a token.
+ * The 128 dims of a head are two groups of 64 (dims 0..63 and 64..127). Word w
+ * (32 bits, little endian) of a code row holds dims 64 (w & 1) + 8 (w >> 1) + i
+ * in nibble i (bits 4 i .. 4 i + 3); a parameter row holds (bf16 scale, bf16
+ * offset) of group 0, then of group 1. A value is scale * (code + 128 + offset).
+ * A group x is quantised with scale = bf16(max((hi - lo) / 15, max|x| / 120)),
+ * zero = rint(lo / scale), code = clamp(rint(x / scale) - zero, 0, 15) and offset =
+ * zero - 128 (codes 0 and offset -128 where scale is 0; a group with a value
+ * that is not finite is held as NaN; magnitudes up to 1e38).
+ * A pool must be zeroed or written before it is read: blocks past a sequence's
+ * keys may hold anything. */
+#define TTS_BB_KV4_TILE_BYTES 4608
+#define TTS_BB_KV4_BLOCK_BYTES 73728 /* 2 * 8 tiles; a bf16 block has 262144 */
+#define TTS_BB_KV4_MAX_QUERIES 64    /* query tokens of a sequence in one attention call */
+/* Bits of a cache's error word. */
+enum {
+    TTS_BB_KV4_ERR_PAGE = 1, /* a page-table entry outside 0..n_blocks-1 was met */
+    TTS_BB_KV4_ERR_RANGE = 2 /* a sequence row >= n_seqs, a position outside the page table or the
+                                cos / sin tables, or a key count outside 0..max_len */
+};
+typedef struct {
+    void* pool;                /* device, 16-byte aligned: n_blocks * TTS_BB_KV4_BLOCK_BYTES */
+    const int32_t* page_table; /* device int32 [n_seqs][blocks_per_seq]: block of each 64 positions */
+    int32_t* err;              /* device word, or NULL: the bits of what calls skipped are ORed into it */
+    int n_blocks;
+    int n_seqs;
+    int blocks_per_seq;
+} tts_bb_kv4;
+
+/* cos and sin of pos * theta^(-2 i / 128), i < 64, for positions 0 .. n_pos - 1, host only: fills two
+ * host fp32 arrays [n_pos][64] (angles and functions in 64 bits, rounded once), to be copied to the
+ * device for tts_bb_kv4_append. TTS_BB_E_INVALID for n_pos < 1, theta <= 0 or a NULL array. */
+tts_bb_status tts_bb_rope_tables(double theta, int n_pos, float* cos_table, float* sin_table);
+
+/* Append T tokens: q/k RMSNorm, half-rotate RoPE and the 4-bit quantisation of keys and values, in one
+ * launch. Token t belongs to cache row seqs[t] at position positions[t]; a negative seqs[t] is padding:
+ * nothing is done for it. A token whose row, position or page is out of range is skipped as a whole (its
+ * q_out row too) and reported in cache->err. The (row, position) pairs of one call must differ, else what
+ * that position holds is unspecified.
+ *   qkv        [T] rows of 4096 (16 q, 8 k, 8 v heads of 128), fp32 or bf16 (qkv_type), rows
+ *              qkv_stride elements apart (>= 4096, a multiple of 4), 16- (fp32) or 8-byte aligned
+ *   q_norm, k_norm  bf16 [128] gains; eps inside the root
+ *   cos_table, sin_table  fp32 [n_pos][64], 16-byte aligned; the pairs (i, i + 64) rotate by row positions[t]
+ *   seqs, positions int32 [T]
+ *   q_out      fp32 or bf16 (q_type) [T][16][128]: the rotated queries, or NULL
+ * The codes and parameters are those of the exact arithmetic (keys next to a border are decided in 64 bits). */
+tts_bb_status tts_bb_kv4_append(const tts_bb_kv4* cache, int T, const void* qkv, int qkv_type, int64_t qkv_stride,
+                                const void* q_norm, const void* k_norm, float eps, const float* cos_table,
+                                const float* sin_table, int n_pos, const int32_t* seqs, const int32_t* positions,
+                                void* q_out, int q_type, void* stream);
+
+/* The values the cache holds for T tokens (seqs, positions as in tts_bb_kv4_append), rounded to bf16:
+ * k_out, v_out bf16 [T][8][128], 8-byte aligned. Rows of padding and of tokens out of range are left as they were. */
+tts_bb_status tts_bb_kv4_read(const tts_bb_kv4* cache, int T, const int32_t* seqs, const int32_t* positions,
+                              void* k_out, void* v_out, void* stream);
+
+/* Grouped-query attention over the cache, S causal query tokens for each of B sequences: a decode step
+ * (S = 1) or a short chunk whose keys are already appended. Query head h reads KV head h / 2, scale
+ * 1 / sqrt(128), softmax and sums in fp32.
+ *   q, out    fp32 or bf16 (type) [B][S][16][128], 16- (fp32) or 8-byte aligned
+ *   seqs      int32 [B], the cache row of each sequence (negative: padding, its out rows are left as
+ *             they were), or NULL: sequence b reads row b
+ *   kv_lens   int32 [B], the sequence's keys, those of the S query tokens among them: query s sees the first
+ *             kv_lens[b] - (S - 1 - s); a query that sees none gives zeros
+ *   max_len   an upper bound of kv_lens (host), at most 64 * blocks_per_seq; it sets the split and
+ *             the workspace, a tight one is faster. A sequence whose row or key count is out of range is
+ *             left as it was; keys behind a page out of range are left out of the sums; both are reported
+ *             in cache->err.
+ *   workspace at least tts_bb_kv4_attention_workspace(B, S, max_len) bytes, 16-byte aligned (NULL where that is 0);
+ *             written before it is read, not shared by calls that overlap
+ * Results do not depend on the order in which blocks of the launch run. TTS_BB_E_INVALID also for
+ * S > TTS_BB_KV4_MAX_QUERIES or B * S > 65535. */
+size_t tts_bb_kv4_attention_workspace(int B, int S, int max_len);
+tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S, const void* q, int type, const int32_t* seqs,
+                                   const int32_t* kv_lens, int max_len, void* out, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* Products with 4-bit weights, y = x W^T for T <= TTS_BB_W4_MAX_TOKENS rows of x: W[n][k] = scale[n][k / group] *
+ * (code[n][k] - zero[n][k / group]).
+ * tts_bb_w4_pack lays the weights out once (tts_bb_w4_packed_bytes bytes, 16-byte aligned; 0 for
+ * sizes that are refused) from
+ *   codes   uint8 [N][K / 2]: code 2 i in the low, 2 i + 1 in the high nibble of byte i
+ *   scales  bf16 [N][K / group]
+ *   zeros   uint8 [N][K / group], 0..15, or NULL: 8 everywhere (above 15: taken modulo 16)
+ * group 32, 64 or 128; K a multiple of group; N >= 1, K >= group. */
+#define TTS_BB_W4_MAX_TOKENS 64
+size_t tts_bb_w4_packed_bytes(int N, int K, int group);
+tts_bb_status tts_bb_w4_pack(int N, int K, int group, const void* codes, const void* scales, const void* zeros,
+                             void* packed, void* stream);
+/*   x  fp32 or bf16 (type) [T] rows of K, x_stride elements apart (>= K, and 16-byte aligned rows)
+ *   y  fp32 or bf16 (the same type) [T][N], 4- or 2-byte aligned
+ * Products are exact (fp32 rows of x enter as three bf16 parts) and summed in fp32, in an order that depends
+ * on the sizes alone. */
+tts_bb_status tts_bb_w4_linear(int T, int N, int K, int group, const void* x, int type, int64_t x_stride,
+                               const void* packed, void* y, void* stream);
+
+/* Log probabilities of R rows of V logits: of a given token, the entropy, the log-sum-exp and the n_top most
+ * probable tokens.
+ *   logits   fp32, bf16 or fp16 (type) [R] rows, row_stride elements apart (>= V), aligned to the element
+ *   targets  int32 [R] or NULL; logprob fp32 [R]: log p(targets[r]); -inf for a target outside 0..V-1, a
+ *            masked one, or one of logit -inf
+ *   allowed  NULL, or uint32 words of 32 ids each (id i: bit i & 31 of word i >> 5; (V + 31) / 32
+ *            words a row, allowed_stride words apart, 0 = one row for all): an id whose bit is 0 has
+ *            probability 0, whatever its logit
+ *   entropy  fp32 [R] (nats); lse fp32 [R]: log of the sum of exp(logit)
+ *   top_ids, top_logprobs  int32 and fp32 [R][n_top], 0 <= n_top <= TTS_BB_LOGPROBS_MAX_TOP: by logit
+ *            downward, ties to the lowest id; ids of probability 0 are no alternatives: (-1, -inf) behind the last
+ * Outputs may be NULL (top_* where n_top is 0, logprob where targets is NULL). A row with nothing left
+ * has logprob and lse -inf and entropy 0; an allowed NaN or +inf makes the row's numbers NaN and its
+ * ids -1.
+ *   workspace at least tts_bb_token_logprobs_workspace(R, V, n_top) bytes, 16-byte aligned (NULL where that is
+ *            0); written before it is read, not shared by calls that overlap */
+#define TTS_BB_LOGPROBS_MAX_TOP 32
+size_t tts_bb_token_logprobs_workspace(int R, int V, int n_top);
+tts_bb_status tts_bb_token_logprobs(int R, int V, const void* logits, int type, int64_t row_stride,
+                                    const int32_t* targets, const uint32_t* allowed, int64_t allowed_stride, int n_top,
+                                    float* logprob, float* entropy, float* lse, int32_t* top_ids, float* top_logprobs,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
