@@ -271,69 +271,279 @@ __device__ __forceinline__ bool attn_row(const Cache& c, const AttnArgs& a, int 
     return true;
 }
 
-// grid (splits, 8, rows), 128 threads. Warp w takes keys w, w + 4, ...; lane l holds dims 4l .. 4l + 3.
+// Tensor-core attention of one (row, KV head, split). 4 warps; warp w takes tokens 16 w .. 16 w + 15 of every cache
+// block of the split, copied by cp.async through a ring of its own (no barrier between warps until the end).
+//
+// Scores: S[key][column] = K Q^T by m16n8k16, K's codes as the A operand. Lane (r = lane / 4, c = lane % 4) reads 16 bytes of
+// the code rows of keys r and r + 8 (16 dims of each group); a nibble becomes the whole number code - zero in bf16 by one
+// logical operation (0x4300 | code = 128 + code) and one exact addition of the offset, so the products of a step are
+// exact and the group's scale multiplies the sum. The pairs of dims that a register holds, (d, d + 4), only permute the
+// contraction; Q is laid out alike. bf16 queries: column n holds head n & 1, so that every lane has both heads' scores of
+// its two keys. fp32 queries: column n holds part n >> 1 (three bf16 parts by truncation: all 24 bits) of head n & 1.
+// Each lane then keeps one score: key r + 8 (c & 1), head c >> 1.
+//
+// Output: O^T[dim][column] += V^T P by the same instruction, V's codes as A (dims are rows; a register holds one dim of two
+// keys: the low or high halves of two keys' words side by side, then the same nibble of both), P times V's scale
+// of the key and group as B in bf16 parts (bf16: two, 16 bits; fp32: three). Whole numbers near zero, not 0..15 with a
+// middle added later: where a softmax is flat the sums cancel, and a common offset would cost its digits.
+//
+// Softmax: a running reference m for each head, moved only when a score exceeds it by 8 (log2): then sums and O are
+// rescaled. It starts at -1e30, not -inf, so that no difference of infinities arises.
+constexpr int WARPS = 4, STAGES = 4, STEP_BYTES = 2304;  // 16 keys: K and V codes 1024 each, parameters 128 each
+constexpr float M_START = -1e30f, M_SLACK = 8.f;
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// nibble j of both halves of w as bf16 whole numbers, with the offsets added (exact)
+__device__ __forceinline__ uint32_t whole(uint32_t w, int j, uint32_t off) {
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"((w >> (4 * j) & 0x000F000Fu) | 0x43004300u), "r"(off));
+    return d;
+}
+__device__ __forceinline__ uint32_t lows(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
+__device__ __forceinline__ uint32_t highs(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
+__device__ __forceinline__ float as_f(uint32_t x) { return __uint_as_float(x); }
+__device__ __forceinline__ uint32_t as_u(float x) { return __float_as_uint(x); }
+// part (0, 1, 2) of x: 8 significant bits each, by truncation; m1, m2 cover the upper half where part >= 1, 2
+__device__ __forceinline__ uint32_t part_of(float x, uint32_t m1, uint32_t m2) {
+    x -= as_f(as_u(x) & m1);
+    return as_u(x - as_f(as_u(x) & m2));
+}
+
+// The B registers of Q for this lane's column: step s = 2 word + half, dims 64 g + 16 c + 8 (word >> 1) + 2 half + {0, 1} and + 4.
+__device__ __forceinline__ void load_q(const bf16* q, int n, int c, uint32_t (&b)[16]) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const uint4 v = *reinterpret_cast<const uint4*>(q + (n & 1) * HD + 64 * (w & 1) + 16 * c + 8 * (w >> 1));
+        b[4 * w] = lows(v.x, v.z);
+        b[4 * w + 1] = highs(v.x, v.z);
+        b[4 * w + 2] = lows(v.y, v.w);
+        b[4 * w + 3] = highs(v.y, v.w);
+    }
+}
+__device__ __forceinline__ void load_q(const float* q, int n, int c, uint32_t (&b)[16]) {
+    const uint32_t m1 = n >= 2 ? 0xFFFF0000u : 0u, m2 = n >= 4 ? 0xFFFF0000u : 0u, on = n < 6 ? ~0u : 0u;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float* p = q + (n & 1) * HD + 64 * (w & 1) + 16 * c + 8 * (w >> 1);
+        const float4 u = load4(p), v = load4(p + 4);
+        b[4 * w] = on & highs(part_of(u.x, m1, m2), part_of(v.x, m1, m2));
+        b[4 * w + 1] = on & highs(part_of(u.y, m1, m2), part_of(v.y, m1, m2));
+        b[4 * w + 2] = on & highs(part_of(u.z, m1, m2), part_of(v.z, m1, m2));
+        b[4 * w + 3] = on & highs(part_of(u.w, m1, m2), part_of(v.w, m1, m2));
+    }
+}
+
 template <typename T>
-__global__ void __launch_bounds__(128) k_kv4_attn(const T* __restrict__ q, Cache c, AttnArgs a, T* __restrict__ out) {
+__global__ void __launch_bounds__(WARPS * 32, 5) k_kv4_attn(const T* __restrict__ q, Cache cache, AttnArgs a, T* __restrict__ out) {
+    constexpr bool F32 = sizeof(T) == 4;
+    constexpr int P = F32 ? 3 : 2;  // bf16 parts of a weight
     pdl_wait();  // upstream results are read below
     pdl_trigger();
     const int split = blockIdx.x, g = blockIdx.y, row = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     int seq, seen;
-    if (!attn_row(c, a, row, threadIdx.x == 0 && split == 0 && g == 0, seq, seen)) return;
-    const int k0 = split * a.bps * KVB, k1 = min(seen, k0 + a.bps * KVB);
-    const float sc = rsqrtf((float)HD) * LOG2E;
-    float4 q0 = load4(q + ((size_t)row * NQ + 2 * g) * HD + lane * 4);
-    float4 q1 = load4(q + ((size_t)row * NQ + 2 * g + 1) * HD + lane * 4);
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][4] = {};
-    const int group = lane >> 4, at = ((lane & 15) >> 1) * 8 + group * 4 + (lane & 1) * 2;
-    for (int j = k0 + warp; j < k1; j += 4) {
-        const int phys = find_block(c, seq, j, lane == 0);
-        if (phys < 0) continue;
-        float x[2][4];
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            const uint8_t* tile = c.pool + (size_t)phys * BLOCK + (size_t)(w * NKV + g) * TILE;
-            const uint32_t par = *reinterpret_cast<const uint32_t*>(tile + PAR + (j % KVB) * 8 + group * 4);
-            const uint32_t code = *reinterpret_cast<const uint16_t*>(tile + (j % KVB) * (HD / 2) + at);
-            const float s = __uint_as_float(par << 16), z = __uint_as_float(par & 0xFFFF0000u) + 128.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[w][e] = s * ((float)(code >> (4 * e) & 15u) + z);
+    if (!attn_row(cache, a, row, threadIdx.x == 0 && split == 0 && g == 0, seq, seen)) return;
+    const int j0 = split * a.bps, j1 = min((seen + KVB - 1) / KVB, j0 + a.bps), n = max(0, j1 - j0);
+
+    extern __shared__ __align__(128) uint8_t ring[];
+    uint8_t* const mine = ring + warp * STAGES * STEP_BYTES;
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(mine);
+    const uint8_t* const src = cache.pool + (size_t)g * TILE + warp * 1024;
+    const int32_t* const pages = cache.table + (size_t)seq * cache.bps + j0;
+    // 16-byte pieces of V rows are swapped between the row's halves for rows 2, 3 of every 4, so that the 8-byte reads
+    // of 4 rows meet all 32 banks
+    const uint32_t vdst = 1024 + (lane * 16 ^ (lane >> 3 & 1) * 32);
+    const int ppiece = (lane & 8 ? NKV * TILE : 0) + PAR - warp * 1024 + warp * 128 + (lane & 7) * 16;
+    uint32_t missing = 0;  // bit s: the block in stage s has no page
+    auto fetch = [&](int i, int page) {
+        const int s = i % STAGES;
+        const bool ok = page >= 0 && page < cache.n_blocks;
+        missing = missing & ~(1u << s) | (ok ? 0u : 1u << s);
+        if (ok) {
+            const uint8_t* b = src + (size_t)page * BLOCK;
+            const uint32_t d = dst + s * STEP_BYTES;
+            cp16(d + lane * 16, b + lane * 16);
+            cp16(d + 512 + lane * 16, b + 512 + lane * 16);
+            cp16(d + vdst, b + NKV * TILE + lane * 16);
+            cp16(d + 512 + vdst, b + NKV * TILE + 512 + lane * 16);
+            if (lane < 16) cp16(d + 2048 + lane * 16, b + ppiece);
+        } else if (lane == 0) {
+            set_err(cache.err, TTS_BB_KV4_ERR_PAGE);
         }
-        float d[2] = {q0.x * x[0][0] + q0.y * x[0][1] + q0.z * x[0][2] + q0.w * x[0][3],
-                      q1.x * x[0][0] + q1.y * x[0][1] + q1.z * x[0][2] + q1.w * x[0][3]};
+    };
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float z = warp_sum(d[h]) * sc, mn = fmaxf(m[h], z);
-            const float f = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn), p = exp2f(z - mn);
-            m[h] = mn;
-            l[h] = l[h] * f + p;
+    for (int i = 0; i < STAGES - 1; ++i) {
+        if (i < n) fetch(i, pages[i]);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    int page = n > STAGES - 1 ? pages[STAGES - 1] : 0;
+
+    uint32_t qb[16];
+    load_q(q + ((size_t)row * NQ + 2 * g) * HD, r, c, qb);
+    const uint32_t m1 = r >= 2 ? 0xFFFF0000u : 0u, m2 = r >= 4 ? 0xFFFF0000u : 0u;
+    const uint32_t half_sel = r & 2 ? 0x5410u : 0x7632u;  // bf16: part 0 in the high halves, part 1 in the low ones
+    const int from = 4 * c + 2 * (r & 1);                 // the lane that has the weight of key c of this column's head
+    const int my = r + 8 * (c & 1);                       // this lane's key of 16; its head is c >> 1
+    const float sc = rsqrtf((float)HD) * LOG2E;
+    float o[8][4] = {}, m = M_START, l = 0.f;
+
+    for (int i = 0; i < n; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+        __syncwarp();
+        if (i + STAGES - 1 < n) fetch(i + STAGES - 1, page);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (i + STAGES < n) page = pages[i + STAGES];
+        const int key0 = (j0 + i) * KVB + warp * 16;
+        if (key0 >= seen || (missing >> (i % STAGES) & 1)) continue;
+        const uint8_t* st = mine + (i % STAGES) * STEP_BYTES;
+        const bool tail = key0 + 16 > seen;
+        const bool on = key0 + my < seen;
+
+        // scores
+        float z;
+        {
+            const uint4 k0 = *reinterpret_cast<const uint4*>(st + r * 64 + c * 16);
+            const uint4 k1 = *reinterpret_cast<const uint4*>(st + (r + 8) * 64 + c * 16);
+            const uint2 p0 = *reinterpret_cast<const uint2*>(st + 2048 + r * 8);
+            const uint2 p1 = *reinterpret_cast<const uint2*>(st + 2048 + (r + 8) * 8);
+            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+            const uint32_t off0[2] = {highs(p0.x, p0.x), highs(p0.y, p0.y)}, off1[2] = {highs(p1.x, p1.x), highs(p1.y, p1.y)};
+            float s[2][4] = {};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[h][e] = o[h][e] * f + p * x[1][e];
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t x[4] = {whole(w0[w], 2 * h, off0[w & 1]), whole(w1[w], 2 * h, off1[w & 1]),
+                                           whole(w0[w], 2 * h + 1, off0[w & 1]), whole(w1[w], 2 * h + 1, off1[w & 1])};
+                    mma(s[w & 1], x, qb[4 * w + 2 * h], qb[4 * w + 2 * h + 1]);
+                }
+            float y[4];  // (key r, head 0), (r, 1), (r + 8, 0), (r + 8, 1)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y[e] = as_f((e < 2 ? p0.x : p1.x) << 16) * s[0][e] + as_f((e < 2 ? p0.y : p1.y) << 16) * s[1][e];
+            if constexpr (F32) {  // the four columns' parts added; each lane ends with its own key and head
+                const float a0 = c & 1 ? y[2] : y[0], a1 = c & 1 ? y[3] : y[1];
+                const float b0 = c & 1 ? y[0] : y[2], b1 = c & 1 ? y[1] : y[3];
+                const float u0 = a0 + __shfl_xor_sync(0xffffffffu, b0, 1), u1 = a1 + __shfl_xor_sync(0xffffffffu, b1, 1);
+                z = (c & 2 ? u1 : u0) + __shfl_xor_sync(0xffffffffu, c & 2 ? u0 : u1, 2);
+            } else {
+                z = c & 2 ? (c & 1 ? y[3] : y[1]) : (c & 1 ? y[2] : y[0]);
+            }
+            z = on ? z * sc : -INFINITY;
+        }
+        if (__any_sync(0xffffffffu, z > m + M_SLACK)) {
+            float mx = z;
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float nm = fmaxf(m, mx), f = ex2(m - nm), other = __shfl_xor_sync(0xffffffffu, f, 2);
+            const float f0 = c & 2 ? other : f, f1 = c & 2 ? f : other;
+            m = nm;
+            l *= f;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                o[t][0] *= f0; o[t][1] *= f1;
+                o[t][2] *= f0; o[t][3] *= f1;
+            }
+        }
+        const float p = on ? ex2(z - m) : 0.f;
+        l += p;
+
+        // output
+        const uint2 vp = *reinterpret_cast<const uint2*>(st + 2176 + my * 8);
+        uint2 w[4], pp[4];  // codes and parameters of keys c, c + 4, c + 8, c + 12
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            w[k] = *reinterpret_cast<const uint2*>(st + 1024 + (c + 4 * k) * 64 + (r * 8 ^ (c >> 1) * 32));
+            pp[k] = *reinterpret_cast<const uint2*>(st + 2176 + (c + 4 * k) * 8);
+            if (tail && key0 + c + 4 * k >= seen) pp[k] = make_uint2(0u, 0u);  // an offset that is not finite times a zero
+        }
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) {
+            const float x = on ? p * as_f((gr ? vp.y : vp.x) << 16) : 0.f;
+            uint32_t b0, b1;
+            if constexpr (F32) {
+                uint32_t y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    y[k] = part_of(__shfl_sync(0xffffffffu, x, from + (k & 1) * 16 + (k >> 1)), m1, m2);
+                b0 = highs(y[0], y[1]);
+                b1 = highs(y[2], y[3]);
+            } else {
+                const uint32_t both = highs(as_u(x - as_f(as_u(x) & 0xFFFF0000u)), as_u(x));  // part 1 below part 0
+                uint32_t y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, both, from + (k & 1) * 16 + (k >> 1));
+                b0 = __byte_perm(y[0], y[1], half_sel);
+                b1 = __byte_perm(y[2], y[3], half_sel);
+            }
+            const uint32_t v0 = gr ? w[0].y : w[0].x, v1 = gr ? w[1].y : w[1].x, v2 = gr ? w[2].y : w[2].x, v3 = gr ? w[3].y : w[3].x;
+            const uint32_t off01 = highs(gr ? pp[0].y : pp[0].x, gr ? pp[1].y : pp[1].x);
+            const uint32_t off23 = highs(gr ? pp[2].y : pp[2].x, gr ? pp[3].y : pp[3].x);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const uint32_t u01 = t < 2 ? lows(v0, v1) : highs(v0, v1), u23 = t < 2 ? lows(v2, v3) : highs(v2, v3);
+                const int j = 2 * (t & 1);
+                const uint32_t x4[4] = {whole(u01, j, off01), whole(u01, j + 1, off01), whole(u23, j, off23), whole(u23, j + 1, off23)};
+                mma(o[4 * gr + t], x4, b0, b1);
+            }
         }
     }
-    __shared__ float sm[4][2], sl[4][2], so[4][2][HD];
+    // merge the warps: every part of O to shared memory, then one thread for each dim
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 4);
+    l += __shfl_xor_sync(0xffffffffu, l, 8);
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    float* const so = reinterpret_cast<float*>(ring);  // [warp][part][head][128]
+    __shared__ float sm[WARPS][2], sl[WARPS][2];
+    if (c < P) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const int d = 64 * (t >> 2) + 8 * r + 2 * (t & 3);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<float2*>(so + ((warp * P + c) * 2 + h) * HD + d) = make_float2(o[t][h], o[t][2 + h]);
+        }
+    }
+    if (lane == 0 || lane == 2) { sm[warp][lane >> 1] = m; sl[warp][lane >> 1] = l; }
+    __syncthreads();
+    const int d = threadIdx.x;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        if (lane == 0) { sm[warp][h] = m[h]; sl[warp][h] = l[h]; }
+        float M = M_START, L = 0.f, O = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) so[warp][h][lane * 4 + e] = o[h][e];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * HD; i += 128) {
-        const int h = i / HD, d = i % HD;
-        float M = -INFINITY, L = 0.f, O = 0.f;
-        for (int w = 0; w < 4; ++w) M = fmaxf(M, sm[w][h]);
-        for (int w = 0; w < 4; ++w) {
-            const float f = sm[w][h] == -INFINITY ? 0.f : exp2f(sm[w][h] - M);
+        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm[w][h]);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            const float f = ex2(sm[w][h] - M);
+            float x = 0.f;
+#pragma unroll
+            for (int part = P - 1; part >= 0; --part) x += so[((w * P + part) * 2 + h) * HD + d];
             L += f * sl[w][h];
-            O += f * so[w][h][d];
+            O += f * x;
         }
         if (a.n_splits == 1) {
             out[((size_t)row * NQ + 2 * g + h) * HD + d] = (T)(L == 0.f ? 0.f : O / L);
         } else {
-            float* dst = a.part + (((size_t)row * NQ + 2 * g + h) * a.n_splits + split) * (HD + 2);
-            dst[d] = O;
-            if (d == 0) { dst[HD] = M; dst[HD + 1] = L; }
+            float* const to = a.part + (((size_t)row * NQ + 2 * g + h) * a.n_splits + split) * (HD + 2);
+            to[d] = O;
+            if (d == 0) { to[HD] = M; to[HD + 1] = L; }
         }
     }
 }
@@ -347,24 +557,24 @@ __global__ void __launch_bounds__(128) k_kv4_combine(Cache c, AttnArgs a, T* __r
     int seq, seen;
     if (!attn_row(c, a, rh / NQ, false, seq, seen)) return;
     const float* p = a.part + (size_t)rh * a.n_splits * (HD + 2);
-    float M = -INFINITY, L = 0.f, O = 0.f;
+    float M = M_START, L = 0.f, O = 0.f;
     for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, p[s * (HD + 2) + HD]);
     for (int s = 0; s < a.n_splits; ++s) {
-        const float ms = p[s * (HD + 2) + HD];
-        const float f = ms == -INFINITY ? 0.f : exp2f(ms - M);
+        const float f = ex2(p[s * (HD + 2) + HD] - M);
         L += f * p[s * (HD + 2) + HD + 1];
         O += f * p[s * (HD + 2) + d];
     }
     out[(size_t)rh * HD + d] = (T)(L == 0.f ? 0.f : O / L);
 }
 
+constexpr int MAX_SPLITS = 64;
 struct Plan {
     int splits, bps;
 };
 Plan attn_plan(long long rows, int max_len) {
     const int nblk = (max_len + KVB - 1) / KVB;
     const long long want = (32ll * 152 + rows * NKV - 1) / (rows * NKV);
-    const int splits = (int)std::max(1ll, std::min({want, (long long)nblk, 64ll}));
+    const int splits = (int)std::max(1ll, std::min({want, (long long)nblk, (long long)MAX_SPLITS}));
     const int bps = (nblk + splits - 1) / splits;
     return {(nblk + bps - 1) / bps, bps};
 }
@@ -458,7 +668,7 @@ TTS_API tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S
     const dim3 grid(p.splits, NKV, B * S);
     auto go = [&](auto t) {
         typedef decltype(t) T;
-        launch_pdl(k_kv4_attn<T>, grid, 128, 0, st, static_cast<const T*>(q), c, a, static_cast<T*>(out));
+        launch_pdl(k_kv4_attn<T>, grid, WARPS * 32, WARPS * STAGES * STEP_BYTES, st, static_cast<const T*>(q), c, a, static_cast<T*>(out));
         if (p.splits > 1) launch_pdl(k_kv4_combine<T>, B * S * NQ, 128, 0, st, c, a, static_cast<T*>(out));
     };
     if (type == TTS_BB_T_F32) go(float{});
