@@ -12,8 +12,11 @@
 //
 // Quantisation of a group x[64]: scale = bf16(max((hi - lo) / 15, max|x| / 120)), zero = rint(lo / scale),
 // code = clamp(rint(x / scale) - zero, 0, 15), offset = zero - 128. The second term bounds zero by 121.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "../../include/tts_bb.h"
@@ -271,26 +274,33 @@ __device__ __forceinline__ bool attn_row(const Cache& c, const AttnArgs& a, int 
     return true;
 }
 
-// Tensor-core attention of one (row, KV head, split). 4 warps; warp w takes tokens 16 w .. 16 w + 15 of every cache
-// block of the split, copied by cp.async through a ring of its own (no barrier between warps until the end).
+// Tensor-core attention of one (row, KV head, split). 4 warps; a warp takes 32 keys at a time (warps 0, 1 the halves of the
+// split's even cache blocks, 2, 3 of the odd ones), copied by cp.async through a ring of its own: no barrier between
+// warps until the end. What bounds it beside memory are the integer instructions that take nibbles apart (two a cycle
+// and SM), so both products take the codes with as few of them as they can:
 //
-// Scores: S[key][column] = K Q^T by m16n8k16, K's codes as the A operand. Lane (r = lane / 4, c = lane % 4) reads 16 bytes of
-// the code rows of keys r and r + 8 (16 dims of each group); a nibble becomes the whole number code - zero in bf16 by one
-// logical operation (0x4300 | code = 128 + code) and one exact addition of the offset, so the products of a step are
-// exact and the group's scale multiplies the sum. The pairs of dims that a register holds, (d, d + 4), only permute the
-// contraction; Q is laid out alike. bf16 queries: column n holds head n & 1, so that every lane has both heads' scores of
-// its two keys. fp32 queries: column n holds part n >> 1 (three bf16 parts by truncation: all 24 bits) of head n & 1.
-// Each lane then keeps one score: key r + 8 (c & 1), head c >> 1.
+// Scores, S[key][column] = K Q^T, by m16n8k32 on e4m3: the byte 0000cccc is c 2^-9 (subnormals and the first binade are
+// evenly spaced), so a word of 8 codes is two operands after one shift and two masks. Lane (r = lane / 4, c = lane % 4) reads
+// 16 bytes of the code rows of keys r and r + 8: 16 dims of each group, even and odd dims apart, which only permutes the
+// contraction. Products are exact and sums fp32. The zero point joins by the queries' sum: s (sum q code + zero sum q).
+// Q, scaled by a power of two to a largest magnitude in [128, 256), enters as e4m3 parts of 4 bits, each the rounding of what
+// the ones before it leave. bf16: two parts hold its 8 bits (below 2^-14 of the head's largest: to 2^-18 of that),
+// multiplied one after the other into the same sums; column n holds head n & 1, so every lane has both heads' scores of
+// its keys. fp32: eight parts, part p scaled up by 16^p, column n of two column tiles holding part n >> 1 (+ 4) of head n & 1.
+// Each lane then keeps one score of 16 keys: key r + 8 (c & 1), head c >> 1.
 //
-// Output: O^T[dim][column] += V^T P by the same instruction, V's codes as A (dims are rows; a register holds one dim of two
-// keys: the low or high halves of two keys' words side by side, then the same nibble of both), P times V's scale
-// of the key and group as B in bf16 parts (bf16: two, 16 bits; fp32: three). Whole numbers near zero, not 0..15 with a
-// middle added later: where a softmax is flat the sums cancel, and a common offset would cost its digits.
+// Output, O^T[dim][column] += V^T P, by m16n8k16 on bf16, V's codes as A: rows are dims, and a register holds one dim of
+// two keys: one byte of both keys' words side by side, then one mask for the byte's even dim and one for its odd dim:
+// 000c is the bf16 number c 2^-133 and 00c0 16 c 2^-133 (subnormals again). Zero points are added to them, exact in 8 bits:
+// whole numbers around zero, not 0..15 with a middle added later, because where a softmax is flat the sums cancel
+// and a common offset would cost their digits. P times V's scale of the key and group is B, as bf16 parts by truncation
+// (bf16: two, 16 bits; fp32: three, all 24) in columns of their own. Weights are scaled by 2^60 to meet the 2^-133.
 //
 // Softmax: a running reference m for each head, moved only when a score exceeds it by 8 (log2): then sums and O are
 // rescaled. It starts at -1e30, not -inf, so that no difference of infinities arises.
-constexpr int WARPS = 4, STAGES = 4, STEP_BYTES = 2304;  // 16 keys: K and V codes 1024 each, parameters 128 each
-constexpr float M_START = -1e30f, M_SLACK = 8.f;
+constexpr int WARPS = 4, STAGES = 2, UNIT = 32, UNIT_BYTES = 4608;  // K and V codes 2048 each, parameters 256 each
+constexpr int V_AT = 2048, KP_AT = 4096, VP_AT = 4352;
+constexpr float M_START = -1e30f, M_SLACK = 8.f, P_LOG2 = 60.f;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -300,54 +310,81 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile(
+__device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// nibble j of both halves of w as bf16 whole numbers, with the offsets added (exact)
-__device__ __forceinline__ uint32_t whole(uint32_t w, int j, uint32_t off) {
+__device__ __forceinline__ void mma_e4m3(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
-    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"((w >> (4 * j) & 0x000F000Fu) | 0x43004300u), "r"(off));
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
 __device__ __forceinline__ uint32_t lows(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 __device__ __forceinline__ uint32_t highs(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 __device__ __forceinline__ float as_f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t as_u(float x) { return __float_as_uint(x); }
-// part (0, 1, 2) of x: 8 significant bits each, by truncation; m1, m2 cover the upper half where part >= 1, 2
+__device__ __forceinline__ float scale_of(uint32_t par) { return as_f(par << 16); }
+__device__ __forceinline__ float zero_of(uint32_t par) { return as_f(par & 0xFFFF0000u) + 128.f; }
+// bf16 part (0, 1, 2) of x: 8 significant bits each, by truncation; m1, m2 cover the upper half where part >= 1, 2
 __device__ __forceinline__ uint32_t part_of(float x, uint32_t m1, uint32_t m2) {
     x -= as_f(as_u(x) & m1);
     return as_u(x - as_f(as_u(x) & m2));
 }
-
-// The B registers of Q for this lane's column: step s = 2 word + half, dims 64 g + 16 c + 8 (word >> 1) + 2 half + {0, 1} and + 4.
-__device__ __forceinline__ void load_q(const bf16* q, int n, int c, uint32_t (&b)[16]) {
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const uint4 v = *reinterpret_cast<const uint4*>(q + (n & 1) * HD + 64 * (w & 1) + 16 * c + 8 * (w >> 1));
-        b[4 * w] = lows(v.x, v.z);
-        b[4 * w + 1] = highs(v.x, v.z);
-        b[4 * w + 2] = lows(v.y, v.w);
-        b[4 * w + 3] = highs(v.y, v.w);
-    }
-}
-__device__ __forceinline__ void load_q(const float* q, int n, int c, uint32_t (&b)[16]) {
-    const uint32_t m1 = n >= 2 ? 0xFFFF0000u : 0u, m2 = n >= 4 ? 0xFFFF0000u : 0u, on = n < 6 ? ~0u : 0u;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float* p = q + (n & 1) * HD + 64 * (w & 1) + 16 * c + 8 * (w >> 1);
-        const float4 u = load4(p), v = load4(p + 4);
-        b[4 * w] = on & highs(part_of(u.x, m1, m2), part_of(v.x, m1, m2));
-        b[4 * w + 1] = on & highs(part_of(u.y, m1, m2), part_of(v.y, m1, m2));
-        b[4 * w + 2] = on & highs(part_of(u.z, m1, m2), part_of(v.z, m1, m2));
-        b[4 * w + 3] = on & highs(part_of(u.w, m1, m2), part_of(v.w, m1, m2));
-    }
+// two values to e4m3 (x in the low byte); what the rounding leaves of them stays in x, y
+__device__ __forceinline__ uint32_t split_e4m3(float& x, float& y) {
+    uint16_t d;
+    uint32_t h;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(y), "f"(x));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(d));
+    const __half2 v = *reinterpret_cast<const __half2*>(&h);
+    x -= __low2float(v);
+    y -= __high2float(v);
+    return d;
 }
 
+// One warp's share of the queries: a head's 128 values (lane l: dims 4l .. 4l + 3) as e4m3 parts in `to` (bytes [part]
+// [2 heads][2 groups][8 pieces][even dims, odd dims], to: this head's) and in `about` its group sums, in the units of the
+// e4m3 sums, and the factor that turns those into scores times log2(e) (NaN where a query is not finite).
+template <int PARTS, typename T>
+__device__ __forceinline__ void stage_q(const T* q, int lane, uint8_t* to, float* about) {
+    const float4 v = load4(q + lane * 4);
+    const float a = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+    // fmaxf drops a NaN
+    const bool fine = __all_sync(0xffffffffu, a < INFINITY && v.x == v.x && v.y == v.y && v.z == v.z && v.w == v.w);
+    // 2^(7 - exponent of the largest), the largest taken as at least 2^-110
+    const float up = __uint_as_float((261u - max(__float_as_uint(fine ? warp_max(a) : 1.f) >> 23, 17u)) << 23);
+    float s = (v.x + v.y) + (v.z + v.w);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((lane & 15) == 0) about[lane >> 4] = s * up * 0x1p-9f;
+    if (lane == 0) about[2] = fine ? rsqrtf((float)HD) * LOG2E * 512.f / up : __int_as_float(0x7FC00000);
+    float x[2][2] = {{v.x * up, v.z * up}, {v.y * up, v.w * up}};
+    to += (lane >> 1) * 8 + (lane & 1) * 2;
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+        for (int odd = 0; odd < 2; ++odd) {
+            *reinterpret_cast<uint16_t*>(to + p * 256 + odd * 4) = (uint16_t)split_e4m3(x[odd][0], x[odd][1]);
+            if (PARTS > 2) { x[odd][0] *= 16.f; x[odd][1] *= 16.f; }
+        }
+}
+
+// seq's unit i of this warp: block j0 + 2 i + (warp >> 1), keys 32 (warp & 1) .. + 31 of it
 template <typename T>
-__global__ void __launch_bounds__(WARPS * 32, 5) k_kv4_attn(const T* __restrict__ q, Cache cache, AttnArgs a, T* __restrict__ out) {
+__global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict__ q, Cache cache, AttnArgs a, T* __restrict__ out) {
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int P = F32 ? 3 : 2;  // bf16 parts of a weight
     pdl_wait();  // upstream results are read below
@@ -356,84 +393,95 @@ __global__ void __launch_bounds__(WARPS * 32, 5) k_kv4_attn(const T* __restrict_
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     int seq, seen;
     if (!attn_row(cache, a, row, threadIdx.x == 0 && split == 0 && g == 0, seq, seen)) return;
-    const int j0 = split * a.bps, j1 = min((seen + KVB - 1) / KVB, j0 + a.bps), n = max(0, j1 - j0);
+    const int j0 = split * a.bps + (warp >> 1), j1 = min((seen + KVB - 1) / KVB, (split + 1) * a.bps);
+    const int n = max(0, (j1 - j0 + 1) >> 1);
 
     extern __shared__ __align__(128) uint8_t ring[];
-    uint8_t* const mine = ring + warp * STAGES * STEP_BYTES;
+    uint8_t* const mine = ring + warp * STAGES * UNIT_BYTES;
     const uint32_t dst = (uint32_t)__cvta_generic_to_shared(mine);
-    const uint8_t* const src = cache.pool + (size_t)g * TILE + warp * 1024;
+    const uint8_t* const src = cache.pool + (size_t)g * TILE + (warp & 1) * 2048 + lane * 16;
     const int32_t* const pages = cache.table + (size_t)seq * cache.bps + j0;
     // 16-byte pieces of V rows are swapped between the row's halves for rows 2, 3 of every 4, so that the 8-byte reads
     // of 4 rows meet all 32 banks
-    const uint32_t vdst = 1024 + (lane * 16 ^ (lane >> 3 & 1) * 32);
-    const int ppiece = (lane & 8 ? NKV * TILE : 0) + PAR - warp * 1024 + warp * 128 + (lane & 7) * 16;
+    const uint32_t vdst = V_AT + (lane * 16 ^ (lane >> 3 & 1) * 32);
+    const int ppiece = (lane & 16 ? NKV * TILE : 0) + PAR + (warp & 1) * (256 - 2048) + ((lane & 15) - lane) * 16;
     uint32_t missing = 0;  // bit s: the block in stage s has no page
-    auto fetch = [&](int i, int page) {
-        const int s = i % STAGES;
+    auto fetch = [&](int s, int page) {
         const bool ok = page >= 0 && page < cache.n_blocks;
         missing = missing & ~(1u << s) | (ok ? 0u : 1u << s);
         if (ok) {
             const uint8_t* b = src + (size_t)page * BLOCK;
-            const uint32_t d = dst + s * STEP_BYTES;
-            cp16(d + lane * 16, b + lane * 16);
-            cp16(d + 512 + lane * 16, b + 512 + lane * 16);
-            cp16(d + vdst, b + NKV * TILE + lane * 16);
-            cp16(d + 512 + vdst, b + NKV * TILE + 512 + lane * 16);
-            if (lane < 16) cp16(d + 2048 + lane * 16, b + ppiece);
+            const uint32_t d = dst + s * UNIT_BYTES;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                cp16(d + lane * 16 + 512 * i, b + 512 * i);
+                cp16(d + vdst + 512 * i, b + NKV * TILE + 512 * i);
+            }
+            cp16(d + KP_AT + lane * 16, b + ppiece);
         } else if (lane == 0) {
             set_err(cache.err, TTS_BB_KV4_ERR_PAGE);
         }
     };
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) {
-        if (i < n) fetch(i, pages[i]);
+        if (i < n) fetch(i, pages[2 * i]);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    int page = n > STAGES - 1 ? pages[STAGES - 1] : 0;
+    int page = n > STAGES - 1 ? pages[2 * (STAGES - 1)] : 0;
 
-    uint32_t qb[16];
-    load_q(q + ((size_t)row * NQ + 2 * g) * HD, r, c, qb);
+    __shared__ __align__(16) uint8_t sq[F32 ? 8 : 2][256];
+    __shared__ float about[2][4];
+    if (warp < 2)
+        stage_q<F32 ? 8 : 2>(q + ((size_t)row * NQ + 2 * g + warp) * HD, lane, &sq[0][warp * HD], about[warp]);
+    __syncthreads();
+    uint2 qb[2][4];    // [part, or tile of 4 parts][word]: even dims, odd dims
+    float qsum[2][2];  // [head][group]; fp32: in lane c = 0 of 4
+    const float factor = about[c >> 1][2], weight = F32 ? 1.f / (float)(1 << 4 * c) : 1.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            qb[h][w] = *reinterpret_cast<const uint2*>(&sq[F32 ? 4 * h + (r >> 1) : h][(r & 1) * HD + 64 * (w & 1) + 16 * c + 8 * (w >> 1)]);
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) qsum[h][gr] = F32 && c ? 0.f : about[h][gr];
+    }
     const uint32_t m1 = r >= 2 ? 0xFFFF0000u : 0u, m2 = r >= 4 ? 0xFFFF0000u : 0u;
     const uint32_t half_sel = r & 2 ? 0x5410u : 0x7632u;  // bf16: part 0 in the high halves, part 1 in the low ones
     const int from = 4 * c + 2 * (r & 1);                 // the lane that has the weight of key c of this column's head
     const int my = r + 8 * (c & 1);                       // this lane's key of 16; its head is c >> 1
-    const float sc = rsqrtf((float)HD) * LOG2E;
-    float o[8][4] = {}, m = M_START, l = 0.f;
+    const uint8_t* const kat = mine + r * 64 + c * 16;
+    const uint8_t* const vat = mine + V_AT + c * 64 + (r * 8 ^ (c >> 1) * 32);
+    float o[8][4] = {}, m = M_START - P_LOG2, l = 0.f;    // m: the reference less P_LOG2
 
-    for (int i = 0; i < n; ++i) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-        __syncwarp();
-        if (i + STAGES - 1 < n) fetch(i + STAGES - 1, page);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (i + STAGES < n) page = pages[i + STAGES];
-        const int key0 = (j0 + i) * KVB + warp * 16;
-        if (key0 >= seen || (missing >> (i % STAGES) & 1)) continue;
-        const uint8_t* st = mine + (i % STAGES) * STEP_BYTES;
-        const bool tail = key0 + 16 > seen;
-        const bool on = key0 + my < seen;
+    // 16 keys: codes at byte `at` of the ring, parameters at `par`
+    auto step = [&](auto tail, const int at, const int par, const int key0) {
+        constexpr bool TAIL = decltype(tail)::value;
 
-        // scores
         float z;
         {
-            const uint4 k0 = *reinterpret_cast<const uint4*>(st + r * 64 + c * 16);
-            const uint4 k1 = *reinterpret_cast<const uint4*>(st + (r + 8) * 64 + c * 16);
-            const uint2 p0 = *reinterpret_cast<const uint2*>(st + 2048 + r * 8);
-            const uint2 p1 = *reinterpret_cast<const uint2*>(st + 2048 + (r + 8) * 8);
+            const uint4 k0 = *reinterpret_cast<const uint4*>(kat + at);
+            const uint4 k1 = *reinterpret_cast<const uint4*>(kat + at + 512);
+            const uint2 p0 = *reinterpret_cast<const uint2*>(mine + par + KP_AT + r * 8);
+            const uint2 p1 = *reinterpret_cast<const uint2*>(mine + par + KP_AT + r * 8 + 64);
             const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-            const uint32_t off0[2] = {highs(p0.x, p0.x), highs(p0.y, p0.y)}, off1[2] = {highs(p1.x, p1.x), highs(p1.y, p1.y)};
-            float s[2][4] = {};
+            float s[2][2][4] = {};  // [fp32: tile][group]
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t x[4] = {whole(w0[w], 2 * h, off0[w & 1]), whole(w1[w], 2 * h, off1[w & 1]),
-                                           whole(w0[w], 2 * h + 1, off0[w & 1]), whole(w1[w], 2 * h + 1, off1[w & 1])};
-                    mma(s[w & 1], x, qb[4 * w + 2 * h], qb[4 * w + 2 * h + 1]);
-                }
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t x[4] = {w0[w] & 0x0F0F0F0Fu, w1[w] & 0x0F0F0F0Fu, w0[w] >> 4 & 0x0F0F0F0Fu, w1[w] >> 4 & 0x0F0F0F0Fu};
+                mma_e4m3(s[0][w & 1], x, qb[0][w].x, qb[0][w].y);
+                mma_e4m3(s[F32][w & 1], x, qb[1][w].x, qb[1][w].y);
+            }
             float y[4];  // (key r, head 0), (r, 1), (r + 8, 0), (r + 8, 1)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                y[e] = as_f((e < 2 ? p0.x : p1.x) << 16) * s[0][e] + as_f((e < 2 ? p0.y : p1.y) << 16) * s[1][e];
+            for (int e = 0; e < 4; ++e) {
+                const uint2 pr = e < 2 ? p0 : p1;
+                float y0 = s[0][0][e], y1 = s[0][1][e];
+                if (F32) { y0 += 0x1p-16f * s[1][0][e]; y1 += 0x1p-16f * s[1][1][e]; }
+                y0 += zero_of(pr.x) * qsum[e & 1][0];
+                y1 += zero_of(pr.y) * qsum[e & 1][1];
+                y[e] = scale_of(pr.x) * y0 + scale_of(pr.y) * y1;
+                if (F32) y[e] *= weight;
+            }
             if constexpr (F32) {  // the four columns' parts added; each lane ends with its own key and head
                 const float a0 = c & 1 ? y[2] : y[0], a1 = c & 1 ? y[3] : y[1];
                 const float b0 = c & 1 ? y[0] : y[2], b1 = c & 1 ? y[1] : y[3];
@@ -442,15 +490,17 @@ __global__ void __launch_bounds__(WARPS * 32, 5) k_kv4_attn(const T* __restrict_
             } else {
                 z = c & 2 ? (c & 1 ? y[3] : y[1]) : (c & 1 ? y[2] : y[0]);
             }
-            z = on ? z * sc : -INFINITY;
+            z *= factor;
         }
-        if (__any_sync(0xffffffffu, z > m + M_SLACK)) {
+        const bool on = !TAIL || key0 + my < seen;
+        if (!on) z = -INFINITY;
+        if (__any_sync(0xffffffffu, z > m + (M_SLACK + P_LOG2))) {
             float mx = z;
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float nm = fmaxf(m, mx), f = ex2(m - nm), other = __shfl_xor_sync(0xffffffffu, f, 2);
+            const float nm = fmaxf(m, mx - P_LOG2), f = ex2(m - nm), other = __shfl_xor_sync(0xffffffffu, f, 2);
             const float f0 = c & 2 ? other : f, f1 = c & 2 ? f : other;
             m = nm;
             l *= f;
@@ -460,47 +510,73 @@ __global__ void __launch_bounds__(WARPS * 32, 5) k_kv4_attn(const T* __restrict_
                 o[t][2] *= f0; o[t][3] *= f1;
             }
         }
-        const float p = on ? ex2(z - m) : 0.f;
-        l += p;
-
-        // output
-        const uint2 vp = *reinterpret_cast<const uint2*>(st + 2176 + my * 8);
-        uint2 w[4], pp[4];  // codes and parameters of keys c, c + 4, c + 8, c + 12
+        {
+            const float p = ex2(z - m);
+            l += p;
+            const uint2 vp = *reinterpret_cast<const uint2*>(mine + par + VP_AT + my * 8);
+            float ps[2] = {p * scale_of(vp.x), p * scale_of(vp.y)};
+            uint2 w[4], pp[4];  // codes and parameters of keys c, c + 4, c + 8, c + 12
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            w[k] = *reinterpret_cast<const uint2*>(st + 1024 + (c + 4 * k) * 64 + (r * 8 ^ (c >> 1) * 32));
-            pp[k] = *reinterpret_cast<const uint2*>(st + 2176 + (c + 4 * k) * 8);
-            if (tail && key0 + c + 4 * k >= seen) pp[k] = make_uint2(0u, 0u);  // an offset that is not finite times a zero
-        }
-#pragma unroll
-        for (int gr = 0; gr < 2; ++gr) {
-            const float x = on ? p * as_f((gr ? vp.y : vp.x) << 16) : 0.f;
-            uint32_t b0, b1;
-            if constexpr (F32) {
-                uint32_t y[4];
+            for (int k = 0; k < 4; ++k) {
+                w[k] = *reinterpret_cast<const uint2*>(vat + at + k * 256);
+                pp[k] = *reinterpret_cast<const uint2*>(mine + par + VP_AT + c * 8 + k * 32);
+            }
+            if constexpr (TAIL) {  // parameters behind the keys may be anything: no scale or offset that is not finite times a zero
+                if (!on) ps[0] = ps[1] = 0.f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    y[k] = part_of(__shfl_sync(0xffffffffu, x, from + (k & 1) * 16 + (k >> 1)), m1, m2);
-                b0 = highs(y[0], y[1]);
-                b1 = highs(y[2], y[3]);
-            } else {
-                const uint32_t both = highs(as_u(x - as_f(as_u(x) & 0xFFFF0000u)), as_u(x));  // part 1 below part 0
-                uint32_t y[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, both, from + (k & 1) * 16 + (k >> 1));
-                b0 = __byte_perm(y[0], y[1], half_sel);
-                b1 = __byte_perm(y[2], y[3], half_sel);
+                    if (key0 + c + 4 * k >= seen) pp[k] = make_uint2(0u, 0u);
             }
-            const uint32_t v0 = gr ? w[0].y : w[0].x, v1 = gr ? w[1].y : w[1].x, v2 = gr ? w[2].y : w[2].x, v3 = gr ? w[3].y : w[3].x;
-            const uint32_t off01 = highs(gr ? pp[0].y : pp[0].x, gr ? pp[1].y : pp[1].x);
-            const uint32_t off23 = highs(gr ? pp[2].y : pp[2].x, gr ? pp[3].y : pp[3].x);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const uint32_t u01 = t < 2 ? lows(v0, v1) : highs(v0, v1), u23 = t < 2 ? lows(v2, v3) : highs(v2, v3);
-                const int j = 2 * (t & 1);
-                const uint32_t x4[4] = {whole(u01, j, off01), whole(u01, j + 1, off01), whole(u23, j, off23), whole(u23, j + 1, off23)};
-                mma(o[4 * gr + t], x4, b0, b1);
+            for (int gr = 0; gr < 2; ++gr) {
+                const float x = ps[gr];
+                uint32_t y[4], b0, b1;
+                if constexpr (F32) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        y[k] = part_of(__shfl_sync(0xffffffffu, x, from + (k & 1) * 16 + (k >> 1)), m1, m2);
+                    b0 = highs(y[0], y[1]);
+                    b1 = highs(y[2], y[3]);
+                } else {
+                    const uint32_t both = highs(as_u(x - as_f(as_u(x) & 0xFFFF0000u)), as_u(x));  // part 1 below part 0
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, both, from + (k & 1) * 16 + (k >> 1));
+                    b0 = __byte_perm(y[0], y[1], half_sel);
+                    b1 = __byte_perm(y[2], y[3], half_sel);
+                }
+                uint32_t zero[2][2];  // [keys 0 1, keys 2 3][even, odd dims]: zero 2^-133, 16 zero 2^-133
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t off = highs(gr ? pp[2 * h].y : pp[2 * h].x, gr ? pp[2 * h + 1].y : pp[2 * h + 1].x);
+                    zero[h][0] = fma_bf16x2(off, 0x00010001u, 0x00800080u);
+                    zero[h][1] = fma_bf16x2(off, 0x00100010u, 0x02800280u);
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {  // byte t of the words: dims 2 t, 2 t + 1 of lane r's 8
+                    const uint32_t sel = 0x0400u + 0x1111u * t;
+                    const uint32_t u01 = __byte_perm(gr ? w[0].y : w[0].x, gr ? w[1].y : w[1].x, sel);
+                    const uint32_t u23 = __byte_perm(gr ? w[2].y : w[2].x, gr ? w[3].y : w[3].x, sel);
+                    const uint32_t x4[4] = {add_bf16x2(u01 & 0x000F000Fu, zero[0][0]), add_bf16x2(u01 & 0x00F000F0u, zero[0][1]),
+                                            add_bf16x2(u23 & 0x000F000Fu, zero[1][0]), add_bf16x2(u23 & 0x00F000F0u, zero[1][1])};
+                    mma_bf16(o[4 * gr + t], x4, b0, b1);
+                }
             }
+        }
+    };
+    for (int i = 0; i < n; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+        __syncwarp();
+        if (i + STAGES - 1 < n) fetch((i + STAGES - 1) % STAGES, page);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (i + STAGES < n) page = pages[2 * (i + STAGES)];
+        const int key0 = (j0 + 2 * i) * KVB + (warp & 1) * UNIT;
+        if (key0 >= seen || (missing >> (i % STAGES) & 1)) continue;
+        const int at = (i % STAGES) * UNIT_BYTES;
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+            const int k = key0 + 16 * u;
+            if (k + 16 <= seen) step(std::false_type{}, at + 1024 * u, at + 128 * u, k);
+            else if (k < seen) step(std::true_type{}, at + 1024 * u, at + 128 * u, k);
         }
     }
     // merge the warps: every part of O to shared memory, then one thread for each dim
@@ -518,15 +594,16 @@ __global__ void __launch_bounds__(WARPS * 32, 5) k_kv4_attn(const T* __restrict_
             const int d = 64 * (t >> 2) + 8 * r + 2 * (t & 3);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<float2*>(so + ((warp * P + c) * 2 + h) * HD + d) = make_float2(o[t][h], o[t][2 + h]);
+                *reinterpret_cast<float2*>(so + ((warp * P + c) * 2 + h) * HD + d) =
+                    make_float2(o[t][h] * 0x1p73f, o[t][2 + h] * 0x1p69f);
         }
     }
-    if (lane == 0 || lane == 2) { sm[warp][lane >> 1] = m; sl[warp][lane >> 1] = l; }
+    if (lane == 0 || lane == 2) { sm[warp][lane >> 1] = m; sl[warp][lane >> 1] = l * 0x1p-60f; }
     __syncthreads();
     const int d = threadIdx.x;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        float M = M_START, L = 0.f, O = 0.f;
+        float M = M_START - P_LOG2, L = 0.f, O = 0.f;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm[w][h]);
 #pragma unroll
@@ -557,7 +634,7 @@ __global__ void __launch_bounds__(128) k_kv4_combine(Cache c, AttnArgs a, T* __r
     int seq, seen;
     if (!attn_row(c, a, rh / NQ, false, seq, seen)) return;
     const float* p = a.part + (size_t)rh * a.n_splits * (HD + 2);
-    float M = M_START, L = 0.f, O = 0.f;
+    float M = M_START - P_LOG2, L = 0.f, O = 0.f;
     for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, p[s * (HD + 2) + HD]);
     for (int s = 0; s < a.n_splits; ++s) {
         const float f = ex2(p[s * (HD + 2) + HD] - M);
@@ -573,7 +650,7 @@ struct Plan {
 };
 Plan attn_plan(long long rows, int max_len) {
     const int nblk = (max_len + KVB - 1) / KVB;
-    const long long want = (32ll * 152 + rows * NKV - 1) / (rows * NKV);
+    const long long want = (8ll * 152 + rows * NKV - 1) / (rows * NKV);
     const int splits = (int)std::max(1ll, std::min({want, (long long)nblk, (long long)MAX_SPLITS}));
     const int bps = (nblk + splits - 1) / splits;
     return {(nblk + bps - 1) / bps, bps};
@@ -668,7 +745,7 @@ TTS_API tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S
     const dim3 grid(p.splits, NKV, B * S);
     auto go = [&](auto t) {
         typedef decltype(t) T;
-        launch_pdl(k_kv4_attn<T>, grid, WARPS * 32, WARPS * STAGES * STEP_BYTES, st, static_cast<const T*>(q), c, a, static_cast<T*>(out));
+        launch_pdl(k_kv4_attn<T>, grid, WARPS * 32, WARPS * STAGES * UNIT_BYTES, st, static_cast<const T*>(q), c, a, static_cast<T*>(out));
         if (p.splits > 1) launch_pdl(k_kv4_combine<T>, B * S * NQ, 128, 0, st, c, a, static_cast<T*>(out));
     };
     if (type == TTS_BB_T_F32) go(float{});
