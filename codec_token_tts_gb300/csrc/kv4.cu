@@ -279,15 +279,16 @@ __device__ __forceinline__ bool attn_row(const Cache& c, const AttnArgs& a, int 
 // warps until the end. What bounds it beside memory are the integer instructions that take nibbles apart (two a cycle
 // and SM), so both products take the codes with as few of them as they can:
 //
-// Scores, S[key][column] = K Q^T, by m16n8k32 on e4m3: the byte 0000cccc is c 2^-9 (subnormals and the first binade are
-// evenly spaced), so a word of 8 codes is two operands after one shift and two masks. Lane (r = lane / 4, c = lane % 4) reads
-// 16 bytes of the code rows of keys r and r + 8: 16 dims of each group, even and odd dims apart, which only permutes the
-// contraction. Products are exact and sums fp32. The zero point joins by the queries' sum: s (sum q code + zero sum q).
-// Q, scaled by a power of two to a largest magnitude in [128, 256), enters as e4m3 parts of 4 bits, each the rounding of what
-// the ones before it leave. bf16: two parts hold its 8 bits (below 2^-14 of the head's largest: to 2^-18 of that),
-// multiplied one after the other into the same sums; column n holds head n & 1, so every lane has both heads' scores of
-// its keys. fp32: eight parts, part p scaled up by 16^p, column n of two column tiles holding part n >> 1 (+ 4) of head n & 1.
-// Each lane then keeps one score of 16 keys: key r + 8 (c & 1), head c >> 1.
+// Scores, S[key][column] = K Q^T, by m16n8k16 on fp16: the half word 000c is the fp16 number c 2^-24 and 00c0 16 c 2^-24
+// (subnormals and the first binade are evenly spaced), so a word of 8 codes is two steps' operands after one shift and
+// four masks. Lane (r = lane / 4, c = lane % 4) reads 16 bytes of the code rows of keys r and r + 8: 16 dims of each group, in
+// pairs (d, d + 4), which only permutes the contraction; Q of the dims that come as 16 c is divided by 16. Products are exact
+// and sums fp32. The zero point joins by the queries' sum: s (sum q code + zero sum q). Q is scaled by a power of two to a
+// largest magnitude in [2^14, 2^15). bf16 queries are then exact in fp16 (down to 2^-25 of the head's largest); column n
+// holds head n & 1, so every lane has both heads' scores of its keys. fp32 queries enter as two fp16 parts, 24 bits
+// together, part (n >> 1) & 1 of head n & 1 in column n.
+// Each lane then keeps one score of 16 keys: key r + 8 (c & 1), head c >> 1. (By m16n8k32 on e4m3, where a byte of two masks
+// is 4 operands, the same took longer: that form is carried out by fp16 products after conversions.)
 //
 // Output, O^T[dim][column] += V^T P, by m16n8k16 on bf16, V's codes as A: rows are dims, and a register holds one dim of
 // two keys: one byte of both keys' words side by side, then one mask for the byte's even dim and one for its odd dim:
@@ -316,9 +317,8 @@ __device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_e4m3(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -343,42 +343,32 @@ __device__ __forceinline__ uint32_t part_of(float x, uint32_t m1, uint32_t m2) {
     x -= as_f(as_u(x) & m1);
     return as_u(x - as_f(as_u(x) & m2));
 }
-// two values to e4m3 (x in the low byte); what the rounding leaves of them stays in x, y
-__device__ __forceinline__ uint32_t split_e4m3(float& x, float& y) {
-    uint16_t d;
-    uint32_t h;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(y), "f"(x));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(d));
-    const __half2 v = *reinterpret_cast<const __half2*>(&h);
-    x -= __low2float(v);
-    y -= __high2float(v);
-    return d;
-}
-
-// One warp's share of the queries: a head's 128 values (lane l: dims 4l .. 4l + 3) as e4m3 parts in `to` (bytes [part]
-// [2 heads][2 groups][8 pieces][even dims, odd dims], to: this head's) and in `about` its group sums, in the units of the
-// e4m3 sums, and the factor that turns those into scores times log2(e) (NaN where a query is not finite).
+// One warp's share of the queries: a head's 128 values (lane l: dims 4l .. 4l + 3) as fp16 parts in `to` ([part][2 heads] rows of
+// 128, to: this head's; 8 dims stand as 0 4 1 5 2 6 3 7, the odd ones divided by 16) and in `about` its group sums,
+// in the units of the products' sums, and the factor that turns those into scores times log2(e) (NaN where a query is not
+// finite).
 template <int PARTS, typename T>
-__device__ __forceinline__ void stage_q(const T* q, int lane, uint8_t* to, float* about) {
+__device__ __forceinline__ void stage_q(const T* q, int lane, __half* to, float* about) {
     const float4 v = load4(q + lane * 4);
     const float a = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
     // fmaxf drops a NaN
     const bool fine = __all_sync(0xffffffffu, a < INFINITY && v.x == v.x && v.y == v.y && v.z == v.z && v.w == v.w);
-    // 2^(7 - exponent of the largest), the largest taken as at least 2^-110
-    const float up = __uint_as_float((261u - max(__float_as_uint(fine ? warp_max(a) : 1.f) >> 23, 17u)) << 23);
+    // 2^(14 - exponent of the largest), the largest taken as at least 2^-103
+    const float up = __uint_as_float((268u - max(__float_as_uint(fine ? warp_max(a) : 1.f) >> 23, 24u)) << 23);
     float s = (v.x + v.y) + (v.z + v.w);
 #pragma unroll
     for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if ((lane & 15) == 0) about[lane >> 4] = s * up * 0x1p-9f;
-    if (lane == 0) about[2] = fine ? rsqrtf((float)HD) * LOG2E * 512.f / up : __int_as_float(0x7FC00000);
-    float x[2][2] = {{v.x * up, v.z * up}, {v.y * up, v.w * up}};
-    to += (lane >> 1) * 8 + (lane & 1) * 2;
+    if ((lane & 15) == 0) about[lane >> 4] = s * up * 0x1p-24f;
+    if (lane == 0) about[2] = fine ? rsqrtf((float)HD) * LOG2E * 0x1p24f / up : __int_as_float(0x7FC00000);
+    float x[4] = {v.x * up, v.y * up, v.z * up, v.w * up};
+    to += (lane >> 1) * 8 + (lane & 1);
 #pragma unroll
     for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-        for (int odd = 0; odd < 2; ++odd) {
-            *reinterpret_cast<uint16_t*>(to + p * 256 + odd * 4) = (uint16_t)split_e4m3(x[odd][0], x[odd][1]);
-            if (PARTS > 2) { x[odd][0] *= 16.f; x[odd][1] *= 16.f; }
+        for (int e = 0; e < 4; ++e) {
+            const __half h = __float2half_rn(x[e]);
+            x[e] -= __half2float(h);
+            to[p * 2 * HD + e * 2] = e & 1 ? __hmul(h, __float2half_rn(0.0625f)) : h;
         }
 }
 
@@ -429,22 +419,20 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict_
     }
     int page = n > STAGES - 1 ? pages[2 * (STAGES - 1)] : 0;
 
-    __shared__ __align__(16) uint8_t sq[F32 ? 8 : 2][256];
+    __shared__ __align__(16) __half sq[F32 ? 2 : 1][2][HD];
     __shared__ float about[2][4];
-    if (warp < 2)
-        stage_q<F32 ? 8 : 2>(q + ((size_t)row * NQ + 2 * g + warp) * HD, lane, &sq[0][warp * HD], about[warp]);
+    if (warp < 2) stage_q<F32 ? 2 : 1>(q + ((size_t)row * NQ + 2 * g + warp) * HD, lane, sq[0][warp], about[warp]);
     __syncthreads();
-    uint2 qb[2][4];    // [part, or tile of 4 parts][word]: even dims, odd dims
-    float qsum[2][2];  // [head][group]; fp32: in lane c = 0 of 4
-    const float factor = about[c >> 1][2], weight = F32 ? 1.f / (float)(1 << 4 * c) : 1.f;
+    uint4 qb[4];       // of word w: the B registers of its two steps
+    float qsum[2][2];  // [head][group]; fp32: in the lanes of part 0
+    const float factor = about[c >> 1][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int w = 0; w < 4; ++w)
+        qb[w] = *reinterpret_cast<const uint4*>(&sq[F32 ? r >> 1 & 1 : 0][r & 1][64 * (w & 1) + 16 * c + 8 * (w >> 1)]);
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-            qb[h][w] = *reinterpret_cast<const uint2*>(&sq[F32 ? 4 * h + (r >> 1) : h][(r & 1) * HD + 64 * (w & 1) + 16 * c + 8 * (w >> 1)]);
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int gr = 0; gr < 2; ++gr) qsum[h][gr] = F32 && c ? 0.f : about[h][gr];
-    }
+        for (int gr = 0; gr < 2; ++gr) qsum[h][gr] = F32 && (c & 1) ? 0.f : about[h][gr];
     const uint32_t m1 = r >= 2 ? 0xFFFF0000u : 0u, m2 = r >= 4 ? 0xFFFF0000u : 0u;
     const uint32_t half_sel = r & 2 ? 0x5410u : 0x7632u;  // bf16: part 0 in the high halves, part 1 in the low ones
     const int from = 4 * c + 2 * (r & 1);                 // the lane that has the weight of key c of this column's head
@@ -464,32 +452,25 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict_
             const uint2 p0 = *reinterpret_cast<const uint2*>(mine + par + KP_AT + r * 8);
             const uint2 p1 = *reinterpret_cast<const uint2*>(mine + par + KP_AT + r * 8 + 64);
             const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-            float s[2][2][4] = {};  // [fp32: tile][group]
+            float s[2][4] = {};  // of each group
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const uint32_t x[4] = {w0[w] & 0x0F0F0F0Fu, w1[w] & 0x0F0F0F0Fu, w0[w] >> 4 & 0x0F0F0F0Fu, w1[w] >> 4 & 0x0F0F0F0Fu};
-                mma_e4m3(s[0][w & 1], x, qb[0][w].x, qb[0][w].y);
-                mma_e4m3(s[F32][w & 1], x, qb[1][w].x, qb[1][w].y);
+                const uint32_t u0 = w0[w] >> 8, u1 = w1[w] >> 8;
+                const uint32_t x[4] = {w0[w] & 0x000F000Fu, w1[w] & 0x000F000Fu, w0[w] & 0x00F000F0u, w1[w] & 0x00F000F0u};
+                const uint32_t y[4] = {u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x00F000F0u};
+                mma_f16(s[w & 1], x, qb[w].x, qb[w].y);
+                mma_f16(s[w & 1], y, qb[w].z, qb[w].w);
             }
             float y[4];  // (key r, head 0), (r, 1), (r + 8, 0), (r + 8, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint2 pr = e < 2 ? p0 : p1;
-                float y0 = s[0][0][e], y1 = s[0][1][e];
-                if (F32) { y0 += 0x1p-16f * s[1][0][e]; y1 += 0x1p-16f * s[1][1][e]; }
-                y0 += zero_of(pr.x) * qsum[e & 1][0];
-                y1 += zero_of(pr.y) * qsum[e & 1][1];
+                const float y0 = s[0][e] + zero_of(pr.x) * qsum[e & 1][0], y1 = s[1][e] + zero_of(pr.y) * qsum[e & 1][1];
                 y[e] = scale_of(pr.x) * y0 + scale_of(pr.y) * y1;
-                if (F32) y[e] *= weight;
             }
-            if constexpr (F32) {  // the four columns' parts added; each lane ends with its own key and head
-                const float a0 = c & 1 ? y[2] : y[0], a1 = c & 1 ? y[3] : y[1];
-                const float b0 = c & 1 ? y[0] : y[2], b1 = c & 1 ? y[1] : y[3];
-                const float u0 = a0 + __shfl_xor_sync(0xffffffffu, b0, 1), u1 = a1 + __shfl_xor_sync(0xffffffffu, b1, 1);
-                z = (c & 2 ? u1 : u0) + __shfl_xor_sync(0xffffffffu, c & 2 ? u0 : u1, 2);
-            } else {
-                z = c & 2 ? (c & 1 ? y[3] : y[1]) : (c & 1 ? y[2] : y[0]);
-            }
+            const float a0 = c & 2 ? y[1] : y[0], a1 = c & 2 ? y[3] : y[2];  // this lane's head: keys r, r + 8
+            z = c & 1 ? a1 : a0;
+            if (F32) z += __shfl_xor_sync(0xffffffffu, c & 1 ? a0 : a1, 1);  // the other part's sum
             z *= factor;
         }
         const bool on = !TAIL || key0 + my < seen;
