@@ -256,8 +256,8 @@ __global__ void __launch_bounds__(256) k_kv4_read(const int32_t* __restrict__ se
 struct AttnArgs {
     const int32_t* seqs;
     const int32_t* kv_lens;
-    int S, max_len, n_splits, bps;  // bps: cache blocks of one split
-    float* part;                    // [rows][16][n_splits][130]: output sums, running max, running sum
+    int S, max_len, rows, n_splits;
+    float* part;  // pieces: 128 output sums, reference, sum of weights
 };
 
 // Row r = (b, s): the cache row it reads and the keys it sees; false where the row is left as it was.
@@ -347,9 +347,8 @@ __device__ __forceinline__ uint32_t part_of(float x, uint32_t m1, uint32_t m2) {
 // 128, to: this head's; 8 dims stand as 0 4 1 5 2 6 3 7, the odd ones divided by 16) and in `about` its group sums,
 // in the units of the products' sums, and the factor that turns those into scores times log2(e) (NaN where a query is not
 // finite).
-template <int PARTS, typename T>
-__device__ __forceinline__ void stage_q(const T* q, int lane, __half* to, float* about) {
-    const float4 v = load4(q + lane * 4);
+template <int PARTS>
+__device__ __forceinline__ void stage_q(const float4 v, int lane, __half* to, float* about) {
     const float a = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
     // fmaxf drops a NaN
     const bool fine = __all_sync(0xffffffffu, a < INFINITY && v.x == v.x && v.y == v.y && v.z == v.z && v.w == v.w);
@@ -372,21 +371,37 @@ __device__ __forceinline__ void stage_q(const T* q, int lane, __half* to, float*
         }
 }
 
-// seq's unit i of this warp: block j0 + 2 i + (warp >> 1), keys 32 (warp & 1) .. + 31 of it
+__device__ __forceinline__ float peer(const float* p, int rank) {  // *p in the shared memory of a block of the cluster
+    uint32_t at;
+    float v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// What a block has in common for its pieces
+struct Shared {
+    __half q[2][2][HD];
+    float about[2][4];
+    float m[WARPS][2], l[WARPS][2];
+};
+
+// One piece: the cache blocks [b0, b1) of KV head g of a row that reads cache row seq and sees `seen` keys; q: its two heads.
+// Unit i of a warp is keys 32 (warp & 1) .. + 31 of block b0 + (warp >> 1) + 2 i. Thread d ends with the piece's reference M, sum of
+// weights L and output sums O of dim d of both heads. All threads of the block call it, with the same arguments.
 template <typename T>
-__global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict__ q, Cache cache, AttnArgs a, T* __restrict__ out) {
+__device__ __forceinline__ void attend_piece(const T* __restrict__ q, const Cache& cache, int seq, int seen, int g, int b0, int b1,
+                                             uint8_t* ring, Shared& sh, float (&M)[2], float (&L)[2], float (&O)[2]) {
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int P = F32 ? 3 : 2;  // bf16 parts of a weight
-    pdl_wait();  // upstream results are read below
-    pdl_trigger();
-    const int split = blockIdx.x, g = blockIdx.y, row = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    int seq, seen;
-    if (!attn_row(cache, a, row, threadIdx.x == 0 && split == 0 && g == 0, seq, seen)) return;
-    const int j0 = split * a.bps + (warp >> 1), j1 = min((seen + KVB - 1) / KVB, (split + 1) * a.bps);
-    const int n = max(0, (j1 - j0 + 1) >> 1);
+    float4 qv = {};
+    if (warp < 2) qv = load4(q + warp * HD + lane * 4);
+    const int j0 = b0 + (warp >> 1), n = max(0, (b1 - j0 + 1) >> 1);
 
-    extern __shared__ __align__(128) uint8_t ring[];
     uint8_t* const mine = ring + warp * STAGES * UNIT_BYTES;
     const uint32_t dst = (uint32_t)__cvta_generic_to_shared(mine);
     const uint8_t* const src = cache.pool + (size_t)g * TILE + (warp & 1) * 2048 + lane * 16;
@@ -419,20 +434,14 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict_
     }
     int page = n > STAGES - 1 ? pages[2 * (STAGES - 1)] : 0;
 
-    __shared__ __align__(16) __half sq[F32 ? 2 : 1][2][HD];
-    __shared__ float about[2][4];
-    if (warp < 2) stage_q<F32 ? 2 : 1>(q + ((size_t)row * NQ + 2 * g + warp) * HD, lane, sq[0][warp], about[warp]);
+    if (warp < 2) stage_q<F32 ? 2 : 1>(qv, lane, sh.q[0][warp], sh.about[warp]);
     __syncthreads();
     uint4 qb[4];       // of word w: the B registers of its two steps
-    float qsum[2][2];  // [head][group]; fp32: in the lanes of part 0
-    const float factor = about[c >> 1][2];
+    const float qsum[2] = {sh.about[c >> 1][0], sh.about[c >> 1][1]};
+    const float factor = sh.about[c >> 1][2];
 #pragma unroll
     for (int w = 0; w < 4; ++w)
-        qb[w] = *reinterpret_cast<const uint4*>(&sq[F32 ? r >> 1 & 1 : 0][r & 1][64 * (w & 1) + 16 * c + 8 * (w >> 1)]);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int gr = 0; gr < 2; ++gr) qsum[h][gr] = F32 && (c & 1) ? 0.f : about[h][gr];
+        qb[w] = *reinterpret_cast<const uint4*>(&sh.q[F32 ? r >> 1 & 1 : 0][r & 1][64 * (w & 1) + 16 * c + 8 * (w >> 1)]);
     const uint32_t m1 = r >= 2 ? 0xFFFF0000u : 0u, m2 = r >= 4 ? 0xFFFF0000u : 0u;
     const uint32_t half_sel = r & 2 ? 0x5410u : 0x7632u;  // bf16: part 0 in the high halves, part 1 in the low ones
     const int from = 4 * c + 2 * (r & 1);                 // the lane that has the weight of key c of this column's head
@@ -449,8 +458,7 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict_
         {
             const uint4 k0 = *reinterpret_cast<const uint4*>(kat + at);
             const uint4 k1 = *reinterpret_cast<const uint4*>(kat + at + 512);
-            const uint2 p0 = *reinterpret_cast<const uint2*>(mine + par + KP_AT + r * 8);
-            const uint2 p1 = *reinterpret_cast<const uint2*>(mine + par + KP_AT + r * 8 + 64);
+            const uint2 kp = *reinterpret_cast<const uint2*>(mine + par + KP_AT + my * 8);
             const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
             float s[2][4] = {};  // of each group
 #pragma unroll
@@ -461,16 +469,14 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict_
                 mma_f16(s[w & 1], x, qb[w].x, qb[w].y);
                 mma_f16(s[w & 1], y, qb[w].z, qb[w].w);
             }
-            float y[4];  // (key r, head 0), (r, 1), (r + 8, 0), (r + 8, 1)
+            float y[2];  // this lane's key and head: sums e = 2 (key r + 8) + head
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint2 pr = e < 2 ? p0 : p1;
-                const float y0 = s[0][e] + zero_of(pr.x) * qsum[e & 1][0], y1 = s[1][e] + zero_of(pr.y) * qsum[e & 1][1];
-                y[e] = scale_of(pr.x) * y0 + scale_of(pr.y) * y1;
+            for (int gr = 0; gr < 2; ++gr) {
+                const float a0 = c & 2 ? s[gr][1] : s[gr][0], a1 = c & 2 ? s[gr][3] : s[gr][2];
+                y[gr] = c & 1 ? a1 : a0;
+                if (F32) y[gr] += __shfl_xor_sync(0xffffffffu, c & 1 ? a0 : a1, 1);  // the other part's sum
             }
-            const float a0 = c & 2 ? y[1] : y[0], a1 = c & 2 ? y[3] : y[2];  // this lane's head: keys r, r + 8
-            z = c & 1 ? a1 : a0;
-            if (F32) z += __shfl_xor_sync(0xffffffffu, c & 1 ? a0 : a1, 1);  // the other part's sum
+            z = scale_of(kp.x) * (y[0] + zero_of(kp.x) * qsum[0]) + scale_of(kp.y) * (y[1] + zero_of(kp.y) * qsum[1]);
             z *= factor;
         }
         const bool on = !TAIL || key0 + my < seen;
@@ -568,7 +574,6 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict_
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     float* const so = reinterpret_cast<float*>(ring);  // [warp][part][head][128]
-    __shared__ float sm[WARPS][2], sl[WARPS][2];
     if (c < P) {
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
@@ -579,62 +584,233 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict_
                     make_float2(o[t][h] * 0x1p73f, o[t][2 + h] * 0x1p69f);
         }
     }
-    if (lane == 0 || lane == 2) { sm[warp][lane >> 1] = m; sl[warp][lane >> 1] = l * 0x1p-60f; }
+    if (lane == 0 || lane == 2) { sh.m[warp][lane >> 1] = m; sh.l[warp][lane >> 1] = l * 0x1p-60f; }
     __syncthreads();
     const int d = threadIdx.x;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        float M = M_START - P_LOG2, L = 0.f, O = 0.f;
+        M[h] = M_START - P_LOG2;
+        L[h] = O[h] = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm[w][h]);
+        for (int w = 0; w < WARPS; ++w) M[h] = fmaxf(M[h], sh.m[w][h]);
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
-            const float f = ex2(sm[w][h] - M);
+            const float f = ex2(sh.m[w][h] - M[h]);
             float x = 0.f;
 #pragma unroll
             for (int part = P - 1; part >= 0; --part) x += so[((w * P + part) * 2 + h) * HD + d];
-            L += f * sl[w][h];
-            O += f * x;
-        }
-        if (a.n_splits == 1) {
-            out[((size_t)row * NQ + 2 * g + h) * HD + d] = (T)(L == 0.f ? 0.f : O / L);
-        } else {
-            float* const to = a.part + (((size_t)row * NQ + 2 * g + h) * a.n_splits + split) * (HD + 2);
-            to[d] = O;
-            if (d == 0) { to[HD] = M; to[HD + 1] = L; }
+            L[h] += f * sh.l[w][h];
+            O[h] += f * x;
         }
     }
 }
 
-// grid rows x 16, 128 threads: the splits of one (row, head) merged in split order.
+// grid (splits, 8, rows): one piece a block, the blocks of a row's keys dealt evenly to its splits. The splits of a (row,
+// head) are one cluster (at most 8), which merges them through its shared memory.
 template <typename T>
-__global__ void __launch_bounds__(128) k_kv4_combine(Cache c, AttnArgs a, T* __restrict__ out) {
+__global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict__ q, Cache cache, AttnArgs a, T* __restrict__ out) {
     pdl_wait();  // upstream results are read below
     pdl_trigger();
-    const int rh = blockIdx.x, d = threadIdx.x;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(16) Shared sh;
+    const int split = blockIdx.x, g = blockIdx.y, row = blockIdx.z, d = threadIdx.x;
     int seq, seen;
-    if (!attn_row(c, a, rh / NQ, false, seq, seen)) return;
-    const float* p = a.part + (size_t)rh * a.n_splits * (HD + 2);
-    float M = M_START - P_LOG2, L = 0.f, O = 0.f;
-    for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, p[s * (HD + 2) + HD]);
-    for (int s = 0; s < a.n_splits; ++s) {
-        const float f = ex2(p[s * (HD + 2) + HD] - M);
-        L += f * p[s * (HD + 2) + HD + 1];
-        O += f * p[s * (HD + 2) + d];
+    if (!attn_row(cache, a, row, d == 0 && split == 0 && g == 0, seq, seen)) return;
+    const int nblk = (seen + KVB - 1) / KVB, bps = (nblk + a.n_splits - 1) / a.n_splits;
+    float M[2], L[2], O[2];
+    attend_piece(q + ((size_t)row * NQ + 2 * g) * HD, cache, seq, seen, g, split * bps, min(nblk, (split + 1) * bps), ring, sh, M, L, O);
+    T* const to = out + ((size_t)row * NQ + 2 * g) * HD;
+    if (a.n_splits == 1) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) to[h * HD + d] = (T)(L[h] == 0.f ? 0.f : O[h] / L[h]);
+        return;
     }
-    out[(size_t)rh * HD + d] = (T)(L == 0.f ? 0.f : O / L);
+    __shared__ float all[2][HD], ml[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        all[h][d] = O[h];
+        if (d == 0) { ml[h][0] = M[h]; ml[h][1] = L[h]; }
+    }
+    cluster_sync();
+    for (int i = split * WARPS * 32 + d; i < 2 * HD; i += a.n_splits * WARPS * 32) {
+        const int h = i / HD;
+        float m1 = M_START - P_LOG2, l1 = 0.f, o1 = 0.f;
+        for (int s = 0; s < a.n_splits; ++s) m1 = fmaxf(m1, peer(&ml[h][0], s));
+        for (int s = 0; s < a.n_splits; ++s) {
+            const float f = ex2(peer(&ml[h][0], s) - m1);
+            l1 += f * peer(&ml[h][1], s);
+            o1 += f * peer(&all[h][i % HD], s);
+        }
+        to[i] = (T)(l1 == 0.f ? 0.f : o1 / l1);
+    }
+    cluster_sync();  // no block leaves while another reads its sums
 }
 
-constexpr int MAX_SPLITS = 64;
-struct Plan {
-    int splits, bps;
+// All cache blocks of all rows and heads as one line, (row, head, block) in that order, cut into equal shares: ragged rows
+// then cost what their keys cost, and no wave of blocks waits for the longest. Share i is blocks [i Q, (i + 1) Q) of the
+// line. A (row, head) that lies in one share is written at once, the others' pieces go to the workspace, two places a share:
+// the piece that starts the share, and the one that ends it.
+struct Line {
+    long long units;  // blocks in all
+    int share;        // blocks of one share
 };
+__device__ __forceinline__ int row_blocks(const Cache& c, const AttnArgs& a, int row, bool report) {
+    int seq, seen;
+    return row < a.rows && attn_row(c, a, row, report, seq, seen) ? (seen + KVB - 1) / KVB : 0;
+}
+__device__ __forceinline__ Line line_of(long long blocks, int shares) {
+    const long long u = blocks * NKV;
+    return {u, max(2, (int)((u + shares - 1) / shares))};
+}
+// the place of a piece: [share][first, last][2 heads][128 sums, reference, weight]
+constexpr int PIECE = HD + 4;  // 16-byte rows
+__device__ __forceinline__ float* place(float* part, int share, int which) { return part + ((size_t)share * 2 + which) * 2 * PIECE; }
+
+// grid: the shares (at most SLOTS); rows <= LINE_ROWS
+constexpr int LINE_ROWS = 1024;
+template <typename T>
+__global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn_line(const T* __restrict__ q, Cache cache, AttnArgs a, T* __restrict__ out) {
+    pdl_wait();  // upstream results are read below
+    pdl_trigger();
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(16) Shared sh;
+    __shared__ int start[2];  // the share's first row, and the blocks of it before the share
+    __shared__ long long sums[WARPS];
+    const int me = blockIdx.x, d = threadIdx.x, warp = d >> 5, lane = d & 31;
+    // where the share begins: sums of the rows' blocks, a row a thread at a time, once for their total and once for the place
+    long long total = 0;
+    for (int i = d; i < a.rows; i += WARPS * 32) total += row_blocks(cache, a, i, me == 0);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) sums[warp] = total;
+    __syncthreads();
+    total = sums[0] + sums[1] + sums[2] + sums[3];
+    const Line line = line_of(total, gridDim.x);
+    const long long first = (long long)me * line.share;
+    long long before = 0;
+    for (int i = d; i - d < a.rows && before * NKV <= first; i += WARPS * 32) {
+        const int n = row_blocks(cache, a, i, false);
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += w;
+        }
+        __syncthreads();
+        if (lane == 31) sums[warp] = incl;
+        __syncthreads();
+        long long mine = before + incl - n;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            if (w < warp) mine += sums[w];
+            before += sums[w];
+        }
+        if (first >= mine * NKV && first < (mine + n) * NKV) { start[0] = i; start[1] = (int)(first - mine * NKV); }
+    }
+    // rows that see nothing: zeros, by the blocks in turn
+    for (int row = me; row < a.rows; row += gridDim.x) {
+        int seq, seen;
+        if (attn_row(cache, a, row, false, seq, seen) && seen == 0)
+            for (int i = d; i < NQ * HD; i += WARPS * 32) out[(size_t)row * NQ * HD + i] = (T)0.f;
+    }
+    __syncthreads();
+    if (first >= line.units) return;
+    int row = start[0], at = start[1], left = (int)min((long long)line.share, line.units - first);
+    bool begins = true;  // the share's first piece
+    for (; left > 0 && row < a.rows;) {
+        int seq, seen;
+        if (!attn_row(cache, a, row, false, seq, seen) || seen == 0) { ++row; continue; }
+        const int nblk = (seen + KVB - 1) / KVB, g = at / nblk, b0 = at - g * nblk, b1 = min(nblk, b0 + left);
+        float M[2], L[2], O[2];
+        attend_piece(q + ((size_t)row * NQ + 2 * g) * HD, cache, seq, seen, g, b0, b1, ring, sh, M, L, O);
+        if (b0 == 0 && b1 == nblk) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) out[((size_t)row * NQ + 2 * g + h) * HD + d] = (T)(L[h] == 0.f ? 0.f : O[h] / L[h]);
+        } else {
+            float* const to = place(a.part, me, begins ? 0 : 1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                to[h * PIECE + d] = O[h];
+                if (d == 0) { to[h * PIECE + HD] = M[h]; to[h * PIECE + HD + 1] = L[h]; }
+            }
+        }
+        begins = false;
+        left -= b1 - b0;
+        at += b1 - b0;
+        if (at == nblk * NKV) { ++row; at = 0; }
+        __syncthreads();  // the ring and the sums are free again
+    }
+}
+
+// grid (16, rows), 128 threads: the pieces of a (row, query head) that lies in several shares. Warp w sums pieces w, w + 4, ..., lane l
+// dims 4l .. 4l + 3, all weighted to the largest reference; then the warps' sums are added in their order.
+template <typename T>
+__global__ void __launch_bounds__(128) k_kv4_combine(Cache c, AttnArgs a, int shares, T* __restrict__ out) {
+    pdl_wait();  // upstream results are read below
+    pdl_trigger();
+    __shared__ long long sums[2][4];
+    __shared__ float4 part[4][32];
+    __shared__ float weight[4];
+    const int g = blockIdx.x >> 1, h = blockIdx.x & 1, row = blockIdx.y, d = threadIdx.x, warp = d >> 5, lane = d & 31;
+    long long before = 0, total = 0;
+    for (int i = d; i < a.rows; i += 128) {
+        const int n = row_blocks(c, a, i, false);
+        total += n;
+        if (i < row) before += n;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (lane == 0) { sums[0][warp] = before; sums[1][warp] = total; }
+    __syncthreads();
+    before = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3];
+    total = sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3];
+    const Line line = line_of(total, shares);
+    const int nblk = row_blocks(c, a, row, false);
+    if (nblk == 0) return;
+    const long long from = before * NKV + (long long)g * nblk;
+    const int s0 = (int)(from / line.share), n = (int)((from + nblk - 1) / line.share) - s0 + 1;
+    if (n == 1) return;  // written by its share
+    const bool inside = from != (long long)s0 * line.share;  // the first piece ends its share
+    auto at = [&](int i) { return place(a.part, s0 + i, i == 0 && inside) + h * PIECE; };
+    float M = M_START - P_LOG2;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, at(i)[HD]);
+    M = warp_max(M);
+    float L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = warp; i < n; i += 4) {
+        const float* p = at(i);
+        const float f = ex2(p[HD] - M);
+        const float4 x = *reinterpret_cast<const float4*>(p + lane * 4);
+        L += f * p[HD + 1];
+        o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
+    }
+    part[warp][lane] = o;
+    if (lane == 0) weight[warp] = L;
+    __syncthreads();
+    const float* const s = reinterpret_cast<const float*>(part);
+    L = weight[0] + weight[1] + weight[2] + weight[3];
+    const float O = s[d] + s[HD + d] + s[2 * HD + d] + s[3 * HD + d];
+    out[((size_t)row * NQ + blockIdx.x) * HD + d] = (T)(L == 0.f ? 0.f : O / L);
+}
+
+constexpr int MAX_CLUSTER = 8, SLOTS = 4 * 152;
+struct Plan {
+    int splits;  // a cluster's blocks; 0: a line
+    int shares;
+};
+// Caches of up to 16 blocks of keys a block of the launch (32 where the pairs fill half the SMs' slots by themselves): one
+// block, or one cluster of up to 8 as the slots allow, for each (row, KV head), in one launch. Longer ones: a line in SLOTS
+// shares (four blocks an SM are resident: one wave) and the launch that merges it. Measured, us: 1 x 8000 keys 9.7 by a
+// cluster, 15.0 by a line; 64 x 20..200 keys 10.8 and 15.4; 64 x 800..8000 by one block each 78, by a line 69.
 Plan attn_plan(long long rows, int max_len) {
-    const int nblk = (max_len + KVB - 1) / KVB;
-    const long long want = (8ll * 152 + rows * NKV - 1) / (rows * NKV);
-    const int splits = (int)std::max(1ll, std::min({want, (long long)nblk, (long long)MAX_SPLITS}));
-    const int bps = (nblk + splits - 1) / splits;
-    return {(nblk + bps - 1) / bps, bps};
+    const long long pairs = rows * NKV, nblk = (max_len + KVB - 1) / KVB, most = (nblk + 1) / 2;
+    const long long n = std::min({(long long)MAX_CLUSTER, SLOTS / pairs, most});
+    if (rows > LINE_ROWS || nblk <= (n >= 2 ? 16 * n : 32)) return {(int)std::max(n, 1ll), 0};
+    return {0, (int)std::min<long long>(SLOTS, pairs * most)};
 }
 
 bool cache_ok(const tts_bb_kv4* c) {
@@ -647,6 +823,25 @@ Cache cache_of(const tts_bb_kv4* c) {
 bool type_ok(int t) { return t == TTS_BB_T_F32 || t == TTS_BB_T_BF16; }
 bool aligned(const void* p, int type) { return (uintptr_t)p % (type == TTS_BB_T_F32 ? 16 : 8) == 0; }
 tts_bb_status status() { return cudaPeekAtLastError() == cudaSuccess ? TTS_BB_OK : TTS_BB_E_CUDA; }
+
+// launch_pdl with clusters of n blocks along x
+template <typename... KArgs, typename... Args>
+void launch_cluster(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, int n, Args... args) {
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = n;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    cudaLaunchKernelEx(&cfg, k, static_cast<KArgs>(args)...);
+}
 
 template <typename TI, typename TQ>
 void append(int T, const void* qkv, int64_t stride, const void* gq, const void* gk, float eps, const float* cos_t,
@@ -706,7 +901,7 @@ TTS_API tts_bb_status tts_bb_kv4_read(const tts_bb_kv4* cache, int T, const int3
 TTS_API size_t tts_bb_kv4_attention_workspace(int B, int S, int max_len) {
     if (B < 1 || S < 1 || S > TTS_BB_KV4_MAX_QUERIES || max_len < 1 || (long long)B * S > 65535) return 0;
     const Plan p = attn_plan((long long)B * S, max_len);
-    return p.splits == 1 ? 0 : (size_t)B * S * NQ * p.splits * (HD + 2) * sizeof(float);
+    return (size_t)p.shares * 2 * 2 * PIECE * sizeof(float);
 }
 
 TTS_API tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S, const void* q, int type,
@@ -722,12 +917,20 @@ TTS_API tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const Plan p = attn_plan((long long)B * S, max_len);
     const Cache c = cache_of(cache);
-    const AttnArgs a{seqs, kv_lens, S, max_len, p.splits, p.bps, static_cast<float*>(workspace)};
-    const dim3 grid(p.splits, NKV, B * S);
+    const AttnArgs a{seqs, kv_lens, S, max_len, B * S, p.splits, static_cast<float*>(workspace)};
     auto go = [&](auto t) {
         typedef decltype(t) T;
-        launch_pdl(k_kv4_attn<T>, grid, WARPS * 32, WARPS * STAGES * UNIT_BYTES, st, static_cast<const T*>(q), c, a, static_cast<T*>(out));
-        if (p.splits > 1) launch_pdl(k_kv4_combine<T>, B * S * NQ, 128, 0, st, c, a, static_cast<T*>(out));
+        const size_t smem = WARPS * STAGES * UNIT_BYTES;
+        const T* const qt = static_cast<const T*>(q);
+        T* const to = static_cast<T*>(out);
+        if (p.splits > 1) {
+            launch_cluster(k_kv4_attn<T>, dim3(p.splits, NKV, B * S), WARPS * 32, smem, st, p.splits, qt, c, a, to);
+        } else if (p.splits) {
+            launch_pdl(k_kv4_attn<T>, dim3(1, NKV, B * S), WARPS * 32, smem, st, qt, c, a, to);
+        } else {
+            launch_pdl(k_kv4_attn_line<T>, p.shares, WARPS * 32, smem, st, qt, c, a, to);
+            launch_pdl(k_kv4_combine<T>, dim3(NQ, B * S), 128, 0, st, c, a, p.shares, to);
+        }
     };
     if (type == TTS_BB_T_F32) go(float{});
     else go(bf16{});

@@ -244,6 +244,38 @@ def test_attention_against_64_bits(lens, S, sharp, io):
     assert torch.equal(loose, attend(s, q, lens, S, s.table.shape[1] * BLK))
 
 
+@pytest.mark.parametrize("io", ["float32", "bfloat16"])
+@pytest.mark.parametrize("lens,S,bps,max_len", [([700, 0, 65, 300], 1, 260, 16640), ([0, 130, 0, 2, 515, 0], 3, 260, 16640), ([20000, 9001], 1, 313, 20000),
+                                                ([1], 1, 300, 19200), ([0, 0], 2, 300, 19200), ([40] * 70, 1, 40, 2560), ([90, 5], 64, 130, 8320)])
+def test_attention_dealt_over_all_blocks(lens, S, bps, max_len, io):
+    """Long bounds, where the keys of all rows are dealt evenly to the launch: rows in several shares, several rows in one,
+    rows that see nothing, and shares that get nothing."""
+    s = filled(sum(lens) + S, lens, bps)
+    q = dev(1.5 * s.rng.standard_normal((len(lens) * S, NQ, HD))).to(getattr(torch, io))
+    out = attend(s, q, lens, S, max_len)
+    check(s, q, lens, S, out)
+    assert torch.equal(out, attend(s, q, lens, S, max_len)) and int(s.err) == 0
+    rows = list(range(len(lens)))[::-1]
+    rows[0] = -1
+    check(s, q, lens[::-1], S, attend(s, q, lens[::-1], S, max_len, rows), rows)
+    if len(lens) > 1:
+        s.err.zero_()
+        bad = list(lens)
+        bad[1] = max_len + 1
+        out = attend(s, q, bad, S, max_len)
+        assert int(s.err) == tb().KV4_ERR_RANGE and bool((out.view(len(lens), -1)[1] == 5).all())
+        check(s, q[:S], lens[:1], S, out[:S])
+
+
+def test_attention_of_very_many_rows():
+    """More rows than the even deal sums over: one block each, at any length."""
+    lens = [70] * 24
+    s = filled(21, lens, 130)
+    q = dev(s.rng.standard_normal((24 * 64, NQ, HD))).bfloat16()
+    out = attend(s, q, lens, 64, 8320)
+    check(s, q, lens, 64, out)
+
+
 def test_attention_rows_and_padding():
     lens = [40, 300, 7]
     s = filled(11, lens, 6)
