@@ -49,8 +49,408 @@ struct Args {
 
 __device__ __forceinline__ bool is_allowed(const uint32_t* a, int i) { return !a || (a[i >> 5] >> (i & 31) & 1u); }
 
-constexpr int THREADS = 256;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr unsigned ALL = 0xffffffffu;
 
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// What a part of a row amounts to: its largest logit m (NONE: nothing with probability), r and t as above, less the one
+// term of m itself. Two parts are joined exactly so: with delta = the smaller m less the larger,
+//   r = r1 + e^delta (1 + r2),  t = t1 + e^delta (t2 + delta (1 + r2))
+constexpr float NONE = -INFINITY;
+struct Part {
+    float m, r, t;
+    int bad;
+};
+__device__ __forceinline__ Part join(const Part& x, const Part& y) {
+    const bool xy = x.m >= y.m;
+    const Part &a = xy ? x : y, &b = xy ? y : x;
+    Part o = {a.m, a.r, a.t, x.bad | y.bad};
+    if (b.m > NONE) {
+        const float d = b.m - a.m, e = ex2(d * LOG2E);
+        o.r += e * (1.f + b.r);
+        o.t += e * (b.t + d * (1.f + b.r));
+    }
+    return o;
+}
+// the row's numbers; z: the target's logit
+__device__ __forceinline__ void finish(const Args& a, int row, const Part& p, bool wanted, float z) {
+    const float nan = __int_as_float(0x7FC00000), log_s = log1pf(p.r);
+    const bool some = p.m > NONE;
+    if (a.targets && a.logprob) a.logprob[row] = p.bad ? nan : some && wanted ? (z - p.m) - log_s : NEG_INF;
+    if (a.entropy) a.entropy[row] = p.bad ? nan : some ? log_s - p.t / (1.f + p.r) : 0.f;
+    if (a.lse) a.lse[row] = p.bad ? nan : some ? p.m + log_s : NEG_INF;
+}
+__device__ __forceinline__ void write_top(const Args& a, int row, int j, u64 key, const Part& p) {
+    const float nan = __int_as_float(0x7FC00000);
+    a.top_ids[(size_t)row * a.n_top + j] = key && !p.bad ? id_of(key) : -1;
+    a.top_lp[(size_t)row * a.n_top + j] = p.bad ? nan : key ? (value_of(key) - p.m) - log1pf(p.r) : NEG_INF;
+}
+template <typename T>
+__device__ __forceinline__ bool target_of(const Args& a, const T* z, const uint32_t* ok, int row, float& v) {
+    v = 0.f;
+    if (!a.targets) return false;
+    const int i = a.targets[row];
+    if (i < 0 || i >= a.V || !is_allowed(ok, i)) return false;
+    v = to_f(z[i]);
+    return true;
+}
+
+// ---------------------------------------------------------------- one warp a row
+// Rows of up to 32 * NV logits, held in registers: lane l has ids l, l + 32, .... One pass for the maximum, one for the sums,
+// one that gathers the alternatives: ids whose logit reaches the n_top-th largest of the 32 lanes' maxima (a bound below
+// the n_top-th largest of all), usually a few more than n_top, ranked by counting. Bound by memory for many rows: 49152 x 1025
+// fp32 with a mask and 5 alternatives.
+constexpr int ROW_WARPS = 4, CAP = 96;
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(ROW_WARPS * 32) k_logprobs_warp(const T* __restrict__ logits, Args a) {
+    pdl_wait();
+    pdl_trigger();
+    __shared__ u64 found[ROW_WARPS][CAP];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.x * ROW_WARPS + warp;
+    if (row >= a.R) return;
+    const T* z = logits + (size_t)row * a.stride;
+    const uint32_t* ok = a.allowed ? a.allowed + (size_t)row * a.allowed_stride : nullptr;
+    float v[NV];
+    T raw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (i * 32 + lane < a.V) raw[i] = z[i * 32 + lane];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = i * 32 + lane < a.V ? to_f(raw[i]) : NEG_INF;
+    float tz;
+    const bool wanted = target_of(a, z, ok, row, tz);
+    if (ok) {
+#pragma unroll
+        for (int i0 = 0; i0 < NV; i0 += 32) {
+            const uint32_t w = (i0 + lane) * 32 < a.V ? ok[i0 + lane] : 0u;  // lane's word of these 32
+#pragma unroll
+            for (int i = i0; i < NV && i < i0 + 32; ++i)
+                if (!(__shfl_sync(ALL, w, i - i0) >> lane & 1u)) v[i] = NEG_INF;
+        }
+    }
+    float mine = NEG_INF;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        odd |= !(v[i] < INFINITY);
+        mine = fmaxf(mine, v[i]);
+    }
+    Part p = {warp_max(mine), 0.f, 0.f, __any_sync(ALL, odd)};
+    float r = 0.f, t = 0.f;
+    int same = 0;
+    const float m = p.m > NONE ? p.m : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const float d = fmaxf(v[i] - m, -1e4f), e = ex2(d * LOG2E);  // not -inf: 0 times it
+        t += e * d;
+        if (d == 0.f) ++same;
+        else r += e;
+    }
+    r = warp_sum(r);
+    t = warp_sum(t);
+    same = __reduce_add_sync(ALL, same);
+    p.r = r + (float)(same - 1);
+    p.t = t;
+    if (lane == 0) finish(a, row, p, wanted, tz);
+    if (a.n_top == 0) return;
+    int n = 0;
+    if (!p.bad && p.m > NONE) {
+        float bound = p.m;
+        if (a.n_top > 1) {  // the lanes' maxima in falling order
+            float s = mine;
+#pragma unroll
+            for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+                for (int j = k >> 1; j; j >>= 1) {
+                    const float o = __shfl_xor_sync(ALL, s, j);
+                    s = ((lane & k) == 0) == ((lane & j) == 0) ? fmaxf(s, o) : fminf(s, o);
+                }
+            bound = __shfl_sync(ALL, s, a.n_top - 1);
+        }
+        bound = fmaxf(bound, -3.4028235e38f);  // -inf is no alternative
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool in = v[i] >= bound;
+            const unsigned b = __ballot_sync(ALL, in);
+            if (b) {
+                const int at = n + __popc(b & ((1u << lane) - 1));
+                if (in && at < CAP) found[warp][at] = key_of(v[i], i * 32 + lane);
+                n += __popc(b);
+            }
+        }
+    }
+    __syncwarp();
+    const int have = min(n, a.n_top);
+    if (n <= CAP) {
+        for (int x = lane; x < n; x += 32) {
+            const u64 k = found[warp][x];
+            int rank = 0;
+            for (int j = 0; j < n; ++j) rank += found[warp][j] > k;
+            if (rank < a.n_top) write_top(a, row, rank, k, p);
+        }
+    } else {  // more equal logits than places: one after the other
+        u64 last = ~0ull;
+        for (int j = 0; j < have; ++j) {
+            u64 k = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const u64 c = v[i] > NEG_INF ? key_of(v[i], i * 32 + lane) : 0ull;
+                if (c < last && c > k) k = c;
+            }
+            last = warp_max_key(k);
+            if (lane == 0) write_top(a, row, j, last, p);
+        }
+    }
+    for (int j = have + lane; j < a.n_top; j += 32) write_top(a, row, j, 0ull, p);
+}
+
+// ---------------------------------------------------------------- a cluster a row
+// A row cut into the slices of 1, 2, 4 or 8 blocks, each slice staged in shared memory (16-byte pieces where the row's alignment
+// has them; the places before and behind it hold -inf, so that all of it is read in 16-byte pieces) and read three times
+// there: maximum (masked ids become -inf in it), then sums and the candidates: logits that reach the n_top-th largest of the
+// threads' maxima, at most LIST of them (with more equal ones, one alternative after the other is looked for). Block 0
+// joins the slices.
+constexpr int THREADS = 256, LIST = 1024, MAX_TOP = TTS_BB_LOGPROBS_MAX_TOP;
+constexpr int SLICE_BYTES = 48 * 1024, MAX_SLICE_BYTES = 192 * 1024;
+
+template <typename T> constexpr int EACH = 16 / sizeof(T);  // logits of a 16-byte piece
+__device__ __forceinline__ void unpack(const uint4& u, float (&v)[4], float) {
+    v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y); v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void unpack(const uint4& u, float (&v)[8], bf16) { unpack8(u, v); }
+__device__ __forceinline__ void unpack(const uint4& u, float (&v)[8], __half) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+struct __align__(16) Block {
+    uint32_t best[THREADS];  // read in 16-byte pieces: first, at the struct's alignment
+    float f[THREADS / 32];
+    float g[THREADS / 32];
+    int n[THREADS / 32];
+    int count;
+    uint32_t bound;
+    u64 list[LIST];
+    u64 top[MAX_TOP];
+    Part part;
+};
+__device__ __forceinline__ u64 block_max_key(u64 k, u64* sm) {
+    k = warp_max_key(k);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = k;
+    __syncthreads();
+    k = sm[0];
+    for (int w = 1; w < THREADS / 32; ++w) k = sm[w] > k ? sm[w] : k;
+    return k;
+}
+template <typename V>
+__device__ __forceinline__ V peer(const V* p, int rank) {  // *p in the shared memory of a block of the cluster
+    static_assert(sizeof(V) == 4 || sizeof(V) == 8, "one word or two");
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    V v;
+    if constexpr (sizeof(V) == 8) {
+        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(*reinterpret_cast<u64*>(&v)) : "r"(at) : "memory");
+    } else {
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(*reinterpret_cast<uint32_t*>(&v)) : "r"(at) : "memory");
+    }
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// grid R * n_parts; slice: a multiple of 32 logits
+template <typename T>
+__global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict__ logits, Args a, int n_parts, int slice) {
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ __align__(16) uint8_t stage[];
+    __shared__ Block sm;
+    constexpr int E = EACH<T>;
+    const int row = blockIdx.x / n_parts, part = blockIdx.x - row * n_parts, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const T* z = logits + (size_t)row * a.stride;
+    const uint32_t* ok = a.allowed ? a.allowed + (size_t)row * a.allowed_stride : nullptr;
+    const int i0 = part * slice, n = max(0, min(slice, a.V - i0));
+    const T* src = z + i0;
+    const int mis = (int)((uintptr_t)src % 16 / sizeof(T));  // the slice's first logit in its 16-byte piece
+    const int pieces = n ? (mis + n + E - 1) / E : 0;
+    T* const st = reinterpret_cast<T*>(stage);
+    const T low = (T)NEG_INF;
+    // piece q holds the slice's logits q E - mis ..; first and last may be cut
+    for (int q = tid; q < pieces; q += THREADS) {
+        const int i = q * E - mis;
+        if (i >= 0 && i + E <= n) {
+            const uint32_t d = (uint32_t)__cvta_generic_to_shared(st + q * E);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src + i) : "memory");
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) st[q * E + e] = i + e >= 0 && i + e < n ? src[i + e] : low;
+        }
+    }
+    float tz = 0.f;
+    const bool wanted = part == 0 && tid == 0 && target_of(a, z, ok, row, tz);
+    if (tid == 0) { sm.count = 0; sm.bound = 0xFFFFFFFFu; }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    // a thread reads the pieces that it copied: its own copies are complete
+
+    // maximum
+    float mine = NEG_INF;
+    bool odd = false;
+    for (int q = tid; q < pieces; q += THREADS) {
+        float v[E];
+        unpack(*reinterpret_cast<const uint4*>(st + q * E), v, T{});
+        if (ok) {
+            const int i = i0 + q * E - mis, w = max(i, 0) >> 5;
+            const uint32_t lo = ok[w], hi = (w + 1) * 32 < a.V ? ok[w + 1] : 0u;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int b = i + e - w * 32;  // 0 .. 38
+                if (b >= 0 && !((b < 32 ? lo >> b : hi >> (b - 32)) & 1u)) {
+                    v[e] = NEG_INF;
+                    st[q * E + e] = low;
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            odd |= !(v[e] < INFINITY);
+            mine = fmaxf(mine, v[e]);
+        }
+    }
+    const float wm = warp_max(mine);
+    if (lane == 0) sm.f[warp] = wm;
+    sm.best[tid] = order_of(mine + 0.f);
+    const int bad = __syncthreads_or(odd);
+    Part p = {NEG_INF, 0.f, 0.f, bad};
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) p.m = fmaxf(p.m, sm.f[w]);
+    const bool some = p.m > NONE;
+    uint32_t bound = 0;
+    if (a.n_top && some) {  // threads whose maximum is among the n_top largest; the least of these maxima
+        const uint32_t b = sm.best[tid];
+        int above = 0;
+        const uint4* all = reinterpret_cast<const uint4*>(sm.best);
+#pragma unroll 8
+        for (int i = 0; i < THREADS / 4; ++i) {
+            const uint4 o = all[i];
+            above += (o.x > b) + (o.y > b) + (o.z > b) + (o.w > b);
+        }
+        uint32_t least = above < a.n_top ? b : 0xFFFFFFFFu;
+        least = __reduce_min_sync(ALL, least);
+        if (lane == 0) atomicMin(&sm.bound, least);
+        __syncthreads();
+        bound = max(sm.bound, order_of(-3.4028235e38f));  // -inf is no alternative
+    }
+    // sums and candidates
+    const float m = some ? p.m : 0.f;
+    const float bv = __uint_as_float(bound & 0x80000000u ? bound & 0x7FFFFFFFu : ~bound);
+    float r = 0.f, t = 0.f;
+    int same = 0;
+    for (int q = tid; q < pieces; q += THREADS) {
+        float v[E];
+        unpack(*reinterpret_cast<const uint4*>(st + q * E), v, T{});
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float d = fmaxf(v[e] - m, -1e4f), x = ex2(d * LOG2E);
+            t += x * d;
+            if (d == 0.f) ++same;
+            else r += x;
+        }
+        if (bound && mine >= bv) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (v[e] >= bv) {
+                    const int at = atomicAdd(&sm.count, 1);
+                    if (at < LIST) sm.list[at] = key_of(v[e], i0 + q * E - mis + e);
+                }
+        }
+    }
+    r = warp_sum(r);
+    t = warp_sum(t);
+    same = __reduce_add_sync(ALL, same);
+    __syncthreads();
+    if (lane == 0) { sm.f[warp] = r; sm.g[warp] = t; sm.n[warp] = same; }
+    __syncthreads();
+    same = -1;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) { p.r += sm.f[w]; p.t += sm.g[w]; same += sm.n[w]; }
+    p.r += (float)same;
+    // the slice's alternatives, in order
+    if (a.n_top) {
+        for (int j = tid; j < MAX_TOP; j += THREADS) sm.top[j] = 0ull;
+        __syncthreads();
+        const int found = bound ? sm.count : 0;
+        if (found <= LIST) {
+            for (int x = tid; x < found; x += THREADS) {
+                const u64 k = sm.list[x];
+                int rank = 0;
+                for (int j = 0; j < found; ++j) rank += sm.list[j] > k;
+                if (rank < a.n_top) sm.top[rank] = k;
+            }
+        } else {
+            u64 last = ~0ull;
+            for (int j = 0; j < a.n_top && last; ++j) {
+                u64 k = 0;
+                for (int q = tid; q < pieces; q += THREADS) {
+                    float v[E];
+                    unpack(*reinterpret_cast<const uint4*>(st + q * E), v, T{});
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const u64 c = v[e] > NEG_INF ? key_of(v[e], i0 + q * E - mis + e) : 0ull;
+                        if (c < last && c > k) k = c;
+                    }
+                }
+                last = block_max_key(k, sm.list);
+                if (tid == 0) sm.top[j] = last;
+            }
+        }
+    }
+    if (tid == 0) sm.part = p;
+    if (n_parts == 1) {
+        __syncthreads();
+        if (tid == 0) finish(a, row, p, wanted, tz);
+        for (int j = tid; j < a.n_top; j += THREADS) write_top(a, row, j, sm.top[j], p);
+        return;
+    }
+    cluster_sync();
+    if (part == 0) {
+        for (int s = 1; s < n_parts; ++s)
+            p = join(p, Part{peer(&sm.part.m, s), peer(&sm.part.r, s), peer(&sm.part.t, s), peer(&sm.part.bad, s)});
+        if (tid == 0) finish(a, row, p, wanted, tz);
+        if (a.n_top) {
+            const int total = n_parts * a.n_top;  // at most 256: a key a thread
+            const u64 k = tid < total ? peer(&sm.top[tid % a.n_top], tid / a.n_top) : 0ull;
+            __syncthreads();
+            sm.list[tid] = k;
+            for (int j = tid; j < a.n_top; j += THREADS) write_top(a, row, j, 0ull, p);
+            __syncthreads();
+            if (k) {
+                int rank = 0;
+                for (int j = 0; j < total; ++j) rank += sm.list[j] > k;
+                if (rank < a.n_top) write_top(a, row, rank, k, p);
+            }
+        }
+    }
+    cluster_sync();  // no block leaves while another reads its slice's results
+}
+
+// ---------------------------------------------------------------- rows longer than 8 slices of shared memory
 template <typename T>
 __device__ __forceinline__ T block_sum(T v, T* sm) {
 #pragma unroll
@@ -62,19 +462,10 @@ __device__ __forceinline__ T block_sum(T v, T* sm) {
     for (int w = 1; w < THREADS / 32; ++w) v += sm[w];
     return v;
 }
-__device__ __forceinline__ u64 block_max_key(u64 k, u64* sm) {
-    k = warp_max_key(k);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = k;
-    __syncthreads();
-    k = sm[0];
-    for (int w = 1; w < THREADS / 32; ++w) k = sm[w] > k ? sm[w] : k;
-    return k;
-}
 
 // grid R, THREADS threads: one row each; a pass for the maximum, one for the sums, one for each alternative.
 template <typename T>
-__global__ void __launch_bounds__(THREADS) k_logprobs(const T* __restrict__ logits, Args a) {
+__global__ void __launch_bounds__(THREADS) k_logprobs_long(const T* __restrict__ logits, Args a) {
     pdl_wait();
     pdl_trigger();
     __shared__ u64 smk[THREADS / 32];
@@ -103,15 +494,11 @@ __global__ void __launch_bounds__(THREADS) k_logprobs(const T* __restrict__ logi
     }
     r = block_sum(r, smf);
     t = block_sum(t, smf);
-    const float nan = __int_as_float(0x7FC00000), log_s = log1pf(r);
+    const Part p = {best ? m : NONE, r, t, bad};
     if (tid == 0) {
-        if (a.targets && a.logprob) {
-            const int i = a.targets[row];
-            const float v = i >= 0 && i < a.V && is_allowed(ok, i) ? to_f(z[i]) : NEG_INF;
-            a.logprob[row] = bad ? nan : best ? (v - m) - log_s : NEG_INF;
-        }
-        if (a.entropy) a.entropy[row] = bad ? nan : best ? log_s - t / (1.f + r) : 0.f;
-        if (a.lse) a.lse[row] = bad ? nan : best ? m + log_s : NEG_INF;
+        float tz;
+        const bool wanted = target_of(a, z, ok, row, tz);
+        finish(a, row, p, wanted, tz);
     }
     u64 last = ~0ull;
     for (int j = 0; j < a.n_top; ++j) {
@@ -125,11 +512,53 @@ __global__ void __launch_bounds__(THREADS) k_logprobs(const T* __restrict__ logi
             }
             last = block_max_key(k, smk);
         }
-        if (tid == 0) {
-            a.top_ids[(size_t)row * a.n_top + j] = last && !bad ? id_of(last) : -1;
-            a.top_lp[(size_t)row * a.n_top + j] = bad ? nan : last ? (value_of(last) - m) - log_s : NEG_INF;
-        }
+        if (tid == 0) write_top(a, row, j, last, p);
     }
+}
+
+// launch_pdl with clusters of n blocks, and shared memory beyond the default
+template <typename T>
+void launch_block(const T* logits, const Args& a, int n, int slice, cudaStream_t st) {
+    const size_t smem = (size_t)slice * sizeof(T) + 16;
+    // every call: the attribute is the current device's
+    if (smem > SLICE_BYTES - 16384)
+        cudaFuncSetAttribute(k_logprobs_block<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SLICE_BYTES + 16);
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = n;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.R * n));
+    cfg.blockDim = THREADS;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = n > 1 ? 2 : 1;
+    cudaLaunchKernelEx(&cfg, k_logprobs_block<T>, logits, a, n, slice);
+}
+
+// Many rows of up to 96 logits a lane: a warp each (below 4 warps an SM a row's latency counts, and a block's threads
+// share it). Else a block a row, or a cluster: slices of at most SLICE_BYTES, so that several blocks share an SM, and more,
+// shorter ones while the rows alone leave SMs idle.
+template <typename T>
+void launch(const T* logits, const Args& a, cudaStream_t st) {
+    const auto warps = [&](auto k) { launch_pdl(k, (a.R + ROW_WARPS - 1) / ROW_WARPS, ROW_WARPS * 32, 0, st, logits, a); };
+    if (a.R >= 4 * 152 || a.V <= 256) {
+        if (a.V <= 8 * 32) return warps(k_logprobs_warp<T, 8>);
+        if (a.V <= 33 * 32) return warps(k_logprobs_warp<T, 33>);
+        if (a.V <= 64 * 32) return warps(k_logprobs_warp<T, 64>);
+        if (a.V <= 96 * 32) return warps(k_logprobs_warp<T, 96>);
+    }
+    const long long bytes = (long long)a.V * sizeof(T);
+    int n = 1;
+    while (n < 8 && (bytes > (long long)n * SLICE_BYTES || (a.R * n < 2 * 152 && bytes > n * 8192))) n *= 2;
+    const int slice = ((a.V + n - 1) / n + 31) / 32 * 32;
+    if ((long long)slice * sizeof(T) > MAX_SLICE_BYTES)
+        launch_pdl(k_logprobs_long<T>, a.R, THREADS, 0, st, logits, a);
+    else
+        launch_block(logits, a, n, slice, st);
 }
 
 }  // namespace
@@ -140,7 +569,7 @@ TTS_API tts_bb_status tts_bb_token_logprobs(int R, int V, const void* logits, in
                                             const int32_t* targets, const uint32_t* allowed, int64_t allowed_stride,
                                             int n_top, float* logprob, float* entropy, float* lse, int32_t* top_ids,
                                             float* top_logprobs, void* workspace, size_t workspace_bytes, void* stream) {
-    if (R < 1 || V < 1 || !logits || row_stride < V || n_top < 0 || n_top > TTS_BB_LOGPROBS_MAX_TOP ||
+    if (R < 1 || R > (1 << 27) || V < 1 || !logits || row_stride < V || n_top < 0 || n_top > TTS_BB_LOGPROBS_MAX_TOP ||
         type < TTS_BB_T_F32 || type > TTS_BB_T_F16 || (uintptr_t)logits % (type == TTS_BB_T_F32 ? 4 : 2) ||
         (targets && !logprob) || (n_top && (!top_ids || !top_logprobs)) ||
         (allowed && allowed_stride != 0 && allowed_stride < ((int64_t)V + 31) / 32))
@@ -150,8 +579,8 @@ TTS_API tts_bb_status tts_bb_token_logprobs(int R, int V, const void* logits, in
     if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const Args a{R, V, n_top, row_stride, allowed_stride, targets, allowed, logprob, entropy, lse, top_ids, top_logprobs};
-    if (type == TTS_BB_T_F32) launch_pdl(k_logprobs<float>, R, THREADS, 0, st, static_cast<const float*>(logits), a);
-    else if (type == TTS_BB_T_BF16) launch_pdl(k_logprobs<bf16>, R, THREADS, 0, st, static_cast<const bf16*>(logits), a);
-    else launch_pdl(k_logprobs<__half>, R, THREADS, 0, st, static_cast<const __half*>(logits), a);
+    if (type == TTS_BB_T_F32) launch(static_cast<const float*>(logits), a, st);
+    else if (type == TTS_BB_T_BF16) launch(static_cast<const bf16*>(logits), a, st);
+    else launch(static_cast<const __half*>(logits), a, st);
     return cudaPeekAtLastError() == cudaSuccess ? TTS_BB_OK : TTS_BB_E_CUDA;
 }

@@ -602,7 +602,7 @@ tts_bb_status tts_bb_w4_pack(int N, int K, int group, const void* codes, const v
 tts_bb_status tts_bb_w4_linear(int T, int N, int K, int group, const void* x, int type, int64_t x_stride,
                                const void* packed, void* y, void* stream);
 
-/* Log probabilities of R rows of V logits: of a given token, the entropy, the log-sum-exp and the n_top most
+/* Log probabilities of R <= 2^27 rows of V logits: of a given token, the entropy, the log-sum-exp and the n_top most
  * probable tokens.
  *   logits   fp32, bf16 or fp16 (type) [R] rows, row_stride elements apart (>= V), aligned to the element
  *   targets  int32 [R] or NULL; logprob fp32 [R]: log p(targets[r]); -inf for a target outside 0..V-1, a
