@@ -427,27 +427,51 @@ def tts_bb_gqa_decode_attention_static(q, kv_pool, page_table, blocks_per_seq: i
 # Device tensors with a dtype and strides (torch CUDA tensors); each call returns its status, or raises TtsBbError
 # with check=True. Shapes, types and strides are checked here, values by the library.
 T_F32, T_BF16, T_F16 = 0, 1, 2
-_TYPES = {"torch.float32": T_F32, "torch.bfloat16": T_BF16, "torch.float16": T_F16}
 KV4_TILE_BYTES, KV4_BLOCK_BYTES, KV4_MAX_QUERIES, W4_MAX_TOKENS, LOGPROBS_MAX_TOP = 4608, 73728, 64, 64, 32
 KV4_ERR_PAGE, KV4_ERR_RANGE = 1, 2
 
 
-def _arg(x, name: str, types, n: int, rows: bool = False):
-    """Address of a device tensor of at least n elements of one of the types; contiguous unless rows (then only
-    its last dimension has to be)."""
+class _Types(dict):
+    """Element types an argument may have: dtype -> type code, None for the others. Filled by name as dtypes are met,
+    so that this module need not import torch and a lookup stays one dict access."""
+
+    def __init__(self, **codes):
+        super().__init__()
+        self.codes = {f"torch.{k}": v for k, v in codes.items()}
+
+    def __missing__(self, dtype):
+        self[dtype] = code = self.codes.get(str(dtype))
+        return code
+
+
+_I32, _F32, _BF16, _U8 = _Types(int32=0), _Types(float32=T_F32), _Types(bfloat16=T_BF16), _Types(uint8=0)
+_IO, _LOGITS = _Types(float32=T_F32, bfloat16=T_BF16), _Types(float32=T_F32, bfloat16=T_BF16, float16=T_F16)
+_WORDS = _Types(uint32=0, int32=0)
+
+
+def _arg(x, name: str, types: _Types, n: int):
+    """Address of a contiguous device tensor of at least n elements of one of the types; None stays None."""
     if x is None:
         return None
-    if str(x.dtype) not in types or not x.is_cuda:
-        raise TypeError(f"{name}: a CUDA tensor of {' or '.join(types)} is wanted, not {x.dtype} on {x.device}")
-    if not (x.is_contiguous() or (rows and x.dim() == 2 and x.stride(1) == 1)):
-        raise ValueError(f"{name}: strides {tuple(x.stride())} of shape {tuple(x.shape)} are not supported")
+    if types[x.dtype] is not None and x.is_cuda and x.is_contiguous() and x.numel() >= n:
+        return x.data_ptr()
+    return _refuse(x, name, types, n)
+
+
+def _rows(x, name: str, types: _Types, R: int, n: int):
+    """(address, row stride) of a device tensor of R rows of at least n elements: two dimensions, the last one
+    contiguous, or anything contiguous."""
+    if x.dim() == 2 and x.shape[0] >= R and x.shape[1] >= n and x.stride(1) == 1 and types[x.dtype] is not None and x.is_cuda:
+        return x.data_ptr(), x.stride(0) if R > 1 else n
+    return _arg(x, name, types, R * n), n
+
+
+def _refuse(x, name: str, types: _Types, n: int):
+    if types[x.dtype] is None or not x.is_cuda:
+        raise TypeError(f"{name}: a CUDA tensor of {' or '.join(types.codes)} is wanted, not {x.dtype} on {x.device}")
     if x.numel() < n:
         raise ValueError(f"{name}: {n} elements are wanted, not {x.numel()}")
-    return x.data_ptr()
-
-
-_I32, _F32, _BF16, _U8 = ("torch.int32",), ("torch.float32",), ("torch.bfloat16",), ("torch.uint8",)
-_IO = ("torch.float32", "torch.bfloat16")
+    raise ValueError(f"{name}: strides {tuple(x.stride())} of shape {tuple(x.shape)} are not supported")
 
 
 def _status(st: int, name: str, check: bool) -> int:
@@ -482,13 +506,12 @@ def tts_bb_rope_tables(theta: float, n_pos: int):
 def tts_bb_kv4_append(cache: Kv4Cache, T: int, qkv, q_norm, k_norm, cos_table, sin_table, n_pos: int, seqs, positions,
                       q_out=None, eps: float = 1e-6, stream: int = 0, check: bool = True) -> int:
     """qkv: [T][4096] fp32 or bf16 (rows may be strided); q_out: [T][16][128] fp32 or bf16, or None."""
-    stride = qkv.stride(0) if qkv.dim() == 2 and T > 1 else 4096
+    x, stride = _rows(qkv, "qkv", _IO, T, 4096)
     st = lib.tts_bb_kv4_append(
-        cache.ref, T, _arg(qkv, "qkv", _IO, T * 4096, True), _TYPES[str(qkv.dtype)], stride,
-        _arg(q_norm, "q_norm", _BF16, 128), _arg(k_norm, "k_norm", _BF16, 128), eps,
+        cache.ref, T, x, _IO[qkv.dtype], stride, _arg(q_norm, "q_norm", _BF16, 128), _arg(k_norm, "k_norm", _BF16, 128), eps,
         _arg(cos_table, "cos_table", _F32, n_pos * 64), _arg(sin_table, "sin_table", _F32, n_pos * 64), n_pos,
         _arg(seqs, "seqs", _I32, T), _arg(positions, "positions", _I32, T), _arg(q_out, "q_out", _IO, T * 2048),
-        T_F32 if q_out is None else _TYPES[str(q_out.dtype)], stream or None)
+        T_F32 if q_out is None else _IO[q_out.dtype], stream or None)
     return _status(st, "tts_bb_kv4_append", check)
 
 
@@ -509,7 +532,7 @@ def tts_bb_kv4_attention(cache: Kv4Cache, B: int, S: int, q, kv_lens, max_len: i
     if q.dtype != out.dtype:
         raise TypeError(f"q and out have to be of one type, not {q.dtype} and {out.dtype}")
     st = lib.tts_bb_kv4_attention(
-        cache.ref, B, S, _arg(q, "q", _IO, B * S * 2048), _TYPES[str(q.dtype)], _arg(seqs, "seqs", _I32, B),
+        cache.ref, B, S, _arg(q, "q", _IO, B * S * 2048), _IO[q.dtype], _arg(seqs, "seqs", _I32, B),
         _arg(kv_lens, "kv_lens", _I32, B), max_len, _arg(out, "out", _IO, B * S * 2048),
         _arg(workspace, "workspace", _U8, 0), 0 if workspace is None else workspace.numel(), stream or None)
     return _status(st, "tts_bb_kv4_attention", check)
@@ -532,9 +555,9 @@ def tts_bb_w4_linear(T: int, N: int, K: int, group: int, x, packed, y, stream: i
     """x: [T][K] (rows may be strided), y: [T][N], both fp32 or both bf16."""
     if x.dtype != y.dtype:
         raise TypeError(f"x and y have to be of one type, not {x.dtype} and {y.dtype}")
-    st = lib.tts_bb_w4_linear(T, N, K, group, _arg(x, "x", _IO, T * K, True), _TYPES[str(x.dtype)],
-                              x.stride(0) if x.dim() == 2 and T > 1 else K,
-                              _arg(packed, "packed", _U8, tts_bb_w4_packed_bytes(N, K, group)), _arg(y, "y", _IO, T * N),
+    at, stride = _rows(x, "x", _IO, T, K)
+    st = lib.tts_bb_w4_linear(T, N, K, group, at, _IO[x.dtype], stride,
+                              _arg(packed, "packed", _U8, lib.tts_bb_w4_packed_bytes(N, K, group)), _arg(y, "y", _IO, T * N),
                               stream or None)
     return _status(st, "tts_bb_w4_linear", check)
 
@@ -548,15 +571,15 @@ def tts_bb_token_logprobs(R: int, V: int, logits, targets=None, n_top: int = 0, 
                           check: bool = True) -> int:
     """logits: [R][>= V] fp32, bf16 or fp16 (rows may be strided); allowed: uint32 or int32 words, [words] for all
     rows or [R][words]."""
-    stride = logits.stride(0) if logits.dim() == 2 and R > 1 else V
-    words = (V + 31) // 32
-    a_rows = allowed is not None and allowed.dim() == 2
+    z, stride = _rows(logits, "logits", _LOGITS, R, V)
+    mask, mask_stride = None, 0
+    if allowed is not None:
+        mask, mask_stride = _rows(allowed, "allowed", _WORDS, R if allowed.dim() == 2 else 1, (V + 31) // 32)
+        if allowed.dim() != 2 or R == 1:
+            mask_stride = 0
     st = lib.tts_bb_token_logprobs(
-        R, V, _arg(logits, "logits", tuple(_TYPES), R * V, True), _TYPES[str(logits.dtype)], stride,
-        _arg(targets, "targets", _I32, R),
-        _arg(allowed, "allowed", ("torch.uint32", "torch.int32"), words * (R if a_rows else 1), True),
-        allowed.stride(0) if a_rows and R > 1 else 0, n_top, _arg(logprob, "logprob", _F32, R), _arg(entropy, "entropy", _F32, R),
-        _arg(lse, "lse", _F32, R), _arg(top_ids, "top_ids", _I32, R * n_top),
-        _arg(top_logprobs, "top_logprobs", _F32, R * n_top), _arg(workspace, "workspace", _U8, 0),
-        0 if workspace is None else workspace.numel(), stream or None)
+        R, V, z, _LOGITS[logits.dtype], stride, _arg(targets, "targets", _I32, R), mask, mask_stride, n_top,
+        _arg(logprob, "logprob", _F32, R), _arg(entropy, "entropy", _F32, R), _arg(lse, "lse", _F32, R),
+        _arg(top_ids, "top_ids", _I32, R * n_top), _arg(top_logprobs, "top_logprobs", _F32, R * n_top),
+        _arg(workspace, "workspace", _U8, 0), 0 if workspace is None else workspace.numel(), stream or None)
     return _status(st, "tts_bb_token_logprobs", check)

@@ -286,7 +286,8 @@ __device__ __forceinline__ bool attn_row(const Cache& c, const AttnArgs& a, int 
 // and sums fp32. The zero point joins by the queries' sum: s (sum q code + zero sum q). Q is scaled by a power of two to a
 // largest magnitude in [2^14, 2^15). bf16 queries are then exact in fp16 (down to 2^-25 of the head's largest); column n
 // holds head n & 1, so every lane has both heads' scores of its keys. fp32 queries enter as two fp16 parts, 24 bits
-// together, part (n >> 1) & 1 of head n & 1 in column n.
+// together, part (n >> 1) & 1 of head n & 1 in column n; and their codes become (code + zero) 2^-9 first, by one exact
+// multiply-add each: the subnormal numbers as operands lose up to 5 bits of a product's sum, which bf16 results do not show.
 // Each lane then keeps one score of 16 keys: key r + 8 (c & 1), head c >> 1. (By m16n8k32 on e4m3, where a byte of two masks
 // is 4 operands, the same took longer: that form is carried out by fp16 products after conversions.)
 //
@@ -322,6 +323,11 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -344,9 +350,9 @@ __device__ __forceinline__ uint32_t part_of(float x, uint32_t m1, uint32_t m2) {
     return as_u(x - as_f(as_u(x) & m2));
 }
 // One warp's share of the queries: a head's 128 values (lane l: dims 4l .. 4l + 3) as fp16 parts in `to` ([part][2 heads] rows of
-// 128, to: this head's; 8 dims stand as 0 4 1 5 2 6 3 7, the odd ones divided by 16) and in `about` its group sums,
-// in the units of the products' sums, and the factor that turns those into scores times log2(e) (NaN where a query is not
-// finite).
+// 128, to: this head's; 8 dims stand as 0 4 1 5 2 6 3 7; with one part (bf16 queries) the odd ones divided by 16) and in
+// `about` its group sums, in the units of the products' sums, and the factor that turns those into scores times log2(e) (NaN
+// where a query is not finite).
 template <int PARTS>
 __device__ __forceinline__ void stage_q(const float4 v, int lane, __half* to, float* about) {
     const float a = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
@@ -358,7 +364,7 @@ __device__ __forceinline__ void stage_q(const float4 v, int lane, __half* to, fl
 #pragma unroll
     for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((lane & 15) == 0) about[lane >> 4] = s * up * 0x1p-24f;
-    if (lane == 0) about[2] = fine ? rsqrtf((float)HD) * LOG2E * 0x1p24f / up : __int_as_float(0x7FC00000);
+    if (lane == 0) about[2] = fine ? rsqrtf((float)HD) * LOG2E * (PARTS == 1 ? 0x1p24f : 0x1p9f) / up : __int_as_float(0x7FC00000);
     float x[4] = {v.x * up, v.y * up, v.z * up, v.w * up};
     to += (lane >> 1) * 8 + (lane & 1);
 #pragma unroll
@@ -367,7 +373,7 @@ __device__ __forceinline__ void stage_q(const float4 v, int lane, __half* to, fl
         for (int e = 0; e < 4; ++e) {
             const __half h = __float2half_rn(x[e]);
             x[e] -= __half2float(h);
-            to[p * 2 * HD + e * 2] = e & 1 ? __hmul(h, __float2half_rn(0.0625f)) : h;
+            to[p * 2 * HD + e * 2] = PARTS == 1 && (e & 1) ? __hmul(h, __float2half_rn(0.0625f)) : h;
         }
 }
 
@@ -460,12 +466,31 @@ __device__ __forceinline__ void attend_piece(const T* __restrict__ q, const Cach
             const uint4 k1 = *reinterpret_cast<const uint4*>(kat + at + 512);
             const uint2 kp = *reinterpret_cast<const uint2*>(mine + par + KP_AT + my * 8);
             const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+            uint32_t kz[2][2] = {};  // fp32: zero 2^-9 of keys r, r + 8 and each group, twice
+            if constexpr (F32) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint2 rp = *reinterpret_cast<const uint2*>(mine + par + KP_AT + r * 8 + h * 64);
+#pragma unroll
+                    for (int gr = 0; gr < 2; ++gr) {
+                        const __half2 v = __float2half2_rn(zero_of(gr ? rp.y : rp.x) * 0x1p-9f);
+                        kz[h][gr] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                }
+            }
             float s[2][4] = {};  // of each group
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const uint32_t u0 = w0[w] >> 8, u1 = w1[w] >> 8;
-                const uint32_t x[4] = {w0[w] & 0x000F000Fu, w1[w] & 0x000F000Fu, w0[w] & 0x00F000F0u, w1[w] & 0x00F000F0u};
-                const uint32_t y[4] = {u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x00F000F0u};
+                uint32_t x[4] = {w0[w] & 0x000F000Fu, w1[w] & 0x000F000Fu, w0[w] & 0x00F000F0u, w1[w] & 0x00F000F0u};
+                uint32_t y[4] = {u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x00F000F0u};
+                if constexpr (F32) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {  // times 2^15 and 2^11
+                        x[e] = fma_f16x2(x[e], e < 2 ? 0x78007800u : 0x68006800u, kz[e & 1][w & 1]);
+                        y[e] = fma_f16x2(y[e], e < 2 ? 0x78007800u : 0x68006800u, kz[e & 1][w & 1]);
+                    }
+                }
                 mma_f16(s[w & 1], x, qb[w].x, qb[w].y);
                 mma_f16(s[w & 1], y, qb[w].z, qb[w].w);
             }
@@ -476,7 +501,11 @@ __device__ __forceinline__ void attend_piece(const T* __restrict__ q, const Cach
                 y[gr] = c & 1 ? a1 : a0;
                 if (F32) y[gr] += __shfl_xor_sync(0xffffffffu, c & 1 ? a0 : a1, 1);  // the other part's sum
             }
-            z = scale_of(kp.x) * (y[0] + zero_of(kp.x) * qsum[0]) + scale_of(kp.y) * (y[1] + zero_of(kp.y) * qsum[1]);
+            if (!F32) {
+                y[0] += zero_of(kp.x) * qsum[0];
+                y[1] += zero_of(kp.y) * qsum[1];
+            }
+            z = scale_of(kp.x) * y[0] + scale_of(kp.y) * y[1];
             z *= factor;
         }
         const bool on = !TAIL || key0 + my < seen;

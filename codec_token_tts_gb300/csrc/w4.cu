@@ -1,16 +1,24 @@
 // Products with 4-bit weights and group scales, y = x W^T for a few rows of x, on the caller's buffers.
 //
-// W[n][k] = scale[n][k / G] (code - zero). The tensor cores take the whole number code - zero, which is exact
-// in bf16: 128 + code is one logical operation on a nibble (0x4300 | code), and adding -(128 + zero) is exact.
-// An fp32 row of x enters as three bf16 parts (8 + 8 + 8 bits by truncation, together x itself), each in
-// a column of its own, so every product is exact, sums are fp32, and a scale multiplies each group's sum.
+// W[n][k] = scale[n][k / G] (code - zero). Bound by the codes' bytes where the matrix is large, by one launch's latency where
+// it is small; what comes next are the integer instructions that take nibbles apart (two a cycle and SM).
 //
-// Layout (tts_bb_w4_pack): for 16 rows (one m16n8k16 tile high) and one group, a record of G * 8 bytes of
+// Main kernel (k_w4_staged): the half word 000c is the fp16 number c 2^-24, 00c0 is 16 c 2^-24 (subnormals and the first
+// binade are evenly spaced), so a word of 8 codes is a step's operand of m16n8k16 after one shift, four masks and four
+// multiply-adds to (code - zero) 2^-9, exact in fp16. (The subnormal numbers themselves as operands lose up to 5 bits of the
+// products' sum, measured; and zeros by the sums of x, scale (sum x code - zero sum x), lose the digits of a small sum
+// beside one large x whose weight is 0.) Each row of x is scaled by a power of two to a largest magnitude in [2^14, 2^15)
+// and stands in shared memory as fp16: bf16 rows exactly (down to 2^-29 of the row's largest), fp32 rows as two parts,
+// 24 bits together, each part a column of its own. So products are exact and sums fp32.
+//
+// Layout (tts_bb_w4_pack): for 16 rows of W (one m16n8k16 tile high) and one group, a record of G * 8 bytes of
 // codes and 16 parameter words. Lane (r = lane / 4, q = lane % 4) of a warp finds its codes of the group in
 // 16-byte pieces, one coalesced load each (G = 32: 8 bytes). Word i is the A operand of step i: nibble j the
 // low, nibble j + 4 the high half of register j: rows r (j even) and r + 8 (j odd), columns q G / 4 + 4 i + {0, 1}
 // (j < 2) and + {2, 3}; the columns of a group may stand in any order as long as x's do too, and this one gives a
-// lane contiguous x. Parameter word: bf16 -(128 + zero) in the low, bf16 scale in the high half.
+// lane contiguous x. Parameter word: fp16 -zero 2^-9 in the low, bf16 scale in the high half.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -50,12 +58,12 @@ __global__ void k_w4_pack(int N, int K, int G, const uint8_t* __restrict__ codes
         const size_t at = (size_t)n * groups + g;
         const uint32_t s = n < N ? __bfloat16_as_ushort(scales[at]) : 0u;
         const float z = n < N && zeros ? (float)(zeros[at] & 15) : 8.f;
-        reinterpret_cast<uint32_t*>(rec + G * 8)[lane] = s << 16 | __bfloat16_as_ushort(__float2bfloat16_rn(-(128.f + z)));
+        reinterpret_cast<uint32_t*>(rec + G * 8)[lane] = s << 16 | __half_as_ushort(__float2half_rn(-z * 0x1p-9f));
     }
 }
 
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -78,6 +86,9 @@ __device__ __forceinline__ float part_of(float x, uint32_t m1, uint32_t m2) {
 
 template <typename T> constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
 
+// For rows of x too long for shared memory: x is taken apart where it is used, into bf16 parts (fp32: three, by truncation:
+// 8 + 8 + 8 bits, together x itself), and the codes become whole numbers: 0x4300 | code is 128 + code, and adding
+// -(128 + zero) is exact.
 // grid (ceil(N / 16), chunks of x rows), WARPS * 32 threads: one 16-row tile, its groups dealt to the warps; NT tiles
 // of 8 columns, a column being one part of one row of x. The warps' sums are added in their order.
 template <typename T, int G, int NT>
@@ -105,7 +116,10 @@ __global__ void __launch_bounds__(WARPS * 32) k_w4_linear(int T_, int N, int K, 
         }
         const uint32_t p0 = reinterpret_cast<const uint32_t*>(rec + G * 8)[r];
         const uint32_t p1 = reinterpret_cast<const uint32_t*>(rec + G * 8)[r + 8];
-        const uint32_t z0 = __byte_perm(p0, p0, 0x1010), z1 = __byte_perm(p1, p1, 0x1010);
+        // -(128 + zero)
+        const float f0 = __half2float(__ushort_as_half((unsigned short)p0)), f1 = __half2float(__ushort_as_half((unsigned short)p1));
+        const uint32_t z0 = 0x10001u * __bfloat16_as_ushort(f2bf(f0 * 512.f - 128.f));
+        const uint32_t z1 = 0x10001u * __bfloat16_as_ushort(f2bf(f1 * 512.f - 128.f));
         float d[NT][4] = {};
         uint32_t a[WORDS][4];
 #pragma unroll
@@ -159,15 +173,203 @@ __global__ void __launch_bounds__(WARPS * 32) k_w4_linear(int T_, int N, int K, 
     }
 }
 
+// ---------------------------------------------------------------- x in shared memory
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) { unpack8(*reinterpret_cast<const uint4*>(p), v); }
+
+template <typename T> constexpr int COLS = sizeof(T) == 4 ? 2 : 1;  // fp16 parts, columns, of a row of x
+constexpr int RED_ROW = 17;
+__host__ __device__ constexpr size_t staged_bytes(int cols, int K) {
+    const int c8 = (cols + 7) / 8 * 8;
+    return (size_t)cols * K * 2 + (size_t)2 * WARPS * c8 * RED_ROW * 4;
+}
+
+template <int G> struct Record {
+    uint32_t w[G / 16], p0, p1;
+    __device__ __forceinline__ void load(const uint8_t* rec, int lane) {
+        if constexpr (G == 32) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(rec + lane * 8));
+            w[0] = v.x; w[1] = v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < G / 64; ++i) {
+                const uint4 v = ldg_nc_v4(rec + (i * 32 + lane) * 16);
+                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+            }
+        }
+        p0 = __ldg(reinterpret_cast<const uint32_t*>(rec + G * 8) + (lane >> 2));
+        p1 = __ldg(reinterpret_cast<const uint32_t*>(rec + G * 8) + (lane >> 2) + 8);
+    }
+};
+
+// grid (blocks, chunks of x rows), WARPS * 32 threads. A block stages its rows of x once and walks the 16-row tiles of W
+// with the stride of the grid; a tile's groups are dealt to the warps, the next record on its way while one is multiplied.
+// Shared memory: x as B registers, 16 bytes (two steps) a lane and piece: [group][G / 32 pieces][columns][4 lanes]; the warps'
+// sums of a tile, twice: one barrier a tile. Sums are added in the warps' order.
+template <typename T, int G, int NT>
+__global__ void __launch_bounds__(WARPS * 32, 2) k_w4_staged(int T_, int N, int K, const T* __restrict__ x, long long stride,
+                                                             const uint8_t* __restrict__ packed, T* __restrict__ y, int per) {
+    constexpr int P = COLS<T>, WORDS = G / 16, PIECES = G / 32, C8 = NT * 8;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ uint32_t largest[TTS_BB_W4_MAX_TOKENS];
+    const int t0 = blockIdx.y * per, rows = min(per, T_ - t0), cols = rows * P, groups = K / G, tiles = (N + 15) / 16;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, q = lane & 3;
+    uint4* const xs = reinterpret_cast<uint4*>(smem);
+    float* const red = reinterpret_cast<float*>(smem + (size_t)cols * K * 2);
+    if (tid < TTS_BB_W4_MAX_TOKENS) largest[tid] = 0u;
+    pdl_wait();  // the weights too: the launch before may be the one that packs them
+    pdl_trigger();
+    Record<G> cur, next;
+    int tile = blockIdx.x;
+    if (warp < groups) cur.load(packed + ((size_t)tile * groups + warp) * record_bytes(G), lane);
+    __syncthreads();
+    const int chunks = K / 8;  // 8 values each
+    for (int u0 = 0; u0 < rows * chunks; u0 += WARPS * 32) {
+        const int u = u0 + tid, row = min(u / chunks, rows - 1);
+        uint32_t b = 0u;  // the bits of magnitudes order them, infinities and NaN above all
+        if (u < rows * chunks) {
+            float v[8];
+            load8(x + (size_t)(t0 + row) * stride + (u - row * chunks) * 8, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b = max(b, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+        }
+        // a warp's 32 chunks mostly lie in one row
+        if (__all_sync(0xffffffffu, row == __shfl_sync(0xffffffffu, row, 0))) {
+            b = __reduce_max_sync(0xffffffffu, b);
+            if (lane == 0) atomicMax(&largest[row], b);
+        } else {
+            atomicMax(&largest[row], b);
+        }
+    }
+    __syncthreads();
+    // 2^(14 - exponent of the largest), the largest taken as at least 2^-103
+    const auto up_of = [&](int row) { return __uint_as_float((268u - min(max(largest[row] >> 23, 24u), 254u)) << 23); };
+    for (int u = tid; u < rows * chunks; u += WARPS * 32) {
+        const int row = u / chunks, chunk = u - row * chunks;
+        float v[8];
+        load8(x + (size_t)(t0 + row) * stride + chunk * 8, v);
+        const float up = up_of(row);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= up;
+        const int g = chunk / (G / 8), sub = chunk % (G / 8), lane_q = sub / PIECES, piece = sub % PIECES;
+#pragma unroll
+        for (int part = 0; part < P; ++part) {
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __half2 w = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+                const float2 f = __half22float2(w);
+                v[2 * e] -= f.x;
+                v[2 * e + 1] -= f.y;
+                h[e] = *reinterpret_cast<const uint32_t*>(&w);
+            }
+            xs[((g * PIECES + piece) * cols + row * P + part) * 4 + lane_q] = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+    }
+    __syncthreads();
+
+    int at[NT];  // this lane's column of each tile of 8; behind the last one, that one again: nobody reads its sums
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) at[nt] = min(nt * 8 + r, cols - 1) * 4 + q;
+    for (int turn = 0; tile < tiles; tile += gridDim.x, turn ^= 1) {
+        float acc[NT][4] = {};
+        for (int g = warp; g < groups; g += WARPS) {
+            const int g2 = g + WARPS < groups ? g + WARPS : warp, tile2 = g + WARPS < groups ? tile : tile + (int)gridDim.x;
+            if (tile2 < tiles) next.load(packed + ((size_t)tile2 * groups + g2) * record_bytes(G), lane);
+            const uint32_t z0 = __byte_perm(cur.p0, 0u, 0x1010), z1 = __byte_perm(cur.p1, 0u, 0x1010);
+            uint32_t a[WORDS][4];
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                const uint32_t w = cur.w[i], h = w >> 8;
+                // times 2^15 and 2^11
+                a[i][0] = fma_f16x2(w & 0x000F000Fu, 0x78007800u, z0);
+                a[i][1] = fma_f16x2(w & 0x00F000F0u, 0x68006800u, z1);
+                a[i][2] = fma_f16x2(h & 0x000F000Fu, 0x78007800u, z0);
+                a[i][3] = fma_f16x2(h & 0x00F000F0u, 0x68006800u, z1);
+            }
+            const float s0 = __uint_as_float(cur.p0 & 0xFFFF0000u), s1 = __uint_as_float(cur.p1 & 0xFFFF0000u);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float d[4] = {};
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i) {
+                    const uint4 b = xs[(g * PIECES + i) * cols * 4 + at[nt]];
+                    mma_f16(d, a[2 * i], b.x, b.y);
+                    mma_f16(d, a[2 * i + 1], b.z, b.w);
+                }
+                acc[nt][0] += s0 * d[0];
+                acc[nt][1] += s0 * d[1];
+                acc[nt][2] += s1 * d[2];
+                acc[nt][3] += s1 * d[3];
+            }
+            cur = next;
+        }
+        float* const mine = red + (size_t)(turn * WARPS + warp) * C8 * RED_ROW;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mine[(nt * 8 + 2 * q + (e & 1)) * RED_ROW + r + (e >> 1) * 8] = acc[nt][e];
+        __syncthreads();
+        for (int i = tid; i < rows * 16; i += WARPS * 32) {
+            const int row = i >> 4, n = i & 15;
+            float v = 0.f;
+#pragma unroll
+            for (int part = P - 1; part >= 0; --part)  // the small part first
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) v += red[((size_t)(turn * WARPS + w) * C8 + row * P + part) * RED_ROW + n];
+            // an infinity or a NaN in the row of x: NaN
+            const float f = largest[row] < 0x7F800000u ? 0x1p9f / up_of(row) : __int_as_float(0x7FC00000);
+            if (tile * 16 + n < N) y[(size_t)(t0 + row) * N + tile * 16 + n] = (T)(v * f);
+        }
+    }
+}
+
+// x in shared memory where 8 columns of it, or all, leave room for two blocks an SM; in chunks of as many rows as do.
+constexpr size_t STAGED_MOST = 100 * 1024, STAGED_ONE = 200 * 1024;
+
 template <typename T, int G>
 void launch(int T_, int N, int K, const void* x, int64_t stride, const void* packed, void* y, cudaStream_t st) {
+    const T* const xt = static_cast<const T*>(x);
+    const uint8_t* const w = static_cast<const uint8_t*>(packed);
+    T* const yt = static_cast<T*>(y);
+    const int tiles = (N + 15) / 16;
+    {
+        constexpr int P = COLS<T>;
+        int per = std::min(T_, 64 / P);
+        while (per * P > 8 && staged_bytes(per * P, K) > STAGED_MOST) per = std::max(8 / P, per / 2);
+        const size_t smem = staged_bytes(per * P, K);
+        if (smem <= STAGED_ONE) {
+            const int nt = (per * P + 7) / 8, chunks = (T_ + per - 1) / per;
+            const int blocks = std::min(tiles, std::max(1, 152 * (smem <= STAGED_MOST ? 2 : 1) / chunks));
+            auto go = [&](auto k) {
+                // every call: the attribute is the current device's
+                if (smem > 48 * 1024 - 1024) cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)STAGED_ONE);
+                launch_pdl(k, dim3(blocks, chunks), WARPS * 32, smem, st, T_, N, K, xt, (long long)stride, w, yt, per);
+            };
+            if (nt <= 1) go(k_w4_staged<T, G, 1>);
+            else if (nt <= 2) go(k_w4_staged<T, G, 2>);
+            else if (nt <= 4) go(k_w4_staged<T, G, 4>);
+            else go(k_w4_staged<T, G, 8>);
+            return;
+        }
+    }
     constexpr int P = PARTS<T>;
     const int per = std::min(T_, 64 / P), nt = (per * P + 7) / 8;
-    const dim3 grid((N + 15) / 16, (T_ + per - 1) / per);
-    auto go = [&](auto k) {
-        launch_pdl(k, grid, WARPS * 32, 0, st, T_, N, K, static_cast<const T*>(x), (long long)stride,
-                   static_cast<const uint8_t*>(packed), static_cast<T*>(y), per);
-    };
+    const dim3 grid(tiles, (T_ + per - 1) / per);
+    auto go = [&](auto k) { launch_pdl(k, grid, WARPS * 32, 0, st, T_, N, K, xt, (long long)stride, w, yt, per); };
     if (nt <= 1) go(k_w4_linear<T, G, 1>);
     else if (nt <= 2) go(k_w4_linear<T, G, 2>);
     else if (nt <= 4) go(k_w4_linear<T, G, 4>);

@@ -134,3 +134,31 @@ def test_two_streams_and_a_captured_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want[1])
+
+
+@pytest.mark.parametrize("io", ["float32", "bfloat16"])
+@pytest.mark.parametrize("N,K,G,T", [(70, 8192, 128, 5), (33, 16384, 64, 9), (16, 4096, 32, 64), (17, 16384, 128, 40), (5000, 256, 64, 2), (9000, 64, 32, 1)])
+def test_many_and_long_rows_of_x(N, K, G, T, io):
+    """Rows of x staged in chunks, rows too long to be staged at all, and more tiles than blocks."""
+    run(N, K, G, T, io, True)
+
+
+def test_pack_and_product_back_to_back():
+    """The product right behind the packing on one stream, again and again on one buffer, sees the new weights."""
+    m = tb()
+    rng = np.random.default_rng(8)
+    N, K, G = 2048, 512, 64
+    st = torch.cuda.current_stream().cuda_stream
+    sets = [weights(rng, N, K, G, True) for _ in range(4)]
+    on = [(dev(c), dev(s).bfloat16(), dev(z)) for c, s, z in sets]
+    x = dev(rng.standard_normal((1, K)).astype(np.float32))
+    p = torch.empty(m.tts_bb_w4_packed_bytes(N, K, G), dtype=torch.uint8, device="cuda")
+    ys = [torch.empty(1, N, device="cuda") for _ in sets]
+    torch.cuda.synchronize()
+    for (c, s, z), y in zip(on, ys):
+        m.tts_bb_w4_pack(N, K, G, c, s, z, p, st)
+        m.tts_bb_w4_linear(1, N, K, G, x, p, y, st)
+    for (c, s, z), y in zip(sets, ys):
+        w = unpack_w4(c, s, z, G)
+        xh = x.double().cpu().numpy()
+        assert (np.abs(y.double().cpu().numpy() - xh @ w.T) <= 2 * (K + 16) * U * (np.abs(xh) @ np.abs(w).T)).all()
