@@ -49,12 +49,6 @@ __device__ __forceinline__ float4 load4(const bf16* p) {
 __device__ __forceinline__ void store4(float* p, const float* x) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }
-__device__ __forceinline__ void store4(bf16* p, const float* x) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-
 // The block of (sequence row, position), or -1 with the reason in *err.
 __device__ __forceinline__ int find_block(const Cache& c, int seq, int pos, bool report) {
     if (seq >= c.n_seqs || pos < 0 || pos / KVB >= c.bps) {
@@ -70,186 +64,409 @@ __device__ __forceinline__ int find_block(const Cache& c, int seq, int pos, bool
 }
 
 // ---------------------------------------------------------------- append
-// Codes and parameters of one head of one token; lane l holds dims 4l .. 4l + 3 (lanes 0..15 group 0).
+// A head is held by 8 lanes (a warp holds four heads): lane l of them has dims 8l .. 8l + 7 of both groups, so the pairs
+// (i, i + 64) that RoPE rotates are a lane's own, and so are words 2l and 2l + 1 of the code row. x[0..7]: group 0, x[8..15]:
+// group 1.
 struct Quant {
-    uint32_t codes;  // 4 nibbles
-    uint32_t par;    // bf16 scale | bf16 offset << 16
+    uint32_t codes[2];  // a word of each group
+    uint32_t par[2];    // bf16 scale | bf16 offset << 16
 };
 
-template <typename F>
-__device__ __forceinline__ F half_min(F v) {
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float m;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+// two floats an instruction
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float a, float b) {
+    f2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void halves(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 mulp(f2 a, f2 b) {
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 addp(f2 a, f2 b) {
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 fmap(f2 a, f2 b, f2 c) {
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f2 both(float a) { return pair(a, a); }
+// over a head's 8 lanes; a NaN stays one
+__device__ __forceinline__ float head_min(float v) {
 #pragma unroll
-    for (int o = 8; o; o >>= 1) { const F w = __shfl_xor_sync(0xffffffffu, v, o); v = w < v ? w : v; }
+    for (int o = 4; o; o >>= 1) { const float w = __shfl_xor_sync(0xffffffffu, v, o); v = min3(v, w, w); }
     return v;
 }
-template <typename F>
-__device__ __forceinline__ F half_max(F v) {
+__device__ __forceinline__ float head_max(float v) {
 #pragma unroll
-    for (int o = 8; o; o >>= 1) { const F w = __shfl_xor_sync(0xffffffffu, v, o); v = w > v ? w : v; }
+    for (int o = 4; o; o >>= 1) { const float w = __shfl_xor_sync(0xffffffffu, v, o); v = max3(v, w, w); }
     return v;
 }
+__device__ __forceinline__ float head_sum(float v) {
+#pragma unroll
+    for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(bf16 x) { return bf2f(x); }
 __device__ __forceinline__ uint32_t bf_bits(float x) { return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 
-// The definition in 64 bits.
-__device__ __noinline__ Quant quant64(const double* x) {
-    const double lo = half_min(fmin(fmin(x[0], x[1]), fmin(x[2], x[3])));
-    const double hi = half_max(fmax(fmax(x[0], x[1]), fmax(x[2], x[3])));
-    const uint32_t sb = bf_bits((float)fmax((hi - lo) / 15.0, fmax(hi, -lo) / 120.0));
-    const double s = (double)__uint_as_float(sb << 16);
-    Quant q{0u, sb};
-    double zero = 0.0;
-    if (s > 0.0) {
-        zero = rint(lo / s);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) q.codes |= (uint32_t)(int)fmin(fmax(rint(x[e] / s) - zero, 0.0), 15.0) << (4 * e);
-    }
-    q.par |= bf_bits((float)zero - 128.f) << 16;
-    return q;
+// 8 values as pairs; 16- (bf16) or 32-byte pieces
+__device__ __forceinline__ void load8(const float* p, f2* v) {
+    const float4 a = load4(p), b = load4(p + 4);
+    v[0] = pair(a.x, a.y); v[1] = pair(a.z, a.w); v[2] = pair(b.x, b.y); v[3] = pair(b.z, b.w);
 }
-
-// The same in 32 bits, where x is known to within delta: false where a rounding could fall either way,
-// or where a group is not finite or too small for the arithmetic (quant64 and poison decide there).
-__device__ __forceinline__ bool quant32(const float* x, float delta, Quant& q) {
-    const float lo = half_min(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])));
-    const float hi = half_max(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
-    const float amax = fmaxf(hi, -lo);
-    const float s0 = fmaxf((hi - lo) * (1.f / 15.f), amax * (1.f / 120.f));
-    const float es = 0.15f * delta + s0 * 0x1p-21f;
-    const uint32_t sb = bf_bits(s0 - es);
-    bool sure = sb == bf_bits(s0 + es) && s0 > 1e-30f;
-    const float s = __uint_as_float(sb << 16);
-    const float inv = 1.f / s;
-    const float rel = 0x1p-21f * amax * inv + delta * inv;  // bound of the error of x / s
-    const float tz = lo * inv, zero = rintf(tz);
-    sure = sure && rintf(tz - rel) == rintf(tz + rel);
-    q.codes = 0u;
+__device__ __forceinline__ void load8(const bf16* p, f2* v) {
+    float f[8];
+    unpack8(*reinterpret_cast<const uint4*>(p), f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
+}
+__device__ __forceinline__ void store8(float* p, const f2* v) {
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) halves(v[e], f[2 * e], f[2 * e + 1]);
+    store4(p, f);
+    store4(p + 4, f + 4);
+}
+__device__ __forceinline__ void store8(bf16* p, const f2* v) {
+    uint32_t o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float t = x[e] * inv;
-        const float a = fminf(fmaxf(rintf(t - rel) - zero, 0.f), 15.f), b = fminf(fmaxf(rintf(t + rel) - zero, 0.f), 15.f);
-        sure = sure && a == b;
-        q.codes |= (uint32_t)(int)a << (4 * e);
+        float a, b;
+        halves(v[e], a, b);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        o[e] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    q.par = sb | bf_bits(zero - 128.f) << 16;
-    return sure;
+    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// grid T, 256 threads: token t's 16 q, 8 k and 8 v heads, four for each warp. q and k: RMSNorm over the
-// head with its gain, then the pairs (i, i + 64) rotated by the token's row of the cos / sin tables.
-// Bound by memory (8 or 16 KB read, 4 or 8 KB + 1152 B written for a token).
+// Numbers as the unevaluated sum of two floats, h the rounding of h + l: 48 bits, by error-free sums (Knuth) and products
+// (by fma). Doubles would do as well, but this GPU has few units for them: a pair of heads took 10 us in them.
+struct Two {
+    float h, l;
+};
+__device__ __forceinline__ Two norm2(float a, float b) {  // |a| >= |b|
+    const float s = __fadd_rn(a, b);
+    return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Two sum2(float a, float b) {
+    const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v))};
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+    const Two s = sum2(a.h, b.h);
+    return norm2(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    const float p = __fmul_rn(a.h, b.h);
+    return norm2(p, __fmaf_rn(a.h, b.h, -p) + __fmaf_rn(a.h, b.l, __fmul_rn(a.l, b.h)));
+}
+__device__ __forceinline__ Two neg2(Two a) { return {-a.h, -a.l}; }
+__device__ __forceinline__ bool less2(Two a, Two b) { return a.h < b.h || (a.h == b.h && a.l < b.l); }
+__device__ __forceinline__ Two div2(Two a, float b) {  // b a whole number: its products with 24 bits are kept by fma
+    const float q = __fdiv_rn(a.h, b);
+    return norm2(q, __fdiv_rn(__fadd_rn(__fmaf_rn(-q, b, a.h), a.l), b));
+}
+__device__ __forceinline__ Two peer2(Two a, int o) { return {__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)}; }
+// x / s to the nearest whole number, ties to even, from one of the two next to it: s has 8 bits, so (k + 1/2) s is exact and
+// one fma tells on which side of it x lies
+__device__ __forceinline__ float rint2(float k, Two x, float s) {
+    const float up = __fadd_rn(__fmaf_rn(-(k + 0.5f), s, x.h), x.l), down = __fadd_rn(__fmaf_rn(-(k - 0.5f), s, x.h), x.l);
+    const bool odd = (int)k & 1;
+    return up > 0.f || (up == 0.f && odd) ? k + 1.f : down < 0.f || (down == 0.f && odd) ? k - 1.f : k;
+}
+__device__ __forceinline__ float rint2(Two x, float s) { return rint2(rintf(__fdiv_rn(x.h, s)), x, s); }
+
+// The definition, in 48 bits: of the head's row x (normalised with its gain and rotated here where gain is given), lane l's dims;
+// all pointers at this lane's first dim. Seldom needed and long, so it is kept small: value by value, read again from
+// memory, and computed twice, for the range and for the codes.
+template <typename T>
+__device__ __forceinline__ void quant48(const T* x, const bf16* gain, const float* cs, const float* sn, float eps, Quant& q) {
+    const auto at = [&](int e) { return Two{to_float(x[e]), 0.f}; };
+    Two r = {1.f, 0.f};
+    if (gain) {
+        Two ss = {0.f, 0.f};
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) ss = add2(ss, add2(mul2(at(e), at(e)), mul2(at(HD / 2 + e), at(HD / 2 + e))));
+#pragma unroll
+        for (int o = 4; o; o >>= 1) ss = add2(ss, peer2(ss, o));
+        ss = add2({ss.h * (1.f / HD), ss.l * (1.f / HD)}, {eps, 0.f});
+        // one Newton step doubles the 23 bits of rsqrtf: r (1 + (1 - ss r r) / 2)
+        r.h = rsqrtf(ss.h);
+        const Two err = add2({1.f, 0.f}, neg2(mul2(ss, mul2(r, r))));
+        r = norm2(r.h, r.h * 0.5f * err.h);
+    }
+    const auto values = [&](int e, Two (&z)[2]) {
+        z[0] = at(e);
+        z[1] = at(HD / 2 + e);
+        if (gain) {
+            const Two a = mul2(mul2(z[0], r), {bf2f(gain[e]), 0.f}), b = mul2(mul2(z[1], r), {bf2f(gain[HD / 2 + e]), 0.f});
+            const Two c = {cs[e], 0.f}, s = {sn[e], 0.f};
+            z[0] = add2(mul2(a, c), neg2(mul2(b, s)));
+            z[1] = add2(mul2(b, c), mul2(a, s));
+        }
+    };
+    Two lo[2], hi[2], z[2];
+    values(0, lo);
+    values(0, hi);
+#pragma unroll 1
+    for (int e = 1; e < 8; ++e) {
+        values(e, z);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            lo[g] = less2(z[g], lo[g]) ? z[g] : lo[g];
+            hi[g] = less2(hi[g], z[g]) ? z[g] : hi[g];
+        }
+    }
+    float s[2], zero[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+#pragma unroll
+        for (int o = 4; o; o >>= 1) {
+            const Two a = peer2(lo[g], o), b = peer2(hi[g], o);
+            lo[g] = less2(a, lo[g]) ? a : lo[g];
+            hi[g] = less2(hi[g], b) ? b : hi[g];
+        }
+        const Two range = div2(add2(hi[g], neg2(lo[g])), 15.f), most = div2(less2(hi[g], neg2(lo[g])) ? neg2(lo[g]) : hi[g], 120.f);
+        const uint32_t sb = bf_bits(less2(range, most) ? most.h : range.h);
+        s[g] = __uint_as_float(sb << 16);
+        zero[g] = s[g] > 0.f ? rint2(lo[g], s[g]) : 0.f;
+        q.codes[g] = 0u;
+        q.par[g] = sb | bf_bits(zero[g] - 128.f) << 16;
+    }
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+        values(e, z);
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+            if (s[g] > 0.f) q.codes[g] |= (uint32_t)fminf(rint2(z[g], s[g]) - zero[g], 15.f) << (4 * e);
+    }
+}
+
+// The same for one group (the pairs x of a lane) in 32 bits, where x is known to within delta. SURE_SCALE: the scale's rounding
+// could not fall the other way (nor is the group too small for this arithmetic); SURE_CODES: no code's could; FINITE: all
+// values are. x / scale is rounded by adding and subtracting 1.5 2^23; the lowest value is one of the x, so its code is 0
+// and no code is below.
+enum { SURE_SCALE = 1, SURE_CODES = 2, SURE = 3, FINITE = 4 };
+constexpr float MAGIC = 12582912.f;
+__device__ __forceinline__ int quant32(const f2* x, float delta, uint32_t& codes, uint32_t& par) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) halves(x[e], v[2 * e], v[2 * e + 1]);
+    const float lo = head_min(min3(min3(min3(v[0], v[1], v[2]), v[3], v[4]), min3(v[5], v[6], v[7]), v[7]));
+    const float hi = head_max(max3(max3(max3(v[0], v[1], v[2]), v[3], v[4]), max3(v[5], v[6], v[7]), v[7]));
+    const float amax = max3(hi, -lo, -lo);
+    const float s0 = fmaxf((hi - lo) * (1.f / 15.f), amax * (1.f / 120.f));
+    const float es = 0.15f * delta + s0 * 0x1p-22f;  // three roundings, and x's
+    const uint32_t sb = bf_bits(s0 - es);
+    const float inv = __frcp_rn(__uint_as_float(sb << 16));
+    const float rel = 0x1p-22f * amax * inv + delta * inv;  // bound of the error of x / s: two roundings, and x's
+    const float zero = (lo * inv + MAGIC) - MAGIC;
+    const f2 inv2 = both(inv), magic = both(MAGIC), unmagic = both(-MAGIC), minus = both(-1.f), unzero = both(-zero);
+    float c[8], d[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const f2 t = mulp(x[e], inv2), k = addp(addp(t, magic), unmagic);
+        halves(fmap(k, minus, t), d[2 * e], d[2 * e + 1]);
+        halves(addp(k, unzero), c[2 * e], c[2 * e + 1]);
+    }
+    float far = 0.f;  // the furthest from a whole number
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) far = max3(far, fabsf(d[e]), fabsf(d[e + 1]));
+    uint32_t h[2];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = fminf(c[e], 15.f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        h[i] = __float_as_uint(fmaf(fmaf(c[4 * i + 3], 16.f, c[4 * i + 2]), 256.f, fmaf(c[4 * i + 1], 16.f, c[4 * i])) + 8388608.f);
+    codes = __byte_perm(h[0], h[1], 0x5410);
+    par = sb | bf_bits(zero - 128.f) << 16;
+    return (sb == bf_bits(s0 + es) && s0 > 1e-30f ? SURE_SCALE : 0) | (far < 0.5f - rel ? SURE_CODES : 0) | (amax < INFINITY ? FINITE : 0);
+}
+// The codes of exact values x for the scale that quant32 found: a value halfway between two codes, which bf16 rows meet
+// often (in two of five sets of four v heads), goes to the even whole number.
+template <typename T>
+__device__ __forceinline__ void exact_codes(const T* x, uint32_t& codes, uint32_t& par) {
+    const float s = __uint_as_float(par << 16), inv = __frcp_rn(s);
+    float first = 1e30f, k[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float v = to_float(x[e]);
+        k[e] = rint2((v * inv + MAGIC) - MAGIC, {v, 0.f}, s);
+        first = fminf(first, k[e]);  // of the lowest value
+    }
+    const float zero = head_min(first);
+    codes = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) codes |= (uint32_t)fminf(k[e] - zero, 15.f) << (4 * e);
+    par = (par & 0xFFFFu) | bf_bits(zero - 128.f) << 16;
+}
+
+// grid (T, 2), 128 threads: token t's 16 q heads, or its 8 k and 8 v heads, four a warp. q and k: RMSNorm over the head with
+// its gain, then the pairs (i, i + 64) rotated by the token's row of the cos / sin tables.
+// Bound by memory (8 or 16 KB read, 4 or 8 KB + 1152 B written for a token) and, nearly as much, by its instructions.
 //
 // A code next to a border between two would fall either way on the rounding of a 32-bit norm, and one
-// code off is a whole scale: 2e-5 of the values sit so near that quant32 is not sure, and their heads are
-// done again in 64 bits (about 1 % of the k heads), so that the codes are those of the definition.
-// delta bounds the 32-bit error of a rotated key: relative to |x_i cos| + |x_j sin|, 2^-24 times 4 (half of
-// the sum of squares' 8 roundings) + 4 (rsqrtf, 2 units) + 2 (norm and gain) + 2 (rotation) is below 16 * 2^-24.
-template <typename TI, typename TQ>
-__global__ void __launch_bounds__(256) k_kv4_append(const TI* __restrict__ qkv, long long stride,
+// code off is a whole scale. Where quant32 is not sure (about 3 % of the fours of k heads) the four are done again in 48
+// bits, so that the codes are those of the definition.
+// delta bounds the 32-bit error of a rotated key: relative to |x_i cos| + |x_j sin|, 2^-24 times 7 (half of the sum of
+// squares' 13 roundings, and the mean's) + 4 (rsqrtf, 2 units) + 2 (norm and gain) + 2 (rotation) is below 16 * 2^-24.
+// WHAT: HEADS_Q, HEADS_KV, or both
+enum { HEADS_Q = 1, HEADS_KV = 2 };
+template <int WHAT, typename TI, typename TQ>
+__global__ void __launch_bounds__(128, WHAT == HEADS_Q ? 12 : 8) k_kv4_append(const TI* __restrict__ qkv, long long stride,
                                                     const bf16* __restrict__ gq, const bf16* __restrict__ gk, float eps,
                                                     const float* __restrict__ cos_t, const float* __restrict__ sin_t,
                                                     int n_pos, const int32_t* __restrict__ seqs,
                                                     const int32_t* __restrict__ positions, Cache c, TQ* __restrict__ q_out) {
     pdl_wait();  // upstream results are read below
     pdl_trigger();
-    const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.x, warp = (WHAT == HEADS_KV ? 4 : blockIdx.y * 4) + (threadIdx.x >> 5), lane = threadIdx.x & 31, l = lane & 7;
+    const int head = warp * 4 + (lane >> 3);
     const int seq = seqs[t], pos = positions[t];
     if (seq < 0) return;
     if (pos >= n_pos) {
         if (threadIdx.x == 0) set_err(c.err, TTS_BB_KV4_ERR_RANGE);
         return;
     }
+    // pairs of dims of group 0, then of group 1
+    const TI* const row = qkv + (size_t)t * stride + head * HD + l * 8;
+    f2 x[8];
+    load8(row, x);
+    load8(row + HD / 2, x + 4);
     const int phys = find_block(c, seq, pos, threadIdx.x == 0);
     if (phys < 0) return;
-    uint8_t* const base = c.pool + (size_t)phys * BLOCK;
-    const int tok = pos % KVB;
-    const TI* row = qkv + (size_t)t * stride + lane * 4;
-    const int i0 = (lane & 15) * 4;
-    const float4 cs4 = load4(cos_t + (size_t)pos * (HD / 2) + i0), sn4 = load4(sin_t + (size_t)pos * (HD / 2) + i0);
-    const float cs[4] = {cs4.x, cs4.y, cs4.z, cs4.w};
-    const float sgn = lane < 16 ? -1.f : 1.f;
-    const float sn[4] = {sgn * sn4.x, sgn * sn4.y, sgn * sn4.z, sgn * sn4.w};
-    float4 in[4];
+    const bool is_q = WHAT == HEADS_Q || (WHAT != HEADS_KV && warp < 4), norm = is_q || warp < 6;
+    f2 y[8];
+    float delta = 0.f;
+    if (norm) {
+        f2 g[8], cs[4], sn[4];
+        const bf16* const gain = (is_q ? gq : gk) + l * 8;
+        load8(gain, g);
+        load8(gain + HD / 2, g + 4);
+        load8(cos_t + (size_t)pos * (HD / 2) + l * 8, cs);
+        load8(sin_t + (size_t)pos * (HD / 2) + l * 8, sn);
+        f2 ss = mulp(x[0], x[0]);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) in[u] = load4(row + (warp + 8 * u) * HD);
-    const float4 gq4 = load4(gq + lane * 4), gk4 = load4(gk + lane * 4);
+        for (int e = 1; e < 8; ++e) ss = fmap(x[e], x[e], ss);
+        float s0, s1;
+        halves(ss, s0, s1);
+        const f2 r = both(rsqrtf(head_sum(s0 + s1) * (1.f / HD) + eps)), minus = both(-1.f);
+        f2 v[8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const float x[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
-        float y[4];
-        float delta = 0.f;
-        const float4 g4 = u < 2 ? gq4 : gk4;
-        const float g[4] = {g4.x, g4.y, g4.z, g4.w};
-        if (u < 3) {
-            const float r = rsqrtf(warp_sum(x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3]) * (1.f / HD) + eps);
+        for (int e = 0; e < 8; ++e) v[e] = mulp(mulp(x[e], r), g[e]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float v = x[e] * r * g[e], a = v * cs[e], b = __shfl_xor_sync(0xffffffffu, v, 16) * sn[e];
-                y[e] = a + b;
-                delta = fmaxf(delta, fabsf(a) + fabsf(b));
+        for (int e = 0; e < 4; ++e) {
+            y[e] = fmap(v[e], cs[e], mulp(mulp(v[4 + e], sn[e]), minus));
+            y[4 + e] = fmap(v[4 + e], cs[e], mulp(v[e], sn[e]));
+        }
+        if (is_q) {
+            if (q_out) {
+                TQ* const to = q_out + ((size_t)t * NQ + head) * HD + l * 8;
+                store8(to, y);
+                store8(to + HD / 2, y + 4);
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = x[e];
+            return;
         }
-        if (u < 2) {
-            if (q_out) store4(q_out + ((size_t)t * NQ + warp + 8 * u) * HD + lane * 4, y);
-            continue;
+        float m = 0.f, n = 0.f;  // |v_i cos| + |v_j sin| is at most m n
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float a, b;
+            halves(v[e], a, b);
+            m = max3(m, fabsf(a), fabsf(b));
         }
-        bool finite = true;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) finite = finite && fabsf(y[e]) < INFINITY;
-        delta = u == 2 ? 0x1p-20f * warp_max(delta) : 0.f;
-        Quant q;
-        const bool sure = quant32(y, delta, q);
-        const unsigned bad = __ballot_sync(0xffffffffu, !finite);
-        if (!bad && __any_sync(0xffffffffu, !sure)) {
-            double z[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] = (double)x[e];
-            if (u == 2) {
-                double ss = z[0] * z[0] + z[1] * z[1] + z[2] * z[2] + z[3] * z[3];
-#pragma unroll
-                for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const double r = 1.0 / sqrt(ss / HD + (double)eps);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const double v = z[e] * r * (double)g[e];
-                    z[e] = v * (double)cs[e] + __shfl_xor_sync(0xffffffffu, v, 16) * (double)sn[e];
-                }
-            }
-            q = quant64(z);
+        for (int e = 0; e < 4; ++e) {
+            float a, b, p, q;
+            halves(cs[e], a, b);
+            halves(sn[e], p, q);
+            n = max3(n, fabsf(a) + fabsf(p), fabsf(b) + fabsf(q));
         }
-        // a group with a value that is not finite is held as NaN
-        if (bad >> (lane & 16) & 0xffffu) q = Quant{0u, 0xC3007FC0u};
-        uint8_t* const tile = base + (size_t)((u - 2) * NKV + warp) * TILE;
-        const int group = lane >> 4, w = ((lane & 15) >> 1) * 2 + group;
-        *reinterpret_cast<uint16_t*>(tile + tok * (HD / 2) + w * 4 + (lane & 1) * 2) = (uint16_t)q.codes;
-        if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(tile + PAR + tok * 8 + group * 4) = q.par;
+        delta = 0x1p-20f * head_max(m * n);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = x[e];
     }
+    Quant q;
+    const int sure0 = quant32(y, delta, q.codes[0], q.par[0]), sure1 = quant32(y + 4, delta, q.codes[1], q.par[1]);
+    if (__any_sync(0xffffffffu, (sure0 & sure1 & SURE) != SURE)) {
+        if (norm || __any_sync(0xffffffffu, !(sure0 & sure1 & SURE_SCALE))) {
+            const size_t at = (size_t)pos * (HD / 2) + l * 8;
+            quant48(row, norm ? gk + l * 8 : nullptr, cos_t + at, sin_t + at, eps, q);
+        } else {
+            if (__any_sync(0xffffffffu, !(sure0 & SURE_CODES))) exact_codes(row, q.codes[0], q.par[0]);
+            if (__any_sync(0xffffffffu, !(sure1 & SURE_CODES))) exact_codes(row + HD / 2, q.codes[1], q.par[1]);
+        }
+    }
+    // a group with a value that is not finite is held as NaN
+    if (!(sure0 & FINITE)) { q.codes[0] = 0u; q.par[0] = 0xC3007FC0u; }
+    if (!(sure1 & FINITE)) { q.codes[1] = 0u; q.par[1] = 0xC3007FC0u; }
+    uint8_t* const tile = c.pool + (size_t)phys * BLOCK + (size_t)(head - NQ) * TILE;  // k heads 0..7, then v heads
+    const int tok = pos % KVB;
+    *reinterpret_cast<uint2*>(tile + tok * (HD / 2) + l * 8) = make_uint2(q.codes[0], q.codes[1]);
+    if (l == 0) *reinterpret_cast<uint2*>(tile + PAR + tok * 8) = make_uint2(q.par[0], q.par[1]);
 }
 
 // ---------------------------------------------------------------- read
-// grid T, 256 threads: thread (head half, word) unpacks one word (8 dims) of K or V.
-__global__ void __launch_bounds__(256) k_kv4_read(const int32_t* __restrict__ seqs, const int32_t* __restrict__ positions,
+// grid ceil(T / N), 256 threads: thread (K or V, head, word) unpacks one word (8 dims) of each of N tokens, whose addresses
+// and words are all on their way before the first is unpacked.
+template <int N>
+__global__ void __launch_bounds__(256) k_kv4_read(int T, const int32_t* __restrict__ seqs, const int32_t* __restrict__ positions,
                                                   Cache c, bf16* __restrict__ k_out, bf16* __restrict__ v_out) {
     pdl_wait();  // upstream results are read below
     pdl_trigger();
-    const int t = blockIdx.x;
-    const int seq = seqs[t], pos = positions[t];
-    if (seq < 0) return;
-    const int phys = find_block(c, seq, pos, threadIdx.x == 0);
-    if (phys < 0) return;
-    const int unit = threadIdx.x >> 4, w = threadIdx.x & 15, tok = pos % KVB;  // unit: which * 8 + head
-    const uint8_t* tile = c.pool + (size_t)phys * BLOCK + (size_t)unit * TILE;
-    const uint32_t word = *reinterpret_cast<const uint32_t*>(tile + tok * (HD / 2) + w * 4);
-    const uint32_t par = *reinterpret_cast<const uint32_t*>(tile + PAR + tok * 8 + (w & 1) * 4);
-    const float s = __uint_as_float(par << 16), z = __uint_as_float(par & 0xFFFF0000u) + 128.f;
-    float x[8];
+    const int t0 = blockIdx.x * N, unit = threadIdx.x >> 4, w = threadIdx.x & 15;  // unit: which * 8 + head
+    int pos[N], phys[N];
+    uint32_t word[N], par[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = s * ((float)(word >> (4 * i) & 15u) + z);
-    bf16* out = (unit < NKV ? k_out : v_out) + ((size_t)t * NKV + (unit & 7)) * HD + 64 * (w & 1) + 8 * (w >> 1);
-    store4(out, x);
-    store4(out + 4, x + 4);
+    for (int i = 0; i < N; ++i) {
+        phys[i] = -1;
+        if (t0 + i < T) {
+            const int seq = seqs[t0 + i];
+            pos[i] = positions[t0 + i];
+            if (seq >= 0) phys[i] = find_block(c, seq, pos[i], threadIdx.x == 0);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (phys[i] < 0) continue;
+        const uint8_t* tile = c.pool + (size_t)phys[i] * BLOCK + (size_t)unit * TILE;
+        const int tok = pos[i] % KVB;
+        word[i] = *reinterpret_cast<const uint32_t*>(tile + tok * (HD / 2) + w * 4);
+        par[i] = *reinterpret_cast<const uint32_t*>(tile + PAR + tok * 8 + (w & 1) * 4);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (phys[i] < 0) continue;
+        // 2^23 + code, less 2^23 and plus the zero point: exact
+        const float s = __uint_as_float(par[i] << 16), z = __uint_as_float(par[i] & 0xFFFF0000u) + (128.f - 8388608.f);
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = __uint_as_float((word[i] >> (8 * e) & 15u) | 0x4B000000u) + z;
+            const float b = __uint_as_float((word[i] >> (8 * e + 4) & 15u) | 0x4B000000u) + z;
+            const __nv_bfloat162 v = __floats2bfloat162_rn(s * a, s * b);
+            o[e] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        bf16* out = (unit < NKV ? k_out : v_out) + ((size_t)(t0 + i) * NKV + (unit & 7)) * HD + 64 * (w & 1) + 8 * (w >> 1);
+        *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
 }
 
 // ---------------------------------------------------------------- attention
@@ -293,16 +510,16 @@ __device__ __forceinline__ bool attn_row(const Cache& c, const AttnArgs& a, int 
 //
 // Output, O^T[dim][column] += V^T P, by m16n8k16 on bf16, V's codes as A: rows are dims, and a register holds one dim of
 // two keys: one byte of both keys' words side by side, then one mask for the byte's even dim and one for its odd dim:
-// 000c is the bf16 number c 2^-133 and 00c0 16 c 2^-133 (subnormals again). Zero points are added to them, exact in 8 bits:
-// whole numbers around zero, not 0..15 with a middle added later, because where a softmax is flat the sums cancel
-// and a common offset would cost their digits. P times V's scale of the key and group is B, as bf16 parts by truncation
-// (bf16: two, 16 bits; fp32: three, all 24) in columns of their own. Weights are scaled by 2^60 to meet the 2^-133.
+// 000c is the bf16 number c 2^-133 and 00c0 16 c 2^-133 (subnormals again). A multiply-add makes them (code + zero) 2^-7,
+// exact in 8 bits: whole numbers around zero, not 0..15 with a middle added later, because where a softmax is flat the
+// sums cancel and a common offset would cost their digits. P times V's scale of the key and group is B, as bf16 parts by
+// truncation (bf16: two, 16 bits; fp32: three, all 24) in columns of their own.
 //
 // Softmax: a running reference m for each head, moved only when a score exceeds it by 8 (log2): then sums and O are
 // rescaled. It starts at -1e30, not -inf, so that no difference of infinities arises.
 constexpr int WARPS = 4, STAGES = 2, UNIT = 32, UNIT_BYTES = 4608;  // K and V codes 2048 each, parameters 256 each
 constexpr int V_AT = 2048, KP_AT = 4096, VP_AT = 4352;
-constexpr float M_START = -1e30f, M_SLACK = 8.f, P_LOG2 = 60.f;
+constexpr float M_START = -1e30f, M_SLACK = 8.f;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -328,17 +545,11 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
-__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
-__device__ __forceinline__ uint32_t lows(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 __device__ __forceinline__ uint32_t highs(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 __device__ __forceinline__ float as_f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t as_u(float x) { return __float_as_uint(x); }
@@ -454,7 +665,7 @@ __device__ __forceinline__ void attend_piece(const T* __restrict__ q, const Cach
     const int my = r + 8 * (c & 1);                       // this lane's key of 16; its head is c >> 1
     const uint8_t* const kat = mine + r * 64 + c * 16;
     const uint8_t* const vat = mine + V_AT + c * 64 + (r * 8 ^ (c >> 1) * 32);
-    float o[8][4] = {}, m = M_START - P_LOG2, l = 0.f;    // m: the reference less P_LOG2
+    float o[8][4] = {}, m = M_START, l = 0.f;
 
     // 16 keys: codes at byte `at` of the ring, parameters at `par`
     auto step = [&](auto tail, const int at, const int par, const int key0) {
@@ -466,7 +677,7 @@ __device__ __forceinline__ void attend_piece(const T* __restrict__ q, const Cach
             const uint4 k1 = *reinterpret_cast<const uint4*>(kat + at + 512);
             const uint2 kp = *reinterpret_cast<const uint2*>(mine + par + KP_AT + my * 8);
             const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-            uint32_t kz[2][2] = {};  // fp32: zero 2^-9 of keys r, r + 8 and each group, twice
+            [[maybe_unused]] uint32_t kz[2][2] = {};  // fp32: zero 2^-9 of keys r, r + 8 and each group, twice
             if constexpr (F32) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -510,13 +721,13 @@ __device__ __forceinline__ void attend_piece(const T* __restrict__ q, const Cach
         }
         const bool on = !TAIL || key0 + my < seen;
         if (!on) z = -INFINITY;
-        if (__any_sync(0xffffffffu, z > m + (M_SLACK + P_LOG2))) {
+        if (__any_sync(0xffffffffu, z > m + M_SLACK)) {
             float mx = z;
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float nm = fmaxf(m, mx - P_LOG2), f = ex2(m - nm), other = __shfl_xor_sync(0xffffffffu, f, 2);
+            const float nm = fmaxf(m, mx), f = ex2(m - nm), other = __shfl_xor_sync(0xffffffffu, f, 2);
             const float f0 = c & 2 ? other : f, f1 = c & 2 ? f : other;
             m = nm;
             l *= f;
@@ -560,20 +771,20 @@ __device__ __forceinline__ void attend_piece(const T* __restrict__ q, const Cach
                     b0 = __byte_perm(y[0], y[1], half_sel);
                     b1 = __byte_perm(y[2], y[3], half_sel);
                 }
-                uint32_t zero[2][2];  // [keys 0 1, keys 2 3][even, odd dims]: zero 2^-133, 16 zero 2^-133
+                uint32_t zero[2];  // keys 0 1, keys 2 3: zero 2^-7
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t off = highs(gr ? pp[2 * h].y : pp[2 * h].x, gr ? pp[2 * h + 1].y : pp[2 * h + 1].x);
-                    zero[h][0] = fma_bf16x2(off, 0x00010001u, 0x00800080u);
-                    zero[h][1] = fma_bf16x2(off, 0x00100010u, 0x02800280u);
+                    zero[h] = fma_bf16x2(off, 0x3C003C00u, 0x3F803F80u);
                 }
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {  // byte t of the words: dims 2 t, 2 t + 1 of lane r's 8
                     const uint32_t sel = 0x0400u + 0x1111u * t;
                     const uint32_t u01 = __byte_perm(gr ? w[0].y : w[0].x, gr ? w[1].y : w[1].x, sel);
                     const uint32_t u23 = __byte_perm(gr ? w[2].y : w[2].x, gr ? w[3].y : w[3].x, sel);
-                    const uint32_t x4[4] = {add_bf16x2(u01 & 0x000F000Fu, zero[0][0]), add_bf16x2(u01 & 0x00F000F0u, zero[0][1]),
-                                            add_bf16x2(u23 & 0x000F000Fu, zero[1][0]), add_bf16x2(u23 & 0x00F000F0u, zero[1][1])};
+                    // times 2^126 and 2^122
+                    const uint32_t x4[4] = {fma_bf16x2(u01 & 0x000F000Fu, 0x7E807E80u, zero[0]), fma_bf16x2(u01 & 0x00F000F0u, 0x7C807C80u, zero[0]),
+                                            fma_bf16x2(u23 & 0x000F000Fu, 0x7E807E80u, zero[1]), fma_bf16x2(u23 & 0x00F000F0u, 0x7C807C80u, zero[1])};
                     mma_bf16(o[4 * gr + t], x4, b0, b1);
                 }
             }
@@ -610,15 +821,15 @@ __device__ __forceinline__ void attend_piece(const T* __restrict__ q, const Cach
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 *reinterpret_cast<float2*>(so + ((warp * P + c) * 2 + h) * HD + d) =
-                    make_float2(o[t][h] * 0x1p73f, o[t][2 + h] * 0x1p69f);
+                    make_float2(o[t][h] * 128.f, o[t][2 + h] * 128.f);
         }
     }
-    if (lane == 0 || lane == 2) { sh.m[warp][lane >> 1] = m; sh.l[warp][lane >> 1] = l * 0x1p-60f; }
+    if (lane == 0 || lane == 2) { sh.m[warp][lane >> 1] = m; sh.l[warp][lane >> 1] = l; }
     __syncthreads();
     const int d = threadIdx.x;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        M[h] = M_START - P_LOG2;
+        M[h] = M_START;
         L[h] = O[h] = 0.f;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) M[h] = fmaxf(M[h], sh.m[w][h]);
@@ -663,7 +874,7 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict_
     cluster_sync();
     for (int i = split * WARPS * 32 + d; i < 2 * HD; i += a.n_splits * WARPS * 32) {
         const int h = i / HD;
-        float m1 = M_START - P_LOG2, l1 = 0.f, o1 = 0.f;
+        float m1 = M_START, l1 = 0.f, o1 = 0.f;
         for (int s = 0; s < a.n_splits; ++s) m1 = fmaxf(m1, peer(&ml[h][0], s));
         for (int s = 0; s < a.n_splits; ++s) {
             const float f = ex2(peer(&ml[h][0], s) - m1);
@@ -804,7 +1015,7 @@ __global__ void __launch_bounds__(128) k_kv4_combine(Cache c, AttnArgs a, int sh
     if (n == 1) return;  // written by its share
     const bool inside = from != (long long)s0 * line.share;  // the first piece ends its share
     auto at = [&](int i) { return place(a.part, s0 + i, i == 0 && inside) + h * PIECE; };
-    float M = M_START - P_LOG2;
+    float M = M_START;
     for (int i = lane; i < n; i += 32) M = fmaxf(M, at(i)[HD]);
     M = warp_max(M);
     float L = 0.f;
@@ -850,7 +1061,7 @@ Cache cache_of(const tts_bb_kv4* c) {
     return Cache{static_cast<uint8_t*>(c->pool), c->page_table, c->err, c->n_blocks, c->n_seqs, c->blocks_per_seq};
 }
 bool type_ok(int t) { return t == TTS_BB_T_F32 || t == TTS_BB_T_BF16; }
-bool aligned(const void* p, int type) { return (uintptr_t)p % (type == TTS_BB_T_F32 ? 16 : 8) == 0; }
+bool aligned(const void* p) { return (uintptr_t)p % 16 == 0; }
 tts_bb_status status() { return cudaPeekAtLastError() == cudaSuccess ? TTS_BB_OK : TTS_BB_E_CUDA; }
 
 // launch_pdl with clusters of n blocks along x
@@ -872,13 +1083,22 @@ void launch_cluster(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cud
     cudaLaunchKernelEx(&cfg, k, static_cast<KArgs>(args)...);
 }
 
+// Prompts take two launches: the q heads need half of the registers, and twice as many of their warps then hide memory.
+constexpr int SPLIT_TOKENS = 4096;
 template <typename TI, typename TQ>
 void append(int T, const void* qkv, int64_t stride, const void* gq, const void* gk, float eps, const float* cos_t,
             const float* sin_t, int n_pos, const int32_t* seqs, const int32_t* positions, const tts_bb_kv4* c, void* q_out,
             cudaStream_t st) {
-    launch_pdl(k_kv4_append<TI, TQ>, T, 256, 0, st, static_cast<const TI*>(qkv), (long long)stride,
-               static_cast<const bf16*>(gq), static_cast<const bf16*>(gk), eps, cos_t, sin_t, n_pos, seqs, positions,
-               cache_of(c), static_cast<TQ*>(q_out));
+    const auto go = [&](auto k, int parts) {
+        launch_pdl(k, dim3(T, parts), 128, 0, st, static_cast<const TI*>(qkv), (long long)stride, static_cast<const bf16*>(gq),
+                   static_cast<const bf16*>(gk), eps, cos_t, sin_t, n_pos, seqs, positions, cache_of(c), static_cast<TQ*>(q_out));
+    };
+    if (T < SPLIT_TOKENS) {
+        go(k_kv4_append<HEADS_Q | HEADS_KV, TI, TQ>, 2);
+    } else {
+        go(k_kv4_append<HEADS_KV, TI, TQ>, 1);
+        if (q_out) go(k_kv4_append<HEADS_Q, TI, TQ>, 1);
+    }
 }
 
 }  // namespace
@@ -900,9 +1120,8 @@ TTS_API tts_bb_status tts_bb_kv4_append(const tts_bb_kv4* cache, int T, const vo
                                         const float* sin_table, int n_pos, const int32_t* seqs, const int32_t* positions,
                                         void* q_out, int q_type, void* stream) {
     if (!cache_ok(cache) || T < 1 || !qkv || !q_norm || !k_norm || !cos_table || !sin_table || n_pos < 1 || !seqs ||
-        !positions || !type_ok(qkv_type) || !type_ok(q_type) || !(eps >= 0.f) || qkv_stride < QKV || qkv_stride % 4 ||
-        !aligned(qkv, qkv_type) || !aligned(q_out, q_type) || (uintptr_t)q_norm % 8 || (uintptr_t)k_norm % 8 ||
-        (uintptr_t)cos_table % 16 || (uintptr_t)sin_table % 16)
+        !positions || !type_ok(qkv_type) || !type_ok(q_type) || !(eps >= 0.f) || qkv_stride < QKV || qkv_stride % (qkv_type == TTS_BB_T_F32 ? 4 : 8) ||
+        !aligned(qkv) || !aligned(q_out) || !aligned(q_norm) || !aligned(k_norm) || !aligned(cos_table) || !aligned(sin_table))
         return TTS_BB_E_INVALID;
     if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -919,11 +1138,15 @@ TTS_API tts_bb_status tts_bb_kv4_append(const tts_bb_kv4* cache, int T, const vo
 
 TTS_API tts_bb_status tts_bb_kv4_read(const tts_bb_kv4* cache, int T, const int32_t* seqs, const int32_t* positions,
                                       void* k_out, void* v_out, void* stream) {
-    if (!cache_ok(cache) || T < 1 || !seqs || !positions || !k_out || !v_out || (uintptr_t)k_out % 8 || (uintptr_t)v_out % 8)
+    if (!cache_ok(cache) || T < 1 || !seqs || !positions || !k_out || !v_out || (uintptr_t)k_out % 16 || (uintptr_t)v_out % 16)
         return TTS_BB_E_INVALID;
     if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
-    launch_pdl(k_kv4_read, T, 256, 0, static_cast<cudaStream_t>(stream), seqs, positions, cache_of(cache),
-               static_cast<bf16*>(k_out), static_cast<bf16*>(v_out));
+    const auto go = [&](auto k, int n) {
+        launch_pdl(k, (T + n - 1) / n, 256, 0, static_cast<cudaStream_t>(stream), T, seqs, positions, cache_of(cache),
+                   static_cast<bf16*>(k_out), static_cast<bf16*>(v_out));
+    };
+    if (T < 4 * 8 * 152) go(k_kv4_read<1>, 1);  // fewer than four tokens for each of the 8 blocks an SM holds
+    else go(k_kv4_read<4>, 4);
     return status();
 }
 
@@ -937,7 +1160,7 @@ TTS_API tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S
                                            const int32_t* seqs, const int32_t* kv_lens, int max_len, void* out,
                                            void* workspace, size_t workspace_bytes, void* stream) {
     if (!cache_ok(cache) || B < 1 || S < 1 || S > TTS_BB_KV4_MAX_QUERIES || (long long)B * S > 65535 || !q || !kv_lens ||
-        !out || !type_ok(type) || !aligned(q, type) || !aligned(out, type) || max_len < 1 ||
+        !out || !type_ok(type) || !aligned(q) || !aligned(out) || max_len < 1 ||
         (long long)max_len > (long long)cache->blocks_per_seq * KVB || (!seqs && B > cache->n_seqs))
         return TTS_BB_E_INVALID;
     const size_t need = tts_bb_kv4_attention_workspace(B, S, max_len);

@@ -191,34 +191,18 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
 __device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) { unpack8(*reinterpret_cast<const uint4*>(p), v); }
 
 template <typename T> constexpr int COLS = sizeof(T) == 4 ? 2 : 1;  // fp16 parts, columns, of a row of x
-constexpr int RED_ROW = 17;
-__host__ __device__ constexpr size_t staged_bytes(int cols, int K) {
-    const int c8 = (cols + 7) / 8 * 8;
-    return (size_t)cols * K * 2 + (size_t)2 * WARPS * c8 * RED_ROW * 4;
+constexpr int RED_ROW = 17, STAGES = 4;
+// tiles of 8 columns that a kernel is built for
+constexpr int tiles_for(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 32 ? 4 : 8; }
+constexpr size_t staged_bytes(int cols, int K, int G) {
+    return (size_t)cols * K * 2 + (size_t)2 * WARPS * tiles_for(cols) * 8 * RED_ROW * 4 + (size_t)WARPS * STAGES * record_bytes(G);
 }
 
-template <int G> struct Record {
-    uint32_t w[G / 16], p0, p1;
-    __device__ __forceinline__ void load(const uint8_t* rec, int lane) {
-        if constexpr (G == 32) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(rec + lane * 8));
-            w[0] = v.x; w[1] = v.y;
-        } else {
-#pragma unroll
-            for (int i = 0; i < G / 64; ++i) {
-                const uint4 v = ldg_nc_v4(rec + (i * 32 + lane) * 16);
-                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-            }
-        }
-        p0 = __ldg(reinterpret_cast<const uint32_t*>(rec + G * 8) + (lane >> 2));
-        p1 = __ldg(reinterpret_cast<const uint32_t*>(rec + G * 8) + (lane >> 2) + 8);
-    }
-};
-
 // grid (blocks, chunks of x rows), WARPS * 32 threads. A block stages its rows of x once and walks the 16-row tiles of W
-// with the stride of the grid; a tile's groups are dealt to the warps, the next record on its way while one is multiplied.
+// with the stride of the grid; a tile's groups are dealt to the warps, whose records come by cp.async through a ring of each
+// warp's own, three on their way while one is multiplied.
 // Shared memory: x as B registers, 16 bytes (two steps) a lane and piece: [group][G / 32 pieces][columns][4 lanes]; the warps'
-// sums of a tile, twice: one barrier a tile. Sums are added in the warps' order.
+// sums of a tile, twice: one barrier a tile; the rings. Sums are added in the warps' order.
 template <typename T, int G, int NT>
 __global__ void __launch_bounds__(WARPS * 32, 2) k_w4_staged(int T_, int N, int K, const T* __restrict__ x, long long stride,
                                                              const uint8_t* __restrict__ packed, T* __restrict__ y, int per) {
@@ -232,9 +216,26 @@ __global__ void __launch_bounds__(WARPS * 32, 2) k_w4_staged(int T_, int N, int 
     if (tid < TTS_BB_W4_MAX_TOKENS) largest[tid] = 0u;
     pdl_wait();  // the weights too: the launch before may be the one that packs them
     pdl_trigger();
-    Record<G> cur, next;
-    int tile = blockIdx.x;
-    if (warp < groups) cur.load(packed + ((size_t)tile * groups + warp) * record_bytes(G), lane);
+    constexpr int REC = record_bytes(G);
+    uint8_t* const ring = reinterpret_cast<uint8_t*>(red + 2 * WARPS * C8 * RED_ROW) + warp * STAGES * REC;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    int ahead_tile = warp < groups ? blockIdx.x : tiles, ahead_g = warp, slot = 0;  // what comes next, and into which place
+    const auto fetch = [&] {
+        if (ahead_tile < tiles) {
+            const uint8_t* src = packed + ((size_t)ahead_tile * groups + ahead_g) * REC + lane * 16;
+            const uint32_t dst = ring_at + slot * REC + lane * 16;
+#pragma unroll
+            for (int i = 0; i < REC; i += 512)
+                if (i + 512 <= REC || lane * 16 < REC - i)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i), "l"(src + i) : "memory");
+            ahead_g += WARPS;
+            if (ahead_g >= groups) { ahead_g = warp; ahead_tile += gridDim.x; }
+        }
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) fetch();
     __syncthreads();
     const int chunks = K / 8;  // 8 values each
     for (int u0 = 0; u0 < rows * chunks; u0 += WARPS * 32) {
@@ -284,23 +285,39 @@ __global__ void __launch_bounds__(WARPS * 32, 2) k_w4_staged(int T_, int N, int 
     int at[NT];  // this lane's column of each tile of 8; behind the last one, that one again: nobody reads its sums
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) at[nt] = min(nt * 8 + r, cols - 1) * 4 + q;
-    for (int turn = 0; tile < tiles; tile += gridDim.x, turn ^= 1) {
+    int use = 0;  // the place of the record at hand
+    for (int tile = blockIdx.x, turn = 0; tile < tiles; tile += gridDim.x, turn ^= 1) {
         float acc[NT][4] = {};
         for (int g = warp; g < groups; g += WARPS) {
-            const int g2 = g + WARPS < groups ? g + WARPS : warp, tile2 = g + WARPS < groups ? tile : tile + (int)gridDim.x;
-            if (tile2 < tiles) next.load(packed + ((size_t)tile2 * groups + g2) * record_bytes(G), lane);
-            const uint32_t z0 = __byte_perm(cur.p0, 0u, 0x1010), z1 = __byte_perm(cur.p1, 0u, 0x1010);
+            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+            __syncwarp();
+            fetch();  // into the place of the record before
+            const uint8_t* const rec = ring + use * REC;
+            use = use + 1 == STAGES ? 0 : use + 1;
+            uint32_t cw[WORDS];
+            if constexpr (WORDS == 2) {
+                const uint2 v = *reinterpret_cast<const uint2*>(rec + lane * 8);
+                cw[0] = v.x; cw[1] = v.y;
+            } else {
+#pragma unroll
+                for (int i = 0; i < WORDS / 4; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(rec + (i * 32 + lane) * 16);
+                    cw[4 * i] = v.x; cw[4 * i + 1] = v.y; cw[4 * i + 2] = v.z; cw[4 * i + 3] = v.w;
+                }
+            }
+            const uint32_t p0 = reinterpret_cast<const uint32_t*>(rec + G * 8)[r], p1 = reinterpret_cast<const uint32_t*>(rec + G * 8)[r + 8];
+            const uint32_t z0 = __byte_perm(p0, 0u, 0x1010), z1 = __byte_perm(p1, 0u, 0x1010);
             uint32_t a[WORDS][4];
 #pragma unroll
             for (int i = 0; i < WORDS; ++i) {
-                const uint32_t w = cur.w[i], h = w >> 8;
+                const uint32_t w = cw[i], h = w >> 8;
                 // times 2^15 and 2^11
                 a[i][0] = fma_f16x2(w & 0x000F000Fu, 0x78007800u, z0);
                 a[i][1] = fma_f16x2(w & 0x00F000F0u, 0x68006800u, z1);
                 a[i][2] = fma_f16x2(h & 0x000F000Fu, 0x78007800u, z0);
                 a[i][3] = fma_f16x2(h & 0x00F000F0u, 0x68006800u, z1);
             }
-            const float s0 = __uint_as_float(cur.p0 & 0xFFFF0000u), s1 = __uint_as_float(cur.p1 & 0xFFFF0000u);
+            const float s0 = __uint_as_float(p0 & 0xFFFF0000u), s1 = __uint_as_float(p1 & 0xFFFF0000u);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float d[4] = {};
@@ -315,7 +332,6 @@ __global__ void __launch_bounds__(WARPS * 32, 2) k_w4_staged(int T_, int N, int 
                 acc[nt][2] += s1 * d[2];
                 acc[nt][3] += s1 * d[3];
             }
-            cur = next;
         }
         float* const mine = red + (size_t)(turn * WARPS + warp) * C8 * RED_ROW;
 #pragma unroll
@@ -338,7 +354,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) k_w4_staged(int T_, int N, int 
 }
 
 // x in shared memory where 8 columns of it, or all, leave room for two blocks an SM; in chunks of as many rows as do.
-constexpr size_t STAGED_MOST = 100 * 1024, STAGED_ONE = 200 * 1024;
+constexpr size_t STAGED_MOST = 112 * 1024, STAGED_ONE = 220 * 1024;
 
 template <typename T, int G>
 void launch(int T_, int N, int K, const void* x, int64_t stride, const void* packed, void* y, cudaStream_t st) {
@@ -349,30 +365,30 @@ void launch(int T_, int N, int K, const void* x, int64_t stride, const void* pac
     {
         constexpr int P = COLS<T>;
         int per = std::min(T_, 64 / P);
-        while (per * P > 8 && staged_bytes(per * P, K) > STAGED_MOST) per = std::max(8 / P, per / 2);
-        const size_t smem = staged_bytes(per * P, K);
+        while (per * P > 8 && staged_bytes(per * P, K, G) > STAGED_MOST) per = std::max(8 / P, per / 2);
+        const size_t smem = staged_bytes(per * P, K, G);
         if (smem <= STAGED_ONE) {
-            const int nt = (per * P + 7) / 8, chunks = (T_ + per - 1) / per;
+            const int nt = tiles_for(per * P), chunks = (T_ + per - 1) / per;
             const int blocks = std::min(tiles, std::max(1, 152 * (smem <= STAGED_MOST ? 2 : 1) / chunks));
             auto go = [&](auto k) {
                 // every call: the attribute is the current device's
                 if (smem > 48 * 1024 - 1024) cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)STAGED_ONE);
                 launch_pdl(k, dim3(blocks, chunks), WARPS * 32, smem, st, T_, N, K, xt, (long long)stride, w, yt, per);
             };
-            if (nt <= 1) go(k_w4_staged<T, G, 1>);
-            else if (nt <= 2) go(k_w4_staged<T, G, 2>);
-            else if (nt <= 4) go(k_w4_staged<T, G, 4>);
+            if (nt == 1) go(k_w4_staged<T, G, 1>);
+            else if (nt == 2) go(k_w4_staged<T, G, 2>);
+            else if (nt == 4) go(k_w4_staged<T, G, 4>);
             else go(k_w4_staged<T, G, 8>);
             return;
         }
     }
     constexpr int P = PARTS<T>;
-    const int per = std::min(T_, 64 / P), nt = (per * P + 7) / 8;
+    const int per = std::min(T_, 64 / P), nt = tiles_for(per * P);
     const dim3 grid(tiles, (T_ + per - 1) / per);
     auto go = [&](auto k) { launch_pdl(k, grid, WARPS * 32, 0, st, T_, N, K, xt, (long long)stride, w, yt, per); };
-    if (nt <= 1) go(k_w4_linear<T, G, 1>);
-    else if (nt <= 2) go(k_w4_linear<T, G, 2>);
-    else if (nt <= 4) go(k_w4_linear<T, G, 4>);
+    if (nt == 1) go(k_w4_linear<T, G, 1>);
+    else if (nt == 2) go(k_w4_linear<T, G, 2>);
+    else if (nt == 4) go(k_w4_linear<T, G, 4>);
     else go(k_w4_linear<T, G, 8>);
 }
 

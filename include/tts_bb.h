@@ -546,26 +546,27 @@ tts_bb_status tts_bb_rope_tables(double theta, int n_pos, float* cos_table, floa
  * q_out row too) and reported in cache->err. The (row, position) pairs of one call must differ, else what
  * that position holds is unspecified.
  *   qkv        [T] rows of 4096 (16 q, 8 k, 8 v heads of 128), fp32 or bf16 (qkv_type), rows
- *              qkv_stride elements apart (>= 4096, a multiple of 4), 16- (fp32) or 8-byte aligned
- *   q_norm, k_norm  bf16 [128] gains; eps inside the root
+ *              qkv_stride elements apart (>= 4096), every row 16-byte aligned
+ *   q_norm, k_norm  bf16 [128] gains, 16-byte aligned; eps inside the root
  *   cos_table, sin_table  fp32 [n_pos][64], 16-byte aligned; the pairs (i, i + 64) rotate by row positions[t]
  *   seqs, positions int32 [T]
- *   q_out      fp32 or bf16 (q_type) [T][16][128]: the rotated queries, or NULL
- * The codes and parameters are those of the exact arithmetic (keys next to a border are decided in 64 bits). */
+ *   q_out      fp32 or bf16 (q_type) [T][16][128]: the rotated queries, 16-byte aligned, or NULL
+ * The codes and parameters are those of the exact arithmetic (values next to a border between two codes are decided
+ * in 48 bits), for q and k up to 1e18 in magnitude, beyond which their squares overflow. */
 tts_bb_status tts_bb_kv4_append(const tts_bb_kv4* cache, int T, const void* qkv, int qkv_type, int64_t qkv_stride,
                                 const void* q_norm, const void* k_norm, float eps, const float* cos_table,
                                 const float* sin_table, int n_pos, const int32_t* seqs, const int32_t* positions,
                                 void* q_out, int q_type, void* stream);
 
 /* The values the cache holds for T tokens (seqs, positions as in tts_bb_kv4_append), rounded to bf16:
- * k_out, v_out bf16 [T][8][128], 8-byte aligned. Rows of padding and of tokens out of range are left as they were. */
+ * k_out, v_out bf16 [T][8][128], 16-byte aligned. Rows of padding and of tokens out of range are left as they were. */
 tts_bb_status tts_bb_kv4_read(const tts_bb_kv4* cache, int T, const int32_t* seqs, const int32_t* positions,
                               void* k_out, void* v_out, void* stream);
 
 /* Grouped-query attention over the cache, S causal query tokens for each of B sequences: a decode step
  * (S = 1) or a short chunk whose keys are already appended. Query head h reads KV head h / 2, scale
  * 1 / sqrt(128), softmax and sums in fp32.
- *   q, out    fp32 or bf16 (type) [B][S][16][128], 16- (fp32) or 8-byte aligned
+ *   q, out    fp32 or bf16 (type) [B][S][16][128], 16-byte aligned
  *   seqs      int32 [B], the cache row of each sequence (negative: padding, its out rows are left as
  *             they were), or NULL: sequence b reads row b
  *   kv_lens   int32 [B], the sequence's keys, those of the S query tokens among them: query s sees the first
