@@ -461,8 +461,11 @@ def _arg(x, name: str, types: _Types, n: int):
 def _rows(x, name: str, types: _Types, R: int, n: int):
     """(address, row stride) of a device tensor of R rows of at least n elements: two dimensions, the last one
     contiguous, or anything contiguous."""
-    if x.dim() == 2 and x.shape[0] >= R and x.shape[1] >= n and x.stride(1) == 1 and types[x.dtype] is not None and x.is_cuda:
-        return x.data_ptr(), x.stride(0) if R > 1 else n
+    if types[x.dtype] is not None and x.is_cuda and x.dim() == 2:
+        rows, cols = x.shape
+        stride, one = x.stride()
+        if one == 1 and rows >= R and cols >= n:
+            return x.data_ptr(), stride if R > 1 else n
     return _arg(x, name, types, R * n), n
 
 
@@ -556,9 +559,9 @@ def tts_bb_w4_linear(T: int, N: int, K: int, group: int, x, packed, y, stream: i
     if x.dtype != y.dtype:
         raise TypeError(f"x and y have to be of one type, not {x.dtype} and {y.dtype}")
     at, stride = _rows(x, "x", _IO, T, K)
-    st = lib.tts_bb_w4_linear(T, N, K, group, at, _IO[x.dtype], stride,
-                              _arg(packed, "packed", _U8, lib.tts_bb_w4_packed_bytes(N, K, group)), _arg(y, "y", _IO, T * N),
-                              stream or None)
+    need = (N + 15) // 16 * (K // group) * (8 * group + 64) if group > 0 else 0
+    st = lib.tts_bb_w4_linear(T, N, K, group, at, _IO[x.dtype], stride, _arg(packed, "packed", _U8, need),
+                              _arg(y, "y", _IO, T * N), stream or None)
     return _status(st, "tts_bb_w4_linear", check)
 
 

@@ -4,6 +4,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace ttsbb {
 
 typedef __nv_bfloat16 bf16;
@@ -147,6 +149,21 @@ inline cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, size_t
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k, static_cast<KArgs>(args)...);
+}
+
+// The largest dynamic shared memory of a kernel raised to `bytes`, once a kernel (each has a `State` of its own) and device:
+// the attribute belongs to the current device.
+struct SmemState {
+    std::atomic<uint64_t> done{0};  // a bit a device
+};
+template <typename K>
+inline void allow_smem(SmemState& s, K* kernel, size_t bytes) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+    if (s.done.load(std::memory_order_acquire) & bit) return;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess)
+        s.done.fetch_or(bit, std::memory_order_release);
 }
 
 // ---------------------------------------------------------------- kernels

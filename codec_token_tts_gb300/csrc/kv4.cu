@@ -126,6 +126,28 @@ __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(bf16 x) { return bf2f(x); }
 __device__ __forceinline__ uint32_t bf_bits(float x) { return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 
+// 8 values as they stand in memory (so few registers hold a row ahead of its use), and as pairs
+template <typename T> struct Raw8 { uint4 v[sizeof(T) / 2]; };
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8(const T* p) {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = ldg_nc_v4(reinterpret_cast<const uint4*>(p) + i);
+    return r;
+}
+__device__ __forceinline__ void pairs_of(const Raw8<float>& r, f2* v) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        v[2 * i] = pair(__uint_as_float(r.v[i].x), __uint_as_float(r.v[i].y));
+        v[2 * i + 1] = pair(__uint_as_float(r.v[i].z), __uint_as_float(r.v[i].w));
+    }
+}
+__device__ __forceinline__ void pairs_of(const Raw8<bf16>& r, f2* v) {
+    float f[8];
+    unpack8(r.v[0], f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
+}
 // 8 values as pairs; 16- (bf16) or 32-byte pieces
 __device__ __forceinline__ void load8(const float* p, f2* v) {
     const float4 a = load4(p), b = load4(p + 4);
@@ -318,8 +340,9 @@ __device__ __forceinline__ void exact_codes(const T* x, uint32_t& codes, uint32_
     par = (par & 0xFFFFu) | bf_bits(zero - 128.f) << 16;
 }
 
-// grid (T, 2), 128 threads: token t's 16 q heads, or its 8 k and 8 v heads, four a warp. q and k: RMSNorm over the head with
-// its gain, then the pairs (i, i + 64) rotated by the token's row of the cos / sin tables.
+// grid (tokens at most, parts), 128 threads: a token's 16 q heads, or its 8 k and 8 v heads, four a warp; a block goes on with
+// the token a grid further, whose row is on its way meanwhile. q and k: RMSNorm over the head with its gain, then the
+// pairs (i, i + 64) rotated by the token's row of the cos / sin tables.
 // Bound by memory (8 or 16 KB read, 4 or 8 KB + 1152 B written for a token) and, nearly as much, by its instructions.
 //
 // A code next to a border between two would fall either way on the rounding of a 32-bit norm, and one
@@ -330,97 +353,107 @@ __device__ __forceinline__ void exact_codes(const T* x, uint32_t& codes, uint32_
 // WHAT: HEADS_Q, HEADS_KV, or both
 enum { HEADS_Q = 1, HEADS_KV = 2 };
 template <int WHAT, typename TI, typename TQ>
-__global__ void __launch_bounds__(128, WHAT == HEADS_Q ? 12 : 8) k_kv4_append(const TI* __restrict__ qkv, long long stride,
+__global__ void __launch_bounds__(128, 8) k_kv4_append(int T, const TI* __restrict__ qkv, long long stride,
                                                     const bf16* __restrict__ gq, const bf16* __restrict__ gk, float eps,
                                                     const float* __restrict__ cos_t, const float* __restrict__ sin_t,
                                                     int n_pos, const int32_t* __restrict__ seqs,
                                                     const int32_t* __restrict__ positions, Cache c, TQ* __restrict__ q_out) {
     pdl_wait();  // upstream results are read below
     pdl_trigger();
-    const int t = blockIdx.x, warp = (WHAT == HEADS_KV ? 4 : blockIdx.y * 4) + (threadIdx.x >> 5), lane = threadIdx.x & 31, l = lane & 7;
+    const int warp = (WHAT == HEADS_KV ? 4 : blockIdx.y * 4) + (threadIdx.x >> 5), lane = threadIdx.x & 31, l = lane & 7;
     const int head = warp * 4 + (lane >> 3);
-    const int seq = seqs[t], pos = positions[t];
-    if (seq < 0) return;
-    if (pos >= n_pos) {
-        if (threadIdx.x == 0) set_err(c.err, TTS_BB_KV4_ERR_RANGE);
-        return;
+    int t = blockIdx.x, next_seq = seqs[t], next_pos = positions[t];
+    Raw8<TI> next0 = raw8(qkv + (size_t)t * stride + head * HD + l * 8), next1 = raw8(qkv + (size_t)t * stride + head * HD + HD / 2 + l * 8);
+    for (; t < T; t += gridDim.x) {
+        const TI* const row = qkv + (size_t)t * stride + head * HD + l * 8;
+        const int seq = next_seq, pos = next_pos;
+        f2 x[8];  // pairs of dims of group 0, then of group 1
+        pairs_of(next0, x);
+        pairs_of(next1, x + 4);
+        if (t + (int)gridDim.x < T) {
+            const TI* const ahead = row + (size_t)gridDim.x * stride;
+            next_seq = seqs[t + gridDim.x];
+            next_pos = positions[t + gridDim.x];
+            next0 = raw8(ahead);
+            next1 = raw8(ahead + HD / 2);
     }
-    // pairs of dims of group 0, then of group 1
-    const TI* const row = qkv + (size_t)t * stride + head * HD + l * 8;
-    f2 x[8];
-    load8(row, x);
-    load8(row + HD / 2, x + 4);
-    const int phys = find_block(c, seq, pos, threadIdx.x == 0);
-    if (phys < 0) return;
-    const bool is_q = WHAT == HEADS_Q || (WHAT != HEADS_KV && warp < 4), norm = is_q || warp < 6;
-    f2 y[8];
-    float delta = 0.f;
-    if (norm) {
-        f2 g[8], cs[4], sn[4];
-        const bf16* const gain = (is_q ? gq : gk) + l * 8;
-        load8(gain, g);
-        load8(gain + HD / 2, g + 4);
-        load8(cos_t + (size_t)pos * (HD / 2) + l * 8, cs);
-        load8(sin_t + (size_t)pos * (HD / 2) + l * 8, sn);
-        f2 ss = mulp(x[0], x[0]);
+        if (seq < 0) continue;
+        if (pos >= n_pos) {
+            if (threadIdx.x == 0) set_err(c.err, TTS_BB_KV4_ERR_RANGE);
+            continue;
+    }
+        const int phys = find_block(c, seq, pos, threadIdx.x == 0);
+        if (phys < 0) continue;
+        const bool is_q = WHAT == HEADS_Q || (WHAT != HEADS_KV && warp < 4), norm = is_q || warp < 6;
+        f2 y[8];
+        float delta = 0.f;
+        if (norm) {
+            f2 g[8], cs[4], sn[4];
+            const bf16* const gain = (is_q ? gq : gk) + l * 8;
+            load8(gain, g);
+            load8(gain + HD / 2, g + 4);
+            load8(cos_t + (size_t)pos * (HD / 2) + l * 8, cs);
+            load8(sin_t + (size_t)pos * (HD / 2) + l * 8, sn);
+            f2 ss = mulp(x[0], x[0]);
 #pragma unroll
-        for (int e = 1; e < 8; ++e) ss = fmap(x[e], x[e], ss);
-        float s0, s1;
-        halves(ss, s0, s1);
-        const f2 r = both(rsqrtf(head_sum(s0 + s1) * (1.f / HD) + eps)), minus = both(-1.f);
-        f2 v[8];
+            for (int e = 1; e < 8; ++e) ss = fmap(x[e], x[e], ss);
+            float s0, s1;
+            halves(ss, s0, s1);
+            const f2 r = both(rsqrtf(head_sum(s0 + s1) * (1.f / HD) + eps)), minus = both(-1.f);
+            f2 v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = mulp(mulp(x[e], r), g[e]);
+            for (int e = 0; e < 8; ++e) v[e] = mulp(mulp(x[e], r), g[e]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            y[e] = fmap(v[e], cs[e], mulp(mulp(v[4 + e], sn[e]), minus));
-            y[4 + e] = fmap(v[4 + e], cs[e], mulp(v[e], sn[e]));
-        }
-        if (is_q) {
-            if (q_out) {
-                TQ* const to = q_out + ((size_t)t * NQ + head) * HD + l * 8;
-                store8(to, y);
-                store8(to + HD / 2, y + 4);
+            for (int e = 0; e < 4; ++e) {
+                y[e] = fmap(v[e], cs[e], mulp(mulp(v[4 + e], sn[e]), minus));
+                y[4 + e] = fmap(v[4 + e], cs[e], mulp(v[e], sn[e]));
             }
-            return;
-        }
-        float m = 0.f, n = 0.f;  // |v_i cos| + |v_j sin| is at most m n
+            if (is_q) {
+                if (q_out) {
+                    TQ* const to = q_out + ((size_t)t * NQ + head) * HD + l * 8;
+                    store8(to, y);
+                    store8(to + HD / 2, y + 4);
+                }
+                continue;
+            }
+            float m = 0.f, n = 0.f;  // |v_i cos| + |v_j sin| is at most m n
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float a, b;
-            halves(v[e], a, b);
-            m = max3(m, fabsf(a), fabsf(b));
-        }
+            for (int e = 0; e < 8; ++e) {
+                float a, b;
+                halves(v[e], a, b);
+                m = max3(m, fabsf(a), fabsf(b));
+            }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float a, b, p, q;
-            halves(cs[e], a, b);
-            halves(sn[e], p, q);
-            n = max3(n, fabsf(a) + fabsf(p), fabsf(b) + fabsf(q));
-        }
-        delta = 0x1p-20f * head_max(m * n);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[e];
-    }
-    Quant q;
-    const int sure0 = quant32(y, delta, q.codes[0], q.par[0]), sure1 = quant32(y + 4, delta, q.codes[1], q.par[1]);
-    if (__any_sync(0xffffffffu, (sure0 & sure1 & SURE) != SURE)) {
-        if (norm || __any_sync(0xffffffffu, !(sure0 & sure1 & SURE_SCALE))) {
-            const size_t at = (size_t)pos * (HD / 2) + l * 8;
-            quant48(row, norm ? gk + l * 8 : nullptr, cos_t + at, sin_t + at, eps, q);
+            for (int e = 0; e < 4; ++e) {
+                float a, b, p, q;
+                halves(cs[e], a, b);
+                halves(sn[e], p, q);
+                n = max3(n, fabsf(a) + fabsf(p), fabsf(b) + fabsf(q));
+            }
+            delta = 0x1p-20f * head_max(m * n);
         } else {
-            if (__any_sync(0xffffffffu, !(sure0 & SURE_CODES))) exact_codes(row, q.codes[0], q.par[0]);
-            if (__any_sync(0xffffffffu, !(sure1 & SURE_CODES))) exact_codes(row + HD / 2, q.codes[1], q.par[1]);
-        }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = x[e];
     }
-    // a group with a value that is not finite is held as NaN
-    if (!(sure0 & FINITE)) { q.codes[0] = 0u; q.par[0] = 0xC3007FC0u; }
-    if (!(sure1 & FINITE)) { q.codes[1] = 0u; q.par[1] = 0xC3007FC0u; }
-    uint8_t* const tile = c.pool + (size_t)phys * BLOCK + (size_t)(head - NQ) * TILE;  // k heads 0..7, then v heads
-    const int tok = pos % KVB;
-    *reinterpret_cast<uint2*>(tile + tok * (HD / 2) + l * 8) = make_uint2(q.codes[0], q.codes[1]);
-    if (l == 0) *reinterpret_cast<uint2*>(tile + PAR + tok * 8) = make_uint2(q.par[0], q.par[1]);
+        Quant q;
+        const int sure0 = quant32(y, delta, q.codes[0], q.par[0]), sure1 = quant32(y + 4, delta, q.codes[1], q.par[1]);
+        if (__any_sync(0xffffffffu, (sure0 & sure1 & SURE) != SURE)) {
+            if (norm || __any_sync(0xffffffffu, !(sure0 & sure1 & SURE_SCALE))) {
+                const size_t at = (size_t)pos * (HD / 2) + l * 8;
+                quant48(row, norm ? gk + l * 8 : nullptr, cos_t + at, sin_t + at, eps, q);
+            } else {
+                if (__any_sync(0xffffffffu, !(sure0 & SURE_CODES))) exact_codes(row, q.codes[0], q.par[0]);
+                if (__any_sync(0xffffffffu, !(sure1 & SURE_CODES))) exact_codes(row + HD / 2, q.codes[1], q.par[1]);
+            }
+    }
+        // a group with a value that is not finite is held as NaN
+        if (!(sure0 & FINITE)) { q.codes[0] = 0u; q.par[0] = 0xC3007FC0u; }
+        if (!(sure1 & FINITE)) { q.codes[1] = 0u; q.par[1] = 0xC3007FC0u; }
+        uint8_t* const tile = c.pool + (size_t)phys * BLOCK + (size_t)(head - NQ) * TILE;  // k heads 0..7, then v heads
+        const int tok = pos % KVB;
+        *reinterpret_cast<uint2*>(tile + tok * (HD / 2) + l * 8) = make_uint2(q.codes[0], q.codes[1]);
+        if (l == 0) *reinterpret_cast<uint2*>(tile + PAR + tok * 8) = make_uint2(q.par[0], q.par[1]);
+    }
 }
 
 // ---------------------------------------------------------------- read
@@ -1090,7 +1123,7 @@ void append(int T, const void* qkv, int64_t stride, const void* gq, const void* 
             const float* sin_t, int n_pos, const int32_t* seqs, const int32_t* positions, const tts_bb_kv4* c, void* q_out,
             cudaStream_t st) {
     const auto go = [&](auto k, int parts) {
-        launch_pdl(k, dim3(T, parts), 128, 0, st, static_cast<const TI*>(qkv), (long long)stride, static_cast<const bf16*>(gq),
+        launch_pdl(k, dim3(std::min(T, 8 * 152), parts), 128, 0, st, T, static_cast<const TI*>(qkv), (long long)stride, static_cast<const bf16*>(gq),
                    static_cast<const bf16*>(gk), eps, cos_t, sin_t, n_pos, seqs, positions, cache_of(c), static_cast<TQ*>(q_out));
     };
     if (T < SPLIT_TOKENS) {

@@ -520,9 +520,8 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_long(const T* __restrict__
 template <typename T>
 void launch_block(const T* logits, const Args& a, int n, int slice, cudaStream_t st) {
     const size_t smem = (size_t)slice * sizeof(T) + 16;
-    // every call: the attribute is the current device's
-    if (smem > SLICE_BYTES - 16384)
-        cudaFuncSetAttribute(k_logprobs_block<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SLICE_BYTES + 16);
+    static SmemState state;
+    if (smem + sizeof(Block) > 48 * 1024) allow_smem(state, k_logprobs_block<T>, MAX_SLICE_BYTES + 16);
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;

@@ -191,7 +191,7 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
 __device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) { unpack8(*reinterpret_cast<const uint4*>(p), v); }
 
 template <typename T> constexpr int COLS = sizeof(T) == 4 ? 2 : 1;  // fp16 parts, columns, of a row of x
-constexpr int RED_ROW = 17, STAGES = 4;
+constexpr int RED_ROW = 17, STAGES = 3;
 // tiles of 8 columns that a kernel is built for
 constexpr int tiles_for(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 32 ? 4 : 8; }
 constexpr size_t staged_bytes(int cols, int K, int G) {
@@ -200,11 +200,11 @@ constexpr size_t staged_bytes(int cols, int K, int G) {
 
 // grid (blocks, chunks of x rows), WARPS * 32 threads. A block stages its rows of x once and walks the 16-row tiles of W
 // with the stride of the grid; a tile's groups are dealt to the warps, whose records come by cp.async through a ring of each
-// warp's own, three on their way while one is multiplied.
+// warp's own, two on their way while one is multiplied.
 // Shared memory: x as B registers, 16 bytes (two steps) a lane and piece: [group][G / 32 pieces][columns][4 lanes]; the warps'
 // sums of a tile, twice: one barrier a tile; the rings. Sums are added in the warps' order.
 template <typename T, int G, int NT>
-__global__ void __launch_bounds__(WARPS * 32, 2) k_w4_staged(int T_, int N, int K, const T* __restrict__ x, long long stride,
+__global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2) k_w4_staged(int T_, int N, int K, const T* __restrict__ x, long long stride,
                                                              const uint8_t* __restrict__ packed, T* __restrict__ y, int per) {
     constexpr int P = COLS<T>, WORDS = G / 16, PIECES = G / 32, C8 = NT * 8;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -219,19 +219,24 @@ __global__ void __launch_bounds__(WARPS * 32, 2) k_w4_staged(int T_, int N, int 
     constexpr int REC = record_bytes(G);
     uint8_t* const ring = reinterpret_cast<uint8_t*>(red + 2 * WARPS * C8 * RED_ROW) + warp * STAGES * REC;
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-    int ahead_tile = warp < groups ? blockIdx.x : tiles, ahead_g = warp, slot = 0;  // what comes next, and into which place
+    // what comes next: its address, the records of the tile from it on, the tile; and its place in the ring
+    const int each = (groups - warp + WARPS - 1) / WARPS;  // records of a tile that are this warp's
+    int ahead_tile = each > 0 ? blockIdx.x : tiles, left = each;
+    const uint8_t* src = packed + ((size_t)blockIdx.x * groups + warp) * REC + lane * 16;
+    const long long jump = ((long long)gridDim.x * groups - (long long)each * WARPS) * REC;
+    uint32_t dst = ring_at + lane * 16;
+    const uint32_t dst_end = ring_at + STAGES * REC;
     const auto fetch = [&] {
         if (ahead_tile < tiles) {
-            const uint8_t* src = packed + ((size_t)ahead_tile * groups + ahead_g) * REC + lane * 16;
-            const uint32_t dst = ring_at + slot * REC + lane * 16;
 #pragma unroll
             for (int i = 0; i < REC; i += 512)
                 if (i + 512 <= REC || lane * 16 < REC - i)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i), "l"(src + i) : "memory");
-            ahead_g += WARPS;
-            if (ahead_g >= groups) { ahead_g = warp; ahead_tile += gridDim.x; }
+            src += WARPS * REC;
+            if (--left == 0) { left = each; ahead_tile += gridDim.x; src += jump; }
         }
-        slot = slot + 1 == STAGES ? 0 : slot + 1;
+        dst += REC;
+        if (dst >= dst_end) dst -= STAGES * REC;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
@@ -285,15 +290,14 @@ __global__ void __launch_bounds__(WARPS * 32, 2) k_w4_staged(int T_, int N, int 
     int at[NT];  // this lane's column of each tile of 8; behind the last one, that one again: nobody reads its sums
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) at[nt] = min(nt * 8 + r, cols - 1) * 4 + q;
-    int use = 0;  // the place of the record at hand
+    const uint8_t* rec = ring;  // the record at hand
     for (int tile = blockIdx.x, turn = 0; tile < tiles; tile += gridDim.x, turn ^= 1) {
         float acc[NT][4] = {};
-        for (int g = warp; g < groups; g += WARPS) {
+        const uint4* xg = xs + (size_t)warp * PIECES * cols * 4;
+        for (int g = 0; g < each; ++g, xg += (size_t)WARPS * PIECES * cols * 4) {
             asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
             __syncwarp();
             fetch();  // into the place of the record before
-            const uint8_t* const rec = ring + use * REC;
-            use = use + 1 == STAGES ? 0 : use + 1;
             uint32_t cw[WORDS];
             if constexpr (WORDS == 2) {
                 const uint2 v = *reinterpret_cast<const uint2*>(rec + lane * 8);
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) k_w4_staged(int T_, int N, int 
                 float d[4] = {};
 #pragma unroll
                 for (int i = 0; i < PIECES; ++i) {
-                    const uint4 b = xs[(g * PIECES + i) * cols * 4 + at[nt]];
+                    const uint4 b = xg[i * cols * 4 + at[nt]];
                     mma_f16(d, a[2 * i], b.x, b.y);
                     mma_f16(d, a[2 * i + 1], b.z, b.w);
                 }
@@ -332,6 +336,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) k_w4_staged(int T_, int N, int 
                 acc[nt][2] += s1 * d[2];
                 acc[nt][3] += s1 * d[3];
             }
+            rec = rec + REC == ring + STAGES * REC ? ring : rec + REC;
         }
         float* const mine = red + (size_t)(turn * WARPS + warp) * C8 * RED_ROW;
 #pragma unroll
@@ -354,7 +359,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) k_w4_staged(int T_, int N, int 
 }
 
 // x in shared memory where 8 columns of it, or all, leave room for two blocks an SM; in chunks of as many rows as do.
-constexpr size_t STAGED_MOST = 112 * 1024, STAGED_ONE = 220 * 1024;
+constexpr size_t STAGED_MOST = 112 * 1024, STAGED_ONE = 220 * 1024, STAGED_THREE = 74 * 1024;
 
 template <typename T, int G>
 void launch(int T_, int N, int K, const void* x, int64_t stride, const void* packed, void* y, cudaStream_t st) {
@@ -369,16 +374,17 @@ void launch(int T_, int N, int K, const void* x, int64_t stride, const void* pac
         const size_t smem = staged_bytes(per * P, K, G);
         if (smem <= STAGED_ONE) {
             const int nt = tiles_for(per * P), chunks = (T_ + per - 1) / per;
-            const int blocks = std::min(tiles, std::max(1, 152 * (smem <= STAGED_MOST ? 2 : 1) / chunks));
-            auto go = [&](auto k) {
-                // every call: the attribute is the current device's
-                if (smem > 48 * 1024 - 1024) cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)STAGED_ONE);
+            const int fit = smem > STAGED_MOST ? 1 : nt <= 2 && smem <= STAGED_THREE ? 3 : 2;  // blocks an SM
+            const int blocks = std::min(tiles, std::max(1, 152 * fit / chunks));
+            auto go = [&](auto k, SmemState& s) {
+                if (smem > 48 * 1024 - 512) allow_smem(s, k, STAGED_ONE);
                 launch_pdl(k, dim3(blocks, chunks), WARPS * 32, smem, st, T_, N, K, xt, (long long)stride, w, yt, per);
             };
-            if (nt == 1) go(k_w4_staged<T, G, 1>);
-            else if (nt == 2) go(k_w4_staged<T, G, 2>);
-            else if (nt == 4) go(k_w4_staged<T, G, 4>);
-            else go(k_w4_staged<T, G, 8>);
+            static SmemState state[4];
+            if (nt == 1) go(k_w4_staged<T, G, 1>, state[0]);
+            else if (nt == 2) go(k_w4_staged<T, G, 2>, state[1]);
+            else if (nt == 4) go(k_w4_staged<T, G, 4>, state[2]);
+            else go(k_w4_staged<T, G, 8>, state[3]);
             return;
         }
     }
