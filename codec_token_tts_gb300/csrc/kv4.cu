@@ -215,79 +215,97 @@ __device__ __forceinline__ float rint2(float k, Two x, float s) {
 }
 __device__ __forceinline__ float rint2(Two x, float s) { return rint2(rintf(__fdiv_rn(x.h, s)), x, s); }
 
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The inverse root mean square of a head's row (x: at this lane's first dim), in 48 bits
+template <typename T>
+__device__ __forceinline__ Two inverse_norm(const T* x, float eps) {
+    Two part[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const Two a = {to_float(x[e]), 0.f}, b = {to_float(x[HD / 2 + e]), 0.f}, c = {to_float(x[4 + e]), 0.f}, d = {to_float(x[HD / 2 + 4 + e]), 0.f};
+        part[e] = add2(add2(mul2(a, a), mul2(b, b)), add2(mul2(c, c), mul2(d, d)));
+    }
+    Two ss = add2(add2(part[0], part[1]), add2(part[2], part[3]));
+#pragma unroll
+    for (int o = 4; o; o >>= 1) ss = add2(ss, peer2(ss, o));
+    ss = add2({ss.h * (1.f / HD), ss.l * (1.f / HD)}, {eps, 0.f});
+    // one Newton step doubles the 23 bits of rsqrtf: r (1 + (1 - ss r r) / 2)
+    const Two r = {rsqrtf(ss.h), 0.f};
+    const Two err = add2({1.f, 0.f}, neg2(mul2(ss, mul2(r, r))));
+    return norm2(r.h, r.h * 0.5f * err.h);
+}
+// dims e and 64 + e of this lane's of a key: normalised, with its gain, rotated
+template <typename T>
+__device__ __forceinline__ void key_values(const T* x, const bf16* gain, const float* cs, const float* sn, Two r, int e, Two (&z)[2]) {
+    const Two a = mul2(mul2({to_float(x[e]), 0.f}, r), {bf2f(gain[e]), 0.f});
+    const Two b = mul2(mul2({to_float(x[HD / 2 + e]), 0.f}, r), {bf2f(gain[HD / 2 + e]), 0.f});
+    const Two c = {cs[e], 0.f}, s = {sn[e], 0.f};
+    z[0] = add2(mul2(a, c), neg2(mul2(b, s)));
+    z[1] = add2(mul2(b, c), mul2(a, s));
+}
+
 // The definition, in 48 bits: of the head's row x (normalised with its gain and rotated here where gain is given), lane l's dims;
-// all pointers at this lane's first dim. Seldom needed and long, so it is kept small: value by value, read again from
-// memory, and computed twice, for the range and for the codes.
+// all pointers at this lane's first dim. Seldom needed, so its code is kept short (what a launch runs once comes from
+// memory): value by value, in one loop that goes over them twice, for the ranges and for the codes.
 template <typename T>
 __device__ __forceinline__ void quant48(const T* x, const bf16* gain, const float* cs, const float* sn, float eps, Quant& q) {
-    const auto at = [&](int e) { return Two{to_float(x[e]), 0.f}; };
     Two r = {1.f, 0.f};
-    if (gain) {
-        Two ss = {0.f, 0.f};
-#pragma unroll 1
-        for (int e = 0; e < 8; ++e) ss = add2(ss, add2(mul2(at(e), at(e)), mul2(at(HD / 2 + e), at(HD / 2 + e))));
-#pragma unroll
-        for (int o = 4; o; o >>= 1) ss = add2(ss, peer2(ss, o));
-        ss = add2({ss.h * (1.f / HD), ss.l * (1.f / HD)}, {eps, 0.f});
-        // one Newton step doubles the 23 bits of rsqrtf: r (1 + (1 - ss r r) / 2)
-        r.h = rsqrtf(ss.h);
-        const Two err = add2({1.f, 0.f}, neg2(mul2(ss, mul2(r, r))));
-        r = norm2(r.h, r.h * 0.5f * err.h);
-    }
-    const auto values = [&](int e, Two (&z)[2]) {
-        z[0] = at(e);
-        z[1] = at(HD / 2 + e);
-        if (gain) {
-            const Two a = mul2(mul2(z[0], r), {bf2f(gain[e]), 0.f}), b = mul2(mul2(z[1], r), {bf2f(gain[HD / 2 + e]), 0.f});
-            const Two c = {cs[e], 0.f}, s = {sn[e], 0.f};
-            z[0] = add2(mul2(a, c), neg2(mul2(b, s)));
-            z[1] = add2(mul2(b, c), mul2(a, s));
-        }
-    };
-    Two lo[2], hi[2], z[2];
-    values(0, lo);
-    values(0, hi);
-#pragma unroll 1
-    for (int e = 1; e < 8; ++e) {
-        values(e, z);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            lo[g] = less2(z[g], lo[g]) ? z[g] : lo[g];
-            hi[g] = less2(hi[g], z[g]) ? z[g] : hi[g];
-        }
-    }
-    float s[2], zero[2];
+    if (gain) r = inverse_norm(x, eps);
+    Two lo[2], hi[2];
+    float s[2] = {1.f, 1.f}, zero[2] = {0.f, 0.f};
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-#pragma unroll
-        for (int o = 4; o; o >>= 1) {
-            const Two a = peer2(lo[g], o), b = peer2(hi[g], o);
-            lo[g] = less2(a, lo[g]) ? a : lo[g];
-            hi[g] = less2(hi[g], b) ? b : hi[g];
-        }
-        const Two range = div2(add2(hi[g], neg2(lo[g])), 15.f), most = div2(less2(hi[g], neg2(lo[g])) ? neg2(lo[g]) : hi[g], 120.f);
-        const uint32_t sb = bf_bits(less2(range, most) ? most.h : range.h);
-        s[g] = __uint_as_float(sb << 16);
-        zero[g] = s[g] > 0.f ? rint2(lo[g], s[g]) : 0.f;
+        lo[g] = {INFINITY, 0.f};
+        hi[g] = {-INFINITY, 0.f};
         q.codes[g] = 0u;
-        q.par[g] = sb | bf_bits(zero[g] - 128.f) << 16;
     }
 #pragma unroll 1
-    for (int e = 0; e < 8; ++e) {
-        values(e, z);
+    for (int i = 0; i < 16; ++i) {
+        const int e = i & 7;
+        Two z[2] = {{to_float(x[e]), 0.f}, {to_float(x[HD / 2 + e]), 0.f}};
+        if (gain) key_values(x, gain, cs, sn, r, e, z);
+        if (i < 8) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
-            if (s[g] > 0.f) q.codes[g] |= (uint32_t)fminf(rint2(z[g], s[g]) - zero[g], 15.f) << (4 * e);
+            for (int g = 0; g < 2; ++g) {
+                lo[g] = less2(z[g], lo[g]) ? z[g] : lo[g];
+                hi[g] = less2(hi[g], z[g]) ? z[g] : hi[g];
+            }
+            if (i < 7) continue;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                for (int o = 4; o; o >>= 1) {
+                    const Two a = peer2(lo[g], o), b = peer2(hi[g], o);
+                    lo[g] = less2(a, lo[g]) ? a : lo[g];
+                    hi[g] = less2(hi[g], b) ? b : hi[g];
+                }
+                const Two range = div2(add2(hi[g], neg2(lo[g])), 15.f), most = div2(less2(hi[g], neg2(lo[g])) ? neg2(lo[g]) : hi[g], 120.f);
+                const uint32_t sb = bf_bits(less2(range, most) ? most.h : range.h);
+                s[g] = __uint_as_float(sb << 16);
+                zero[g] = s[g] > 0.f ? rint2(lo[g], s[g]) : 0.f;
+                q.par[g] = sb | bf_bits(zero[g] - 128.f) << 16;
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+                if (s[g] > 0.f) q.codes[g] |= (uint32_t)fminf(rint2(z[g], s[g]) - zero[g], 15.f) << (4 * e);
+        }
     }
 }
 
-// The same for one group (the pairs x of a lane) in 32 bits, where x is known to within delta. SURE_SCALE: the scale's rounding
-// could not fall the other way (nor is the group too small for this arithmetic); SURE_CODES: no code's could; FINITE: all
-// values are. x / scale is rounded by adding and subtracting 1.5 2^23; the lowest value is one of the x, so its code is 0
-// and no code is below.
-enum { SURE_SCALE = 1, SURE_CODES = 2, SURE = 3, FINITE = 4 };
+// The same for one group (the pairs x of a lane) in 32 bits. Keys are known to within delta; values are exact (EXACT), and
+// x / scale is then divided out in full: a value halfway between two codes, which bf16 rows meet often, goes to the even whole
+// number. SURE_SCALE: the scale's rounding could not fall the other way (nor is the group too small for this arithmetic);
+// FINITE: all values are; unsure: a bit for each value whose code could be another. Rounding is by adding and subtracting
+// 1.5 2^23; the lowest value is one of the x, so its code is 0 and no code is below.
+enum { SURE_SCALE = 1, FINITE = 2 };
 constexpr float MAGIC = 12582912.f;
-__device__ __forceinline__ int quant32(const f2* x, float delta, uint32_t& codes, uint32_t& par) {
+template <bool EXACT>
+__device__ __forceinline__ int quant32(const f2* x, float delta, uint32_t& codes, uint32_t& par, uint32_t& unsure) {
     float v[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) halves(x[e], v[2 * e], v[2 * e + 1]);
@@ -297,20 +315,27 @@ __device__ __forceinline__ int quant32(const f2* x, float delta, uint32_t& codes
     const float s0 = fmaxf((hi - lo) * (1.f / 15.f), amax * (1.f / 120.f));
     const float es = 0.15f * delta + s0 * 0x1p-22f;  // three roundings, and x's
     const uint32_t sb = bf_bits(s0 - es);
-    const float inv = __frcp_rn(__uint_as_float(sb << 16));
-    const float rel = 0x1p-22f * amax * inv + delta * inv;  // bound of the error of x / s: two roundings, and x's
-    const float zero = (lo * inv + MAGIC) - MAGIC;
-    const f2 inv2 = both(inv), magic = both(MAGIC), unmagic = both(-MAGIC), minus = both(-1.f), unzero = both(-zero);
+    const float s = __uint_as_float(sb << 16), inv = rcp(s);
+    // bound of the error of x / s: EXACT: one rounding; else two and the reciprocal's, and x's
+    const float rel = EXACT ? 0x1p-23f * amax * inv : 0x1p-22f * amax * inv + delta * inv;
+    float t0 = lo * inv;
+    if (EXACT) t0 = fmaf(fmaf(-t0, s, lo), inv, t0);
+    const float zero = (t0 + MAGIC) - MAGIC;
+    const f2 inv2 = both(inv), magic = both(MAGIC), unmagic = both(-MAGIC), minus = both(-1.f), unzero = both(-zero), ms = both(-s);
     float c[8], d[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const f2 t = mulp(x[e], inv2), k = addp(addp(t, magic), unmagic);
+        f2 t = mulp(x[e], inv2);
+        if (EXACT) t = fmap(fmap(t, ms, x[e]), inv2, t);
+        const f2 k = addp(addp(t, magic), unmagic);
         halves(fmap(k, minus, t), d[2 * e], d[2 * e + 1]);
         halves(addp(k, unzero), c[2 * e], c[2 * e + 1]);
     }
-    float far = 0.f;  // the furthest from a whole number
+    unsure = 0u;
+    const float far = max3(max3(max3(fabsf(d[0]), fabsf(d[1]), fabsf(d[2])), fabsf(d[3]), fabsf(d[4])), max3(fabsf(d[5]), fabsf(d[6]), fabsf(d[7])), 0.f);
+    if (far >= 0.5f - rel)  // from a whole number
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) far = max3(far, fabsf(d[e]), fabsf(d[e + 1]));
+        for (int e = 0; e < 8; ++e) unsure |= fabsf(d[e]) >= 0.5f - rel ? 1u << e : 0u;
     uint32_t h[2];
 #pragma unroll
     for (int e = 0; e < 8; ++e) c[e] = fminf(c[e], 15.f);
@@ -319,25 +344,31 @@ __device__ __forceinline__ int quant32(const f2* x, float delta, uint32_t& codes
         h[i] = __float_as_uint(fmaf(fmaf(c[4 * i + 3], 16.f, c[4 * i + 2]), 256.f, fmaf(c[4 * i + 1], 16.f, c[4 * i])) + 8388608.f);
     codes = __byte_perm(h[0], h[1], 0x5410);
     par = sb | bf_bits(zero - 128.f) << 16;
-    return (sb == bf_bits(s0 + es) && s0 > 1e-30f ? SURE_SCALE : 0) | (far < 0.5f - rel ? SURE_CODES : 0) | (amax < INFINITY ? FINITE : 0);
+    return (sb == bf_bits(s0 + es) && s0 > 1e-30f ? SURE_SCALE : 0) | (amax < INFINITY ? FINITE : 0);
 }
-// The codes of exact values x for the scale that quant32 found: a value halfway between two codes, which bf16 rows meet
-// often (in two of five sets of four v heads), goes to the even whole number.
+// The unsure codes of keys whose scale is sure, decided in 48 bits: the warp goes through the places that any lane asks for.
+// False where one of them is a group's lowest value (code 0), whose rounding moves the zero point.
 template <typename T>
-__device__ __forceinline__ void exact_codes(const T* x, uint32_t& codes, uint32_t& par) {
-    const float s = __uint_as_float(par << 16), inv = __frcp_rn(s);
-    float first = 1e30f, k[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float v = to_float(x[e]);
-        k[e] = rint2((v * inv + MAGIC) - MAGIC, {v, 0.f}, s);
-        first = fminf(first, k[e]);  // of the lowest value
+__device__ __forceinline__ bool settle(const T* x, const bf16* gain, const float* cs, const float* sn, float eps, uint32_t unsure, Quant& q) {
+    const Two r = inverse_norm(x, eps);
+    uint32_t all = __reduce_or_sync(0xffffffffu, unsure);
+    bool fine = true;
+    while (all) {
+        const int e = __ffs(all) - 1, g = e >> 3, d = e & 7;
+        all &= all - 1;
+        Two z[2];
+        key_values(x, gain, cs, sn, r, d, z);
+        const uint32_t par = g ? q.par[1] : q.par[0];
+        const float s = __uint_as_float(par << 16), zero = __uint_as_float(par & 0xFFFF0000u) + 128.f;
+        const float k = rint2(g ? z[1] : z[0], s) - zero;
+        if (unsure >> e & 1u) {
+            fine = fine && k > 0.f && ((g ? q.codes[1] : q.codes[0]) >> (4 * d) & 15u) != 0u;
+            const uint32_t put = (uint32_t)fminf(fmaxf(k, 0.f), 15.f) << (4 * d), keep = ~(15u << (4 * d));
+            if (g) q.codes[1] = (q.codes[1] & keep) | put;
+            else q.codes[0] = (q.codes[0] & keep) | put;
+        }
     }
-    const float zero = head_min(first);
-    codes = 0u;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) codes |= (uint32_t)fminf(k[e] - zero, 15.f) << (4 * e);
-    par = (par & 0xFFFFu) | bf_bits(zero - 128.f) << 16;
+    return fine;
 }
 
 // grid (tokens at most, parts), 128 threads: a token's 16 q heads, or its 8 k and 8 v heads, four a warp; a block goes on with
@@ -346,14 +377,14 @@ __device__ __forceinline__ void exact_codes(const T* x, uint32_t& codes, uint32_
 // Bound by memory (8 or 16 KB read, 4 or 8 KB + 1152 B written for a token) and, nearly as much, by its instructions.
 //
 // A code next to a border between two would fall either way on the rounding of a 32-bit norm, and one
-// code off is a whole scale. Where quant32 is not sure (about 3 % of the fours of k heads) the four are done again in 48
-// bits, so that the codes are those of the definition.
-// delta bounds the 32-bit error of a rotated key: relative to |x_i cos| + |x_j sin|, 2^-24 times 7 (half of the sum of
-// squares' 13 roundings, and the mean's) + 4 (rsqrtf, 2 units) + 2 (norm and gain) + 2 (rotation) is below 16 * 2^-24.
+// code off is a whole scale. Where quant32 is not sure (about 3 % of the fours of k heads) those codes, or the four heads where it is the scale,
+// are done again in 48 bits, so that all are those of the definition.
+// delta bounds the 32-bit error of a rotated key: relative to |x_i cos| + |x_j sin|, 2^-24 times 5 (half of the sum of
+// squares' 8 roundings, and the mean's two) + 2 (Newton's step) + 2 (norm and gain) + 2 (rotation) is below 12 * 2^-24.
 // WHAT: HEADS_Q, HEADS_KV, or both
 enum { HEADS_Q = 1, HEADS_KV = 2 };
 template <int WHAT, typename TI, typename TQ>
-__global__ void __launch_bounds__(128, 8) k_kv4_append(int T, const TI* __restrict__ qkv, long long stride,
+__global__ void __launch_bounds__(128, 6) k_kv4_append(int T, const TI* __restrict__ qkv, long long stride,
                                                     const bf16* __restrict__ gq, const bf16* __restrict__ gk, float eps,
                                                     const float* __restrict__ cos_t, const float* __restrict__ sin_t,
                                                     int n_pos, const int32_t* __restrict__ seqs,
@@ -362,21 +393,30 @@ __global__ void __launch_bounds__(128, 8) k_kv4_append(int T, const TI* __restri
     pdl_trigger();
     const int warp = (WHAT == HEADS_KV ? 4 : blockIdx.y * 4) + (threadIdx.x >> 5), lane = threadIdx.x & 31, l = lane & 7;
     const int head = warp * 4 + (lane >> 3);
-    int t = blockIdx.x, next_seq = seqs[t], next_pos = positions[t];
-    Raw8<TI> next0 = raw8(qkv + (size_t)t * stride + head * HD + l * 8), next1 = raw8(qkv + (size_t)t * stride + head * HD + HD / 2 + l * 8);
+    // a token's row is fetched while the one before is at hand, its place one token earlier (rows of padding stay unread)
+    int t = blockIdx.x, next_seq = seqs[t], next_pos = positions[t], far_seq = -1, far_pos = 0;
+    Raw8<TI> next0 = {}, next1 = {};
+    if (t + (int)gridDim.x < T) { far_seq = seqs[t + gridDim.x]; far_pos = positions[t + gridDim.x]; }
+    {
+        const TI* const first = qkv + (size_t)t * stride + head * HD + l * 8;
+        next0 = raw8(first);
+        next1 = raw8(first + HD / 2);
+    }
     for (; t < T; t += gridDim.x) {
         const TI* const row = qkv + (size_t)t * stride + head * HD + l * 8;
         const int seq = next_seq, pos = next_pos;
         f2 x[8];  // pairs of dims of group 0, then of group 1
         pairs_of(next0, x);
         pairs_of(next1, x + 4);
-        if (t + (int)gridDim.x < T) {
+        next_seq = far_seq;
+        next_pos = far_pos;
+        far_seq = -1;
+        if (next_seq >= 0) {
             const TI* const ahead = row + (size_t)gridDim.x * stride;
-            next_seq = seqs[t + gridDim.x];
-            next_pos = positions[t + gridDim.x];
             next0 = raw8(ahead);
             next1 = raw8(ahead + HD / 2);
-    }
+        }
+        if (t + 2ll * gridDim.x < T) { far_seq = seqs[t + 2 * gridDim.x]; far_pos = positions[t + 2 * gridDim.x]; }
         if (seq < 0) continue;
         if (pos >= n_pos) {
             if (threadIdx.x == 0) set_err(c.err, TTS_BB_KV4_ERR_RANGE);
@@ -394,12 +434,14 @@ __global__ void __launch_bounds__(128, 8) k_kv4_append(int T, const TI* __restri
             load8(gain + HD / 2, g + 4);
             load8(cos_t + (size_t)pos * (HD / 2) + l * 8, cs);
             load8(sin_t + (size_t)pos * (HD / 2) + l * 8, sn);
-            f2 ss = mulp(x[0], x[0]);
+            f2 ss[4];
 #pragma unroll
-            for (int e = 1; e < 8; ++e) ss = fmap(x[e], x[e], ss);
+            for (int e = 0; e < 4; ++e) ss[e] = fmap(x[e], x[e], mulp(x[4 + e], x[4 + e]));
             float s0, s1;
-            halves(ss, s0, s1);
-            const f2 r = both(rsqrtf(head_sum(s0 + s1) * (1.f / HD) + eps)), minus = both(-1.f);
+            halves(addp(addp(ss[0], ss[1]), addp(ss[2], ss[3])), s0, s1);
+            const float ms = head_sum(s0 + s1) * (1.f / HD) + eps, r0 = rsqrtf(ms);
+            // a step of Newton's takes rsqrtf's last bits
+            const f2 r = both(fmaf(r0 * 0.5f, fmaf(-ms * r0, r0, 1.f), r0)), minus = both(-1.f);
             f2 v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = mulp(mulp(x[e], r), g[e]);
@@ -430,22 +472,29 @@ __global__ void __launch_bounds__(128, 8) k_kv4_append(int T, const TI* __restri
                 halves(sn[e], p, q);
                 n = max3(n, fabsf(a) + fabsf(p), fabsf(b) + fabsf(q));
             }
-            delta = 0x1p-20f * head_max(m * n);
+            delta = 0x1.8p-21f * head_max(m * n);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = x[e];
     }
         Quant q;
-        const int sure0 = quant32(y, delta, q.codes[0], q.par[0]), sure1 = quant32(y + 4, delta, q.codes[1], q.par[1]);
-        if (__any_sync(0xffffffffu, (sure0 & sure1 & SURE) != SURE)) {
-            if (norm || __any_sync(0xffffffffu, !(sure0 & sure1 & SURE_SCALE))) {
-                const size_t at = (size_t)pos * (HD / 2) + l * 8;
-                quant48(row, norm ? gk + l * 8 : nullptr, cos_t + at, sin_t + at, eps, q);
-            } else {
-                if (__any_sync(0xffffffffu, !(sure0 & SURE_CODES))) exact_codes(row, q.codes[0], q.par[0]);
-                if (__any_sync(0xffffffffu, !(sure1 & SURE_CODES))) exact_codes(row + HD / 2, q.codes[1], q.par[1]);
-            }
-    }
+        uint32_t un0, un1;
+        int sure0, sure1;
+        bool again;  // in 48 bits
+        const size_t at = (size_t)pos * (HD / 2) + l * 8;
+        if (norm) {
+            sure0 = quant32<false>(y, delta, q.codes[0], q.par[0], un0);
+            sure1 = quant32<false>(y + 4, delta, q.codes[1], q.par[1], un1);
+            again = __any_sync(0xffffffffu, !(sure0 & sure1 & SURE_SCALE));
+            if (!again && __any_sync(0xffffffffu, un0 | un1))
+                again = __any_sync(0xffffffffu, !settle(row, gk + l * 8, cos_t + at, sin_t + at, eps, un0 | un1 << 8, q));
+        } else {
+            sure0 = quant32<true>(y, 0.f, q.codes[0], q.par[0], un0);
+            sure1 = quant32<true>(y + 4, 0.f, q.codes[1], q.par[1], un1);
+            // quotients of two bf16 numbers that are not halfway stay further from it than their rounding
+            again = __any_sync(0xffffffffu, !(sure0 & sure1 & SURE_SCALE) || (sizeof(TI) == 4 && (un0 | un1)));
+        }
+        if (again) quant48(row, norm ? gk + l * 8 : nullptr, cos_t + at, sin_t + at, eps, q);
         // a group with a value that is not finite is held as NaN
         if (!(sure0 & FINITE)) { q.codes[0] = 0u; q.par[0] = 0xC3007FC0u; }
         if (!(sure1 & FINITE)) { q.codes[1] = 0u; q.par[1] = 0xC3007FC0u; }
@@ -457,6 +506,16 @@ __global__ void __launch_bounds__(128, 8) k_kv4_append(int T, const TI* __restri
 }
 
 // ---------------------------------------------------------------- read
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
 // grid ceil(T / N), 256 threads: thread (K or V, head, word) unpacks one word (8 dims) of each of N tokens, whose addresses
 // and words are all on their way before the first is unpacked.
 template <int N>
@@ -487,16 +546,13 @@ __global__ void __launch_bounds__(256) k_kv4_read(int T, const int32_t* __restri
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         if (phys[i] < 0) continue;
-        // 2^23 + code, less 2^23 and plus the zero point: exact
-        const float s = __uint_as_float(par[i] << 16), z = __uint_as_float(par[i] & 0xFFFF0000u) + (128.f - 8388608.f);
-        uint32_t o[4];
+        // pairs of dims (d, d + 4): 128 + code, the offset added (exact), times the scale (rounded once); then side by side
+        const uint32_t s = __byte_perm(par[i], 0u, 0x1010), off = __byte_perm(par[i], 0u, 0x3232);
+        uint32_t v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float a = __uint_as_float((word[i] >> (8 * e) & 15u) | 0x4B000000u) + z;
-            const float b = __uint_as_float((word[i] >> (8 * e + 4) & 15u) | 0x4B000000u) + z;
-            const __nv_bfloat162 v = __floats2bfloat162_rn(s * a, s * b);
-            o[e] = *reinterpret_cast<const uint32_t*>(&v);
-        }
+        for (int e = 0; e < 4; ++e) v[e] = mul_bf16x2(add_bf16x2((word[i] >> (4 * e) & 0x000F000Fu) | 0x43004300u, off), s);
+        const uint32_t o[4] = {__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632),
+                               __byte_perm(v[2], v[3], 0x7632)};
         bf16* out = (unit < NKV ? k_out : v_out) + ((size_t)(t0 + i) * NKV + (unit & 7)) * HD + 64 * (w & 1) + 8 * (w >> 1);
         *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
     }
@@ -1123,7 +1179,7 @@ void append(int T, const void* qkv, int64_t stride, const void* gq, const void* 
             const float* sin_t, int n_pos, const int32_t* seqs, const int32_t* positions, const tts_bb_kv4* c, void* q_out,
             cudaStream_t st) {
     const auto go = [&](auto k, int parts) {
-        launch_pdl(k, dim3(std::min(T, 8 * 152), parts), 128, 0, st, T, static_cast<const TI*>(qkv), (long long)stride, static_cast<const bf16*>(gq),
+        launch_pdl(k, dim3(std::min(T, 6 * 152), parts), 128, 0, st, T, static_cast<const TI*>(qkv), (long long)stride, static_cast<const bf16*>(gq),
                    static_cast<const bf16*>(gk), eps, cos_t, sin_t, n_pos, seqs, positions, cache_of(c), static_cast<TQ*>(q_out));
     };
     if (T < SPLIT_TOKENS) {
