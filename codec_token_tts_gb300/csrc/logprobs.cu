@@ -8,6 +8,7 @@
 // one: no two keys are equal, and the larger key is the larger logit or, among equals, the lower id.
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -77,18 +78,18 @@ __device__ __forceinline__ Part join(const Part& x, const Part& y) {
     }
     return o;
 }
-// the row's numbers; z: the target's logit
-__device__ __forceinline__ void finish(const Args& a, int row, const Part& p, bool wanted, float z) {
-    const float nan = __int_as_float(0x7FC00000), log_s = log1pf(p.r);
+// the row's numbers; log_s: log1p(r), z: the target's logit
+__device__ __forceinline__ void finish(const Args& a, int row, const Part& p, float log_s, bool wanted, float z) {
+    const float nan = __int_as_float(0x7FC00000);
     const bool some = p.m > NONE;
     if (a.targets && a.logprob) a.logprob[row] = p.bad ? nan : some && wanted ? (z - p.m) - log_s : NEG_INF;
     if (a.entropy) a.entropy[row] = p.bad ? nan : some ? log_s - p.t / (1.f + p.r) : 0.f;
     if (a.lse) a.lse[row] = p.bad ? nan : some ? p.m + log_s : NEG_INF;
 }
-__device__ __forceinline__ void write_top(const Args& a, int row, int j, u64 key, const Part& p) {
+__device__ __forceinline__ void write_top(const Args& a, int row, int j, u64 key, const Part& p, float log_s) {
     const float nan = __int_as_float(0x7FC00000);
     a.top_ids[(size_t)row * a.n_top + j] = key && !p.bad ? id_of(key) : -1;
-    a.top_lp[(size_t)row * a.n_top + j] = p.bad ? nan : key ? (value_of(key) - p.m) - log1pf(p.r) : NEG_INF;
+    a.top_lp[(size_t)row * a.n_top + j] = p.bad ? nan : key ? (value_of(key) - p.m) - log_s : NEG_INF;
 }
 template <typename T>
 __device__ __forceinline__ bool target_of(const Args& a, const T* z, const uint32_t* ok, int row, float& v) {
@@ -100,69 +101,181 @@ __device__ __forceinline__ bool target_of(const Args& a, const T* z, const uint3
     return true;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float m;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+// two floats an instruction
+typedef u64 f2;
+__device__ __forceinline__ f2 pair(float a, float b) {
+    f2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void halves(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 mulp(f2 a, f2 b) {
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 addp(f2 a, f2 b) {
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 fmap(f2 a, f2 b, f2 c) {
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // ---------------------------------------------------------------- one warp a row
-// Rows of up to 32 * NV logits, held in registers: lane l has ids l, l + 32, .... One pass for the maximum, one for the sums,
-// one that gathers the alternatives: ids whose logit reaches the n_top-th largest of the 32 lanes' maxima (a bound below
-// the n_top-th largest of all), usually a few more than n_top, ranked by counting. Bound by memory for many rows: 49152 x 1025
-// fp32 with a mask and 5 alternatives.
+// Rows of up to 32 * NV logits (NV even), held in registers: lane l has ids l, l + 32, .... One pass for the maximum, one for the
+// sums, one that marks the alternatives: ids whose logit reaches the n_top-th largest of the 32 lanes' maxima (a bound below
+// the n_top-th largest of all), usually a few more than n_top, ranked by counting. What bounds it are the instructions of
+// these passes (49152 x 1025 fp32 with a mask and 5 alternatives: a third of the time memory alone would leave), so a
+// pass is kept to what most rows need; and their number, since code that does not fit the instruction cache stalls: what
+// few rows need is a loop over memory. These are rows with a logit that is not within 1e30 (a NaN, an infinity, the
+// type's lowest value) and rows with more equal candidates than CAP.
 constexpr int ROW_WARPS = 4, CAP = 96;
+constexpr float OUT = -1e30f;  // stands for a masked logit
+
+__device__ __forceinline__ float row_max(float v) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+// One row by a warp, in loops over memory: any values.
+template <typename T>
+__device__ __noinline__ Part sums_of(const T* z, const uint32_t* ok, int V, int lane) {
+    Part p = {NEG_INF, 0.f, 0.f, 0};
+    bool bad = false;
+    for (int i = lane; i < V; i += 32) {
+        const float v = is_allowed(ok, i) ? to_f(z[i]) : NEG_INF;
+        bad |= !(v < INFINITY);
+        p.m = fmaxf(p.m, v);
+    }
+    p.m = warp_max(p.m);
+    p.bad = __any_sync(ALL, bad);
+    int same = 0;
+    for (int i = lane; i < V; i += 32) {
+        const float v = is_allowed(ok, i) ? to_f(z[i]) : NEG_INF, d = fmaxf(v - (p.m > NONE ? p.m : 0.f), -1e4f), e = ex2(d * LOG2E);
+        p.t += e * d;
+        if (d == 0.f) ++same;
+        else p.r += e;
+    }
+    p.r = warp_sum(p.r) + (float)(__reduce_add_sync(ALL, same) - 1);
+    p.t = warp_sum(p.t);
+    return p;
+}
+// The n largest keys of a row, one after the other.
+template <typename T>
+__device__ __noinline__ void tops_of(const T* z, const uint32_t* ok, const Args& a, int row, const Part& p, int lane) {
+    const float log_s = log1pf(p.r);
+    u64 last = ~0ull;
+    for (int j = 0; j < a.n_top; ++j) {
+        if (last && !p.bad) {
+            u64 k = 0;
+            for (int i = lane; i < a.V; i += 32) {
+                const float v = is_allowed(ok, i) ? to_f(z[i]) : NEG_INF;
+                const u64 c = v > NEG_INF ? key_of(v, i) : 0ull;
+                if (c < last && c > k) k = c;
+            }
+            last = warp_max_key(k);
+        }
+        if (lane == 0) write_top(a, row, j, last, p, log_s);
+    }
+}
 
 template <typename T, int NV>
 __global__ void __launch_bounds__(ROW_WARPS * 32) k_logprobs_warp(const T* __restrict__ logits, Args a) {
     pdl_wait();
     pdl_trigger();
     __shared__ u64 found[ROW_WARPS][CAP];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.x * ROW_WARPS + warp;
-    if (row >= a.R) return;
-    const T* z = logits + (size_t)row * a.stride;
-    const uint32_t* ok = a.allowed ? a.allowed + (size_t)row * a.allowed_stride : nullptr;
-    float v[NV];
-    T raw[NV];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int WORDS = (NV + 31) / 32;
+    uint32_t mask[WORDS];  // this lane's ids of the row that are not masked: bit i of id 32 i + lane
+    for (int row = blockIdx.x * ROW_WARPS + warp, turn = 0; row < a.R; row += gridDim.x * ROW_WARPS, ++turn) {
+        const T* z = logits + (size_t)row * a.stride;
+        const uint32_t* ok = a.allowed ? a.allowed + (size_t)row * a.allowed_stride : nullptr;
+        if (turn == 0 || a.allowed_stride) {  // once for all rows
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (i * 32 + lane < a.V) raw[i] = z[i * 32 + lane];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = i * 32 + lane < a.V ? to_f(raw[i]) : NEG_INF;
-    float tz;
-    const bool wanted = target_of(a, z, ok, row, tz);
-    if (ok) {
-#pragma unroll
-        for (int i0 = 0; i0 < NV; i0 += 32) {
-            const uint32_t w = (i0 + lane) * 32 < a.V ? ok[i0 + lane] : 0u;  // lane's word of these 32
-#pragma unroll
-            for (int i = i0; i < NV && i < i0 + 32; ++i)
-                if (!(__shfl_sync(ALL, w, i - i0) >> lane & 1u)) v[i] = NEG_INF;
+            for (int w = 0; w < WORDS; ++w) {
+                const int n = a.V - lane - 1024 * w;  // of the ids from 1024 w + lane on, in steps of 32
+                mask[w] = n >= 993 ? 0xFFFFFFFFu : n > 0 ? (1u << ((n + 31) >> 5)) - 1u : 0u;
+                if (ok) {
+                    uint32_t bits = 0u;
+#pragma unroll 8
+                    for (int i = 32 * w; i < NV && i < 32 * w + 32; ++i)
+                        if (i * 32 < a.V) bits |= (ok[i] >> lane & 1u) << (i & 31);
+                    mask[w] &= bits;
+                }
+            }
         }
-    }
-    float mine = NEG_INF;
-    bool odd = false;
+        float v[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        odd |= !(v[i] < INFINITY);
-        mine = fmaxf(mine, v[i]);
-    }
-    Part p = {warp_max(mine), 0.f, 0.f, __any_sync(ALL, odd)};
-    float r = 0.f, t = 0.f;
-    int same = 0;
-    const float m = p.m > NONE ? p.m : 0.f;
+        for (int i = 0; i < NV; ++i) v[i] = mask[i / 32] >> (i & 31) & 1u ? to_f(z[i * 32 + lane]) : OUT;
+        float tz;
+        const bool wanted = target_of(a, z, ok, row, tz);
+        float mine = v[0], most = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const float d = fmaxf(v[i] - m, -1e4f), e = ex2(d * LOG2E);  // not -inf: 0 times it
-        t += e * d;
-        if (d == 0.f) ++same;
-        else r += e;
-    }
-    r = warp_sum(r);
-    t = warp_sum(t);
-    same = __reduce_add_sync(ALL, same);
-    p.r = r + (float)(same - 1);
-    p.t = t;
-    if (lane == 0) finish(a, row, p, wanted, tz);
-    if (a.n_top == 0) return;
-    int n = 0;
-    if (!p.bad && p.m > NONE) {
+        for (int i = 0; i < NV; i += 2) {
+            mine = max3(mine, v[i], v[i + 1]);
+            most = max3_nan(most, fabsf(v[i]), fabsf(v[i + 1]));
+        }
+        const bool odd = !(most <= 1e30f);
+        Part p = {row_max(mine), 0.f, 0.f, 0};
+        if (__any_sync(ALL, odd) || p.m == OUT) {
+            p = sums_of(z, ok, a.V, lane);
+            if (lane == 0) finish(a, row, p, log1pf(p.r), wanted, tz);
+            tops_of(z, ok, a, row, p, lane);
+            continue;
+        }
+        f2 r2 = 0, t2 = 0;  // two zeros each
+        const f2 m2 = pair(-p.m, -p.m), l2e = pair(LOG2E, LOG2E);
+#pragma unroll
+        for (int i = 0; i < NV; i += 2) {
+            const f2 d = addp(pair(v[i], v[i + 1]), m2);
+            float x0, x1;
+            halves(mulp(d, l2e), x0, x1);
+            const f2 e = pair(ex2(x0), ex2(x1));
+            r2 = addp(r2, e);
+            t2 = fmap(e, d, t2);
+        }
+        float r0, r1, t0, t1;
+        halves(r2, r0, r1);
+        halves(t2, t0, t1);
+        p.r = warp_sum(r0 + r1) - 1.f;
+        p.t = warp_sum(t0 + t1);
+        if (p.r < 1.f) {  // the digits behind the 1: lost only in the lanes that hold m, whose logits the warp sums again without it
+            const bool owner = mine == p.m;
+            float rest = 0.f;
+            int same = 0;
+            for (unsigned b = __ballot_sync(ALL, owner); b; b &= b - 1)
+                for (int i = lane * 32 + __ffs(b) - 1; i < a.V; i += 32 * 32) {
+                    const float d = (is_allowed(ok, i) ? to_f(z[i]) : OUT) - p.m;
+                    if (d == 0.f) ++same;
+                    else rest += ex2(d * LOG2E);
+                }
+            p.r = warp_sum((owner ? 0.f : r0 + r1) + rest) + (float)(__reduce_add_sync(ALL, same) - 1);
+        }
+        const float log_s = log1pf(p.r);
+        if (lane == 0) finish(a, row, p, log_s, wanted, tz);
+        if (a.n_top == 0) continue;
         float bound = p.m;
-        if (a.n_top > 1) {  // the lanes' maxima in falling order
+        if (a.n_top <= 8) {  // the largest of the lanes' maxima taken out n_top - 1 times, equal ones together
+            float s = mine;
+            for (int j = 1; j < a.n_top; ++j) {
+                if (s == bound) s = NEG_INF;
+                bound = row_max(s);
+            }
+        } else {  // the lanes' maxima in falling order
             float s = mine;
 #pragma unroll
             for (int k = 2; k <= 32; k <<= 1)
@@ -173,48 +286,52 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) k_logprobs_warp(const T* __res
                 }
             bound = __shfl_sync(ALL, s, a.n_top - 1);
         }
-        bound = fmaxf(bound, -3.4028235e38f);  // -inf is no alternative
+        bound = fmaxf(bound, -9e29f);  // OUT is no alternative
+        uint32_t in[(NV + 31) / 32];
+        int count = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool in = v[i] >= bound;
-            const unsigned b = __ballot_sync(ALL, in);
-            if (b) {
-                const int at = n + __popc(b & ((1u << lane) - 1));
-                if (in && at < CAP) found[warp][at] = key_of(v[i], i * 32 + lane);
-                n += __popc(b);
-            }
+        for (int w = 0; w < (NV + 31) / 32; ++w) {
+            in[w] = 0u;
+#pragma unroll
+            for (int i = 32 * w; i < NV && i < 32 * w + 32; ++i)
+                if (v[i] >= bound) in[w] |= 1u << (i & 31);
+            count += __popc(in[w]);
         }
-    }
-    __syncwarp();
-    const int have = min(n, a.n_top);
-    if (n <= CAP) {
+        int at = count;  // places of the lanes before this one, and of this one
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(ALL, at, o);
+            if (lane >= o) at += u;
+        }
+        const int n = __shfl_sync(ALL, at, 31);
+        if (n > CAP) {
+            tops_of(z, ok, a, row, p, lane);
+            continue;
+        }
+        at -= count;
+#pragma unroll
+        for (int w = 0; w < (NV + 31) / 32; ++w)
+            for (uint32_t b = in[w]; b; b &= b - 1) {
+                const int i = (w * 32 + __ffs(b) - 1) * 32 + lane;
+                found[warp][at++] = key_of(to_f(z[i]), i);
+            }
+        __syncwarp();
         for (int x = lane; x < n; x += 32) {
             const u64 k = found[warp][x];
             int rank = 0;
             for (int j = 0; j < n; ++j) rank += found[warp][j] > k;
-            if (rank < a.n_top) write_top(a, row, rank, k, p);
+            if (rank < a.n_top) write_top(a, row, rank, k, p, log_s);
         }
-    } else {  // more equal logits than places: one after the other
-        u64 last = ~0ull;
-        for (int j = 0; j < have; ++j) {
-            u64 k = 0;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const u64 c = v[i] > NEG_INF ? key_of(v[i], i * 32 + lane) : 0ull;
-                if (c < last && c > k) k = c;
-            }
-            last = warp_max_key(k);
-            if (lane == 0) write_top(a, row, j, last, p);
-        }
+        for (int j = min(n, a.n_top) + lane; j < a.n_top; j += 32) write_top(a, row, j, 0ull, p, log_s);
+        __syncwarp();  // before the next row's candidates
     }
-    for (int j = have + lane; j < a.n_top; j += 32) write_top(a, row, j, 0ull, p);
 }
 
 // ---------------------------------------------------------------- a cluster a row
 // A row cut into the slices of 1, 2, 4 or 8 blocks, each slice staged in shared memory (16-byte pieces where the row's alignment
 // has them; the places before and behind it hold -inf, so that all of it is read in 16-byte pieces) and read three times
-// there: maximum (masked ids become -inf in it), then sums and the candidates: logits that reach the n_top-th largest of the
-// threads' maxima, at most LIST of them (with more equal ones, one alternative after the other is looked for). Block 0
+// there: maximum (masked ids become -inf in it), then sums and the candidates: logits that reach a bound below the n_top-th
+// largest, at most LIST of them (with more equal ones, one alternative after the other is looked for). Block 0
 // joins the slices.
 constexpr int THREADS = 256, LIST = 1024, MAX_TOP = TTS_BB_LOGPROBS_MAX_TOP;
 constexpr int SLICE_BYTES = 48 * 1024, MAX_SLICE_BYTES = 192 * 1024;
@@ -233,18 +350,11 @@ __device__ __forceinline__ void unpack(const uint4& u, float (&v)[8], __half) {
         v[2 * i + 1] = f.y;
     }
 }
-__device__ __forceinline__ uint32_t order_of(float x) {
-    const uint32_t u = __float_as_uint(x);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
-struct __align__(16) Block {
-    uint32_t best[THREADS];  // read in 16-byte pieces: first, at the struct's alignment
+struct Block {
     float f[THREADS / 32];
     float g[THREADS / 32];
     int n[THREADS / 32];
     int count;
-    uint32_t bound;
     u64 list[LIST];
     u64 top[MAX_TOP];
     Part part;
@@ -293,6 +403,7 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
     T* const st = reinterpret_cast<T*>(stage);
     const T low = (T)NEG_INF;
     // piece q holds the slice's logits q E - mis ..; first and last may be cut
+#pragma unroll 4
     for (int q = tid; q < pieces; q += THREADS) {
         const int i = q * E - mis;
         if (i >= 0 && i + E <= n) {
@@ -305,7 +416,7 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
     }
     float tz = 0.f;
     const bool wanted = part == 0 && tid == 0 && target_of(a, z, ok, row, tz);
-    if (tid == 0) { sm.count = 0; sm.bound = 0xFFFFFFFFu; }
+    if (tid == 0) sm.count = 0;
     asm volatile("cp.async.wait_all;" ::: "memory");
     // a thread reads the pieces that it copied: its own copies are complete
 
@@ -334,32 +445,29 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
         }
     }
     const float wm = warp_max(mine);
-    if (lane == 0) sm.f[warp] = wm;
-    sm.best[tid] = order_of(mine + 0.f);
+    // the j-th largest of each warp's 32 maxima, j = n_top / warps rounded up: so many logits of each warp are that large, and
+    // the least of these bounds is one for n_top of the slice
+    float bv = NEG_INF;
+    if (a.n_top) {
+        float s = mine;
+#pragma unroll
+        for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+            for (int j = k >> 1; j; j >>= 1) {
+                const float o = __shfl_xor_sync(ALL, s, j);
+                s = ((lane & k) == 0) == ((lane & j) == 0) ? fmaxf(s, o) : fminf(s, o);
+            }
+        bv = __shfl_sync(ALL, s, (a.n_top - 1) / (THREADS / 32));
+    }
+    if (lane == 0) { sm.f[warp] = wm; sm.g[warp] = bv; }
     const int bad = __syncthreads_or(odd);
     Part p = {NEG_INF, 0.f, 0.f, bad};
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) p.m = fmaxf(p.m, sm.f[w]);
-    const bool some = p.m > NONE;
-    uint32_t bound = 0;
-    if (a.n_top && some) {  // threads whose maximum is among the n_top largest; the least of these maxima
-        const uint32_t b = sm.best[tid];
-        int above = 0;
-        const uint4* all = reinterpret_cast<const uint4*>(sm.best);
-#pragma unroll 8
-        for (int i = 0; i < THREADS / 4; ++i) {
-            const uint4 o = all[i];
-            above += (o.x > b) + (o.y > b) + (o.z > b) + (o.w > b);
-        }
-        uint32_t least = above < a.n_top ? b : 0xFFFFFFFFu;
-        least = __reduce_min_sync(ALL, least);
-        if (lane == 0) atomicMin(&sm.bound, least);
-        __syncthreads();
-        bound = max(sm.bound, order_of(-3.4028235e38f));  // -inf is no alternative
-    }
+    for (int w = 0; w < THREADS / 32; ++w) { p.m = fmaxf(p.m, sm.f[w]); bv = fminf(bv, sm.g[w]); }
+    const bool some = p.m > NONE, seek = a.n_top && some;
+    bv = fmaxf(bv, -3.4028235e38f);  // -inf is no alternative
     // sums and candidates
     const float m = some ? p.m : 0.f;
-    const float bv = __uint_as_float(bound & 0x80000000u ? bound & 0x7FFFFFFFu : ~bound);
     float r = 0.f, t = 0.f;
     int same = 0;
     for (int q = tid; q < pieces; q += THREADS) {
@@ -372,7 +480,7 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
             if (d == 0.f) ++same;
             else r += x;
         }
-        if (bound && mine >= bv) {
+        if (seek && mine >= bv) {
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 if (v[e] >= bv) {
@@ -395,7 +503,7 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
     if (a.n_top) {
         for (int j = tid; j < MAX_TOP; j += THREADS) sm.top[j] = 0ull;
         __syncthreads();
-        const int found = bound ? sm.count : 0;
+        const int found = seek ? sm.count : 0;
         if (found <= LIST) {
             for (int x = tid; x < found; x += THREADS) {
                 const u64 k = sm.list[x];
@@ -424,26 +532,28 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
     if (tid == 0) sm.part = p;
     if (n_parts == 1) {
         __syncthreads();
-        if (tid == 0) finish(a, row, p, wanted, tz);
-        for (int j = tid; j < a.n_top; j += THREADS) write_top(a, row, j, sm.top[j], p);
+        const float log_s = log1pf(p.r);
+        if (tid == 0) finish(a, row, p, log_s, wanted, tz);
+        for (int j = tid; j < a.n_top; j += THREADS) write_top(a, row, j, sm.top[j], p, log_s);
         return;
     }
     cluster_sync();
     if (part == 0) {
         for (int s = 1; s < n_parts; ++s)
             p = join(p, Part{peer(&sm.part.m, s), peer(&sm.part.r, s), peer(&sm.part.t, s), peer(&sm.part.bad, s)});
-        if (tid == 0) finish(a, row, p, wanted, tz);
+        const float log_s = log1pf(p.r);
+        if (tid == 0) finish(a, row, p, log_s, wanted, tz);
         if (a.n_top) {
             const int total = n_parts * a.n_top;  // at most 256: a key a thread
             const u64 k = tid < total ? peer(&sm.top[tid % a.n_top], tid / a.n_top) : 0ull;
             __syncthreads();
             sm.list[tid] = k;
-            for (int j = tid; j < a.n_top; j += THREADS) write_top(a, row, j, 0ull, p);
+            for (int j = tid; j < a.n_top; j += THREADS) write_top(a, row, j, 0ull, p, log_s);
             __syncthreads();
             if (k) {
                 int rank = 0;
                 for (int j = 0; j < total; ++j) rank += sm.list[j] > k;
-                if (rank < a.n_top) write_top(a, row, rank, k, p);
+                if (rank < a.n_top) write_top(a, row, rank, k, p, log_s);
             }
         }
     }
@@ -495,10 +605,11 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_long(const T* __restrict__
     r = block_sum(r, smf);
     t = block_sum(t, smf);
     const Part p = {best ? m : NONE, r, t, bad};
+    const float log_s = log1pf(r);
     if (tid == 0) {
         float tz;
         const bool wanted = target_of(a, z, ok, row, tz);
-        finish(a, row, p, wanted, tz);
+        finish(a, row, p, log_s, wanted, tz);
     }
     u64 last = ~0ull;
     for (int j = 0; j < a.n_top; ++j) {
@@ -512,7 +623,7 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_long(const T* __restrict__
             }
             last = block_max_key(k, smk);
         }
-        if (tid == 0) write_top(a, row, j, last, p);
+        if (tid == 0) write_top(a, row, j, last, p, log_s);
     }
 }
 
@@ -543,12 +654,15 @@ void launch_block(const T* logits, const Args& a, int n, int slice, cudaStream_t
 // shorter ones while the rows alone leave SMs idle.
 template <typename T>
 void launch(const T* logits, const Args& a, cudaStream_t st) {
-    const auto warps = [&](auto k) { launch_pdl(k, (a.R + ROW_WARPS - 1) / ROW_WARPS, ROW_WARPS * 32, 0, st, logits, a); };
+    // as many blocks as fit at a time: a warp goes on with further rows, and takes the mask apart once
+    const auto warps = [&](auto k, int fit) {
+        launch_pdl(k, std::min((a.R + ROW_WARPS - 1) / ROW_WARPS, fit * 152), ROW_WARPS * 32, 0, st, logits, a);
+    };
     if (a.R >= 4 * 152 || a.V <= 256) {
-        if (a.V <= 8 * 32) return warps(k_logprobs_warp<T, 8>);
-        if (a.V <= 33 * 32) return warps(k_logprobs_warp<T, 33>);
-        if (a.V <= 64 * 32) return warps(k_logprobs_warp<T, 64>);
-        if (a.V <= 96 * 32) return warps(k_logprobs_warp<T, 96>);
+        if (a.V <= 8 * 32) return warps(k_logprobs_warp<T, 8>, 10);
+        if (a.V <= 34 * 32) return warps(k_logprobs_warp<T, 34>, 8);
+        if (a.V <= 64 * 32) return warps(k_logprobs_warp<T, 64>, 4);
+        if (a.V <= 96 * 32) return warps(k_logprobs_warp<T, 96>, 3);
     }
     const long long bytes = (long long)a.V * sizeof(T);
     int n = 1;
