@@ -353,7 +353,6 @@ __device__ __forceinline__ void unpack(const uint4& u, float (&v)[8], __half) {
 struct Block {
     float f[THREADS / 32];
     float g[THREADS / 32];
-    int n[THREADS / 32];
     int count;
     u64 list[LIST];
     u64 top[MAX_TOP];
@@ -402,30 +401,15 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
     const int pieces = n ? (mis + n + E - 1) / E : 0;
     T* const st = reinterpret_cast<T*>(stage);
     const T low = (T)NEG_INF;
-    // piece q holds the slice's logits q E - mis ..; first and last may be cut
-#pragma unroll 4
-    for (int q = tid; q < pieces; q += THREADS) {
-        const int i = q * E - mis;
-        if (i >= 0 && i + E <= n) {
-            const uint32_t d = (uint32_t)__cvta_generic_to_shared(st + q * E);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src + i) : "memory");
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) st[q * E + e] = i + e >= 0 && i + e < n ? src[i + e] : low;
-        }
-    }
     float tz = 0.f;
     const bool wanted = part == 0 && tid == 0 && target_of(a, z, ok, row, tz);
     if (tid == 0) sm.count = 0;
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    // a thread reads the pieces that it copied: its own copies are complete
-
-    // maximum
+    // Staging, and the maximum on the way. Piece q holds the slice's logits q E - mis ..; the first and the last may be cut. A
+    // thread later reads the pieces that it wrote.
     float mine = NEG_INF;
-    bool odd = false;
-    for (int q = tid; q < pieces; q += THREADS) {
+    const auto take = [&](int q, uint4 u) {
         float v[E];
-        unpack(*reinterpret_cast<const uint4*>(st + q * E), v, T{});
+        unpack(u, v, T{});
         if (ok) {
             const int i = i0 + q * E - mis, w = max(i, 0) >> 5;
             const uint32_t lo = ok[w], hi = (w + 1) * 32 < a.V ? ok[w + 1] : 0u;
@@ -434,16 +418,38 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
                 const int b = i + e - w * 32;  // 0 .. 38
                 if (b >= 0 && !((b < 32 ? lo >> b : hi >> (b - 32)) & 1u)) {
                     v[e] = NEG_INF;
-                    st[q * E + e] = low;
+                    reinterpret_cast<T*>(&u)[e] = low;
                 }
             }
         }
+        *reinterpret_cast<uint4*>(st + q * E) = u;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) mine = max3_nan(mine, v[e], v[e + 1]);
+    };
+    const int q0 = mis ? 1 : 0, q1 = (mis + n) / E;  // whole pieces
+    int q = q0 + tid;
+    for (; q + 3 * THREADS < q1; q += 4 * THREADS) {
+        uint4 u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] = ldg_nc_v4(src + (q + k * THREADS) * E - mis);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) take(q + k * THREADS, u[k]);
+    }
+    for (; q < q1; q += THREADS) take(q, ldg_nc_v4(src + q * E - mis));
+    // the cut ones: by the threads that the later passes give them to
+    for (int c = 0; c < 2; ++c) {
+        const int p = c ? q1 : 0;
+        if ((c ? q1 >= pieces || (q1 == 0 && q0) : !q0) || (p + THREADS - q0) % THREADS != tid || !pieces) continue;
+        uint4 u;
+        T* const to = reinterpret_cast<T*>(&u);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            odd |= !(v[e] < INFINITY);
-            mine = fmaxf(mine, v[e]);
+            const int i = p * E - mis + e;
+            to[e] = i >= 0 && i < n ? src[i] : low;
         }
+        take(p, u);
     }
+    const bool odd = !(mine < INFINITY);  // a NaN stays one
     const float wm = warp_max(mine);
     // the j-th largest of each warp's 32 maxima, j = n_top / warps rounded up: so many logits of each warp are that large, and
     // the least of these bounds is one for n_top of the slice
@@ -468,19 +474,24 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
     bv = fmaxf(bv, -3.4028235e38f);  // -inf is no alternative
     // sums and candidates
     const float m = some ? p.m : 0.f;
-    float r = 0.f, t = 0.f;
-    int same = 0;
-    for (int q = tid; q < pieces; q += THREADS) {
+    const int mine0 = (tid + q0) % THREADS;  // this thread's pieces: those of the staging
+    f2 r2 = 0, t2 = 0;                       // two zeros each
+    const f2 m2 = pair(-m, -m), l2e = pair(LOG2E, LOG2E);
+    const bool look = seek && mine >= bv;
+    for (int q = mine0; q < pieces; q += THREADS) {
         float v[E];
         unpack(*reinterpret_cast<const uint4*>(st + q * E), v, T{});
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float d = fmaxf(v[e] - m, -1e4f), x = ex2(d * LOG2E);
-            t += x * d;
-            if (d == 0.f) ++same;
-            else r += x;
+        for (int e = 0; e < E; e += 2) {
+            float d0, d1, x0, x1;
+            halves(addp(pair(v[e], v[e + 1]), m2), d0, d1);
+            const f2 d = pair(fmaxf(d0, -1e30f), fmaxf(d1, -1e30f));  // not -inf: 0 times it
+            halves(mulp(d, l2e), x0, x1);
+            const f2 x = pair(ex2(x0), ex2(x1));
+            r2 = addp(r2, x);
+            t2 = fmap(x, d, t2);
         }
-        if (seek && mine >= bv) {
+        if (look) {
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 if (v[e] >= bv) {
@@ -489,16 +500,39 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
                 }
         }
     }
-    r = warp_sum(r);
-    t = warp_sum(t);
-    same = __reduce_add_sync(ALL, same);
-    __syncthreads();
-    if (lane == 0) { sm.f[warp] = r; sm.g[warp] = t; sm.n[warp] = same; }
-    __syncthreads();
-    same = -1;
+    const auto sum_up = [&](float x, float y, float& sx, float& sy) {
+        x = warp_sum(x);
+        y = warp_sum(y);
+        __syncthreads();
+        if (lane == 0) { sm.f[warp] = x; sm.g[warp] = y; }
+        __syncthreads();
+        sx = sy = 0.f;
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) { p.r += sm.f[w]; p.t += sm.g[w]; same += sm.n[w]; }
-    p.r += (float)same;
+        for (int w = 0; w < THREADS / 32; ++w) { sx += sm.f[w]; sy += sm.g[w]; }
+    };
+    {
+        float a0, a1, b0, b1;
+        halves(r2, a0, a1);
+        halves(t2, b0, b1);
+        sum_up(a0 + a1, b0 + b1, p.r, p.t);
+        p.r -= 1.f;
+    }
+    if (p.r < 1.f) {  // the digits behind the 1: once more without the largest
+        float x = 0.f, same = 0.f;
+        for (int q = mine0; q < pieces; q += THREADS) {
+            float v[E];
+            unpack(*reinterpret_cast<const uint4*>(st + q * E), v, T{});
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float d = fmaxf(v[e] - m, -1e30f);
+                if (d == 0.f) same += 1.f;
+                else x += ex2(d * LOG2E);
+            }
+        }
+        float rest;
+        sum_up(x, same, rest, p.r);
+        p.r = rest + (p.r - 1.f);
+    }
     // the slice's alternatives, in order
     if (a.n_top) {
         for (int j = tid; j < MAX_TOP; j += THREADS) sm.top[j] = 0ull;
@@ -515,7 +549,7 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
             u64 last = ~0ull;
             for (int j = 0; j < a.n_top && last; ++j) {
                 u64 k = 0;
-                for (int q = tid; q < pieces; q += THREADS) {
+                for (int q = mine0; q < pieces; q += THREADS) {
                     float v[E];
                     unpack(*reinterpret_cast<const uint4*>(st + q * E), v, T{});
 #pragma unroll
