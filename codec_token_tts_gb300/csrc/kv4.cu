@@ -607,7 +607,7 @@ __device__ __forceinline__ bool attn_row(const Cache& c, const AttnArgs& a, int 
 // Softmax: a running reference m for each head, moved only when a score exceeds it by 8 (log2): then sums and O are
 // rescaled. It starts at -1e30, not -inf, so that no difference of infinities arises.
 constexpr int WARPS = 4, STAGES = 2, UNIT = 32, UNIT_BYTES = 4608;  // K and V codes 2048 each, parameters 256 each
-constexpr int V_AT = 2048, KP_AT = 4096, VP_AT = 4352;
+constexpr int V_AT = 2048, KP_AT = 4096, VP_AT = 4352, RING_BYTES = WARPS * STAGES * UNIT_BYTES;
 constexpr float M_START = -1e30f, M_SLACK = 8.f;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
@@ -696,52 +696,76 @@ struct Shared {
 };
 
 // One piece: the cache blocks [b0, b1) of KV head g of a row that reads cache row seq and sees `seen` keys; q: its two heads.
-// Unit i of a warp is keys 32 (warp & 1) .. + 31 of block b0 + (warp >> 1) + 2 i. Thread d ends with the piece's reference M, sum of
-// weights L and output sums O of dim d of both heads. All threads of the block call it, with the same arguments.
+template <typename T> struct Piece {
+    const T* q;
+    int seq, seen, g, b0, b1;
+    // units of a warp: unit i is keys 32 (warp & 1) .. + 31 of block b0 + (warp >> 1) + 2 i
+    __device__ __forceinline__ int units(int warp) const { return max(0, (b1 - b0 - (warp >> 1) + 1) >> 1); }
+    __device__ __forceinline__ const int32_t* pages(const Cache& c, int warp) const {
+        return c.table + (size_t)seq * c.bps + b0 + (warp >> 1);
+    }
+};
+// What is on its way for a piece before its turn: the first unit (STAGES - 1 of them) and the queries
+struct Ahead {
+    float4 q;
+    int page;          // of the first unit not fetched yet
+    uint32_t missing;  // bit s: the block in stage s has no page
+};
+// A unit's codes and parameters into stage s of the warp's ring; the group is committed by the caller
+__device__ __forceinline__ void fetch_unit(const Cache& cache, int g, uint8_t* ring, int s, int page, uint32_t& missing) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool ok = page >= 0 && page < cache.n_blocks;
+    missing = missing & ~(1u << s) | (ok ? 0u : 1u << s);
+    if (ok) {
+        const uint8_t* const b = cache.pool + (size_t)page * BLOCK + (size_t)g * TILE + (warp & 1) * 2048 + lane * 16;
+        const uint32_t d = (uint32_t)__cvta_generic_to_shared(ring) + (warp * STAGES + s) * UNIT_BYTES;
+        // 16-byte pieces of V rows are swapped between the row's halves for rows 2, 3 of every 4, so that the 8-byte reads
+        // of 4 rows meet all 32 banks
+        const uint32_t vd = d + V_AT + (lane * 16 ^ (lane >> 3 & 1) * 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            cp16(d + lane * 16 + 512 * i, b + 512 * i);
+            cp16(vd + 512 * i, b + NKV * TILE + 512 * i);
+        }
+        cp16(d + KP_AT + lane * 16, b + (lane & 16 ? NKV * TILE : 0) + PAR + (warp & 1) * (256 - 2048) + ((lane & 15) - lane) * 16);
+    } else if (lane == 0) {
+        set_err(cache.err, TTS_BB_KV4_ERR_PAGE);
+    }
+}
 template <typename T>
-__device__ __forceinline__ void attend_piece(const T* __restrict__ q, const Cache& cache, int seq, int seen, int g, int b0, int b1,
-                                             uint8_t* ring, Shared& sh, float (&M)[2], float (&L)[2], float (&O)[2]) {
+__device__ __forceinline__ void start_piece(const Piece<T>& p, const Cache& cache, uint8_t* ring, int page0, Ahead& a) {
+    static_assert(STAGES == 2, "one unit ahead");
+    const int warp = threadIdx.x >> 5, n = p.units(warp);
+    a.missing = 0u;
+    if (n > 0) fetch_unit(cache, p.g, ring, 0, page0, a.missing);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    a.page = n > 1 ? p.pages(cache, warp)[2] : 0;
+}
+template <typename T>
+__device__ __forceinline__ void load_queries(const Piece<T>& p, Ahead& a) {
+    if (threadIdx.x < 64) a.q = load4(p.q + threadIdx.x * 4);  // warps 0, 1: a head each
+}
+
+// A piece that is started already; the next one (where more) is started before the warps' results are merged, so that its
+// keys come meanwhile. Thread d ends with the piece's reference M, sum of weights L and output sums O of dim d of both
+// heads. All threads of the block call it, with the same arguments; `so` is free again when the next call has merged.
+template <typename T>
+__device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const Piece<T>& next, const Cache& cache, uint8_t* ring, float* so,
+                                             Shared& sh, Ahead& ahead, float (&M)[2], float (&L)[2], float (&O)[2]) {
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int P = F32 ? 3 : 2;  // bf16 parts of a weight
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    float4 qv = {};
-    if (warp < 2) qv = load4(q + warp * HD + lane * 4);
-    const int j0 = b0 + (warp >> 1), n = max(0, (b1 - j0 + 1) >> 1);
-
+    const int seen = p.seen, j0 = p.b0 + (warp >> 1), n = p.units(warp);
     uint8_t* const mine = ring + warp * STAGES * UNIT_BYTES;
-    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(mine);
-    const uint8_t* const src = cache.pool + (size_t)g * TILE + (warp & 1) * 2048 + lane * 16;
-    const int32_t* const pages = cache.table + (size_t)seq * cache.bps + j0;
-    // 16-byte pieces of V rows are swapped between the row's halves for rows 2, 3 of every 4, so that the 8-byte reads
-    // of 4 rows meet all 32 banks
-    const uint32_t vdst = V_AT + (lane * 16 ^ (lane >> 3 & 1) * 32);
-    const int ppiece = (lane & 16 ? NKV * TILE : 0) + PAR + (warp & 1) * (256 - 2048) + ((lane & 15) - lane) * 16;
-    uint32_t missing = 0;  // bit s: the block in stage s has no page
-    auto fetch = [&](int s, int page) {
-        const bool ok = page >= 0 && page < cache.n_blocks;
-        missing = missing & ~(1u << s) | (ok ? 0u : 1u << s);
-        if (ok) {
-            const uint8_t* b = src + (size_t)page * BLOCK;
-            const uint32_t d = dst + s * UNIT_BYTES;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                cp16(d + lane * 16 + 512 * i, b + 512 * i);
-                cp16(d + vdst + 512 * i, b + NKV * TILE + 512 * i);
-            }
-            cp16(d + KP_AT + lane * 16, b + ppiece);
-        } else if (lane == 0) {
-            set_err(cache.err, TTS_BB_KV4_ERR_PAGE);
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) {
-        if (i < n) fetch(i, pages[2 * i]);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    int page = n > STAGES - 1 ? pages[2 * (STAGES - 1)] : 0;
+    const int32_t* const pages = p.pages(cache, warp);
 
-    if (warp < 2) stage_q<F32 ? 2 : 1>(qv, lane, sh.q[0][warp], sh.about[warp]);
+    if (warp < 2) stage_q<F32 ? 2 : 1>(ahead.q, lane, sh.q[0][warp], sh.about[warp]);
     __syncthreads();
+    int next_page = 0;
+    if (more) {
+        if (next.units(warp) > 0) next_page = next.pages(cache, warp)[0];
+        load_queries(next, ahead);
+    }
     uint4 qb[4];       // of word w: the B registers of its two steps
     const float qsum[2] = {sh.about[c >> 1][0], sh.about[c >> 1][1]};
     const float factor = sh.about[c >> 1][2];
@@ -882,11 +906,11 @@ __device__ __forceinline__ void attend_piece(const T* __restrict__ q, const Cach
     for (int i = 0; i < n; ++i) {
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
         __syncwarp();
-        if (i + STAGES - 1 < n) fetch((i + STAGES - 1) % STAGES, page);
+        if (i + STAGES - 1 < n) fetch_unit(cache, p.g, ring, (i + STAGES - 1) % STAGES, ahead.page, ahead.missing);
         asm volatile("cp.async.commit_group;" ::: "memory");
-        if (i + STAGES < n) page = pages[2 * (i + STAGES)];
+        if (i + STAGES < n) ahead.page = pages[2 * (i + STAGES)];
         const int key0 = (j0 + 2 * i) * KVB + (warp & 1) * UNIT;
-        if (key0 >= seen || (missing >> (i % STAGES) & 1)) continue;
+        if (key0 >= seen || (ahead.missing >> (i % STAGES) & 1)) continue;
         const int at = (i % STAGES) * UNIT_BYTES;
 #pragma unroll 1
         for (int u = 0; u < 2; ++u) {
@@ -895,14 +919,15 @@ __device__ __forceinline__ void attend_piece(const T* __restrict__ q, const Cach
             else if (k < seen) step(std::true_type{}, at + 1024 * u, at + 128 * u, k);
         }
     }
-    // merge the warps: every part of O to shared memory, then one thread for each dim
+    // merge the warps: every part of O to shared memory (so: [warp][part][head][128]), then one thread for each dim
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 4);
     l += __shfl_xor_sync(0xffffffffu, l, 8);
     l += __shfl_xor_sync(0xffffffffu, l, 16);
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
-    float* const so = reinterpret_cast<float*>(ring);  // [warp][part][head][128]
+    if (more) {
+        __syncwarp();  // the warp's ring is free
+        start_piece(next, cache, ring, next_page, ahead);
+    }
     if (c < P) {
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
@@ -947,7 +972,11 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict_
     if (!attn_row(cache, a, row, d == 0 && split == 0 && g == 0, seq, seen)) return;
     const int nblk = (seen + KVB - 1) / KVB, bps = (nblk + a.n_splits - 1) / a.n_splits;
     float M[2], L[2], O[2];
-    attend_piece(q + ((size_t)row * NQ + 2 * g) * HD, cache, seq, seen, g, split * bps, min(nblk, (split + 1) * bps), ring, sh, M, L, O);
+    const Piece<T> p = {q + ((size_t)row * NQ + 2 * g) * HD, seq, seen, g, split * bps, min(nblk, (split + 1) * bps)};
+    Ahead ahead;
+    load_queries(p, ahead);
+    start_piece(p, cache, ring, p.units(d >> 5) > 0 ? p.pages(cache, d >> 5)[0] : 0, ahead);
+    attend_piece(p, false, p, cache, ring, reinterpret_cast<float*>(ring + RING_BYTES), sh, ahead, M, L, O);
     T* const to = out + ((size_t)row * NQ + 2 * g) * HD;
     if (a.n_splits == 1) {
 #pragma unroll
@@ -1003,22 +1032,26 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn_line(const T* __rest
     pdl_trigger();
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(16) Shared sh;
-    __shared__ int start[2];  // the share's first row, and the blocks of it before the share
+    __shared__ int start[4];  // the share's first row, the blocks of it before the share, its cache row and its keys
     __shared__ long long sums[WARPS];
     const int me = blockIdx.x, d = threadIdx.x, warp = d >> 5, lane = d & 31;
-    // where the share begins: sums of the rows' blocks, a row a thread at a time, once for their total and once for the place
-    long long total = 0;
-    for (int i = d; i < a.rows; i += WARPS * 32) total += row_blocks(cache, a, i, me == 0);
+    // where the share begins: the rows' blocks, a row a thread at a time; the sums of all rows first, where one turn is not enough
+    long long total = 0, before = 0, first = 0;
+    Line line = {0, 0};
+    const bool one_turn = a.rows <= WARPS * 32;
+    if (!one_turn) {
+        for (int i = d; i < a.rows; i += WARPS * 32) total += row_blocks(cache, a, i, me == 0);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) sums[warp] = total;
-    __syncthreads();
-    total = sums[0] + sums[1] + sums[2] + sums[3];
-    const Line line = line_of(total, gridDim.x);
-    const long long first = (long long)me * line.share;
-    long long before = 0;
+        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        if (lane == 0) sums[warp] = total;
+        __syncthreads();
+        total = sums[0] + sums[1] + sums[2] + sums[3];
+        line = line_of(total, gridDim.x);
+        first = (long long)me * line.share;
+    }
     for (int i = d; i - d < a.rows && before * NKV <= first; i += WARPS * 32) {
-        const int n = row_blocks(cache, a, i, false);
+        int row_seq = 0, row_seen = 0;
+        const int n = i < a.rows && attn_row(cache, a, i, one_turn && me == 0, row_seq, row_seen) ? (row_seen + KVB - 1) / KVB : 0;
         int incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -1034,40 +1067,69 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn_line(const T* __rest
             if (w < warp) mine += sums[w];
             before += sums[w];
         }
-        if (first >= mine * NKV && first < (mine + n) * NKV) { start[0] = i; start[1] = (int)(first - mine * NKV); }
-    }
-    // rows that see nothing: zeros, by the blocks in turn
-    for (int row = me; row < a.rows; row += gridDim.x) {
-        int seq, seen;
-        if (attn_row(cache, a, row, false, seq, seen) && seen == 0)
-            for (int i = d; i < NQ * HD; i += WARPS * 32) out[(size_t)row * NQ * HD + i] = (T)0.f;
+        if (one_turn) {
+            line = line_of(before, gridDim.x);
+            first = (long long)me * line.share;
+        }
+        if (first >= mine * NKV && first < (mine + n) * NKV) {
+            start[0] = i;
+            start[1] = (int)(first - mine * NKV);
+            start[2] = row_seq;
+            start[3] = row_seen;
+        }
     }
     __syncthreads();
-    if (first >= line.units) return;
-    int row = start[0], at = start[1], left = (int)min((long long)line.share, line.units - first);
-    bool begins = true;  // the share's first piece
-    for (; left > 0 && row < a.rows;) {
-        int seq, seen;
-        if (!attn_row(cache, a, row, false, seq, seen) || seen == 0) { ++row; continue; }
-        const int nblk = (seen + KVB - 1) / KVB, g = at / nblk, b0 = at - g * nblk, b1 = min(nblk, b0 + left);
-        float M[2], L[2], O[2];
-        attend_piece(q + ((size_t)row * NQ + 2 * g) * HD, cache, seq, seen, g, b0, b1, ring, sh, M, L, O);
-        if (b0 == 0 && b1 == nblk) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) out[((size_t)row * NQ + 2 * g + h) * HD + d] = (T)(L[h] == 0.f ? 0.f : O[h] / L[h]);
-        } else {
-            float* const to = place(a.part, me, begins ? 0 : 1);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                to[h * PIECE + d] = O[h];
-                if (d == 0) { to[h * PIECE + HD] = M[h]; to[h * PIECE + HD + 1] = L[h]; }
+    if (first < line.units) {
+        int row = start[0], at = start[1], seq = start[2], seen = start[3], left = (int)min((long long)line.share, line.units - first);
+        // the piece from `at` of the row on; then the place behind it
+        const auto take = [&](Piece<T>& p, int& piece_row, bool& whole) {
+            const int nblk = (seen + KVB - 1) / KVB, g = at / nblk, b0 = at - g * nblk, b1 = min(nblk, b0 + left);
+            p = {q + ((size_t)row * NQ + 2 * g) * HD, seq, seen, g, b0, b1};
+            piece_row = row;
+            whole = b0 == 0 && b1 == nblk;
+            left -= b1 - b0;
+            at += b1 - b0;
+            if (at == nblk * NKV) {
+                at = 0;
+                if (left > 0)
+                    do ++row; while (row < a.rows && (!attn_row(cache, a, row, false, seq, seen) || seen == 0));
+                if (row >= a.rows) left = 0;
             }
+        };
+        Piece<T> p, next;
+        int piece_row, next_row = 0;
+        bool whole, next_whole = false, begins = true;  // the share's first piece
+        take(p, piece_row, whole);
+        Ahead ahead;
+        load_queries(p, ahead);
+        start_piece(p, cache, ring, p.units(warp) > 0 ? p.pages(cache, warp)[0] : 0, ahead);
+        for (bool more = true; more;) {
+            more = left > 0;
+            if (more) take(next, next_row, next_whole);
+            float M[2], L[2], O[2];
+            attend_piece(p, more, next, cache, ring, reinterpret_cast<float*>(ring + RING_BYTES), sh, ahead, M, L, O);
+            if (whole) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) out[((size_t)piece_row * NQ + 2 * p.g + h) * HD + d] = (T)(L[h] == 0.f ? 0.f : O[h] / L[h]);
+            } else {
+                float* const to = place(a.part, me, begins ? 0 : 1);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    to[h * PIECE + d] = O[h];
+                    if (d == 0) { to[h * PIECE + HD] = M[h]; to[h * PIECE + HD + 1] = L[h]; }
+                }
+            }
+            begins = false;
+            p = next;
+            piece_row = next_row;
+            whole = next_whole;
         }
-        begins = false;
-        left -= b1 - b0;
-        at += b1 - b0;
-        if (at == nblk * NKV) { ++row; at = 0; }
-        __syncthreads();  // the ring and the sums are free again
+    }
+    // rows that see nothing: zeros, by the blocks in turn
+    for (int i = me; i < a.rows; i += gridDim.x) {
+        int seq, seen;
+        if (attn_row(cache, a, i, false, seq, seen) && seen == 0)
+            for (int e = d; e < NQ * HD; e += WARPS * 32) out[(size_t)i * NQ * HD + e] = (T)0.f;
     }
 }
 
@@ -1261,7 +1323,10 @@ TTS_API tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S
     const AttnArgs a{seqs, kv_lens, S, max_len, B * S, p.splits, static_cast<float*>(workspace)};
     auto go = [&](auto t) {
         typedef decltype(t) T;
-        const size_t smem = WARPS * STAGES * UNIT_BYTES;
+        constexpr size_t smem = RING_BYTES + (size_t)WARPS * (sizeof(T) == 4 ? 3 : 2) * 2 * HD * sizeof(float);
+        static SmemState grid_state, line_state;
+        allow_smem(grid_state, k_kv4_attn<T>, smem);
+        allow_smem(line_state, k_kv4_attn_line<T>, smem);
         const T* const qt = static_cast<const T*>(q);
         T* const to = static_cast<T*>(out);
         if (p.splits > 1) {
