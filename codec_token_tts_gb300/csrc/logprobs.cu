@@ -333,8 +333,8 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) k_logprobs_warp(const T* __res
 // there: maximum (masked ids become -inf in it), then sums and the candidates: logits that reach a bound below the n_top-th
 // largest, at most LIST of them (with more equal ones, one alternative after the other is looked for). Block 0
 // joins the slices.
-constexpr int THREADS = 256, LIST = 1024, MAX_TOP = TTS_BB_LOGPROBS_MAX_TOP;
-constexpr int SLICE_BYTES = 48 * 1024, MAX_SLICE_BYTES = 192 * 1024;
+constexpr int LIST = 1024, MAX_TOP = TTS_BB_LOGPROBS_MAX_TOP;
+constexpr int SLICE_BYTES = 48 * 1024, MAX_SLICE_BYTES = 192 * 1024, SMALL_SLICE = 16 * 1024;  // up to it: 128 threads a block
 
 template <typename T> constexpr int EACH = 16 / sizeof(T);  // logits of a 16-byte piece
 __device__ __forceinline__ void unpack(const uint4& u, float (&v)[4], float) {
@@ -350,7 +350,7 @@ __device__ __forceinline__ void unpack(const uint4& u, float (&v)[8], __half) {
         v[2 * i + 1] = f.y;
     }
 }
-struct Block {
+template <int THREADS> struct Block {
     float f[THREADS / 32];
     float g[THREADS / 32];
     int count;
@@ -358,6 +358,7 @@ struct Block {
     u64 top[MAX_TOP];
     Part part;
 };
+template <int THREADS>
 __device__ __forceinline__ u64 block_max_key(u64 k, u64* sm) {
     k = warp_max_key(k);
     __syncthreads();
@@ -385,12 +386,12 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // grid R * n_parts; slice: a multiple of 32 logits
-template <typename T>
+template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict__ logits, Args a, int n_parts, int slice) {
     pdl_wait();
     pdl_trigger();
     extern __shared__ __align__(16) uint8_t stage[];
-    __shared__ Block sm;
+    __shared__ Block<THREADS> sm;
     constexpr int E = EACH<T>;
     const int row = blockIdx.x / n_parts, part = blockIdx.x - row * n_parts, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const T* z = logits + (size_t)row * a.stride;
@@ -451,8 +452,9 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
     }
     const bool odd = !(mine < INFINITY);  // a NaN stays one
     const float wm = warp_max(mine);
-    // the j-th largest of each warp's 32 maxima, j = n_top / warps rounded up: so many logits of each warp are that large, and
-    // the least of these bounds is one for n_top of the slice
+    // the j-th largest of a warp's 32 maxima, j = n_top / warps rounded up: so many logits of each warp are that large, and
+    // the least of these bounds is one for n_top of the slice. Of the warps whose lanes all have a piece (or the first).
+    const int full = min(max(pieces / 32, 1), THREADS / 32);
     float bv = NEG_INF;
     if (a.n_top) {
         float s = mine;
@@ -463,13 +465,16 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
                 const float o = __shfl_xor_sync(ALL, s, j);
                 s = ((lane & k) == 0) == ((lane & j) == 0) ? fmaxf(s, o) : fminf(s, o);
             }
-        bv = __shfl_sync(ALL, s, (a.n_top - 1) / (THREADS / 32));
+        bv = __shfl_sync(ALL, s, min((a.n_top - 1) / full, 31));
     }
-    if (lane == 0) { sm.f[warp] = wm; sm.g[warp] = bv; }
+    if (lane == 0) { sm.f[warp] = wm; sm.g[warp] = warp < full ? bv : INFINITY; }
     const int bad = __syncthreads_or(odd);
     Part p = {NEG_INF, 0.f, 0.f, bad};
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) { p.m = fmaxf(p.m, sm.f[w]); bv = fminf(bv, sm.g[w]); }
+    for (int w = 0; w < THREADS / 32; ++w) p.m = fmaxf(p.m, sm.f[w]);
+    bv = sm.g[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 32; ++w) bv = fminf(bv, sm.g[w]);
     const bool some = p.m > NONE, seek = a.n_top && some;
     bv = fmaxf(bv, -3.4028235e38f);  // -inf is no alternative
     // sums and candidates
@@ -558,7 +563,7 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
                         if (c < last && c > k) k = c;
                     }
                 }
-                last = block_max_key(k, sm.list);
+                last = block_max_key<THREADS>(k, sm.list);
                 if (tid == 0) sm.top[j] = last;
             }
         }
@@ -578,13 +583,14 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
         const float log_s = log1pf(p.r);
         if (tid == 0) finish(a, row, p, log_s, wanted, tz);
         if (a.n_top) {
-            const int total = n_parts * a.n_top;  // at most 256: a key a thread
-            const u64 k = tid < total ? peer(&sm.top[tid % a.n_top], tid / a.n_top) : 0ull;
+            const int total = n_parts * a.n_top;  // at most 256
             __syncthreads();
-            sm.list[tid] = k;
+            for (int x = tid; x < total; x += THREADS) sm.list[x] = peer(&sm.top[x % a.n_top], x / a.n_top);
             for (int j = tid; j < a.n_top; j += THREADS) write_top(a, row, j, 0ull, p, log_s);
             __syncthreads();
-            if (k) {
+            for (int x = tid; x < total; x += THREADS) {
+                const u64 k = sm.list[x];
+                if (!k) continue;
                 int rank = 0;
                 for (int j = 0; j < total; ++j) rank += sm.list[j] > k;
                 if (rank < a.n_top) write_top(a, row, rank, k, p, log_s);
@@ -595,6 +601,7 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
 }
 
 // ---------------------------------------------------------------- rows longer than 8 slices of shared memory
+constexpr int THREADS = 256;
 template <typename T>
 __device__ __forceinline__ T block_sum(T v, T* sm) {
 #pragma unroll
@@ -626,7 +633,7 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_long(const T* __restrict__
         else if (v > NEG_INF) { const u64 k = key_of(v, i); best = k > best ? k : best; }
     }
     bad = __syncthreads_or(bad);
-    best = block_max_key(best, smk);
+    best = block_max_key<THREADS>(best, smk);
     const int top = best ? id_of(best) : -1;
     const float m = best ? value_of(best) : 0.f;
     float r = 0.f, t = 0.f;
@@ -655,18 +662,18 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_long(const T* __restrict__
                 const u64 c = key_of(v, i);
                 if (c < last && c > k) k = c;
             }
-            last = block_max_key(k, smk);
+            last = block_max_key<THREADS>(k, smk);
         }
         if (tid == 0) write_top(a, row, j, last, p, log_s);
     }
 }
 
 // launch_pdl with clusters of n blocks, and shared memory beyond the default
-template <typename T>
+template <typename T, int TH>
 void launch_block(const T* logits, const Args& a, int n, int slice, cudaStream_t st) {
     const size_t smem = (size_t)slice * sizeof(T) + 16;
     static SmemState state;
-    if (smem + sizeof(Block) > 48 * 1024) allow_smem(state, k_logprobs_block<T>, MAX_SLICE_BYTES + 16);
+    if (smem + sizeof(Block<TH>) > 48 * 1024) allow_smem(state, k_logprobs_block<T, TH>, MAX_SLICE_BYTES + 16);
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -675,12 +682,12 @@ void launch_block(const T* logits, const Args& a, int n, int slice, cudaStream_t
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.R * n));
-    cfg.blockDim = THREADS;
+    cfg.blockDim = TH;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = n > 1 ? 2 : 1;
-    cudaLaunchKernelEx(&cfg, k_logprobs_block<T>, logits, a, n, slice);
+    cudaLaunchKernelEx(&cfg, k_logprobs_block<T, TH>, logits, a, n, slice);
 }
 
 // Many rows of up to 96 logits a lane: a warp each (below 4 warps an SM a row's latency counts, and a block's threads
@@ -704,8 +711,10 @@ void launch(const T* logits, const Args& a, cudaStream_t st) {
     const int slice = ((a.V + n - 1) / n + 31) / 32 * 32;
     if ((long long)slice * sizeof(T) > MAX_SLICE_BYTES)
         launch_pdl(k_logprobs_long<T>, a.R, THREADS, 0, st, logits, a);
+    else if ((long long)slice * sizeof(T) <= SMALL_SLICE)
+        launch_block<T, 128>(logits, a, n, slice, st);
     else
-        launch_block(logits, a, n, slice, st);
+        launch_block<T, 256>(logits, a, n, slice, st);
 }
 
 }  // namespace

@@ -87,7 +87,7 @@ def test_rows_against_64_bits(R, V, k, io):
 
 
 @pytest.mark.parametrize("io", TYPES)
-@pytest.mark.parametrize("R,V,k", [(4, 1025, 5), (3, 3001, 20), (2, 40000, 32), (5, 40, 32), (609, 1025, 5), (608, 2047, 3), (2, 500001, 4)])
+@pytest.mark.parametrize("R,V,k", [(4, 1025, 5), (3, 3001, 20), (2, 40000, 32), (5, 40, 32), (609, 1025, 5), (608, 2047, 3), (2, 500001, 4), (9, 1025, 20), (4, 520, 32), (3, 9000, 32), (620, 3300, 9)])
 def test_masked_places_do_not_count(R, V, k, io):
     """Masked NaN, infinities and the type's lowest value; one mask for all rows, and one a row; a row with nothing
     left, with one id left, and targets that are masked or out of range."""
