@@ -20,6 +20,8 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "../../include/tts_bb.h"
@@ -62,118 +64,6 @@ __global__ void k_w4_pack(int N, int K, int G, const uint8_t* __restrict__ codes
     }
 }
 
-__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-// one word of codes -> the A registers of a step; z0, z1: -(128 + zero) of rows r, r + 8, twice each
-__device__ __forceinline__ void dequant(uint32_t w, uint32_t z0, uint32_t z1, uint32_t* a) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) a[j] = add_bf16x2((w >> (4 * j) & 0x000F000Fu) | 0x43004300u, j & 1 ? z1 : z0);
-}
-// part (0, 1, 2) of an fp32 value: 8 significant bits each, by truncation; m1, m2: all ones above bit 15 where part >= 1, 2
-__device__ __forceinline__ float part_of(float x, uint32_t m1, uint32_t m2) {
-    x -= __uint_as_float(__float_as_uint(x) & m1);
-    return x - __uint_as_float(__float_as_uint(x) & m2);
-}
-
-template <typename T> constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
-
-// For rows of x too long for shared memory: x is taken apart where it is used, into bf16 parts (fp32: three, by truncation:
-// 8 + 8 + 8 bits, together x itself), and the codes become whole numbers: 0x4300 | code is 128 + code, and adding
-// -(128 + zero) is exact.
-// grid (ceil(N / 16), chunks of x rows), WARPS * 32 threads: one 16-row tile, its groups dealt to the warps; NT tiles
-// of 8 columns, a column being one part of one row of x. The warps' sums are added in their order.
-template <typename T, int G, int NT>
-__global__ void __launch_bounds__(WARPS * 32) k_w4_linear(int T_, int N, int K, const T* __restrict__ x, long long stride,
-                                                          const uint8_t* __restrict__ packed, T* __restrict__ y, int per) {
-    pdl_wait();
-    pdl_trigger();
-    constexpr int P = PARTS<T>, WORDS = G / 16;
-    const int tile = blockIdx.x, t0 = blockIdx.y * per, nt_tok = min(per, T_ - t0);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
-    const int groups = K / G;
-    float acc[NT][4] = {};
-    for (int g = warp; g < groups; g += WARPS) {
-        const uint8_t* rec = packed + ((size_t)tile * groups + g) * record_bytes(G);
-        uint32_t w[WORDS];
-        if constexpr (WORDS == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(rec + lane * 8);
-            w[0] = v.x; w[1] = v.y;
-        } else {
-#pragma unroll
-            for (int i = 0; i < WORDS / 4; ++i) {
-                const uint4 v = *reinterpret_cast<const uint4*>(rec + (i * 32 + lane) * 16);
-                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-            }
-        }
-        const uint32_t p0 = reinterpret_cast<const uint32_t*>(rec + G * 8)[r];
-        const uint32_t p1 = reinterpret_cast<const uint32_t*>(rec + G * 8)[r + 8];
-        // -(128 + zero)
-        const float f0 = __half2float(__ushort_as_half((unsigned short)p0)), f1 = __half2float(__ushort_as_half((unsigned short)p1));
-        const uint32_t z0 = 0x10001u * __bfloat16_as_ushort(f2bf(f0 * 512.f - 128.f));
-        const uint32_t z1 = 0x10001u * __bfloat16_as_ushort(f2bf(f1 * 512.f - 128.f));
-        float d[NT][4] = {};
-        uint32_t a[WORDS][4];
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) dequant(w[i], z0, z1, a[i]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int c = nt * 8 + r, tok = c / P;
-            const bool on = tok < nt_tok;
-            const T* src = x + (size_t)(t0 + (on ? tok : 0)) * stride + g * G + q * (G / 4);
-            uint32_t b[2 * WORDS];
-            if constexpr (P == 1) {
-#pragma unroll
-                for (int i = 0; i < WORDS / 2; ++i) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
-                    b[4 * i] = v.x; b[4 * i + 1] = v.y; b[4 * i + 2] = v.z; b[4 * i + 3] = v.w;
-                }
-            } else {
-                const int part = c - tok * P;
-                const uint32_t m1 = part >= 1 ? 0xFFFF0000u : 0u, m2 = part >= 2 ? 0xFFFF0000u : 0u;
-#pragma unroll
-                for (int i = 0; i < WORDS; ++i) {
-                    const float4 v = *reinterpret_cast<const float4*>(src + 4 * i);
-                    b[2 * i] = __byte_perm(__float_as_uint(part_of(v.x, m1, m2)), __float_as_uint(part_of(v.y, m1, m2)), 0x7632);
-                    b[2 * i + 1] = __byte_perm(__float_as_uint(part_of(v.z, m1, m2)), __float_as_uint(part_of(v.w, m1, m2)), 0x7632);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < WORDS; ++i) mma(d[nt], a[i], on ? b[2 * i] : 0u, on ? b[2 * i + 1] : 0u);
-        }
-        const float s0 = __uint_as_float(p0 & 0xFFFF0000u), s1 = __uint_as_float(p1 & 0xFFFF0000u);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            acc[nt][0] += s0 * d[nt][0]; acc[nt][1] += s0 * d[nt][1];
-            acc[nt][2] += s1 * d[nt][2]; acc[nt][3] += s1 * d[nt][3];
-        }
-    }
-    __shared__ float red[WARPS][NT * 8][17];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) red[warp][nt * 8 + 2 * q + (e & 1)][r + (e >> 1) * 8] = acc[nt][e];
-    __syncthreads();
-    for (int i = threadIdx.x; i < nt_tok * 16; i += WARPS * 32) {
-        const int tok = i >> 4, n = i & 15;
-        float v = 0.f;
-#pragma unroll
-        for (int p = P - 1; p >= 0; --p)  // the small parts first
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) v += red[w][tok * P + p][n];
-        if (tile * 16 + n < N) y[(size_t)(t0 + tok) * N + tile * 16 + n] = (T)v;
-    }
-}
-
-// ---------------------------------------------------------------- x in shared memory
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -190,10 +80,21 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
 }
 __device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) { unpack8(*reinterpret_cast<const uint4*>(p), v); }
 
+__device__ __forceinline__ float peer(const float* p, int rank) {  // *p in the shared memory of a block of the cluster
+    uint32_t at;
+    float v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 template <typename T> constexpr int COLS = sizeof(T) == 4 ? 2 : 1;  // fp16 parts, columns, of a row of x
 constexpr int RED_ROW = 17, STAGES = 3;
+constexpr int MOST_COLS = 32;
 // tiles of 8 columns that a kernel is built for
-constexpr int tiles_for(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 32 ? 4 : 8; }
+constexpr int tiles_for(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
 constexpr size_t staged_bytes(int cols, int K, int G) {
     return (size_t)cols * K * 2 + (size_t)2 * WARPS * tiles_for(cols) * 8 * RED_ROW * 4 + (size_t)WARPS * STAGES * record_bytes(G);
 }
@@ -203,16 +104,24 @@ constexpr size_t staged_bytes(int cols, int K, int G) {
 // warp's own, two on their way while one is multiplied.
 // Shared memory: x as B registers, 16 bytes (two steps) a lane and piece: [group][G / 32 pieces][columns][4 lanes]; the warps'
 // sums of a tile, twice: one barrier a tile; the rings. Sums are added in the warps' order.
-template <typename T, int G, int NT>
-__global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2) k_w4_staged(int T_, int N, int K, const T* __restrict__ x, long long stride,
-                                                             const uint8_t* __restrict__ packed, T* __restrict__ y, int per) {
+// With SPLIT a cluster of blocks has K in slices of `slice` columns, a block each (the last may have fewer, or none), and a
+// warp a tile of its own. After a round of WARPS tiles the blocks lay down their sums, arrive at the cluster's barrier, go
+// on with the next round, and only then wait and add up a share of the tiles each. A block scales its slices of the rows by
+// itself.
+template <typename T, int G, int NT, bool SPLIT>
+__global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2)
+    k_w4_staged(int T_, int N, int K_all, const T* __restrict__ x, long long stride, const uint8_t* __restrict__ packed,
+                T* __restrict__ y, int per, int slice, int n_split) {
     constexpr int P = COLS<T>, WORDS = G / 16, PIECES = G / 32, C8 = NT * 8;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint32_t largest[TTS_BB_W4_MAX_TOKENS];
-    const int t0 = blockIdx.y * per, rows = min(per, T_ - t0), cols = rows * P, groups = K / G, tiles = (N + 15) / 16;
+    const int t0 = blockIdx.y * per, rows = min(per, T_ - t0), cols = rows * P, groups = K_all / G, tiles = (N + 15) / 16;
+    const int rank = SPLIT ? blockIdx.x % n_split : 0, team = SPLIT ? blockIdx.x / n_split : blockIdx.x;
+    const int teams = SPLIT ? gridDim.x / n_split : gridDim.x;
+    const int k0 = SPLIT ? min(rank * slice, K_all) : 0, K = SPLIT ? min(slice, K_all - k0) : K_all;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, q = lane & 3;
     uint4* const xs = reinterpret_cast<uint4*>(smem);
-    float* const red = reinterpret_cast<float*>(smem + (size_t)cols * K * 2);
+    float* const red = reinterpret_cast<float*>(smem + (size_t)cols * (SPLIT ? slice : K) * 2);
     if (tid < TTS_BB_W4_MAX_TOKENS) largest[tid] = 0u;
     pdl_wait();  // the weights too: the launch before may be the one that packs them
     pdl_trigger();
@@ -220,10 +129,12 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2) k_w4_staged(int T
     uint8_t* const ring = reinterpret_cast<uint8_t*>(red + 2 * WARPS * C8 * RED_ROW) + warp * STAGES * REC;
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
     // what comes next: its address, the records of the tile from it on, the tile; and its place in the ring
-    const int each = (groups - warp + WARPS - 1) / WARPS;  // records of a tile that are this warp's
-    int ahead_tile = each > 0 ? blockIdx.x : tiles, left = each;
-    const uint8_t* src = packed + ((size_t)blockIdx.x * groups + warp) * REC + lane * 16;
-    const long long jump = ((long long)gridDim.x * groups - (long long)each * WARPS) * REC;
+    constexpr int STEP = SPLIT ? 1 : WARPS, TILE_STEP = SPLIT ? WARPS : 1;
+    const int first = team * TILE_STEP + (SPLIT ? warp : 0), group0 = SPLIT ? k0 / G : warp;
+    const int each = SPLIT ? K / G : (groups - warp + WARPS - 1) / WARPS;  // records of a tile that are this warp's
+    int ahead_tile = each > 0 ? first : tiles, left = each;
+    const uint8_t* src = packed + ((size_t)first * groups + group0) * REC + lane * 16;
+    const long long jump = ((long long)teams * TILE_STEP * groups - (long long)each * STEP) * REC;
     uint32_t dst = ring_at + lane * 16;
     const uint32_t dst_end = ring_at + STAGES * REC;
     const auto fetch = [&] {
@@ -232,8 +143,8 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2) k_w4_staged(int T
             for (int i = 0; i < REC; i += 512)
                 if (i + 512 <= REC || lane * 16 < REC - i)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i), "l"(src + i) : "memory");
-            src += WARPS * REC;
-            if (--left == 0) { left = each; ahead_tile += gridDim.x; src += jump; }
+            src += STEP * REC;
+            if (--left == 0) { left = each; ahead_tile += teams * TILE_STEP; src += jump; }
         }
         dst += REC;
         if (dst >= dst_end) dst -= STAGES * REC;
@@ -248,7 +159,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2) k_w4_staged(int T
         uint32_t b = 0u;  // the bits of magnitudes order them, infinities and NaN above all
         if (u < rows * chunks) {
             float v[8];
-            load8(x + (size_t)(t0 + row) * stride + (u - row * chunks) * 8, v);
+            load8(x + (size_t)(t0 + row) * stride + k0 + (u - row * chunks) * 8, v);
 #pragma unroll
             for (int e = 0; e < 8; ++e) b = max(b, __float_as_uint(v[e]) & 0x7FFFFFFFu);
         }
@@ -266,7 +177,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2) k_w4_staged(int T
     for (int u = tid; u < rows * chunks; u += WARPS * 32) {
         const int row = u / chunks, chunk = u - row * chunks;
         float v[8];
-        load8(x + (size_t)(t0 + row) * stride + chunk * 8, v);
+        load8(x + (size_t)(t0 + row) * stride + k0 + chunk * 8, v);
         const float up = up_of(row);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= up;
@@ -285,16 +196,45 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2) k_w4_staged(int T
             xs[((g * PIECES + piece) * cols + row * P + part) * 4 + lane_q] = make_uint4(h[0], h[1], h[2], h[3]);
         }
     }
+    __shared__ float down[TTS_BB_W4_MAX_TOKENS];  // what takes a row's scaling back; an infinity or a NaN in the row: NaN
+    if (tid < rows) down[tid] = largest[tid] < 0x7F800000u ? 0x1p9f / up_of(tid) : __int_as_float(0x7FC00000);
     __syncthreads();
 
     int at[NT];  // this lane's column of each tile of 8; behind the last one, that one again: nobody reads its sums
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) at[nt] = min(nt * 8 + r, cols - 1) * 4 + q;
+    // waits for the cluster's sums of a round, adds up this block's share of it
+    const auto add_up = [&](int tile, int turn) {
+        cluster_wait();
+        const auto go = [&](auto split) {
+            constexpr int S = decltype(split)::value;
+            for (int i = rank * (WARPS * 32) + tid; i < WARPS * rows * 16; i += S * WARPS * 32) {
+                const int n = i & 15, row = (i >> 4) % rows, w = (i >> 4) / rows;
+                float part[P][S];
+#pragma unroll
+                for (int j = 0; j < P; ++j)
+#pragma unroll
+                    for (int s = 0; s < S; ++s)
+                        part[j][s] = peer(red + ((size_t)(turn * WARPS + w) * C8 + row * P + j) * RED_ROW + n, s);
+                float v = 0.f;
+#pragma unroll
+                for (int j = P - 1; j >= 0; --j)  // the small part first
+#pragma unroll
+                    for (int s = 0; s < S; ++s) v += part[j][s];
+                if ((tile + w) * 16 + n < N) y[(size_t)(t0 + row) * N + (tile + w) * 16 + n] = (T)v;
+            }
+        };
+        if (n_split == 2) go(std::integral_constant<int, 2>{});
+        else if (n_split == 4) go(std::integral_constant<int, 4>{});
+        else go(std::integral_constant<int, 8>{});
+    };
+    int last = 0, last_turn = 0;
     const uint8_t* rec = ring;  // the record at hand
-    for (int tile = blockIdx.x, turn = 0; tile < tiles; tile += gridDim.x, turn ^= 1) {
+    for (int tile = team * TILE_STEP, turn = 0; tile < tiles; tile += teams * TILE_STEP, turn ^= 1) {
         float acc[NT][4] = {};
-        const uint4* xg = xs + (size_t)warp * PIECES * cols * 4;
-        for (int g = 0; g < each; ++g, xg += (size_t)WARPS * PIECES * cols * 4) {
+        const uint4* xg = xs + (size_t)(SPLIT ? 0 : warp) * PIECES * cols * 4;
+        const int n_rec = !SPLIT || tile + warp < tiles ? each : 0;
+        for (int g = 0; g < n_rec; ++g, xg += (size_t)STEP * PIECES * cols * 4) {
             asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
             __syncwarp();
             fetch();  // into the place of the record before
@@ -311,95 +251,165 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2) k_w4_staged(int T
             }
             const uint32_t p0 = reinterpret_cast<const uint32_t*>(rec + G * 8)[r], p1 = reinterpret_cast<const uint32_t*>(rec + G * 8)[r + 8];
             const uint32_t z0 = __byte_perm(p0, 0u, 0x1010), z1 = __byte_perm(p1, 0u, 0x1010);
-            uint32_t a[WORDS][4];
-#pragma unroll
-            for (int i = 0; i < WORDS; ++i) {
-                const uint32_t w = cw[i], h = w >> 8;
-                // times 2^15 and 2^11
-                a[i][0] = fma_f16x2(w & 0x000F000Fu, 0x78007800u, z0);
-                a[i][1] = fma_f16x2(w & 0x00F000F0u, 0x68006800u, z1);
-                a[i][2] = fma_f16x2(h & 0x000F000Fu, 0x78007800u, z0);
-                a[i][3] = fma_f16x2(h & 0x00F000F0u, 0x68006800u, z1);
-            }
+            // times 2^15 and 2^11
+            const auto take = [&](uint32_t w, uint32_t (&a)[4]) {
+                const uint32_t h = w >> 8;
+                a[0] = fma_f16x2(w & 0x000F000Fu, 0x78007800u, z0);
+                a[1] = fma_f16x2(w & 0x00F000F0u, 0x68006800u, z1);
+                a[2] = fma_f16x2(h & 0x000F000Fu, 0x78007800u, z0);
+                a[3] = fma_f16x2(h & 0x00F000F0u, 0x68006800u, z1);
+            };
             const float s0 = __uint_as_float(p0 & 0xFFFF0000u), s1 = __uint_as_float(p1 & 0xFFFF0000u);
+            float d[NT][4] = {};
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                uint32_t a[2][4];
+                take(cw[2 * i], a[0]);
+                take(cw[2 * i + 1], a[1]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint4 b = xg[i * cols * 4 + at[nt]];
+                    mma_f16(d[nt], a[0], b.x, b.y);
+                    mma_f16(d[nt], a[1], b.z, b.w);
+                }
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float d[4] = {};
-#pragma unroll
-                for (int i = 0; i < PIECES; ++i) {
-                    const uint4 b = xg[i * cols * 4 + at[nt]];
-                    mma_f16(d, a[2 * i], b.x, b.y);
-                    mma_f16(d, a[2 * i + 1], b.z, b.w);
-                }
-                acc[nt][0] += s0 * d[0];
-                acc[nt][1] += s0 * d[1];
-                acc[nt][2] += s1 * d[2];
-                acc[nt][3] += s1 * d[3];
+                acc[nt][0] += s0 * d[nt][0];
+                acc[nt][1] += s0 * d[nt][1];
+                acc[nt][2] += s1 * d[nt][2];
+                acc[nt][3] += s1 * d[nt][3];
             }
             rec = rec + REC == ring + STAGES * REC ? ring : rec + REC;
         }
         float* const mine = red + (size_t)(turn * WARPS + warp) * C8 * RED_ROW;
+        if constexpr (SPLIT) {
+            if (tile != team * TILE_STEP) add_up(tile - teams * TILE_STEP, turn ^ 1);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mine[(nt * 8 + 2 * q + (e & 1)) * RED_ROW + r + (e >> 1) * 8] = acc[nt][e];
-        __syncthreads();
-        for (int i = tid; i < rows * 16; i += WARPS * 32) {
-            const int row = i >> 4, n = i & 15;
-            float v = 0.f;
+            for (int e = 0; e < 4; ++e) {
+                const int col = nt * 8 + 2 * q + (e & 1);
+                float v = acc[nt][e];
+                if constexpr (SPLIT) v *= down[min(col, cols - 1) / P];
+                mine[col * RED_ROW + r + (e >> 1) * 8] = v;
+            }
+        if constexpr (SPLIT) {
+            cluster_arrive();
+            last = tile;
+            last_turn = turn;
+        } else {
+            __syncthreads();
+            for (int i = tid; i < rows * 16; i += WARPS * 32) {
+                const int row = i >> 4, n = i & 15;
+                float v = 0.f;
 #pragma unroll
-            for (int part = P - 1; part >= 0; --part)  // the small part first
+                for (int part = P - 1; part >= 0; --part)  // the small part first
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w) v += red[((size_t)(turn * WARPS + w) * C8 + row * P + part) * RED_ROW + n];
-            // an infinity or a NaN in the row of x: NaN
-            const float f = largest[row] < 0x7F800000u ? 0x1p9f / up_of(row) : __int_as_float(0x7FC00000);
-            if (tile * 16 + n < N) y[(size_t)(t0 + row) * N + tile * 16 + n] = (T)(v * f);
+                    for (int w = 0; w < WARPS; ++w) v += red[((size_t)(turn * WARPS + w) * C8 + row * P + part) * RED_ROW + n];
+                if (tile * 16 + n < N) y[(size_t)(t0 + row) * N + tile * 16 + n] = (T)(v * down[row]);
+            }
         }
+    }
+    if constexpr (SPLIT) {
+        add_up(last, last_turn);
+        cluster_arrive();  // no block leaves while another reads its sums
+        cluster_wait();
     }
 }
 
-// x in shared memory where 8 columns of it, or all, leave room for two blocks an SM; in chunks of as many rows as do.
+// Blocks or clusters of a kernel that run at a time on the current device, asked once.
+struct Resident {
+    std::atomic<int> n[64];
+};
+template <typename K>
+int clusters_at_a_time(Resident& s, K* kernel, const cudaLaunchConfig_t& cfg) {
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    std::atomic<int>& kept = s.n[dev & 63];
+    if ((n = kept.load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return 1;
+    kept.store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// Room of two blocks an SM, of one, of three.
 constexpr size_t STAGED_MOST = 112 * 1024, STAGED_ONE = 220 * 1024, STAGED_THREE = 74 * 1024;
 
+int blocks_an_sm(size_t smem, int nt) { return smem > STAGED_MOST ? 1 : nt <= 2 && smem <= STAGED_THREE ? 3 : 2; }
+
+template <typename T, int G, bool SPLIT>
+void launch_staged(int T_, int N, int K, const T* x, int64_t stride, const uint8_t* w, T* y, int per, int n_split,
+                   cudaStream_t st) {
+    constexpr int P = COLS<T>;
+    const int tiles = (N + 15) / 16, groups = K / G, slice = (groups + n_split - 1) / n_split * G;
+    const int nt = tiles_for(per * P), chunks = (T_ + per - 1) / per;
+    const size_t smem = staged_bytes(per * P, slice, G);
+    const int fit = blocks_an_sm(smem, nt);
+    auto go = [&](auto k, int which) {
+        static SmemState state[3];
+        if (smem > 48 * 1024 - 512) allow_smem(state[which], k, STAGED_ONE);
+        cudaLaunchAttribute at[2];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = n_split;
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(n_split, chunks);
+        cfg.blockDim = WARPS * 32;
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cfg.attrs = at;
+        cfg.numAttrs = SPLIT ? 2 : 1;
+        if constexpr (SPLIT) {
+            // as many clusters as run at a time: with 19 of 8 blocks asked for and fewer resident, the last would wait for
+            // the first to end
+            static Resident resident[3][3][3];
+            const int at_a_time = clusters_at_a_time(resident[which][n_split == 2 ? 0 : n_split == 4 ? 1 : 2][fit - 1], k, cfg);
+            cfg.gridDim.x = n_split * std::min((tiles + WARPS - 1) / WARPS, std::max(1, at_a_time / chunks));
+        } else {
+            cfg.gridDim.x = std::min(tiles, std::max(1, 152 * fit / chunks));
+        }
+        cudaLaunchKernelEx(&cfg, k, T_, N, K, x, (long long)stride, w, y, per, slice, n_split);
+    };
+    if (nt == 1) go(k_w4_staged<T, G, 1, SPLIT>, 0);
+    else if (nt == 2) go(k_w4_staged<T, G, 2, SPLIT>, 1);
+    else go(k_w4_staged<T, G, 4, SPLIT>, 2);
+}
+
+// At most 32 columns at a time (64 in one pass over the weights spill or leave one block an SM: 64 rows x 4096 x 4096 fp32
+// 41 us, bf16 30; by 32 columns 26 and 19). Whether K is split:
+// - No, where a block has little to stage for each of its tiles: 1 x 4096 x 1024 3.1 us (split in 4: 3.6), 1 x 16384 x 4096
+//   10.5 (11.6).
+// - Else over as few blocks as give nearly every SM one, or more than two (between one and two, some SMs have twice the
+//   work of others): fp32 4 x 4096 x 4096 9.9 -> 6.2 us by 4, 8 x 1024 x 4096 13.0 -> 5.8 by 8, 8 x 8192 x 2048 11.0 -> 8.0
+//   by 2 (9.2 by 4), 4 x 16384 x 16384 56 by 2 -> 40 by 4. A single row of few tiles stays whole: 1 x 2048 x 8192 6.7 us,
+//   7.4 by 8.
+// - As many as two blocks an SM have room for, at most 8; in chunks of fewer rows where a slice is too long even then.
 template <typename T, int G>
 void launch(int T_, int N, int K, const void* x, int64_t stride, const void* packed, void* y, cudaStream_t st) {
+    constexpr int P = COLS<T>;
+    const auto bytes = [&](int per, int n) { return staged_bytes(per * P, (K / G + n - 1) / n * G, G); };
+    int per = std::min(T_, MOST_COLS / P), n = 1;
+    const int tiles = (N + 15) / 16, rounds = (tiles + WARPS - 1) / WARPS, chunks = (T_ + per - 1) / per;
+    const int blocks = std::min(tiles, std::max(1, 152 * blocks_an_sm(bytes(per, 1), tiles_for(per * P)) / chunks));
+    const long long stage_a_tile = (long long)per * K * blocks / tiles;
+    if (stage_a_tile >= 4500 && (T_ > 1 || rounds >= 32)) {
+        const auto uneven = [&](long long b) { return b < 128 || (b > 152 && b <= 304); };
+        for (n = 2; n < 8 && 2 * n <= K / G && uneven((long long)rounds * n * chunks);) n *= 2;
+    }
+    while (n < 8 && bytes(per, n) > STAGED_MOST) n *= 2;
+    while (per > 1 && bytes(per, n) > STAGED_ONE) per = (per + 1) / 2;
     const T* const xt = static_cast<const T*>(x);
     const uint8_t* const w = static_cast<const uint8_t*>(packed);
-    T* const yt = static_cast<T*>(y);
-    const int tiles = (N + 15) / 16;
-    {
-        constexpr int P = COLS<T>;
-        int per = std::min(T_, 64 / P);
-        while (per * P > 8 && staged_bytes(per * P, K, G) > STAGED_MOST) per = std::max(8 / P, per / 2);
-        const size_t smem = staged_bytes(per * P, K, G);
-        if (smem <= STAGED_ONE) {
-            const int nt = tiles_for(per * P), chunks = (T_ + per - 1) / per;
-            const int fit = smem > STAGED_MOST ? 1 : nt <= 2 && smem <= STAGED_THREE ? 3 : 2;  // blocks an SM
-            const int blocks = std::min(tiles, std::max(1, 152 * fit / chunks));
-            auto go = [&](auto k, SmemState& s) {
-                if (smem > 48 * 1024 - 512) allow_smem(s, k, STAGED_ONE);
-                launch_pdl(k, dim3(blocks, chunks), WARPS * 32, smem, st, T_, N, K, xt, (long long)stride, w, yt, per);
-            };
-            static SmemState state[4];
-            if (nt == 1) go(k_w4_staged<T, G, 1>, state[0]);
-            else if (nt == 2) go(k_w4_staged<T, G, 2>, state[1]);
-            else if (nt == 4) go(k_w4_staged<T, G, 4>, state[2]);
-            else go(k_w4_staged<T, G, 8>, state[3]);
-            return;
-        }
-    }
-    constexpr int P = PARTS<T>;
-    const int per = std::min(T_, 64 / P), nt = tiles_for(per * P);
-    const dim3 grid(tiles, (T_ + per - 1) / per);
-    auto go = [&](auto k) { launch_pdl(k, grid, WARPS * 32, 0, st, T_, N, K, xt, (long long)stride, w, yt, per); };
-    if (nt == 1) go(k_w4_linear<T, G, 1>);
-    else if (nt == 2) go(k_w4_linear<T, G, 2>);
-    else if (nt == 4) go(k_w4_linear<T, G, 4>);
-    else go(k_w4_linear<T, G, 8>);
+    if (n == 1) launch_staged<T, G, false>(T_, N, K, xt, stride, w, static_cast<T*>(y), per, n, st);
+    else launch_staged<T, G, true>(T_, N, K, xt, stride, w, static_cast<T*>(y), per, n, st);
 }
 
 bool sizes_ok(int N, int K, int G) {
-    return N >= 1 && N <= (1 << 20) && (G == 32 || G == 64 || G == 128) && K >= G && K % G == 0 && K <= (1 << 20);
+    return N >= 1 && N <= (1 << 20) && (G == 32 || G == 64 || G == 128) && K >= G && K % G == 0 && K <= (1 << 18);
 }
 
 }  // namespace

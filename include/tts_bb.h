@@ -591,15 +591,16 @@ tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S, const 
  *   codes   uint8 [N][K / 2]: code 2 i in the low, 2 i + 1 in the high nibble of byte i
  *   scales  bf16 [N][K / group]
  *   zeros   uint8 [N][K / group], 0..15, or NULL: 8 everywhere (above 15: taken modulo 16)
- * group 32, 64 or 128; K a multiple of group; N >= 1, K >= group. */
+ * group 32, 64 or 128; K a multiple of group, at most 2^18; N at most 2^20. */
 #define TTS_BB_W4_MAX_TOKENS 64
 size_t tts_bb_w4_packed_bytes(int N, int K, int group);
 tts_bb_status tts_bb_w4_pack(int N, int K, int group, const void* codes, const void* scales, const void* zeros,
                              void* packed, void* stream);
 /*   x  fp32 or bf16 (type) [T] rows of K, x_stride elements apart (>= K, and 16-byte aligned rows)
  *   y  fp32 or bf16 (the same type) [T][N], 4- or 2-byte aligned
- * Products are exact (fp32 rows of x enter as three bf16 parts) and summed in fp32, in an order that depends
- * on the sizes alone. */
+ * A row of x enters to within half an fp32 step of each value, or 2^-39 of the row's largest magnitude where that is
+ * more; products are exact and summed in fp32, in an order that depends on the sizes alone. An infinity or a NaN
+ * in a row of x makes that row of y NaN. */
 tts_bb_status tts_bb_w4_linear(int T, int N, int K, int group, const void* x, int type, int64_t x_stride,
                                const void* packed, void* y, void* stream);
 

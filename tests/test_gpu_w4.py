@@ -137,9 +137,10 @@ def test_two_streams_and_a_captured_graph():
 
 
 @pytest.mark.parametrize("io", ["float32", "bfloat16"])
-@pytest.mark.parametrize("N,K,G,T", [(70, 8192, 128, 5), (33, 16384, 64, 9), (16, 4096, 32, 64), (17, 16384, 128, 40), (5000, 256, 64, 2), (9000, 64, 32, 1)])
+@pytest.mark.parametrize("N,K,G,T", [(70, 8192, 128, 5), (33, 16384, 64, 9), (16, 4096, 32, 64), (17, 16384, 128, 40), (5000, 256, 64, 2), (9000, 64, 32, 1),
+                                         (300, 4224, 128, 64), (40, 65536, 128, 3), (2100, 4096, 64, 33), (16, 262144, 128, 1), (17, 3168, 32, 64)])
 def test_many_and_long_rows_of_x(N, K, G, T, io):
-    """Rows of x staged in chunks, rows too long to be staged at all, and more tiles than blocks."""
+    """Rows of x in slices of a cluster's blocks, uneven ones too, and in chunks; more tiles than blocks."""
     run(N, K, G, T, io, True)
 
 
