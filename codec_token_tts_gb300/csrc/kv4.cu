@@ -559,16 +559,21 @@ __global__ void __launch_bounds__(256) k_kv4_read(int T, const int32_t* __restri
 }
 
 // ---------------------------------------------------------------- attention
+// A row is a query token, or two tokens of a sequence that follow one another (the last of an odd number alone).
 struct AttnArgs {
     const int32_t* seqs;
     const int32_t* kv_lens;
-    int S, max_len, rows, n_splits;
+    int S, max_len;
+    int each, per_seq, rows;  // query tokens of a row, rows of a sequence, rows in all
+    int n_splits;
     float* part;  // pieces: 128 output sums, reference, sum of weights
+    __device__ __forceinline__ int token(int r) const { return r / per_seq * S + r % per_seq * each; }     // its first
+    __device__ __forceinline__ bool two(int r) const { return each == 2 && 2 * (r % per_seq) + 1 < S; }
 };
 
-// Row r = (b, s): the cache row it reads and the keys it sees; false where the row is left as it was.
+// Row r: the cache row it reads and the keys its last token sees; false where the row is left as it was.
 __device__ __forceinline__ bool attn_row(const Cache& c, const AttnArgs& a, int r, bool report, int& seq, int& seen) {
-    const int b = r / a.S, s = r - b * a.S;
+    const int b = r / a.per_seq, s = min((r - b * a.per_seq + 1) * a.each, a.S) - 1;
     seq = a.seqs ? a.seqs[b] : b;
     if (seq < 0) return false;
     int len = a.kv_lens[b];
@@ -603,6 +608,11 @@ __device__ __forceinline__ bool attn_row(const Cache& c, const AttnArgs& a, int 
 // exact in 8 bits: whole numbers around zero, not 0..15 with a middle added later, because where a softmax is flat the
 // sums cancel and a common offset would cost their digits. P times V's scale of the key and group is B, as bf16 parts by
 // truncation (bf16: two, 16 bits; fp32: three, all 24) in columns of their own.
+//
+// Two query tokens that follow one another (N = 2, bf16): the columns that one token only repeats are the second one's, query
+// c & 1 in a lane, which then has both of 16 keys' scores r and r + 8 of its head. Codes are taken apart once for both: 8
+// sequences of 8 tokens and 2000 keys 28 -> 19 us, 64 of 2 and 1000 keys 25 -> 18. The first token does not see the
+// second's key: its weight is 0 there. (fp32 has no column left: three parts of a weight by two heads are six of eight.)
 //
 // Softmax: a running reference m for each head, moved only when a score exceeds it by 8 (log2): then sums and O are
 // rescaled. It starts at -1e30, not -inf, so that no difference of infinities arises.
@@ -690,15 +700,16 @@ __device__ __forceinline__ void cluster_sync() {
 
 // What a block has in common for its pieces
 struct Shared {
-    __half q[2][2][HD];
-    float about[2][4];
-    float m[WARPS][2], l[WARPS][2];
+    __half q[2][2][HD];  // [part or query][head]
+    float about[4][4];   // of head h of query j at 2 j + h, here and below
+    float m[WARPS][4], l[WARPS][4];
 };
 
-// One piece: the cache blocks [b0, b1) of KV head g of a row that reads cache row seq and sees `seen` keys; q: its two heads.
+// One piece: the cache blocks [b0, b1) of KV head g of a row that reads cache row seq and whose last token sees `seen` keys;
+// q: its two heads; gap: 1 where there is a second token, whose heads are NQ rows further and which sees one key more.
 template <typename T> struct Piece {
     const T* q;
-    int seq, seen, g, b0, b1;
+    int seq, seen, gap, g, b0, b1;
     // units of a warp: unit i is keys 32 (warp & 1) .. + 31 of block b0 + (warp >> 1) + 2 i
     __device__ __forceinline__ int units(int warp) const { return max(0, (b1 - b0 - (warp >> 1) + 1) >> 1); }
     __device__ __forceinline__ const int32_t* pages(const Cache& c, int warp) const {
@@ -741,41 +752,45 @@ __device__ __forceinline__ void start_piece(const Piece<T>& p, const Cache& cach
     asm volatile("cp.async.commit_group;" ::: "memory");
     a.page = n > 1 ? p.pages(cache, warp)[2] : 0;
 }
-template <typename T>
+template <int N, typename T>
 __device__ __forceinline__ void load_queries(const Piece<T>& p, Ahead& a) {
-    if (threadIdx.x < 64) a.q = load4(p.q + threadIdx.x * 4);  // warps 0, 1: a head each
+    // a head a warp; the second token's by warps 2, 3 (where there is none, the first's again, and nobody reads the results)
+    if (threadIdx.x < 64 * N) a.q = load4(p.q + (threadIdx.x >> 6) * p.gap * (NQ * HD) + (threadIdx.x & 63) * 4);
 }
 
 // A piece that is started already; the next one (where more) is started before the warps' results are merged, so that its
 // keys come meanwhile. Thread d ends with the piece's reference M, sum of weights L and output sums O of dim d of both
-// heads. All threads of the block call it, with the same arguments; `so` is free again when the next call has merged.
-template <typename T>
+// heads of each of the N query tokens. All threads of the block call it, with the same arguments; `so` is free again when the next call has merged.
+template <typename T, int N>
 __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const Piece<T>& next, const Cache& cache, uint8_t* ring, float* so,
-                                             Shared& sh, Ahead& ahead, float (&M)[2], float (&L)[2], float (&O)[2]) {
+                                             Shared& sh, Ahead& ahead, float (&M)[2 * N], float (&L)[2 * N], float (&O)[2 * N]) {
     constexpr bool F32 = sizeof(T) == 4;
+    static_assert(N == 1 || !F32, "columns");
     constexpr int P = F32 ? 3 : 2;  // bf16 parts of a weight
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int seen = p.seen, j0 = p.b0 + (warp >> 1), n = p.units(warp);
     uint8_t* const mine = ring + warp * STAGES * UNIT_BYTES;
     const int32_t* const pages = p.pages(cache, warp);
 
-    if (warp < 2) stage_q<F32 ? 2 : 1>(ahead.q, lane, sh.q[0][warp], sh.about[warp]);
+    if (warp < 2 * N) stage_q<F32 ? 2 : 1>(ahead.q, lane, sh.q[warp >> 1][warp & 1], sh.about[warp]);
     __syncthreads();
     int next_page = 0;
     if (more) {
         if (next.units(warp) > 0) next_page = next.pages(cache, warp)[0];
-        load_queries(next, ahead);
+        load_queries<N>(next, ahead);
     }
     uint4 qb[4];       // of word w: the B registers of its two steps
-    const float qsum[2] = {sh.about[c >> 1][0], sh.about[c >> 1][1]};
-    const float factor = sh.about[c >> 1][2];
+    const int hq = N == 1 ? c >> 1 : (c >> 1) + 2 * (c & 1);  // this lane's head (and query)
+    const float qsum[2] = {sh.about[hq][0], sh.about[hq][1]};
+    const float factor = sh.about[hq][2];
 #pragma unroll
     for (int w = 0; w < 4; ++w)
-        qb[w] = *reinterpret_cast<const uint4*>(&sh.q[F32 ? r >> 1 & 1 : 0][r & 1][64 * (w & 1) + 16 * c + 8 * (w >> 1)]);
+        qb[w] = *reinterpret_cast<const uint4*>(&sh.q[F32 || N == 2 ? r >> 1 & 1 : 0][r & 1][64 * (w & 1) + 16 * c + 8 * (w >> 1)]);
     const uint32_t m1 = r >= 2 ? 0xFFFF0000u : 0u, m2 = r >= 4 ? 0xFFFF0000u : 0u;
-    const uint32_t half_sel = r & 2 ? 0x5410u : 0x7632u;  // bf16: part 0 in the high halves, part 1 in the low ones
-    const int from = 4 * c + 2 * (r & 1);                 // the lane that has the weight of key c of this column's head
-    const int my = r + 8 * (c & 1);                       // this lane's key of 16; its head is c >> 1
+    const uint32_t half_sel = r & (N == 1 ? 2 : 4) ? 0x5410u : 0x7632u;  // bf16: part 0 in the high halves, part 1 in the low ones
+    const int from = 4 * c + 2 * (r & 1) + (N == 1 ? 0 : r >> 1 & 1);    // the lane that has the weight of key c of this column
+    const int my = N == 1 ? r + 8 * (c & 1) : r;                         // this lane's key of 16 (the first; the second 8 behind)
+    const int sees = seen - (N == 2 && !(c & 1) ? p.gap : 0);
     const uint8_t* const kat = mine + r * 64 + c * 16;
     const uint8_t* const vat = mine + V_AT + c * 64 + (r * 8 ^ (c >> 1) * 32);
     float o[8][4] = {}, m = M_START, l = 0.f;
@@ -784,11 +799,13 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
     auto step = [&](auto tail, const int at, const int par, const int key0) {
         constexpr bool TAIL = decltype(tail)::value;
 
-        float z;
+        float z[N];
         {
             const uint4 k0 = *reinterpret_cast<const uint4*>(kat + at);
             const uint4 k1 = *reinterpret_cast<const uint4*>(kat + at + 512);
-            const uint2 kp = *reinterpret_cast<const uint2*>(mine + par + KP_AT + my * 8);
+            uint2 kp[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) kp[j] = *reinterpret_cast<const uint2*>(mine + par + KP_AT + my * 8 + j * 64);
             const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
             [[maybe_unused]] uint32_t kz[2][2] = {};  // fp32: zero 2^-9 of keys r, r + 8 and each group, twice
             if constexpr (F32) {
@@ -818,25 +835,33 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
                 mma_f16(s[w & 1], x, qb[w].x, qb[w].y);
                 mma_f16(s[w & 1], y, qb[w].z, qb[w].w);
             }
-            float y[2];  // this lane's key and head: sums e = 2 (key r + 8) + head
+            // this lane's keys and head: sums e = 2 (key r + 8) + head
 #pragma unroll
-            for (int gr = 0; gr < 2; ++gr) {
-                const float a0 = c & 2 ? s[gr][1] : s[gr][0], a1 = c & 2 ? s[gr][3] : s[gr][2];
-                y[gr] = c & 1 ? a1 : a0;
-                if (F32) y[gr] += __shfl_xor_sync(0xffffffffu, c & 1 ? a0 : a1, 1);  // the other part's sum
+            for (int j = 0; j < N; ++j) {
+                float y[2];
+#pragma unroll
+                for (int gr = 0; gr < 2; ++gr) {
+                    const float a0 = c & 2 ? s[gr][1] : s[gr][0], a1 = c & 2 ? s[gr][3] : s[gr][2];
+                    y[gr] = N == 2 ? (j ? a1 : a0) : c & 1 ? a1 : a0;
+                    if (F32) y[gr] += __shfl_xor_sync(0xffffffffu, c & 1 ? a0 : a1, 1);  // the other part's sum
+                }
+                if (!F32) {
+                    y[0] += zero_of(kp[j].x) * qsum[0];
+                    y[1] += zero_of(kp[j].y) * qsum[1];
+                }
+                z[j] = scale_of(kp[j].x) * y[0] + scale_of(kp[j].y) * y[1];
+                z[j] *= factor;
             }
-            if (!F32) {
-                y[0] += zero_of(kp.x) * qsum[0];
-                y[1] += zero_of(kp.y) * qsum[1];
-            }
-            z = scale_of(kp.x) * y[0] + scale_of(kp.y) * y[1];
-            z *= factor;
         }
-        const bool on = !TAIL || key0 + my < seen;
-        if (!on) z = -INFINITY;
-        if (__any_sync(0xffffffffu, z > m + M_SLACK)) {
-            float mx = z;
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        bool on[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            on[j] = !TAIL || key0 + my + 8 * j < sees;
+            if (!on[j]) z[j] = -INFINITY;
+        }
+        if (__any_sync(0xffffffffu, z[0] > m + M_SLACK || z[N - 1] > m + M_SLACK)) {
+            float mx = fmaxf(z[0], z[N - 1]);
+            if (N == 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -851,36 +876,43 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
             }
         }
         {
-            const float p = ex2(z - m);
-            l += p;
-            const uint2 vp = *reinterpret_cast<const uint2*>(mine + par + VP_AT + my * 8);
-            float ps[2] = {p * scale_of(vp.x), p * scale_of(vp.y)};
+            float ps[N][2];
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float p = ex2(z[j] - m);
+                l += p;
+                const uint2 vp = *reinterpret_cast<const uint2*>(mine + par + VP_AT + my * 8 + j * 64);
+                ps[j][0] = p * scale_of(vp.x);
+                ps[j][1] = p * scale_of(vp.y);
+                if (TAIL && !on[j]) ps[j][0] = ps[j][1] = 0.f;  // parameters behind the keys may be anything
+            }
             uint2 w[4], pp[4];  // codes and parameters of keys c, c + 4, c + 8, c + 12
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 w[k] = *reinterpret_cast<const uint2*>(vat + at + k * 256);
                 pp[k] = *reinterpret_cast<const uint2*>(mine + par + VP_AT + c * 8 + k * 32);
             }
-            if constexpr (TAIL) {  // parameters behind the keys may be anything: no scale or offset that is not finite times a zero
-                if (!on) ps[0] = ps[1] = 0.f;
+            if constexpr (TAIL) {  // nor an offset that is not finite times a zero
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     if (key0 + c + 4 * k >= seen) pp[k] = make_uint2(0u, 0u);
             }
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr) {
-                const float x = ps[gr];
                 uint32_t y[4], b0, b1;
                 if constexpr (F32) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        y[k] = part_of(__shfl_sync(0xffffffffu, x, from + (k & 1) * 16 + (k >> 1)), m1, m2);
+                        y[k] = part_of(__shfl_sync(0xffffffffu, ps[0][gr], from + (k & 1) * 16 + (k >> 1)), m1, m2);
                     b0 = highs(y[0], y[1]);
                     b1 = highs(y[2], y[3]);
                 } else {
-                    const uint32_t both = highs(as_u(x - as_f(as_u(x) & 0xFFFF0000u)), as_u(x));  // part 1 below part 0
+                    uint32_t both[N];  // part 1 below part 0
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) y[k] = __shfl_sync(0xffffffffu, both, from + (k & 1) * 16 + (k >> 1));
+                    for (int j = 0; j < N; ++j) both[j] = highs(as_u(ps[j][gr] - as_f(as_u(ps[j][gr]) & 0xFFFF0000u)), as_u(ps[j][gr]));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        y[k] = __shfl_sync(0xffffffffu, both[N == 2 ? k >> 1 : 0], from + (k & 1) * 16 + (N == 1 ? k >> 1 : 0));
                     b0 = __byte_perm(y[0], y[1], half_sel);
                     b1 = __byte_perm(y[2], y[3], half_sel);
                 }
@@ -915,12 +947,12 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
 #pragma unroll 1
         for (int u = 0; u < 2; ++u) {
             const int k = key0 + 16 * u;
-            if (k + 16 <= seen) step(std::false_type{}, at + 1024 * u, at + 128 * u, k);
+            if (k + 16 <= seen - (N == 2 ? p.gap : 0)) step(std::false_type{}, at + 1024 * u, at + 128 * u, k);
             else if (k < seen) step(std::true_type{}, at + 1024 * u, at + 128 * u, k);
         }
     }
-    // merge the warps: every part of O to shared memory (so: [warp][part][head][128]), then one thread for each dim
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    // merge the warps: every part of O to shared memory (so: [warp][part][query][head][128]), then one thread for each dim
+    if (N == 1) l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 4);
     l += __shfl_xor_sync(0xffffffffu, l, 8);
     l += __shfl_xor_sync(0xffffffffu, l, 16);
@@ -928,21 +960,22 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
         __syncwarp();  // the warp's ring is free
         start_piece(next, cache, ring, next_page, ahead);
     }
-    if (c < P) {
+    if (N == 2 || c < P) {
+        const int at = N == 1 ? warp * P + c : (warp * P + (c >> 1)) * 2 + (c & 1);
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             const int d = 64 * (t >> 2) + 8 * r + 2 * (t & 3);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<float2*>(so + ((warp * P + c) * 2 + h) * HD + d) =
+                *reinterpret_cast<float2*>(so + (at * 2 + h) * HD + d) =
                     make_float2(o[t][h] * 128.f, o[t][2 + h] * 128.f);
         }
     }
-    if (lane == 0 || lane == 2) { sh.m[warp][lane >> 1] = m; sh.l[warp][lane >> 1] = l; }
+    if (lane < 4 && (N == 2 || !(lane & 1))) { sh.m[warp][hq] = m; sh.l[warp][hq] = l; }
     __syncthreads();
     const int d = threadIdx.x;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2 * N; ++h) {
         M[h] = M_START;
         L[h] = O[h] = 0.f;
 #pragma unroll
@@ -952,7 +985,7 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
             const float f = ex2(sh.m[w][h] - M[h]);
             float x = 0.f;
 #pragma unroll
-            for (int part = P - 1; part >= 0; --part) x += so[((w * P + part) * 2 + h) * HD + d];
+            for (int part = P - 1; part >= 0; --part) x += so[((w * P + part) * 2 * N + h) * HD + d];
             L[h] += f * sh.l[w][h];
             O[h] += f * x;
         }
@@ -961,7 +994,7 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
 
 // grid (splits, 8, rows): one piece a block, the blocks of a row's keys dealt evenly to its splits. The splits of a (row,
 // head) are one cluster (at most 8), which merges them through its shared memory.
-template <typename T>
+template <typename T, int N>
 __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict__ q, Cache cache, AttnArgs a, T* __restrict__ out) {
     pdl_wait();  // upstream results are read below
     pdl_trigger();
@@ -971,26 +1004,30 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict_
     int seq, seen;
     if (!attn_row(cache, a, row, d == 0 && split == 0 && g == 0, seq, seen)) return;
     const int nblk = (seen + KVB - 1) / KVB, bps = (nblk + a.n_splits - 1) / a.n_splits;
-    float M[2], L[2], O[2];
-    const Piece<T> p = {q + ((size_t)row * NQ + 2 * g) * HD, seq, seen, g, split * bps, min(nblk, (split + 1) * bps)};
+    float M[2 * N], L[2 * N], O[2 * N];
+    const int gap = N == 2 && a.two(row);
+    const size_t token = N == 1 ? row : a.token(row);
+    const Piece<T> p = {q + (token * NQ + 2 * g) * HD, seq, seen, gap, g, split * bps, min(nblk, (split + 1) * bps)};
     Ahead ahead;
-    load_queries(p, ahead);
+    load_queries<N>(p, ahead);
     start_piece(p, cache, ring, p.units(d >> 5) > 0 ? p.pages(cache, d >> 5)[0] : 0, ahead);
-    attend_piece(p, false, p, cache, ring, reinterpret_cast<float*>(ring + RING_BYTES), sh, ahead, M, L, O);
-    T* const to = out + ((size_t)row * NQ + 2 * g) * HD;
+    attend_piece<T, N>(p, false, p, cache, ring, reinterpret_cast<float*>(ring + RING_BYTES), sh, ahead, M, L, O);
+    T* const to = out + (token * NQ + 2 * g) * HD;
+    const int heads = N == 1 ? 2 : 2 + 2 * gap;
     if (a.n_splits == 1) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) to[h * HD + d] = (T)(L[h] == 0.f ? 0.f : O[h] / L[h]);
+        for (int h = 0; h < 2 * N; ++h)
+            if (h < heads) to[((h >> 1) * NQ + (h & 1)) * HD + d] = (T)(L[h] == 0.f ? 0.f : O[h] / L[h]);
         return;
     }
-    __shared__ float all[2][HD], ml[2][2];
+    __shared__ float all[2 * N][HD], ml[2 * N][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2 * N; ++h) {
         all[h][d] = O[h];
         if (d == 0) { ml[h][0] = M[h]; ml[h][1] = L[h]; }
     }
     cluster_sync();
-    for (int i = split * WARPS * 32 + d; i < 2 * HD; i += a.n_splits * WARPS * 32) {
+    for (int i = split * WARPS * 32 + d; i < heads * HD; i += a.n_splits * WARPS * 32) {
         const int h = i / HD;
         float m1 = M_START, l1 = 0.f, o1 = 0.f;
         for (int s = 0; s < a.n_splits; ++s) m1 = fmaxf(m1, peer(&ml[h][0], s));
@@ -999,7 +1036,7 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict_
             l1 += f * peer(&ml[h][1], s);
             o1 += f * peer(&all[h][i % HD], s);
         }
-        to[i] = (T)(l1 == 0.f ? 0.f : o1 / l1);
+        to[((h >> 1) * NQ + (h & 1)) * HD + i % HD] = (T)(l1 == 0.f ? 0.f : o1 / l1);
     }
     cluster_sync();  // no block leaves while another reads its sums
 }
@@ -1020,13 +1057,14 @@ __device__ __forceinline__ Line line_of(long long blocks, int shares) {
     const long long u = blocks * NKV;
     return {u, max(2, (int)((u + shares - 1) / shares))};
 }
-// the place of a piece: [share][first, last][2 heads][128 sums, reference, weight]
+// the place of a piece: [share][first, last][N queries][2 heads][128 sums, reference, weight]
 constexpr int PIECE = HD + 4;  // 16-byte rows
-__device__ __forceinline__ float* place(float* part, int share, int which) { return part + ((size_t)share * 2 + which) * 2 * PIECE; }
+template <int N>
+__device__ __forceinline__ float* place(float* part, int share, int which) { return part + ((size_t)share * 2 + which) * 2 * N * PIECE; }
 
 // grid: the shares (at most SLOTS); rows <= LINE_ROWS
 constexpr int LINE_ROWS = 1024;
-template <typename T>
+template <typename T, int N>
 __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn_line(const T* __restrict__ q, Cache cache, AttnArgs a, T* __restrict__ out) {
     pdl_wait();  // upstream results are read below
     pdl_trigger();
@@ -1084,7 +1122,7 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn_line(const T* __rest
         // the piece from `at` of the row on; then the place behind it
         const auto take = [&](Piece<T>& p, int& piece_row, bool& whole) {
             const int nblk = (seen + KVB - 1) / KVB, g = at / nblk, b0 = at - g * nblk, b1 = min(nblk, b0 + left);
-            p = {q + ((size_t)row * NQ + 2 * g) * HD, seq, seen, g, b0, b1};
+            p = {q + ((size_t)(N == 1 ? row : a.token(row)) * NQ + 2 * g) * HD, seq, seen, N == 2 && a.two(row), g, b0, b1};
             piece_row = row;
             whole = b0 == 0 && b1 == nblk;
             left -= b1 - b0;
@@ -1101,20 +1139,23 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn_line(const T* __rest
         bool whole, next_whole = false, begins = true;  // the share's first piece
         take(p, piece_row, whole);
         Ahead ahead;
-        load_queries(p, ahead);
+        load_queries<N>(p, ahead);
         start_piece(p, cache, ring, p.units(warp) > 0 ? p.pages(cache, warp)[0] : 0, ahead);
         for (bool more = true; more;) {
             more = left > 0;
             if (more) take(next, next_row, next_whole);
-            float M[2], L[2], O[2];
-            attend_piece(p, more, next, cache, ring, reinterpret_cast<float*>(ring + RING_BYTES), sh, ahead, M, L, O);
+            float M[2 * N], L[2 * N], O[2 * N];
+            attend_piece<T, N>(p, more, next, cache, ring, reinterpret_cast<float*>(ring + RING_BYTES), sh, ahead, M, L, O);
             if (whole) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) out[((size_t)piece_row * NQ + 2 * p.g + h) * HD + d] = (T)(L[h] == 0.f ? 0.f : O[h] / L[h]);
+                for (int h = 0; h < 2 * N; ++h)
+                    if (h < 2 || p.gap)
+                        out[((size_t)((N == 1 ? piece_row : a.token(piece_row)) + (h >> 1)) * NQ + 2 * p.g + (h & 1)) * HD + d] =
+                            (T)(L[h] == 0.f ? 0.f : O[h] / L[h]);
             } else {
-                float* const to = place(a.part, me, begins ? 0 : 1);
+                float* const to = place<N>(a.part, me, begins ? 0 : 1);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < 2 * N; ++h) {
                     to[h * PIECE + d] = O[h];
                     if (d == 0) { to[h * PIECE + HD] = M[h]; to[h * PIECE + HD + 1] = L[h]; }
                 }
@@ -1129,20 +1170,21 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn_line(const T* __rest
     for (int i = me; i < a.rows; i += gridDim.x) {
         int seq, seen;
         if (attn_row(cache, a, i, false, seq, seen) && seen == 0)
-            for (int e = d; e < NQ * HD; e += WARPS * 32) out[(size_t)i * NQ * HD + e] = (T)0.f;
+            for (int e = d; e < (N == 2 && a.two(i) ? 2 : 1) * NQ * HD; e += WARPS * 32)
+                out[(size_t)(N == 1 ? i : a.token(i)) * NQ * HD + e] = (T)0.f;
     }
 }
 
-// grid (16, rows), 128 threads: the pieces of a (row, query head) that lies in several shares. Warp w sums pieces w, w + 4, ..., lane l
+// grid (16 N, rows), 128 threads: the pieces of a (row, query, head) that lies in several shares. Warp w sums pieces w, w + 4, ..., lane l
 // dims 4l .. 4l + 3, all weighted to the largest reference; then the warps' sums are added in their order.
-template <typename T>
+template <typename T, int N>
 __global__ void __launch_bounds__(128) k_kv4_combine(Cache c, AttnArgs a, int shares, T* __restrict__ out) {
     pdl_wait();  // upstream results are read below
     pdl_trigger();
     __shared__ long long sums[2][4];
     __shared__ float4 part[4][32];
     __shared__ float weight[4];
-    const int g = blockIdx.x >> 1, h = blockIdx.x & 1, row = blockIdx.y, d = threadIdx.x, warp = d >> 5, lane = d & 31;
+    const int g = blockIdx.x / (2 * N), h = blockIdx.x % (2 * N), row = blockIdx.y, d = threadIdx.x, warp = d >> 5, lane = d & 31;
     long long before = 0, total = 0;
     for (int i = d; i < a.rows; i += 128) {
         const int n = row_blocks(c, a, i, false);
@@ -1160,12 +1202,12 @@ __global__ void __launch_bounds__(128) k_kv4_combine(Cache c, AttnArgs a, int sh
     total = sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3];
     const Line line = line_of(total, shares);
     const int nblk = row_blocks(c, a, row, false);
-    if (nblk == 0) return;
+    if (nblk == 0 || (h >= 2 && !a.two(row))) return;
     const long long from = before * NKV + (long long)g * nblk;
     const int s0 = (int)(from / line.share), n = (int)((from + nblk - 1) / line.share) - s0 + 1;
     if (n == 1) return;  // written by its share
     const bool inside = from != (long long)s0 * line.share;  // the first piece ends its share
-    auto at = [&](int i) { return place(a.part, s0 + i, i == 0 && inside) + h * PIECE; };
+    auto at = [&](int i) { return place<N>(a.part, s0 + i, i == 0 && inside) + h * PIECE; };
     float M = M_START;
     for (int i = lane; i < n; i += 32) M = fmaxf(M, at(i)[HD]);
     M = warp_max(M);
@@ -1185,7 +1227,7 @@ __global__ void __launch_bounds__(128) k_kv4_combine(Cache c, AttnArgs a, int sh
     const float* const s = reinterpret_cast<const float*>(part);
     L = weight[0] + weight[1] + weight[2] + weight[3];
     const float O = s[d] + s[HD + d] + s[2 * HD + d] + s[3 * HD + d];
-    out[((size_t)row * NQ + blockIdx.x) * HD + d] = (T)(L == 0.f ? 0.f : O / L);
+    out[((size_t)((N == 1 ? row : a.token(row)) + (h >> 1)) * NQ + 2 * g + (h & 1)) * HD + d] = (T)(L == 0.f ? 0.f : O / L);
 }
 
 constexpr int MAX_CLUSTER = 8, SLOTS = 4 * 152;
@@ -1303,8 +1345,10 @@ TTS_API tts_bb_status tts_bb_kv4_read(const tts_bb_kv4* cache, int T, const int3
 
 TTS_API size_t tts_bb_kv4_attention_workspace(int B, int S, int max_len) {
     if (B < 1 || S < 1 || S > TTS_BB_KV4_MAX_QUERIES || max_len < 1 || (long long)B * S > 65535) return 0;
-    const Plan p = attn_plan((long long)B * S, max_len);
-    return (size_t)p.shares * 2 * 2 * PIECE * sizeof(float);
+    size_t most = 0;
+    for (int each = 1; each <= std::min(S, 2); ++each)
+        most = std::max(most, (size_t)attn_plan((long long)B * ((S + each - 1) / each), max_len).shares * 2 * 2 * each * PIECE * sizeof(float));
+    return most;
 }
 
 TTS_API tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S, const void* q, int type,
@@ -1318,27 +1362,31 @@ TTS_API tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S
     if (need && (!workspace || workspace_bytes < need || (uintptr_t)workspace % 16)) return TTS_BB_E_INVALID;
     if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const Plan p = attn_plan((long long)B * S, max_len);
     const Cache c = cache_of(cache);
-    const AttnArgs a{seqs, kv_lens, S, max_len, B * S, p.splits, static_cast<float*>(workspace)};
-    auto go = [&](auto t) {
-        typedef decltype(t) T;
-        constexpr size_t smem = RING_BYTES + (size_t)WARPS * (sizeof(T) == 4 ? 3 : 2) * 2 * HD * sizeof(float);
+    // bf16 queries of a sequence two at a time, in the columns of the products that one leaves empty
+    auto go = [&](auto type_of, auto tokens) {
+        typedef decltype(type_of) T;
+        constexpr int N = decltype(tokens)::value;
+        const int per_seq = (S + N - 1) / N, rows = B * per_seq;
+        const Plan p = attn_plan(rows, max_len);
+        const AttnArgs a{seqs, kv_lens, S, max_len, N, per_seq, rows, p.splits, static_cast<float*>(workspace)};
+        constexpr size_t smem = RING_BYTES + (size_t)WARPS * (sizeof(T) == 4 ? 3 : 2) * 2 * N * HD * sizeof(float);
         static SmemState grid_state, line_state;
-        allow_smem(grid_state, k_kv4_attn<T>, smem);
-        allow_smem(line_state, k_kv4_attn_line<T>, smem);
+        allow_smem(grid_state, k_kv4_attn<T, N>, smem);
+        allow_smem(line_state, k_kv4_attn_line<T, N>, smem);
         const T* const qt = static_cast<const T*>(q);
         T* const to = static_cast<T*>(out);
         if (p.splits > 1) {
-            launch_cluster(k_kv4_attn<T>, dim3(p.splits, NKV, B * S), WARPS * 32, smem, st, p.splits, qt, c, a, to);
+            launch_cluster(k_kv4_attn<T, N>, dim3(p.splits, NKV, rows), WARPS * 32, smem, st, p.splits, qt, c, a, to);
         } else if (p.splits) {
-            launch_pdl(k_kv4_attn<T>, dim3(1, NKV, B * S), WARPS * 32, smem, st, qt, c, a, to);
+            launch_pdl(k_kv4_attn<T, N>, dim3(1, NKV, rows), WARPS * 32, smem, st, qt, c, a, to);
         } else {
-            launch_pdl(k_kv4_attn_line<T>, p.shares, WARPS * 32, smem, st, qt, c, a, to);
-            launch_pdl(k_kv4_combine<T>, dim3(NQ, B * S), 128, 0, st, c, a, p.shares, to);
+            launch_pdl(k_kv4_attn_line<T, N>, p.shares, WARPS * 32, smem, st, qt, c, a, to);
+            launch_pdl(k_kv4_combine<T, N>, dim3(NQ * N, rows), 128, 0, st, c, a, p.shares, to);
         }
     };
-    if (type == TTS_BB_T_F32) go(float{});
-    else go(bf16{});
+    if (type == TTS_BB_T_F32) go(float{}, std::integral_constant<int, 1>{});
+    else if (S == 1) go(bf16{}, std::integral_constant<int, 1>{});
+    else go(bf16{}, std::integral_constant<int, 2>{});
     return status();
 }

@@ -330,6 +330,37 @@ def test_attention_nan_in_a_seen_key_reaches_the_output():
     assert np.array_equal(nan, want)
 
 
+@pytest.mark.parametrize("io", ["float32", "bfloat16"])
+@pytest.mark.parametrize("S,max_len", [(2, 128), (3, 128), (2, 16640), (5, 16640)])
+def test_attention_nan_in_a_later_key_stays_with_the_later_queries(S, max_len, io):
+    """The last query's own key is NaN, and its value: the queries before it do not see either; nor do queries that are not
+    finite reach one another."""
+    lens = [90, 65, 49]
+    s = filled(14, lens, 260)
+    tiles = s.pool_h.reshape(-1, 2, NKV, 4608)
+    for b, which in ((0, 0), (1, 1)):
+        n = lens[b] - 1
+        tiles[s.table[b, n // BLK], which, :, 4096 + 8 * (n % BLK) : 4104 + 8 * (n % BLK)] = (0xC0, 0x7F, 0x00, 0xC3) * 2
+    s.pool.copy_(dev(s.pool_h))
+    q = dev(s.rng.standard_normal((3 * S, NQ, HD))).to(getattr(torch, io))
+    q[3 * S - 1, 5, 77] = float("inf")
+    q[2 * S, 4, 3] = float("nan")
+    out = attend(s, q, lens, S, max_len)
+    nan = out.isnan().view(3, S, NQ, HD).cpu().numpy()
+    want = np.zeros_like(nan)
+    want[:2, S - 1] = True
+    want[2, S - 1, 5] = want[2, 0, 4] = True
+    assert np.array_equal(nan, want)
+    s.v[1][lens[1] - 1] = s.k[0][lens[0] - 1] = 0.0
+    out.view(3, S, NQ, HD)[:2, S - 1] = 0.0
+    got, qh = out.view(3, S, NQ, HD).double().cpu().numpy(), q.view(3, S, NQ, HD).double().cpu().numpy()
+    for b in range(2):
+        for i in range(S - 1):
+            seen = lens[b] - (S - 1 - i)
+            ref, mag, dots = attention(qh[b, i], s.k[b], s.v[b], seen)
+            assert (np.abs(got[b, i] - ref) <= attention_tol(ref, mag, dots, seen, io == "bfloat16")).all()
+
+
 def test_attention_matches_the_bf16_entry_point():
     """The same values in a bf16 pool through tts_bb_gqa_decode_attention_static."""
     m = tb()
