@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import sys
 from typing import Dict, List, Optional, Sequence
 
 import numpy as np
@@ -425,7 +426,8 @@ def tts_bb_gqa_decode_attention_static(q, kv_pool, page_table, blocks_per_seq: i
 
 # ---------------------------------------------------------------- low-bit decode operators
 # Device tensors with a dtype and strides (torch CUDA tensors); each call returns its status, or raises TtsBbError
-# with check=True. Shapes, types and strides are checked here, values by the library.
+# with check=True. Shapes, types, strides and devices are checked here, values by the library. The tensors are on the
+# current device, and stream belongs to it.
 T_F32, T_BF16, T_F16 = 0, 1, 2
 KV4_TILE_BYTES, KV4_BLOCK_BYTES, KV4_MAX_QUERIES, W4_MAX_TOKENS, LOGPROBS_MAX_TOP = 4608, 73728, 64, 64, 32
 KV4_ERR_PAGE, KV4_ERR_RANGE = 1, 2
@@ -449,29 +451,37 @@ _IO, _LOGITS = _Types(float32=T_F32, bfloat16=T_BF16), _Types(float32=T_F32, bfl
 _WORDS = _Types(uint32=0, int32=0)
 
 
-def _arg(x, name: str, types: _Types, n: int):
-    """Address of a contiguous device tensor of at least n elements of one of the types; None stays None."""
+def _here() -> int:
+    """The current device, -2 where there is none yet (and so no tensor on one)."""
+    cuda = sys.modules["torch"].cuda
+    return cuda.current_device() if cuda.is_initialized() else -2
+
+
+def _arg(here: int, x, name: str, types: _Types, n: int):
+    """Address of a contiguous tensor of at least n elements of one of the types on the device `here`; None stays None."""
     if x is None:
         return None
-    if types[x.dtype] is not None and x.is_cuda and x.is_contiguous() and x.numel() >= n:
+    if types[x.dtype] is not None and x.get_device() == here and x.is_contiguous() and x.numel() >= n:
         return x.data_ptr()
-    return _refuse(x, name, types, n)
+    return _refuse(here, x, name, types, n)
 
 
-def _rows(x, name: str, types: _Types, R: int, n: int):
+def _rows(here: int, x, name: str, types: _Types, R: int, n: int):
     """(address, row stride) of a device tensor of R rows of at least n elements: two dimensions, the last one
     contiguous, or anything contiguous."""
-    if types[x.dtype] is not None and x.is_cuda and x.dim() == 2:
+    if types[x.dtype] is not None and x.get_device() == here and x.dim() == 2:
         rows, cols = x.shape
         stride, one = x.stride()
         if one == 1 and rows >= R and cols >= n:
             return x.data_ptr(), stride if R > 1 else n
-    return _arg(x, name, types, R * n), n
+    return _arg(here, x, name, types, R * n), n
 
 
-def _refuse(x, name: str, types: _Types, n: int):
+def _refuse(here: int, x, name: str, types: _Types, n: int):
     if types[x.dtype] is None or not x.is_cuda:
         raise TypeError(f"{name}: a CUDA tensor of {' or '.join(types.codes)} is wanted, not {x.dtype} on {x.device}")
+    if x.get_device() != here:
+        raise ValueError(f"{name}: a tensor on the current device, cuda:{here}, is wanted, not on {x.device}")
     if x.numel() < n:
         raise ValueError(f"{name}: {n} elements are wanted, not {x.numel()}")
     raise ValueError(f"{name}: strides {tuple(x.stride())} of shape {tuple(x.shape)} are not supported")
@@ -491,10 +501,17 @@ class Kv4Cache:
         self.pool, self.page_table, self.err = pool, page_table, err
         if page_table.dim() != 2:
             raise ValueError("page_table: two dimensions are wanted")
+        here = _here()
         n = pool.numel() // KV4_BLOCK_BYTES
-        self.struct = tts_bb_kv4(_arg(pool, "pool", _U8, KV4_BLOCK_BYTES), _arg(page_table, "page_table", _I32, 1),
-                                 _arg(err, "err", _I32, 1), n, *page_table.shape)
-        self.ref = C.byref(self.struct)
+        self.struct = tts_bb_kv4(_arg(here, pool, "pool", _U8, KV4_BLOCK_BYTES), _arg(here, page_table, "page_table", _I32, 1),
+                                 _arg(here, err, "err", _I32, 1), n, *page_table.shape)
+        self.ref, self.device = C.byref(self.struct), here
+
+    def on(self, here: int):
+        """The argument of a call on the device `here`."""
+        if self.device != here:
+            raise ValueError(f"cache: a cache on the current device, cuda:{here}, is wanted, not on cuda:{self.device}")
+        return self.ref
 
 
 def tts_bb_rope_tables(theta: float, n_pos: int):
@@ -509,19 +526,21 @@ def tts_bb_rope_tables(theta: float, n_pos: int):
 def tts_bb_kv4_append(cache: Kv4Cache, T: int, qkv, q_norm, k_norm, cos_table, sin_table, n_pos: int, seqs, positions,
                       q_out=None, eps: float = 1e-6, stream: int = 0, check: bool = True) -> int:
     """qkv: [T][4096] fp32 or bf16 (rows may be strided); q_out: [T][16][128] fp32 or bf16, or None."""
-    x, stride = _rows(qkv, "qkv", _IO, T, 4096)
+    here = _here()
+    x, stride = _rows(here, qkv, "qkv", _IO, T, 4096)
     st = lib.tts_bb_kv4_append(
-        cache.ref, T, x, _IO[qkv.dtype], stride, _arg(q_norm, "q_norm", _BF16, 128), _arg(k_norm, "k_norm", _BF16, 128), eps,
-        _arg(cos_table, "cos_table", _F32, n_pos * 64), _arg(sin_table, "sin_table", _F32, n_pos * 64), n_pos,
-        _arg(seqs, "seqs", _I32, T), _arg(positions, "positions", _I32, T), _arg(q_out, "q_out", _IO, T * 2048),
+        cache.on(here), T, x, _IO[qkv.dtype], stride, _arg(here, q_norm, "q_norm", _BF16, 128), _arg(here, k_norm, "k_norm", _BF16, 128), eps,
+        _arg(here, cos_table, "cos_table", _F32, n_pos * 64), _arg(here, sin_table, "sin_table", _F32, n_pos * 64), n_pos,
+        _arg(here, seqs, "seqs", _I32, T), _arg(here, positions, "positions", _I32, T), _arg(here, q_out, "q_out", _IO, T * 2048),
         T_F32 if q_out is None else _IO[q_out.dtype], stream or None)
     return _status(st, "tts_bb_kv4_append", check)
 
 
 def tts_bb_kv4_read(cache: Kv4Cache, T: int, seqs, positions, k_out, v_out, stream: int = 0, check: bool = True) -> int:
     """k_out, v_out: bf16 [T][8][128]."""
-    st = lib.tts_bb_kv4_read(cache.ref, T, _arg(seqs, "seqs", _I32, T), _arg(positions, "positions", _I32, T),
-                             _arg(k_out, "k_out", _BF16, T * 1024), _arg(v_out, "v_out", _BF16, T * 1024), stream or None)
+    here = _here()
+    st = lib.tts_bb_kv4_read(cache.on(here), T, _arg(here, seqs, "seqs", _I32, T), _arg(here, positions, "positions", _I32, T),
+                             _arg(here, k_out, "k_out", _BF16, T * 1024), _arg(here, v_out, "v_out", _BF16, T * 1024), stream or None)
     return _status(st, "tts_bb_kv4_read", check)
 
 
@@ -534,10 +553,11 @@ def tts_bb_kv4_attention(cache: Kv4Cache, B: int, S: int, q, kv_lens, max_len: i
     """q, out: [B][S][16][128], both fp32 or both bf16; workspace: a uint8 tensor, or None where none is needed."""
     if q.dtype != out.dtype:
         raise TypeError(f"q and out have to be of one type, not {q.dtype} and {out.dtype}")
+    here = _here()
     st = lib.tts_bb_kv4_attention(
-        cache.ref, B, S, _arg(q, "q", _IO, B * S * 2048), _IO[q.dtype], _arg(seqs, "seqs", _I32, B),
-        _arg(kv_lens, "kv_lens", _I32, B), max_len, _arg(out, "out", _IO, B * S * 2048),
-        _arg(workspace, "workspace", _U8, 0), 0 if workspace is None else workspace.numel(), stream or None)
+        cache.on(here), B, S, _arg(here, q, "q", _IO, B * S * 2048), _IO[q.dtype], _arg(here, seqs, "seqs", _I32, B),
+        _arg(here, kv_lens, "kv_lens", _I32, B), max_len, _arg(here, out, "out", _IO, B * S * 2048),
+        _arg(here, workspace, "workspace", _U8, 0), 0 if workspace is None else workspace.numel(), stream or None)
     return _status(st, "tts_bb_kv4_attention", check)
 
 
@@ -547,10 +567,10 @@ def tts_bb_w4_packed_bytes(N: int, K: int, group: int) -> int:
 
 def tts_bb_w4_pack(N: int, K: int, group: int, codes, scales, zeros, packed, stream: int = 0, check: bool = True) -> int:
     """codes uint8 [N][K / 2], scales bf16 [N][K / group], zeros uint8 [N][K / group] or None -> packed uint8."""
-    n = N * (K // group) if group > 0 else 0
-    st = lib.tts_bb_w4_pack(N, K, group, _arg(codes, "codes", _U8, N * K // 2), _arg(scales, "scales", _BF16, n),
-                            _arg(zeros, "zeros", _U8, n),
-                            _arg(packed, "packed", _U8, tts_bb_w4_packed_bytes(N, K, group)), stream or None)
+    here, n = _here(), N * (K // group) if group > 0 else 0
+    st = lib.tts_bb_w4_pack(N, K, group, _arg(here, codes, "codes", _U8, N * K // 2), _arg(here, scales, "scales", _BF16, n),
+                            _arg(here, zeros, "zeros", _U8, n),
+                            _arg(here, packed, "packed", _U8, tts_bb_w4_packed_bytes(N, K, group)), stream or None)
     return _status(st, "tts_bb_w4_pack", check)
 
 
@@ -558,10 +578,11 @@ def tts_bb_w4_linear(T: int, N: int, K: int, group: int, x, packed, y, stream: i
     """x: [T][K] (rows may be strided), y: [T][N], both fp32 or both bf16."""
     if x.dtype != y.dtype:
         raise TypeError(f"x and y have to be of one type, not {x.dtype} and {y.dtype}")
-    at, stride = _rows(x, "x", _IO, T, K)
+    here = _here()
+    at, stride = _rows(here, x, "x", _IO, T, K)
     need = (N + 15) // 16 * (K // group) * (8 * group + 64) if group > 0 else 0
-    st = lib.tts_bb_w4_linear(T, N, K, group, at, _IO[x.dtype], stride, _arg(packed, "packed", _U8, need),
-                              _arg(y, "y", _IO, T * N), stream or None)
+    st = lib.tts_bb_w4_linear(T, N, K, group, at, _IO[x.dtype], stride, _arg(here, packed, "packed", _U8, need),
+                              _arg(here, y, "y", _IO, T * N), stream or None)
     return _status(st, "tts_bb_w4_linear", check)
 
 
@@ -574,15 +595,16 @@ def tts_bb_token_logprobs(R: int, V: int, logits, targets=None, n_top: int = 0, 
                           check: bool = True) -> int:
     """logits: [R][>= V] fp32, bf16 or fp16 (rows may be strided); allowed: uint32 or int32 words, [words] for all
     rows or [R][words]."""
-    z, stride = _rows(logits, "logits", _LOGITS, R, V)
+    here = _here()
+    z, stride = _rows(here, logits, "logits", _LOGITS, R, V)
     mask, mask_stride = None, 0
     if allowed is not None:
-        mask, mask_stride = _rows(allowed, "allowed", _WORDS, R if allowed.dim() == 2 else 1, (V + 31) // 32)
+        mask, mask_stride = _rows(here, allowed, "allowed", _WORDS, R if allowed.dim() == 2 else 1, (V + 31) // 32)
         if allowed.dim() != 2 or R == 1:
             mask_stride = 0
     st = lib.tts_bb_token_logprobs(
-        R, V, z, _LOGITS[logits.dtype], stride, _arg(targets, "targets", _I32, R), mask, mask_stride, n_top,
-        _arg(logprob, "logprob", _F32, R), _arg(entropy, "entropy", _F32, R), _arg(lse, "lse", _F32, R),
-        _arg(top_ids, "top_ids", _I32, R * n_top), _arg(top_logprobs, "top_logprobs", _F32, R * n_top),
-        _arg(workspace, "workspace", _U8, 0), 0 if workspace is None else workspace.numel(), stream or None)
+        R, V, z, _LOGITS[logits.dtype], stride, _arg(here, targets, "targets", _I32, R), mask, mask_stride, n_top,
+        _arg(here, logprob, "logprob", _F32, R), _arg(here, entropy, "entropy", _F32, R), _arg(here, lse, "lse", _F32, R),
+        _arg(here, top_ids, "top_ids", _I32, R * n_top), _arg(here, top_logprobs, "top_logprobs", _F32, R * n_top),
+        _arg(here, workspace, "workspace", _U8, 0), 0 if workspace is None else workspace.numel(), stream or None)
     return _status(st, "tts_bb_token_logprobs", check)

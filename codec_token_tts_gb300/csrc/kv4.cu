@@ -1344,7 +1344,7 @@ TTS_API tts_bb_status tts_bb_kv4_read(const tts_bb_kv4* cache, int T, const int3
 }
 
 TTS_API size_t tts_bb_kv4_attention_workspace(int B, int S, int max_len) {
-    if (B < 1 || S < 1 || S > TTS_BB_KV4_MAX_QUERIES || max_len < 1 || (long long)B * S > 65535) return 0;
+    if (B < 1 || S < 1 || S > TTS_BB_KV4_MAX_QUERIES || max_len < 1 || max_len > (1 << 30) || (long long)B * S > 65535) return 0;
     size_t most = 0;
     for (int each = 1; each <= std::min(S, 2); ++each)
         most = std::max(most, (size_t)attn_plan((long long)B * ((S + each - 1) / each), max_len).shares * 2 * 2 * each * PIECE * sizeof(float));
@@ -1355,7 +1355,7 @@ TTS_API tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S
                                            const int32_t* seqs, const int32_t* kv_lens, int max_len, void* out,
                                            void* workspace, size_t workspace_bytes, void* stream) {
     if (!cache_ok(cache) || B < 1 || S < 1 || S > TTS_BB_KV4_MAX_QUERIES || (long long)B * S > 65535 || !q || !kv_lens ||
-        !out || !type_ok(type) || !aligned(q) || !aligned(out) || max_len < 1 ||
+        !out || !type_ok(type) || !aligned(q) || !aligned(out) || max_len < 1 || max_len > (1 << 30) ||
         (long long)max_len > (long long)cache->blocks_per_seq * KVB || (!seqs && B > cache->n_seqs))
         return TTS_BB_E_INVALID;
     const size_t need = tts_bb_kv4_attention_workspace(B, S, max_len);

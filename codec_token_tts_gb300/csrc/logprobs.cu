@@ -725,7 +725,7 @@ TTS_API tts_bb_status tts_bb_token_logprobs(int R, int V, const void* logits, in
                                             const int32_t* targets, const uint32_t* allowed, int64_t allowed_stride,
                                             int n_top, float* logprob, float* entropy, float* lse, int32_t* top_ids,
                                             float* top_logprobs, void* workspace, size_t workspace_bytes, void* stream) {
-    if (R < 1 || R > (1 << 27) || V < 1 || !logits || row_stride < V || n_top < 0 || n_top > TTS_BB_LOGPROBS_MAX_TOP ||
+    if (R < 1 || R > (1 << 27) || V < 1 || V > (1 << 30) || !logits || row_stride < V || n_top < 0 || n_top > TTS_BB_LOGPROBS_MAX_TOP ||
         type < TTS_BB_T_F32 || type > TTS_BB_T_F16 || (uintptr_t)logits % (type == TTS_BB_T_F32 ? 4 : 2) ||
         (targets && !logprob) || (n_top && (!top_ids || !top_logprobs)) ||
         (allowed && allowed_stride != 0 && allowed_stride < ((int64_t)V + 31) / 32))

@@ -571,7 +571,7 @@ tts_bb_status tts_bb_kv4_read(const tts_bb_kv4* cache, int T, const int32_t* seq
  *             they were), or NULL: sequence b reads row b
  *   kv_lens   int32 [B], the sequence's keys, those of the S query tokens among them: query s sees the first
  *             kv_lens[b] - (S - 1 - s); a query that sees none gives zeros
- *   max_len   an upper bound of kv_lens (host), at most 64 * blocks_per_seq; it sets the split and
+ *   max_len   an upper bound of kv_lens (host), at most 64 * blocks_per_seq and 2^30; it sets the split and
  *             the workspace, a tight one is faster. A sequence whose row or key count is out of range is
  *             left as it was; keys behind a page out of range are left out of the sums; both are reported
  *             in cache->err.
@@ -604,7 +604,7 @@ tts_bb_status tts_bb_w4_pack(int N, int K, int group, const void* codes, const v
 tts_bb_status tts_bb_w4_linear(int T, int N, int K, int group, const void* x, int type, int64_t x_stride,
                                const void* packed, void* y, void* stream);
 
-/* Log probabilities of R <= 2^27 rows of V logits: of a given token, the entropy, the log-sum-exp and the n_top most
+/* Log probabilities of R <= 2^27 rows of V <= 2^30 logits: of a given token, the entropy, the log-sum-exp and the n_top most
  * probable tokens.
  *   logits   fp32, bf16 or fp16 (type) [R] rows, row_stride elements apart (>= V), aligned to the element
  *   targets  int32 [R] or NULL; logprob fp32 [R]: log p(targets[r]); -inf for a target outside 0..V-1, a

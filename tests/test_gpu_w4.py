@@ -163,3 +163,32 @@ def test_pack_and_product_back_to_back():
         w = unpack_w4(c, s, z, G)
         xh = x.double().cpu().numpy()
         assert (np.abs(y.double().cpu().numpy() - xh @ w.T) <= 2 * (K + 16) * U * (np.abs(xh) @ np.abs(w).T)).all()
+
+
+@pytest.mark.parametrize("N,K,G,T", [(257, 4096, 128, 8), (1030, 2048, 64, 33)])
+def test_slices_of_a_cluster_captured(N, K, G, T):
+    """A call that splits K, captured as the first of its kind, and replayed beside another on a stream of its own."""
+    m = tb()
+    rng = np.random.default_rng(N)
+    codes, scales, z = weights(rng, N, K, G, True)
+    p = pack(N, K, G, codes, scales, z)
+    xs = [dev(rng.standard_normal((T, K))).bfloat16() for _ in range(3)]
+    x, y = xs[2].clone(), torch.zeros(T, N, device="cuda", dtype=torch.bfloat16)
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=side):
+        m.tts_bb_w4_linear(T, N, K, G, x, p, y, torch.cuda.current_stream().cuda_stream)
+    want = []
+    for v in xs:
+        want.append(torch.empty(T, N, device="cuda", dtype=torch.bfloat16))
+        m.tts_bb_w4_linear(T, N, K, G, v, p, want[-1], torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    other, out = torch.cuda.Stream(), torch.empty(T, N, device="cuda", dtype=torch.bfloat16)
+    for v, w in zip(xs, want):
+        x.copy_(v)
+        torch.cuda.synchronize()
+        for _ in range(10):
+            with torch.cuda.stream(side):
+                g.replay()
+            m.tts_bb_w4_linear(T, N, K, G, xs[0], p, out, other.cuda_stream)
+        torch.cuda.synchronize()
+        assert torch.equal(y, w) and torch.equal(out, want[0])

@@ -52,13 +52,15 @@ def test_attention_refuses():
     refused(m.lib.tts_bb_kv4_attention, good, bad)
     good.update(seqs=P, B=1024, S=64, n=2**62)
     assert m.lib.tts_bb_kv4_attention(*good.values()) == -1  # B * S = 65536
-    for args in ((0, 1, 1), (1, 0, 1), (1, 65, 1), (1, 1, 0), (1024, 64, 64), (2**31 - 1, 64, 64)):
+    good = dict(cache=C.byref(cache(m, blocks_per_seq=2**25)), B=1, S=1, q=P, type=0, seqs=None, lens=P, max_len=2**30 + 1, out=P, ws=P, n=2**62, stream=None)
+    assert m.lib.tts_bb_kv4_attention(*good.values()) == -1
+    for args in ((0, 1, 1), (1, 0, 1), (1, 1, 2**30 + 1), (1, 65, 1), (1, 1, 0), (1024, 64, 64), (2**31 - 1, 64, 64)):
         assert m.tts_bb_kv4_attention_workspace(*args) == 0
 
 
 def test_w4_refuses():
     m = tb()
-    for args in ((0, 128, 128), (1, 0, 128), (1, 128, 16), (1, 128, 256), (1, 100, 32), (1, 64, 128), (2**20 + 1, 128, 128), (1, 2**20 + 128, 128), (-1, 128, 64)):
+    for args in ((0, 128, 128), (1, 0, 128), (1, 128, 16), (1, 128, 256), (1, 100, 32), (1, 64, 128), (2**20 + 1, 128, 128), (1, 2**20 + 128, 128), (1, 2**18 + 128, 128), (-1, 128, 64)):
         assert m.tts_bb_w4_packed_bytes(*args) == 0
         assert m.lib.tts_bb_w4_pack(*args, P, P, P, P, None) == -1
         assert m.lib.tts_bb_w4_linear(1, *args, P, 0, 2**21, P, P, None) == -1
@@ -72,7 +74,7 @@ def test_w4_refuses():
 def test_logprobs_refuses():
     m = tb()
     good = dict(R=2, V=100, z=P, type=0, stride=100, targets=P, allowed=P, a_stride=4, k=2, lp=P, ent=None, lse=None, ids=P, top=P, ws=P, n=2**40, stream=None)
-    refused(m.lib.tts_bb_token_logprobs, good, dict(R=[0, -1], V=[0, -3], z=[None, P + 2], type=[-1, 3], stride=[99, 0, -1], a_stride=[3, 1, -4], k=[-1, 33],
+    refused(m.lib.tts_bb_token_logprobs, good, dict(R=[0, -1, 2**27 + 1], V=[0, -3, 2**30 + 1], z=[None, P + 2], type=[-1, 3], stride=[99, 0, -1], a_stride=[3, 1, -4], k=[-1, 33],
                                                     lp=[None], ids=[None], top=[None]))
     good.update(V=300000, stride=300000, a_stride=0, n=0)
     if m.tts_bb_token_logprobs_workspace(2, 300000, 2):
@@ -107,6 +109,54 @@ def test_wrappers_check_tensors():
         m.Kv4Cache(x, torch.zeros(1, 1, dtype=torch.int32))
     with pytest.raises(ValueError):
         m.Kv4Cache(x, torch.zeros(1, dtype=torch.int32))
+
+
+class On:
+    """Stands for a tensor on another device than the current one."""
+
+    def __init__(self, t, device):
+        self.t, self.device, self.is_cuda, self.dtype = t, f"cuda:{device}", True, t.dtype
+        self.get_device = lambda: device
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_wrappers_refuse_another_device(monkeypatch):
+    """A tensor that is not on the current device is refused, whichever argument it is, and a cache made on another."""
+    torch = pytest.importorskip("torch")
+    m = tb()
+    monkeypatch.setattr(m, "_here", lambda: 1)
+    calls = []
+    monkeypatch.setattr(m, "lib", type("Lib", (), {"__getattr__": lambda self, name: lambda *a: calls.append(name) or 0})())
+    z = lambda n, dt=torch.float32: On(torch.zeros(n, dtype=dt), 1)
+    i32, u8, bf = torch.int32, torch.uint8, torch.bfloat16
+    cache = m.Kv4Cache(z(m.KV4_BLOCK_BYTES, u8), On(torch.zeros(1, 2, dtype=i32), 1), z(1, i32))
+    here = {
+        "tts_bb_kv4_append": dict(cache=cache, T=1, qkv=z(4096), q_norm=z(128, bf), k_norm=z(128, bf), cos_table=z(64), sin_table=z(64), n_pos=1,
+                                  seqs=z(1, i32), positions=z(1, i32), q_out=z(2048)),
+        "tts_bb_kv4_read": dict(cache=cache, T=1, seqs=z(1, i32), positions=z(1, i32), k_out=z(1024, bf), v_out=z(1024, bf)),
+        "tts_bb_kv4_attention": dict(cache=cache, B=1, S=1, q=z(2048), kv_lens=z(1, i32), max_len=64, out=z(2048), workspace=z(16, u8), seqs=z(1, i32)),
+        "tts_bb_w4_pack": dict(N=16, K=64, group=64, codes=z(512, u8), scales=z(16, bf), zeros=z(16, u8), packed=z(576, u8)),
+        "tts_bb_w4_linear": dict(T=1, N=16, K=64, group=64, x=z(64), packed=z(576, u8), y=z(16)),
+        "tts_bb_token_logprobs": dict(R=1, V=64, logits=z(64), targets=z(1, i32), n_top=1, logprob=z(1), entropy=z(1), lse=z(1), top_ids=z(1, i32),
+                                      top_logprobs=z(1), allowed=z(2, i32), workspace=z(16, u8)),
+    }
+    monkeypatch.setattr(m, "tts_bb_w4_packed_bytes", lambda *a: 576)
+    for name, args in here.items():
+        f = getattr(m, name)
+        f(**args)
+        assert calls and calls.pop() == name
+        for k, v in args.items():
+            if isinstance(v, On):
+                with pytest.raises(ValueError, match="current device"):
+                    f(**{**args, k: On(v.t, 0)})
+        assert not calls
+    monkeypatch.setattr(m, "_here", lambda: 0)
+    for name in ("tts_bb_kv4_append", "tts_bb_kv4_read", "tts_bb_kv4_attention"):
+        with pytest.raises(ValueError, match="current device"):
+            getattr(m, name)(**{k: On(v.t, 0) if isinstance(v, On) else v for k, v in here[name].items()})
+    assert not calls
 
 
 def test_the_plain_quantiser():
