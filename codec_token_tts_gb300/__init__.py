@@ -453,8 +453,13 @@ _WORDS = _Types(uint32=0, int32=0)
 
 def _here() -> int:
     """The current device, -2 where there is none yet (and so no tensor on one)."""
-    cuda = sys.modules["torch"].cuda
-    return cuda.current_device() if cuda.is_initialized() else -2
+    global _here
+    torch = sys.modules["torch"]
+    if not torch.cuda.is_initialized():
+        return -2
+    # from now on without the question whether CUDA is initialised, which current_device repeats: 1 us a call
+    _here = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _here()
 
 
 def _arg(here: int, x, name: str, types: _Types, n: int):
