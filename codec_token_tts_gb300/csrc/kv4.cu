@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(128, 6) k_kv4_append(int T, const TI* __restri
         if (pos >= n_pos) {
             if (threadIdx.x == 0) set_err(c.err, TTS_BB_KV4_ERR_RANGE);
             continue;
-    }
+        }
         const int phys = find_block(c, seq, pos, threadIdx.x == 0);
         if (phys < 0) continue;
         const bool is_q = WHAT == HEADS_Q || (WHAT != HEADS_KV && warp < 4), norm = is_q || warp < 6;
@@ -1237,8 +1237,9 @@ struct Plan {
 };
 // Caches of up to 16 blocks of keys a block of the launch (32 where the pairs fill half the SMs' slots by themselves): one
 // block, or one cluster of up to 8 as the slots allow, for each (row, KV head), in one launch. Longer ones: a line in SLOTS
-// shares (four blocks an SM are resident: one wave) and the launch that merges it. Measured, us: 1 x 8000 keys 9.7 by a
-// cluster, 15.0 by a line; 64 x 20..200 keys 10.8 and 15.4; 64 x 800..8000 by one block each 78, by a line 69.
+// shares (four blocks an SM are resident: one wave) and the launch that merges it. Measured, us: 1 x 8000 keys 10.0 by a
+// cluster, 14.1 by a line; 64 x 20..200 keys 6.0 and 14.3; 16 x 400..4000 17.5 and 18.6; 64 x 800..8000 by one block each 78,
+// by a line 69.
 Plan attn_plan(long long rows, int max_len) {
     const long long pairs = rows * NKV, nblk = (max_len + KVB - 1) / KVB, most = (nblk + 1) / 2;
     const long long n = std::min({(long long)MAX_CLUSTER, SLOTS / pairs, most});
@@ -1276,7 +1277,8 @@ void launch_cluster(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cud
     cudaLaunchKernelEx(&cfg, k, static_cast<KArgs>(args)...);
 }
 
-// Prompts take two launches: the q heads need half of the registers, and twice as many of their warps then hide memory.
+// fp32 prompts take two launches: the q heads need half of the registers, and twice as many of their warps then hide memory:
+// 32768 tokens 187 us, 196 in one. bf16 ones, whose values on the way take half the registers, take one: 137 us, 139 in two.
 constexpr int SPLIT_TOKENS = 4096;
 template <typename TI, typename TQ>
 void append(int T, const void* qkv, int64_t stride, const void* gq, const void* gk, float eps, const float* cos_t,
@@ -1286,12 +1288,14 @@ void append(int T, const void* qkv, int64_t stride, const void* gq, const void* 
         launch_pdl(k, dim3(std::min(T, 6 * 152), parts), 128, 0, st, T, static_cast<const TI*>(qkv), (long long)stride, static_cast<const bf16*>(gq),
                    static_cast<const bf16*>(gk), eps, cos_t, sin_t, n_pos, seqs, positions, cache_of(c), static_cast<TQ*>(q_out));
     };
-    if (T < SPLIT_TOKENS) {
-        go(k_kv4_append<HEADS_Q | HEADS_KV, TI, TQ>, 2);
-    } else {
-        go(k_kv4_append<HEADS_KV, TI, TQ>, 1);
-        if (q_out) go(k_kv4_append<HEADS_Q, TI, TQ>, 1);
+    if constexpr (sizeof(TI) == 4) {
+        if (T >= SPLIT_TOKENS) {
+            go(k_kv4_append<HEADS_KV, TI, TQ>, 1);
+            if (q_out) go(k_kv4_append<HEADS_Q, TI, TQ>, 1);
+            return;
+        }
     }
+    go(k_kv4_append<HEADS_Q | HEADS_KV, TI, TQ>, 2);
 }
 
 }  // namespace

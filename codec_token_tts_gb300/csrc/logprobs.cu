@@ -138,9 +138,12 @@ __device__ __forceinline__ f2 fmap(f2 a, f2 b, f2 c) {
 // ---------------------------------------------------------------- one warp a row
 // Rows of up to 32 * NV logits (NV even), held in registers: lane l has ids l, l + 32, .... One pass for the maximum, one for the
 // sums, one that marks the alternatives: ids whose logit reaches the n_top-th largest of the 32 lanes' maxima (a bound below
-// the n_top-th largest of all), usually a few more than n_top, ranked by counting. What bounds it are the instructions of
-// these passes (49152 x 1025 fp32 with a mask and 5 alternatives: a third of the time memory alone would leave), so a
-// pass is kept to what most rows need; and their number, since code that does not fit the instruction cache stalls: what
+// the n_top-th largest of all), usually a few more than n_top, ranked by counting. Near the least of the 32 maxima that bound
+// gets loose (all 32 of 1025 ids: about 130 candidates): more than 12 alternatives start at place 0.7 n_top and halve their
+// way to one that at least n_top and at most CAP ids reach (49152 x 1025, 32 alternatives: 75 us, 98 from the last place
+// on; 20: 57 and 62).
+// What bounds it are the instructions of these passes (49152 x 1025 fp32 with a mask and 5 alternatives: 47 us, 4.3 TB/s), so
+// a pass is kept to what most rows need; and their number, since code that does not fit the instruction cache stalls: what
 // few rows need is a loop over memory. These are rows with a logit that is not within 1e30 (a NaN, an infinity, the
 // type's lowest value) and rows with more equal candidates than CAP.
 constexpr int ROW_WARPS = 4, CAP = 96;
@@ -268,45 +271,59 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) k_logprobs_warp(const T* __res
         const float log_s = log1pf(p.r);
         if (lane == 0) finish(a, row, p, log_s, wanted, tz);
         if (a.n_top == 0) continue;
-        float bound = p.m;
+        float bound = p.m, s = mine;
+        int k = a.n_top - 1, few = -1, enough = k;  // places among the lanes' maxima; few: fewer than n_top reach it
         if (a.n_top <= 8) {  // the largest of the lanes' maxima taken out n_top - 1 times, equal ones together
-            float s = mine;
             for (int j = 1; j < a.n_top; ++j) {
                 if (s == bound) s = NEG_INF;
                 bound = row_max(s);
             }
         } else {  // the lanes' maxima in falling order
-            float s = mine;
 #pragma unroll
-            for (int k = 2; k <= 32; k <<= 1)
+            for (int m = 2; m <= 32; m <<= 1)
 #pragma unroll
-                for (int j = k >> 1; j; j >>= 1) {
+                for (int j = m >> 1; j; j >>= 1) {
                     const float o = __shfl_xor_sync(ALL, s, j);
-                    s = ((lane & k) == 0) == ((lane & j) == 0) ? fmaxf(s, o) : fminf(s, o);
+                    s = ((lane & m) == 0) == ((lane & j) == 0) ? fmaxf(s, o) : fminf(s, o);
                 }
-            bound = __shfl_sync(ALL, s, a.n_top - 1);
+            if (a.n_top > 12 && a.V > CAP) k = a.n_top * 7 / 10;
+            bound = __shfl_sync(ALL, s, k);
         }
-        bound = fmaxf(bound, -9e29f);  // OUT is no alternative
+        constexpr float LEAST = -9e29f;  // OUT is no alternative
         uint32_t in[(NV + 31) / 32];
-        int count = 0;
+        int count, n;
+        while (true) {
+            bound = fmaxf(bound, LEAST);
+            count = 0;
 #pragma unroll
-        for (int w = 0; w < (NV + 31) / 32; ++w) {
-            in[w] = 0u;
+            for (int w = 0; w < (NV + 31) / 32; ++w) {
+                in[w] = 0u;
 #pragma unroll
-            for (int i = 32 * w; i < NV && i < 32 * w + 32; ++i)
-                if (v[i] >= bound) in[w] |= 1u << (i & 31);
-            count += __popc(in[w]);
+                for (int i = 32 * w; i < NV && i < 32 * w + 32; ++i)
+                    if (v[i] >= bound) in[w] |= 1u << (i & 31);
+                count += __popc(in[w]);
+            }
+            n = __reduce_add_sync(ALL, count);
+            if (n < a.n_top && k < a.n_top - 1 && bound > LEAST) {
+                few = k;
+                k = (k + enough + 1) / 2;
+            } else if (n > CAP && a.n_top > 8 && k - few > 1) {
+                enough = k;
+                k = (few + k) / 2;
+            } else {
+                break;
+            }
+            bound = __shfl_sync(ALL, s, k);
+        }
+        if (n > CAP) {
+            tops_of(z, ok, a, row, p, lane);
+            continue;
         }
         int at = count;  // places of the lanes before this one, and of this one
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(ALL, at, o);
             if (lane >= o) at += u;
-        }
-        const int n = __shfl_sync(ALL, at, 31);
-        if (n > CAP) {
-            tops_of(z, ok, a, row, p, lane);
-            continue;
         }
         at -= count;
 #pragma unroll
@@ -332,9 +349,12 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) k_logprobs_warp(const T* __res
 // has them; the places before and behind it hold -inf, so that all of it is read in 16-byte pieces) and read three times
 // there: maximum (masked ids become -inf in it), then sums and the candidates: logits that reach a bound below the n_top-th
 // largest, at most LIST of them (with more equal ones, one alternative after the other is looked for). Block 0
-// joins the slices.
+// joins the slices. A few long rows are bound by the passes' latency (64 x 151676 bf16, 20 alternatives: 16 us, of which
+// memory would take 3), many by the passes' instructions (2000 x 25000 fp32: 88 us, 2.3 TB/s).
 constexpr int LIST = 1024, MAX_TOP = TTS_BB_LOGPROBS_MAX_TOP;
-constexpr int SLICE_BYTES = 48 * 1024, MAX_SLICE_BYTES = 192 * 1024, SMALL_SLICE = 16 * 1024;  // up to it: 128 threads a block
+// A slice of SLICE_BYTES leaves room for two blocks an SM (2000 x 25000 fp32 in one slice 88 us, in slices of 48 KB 103); one of
+// up to SMALL_SLICE gets 128 threads (16000 x 3100 fp32 77 us, by 256 threads 128; 64 x 100000 fp32 25 us by 128, 20 by 256).
+constexpr int SLICE_BYTES = 100 * 1024, MAX_SLICE_BYTES = 192 * 1024, SMALL_SLICE = 16 * 1024;
 
 template <typename T> constexpr int EACH = 16 / sizeof(T);  // logits of a 16-byte piece
 __device__ __forceinline__ void unpack(const uint4& u, float (&v)[4], float) {
@@ -691,8 +711,8 @@ void launch_block(const T* logits, const Args& a, int n, int slice, cudaStream_t
 }
 
 // Many rows of up to 96 logits a lane: a warp each (below 4 warps an SM a row's latency counts, and a block's threads
-// share it). Else a block a row, or a cluster: slices of at most SLICE_BYTES, so that several blocks share an SM, and more,
-// shorter ones while the rows alone leave SMs idle.
+// share it: 600 x 2048 bf16, masked, 5 alternatives 5.7 us, by warps 6.8). Else a block a row, or a cluster: slices of at most
+// SLICE_BYTES, and more, shorter ones while the rows alone leave SMs idle.
 template <typename T>
 void launch(const T* logits, const Args& a, cudaStream_t st) {
     // as many blocks as fit at a time: a warp goes on with further rows, and takes the mask apart once
