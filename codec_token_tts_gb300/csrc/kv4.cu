@@ -609,10 +609,10 @@ __device__ __forceinline__ bool attn_row(const Cache& c, const AttnArgs& a, int 
 // sums cancel and a common offset would cost their digits. P times V's scale of the key and group is B, as bf16 parts by
 // truncation (bf16: two, 16 bits; fp32: three, all 24) in columns of their own.
 //
-// Two query tokens that follow one another (N = 2, bf16): the columns that one token only repeats are the second one's, query
-// c & 1 in a lane, which then has both of 16 keys' scores r and r + 8 of its head. Codes are taken apart once for both: 8
-// sequences of 8 tokens and 2000 keys 28 -> 19 us, 64 of 2 and 1000 keys 25 -> 18. The first token does not see the
-// second's key: its weight is 0 there. (fp32 has no column left: three parts of a weight by two heads are six of eight.)
+// Two query tokens that follow one another (N = 2): the columns that one token only repeats are the second one's, query
+// c & 1 in a lane, which then has both of 16 keys' scores r and r + 8 of its head; fp32's third parts of the weights take
+// products of their own (and registers: three blocks an SM). Codes are taken apart once for both: 8
+// sequences of 8 tokens and 2000 keys 28 -> 19 us (fp32 33 -> 28), 44 of 7 and 943 fp32 49 -> 40. The first token does not see the second's key: its weight is 0 there.
 //
 // Softmax: a running reference m for each head, moved only when a score exceeds it by 8 (log2): then sums and O are
 // rescaled. It starts at -1e30, not -inf, so that no difference of infinities arises.
@@ -663,7 +663,7 @@ __device__ __forceinline__ uint32_t part_of(float x, uint32_t m1, uint32_t m2) {
 // 128, to: this head's; 8 dims stand as 0 4 1 5 2 6 3 7; with one part (bf16 queries) the odd ones divided by 16) and in
 // `about` its group sums, in the units of the products' sums, and the factor that turns those into scores times log2(e) (NaN
 // where a query is not finite).
-template <int PARTS>
+template <int PARTS, int N>
 __device__ __forceinline__ void stage_q(const float4 v, int lane, __half* to, float* about) {
     const float a = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
     // fmaxf drops a NaN
@@ -683,7 +683,7 @@ __device__ __forceinline__ void stage_q(const float4 v, int lane, __half* to, fl
         for (int e = 0; e < 4; ++e) {
             const __half h = __float2half_rn(x[e]);
             x[e] -= __half2float(h);
-            to[p * 2 * HD + e * 2] = PARTS == 1 && (e & 1) ? __hmul(h, __float2half_rn(0.0625f)) : h;
+            to[p * 2 * N * HD + e * 2] = PARTS == 1 && (e & 1) ? __hmul(h, __float2half_rn(0.0625f)) : h;
         }
 }
 
@@ -698,9 +698,10 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+template <typename T, int N> constexpr int AN_SM = sizeof(T) * N == 8 ? 3 : 4;  // blocks an SM
 // What a block has in common for its pieces
 struct Shared {
-    __half q[2][2][HD];  // [part or query][head]
+    __half q[4][2][HD];  // [2 part + query, or part][head]
     float about[4][4];   // of head h of query j at 2 j + h, here and below
     float m[WARPS][4], l[WARPS][4];
 };
@@ -765,14 +766,13 @@ template <typename T, int N>
 __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const Piece<T>& next, const Cache& cache, uint8_t* ring, float* so,
                                              Shared& sh, Ahead& ahead, float (&M)[2 * N], float (&L)[2 * N], float (&O)[2 * N]) {
     constexpr bool F32 = sizeof(T) == 4;
-    static_assert(N == 1 || !F32, "columns");
     constexpr int P = F32 ? 3 : 2;  // bf16 parts of a weight
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int seen = p.seen, j0 = p.b0 + (warp >> 1), n = p.units(warp);
     uint8_t* const mine = ring + warp * STAGES * UNIT_BYTES;
     const int32_t* const pages = p.pages(cache, warp);
 
-    if (warp < 2 * N) stage_q<F32 ? 2 : 1>(ahead.q, lane, sh.q[warp >> 1][warp & 1], sh.about[warp]);
+    if (warp < 2 * N) stage_q<F32 ? 2 : 1, N>(ahead.q, lane, sh.q[warp >> 1][warp & 1], sh.about[warp]);
     __syncthreads();
     int next_page = 0;
     if (more) {
@@ -785,8 +785,8 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
     const float factor = sh.about[hq][2];
 #pragma unroll
     for (int w = 0; w < 4; ++w)
-        qb[w] = *reinterpret_cast<const uint4*>(&sh.q[F32 || N == 2 ? r >> 1 & 1 : 0][r & 1][64 * (w & 1) + 16 * c + 8 * (w >> 1)]);
-    const uint32_t m1 = r >= 2 ? 0xFFFF0000u : 0u, m2 = r >= 4 ? 0xFFFF0000u : 0u;
+        qb[w] = *reinterpret_cast<const uint4*>(&sh.q[F32 && N == 2 ? r >> 1 : F32 || N == 2 ? r >> 1 & 1 : 0][r & 1][64 * (w & 1) + 16 * c + 8 * (w >> 1)]);
+    const uint32_t m1 = r >= 2 * N ? 0xFFFF0000u : 0u, m2 = N == 1 && r >= 4 ? 0xFFFF0000u : 0u;
     const uint32_t half_sel = r & (N == 1 ? 2 : 4) ? 0x5410u : 0x7632u;  // bf16: part 0 in the high halves, part 1 in the low ones
     const int from = 4 * c + 2 * (r & 1) + (N == 1 ? 0 : r >> 1 & 1);    // the lane that has the weight of key c of this column
     const int my = N == 1 ? r + 8 * (c & 1) : r;                         // this lane's key of 16 (the first; the second 8 behind)
@@ -794,6 +794,7 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
     const uint8_t* const kat = mine + r * 64 + c * 16;
     const uint8_t* const vat = mine + V_AT + c * 64 + (r * 8 ^ (c >> 1) * 32);
     float o[8][4] = {}, m = M_START, l = 0.f;
+    [[maybe_unused]] float o3[F32 && N == 2 ? 8 : 1][4] = {};  // the third parts' sums, by columns 0 to 3 of products of their own
 
     // 16 keys: codes at byte `at` of the ring, parameters at `par`
     auto step = [&](auto tail, const int at, const int par, const int key0) {
@@ -843,7 +844,9 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
                 for (int gr = 0; gr < 2; ++gr) {
                     const float a0 = c & 2 ? s[gr][1] : s[gr][0], a1 = c & 2 ? s[gr][3] : s[gr][2];
                     y[gr] = N == 2 ? (j ? a1 : a0) : c & 1 ? a1 : a0;
-                    if (F32) y[gr] += __shfl_xor_sync(0xffffffffu, c & 1 ? a0 : a1, 1);  // the other part's sum
+                    // the other part's sum
+                    if (F32 && N == 1) y[gr] += __shfl_xor_sync(0xffffffffu, c & 1 ? a0 : a1, 1);
+                    if (F32 && N == 2) y[gr] += __shfl_xor_sync(0xffffffffu, c & 2 ? s[gr][2 * j] : s[gr][2 * j + 1], 2);
                 }
                 if (!F32) {
                     y[0] += zero_of(kp[j].x) * qsum[0];
@@ -873,6 +876,10 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
             for (int t = 0; t < 8; ++t) {
                 o[t][0] *= f0; o[t][1] *= f1;
                 o[t][2] *= f0; o[t][3] *= f1;
+                if constexpr (F32 && N == 2) {
+                    o3[t][0] *= f0; o3[t][1] *= f1;
+                    o3[t][2] *= f0; o3[t][3] *= f1;
+                }
             }
         }
         {
@@ -900,7 +907,20 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr) {
                 uint32_t y[4], b0, b1;
-                if constexpr (F32) {
+                [[maybe_unused]] uint32_t b2 = 0u, b3 = 0u;
+                if constexpr (F32 && N == 2) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float x = __shfl_sync(0xffffffffu, ps[k >> 1][gr], from + (k & 1) * 16);
+                        const float rest = x - as_f(as_u(x) & 0xFFFF0000u);
+                        y[k] = r >= 4 ? as_u(rest) : as_u(x);
+                        const uint32_t third = r >= 4 ? 0u : as_u(rest - as_f(as_u(rest) & 0xFFFF0000u));
+                        if (k < 2) b2 |= third >> 16 << (16 * (k & 1));
+                        else b3 |= third >> 16 << (16 * (k & 1));
+                    }
+                    b0 = highs(y[0], y[1]);
+                    b1 = highs(y[2], y[3]);
+                } else if constexpr (F32) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         y[k] = part_of(__shfl_sync(0xffffffffu, ps[0][gr], from + (k & 1) * 16 + (k >> 1)), m1, m2);
@@ -931,6 +951,7 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
                     const uint32_t x4[4] = {fma_bf16x2(u01 & 0x000F000Fu, 0x7E807E80u, zero[0]), fma_bf16x2(u01 & 0x00F000F0u, 0x7C807C80u, zero[0]),
                                             fma_bf16x2(u23 & 0x000F000Fu, 0x7E807E80u, zero[1]), fma_bf16x2(u23 & 0x00F000F0u, 0x7C807C80u, zero[1])};
                     mma_bf16(o[4 * gr + t], x4, b0, b1);
+                    if constexpr (F32 && N == 2) mma_bf16(o3[4 * gr + t], x4, b2, b3);
                 }
             }
         }
@@ -969,6 +990,14 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
             for (int h = 0; h < 2; ++h)
                 *reinterpret_cast<float2*>(so + (at * 2 + h) * HD + d) =
                     make_float2(o[t][h] * 128.f, o[t][2 + h] * 128.f);
+            if constexpr (F32 && N == 2) {
+                if (c < 2) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        *reinterpret_cast<float2*>(so + (((warp * P + 2) * 2 + c) * 2 + h) * HD + d) =
+                            make_float2(o3[t][h] * 128.f, o3[t][2 + h] * 128.f);
+                }
+            }
         }
     }
     if (lane < 4 && (N == 2 || !(lane & 1))) { sh.m[warp][hq] = m; sh.l[warp][hq] = l; }
@@ -995,7 +1024,7 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
 // grid (splits, 8, rows): one piece a block, the blocks of a row's keys dealt evenly to its splits. The splits of a (row,
 // head) are one cluster (at most 8), which merges them through its shared memory.
 template <typename T, int N>
-__global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict__ q, Cache cache, AttnArgs a, T* __restrict__ out) {
+__global__ void __launch_bounds__(WARPS * 32, AN_SM<T, N>) k_kv4_attn(const T* __restrict__ q, Cache cache, AttnArgs a, T* __restrict__ out) {
     pdl_wait();  // upstream results are read below
     pdl_trigger();
     extern __shared__ __align__(128) uint8_t ring[];
@@ -1020,7 +1049,8 @@ __global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn(const T* __restrict_
             if (h < heads) to[((h >> 1) * NQ + (h & 1)) * HD + d] = (T)(L[h] == 0.f ? 0.f : O[h] / L[h]);
         return;
     }
-    __shared__ float all[2 * N][HD], ml[2 * N][2];
+    float(*const all)[HD] = reinterpret_cast<float(*)[HD]>(ring);  // which is free: every copy was waited for
+    __shared__ float ml[2 * N][2];
 #pragma unroll
     for (int h = 0; h < 2 * N; ++h) {
         all[h][d] = O[h];
@@ -1062,10 +1092,10 @@ constexpr int PIECE = HD + 4;  // 16-byte rows
 template <int N>
 __device__ __forceinline__ float* place(float* part, int share, int which) { return part + ((size_t)share * 2 + which) * 2 * N * PIECE; }
 
-// grid: the shares (at most SLOTS); rows <= LINE_ROWS
+// grid: the shares; rows <= LINE_ROWS
 constexpr int LINE_ROWS = 1024;
 template <typename T, int N>
-__global__ void __launch_bounds__(WARPS * 32, 4) k_kv4_attn_line(const T* __restrict__ q, Cache cache, AttnArgs a, T* __restrict__ out) {
+__global__ void __launch_bounds__(WARPS * 32, AN_SM<T, N>) k_kv4_attn_line(const T* __restrict__ q, Cache cache, AttnArgs a, T* __restrict__ out) {
     pdl_wait();  // upstream results are read below
     pdl_trigger();
     extern __shared__ __align__(128) uint8_t ring[];
@@ -1230,21 +1260,22 @@ __global__ void __launch_bounds__(128) k_kv4_combine(Cache c, AttnArgs a, int sh
     out[((size_t)((N == 1 ? row : a.token(row)) + (h >> 1)) * NQ + 2 * g + (h & 1)) * HD + d] = (T)(L == 0.f ? 0.f : O / L);
 }
 
-constexpr int MAX_CLUSTER = 8, SLOTS = 4 * 152;
+constexpr int MAX_CLUSTER = 8;
 struct Plan {
     int splits;  // a cluster's blocks; 0: a line
     int shares;
 };
 // Caches of up to 16 blocks of keys a block of the launch (32 where the pairs fill half the SMs' slots by themselves): one
-// block, or one cluster of up to 8 as the slots allow, for each (row, KV head), in one launch. Longer ones: a line in SLOTS
-// shares (four blocks an SM are resident: one wave) and the launch that merges it. Measured, us: 1 x 8000 keys 10.0 by a
+// block, or one cluster of up to 8 as the slots allow, for each (row, KV head), in one launch. Longer ones: a line in `slots`
+// shares (as many blocks as are resident: one wave) and the launch that merges it. Measured, us: 1 x 8000 keys 10.0 by a
 // cluster, 14.1 by a line; 64 x 20..200 keys 6.0 and 14.3; 16 x 400..4000 17.5 and 18.6; 64 x 800..8000 by one block each 78,
-// by a line 69.
-Plan attn_plan(long long rows, int max_len) {
+// by a line 69. A twentieth of the slots stays free, since clusters do not fill every SM: 19 x 1000 keys in clusters of 3 of
+// 4 blocks an SM 11.1, of 4 (all slots, two waves) 12.6.
+Plan attn_plan(long long rows, int max_len, int slots) {
     const long long pairs = rows * NKV, nblk = (max_len + KVB - 1) / KVB, most = (nblk + 1) / 2;
-    const long long n = std::min({(long long)MAX_CLUSTER, SLOTS / pairs, most});
+    const long long n = std::min({(long long)MAX_CLUSTER, slots * 19 / 20 / pairs, most});
     if (rows > LINE_ROWS || nblk <= (n >= 2 ? 16 * n : 32)) return {(int)std::max(n, 1ll), 0};
-    return {0, (int)std::min<long long>(SLOTS, pairs * most)};
+    return {0, (int)std::min<long long>(slots, pairs * most)};
 }
 
 bool cache_ok(const tts_bb_kv4* c) {
@@ -1349,9 +1380,11 @@ TTS_API tts_bb_status tts_bb_kv4_read(const tts_bb_kv4* cache, int T, const int3
 
 TTS_API size_t tts_bb_kv4_attention_workspace(int B, int S, int max_len) {
     if (B < 1 || S < 1 || S > TTS_BB_KV4_MAX_QUERIES || max_len < 1 || max_len > (1 << 30) || (long long)B * S > 65535) return 0;
-    size_t most = 0;
+    size_t most = 0;  // of both types
     for (int each = 1; each <= std::min(S, 2); ++each)
-        most = std::max(most, (size_t)attn_plan((long long)B * ((S + each - 1) / each), max_len).shares * 2 * 2 * each * PIECE * sizeof(float));
+        for (int an_sm = each == 1 ? 4 : 3; an_sm <= 4; ++an_sm)
+            most = std::max(most, (size_t)attn_plan((long long)B * ((S + each - 1) / each), max_len, an_sm * 152).shares * 2 * 2 * each * PIECE *
+                                      sizeof(float));
     return most;
 }
 
@@ -1367,12 +1400,12 @@ TTS_API tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S
     if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const Cache c = cache_of(cache);
-    // bf16 queries of a sequence two at a time, in the columns of the products that one leaves empty
+    // query tokens of a sequence two at a time, in the columns of the products that one leaves empty
     auto go = [&](auto type_of, auto tokens) {
         typedef decltype(type_of) T;
         constexpr int N = decltype(tokens)::value;
         const int per_seq = (S + N - 1) / N, rows = B * per_seq;
-        const Plan p = attn_plan(rows, max_len);
+        const Plan p = attn_plan(rows, max_len, AN_SM<T, N> * 152);
         const AttnArgs a{seqs, kv_lens, S, max_len, N, per_seq, rows, p.splits, static_cast<float*>(workspace)};
         constexpr size_t smem = RING_BYTES + (size_t)WARPS * (sizeof(T) == 4 ? 3 : 2) * 2 * N * HD * sizeof(float);
         static SmemState grid_state, line_state;
@@ -1389,7 +1422,8 @@ TTS_API tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S
             launch_pdl(k_kv4_combine<T, N>, dim3(NQ * N, rows), 128, 0, st, c, a, p.shares, to);
         }
     };
-    if (type == TTS_BB_T_F32) go(float{}, std::integral_constant<int, 1>{});
+    if (type == TTS_BB_T_F32 && S == 1) go(float{}, std::integral_constant<int, 1>{});
+    else if (type == TTS_BB_T_F32) go(float{}, std::integral_constant<int, 2>{});
     else if (S == 1) go(bf16{}, std::integral_constant<int, 1>{});
     else go(bf16{}, std::integral_constant<int, 2>{});
     return status();
