@@ -350,11 +350,13 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) k_logprobs_warp(const T* __res
 // there: maximum (masked ids become -inf in it), then sums and the candidates: logits that reach a bound below the n_top-th
 // largest, at most LIST of them (with more equal ones, one alternative after the other is looked for). Block 0
 // joins the slices. A few long rows are bound by the passes' latency (64 x 151676 bf16, 20 alternatives: 16 us, of which
-// memory would take 3), many by the passes' instructions (2000 x 25000 fp32: 88 us, 2.3 TB/s).
+// memory would take 3), many by the passes' instructions (2000 x 25000 fp32: 77 us, 2.6 TB/s).
 constexpr int LIST = 1024, MAX_TOP = TTS_BB_LOGPROBS_MAX_TOP;
-// A slice of SLICE_BYTES leaves room for two blocks an SM (2000 x 25000 fp32 in one slice 88 us, in slices of 48 KB 103); one of
-// up to SMALL_SLICE gets 128 threads (16000 x 3100 fp32 77 us, by 256 threads 128; 64 x 100000 fp32 25 us by 128, 20 by 256).
-constexpr int SLICE_BYTES = 100 * 1024, MAX_SLICE_BYTES = 192 * 1024, SMALL_SLICE = 16 * 1024;
+// A slice of SLICE_BYTES leaves room for two blocks an SM (2000 x 25000 fp32 in one slice 77 us, in slices of 48 KB 103). Threads of
+// a block, by its slice: 128 up to SMALL_SLICE (16000 x 3100 fp32 77 us, by 256 threads 128; 64 x 100000 fp32 25 us by 128,
+// 20 by 256), 512 beyond MEDIUM_SLICE, where fewer blocks share an SM (2000 x 25000 fp32 77 us, by 256 threads 88; 800 x 60000
+// in slices of 60 KB 117 by 512, 95 by 256).
+constexpr int SLICE_BYTES = 100 * 1024, MAX_SLICE_BYTES = 192 * 1024, SMALL_SLICE = 16 * 1024, MEDIUM_SLICE = 80 * 1024;
 
 template <typename T> constexpr int EACH = 16 / sizeof(T);  // logits of a 16-byte piece
 __device__ __forceinline__ void unpack(const uint4& u, float (&v)[4], float) {
@@ -733,8 +735,10 @@ void launch(const T* logits, const Args& a, cudaStream_t st) {
         launch_pdl(k_logprobs_long<T>, a.R, THREADS, 0, st, logits, a);
     else if ((long long)slice * sizeof(T) <= SMALL_SLICE)
         launch_block<T, 128>(logits, a, n, slice, st);
-    else
+    else if ((long long)slice * sizeof(T) <= MEDIUM_SLICE)
         launch_block<T, 256>(logits, a, n, slice, st);
+    else
+        launch_block<T, 512>(logits, a, n, slice, st);
 }
 
 }  // namespace
