@@ -454,8 +454,8 @@ _WORDS = _Types(uint32=0, int32=0)
 def _here() -> int:
     """The current device, -2 where there is none yet (and so no tensor on one)."""
     global _here
-    torch = sys.modules["torch"]
-    if not torch.cuda.is_initialized():
+    torch = sys.modules.get("torch")
+    if torch is None or not torch.cuda.is_initialized():
         return -2
     # from now on without the question whether CUDA is initialised, which current_device repeats: 1 us a call
     _here = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)

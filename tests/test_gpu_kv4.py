@@ -267,11 +267,12 @@ def test_attention_dealt_over_all_blocks(lens, S, bps, max_len, io):
         check(s, q[:S], lens[:1], S, out[:S])
 
 
-def test_attention_of_very_many_rows():
-    """More rows than the even deal sums over: one block each, at any length."""
-    lens = [70] * 24
+@pytest.mark.parametrize("B", [24, 40])
+def test_attention_of_very_many_rows(B):
+    """More rows than a block's threads in the even deal, and more than it sums over: one block each, at any length."""
+    lens = [70] * B
     s = filled(21, lens, 130)
-    q = dev(s.rng.standard_normal((24 * 64, NQ, HD))).bfloat16()
+    q = dev(s.rng.standard_normal((B * 64, NQ, HD))).bfloat16()
     out = attend(s, q, lens, 64, 8320)
     check(s, q, lens, 64, out)
 
