@@ -74,6 +74,22 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
+// loads by 32-bit addresses of shared memory (1 x 16384 x 16384 bf16 35.2 us, by pointers 36.3)
+__device__ __forceinline__ uint4 shared4(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 shared2(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t shared1(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -126,8 +142,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2)
     pdl_wait();  // the weights too: the launch before may be the one that packs them
     pdl_trigger();
     constexpr int REC = record_bytes(G);
-    uint8_t* const ring = reinterpret_cast<uint8_t*>(red + 2 * WARPS * C8 * RED_ROW) + warp * STAGES * REC;
-    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(red + 2 * WARPS * C8 * RED_ROW) + warp * STAGES * REC;
     // what comes next: its address, the records of the tile from it on, the tile; and its place in the ring
     constexpr int STEP = SPLIT ? 1 : WARPS, TILE_STEP = SPLIT ? WARPS : 1;
     const int first = team * TILE_STEP + (SPLIT ? warp : 0), group0 = SPLIT ? k0 / G : warp;
@@ -135,9 +150,9 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2)
     int ahead_tile = each > 0 ? first : tiles, left = each;
     const uint8_t* src = packed + ((size_t)first * groups + group0) * REC + lane * 16;
     const long long jump = ((long long)teams * TILE_STEP * groups - (long long)each * STEP) * REC;
-    uint32_t dst = ring_at + lane * 16;
-    const uint32_t dst_end = ring_at + STAGES * REC;
-    const auto fetch = [&] {
+    const uint32_t dst0 = ring_at + lane * 16;
+    const auto fetch = [&](uint32_t place) {
+        const uint32_t dst = dst0 + place;
         if (ahead_tile < tiles) {
 #pragma unroll
             for (int i = 0; i < REC; i += 512)
@@ -146,12 +161,10 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2)
             src += STEP * REC;
             if (--left == 0) { left = each; ahead_tile += teams * TILE_STEP; src += jump; }
         }
-        dst += REC;
-        if (dst >= dst_end) dst -= STAGES * REC;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) fetch();
+    for (int i = 0; i < STAGES - 1; ++i) fetch(i * REC);
     __syncthreads();
     const int chunks = K / 8;  // 8 values each
     for (int u0 = 0; u0 < rows * chunks; u0 += WARPS * 32) {
@@ -200,9 +213,11 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2)
     if (tid < rows) down[tid] = largest[tid] < 0x7F800000u ? 0x1p9f / up_of(tid) : __int_as_float(0x7FC00000);
     __syncthreads();
 
-    int at[NT];  // this lane's column of each tile of 8; behind the last one, that one again: nobody reads its sums
+    uint32_t at[NT];  // this lane's column of each tile of 8; behind the last one, that one again: nobody reads its sums
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) at[nt] = min(nt * 8 + r, cols - 1) * 4 + q;
+    for (int nt = 0; nt < NT; ++nt) at[nt] = (uint32_t)(min(nt * 8 + r, cols - 1) * 4 + q) * 16;
+    const uint32_t x_at = (uint32_t)__cvta_generic_to_shared(xs), piece = cols * 64;  // bytes of a piece
+    const uint32_t code_at = ring_at + lane * (WORDS == 2 ? 8 : 16), par_at = ring_at + G * 8 + r * 4;
     // waits for the cluster's sums of a round, adds up this block's share of it
     const auto add_up = [&](int tile, int turn) {
         cluster_wait();
@@ -229,27 +244,27 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2)
         else go(std::integral_constant<int, 8>{});
     };
     int last = 0, last_turn = 0;
-    const uint8_t* rec = ring;  // the record at hand
+    uint32_t rec = 0, before = (STAGES - 1) * REC;  // the places of the record at hand, and of the one before it
     for (int tile = team * TILE_STEP, turn = 0; tile < tiles; tile += teams * TILE_STEP, turn ^= 1) {
         float acc[NT][4] = {};
-        const uint4* xg = xs + (size_t)(SPLIT ? 0 : warp) * PIECES * cols * 4;
+        uint32_t xg = x_at + (SPLIT ? 0 : warp) * PIECES * piece;
         const int n_rec = !SPLIT || tile + warp < tiles ? each : 0;
-        for (int g = 0; g < n_rec; ++g, xg += (size_t)STEP * PIECES * cols * 4) {
+        for (int g = 0; g < n_rec; ++g, xg += STEP * PIECES * piece) {
             asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
             __syncwarp();
-            fetch();  // into the place of the record before
+            fetch(before);  // which every lane has read
             uint32_t cw[WORDS];
             if constexpr (WORDS == 2) {
-                const uint2 v = *reinterpret_cast<const uint2*>(rec + lane * 8);
+                const uint2 v = shared2(code_at + rec);
                 cw[0] = v.x; cw[1] = v.y;
             } else {
 #pragma unroll
                 for (int i = 0; i < WORDS / 4; ++i) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(rec + (i * 32 + lane) * 16);
+                    const uint4 v = shared4(code_at + rec + i * 512);
                     cw[4 * i] = v.x; cw[4 * i + 1] = v.y; cw[4 * i + 2] = v.z; cw[4 * i + 3] = v.w;
                 }
             }
-            const uint32_t p0 = reinterpret_cast<const uint32_t*>(rec + G * 8)[r], p1 = reinterpret_cast<const uint32_t*>(rec + G * 8)[r + 8];
+            const uint32_t p0 = shared1(par_at + rec), p1 = shared1(par_at + rec + 32);
             const uint32_t z0 = __byte_perm(p0, 0u, 0x1010), z1 = __byte_perm(p1, 0u, 0x1010);
             // times 2^15 and 2^11
             const auto take = [&](uint32_t w, uint32_t (&a)[4]) {
@@ -268,7 +283,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2)
                 take(cw[2 * i + 1], a[1]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const uint4 b = xg[i * cols * 4 + at[nt]];
+                    const uint4 b = shared4(xg + at[nt] + i * piece);
                     mma_f16(d[nt], a[0], b.x, b.y);
                     mma_f16(d[nt], a[1], b.z, b.w);
                 }
@@ -280,7 +295,8 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2)
                 acc[nt][2] += s1 * d[nt][2];
                 acc[nt][3] += s1 * d[nt][3];
             }
-            rec = rec + REC == ring + STAGES * REC ? ring : rec + REC;
+            before = rec;
+            rec = rec == (STAGES - 1) * REC ? 0u : rec + REC;
         }
         float* const mine = red + (size_t)(turn * WARPS + warp) * C8 * RED_ROW;
         if constexpr (SPLIT) {
@@ -386,7 +402,8 @@ void launch_staged(int T_, int N, int K, const T* x, int64_t stride, const uint8
 // - Else over as few blocks as give nearly every SM one, or more than two (between one and two, some SMs have twice the
 //   work of others): fp32 4 x 4096 x 4096 9.9 -> 6.2 us by 4, 8 x 1024 x 4096 13.0 -> 5.8 by 8, 8 x 8192 x 2048 11.0 -> 8.0
 //   by 2 (9.2 by 4), 4 x 16384 x 16384 56 by 2 -> 40 by 4. A single row of few tiles stays whole: 1 x 2048 x 8192 6.7 us,
-//   7.4 by 8.
+//   7.4 by 8; and one of many: 1 x 16384 x 16384 bf16 by 4 took 1.05 times as
+//   long (in a stream of launches; in a captured graph both the same).
 // - As many as two blocks an SM have room for, at most 8; in chunks of fewer rows where a slice is too long even then.
 template <typename T, int G>
 void launch(int T_, int N, int K, const void* x, int64_t stride, const void* packed, void* y, cudaStream_t st) {
@@ -396,7 +413,7 @@ void launch(int T_, int N, int K, const void* x, int64_t stride, const void* pac
     const int tiles = (N + 15) / 16, rounds = (tiles + WARPS - 1) / WARPS, chunks = (T_ + per - 1) / per;
     const int blocks = std::min(tiles, std::max(1, 152 * blocks_an_sm(bytes(per, 1), tiles_for(per * P)) / chunks));
     const long long stage_a_tile = (long long)per * K * blocks / tiles;
-    if (stage_a_tile >= 4500 && (T_ > 1 || rounds >= 32)) {
+    if (stage_a_tile >= 4500 && (T_ > 1 || (rounds >= 32 && tiles < 2 * blocks))) {
         const auto uneven = [&](long long b) { return b < 128 || (b > 152 && b <= 304); };
         for (n = 2; n < 8 && 2 * n <= K / G && uneven((long long)rounds * n * chunks);) n *= 2;
     }
