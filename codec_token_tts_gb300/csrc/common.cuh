@@ -151,18 +151,19 @@ inline cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, size_t
     return cudaLaunchKernelEx(&cfg, k, static_cast<KArgs>(args)...);
 }
 
-// The largest dynamic shared memory of a kernel raised to `bytes`, once a kernel (each has a `State` of its own) and device:
+// The largest dynamic shared memory of a kernel raised to `bytes` (and clusters of more than 8 blocks allowed), once a kernel (each has a `State` of its own) and device:
 // the attribute belongs to the current device.
 struct SmemState {
     std::atomic<uint64_t> done{0};  // a bit a device
 };
 template <typename K>
-inline void allow_smem(SmemState& s, K* kernel, size_t bytes) {
+inline void allow_smem(SmemState& s, K* kernel, size_t bytes, bool clusters_of_16 = false) {
     int dev = 0;
     cudaGetDevice(&dev);
     const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
     if (s.done.load(std::memory_order_acquire) & bit) return;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess &&
+        (!clusters_of_16 || cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess))
         s.done.fetch_or(bit, std::memory_order_release);
 }
 

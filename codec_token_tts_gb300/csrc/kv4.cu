@@ -1022,7 +1022,7 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
 }
 
 // grid (splits, 8, rows): one piece a block, the blocks of a row's keys dealt evenly to its splits. The splits of a (row,
-// head) are one cluster (at most 8), which merges them through its shared memory.
+// head) are one cluster (at most 16), which merges them through its shared memory.
 template <typename T, int N>
 __global__ void __launch_bounds__(WARPS * 32, AN_SM<T, N>) k_kv4_attn(const T* __restrict__ q, Cache cache, AttnArgs a, T* __restrict__ out) {
     pdl_wait();  // upstream results are read below
@@ -1060,7 +1060,9 @@ __global__ void __launch_bounds__(WARPS * 32, AN_SM<T, N>) k_kv4_attn(const T* _
     for (int i = split * WARPS * 32 + d; i < heads * HD; i += a.n_splits * WARPS * 32) {
         const int h = i / HD;
         float m1 = M_START, l1 = 0.f, o1 = 0.f;
+#pragma unroll 8
         for (int s = 0; s < a.n_splits; ++s) m1 = fmaxf(m1, peer(&ml[h][0], s));
+#pragma unroll 8
         for (int s = 0; s < a.n_splits; ++s) {
             const float f = ex2(peer(&ml[h][0], s) - m1);
             l1 += f * peer(&ml[h][1], s);
@@ -1260,21 +1262,23 @@ __global__ void __launch_bounds__(128) k_kv4_combine(Cache c, AttnArgs a, int sh
     out[((size_t)((N == 1 ? row : a.token(row)) + (h >> 1)) * NQ + 2 * g + (h & 1)) * HD + d] = (T)(L == 0.f ? 0.f : O / L);
 }
 
-constexpr int MAX_CLUSTER = 8;
 struct Plan {
     int splits;  // a cluster's blocks; 0: a line
     int shares;
 };
 // Caches of up to 16 blocks of keys a block of the launch (32 where the pairs fill half the SMs' slots by themselves): one
-// block, or one cluster of up to 8 as the slots allow, for each (row, KV head), in one launch. Longer ones: a line in `slots`
-// shares (as many blocks as are resident: one wave) and the launch that merges it. Measured, us: 1 x 8000 keys 10.0 by a
-// cluster, 14.1 by a line; 64 x 20..200 keys 6.0 and 14.3; 16 x 400..4000 17.5 and 18.6; 64 x 800..8000 by one block each 78,
-// by a line 69. A twentieth of the slots stays free, since clusters do not fill every SM: 19 x 1000 keys in clusters of 3 of
-// 4 blocks an SM 11.1, of 4 (all slots, two waves) 12.6.
+// block, or one cluster of up to 8 as the slots allow, for each (row, KV head), in one launch; clusters of 16 for few rows, up
+// to 24 blocks of keys each. Longer ones: a line in `slots`
+// shares (as many blocks as are resident: one wave) and the launch that merges it. Measured, us: 1 x 8000 keys 7.9 by a
+// cluster of 16, 9.9 of 8, 14.1 by a line; 1 x 20000 14.2 and 16.4 by a line; 4 x 4000 fp32 8.5 by clusters of 8, 10.6 of 16,
+// 4 x 16000 20.2 of 16 and 24.1 by a line; 64 x 20..200 keys 6.0 by a block each, 14.3 by a line; 64 x 800..8000 78 by one
+// block each, 69 by a line. A twentieth of the slots stays free, since clusters do not fill every SM: 19 x 1000 keys in
+// clusters of 3 of 4 blocks an SM 11.1, of 4 (all slots, two waves) 12.6.
 Plan attn_plan(long long rows, int max_len, int slots) {
-    const long long pairs = rows * NKV, nblk = (max_len + KVB - 1) / KVB, most = (nblk + 1) / 2;
-    const long long n = std::min({(long long)MAX_CLUSTER, slots * 19 / 20 / pairs, most});
-    if (rows > LINE_ROWS || nblk <= (n >= 2 ? 16 * n : 32)) return {(int)std::max(n, 1ll), 0};
+    const long long pairs = rows * NKV, nblk = (max_len + KVB - 1) / KVB, most = (nblk + 1) / 2, room = slots * 19 / 20;
+    long long n = std::min({8ll, room / pairs, most});
+    if (16 * pairs <= room && nblk > (32 * pairs <= slots ? 32 : 128)) n = 16;
+    if (rows > LINE_ROWS || nblk <= (n == 16 ? 24 * n : n >= 2 ? 16 * n : 32)) return {(int)std::max(n, 1ll), 0};
     return {0, (int)std::min<long long>(slots, pairs * most)};
 }
 
@@ -1409,7 +1413,7 @@ TTS_API tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S
         const AttnArgs a{seqs, kv_lens, S, max_len, N, per_seq, rows, p.splits, static_cast<float*>(workspace)};
         constexpr size_t smem = RING_BYTES + (size_t)WARPS * (sizeof(T) == 4 ? 3 : 2) * 2 * N * HD * sizeof(float);
         static SmemState grid_state, line_state;
-        allow_smem(grid_state, k_kv4_attn<T, N>, smem);
+        allow_smem(grid_state, k_kv4_attn<T, N>, smem, true);
         allow_smem(line_state, k_kv4_attn_line<T, N>, smem);
         const T* const qt = static_cast<const T*>(q);
         T* const to = static_cast<T*>(out);

@@ -246,7 +246,8 @@ def test_attention_against_64_bits(lens, S, sharp, io):
 
 @pytest.mark.parametrize("io", ["float32", "bfloat16"])
 @pytest.mark.parametrize("lens,S,bps,max_len", [([700, 0, 65, 300], 1, 260, 16640), ([0, 130, 0, 2, 515, 0], 3, 260, 16640), ([20000, 9001], 1, 313, 20000),
-                                                ([1], 1, 300, 19200), ([0, 0], 2, 300, 19200), ([40] * 70, 1, 40, 2560), ([90, 5], 64, 130, 8320)])
+                                                ([1], 1, 300, 19200), ([0, 0], 2, 300, 19200), ([40] * 70, 1, 40, 2560), ([90, 5], 64, 130, 8320),
+                                                ([5000, 2100], 1, 90, 5760), ([10000, 33, 9000], 1, 160, 10240), ([2100], 2, 34, 2176), ([30000], 1, 470, 30080)])
 def test_attention_dealt_over_all_blocks(lens, S, bps, max_len, io):
     """Long bounds, where the keys of all rows are dealt evenly to the launch: rows in several shares, several rows in one,
     rows that see nothing, and shares that get nothing."""
