@@ -378,7 +378,7 @@ template <int THREADS> struct Block {
     int count;
     u64 list[LIST];
     u64 top[MAX_TOP];
-    Part part;
+    Part part, parts[8];
 };
 template <int THREADS>
 __device__ __forceinline__ u64 block_max_key(u64 k, u64* sm) {
@@ -569,6 +569,7 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
             for (int x = tid; x < found; x += THREADS) {
                 const u64 k = sm.list[x];
                 int rank = 0;
+#pragma unroll 16
                 for (int j = 0; j < found; ++j) rank += sm.list[j] > k;
                 if (rank < a.n_top) sm.top[rank] = k;
             }
@@ -600,20 +601,23 @@ __global__ void __launch_bounds__(THREADS) k_logprobs_block(const T* __restrict_
     }
     cluster_sync();
     if (part == 0) {
-        for (int s = 1; s < n_parts; ++s)
-            p = join(p, Part{peer(&sm.part.m, s), peer(&sm.part.r, s), peer(&sm.part.t, s), peer(&sm.part.bad, s)});
+        // all that is elsewhere at once
+        const int total = n_parts * a.n_top;  // at most 256
+        for (int x = tid; x < total; x += THREADS) sm.list[x] = peer(&sm.top[x % a.n_top], x / a.n_top);
+        if (tid < n_parts) sm.parts[tid] = Part{peer(&sm.part.m, tid), peer(&sm.part.r, tid), peer(&sm.part.t, tid), peer(&sm.part.bad, tid)};
+        __syncthreads();
+        p = sm.parts[0];
+        for (int s = 1; s < n_parts; ++s) p = join(p, sm.parts[s]);
         const float log_s = log1pf(p.r);
         if (tid == 0) finish(a, row, p, log_s, wanted, tz);
         if (a.n_top) {
-            const int total = n_parts * a.n_top;  // at most 256
-            __syncthreads();
-            for (int x = tid; x < total; x += THREADS) sm.list[x] = peer(&sm.top[x % a.n_top], x / a.n_top);
             for (int j = tid; j < a.n_top; j += THREADS) write_top(a, row, j, 0ull, p, log_s);
             __syncthreads();
             for (int x = tid; x < total; x += THREADS) {
                 const u64 k = sm.list[x];
                 if (!k) continue;
                 int rank = 0;
+#pragma unroll 16
                 for (int j = 0; j < total; ++j) rank += sm.list[j] > k;
                 if (rank < a.n_top) write_top(a, row, rank, k, p, log_s);
             }
