@@ -608,8 +608,9 @@ __device__ __forceinline__ bool attn_row(const Cache& c, const AttnArgs& a, int 
 // two keys: one byte of both keys' words side by side, then one mask for the byte's even dim and one for its odd dim:
 // 000c is the bf16 number c 2^-133 and 00c0 16 c 2^-133 (subnormals again). A multiply-add makes them (code + zero) 2^-7,
 // exact in 8 bits: whole numbers around zero, not 0..15 with a middle added later, because where a softmax is flat the
-// sums cancel and a common offset would cost their digits. P times V's scale of the key and group is B, as bf16 parts by
-// truncation (bf16: two, 16 bits; fp32: three, all 24) in columns of their own.
+// sums cancel and a common offset would cost their digits. P times V's scale of the key and group is B, as bf16 parts in
+// columns of their own: for fp32 three by truncation, all 24 bits; for bf16 two, the first by truncation, the second rounded:
+// within 2^-16 of the weight, on either side (a second part by truncation, as fast, takes 2^-17 off the outputs on average).
 //
 // Two query tokens that follow one another (N = 2): the columns that one token only repeats are the second one's, query
 // c & 1 in a lane, which then has both of 16 keys' scores r and r + 8 of its head; fp32's third parts of the weights take
@@ -660,6 +661,13 @@ __device__ __forceinline__ float zero_of(uint32_t par) { return as_f(par & 0xFFF
 __device__ __forceinline__ uint32_t part_of(float x, uint32_t m1, uint32_t m2) {
     x -= as_f(as_u(x) & m1);
     return as_u(x - as_f(as_u(x) & m2));
+}
+// x as two bf16 parts, the first (by truncation) in the high half, the second (the rest, rounded) in the low one
+__device__ __forceinline__ uint32_t two_parts(float x) {
+    const float first = as_f(as_u(x) & 0xFFFF0000u);
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(first), "f"(x - first));
+    return d;
 }
 // One warp's share of the queries: a head's 128 values (lane l: dims 4l .. 4l + 3) as fp16 parts in `to` ([part][2 heads] rows of
 // 128, to: this head's; 8 dims stand as 0 4 1 5 2 6 3 7; with one part (bf16 queries) the odd ones divided by 16) and in
@@ -931,7 +939,7 @@ __device__ __forceinline__ void attend_piece(const Piece<T>& p, bool more, const
                 } else {
                     uint32_t both[N];  // part 1 below part 0
 #pragma unroll
-                    for (int j = 0; j < N; ++j) both[j] = highs(as_u(ps[j][gr] - as_f(as_u(ps[j][gr]) & 0xFFFF0000u)), as_u(ps[j][gr]));
+                    for (int j = 0; j < N; ++j) both[j] = two_parts(ps[j][gr]);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         y[k] = __shfl_sync(0xffffffffu, both[N == 2 ? k >> 1 : 0], from + (k & 1) * 16 + (N == 1 ? k >> 1 : 0));

@@ -440,3 +440,24 @@ def test_offsets_past_two_gib():
     s.v = [np.array([[decode(flat, p // BLK, 1, h, p % BLK) for h in range(NKV)] for p in range(150)])]
     check(s, q[149:], [150], 1, attend(s, q[149:], [150], 1, 150))
     assert int(s.err) == 0
+
+
+@pytest.mark.parametrize("S,n", [(1, 48), (2, 49)])
+def test_bf16_attention_has_no_bias(S, n):
+    """Outputs of values above zero that round to another bf16 number than the exact ones do so upward as often as downward: weights
+    that are all taken too low would move them all downward."""
+    B = 64
+    s = Setup(7, B, 1)
+    s.k, s.v = [], []
+    for b in range(B):
+        s.k.append(fill(s.pool_h, s.table[b], s.rng.standard_normal((n, NKV, HD)), 0))
+        s.v.append(fill(s.pool_h, s.table[b], np.abs(s.rng.standard_normal((n, NKV, HD))) + 0.5, 1))
+    s.pool.copy_(dev(s.pool_h))
+    q = dev(1.5 * s.rng.standard_normal((B * S, NQ, HD))).bfloat16()
+    got = attend(s, q, [n] * B, S, n).double().cpu().numpy().reshape(B, S, NQ, HD)
+    qh = q.double().cpu().numpy().reshape(B, S, NQ, HD)
+    want = bf16_f64([[attention(qh[b, i], s.k[b], s.v[b], n - (S - 1 - i))[0] for i in range(S)] for b in range(B)])
+    low, high = int((got < want).sum()), int((got > want).sum())
+    # six deviations of a fair coin's difference; and fp32 sums by truncation, at most 4 steps of 2^-23, move 2^-21 of the
+    # outputs' 2^-8 steps
+    assert abs(low - high) <= 6 * np.sqrt(low + high) + got.size * 2.0 ** -13, (low, high)
