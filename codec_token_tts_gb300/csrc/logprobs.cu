@@ -73,8 +73,10 @@ __device__ __forceinline__ Part join(const Part& x, const Part& y) {
     Part o = {a.m, a.r, a.t, x.bad | y.bad};
     if (b.m > NONE) {
         const float d = b.m - a.m, e = ex2(d * LOG2E);
-        o.r += e * (1.f + b.r);
-        o.t += e * (b.t + d * (1.f + b.r));
+        if (e > 0.f) {  // else d may be so large (the type's lowest value) that its product overflows: 0 times an infinity
+            o.r += e * (1.f + b.r);
+            o.t += e * (b.t + d * (1.f + b.r));
+        }
     }
     return o;
 }

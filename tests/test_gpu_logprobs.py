@@ -184,3 +184,17 @@ def test_two_streams_and_a_captured_graph():
     torch.cuda.synchronize()
     assert np.array_equal(lp.double().cpu().numpy(), want[1][0]) and np.array_equal(ids.cpu().numpy(), want[1][3])
     assert np.array_equal(top.double().cpu().numpy(), want[1][4])
+
+
+@pytest.mark.parametrize("io", TYPES)
+@pytest.mark.parametrize("R,V,k", [(1, 20000, 5), (3, 70000, 20), (2, 250001, 32), (305, 26000, 5), (2, 420000, 3)])
+def test_lowest_values_that_are_not_masked(R, V, k, io):
+    """Ids at the type's lowest value that no mask excludes: whole slices of a row of them, behind, before and around the others."""
+    rng = np.random.default_rng(V)
+    dt = getattr(torch, io)
+    for others in (slice(0, V // 2), slice(V // 2, V), slice(V // 3, V // 3 + 3), slice(V - 1, V)):
+        z = torch.full((R, V), torch.finfo(dt).min, dtype=dt, device="cuda")
+        z[:, others] = dev(3.0 * rng.standard_normal((R, others.stop - others.start)) - 5.0).to(dt)
+        targets = rng.integers(0, V, R)
+        targets[0] = others.start
+        check(z, V, targets, k)
