@@ -291,11 +291,10 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) k_logprobs_warp(const T* __res
             if (a.n_top > 12 && a.V > CAP) k = a.n_top * 7 / 10;
             bound = __shfl_sync(ALL, s, k);
         }
-        constexpr float LEAST = -9e29f;  // OUT is no alternative
         uint32_t in[(NV + 31) / 32];
         int count, n;
         while (true) {
-            bound = fmaxf(bound, LEAST);
+            bound = fmaxf(bound, OUT);
             count = 0;
 #pragma unroll
             for (int w = 0; w < (NV + 31) / 32; ++w) {
@@ -303,10 +302,11 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) k_logprobs_warp(const T* __res
 #pragma unroll
                 for (int i = 32 * w; i < NV && i < 32 * w + 32; ++i)
                     if (v[i] >= bound) in[w] |= 1u << (i & 31);
+                in[w] &= mask[w];  // an id that counts may be as low as OUT
                 count += __popc(in[w]);
             }
             n = __reduce_add_sync(ALL, count);
-            if (n < a.n_top && k < a.n_top - 1 && bound > LEAST) {
+            if (n < a.n_top && k < a.n_top - 1 && bound > OUT) {
                 few = k;
                 k = (k + enough + 1) / 2;
             } else if (n > CAP && a.n_top > 8 && k - few > 1) {

@@ -198,3 +198,24 @@ def test_lowest_values_that_are_not_masked(R, V, k, io):
         targets = rng.integers(0, V, R)
         targets[0] = others.start
         check(z, V, targets, k)
+
+
+@pytest.mark.parametrize("io", ["float32", "bfloat16"])
+@pytest.mark.parametrize("R,V,k", [(6, 200, 20), (608, 200, 32), (609, 1025, 5), (608, 1900, 20), (610, 3001, 32), (6, 3001, 20), (6, 100, 8)])
+def test_alternatives_of_very_low_logits(R, V, k, io):
+    """Allowed ids around -1e30 (a common fill) are alternatives as long as they are finite; masked ones are not, whatever their logit."""
+    rng = np.random.default_rng(V)
+    dt = getattr(torch, io)
+    z = torch.full((R, V), -1e30, dtype=dt, device="cuda")
+    z[0::6, 7:10] = dev(rng.standard_normal((len(z[0::6]), 3))).to(dt)
+    z[1::6] = dev(rng.uniform(-1e30, -9e29, (len(z[1::6]), V))).to(dt)
+    z[2::6, ::2] = dev(rng.uniform(-1.1e30, -8e29, (len(z[2::6]), (V + 1) // 2))).to(dt)
+    z[3::6, 5:] = -9.5e29
+    z[4::6, V // 2] = 0.0
+    z[5::6] = -9e29
+    targets = rng.integers(0, V, R)
+    check(z, V, targets, k)
+    ok = rng.random(V) < 0.3
+    ok[8] = True
+    z[:, dev(~ok)] = 1.0
+    check(z, V, targets, k, ok, dev(words(ok)))
