@@ -36,12 +36,12 @@ constexpr int WARPS = 8;
 
 __host__ __device__ constexpr int record_bytes(int G) { return G * 8 + 64; }
 
-// grid (K / G, ceil(N / 16)), 32 threads
+// grid (ceil(N / 16), K / G), 32 threads: up to 65536 tiles, which only a grid's first dimension may have
 __global__ void k_w4_pack(int N, int K, int G, const uint8_t* __restrict__ codes, const bf16* __restrict__ scales,
                           const uint8_t* __restrict__ zeros, uint8_t* __restrict__ packed) {
     pdl_wait();
     pdl_trigger();
-    const int g = blockIdx.x, tile = blockIdx.y, lane = threadIdx.x, r = lane >> 2, q = lane & 3;
+    const int g = blockIdx.y, tile = blockIdx.x, lane = threadIdx.x, r = lane >> 2, q = lane & 3;
     const int groups = K / G, words = G / 16;  // words of a lane
     uint8_t* rec = packed + ((size_t)tile * groups + g) * record_bytes(G);
     for (int i = 0; i < words; ++i) {
@@ -440,7 +440,7 @@ TTS_API tts_bb_status tts_bb_w4_pack(int N, int K, int group, const void* codes,
     if (!sizes_ok(N, K, group) || !codes || !scales || !packed || (uintptr_t)packed % 16 || (uintptr_t)scales % 2)
         return TTS_BB_E_INVALID;
     if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
-    launch_pdl(k_w4_pack, dim3(K / group, (N + 15) / 16), 32, 0, static_cast<cudaStream_t>(stream), N, K, group,
+    launch_pdl(k_w4_pack, dim3((N + 15) / 16, K / group), 32, 0, static_cast<cudaStream_t>(stream), N, K, group,
                static_cast<const uint8_t*>(codes), static_cast<const bf16*>(scales), static_cast<const uint8_t*>(zeros),
                static_cast<uint8_t*>(packed));
     return cudaPeekAtLastError() == cudaSuccess ? TTS_BB_OK : TTS_BB_E_CUDA;

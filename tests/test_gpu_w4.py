@@ -192,3 +192,9 @@ def test_slices_of_a_cluster_captured(N, K, G, T):
             m.tts_bb_w4_linear(T, N, K, G, xs[0], p, out, other.cuda_stream)
         torch.cuda.synchronize()
         assert torch.equal(y, w) and torch.equal(out, want[0])
+
+
+@pytest.mark.parametrize("N", [2**20, 2**20 - 15, 2**20 - 16])
+def test_most_rows_of_weights(N):
+    """The largest matrices that are not refused: more tiles of 16 rows than a grid's second dimension may have."""
+    run(N, 32, 32, 1, "float32", True)
