@@ -8,8 +8,8 @@
 // multiply-adds to (code - zero) 2^-9, exact in fp16. (The subnormal numbers themselves as operands lose up to 5 bits of the
 // products' sum, measured; and zeros by the sums of x, scale (sum x code - zero sum x), lose the digits of a small sum
 // beside one large x whose weight is 0.) Each row of x is scaled by a power of two to a largest magnitude in [2^14, 2^15)
-// and stands in shared memory as fp16: bf16 rows exactly (down to 2^-29 of the row's largest), fp32 rows as two parts,
-// 24 bits together, each part a column of its own. So products are exact and sums fp32.
+// and stands in shared memory as fp16: bf16 rows exactly (down to 2^-29 of the row's largest), fp32 rows as two parts, to
+// within one fp32 step together (twice 11 bits and a sign), each part a column of its own. So products are exact and sums fp32.
 //
 // Layout (tts_bb_w4_pack): for 16 rows of W (one m16n8k16 tile high) and one group, a record of G * 8 bytes of
 // codes and 16 parameter words. Lane (r = lane / 4, q = lane % 4) of a warp finds its codes of the group in
@@ -185,8 +185,9 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2)
         }
     }
     __syncthreads();
-    // 2^(14 - exponent of the largest), the largest taken as at least 2^-103
-    const auto up_of = [&](int row) { return __uint_as_float((268u - min(max(largest[row] >> 23, 24u), 254u)) << 23); };
+    // 2^(14 - exponent of the largest), the largest taken as at least 2^-113: 2^127 is the largest power of two, and brings
+    // what is smaller to whole multiples of fp16's least number, so that no digit is lost there either
+    const auto up_of = [&](int row) { return __uint_as_float((268u - min(max(largest[row] >> 23, 14u), 254u)) << 23); };
     for (int u = tid; u < rows * chunks; u += WARPS * 32) {
         const int row = u / chunks, chunk = u - row * chunks;
         float v[8];

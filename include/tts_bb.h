@@ -598,7 +598,7 @@ tts_bb_status tts_bb_w4_pack(int N, int K, int group, const void* codes, const v
                              void* packed, void* stream);
 /*   x  fp32 or bf16 (type) [T] rows of K, x_stride elements apart (>= K, and 16-byte aligned rows)
  *   y  fp32 or bf16 (the same type) [T][N], 4- or 2-byte aligned
- * A row of x enters to within half an fp32 step of each value, or 2^-39 of the row's largest magnitude where that is
+ * A row of x enters to within one fp32 step of each value, or 2^-39 of the row's largest magnitude where that is
  * more; products are exact and summed in fp32, in an order that depends on the sizes alone. An infinity or a NaN
  * in a row of x makes that row of y NaN. */
 tts_bb_status tts_bb_w4_linear(int T, int N, int K, int group, const void* x, int type, int64_t x_stride,

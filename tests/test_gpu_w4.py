@@ -198,3 +198,25 @@ def test_slices_of_a_cluster_captured(N, K, G, T):
 def test_most_rows_of_weights(N):
     """The largest matrices that are not refused: more tiles of 16 rows than a grid's second dimension may have."""
     run(N, 32, 32, 1, "float32", True)
+
+
+@pytest.mark.parametrize("io", ["float32", "bfloat16"])
+@pytest.mark.parametrize("K,T", [(32, 32), (4096, 8)])
+def test_tiny_rows_of_x(K, T, io):
+    """Rows whose largest value lies near the least numbers of the type, subnormal ones too, keep their digits."""
+    m = tb()
+    rng = np.random.default_rng(K)
+    N, G = 48, 32
+    codes = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+    scales, z = np.full((N, K // G), 2.0 ** 30), rng.integers(0, 16, (N, K // G), dtype=np.uint8)
+    p = pack(N, K, G, codes, scales, z)
+    w = unpack_w4(codes, scales, z, G)
+    for top in (2.0 ** -100, 2.0 ** -104, 2.0 ** -113, 2.0 ** -114, 2.0 ** -120, 1.7e-38, 1e-40, 2.0 ** -149):
+        x = torch.zeros(T, K, dtype=getattr(torch, io), device="cuda")
+        x[torch.arange(T), torch.arange(T) * (K // T)] = dev(top * (1 + rng.random(T))).to(x.dtype)
+        y = torch.empty(T, N, dtype=x.dtype, device="cuda")
+        m.tts_bb_w4_linear(T, N, K, G, x, p, y, torch.cuda.current_stream().cuda_stream)
+        want = x.double().cpu().numpy() @ w.T
+        # one value a row: within one step (2 U), its two parts' products added (U); the scale is a power of two
+        tol = (2.0 ** -8 + 6 * U if io == "bfloat16" else 6 * U) * np.abs(want)
+        assert (np.abs(y.double().cpu().numpy() - want) <= tol).all(), top
