@@ -618,10 +618,11 @@ __device__ __forceinline__ bool attn_row(const Cache& c, const AttnArgs& a, int 
 // sequences of 8 tokens and 2000 keys 28 -> 19 us (fp32 33 -> 28), 44 of 7 and 943 fp32 49 -> 40. The first token does not see the second's key: its weight is 0 there.
 //
 // Softmax: a running reference m for each head, moved only when a score exceeds it by 8 (log2): then sums and O are
-// rescaled. It starts at -1e30, not -inf, so that no difference of infinities arises.
+// rescaled. It starts at about the lowest number, not -inf, so that no difference of infinities arises, and no finite score
+// has a weight of 0 beside nothing larger.
 constexpr int WARPS = 4, STAGES = 2, UNIT = 32, UNIT_BYTES = 4608;  // K and V codes 2048 each, parameters 256 each
 constexpr int V_AT = 2048, KP_AT = 4096, VP_AT = 4352, RING_BYTES = WARPS * STAGES * UNIT_BYTES;
-constexpr float M_START = -1e30f, M_SLACK = 8.f;
+constexpr float M_START = -3.4e38f, M_SLACK = 8.f;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");

@@ -461,3 +461,24 @@ def test_bf16_attention_has_no_bias(S, n):
     # six deviations of a fair coin's difference; and fp32 sums by truncation, at most 4 steps of 2^-23, move 2^-21 of the
     # outputs' 2^-8 steps
     assert abs(low - high) <= 6 * np.sqrt(low + high) + got.size * 2.0 ** -13, (low, high)
+
+
+@pytest.mark.parametrize("io", ["float32", "bfloat16"])
+@pytest.mark.parametrize("S,max_len", [(1, 70), (2, 70), (1, 1000), (1, 16640), (2, 16640)])
+def test_attention_of_very_low_scores(S, max_len, io):
+    """Scores around -1e32, all of them: the largest one's key has the whole weight."""
+    s = Setup(8, 2, 260)
+    lens = [70, 66]
+    s.k, s.v = [], []
+    for b, n in enumerate(lens):
+        k = 1e15 * (1 + 0.1 * s.rng.standard_normal((n, NKV, HD)))
+        k[11 + b] *= 0.5
+        s.k.append(fill(s.pool_h, s.table[b], k, 0))
+        s.v.append(fill(s.pool_h, s.table[b], s.rng.standard_normal((n, NKV, HD)), 1))
+    s.pool.copy_(dev(s.pool_h))
+    q = dev(-1e16 * (1 + 0.1 * s.rng.standard_normal((2 * S, NQ, HD)))).to(getattr(torch, io))
+    out = attend(s, q, lens, S, max_len).double().cpu().numpy()
+    for b in range(2):
+        want = s.v[b][11 + b].repeat(2, 0)
+        for i in range(S):
+            assert (np.abs(out[b * S + i] - want) <= np.abs(want) * (2.0 ** -8 if io == "bfloat16" else 4 * U)).all()
