@@ -151,6 +151,12 @@ inline cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, size_t
     return cudaLaunchKernelEx(&cfg, k, static_cast<KArgs>(args)...);
 }
 
+// Addresses of 32-bit arrays (or NULL) that are 4-byte aligned: what a kernel would fault on otherwise.
+template <typename... P>
+inline bool words_aligned(const P*... p) {
+    return ((reinterpret_cast<uintptr_t>(p) | ...) & 3) == 0;
+}
+
 // The largest dynamic shared memory of a kernel raised to `bytes` (and clusters of more than 8 blocks allowed), once a kernel (each has a `State` of its own) and device:
 // the attribute belongs to the current device.
 struct SmemState {

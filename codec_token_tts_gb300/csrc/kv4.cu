@@ -1295,7 +1295,7 @@ Plan attn_plan(long long rows, int max_len, int slots) {
 
 bool cache_ok(const tts_bb_kv4* c) {
     return c && c->pool && c->page_table && c->n_blocks >= 1 && c->n_seqs >= 1 && c->blocks_per_seq >= 1 &&
-           (uintptr_t)c->pool % 16 == 0;
+           (uintptr_t)c->pool % 16 == 0 && words_aligned(c->page_table, c->err);
 }
 Cache cache_of(const tts_bb_kv4* c) {
     return Cache{static_cast<uint8_t*>(c->pool), c->page_table, c->err, c->n_blocks, c->n_seqs, c->blocks_per_seq};
@@ -1364,7 +1364,8 @@ TTS_API tts_bb_status tts_bb_kv4_append(const tts_bb_kv4* cache, int T, const vo
                                         void* q_out, int q_type, void* stream) {
     if (!cache_ok(cache) || T < 1 || !qkv || !q_norm || !k_norm || !cos_table || !sin_table || n_pos < 1 || !seqs ||
         !positions || !type_ok(qkv_type) || !type_ok(q_type) || !(eps >= 0.f) || qkv_stride < QKV || qkv_stride % (qkv_type == TTS_BB_T_F32 ? 4 : 8) ||
-        !aligned(qkv) || !aligned(q_out) || !aligned(q_norm) || !aligned(k_norm) || !aligned(cos_table) || !aligned(sin_table))
+        !aligned(qkv) || !aligned(q_out) || !aligned(q_norm) || !aligned(k_norm) || !aligned(cos_table) || !aligned(sin_table) ||
+        !words_aligned(seqs, positions))
         return TTS_BB_E_INVALID;
     if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1381,7 +1382,8 @@ TTS_API tts_bb_status tts_bb_kv4_append(const tts_bb_kv4* cache, int T, const vo
 
 TTS_API tts_bb_status tts_bb_kv4_read(const tts_bb_kv4* cache, int T, const int32_t* seqs, const int32_t* positions,
                                       void* k_out, void* v_out, void* stream) {
-    if (!cache_ok(cache) || T < 1 || !seqs || !positions || !k_out || !v_out || (uintptr_t)k_out % 16 || (uintptr_t)v_out % 16)
+    if (!cache_ok(cache) || T < 1 || !seqs || !positions || !k_out || !v_out || (uintptr_t)k_out % 16 || (uintptr_t)v_out % 16 ||
+        !words_aligned(seqs, positions))
         return TTS_BB_E_INVALID;
     if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
     const auto go = [&](auto k, int n) {
@@ -1408,7 +1410,8 @@ TTS_API tts_bb_status tts_bb_kv4_attention(const tts_bb_kv4* cache, int B, int S
                                            void* workspace, size_t workspace_bytes, void* stream) {
     if (!cache_ok(cache) || B < 1 || S < 1 || S > TTS_BB_KV4_MAX_QUERIES || (long long)B * S > 65535 || !q || !kv_lens ||
         !out || !type_ok(type) || !aligned(q) || !aligned(out) || max_len < 1 || max_len > (1 << 30) ||
-        (long long)max_len > (long long)cache->blocks_per_seq * KVB || (!seqs && B > cache->n_seqs))
+        (long long)max_len > (long long)cache->blocks_per_seq * KVB || (!seqs && B > cache->n_seqs) ||
+        !words_aligned(seqs, kv_lens))
         return TTS_BB_E_INVALID;
     const size_t need = tts_bb_kv4_attention_workspace(B, S, max_len);
     if (need && (!workspace || workspace_bytes < need || (uintptr_t)workspace % 16)) return TTS_BB_E_INVALID;

@@ -758,7 +758,8 @@ TTS_API tts_bb_status tts_bb_token_logprobs(int R, int V, const void* logits, in
     if (R < 1 || R > (1 << 27) || V < 1 || V > (1 << 30) || !logits || row_stride < V || n_top < 0 || n_top > TTS_BB_LOGPROBS_MAX_TOP ||
         type < TTS_BB_T_F32 || type > TTS_BB_T_F16 || (uintptr_t)logits % (type == TTS_BB_T_F32 ? 4 : 2) ||
         (targets && !logprob) || (n_top && (!top_ids || !top_logprobs)) ||
-        (allowed && allowed_stride != 0 && allowed_stride < ((int64_t)V + 31) / 32))
+        (allowed && allowed_stride != 0 && allowed_stride < ((int64_t)V + 31) / 32) ||
+        !words_aligned(targets, allowed, logprob, entropy, lse, top_ids, top_logprobs))
         return TTS_BB_E_INVALID;
     const size_t need = tts_bb_token_logprobs_workspace(R, V, n_top);
     if (need && (!workspace || workspace_bytes < need || (uintptr_t)workspace % 16)) return TTS_BB_E_INVALID;

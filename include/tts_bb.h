@@ -496,9 +496,10 @@ tts_bb_status tts_bb_gqa_decode_attention_static(const void* q, const void* kv_p
  * default stream), allocates nothing, keeps nothing between calls and may be
  * captured into a CUDA graph. Calls on several streams or threads at once are
  * independent as long as what they write (outputs, workspaces, the same cache
- * rows) is not shared. Host-side argument errors return TTS_BB_E_INVALID before
- * anything is enqueued; TTS_BB_E_CUDA: a CUDA error was already pending (it
- * is left pending) or a launch failed. */
+ * rows) is not shared. Arrays of int32, uint32 and fp32 are 4-byte aligned, others as
+ * stated. Host-side argument errors return TTS_BB_E_INVALID before anything is
+ * enqueued; TTS_BB_E_CUDA: a CUDA error was already pending (it is left pending)
+ * or a launch failed. */
 
 /* Element types of arrays that may have several. */
 enum { TTS_BB_T_F32 = 0, TTS_BB_T_BF16 = 1, TTS_BB_T_F16 = 2 };

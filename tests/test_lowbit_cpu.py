@@ -173,3 +173,17 @@ def test_the_plain_quantiser():
     swapped = code.copy()
     swapped[:, [0, 64]] = swapped[:, [64, 0]]
     assert not np.array_equal(code_bytes(code), code_bytes(swapped))
+
+
+def test_misaligned_words_are_refused():
+    """32-bit arrays off a 4-byte boundary, which a kernel would fault on."""
+    m = tb()
+    off = [P + 1, P + 2, P + 3]
+    bad_cache = [C.byref(cache(m, **{k: v})) for k in ("page_table", "err") for v in off]
+    refused(m.lib.tts_bb_kv4_append, dict(cache=C.byref(cache(m)), T=1, qkv=P, qkv_type=0, stride=4096, gq=P, gk=P, eps=1e-6, cos=P, sin=P, n_pos=1, seqs=P,
+                                          pos=P, q=P, q_type=0, stream=None), dict(cache=bad_cache, seqs=off, pos=off))
+    refused(m.lib.tts_bb_kv4_read, dict(cache=C.byref(cache(m)), T=1, seqs=P, pos=P, k=P, v=P, stream=None), dict(cache=bad_cache, seqs=off, pos=off))
+    refused(m.lib.tts_bb_kv4_attention, dict(cache=C.byref(cache(m)), B=2, S=1, q=P, type=0, seqs=None, lens=P, max_len=128, out=P, ws=P, n=2**40, stream=None),
+            dict(cache=bad_cache, seqs=off, lens=off))
+    refused(m.lib.tts_bb_token_logprobs, dict(R=2, V=100, z=P, type=0, stride=100, targets=P, allowed=P, a_stride=4, k=2, lp=P, ent=P, lse=P, ids=P, top=P, ws=P,
+                                              n=2**40, stream=None), {k: off for k in ("targets", "allowed", "lp", "ent", "lse", "ids", "top")})
