@@ -482,3 +482,90 @@ def test_attention_of_very_low_scores(S, max_len, io):
         want = s.v[b][11 + b].repeat(2, 0)
         for i in range(S):
             assert (np.abs(out[b * S + i] - want) <= np.abs(want) * (2.0 ** -8 if io == "bfloat16" else 4 * U)).all()
+
+
+def queries_ok(got, q, rows, bf16):
+    """As in test_append_writes_the_definitions_bytes: 16 U of the pair's |x cos| + |x' sin|, then one rounding of the type."""
+    pair = np.sqrt(q[..., :64] ** 2 + q[..., 64:] ** 2)
+    tol = 16 * U * np.sqrt(2) * np.concatenate((pair, pair), -1) + (np.abs(q) * 2.0 ** -8 if bf16 else 0)
+    return (np.abs(got - q) <= tol)[rows].all()
+
+
+@pytest.mark.parametrize("io", ["float32", "bfloat16"])
+@pytest.mark.parametrize("T,q_io", [(1900, "float32"), (1900, "bfloat16"), (4099, "float32"), (4099, "bfloat16"), (4099, None)])
+def test_append_of_prompts(T, q_io, io):
+    """More tokens than blocks, so that a block goes on with further ones, and enough of fp32 for two launches; padding before, among and
+    behind the tokens, one token out of range among them, queries of either type or none."""
+    s = Setup(T, 3, 24)
+    x = s.rng.standard_normal((T, 4096)) * np.exp(0.6 * s.rng.standard_normal((1, 4096))) + 0.3 * s.rng.standard_normal((1, 4096))
+    xd = dev(x).to(getattr(torch, io))
+    x = xd.double().cpu().numpy()
+    cells = s.rng.permutation(3 * 24 * BLK)[:T]
+    seqs, pos = (cells // (24 * BLK)).astype(np.int32), (cells % (24 * BLK)).astype(np.int32)
+    seqs[s.rng.random(T) < 0.2] = -1
+    seqs[[0, 912, 1023, T - 1]] = -1
+    seqs[1024] = 3
+    q_out = None if q_io is None else torch.full((T + 1, NQ, HD), 7.0, dtype=getattr(torch, q_io), device="cuda")
+    assert s.append(xd, seqs, pos, q_out) == 0
+    assert int(s.err) == tb().KV4_ERR_RANGE
+    seqs[1024] = -1
+    pool, q = s.expect(x, seqs, pos)
+    same_pool(s.pool.cpu().numpy(), pool)
+    if q_out is not None:
+        got, live = q_out.double().cpu().numpy(), seqs >= 0
+        assert (got[:T][~live] == 7).all() and (got[T] == 7).all()
+        assert queries_ok(got[:T], q, live, q_io == "bfloat16")
+
+
+@pytest.mark.parametrize("io,q_io", [("float32", "bfloat16"), ("bfloat16", "float32")])
+def test_append_with_queries_of_the_other_type(io, q_io):
+    s = Setup(31, 2, 2)
+    xd = dev(s.rng.standard_normal((50, 4096))).to(getattr(torch, io))
+    seqs, pos = np.repeat([0, 1], 25).astype(np.int32), np.tile(np.arange(25), 2).astype(np.int32) * 5
+    q_out = torch.zeros(50, NQ, HD, dtype=getattr(torch, q_io), device="cuda")
+    assert s.append(xd, seqs, pos, q_out) == 0
+    pool, q = s.expect(xd.double().cpu().numpy(), seqs, pos)
+    same_pool(s.pool.cpu().numpy(), pool)
+    assert queries_ok(q_out.double().cpu().numpy(), q, np.arange(50), q_io == "bfloat16")
+
+
+def test_append_of_rows_far_apart():
+    """Rows of QKV more than 2^32 bytes from one another."""
+    s = Setup(32, 1, 1)
+    far = 2**29 + 8
+    xd = torch.empty(2 * far + 4096, dtype=torch.float32, device="cuda").as_strided((3, 4096), (far, 1))
+    xd.copy_(dev(s.rng.standard_normal((3, 4096)).astype(np.float32)))
+    assert s.append(xd, [0] * 3, np.arange(3)) == 0
+    same_pool(s.pool.cpu().numpy(), s.expect(xd.double().cpu().numpy(), [0] * 3, np.arange(3))[0])
+
+
+def test_read_of_prompts():
+    """Enough tokens for four a thread, with a remainder of three, padding and a row out of range among them."""
+    T, n = 4867, 300
+    s = Setup(9, 1, 5)
+    val = [fill(s.pool_h, s.table[0], s.rng.standard_normal((n, NKV, HD)), w) for w in (0, 1)]
+    s.pool.copy_(dev(s.pool_h))
+    seqs, pos = np.zeros(T, np.int32), s.rng.integers(0, n, T).astype(np.int32)
+    seqs[s.rng.random(T) < 0.2] = -1
+    seqs[[T - 1, 17]] = 0, 1
+    k, v = (torch.full((T + 4, NKV, HD), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert tb().tts_bb_kv4_read(s.cache, T, dev(seqs), dev(pos), k, v, stream=stream()) == 0
+    assert int(s.err) == tb().KV4_ERR_RANGE
+    live = seqs == 0
+    for y, w in ((k, val[0]), (v, val[1])):
+        y = y.double().cpu().numpy()
+        assert (y[T:] == 9).all() and (y[:T][~live] == 9).all() and np.array_equal(y[:T][live], bf16_f64(w)[pos][live])
+
+
+def test_attention_of_the_most_sequences():
+    """As many query tokens as a call takes, over a few cache rows that many of them read."""
+    B = 65535
+    lens = [3, 70, 1]
+    s = filled(33, lens, 2)
+    rows = (np.arange(B) % 4 - 1).astype(np.int32)
+    kl = np.array([0] + lens, np.int32)[rows + 1]
+    q = torch.randn(B, NQ, HD, device="cuda", generator=torch.Generator("cuda").manual_seed(3)).bfloat16()
+    out = attend(s, q, kl, 1, 70, rows)
+    some = [0, 1, 2, 3, 30000, 30001, 30002, B - 3, B - 2, B - 1]
+    check(s, q[some], kl[some], 1, out[some], rows[some])
+    assert bool((out[::4] == 5).all()) and int(s.err) == 0

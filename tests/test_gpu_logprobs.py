@@ -219,3 +219,17 @@ def test_alternatives_of_very_low_logits(R, V, k, io):
     ok[8] = True
     z[:, dev(~ok)] = 1.0
     check(z, V, targets, k, ok, dev(words(ok)))
+
+
+@pytest.mark.parametrize("V,R", [(200, 3), (40000, 3), (420000, 2)])
+def test_rows_far_apart(V, R):
+    """Rows of logits and of masks more than 2^32 bytes from one another."""
+    rng = np.random.default_rng(V)
+    far, mask_far = 2**30 + 4, 2**30 + 3
+    z = torch.empty((R - 1) * far + V, dtype=torch.float32, device="cuda").as_strided((R, V), (far, 1))
+    z.copy_(dev(3.0 * rng.standard_normal((R, V)).astype(np.float32)))
+    ok = rng.random((R, V)) < 0.7
+    n = -(-V // 32)
+    allowed = torch.empty((R - 1) * mask_far + n, dtype=torch.int32, device="cuda").as_strided((R, n), (mask_far, 1))
+    allowed.copy_(dev(np.stack([words(o) for o in ok])))
+    check(z, V, rng.integers(0, V, R), 7, ok, allowed)

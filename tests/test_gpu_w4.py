@@ -220,3 +220,18 @@ def test_tiny_rows_of_x(K, T, io):
         # one value a row: within one step (2 U), its two parts' products added (U); the scale is a power of two
         tol = (2.0 ** -8 + 6 * U if io == "bfloat16" else 6 * U) * np.abs(want)
         assert (np.abs(y.double().cpu().numpy() - want) <= tol).all(), top
+
+
+def test_rows_of_x_far_apart():
+    """Rows more than 2^32 bytes from one another."""
+    m = tb()
+    rng = np.random.default_rng(4)
+    N, K, G, far = 40, 256, 64, 2**29 + 4
+    codes, scales, z = weights(rng, N, K, G, True)
+    p = pack(N, K, G, codes, scales, z)
+    x = torch.empty(4 * far + K, dtype=torch.float32, device="cuda").as_strided((3, K), (2 * far, 1))
+    x.copy_(dev(rng.standard_normal((3, K)).astype(np.float32)))
+    y = torch.empty(3, N, device="cuda")
+    m.tts_bb_w4_linear(3, N, K, G, x, p, y, torch.cuda.current_stream().cuda_stream)
+    xh, w = x.double().cpu().numpy(), unpack_w4(codes, scales, z, G)
+    assert (np.abs(y.double().cpu().numpy() - xh @ w.T) <= 2 * (K + 16) * U * (np.abs(xh) @ np.abs(w).T)).all()
