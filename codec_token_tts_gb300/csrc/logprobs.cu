@@ -146,8 +146,8 @@ __device__ __forceinline__ f2 fmap(f2 a, f2 b, f2 c) {
 // on; 20: 57 and 62).
 // What bounds it are the instructions of these passes (49152 x 1025 fp32 with a mask and 5 alternatives: 47 us, 4.3 TB/s), so
 // a pass is kept to what most rows need; and their number, since code that does not fit the instruction cache stalls: what
-// few rows need is a loop over memory. These are rows with a logit that is not within 1e30 (a NaN, an infinity, the
-// type's lowest value) and rows with more equal candidates than CAP.
+// few rows need is a loop over memory. These are rows with an allowed logit that is not within 1e30 (a NaN, an infinity, the
+// type's lowest value: 49152 x 1025 with -inf in every row 444 us) and rows with more equal candidates than CAP.
 constexpr int ROW_WARPS = 4, CAP = 96;
 constexpr float OUT = -1e30f;  // stands for a masked logit
 
@@ -350,7 +350,8 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) k_logprobs_warp(const T* __res
 // A row cut into the slices of 1, 2, 4 or 8 blocks, each slice staged in shared memory (16-byte pieces where the row's alignment
 // has them; the places before and behind it hold -inf, so that all of it is read in 16-byte pieces) and read three times
 // there: maximum (masked ids become -inf in it), then sums and the candidates: logits that reach a bound below the n_top-th
-// largest, at most LIST of them (with more equal ones, one alternative after the other is looked for). Block 0
+// largest, at most LIST of them (with more equal ones, or where the only logits above -inf lie in few of the warps' places, one
+// alternative after the other is looked for: 64 x 151676 with 1500 ids side by side, 20 alternatives 158 us). Block 0
 // joins the slices. A few long rows are bound by the passes' latency (64 x 151676 bf16, 20 alternatives: 16 us, of which
 // memory would take 3), many by the passes' instructions (2000 x 25000 fp32: 77 us, 2.6 TB/s).
 constexpr int LIST = 1024, MAX_TOP = TTS_BB_LOGPROBS_MAX_TOP;
@@ -749,20 +750,18 @@ void launch(const T* logits, const Args& a, cudaStream_t st) {
 
 }  // namespace
 
-TTS_API size_t tts_bb_token_logprobs_workspace(int, int, int) { return 0; }
+TTS_API size_t tts_bb_token_logprobs_workspace(int, int, int) { return 0; }  // no sizes need any
 
 TTS_API tts_bb_status tts_bb_token_logprobs(int R, int V, const void* logits, int type, int64_t row_stride,
                                             const int32_t* targets, const uint32_t* allowed, int64_t allowed_stride,
                                             int n_top, float* logprob, float* entropy, float* lse, int32_t* top_ids,
-                                            float* top_logprobs, void* workspace, size_t workspace_bytes, void* stream) {
+                                            float* top_logprobs, void* /*workspace*/, size_t /*workspace_bytes*/, void* stream) {
     if (R < 1 || R > (1 << 27) || V < 1 || V > (1 << 30) || !logits || row_stride < V || n_top < 0 || n_top > TTS_BB_LOGPROBS_MAX_TOP ||
         type < TTS_BB_T_F32 || type > TTS_BB_T_F16 || (uintptr_t)logits % (type == TTS_BB_T_F32 ? 4 : 2) ||
         (targets && !logprob) || (n_top && (!top_ids || !top_logprobs)) ||
         (allowed && allowed_stride != 0 && allowed_stride < ((int64_t)V + 31) / 32) ||
         !words_aligned(targets, allowed, logprob, entropy, lse, top_ids, top_logprobs))
         return TTS_BB_E_INVALID;
-    const size_t need = tts_bb_token_logprobs_workspace(R, V, n_top);
-    if (need && (!workspace || workspace_bytes < need || (uintptr_t)workspace % 16)) return TTS_BB_E_INVALID;
     if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const Args a{R, V, n_top, row_stride, allowed_stride, targets, allowed, logprob, entropy, lse, top_ids, top_logprobs};

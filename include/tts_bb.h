@@ -542,7 +542,7 @@ typedef struct {
 tts_bb_status tts_bb_rope_tables(double theta, int n_pos, float* cos_table, float* sin_table);
 
 /* Append T tokens: q/k RMSNorm, half-rotate RoPE and the 4-bit quantisation of keys and values, in one
- * launch. Token t belongs to cache row seqs[t] at position positions[t]; a negative seqs[t] is padding:
+ * launch (fp32 prompts in two). Token t belongs to cache row seqs[t] at position positions[t]; a negative seqs[t] is padding:
  * nothing is done for it. A token whose row, position or page is out of range is skipped as a whole (its
  * q_out row too) and reported in cache->err. The (row, position) pairs of one call must differ, else what
  * that position holds is unspecified.
@@ -566,7 +566,7 @@ tts_bb_status tts_bb_kv4_read(const tts_bb_kv4* cache, int T, const int32_t* seq
 
 /* Grouped-query attention over the cache, S causal query tokens for each of B sequences: a decode step
  * (S = 1) or a short chunk whose keys are already appended. Query head h reads KV head h / 2, scale
- * 1 / sqrt(128), softmax and sums in fp32.
+ * 1 / sqrt(128), softmax and sums in fp32: keys and values of magnitudes up to 1e25 leave room for them.
  *   q, out    fp32 or bf16 (type) [B][S][16][128], 16-byte aligned
  *   seqs      int32 [B], the cache row of each sequence (negative: padding, its out rows are left as
  *             they were), or NULL: sequence b reads row b
@@ -619,8 +619,12 @@ tts_bb_status tts_bb_w4_linear(int T, int N, int K, int group, const void* x, in
  * Outputs may be NULL (top_* where n_top is 0, logprob where targets is NULL). A row with nothing left
  * has logprob and lse -inf and entropy 0; an allowed NaN or +inf makes the row's numbers NaN and its
  * ids -1.
- *   workspace at least tts_bb_token_logprobs_workspace(R, V, n_top) bytes, 16-byte aligned (NULL where that is
- *            0); written before it is read, not shared by calls that overlap */
+ * Slower, with the same results: many rows of up to 96 * 32 logits that hold an allowed one of -inf or beyond 1e30 in
+ * magnitude (49152 x 1025: ten times), alternatives of rows whose ids of probability above 0 all lie in one of their parts
+ * (64 x 151676, 1500 ids side by side: ten times), and rows of more than 393216 fp32 or 786432 16-bit logits, which
+ * a single block reads once more for each alternative. The allowed bits exclude ids at no cost.
+ *   workspace  not used: no sizes need one so far, tts_bb_token_logprobs_workspace gives 0 and NULL will do. Callers that
+ *            ask and pass what is asked for need no change where that ends */
 #define TTS_BB_LOGPROBS_MAX_TOP 32
 size_t tts_bb_token_logprobs_workspace(int R, int V, int n_top);
 tts_bb_status tts_bb_token_logprobs(int R, int V, const void* logits, int type, int64_t row_stride,
