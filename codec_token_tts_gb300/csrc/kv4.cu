@@ -374,8 +374,8 @@ __device__ __forceinline__ bool settle(const T* x, const bf16* gain, const float
 // grid (tokens at most, parts), 128 threads: a token's 16 q heads, or its 8 k and 8 v heads, four a warp; a block goes on with
 // the token a grid further, whose row is on its way meanwhile. q and k: RMSNorm over the head with its gain, then the
 // pairs (i, i + 64) rotated by the token's row of the cos / sin tables.
-// Bound by memory (8 or 16 KB read, 4 or 8 KB + 1152 B written for a token) and, nearly as much, by its instructions: 32768 bf16
-// tokens 107 us, 4.1 TB/s (memory alone: 65 us).
+// Bound by memory (8 or 16 KB read, 4 or 8 KB + 1152 B written for a token) and, nearly as much, by its instructions: 24463 bf16
+// tokens (16 prompts padded to 2048) 107 us, 3.2 TB/s (memory alone: 50 us); fp32 159 us, 4.0 TB/s (95 us).
 //
 // A code next to a border between two would fall either way on the rounding of a 32-bit norm, and one
 // code off is a whole scale. Where quant32 is not sure (about 3 % of the fours of k heads) those codes, or the four heads where
@@ -519,7 +519,7 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 }
 // grid ceil(T / N), 256 threads: thread (K or V, head, word) unpacks one word (8 dims) of each of N tokens, whose addresses
 // and words are all on their way before the first is unpacked: bound by the latency of three loads in a row where a thread has
-// one token, so long calls take four (32768 tokens 26 us, by one 46).
+// one token, so long calls take four (24463 tokens and 8305 of padding 26 us, 4.9 TB/s; by one 46 us).
 template <int N>
 __global__ void __launch_bounds__(256) k_kv4_read(int T, const int32_t* __restrict__ seqs, const int32_t* __restrict__ positions,
                                                   Cache c, bf16* __restrict__ k_out, bf16* __restrict__ v_out) {
@@ -598,9 +598,10 @@ __device__ __forceinline__ bool attn_row(const Cache& c, const AttnArgs& a, int 
 // pairs (d, d + 4), which only permutes the contraction; Q of the dims that come as 16 c is divided by 16. Products are exact
 // and sums fp32. The zero point joins by the queries' sum: s (sum q code + zero sum q). Q is scaled by a power of two to a
 // largest magnitude in [2^14, 2^15). bf16 queries are then exact in fp16 (down to 2^-25 of the head's largest); column n
-// holds head n & 1, so every lane has both heads' scores of its keys. fp32 queries enter as two fp16 parts, 24 bits
-// together, part (n >> 1) & 1 of head n & 1 in column n; and their codes become (code + zero) 2^-9 first, by one exact
-// multiply-add each: the subnormal numbers as operands lose up to 5 bits of a product's sum, which bf16 results do not show.
+// holds head n & 1, so every lane has both heads' scores of its keys. fp32 queries enter as two fp16 parts, to within one fp32
+// step together, part (n >> 1) & 1 of head n & 1 in column n; and their codes become (code + zero) 2^-9 first, by one exact
+// multiply-add each: the subnormal numbers as operands lose up to 5 bits of a product's sum. bf16 results do not show that: with
+// those multiply-adds as many of them round to another number than the exact ones do, and 8 x 65537 keys take 117 us, not 111.
 // Each lane then keeps one score of 16 keys: key r + 8 (c & 1), head c >> 1. (By m16n8k32 on e4m3, where a byte of two masks
 // is 4 operands, the same took longer: that form is carried out by fp16 products after conversions.)
 //
@@ -615,8 +616,8 @@ __device__ __forceinline__ bool attn_row(const Cache& c, const AttnArgs& a, int 
 //
 // Two query tokens that follow one another (N = 2): the columns that one token only repeats are the second one's, query
 // c & 1 in a lane, which then has both of 16 keys' scores r and r + 8 of its head; fp32's third parts of the weights take
-// products of their own (and registers: three blocks an SM). Codes are taken apart once for both: 8
-// sequences of 8 tokens and 2000 keys 28 -> 19 us (fp32 33 -> 28), 44 of 7 and 943 fp32 49 -> 40. The first token does not see the second's key: its weight is 0 there.
+// products of their own (and registers: three blocks an SM). Codes are taken apart once for both: 8 sequences of 8 tokens and
+// 200..2000 keys 28 -> 19 us (fp32 33 -> 28). The first token does not see the second's key: its weight is 0 there.
 //
 // Softmax: a running reference m for each head, moved only when a score exceeds it by 8 (log2): then sums and O are
 // rescaled. It starts at about the lowest number, not -inf, so that no difference of infinities arises, and no finite score
@@ -1284,8 +1285,9 @@ struct Plan {
 // to 24 blocks of keys each. Longer ones: a line in `slots`
 // shares (as many blocks as are resident: one wave) and the launch that merges it. Measured, us: 1 x 8000 keys 7.9 by a
 // cluster of 16, 9.9 of 8, 14.1 by a line; 1 x 20000 14.2 and 16.4 by a line; 4 x 4000 fp32 8.5 by clusters of 8, 10.6 of 16,
-// 4 x 16000 20.2 of 16 and 24.1 by a line; 64 x 20..200 keys 6.0 by a block each, 14.3 by a line; 64 x 800..8000 78 by one
-// block each, 69 by a line. A twentieth of the slots stays free, since clusters do not fill every SM: 19 x 1000 keys in
+// 4 x 16000 20.2 of 16 and 24.1 by a line; 64 x 20..200 keys 6.0 by a block each, 14.3 by a line; 64 x 100..1000 fp32 17.7
+// and 22.9, 64 x 200..2000 31.7 and 31.0 (even rows of 2000 37.1 and 42.7), 64 x 400..4000 56 and 46 (even 69 and 73), 64 x 800..8000
+// 78 and 69. A twentieth of the slots stays free, since clusters do not fill every SM: 19 x 1000 keys in
 // clusters of 3 of 4 blocks an SM 11.1, of 4 (all slots, two waves) 12.6.
 Plan attn_plan(long long rows, int max_len, int slots) {
     const long long pairs = rows * NKV, nblk = (max_len + KVB - 1) / KVB, most = (nblk + 1) / 2, room = slots * 19 / 20;
@@ -1326,7 +1328,7 @@ void launch_cluster(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cud
 }
 
 // fp32 prompts take two launches: the q heads need half of the registers, and twice as many of their warps then hide memory:
-// 32768 tokens 187 us, 196 in one. bf16 ones, whose values on the way take half the registers, take one: 137 us, 139 in two.
+// 24463 tokens 159 us, 168 in one. bf16 ones, whose values on the way take half the registers, take one: 107 us, 110 in two.
 constexpr int SPLIT_TOKENS = 4096;
 template <typename TI, typename TQ>
 void append(int T, const void* qkv, int64_t stride, const void* gq, const void* gk, float eps, const float* cos_t,

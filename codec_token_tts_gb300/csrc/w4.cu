@@ -336,7 +336,8 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 3 : 2)
     }
 }
 
-// Blocks or clusters of a kernel that run at a time on the current device, asked once.
+// Blocks or clusters of a kernel that run at a time on the current device, asked once for a count of blocks an SM: sizes of shared
+// memory with the same count share the answer of the first, which sets the grid, not the results.
 struct Resident {
     std::atomic<int> n[64];
 };

@@ -569,3 +569,16 @@ def test_attention_of_the_most_sequences():
     some = [0, 1, 2, 3, 30000, 30001, 30002, B - 3, B - 2, B - 1]
     check(s, q[some], kl[some], 1, out[some], rows[some])
     assert bool((out[::4] == 5).all()) and int(s.err) == 0
+
+
+@pytest.mark.parametrize("io", ["float32", "bfloat16"])
+@pytest.mark.parametrize("S,max_len", [(1, 200), (3, 200), (1, 16640)])
+def test_attention_of_large_magnitudes(S, max_len, io):
+    """Keys and values of 1e25, queries of 1e-25 (scores near 1), and small keys and values with large queries."""
+    for big in (1e25, 1e-25):
+        s = Setup(34, 2, 260)
+        lens = [200, 67]
+        s.k, s.v = ([fill(s.pool_h, s.table[b], big * s.rng.standard_normal((n, NKV, HD)), w) for b, n in enumerate(lens)] for w in (0, 1))
+        s.pool.copy_(dev(s.pool_h))
+        q = dev(s.rng.standard_normal((2 * S, NQ, HD)) / big).to(getattr(torch, io))
+        check(s, q, lens, S, attend(s, q, lens, S, max_len))
