@@ -53,6 +53,11 @@ class tts_bb_kv4(C.Structure):
                 ("n_seqs", C.c_int), ("blocks_per_seq", C.c_int)]
 
 
+class tts_bb_kv_cache(C.Structure):
+    _fields_ = [("pool", C.c_void_p), ("page_table", C.c_void_p), ("err", C.c_void_p), ("layer_stride", C.c_int64),
+                ("n_layers", C.c_int), ("n_blocks", C.c_int), ("n_seqs", C.c_int), ("blocks_per_seq", C.c_int)]
+
+
 class TtsBbError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {msg}")
@@ -123,6 +128,11 @@ def _load() -> C.CDLL:
         "tts_bb_w4_linear": (I, [I, I, I, I, P, I, C.c_int64, P, P, P]),
         "tts_bb_token_logprobs_workspace": (C.c_size_t, [I, I, I]),
         "tts_bb_token_logprobs": (I, [I, I, P, I, C.c_int64, P, P, C.c_int64, I, P, P, P, P, P, P, C.c_size_t, P]),
+        "tts_bb_tree_attention_workspace": (C.c_size_t, [I, I, I]),
+        "tts_bb_tree_attention": (I, [C.POINTER(tts_bb_kv_cache), I, I, I, P, I, C.c_int64, P, P, C.c_int64, P, P, P, P, I, P, P, C.c_size_t, P]),
+        "tts_bb_tree_verify": (I, [I, I, I, P, P, P, P, C.c_int64, P, C.c_int64, P, P, P, P, P, P, P]),
+        "tts_bb_tree_verify_greedy": (I, [I, I, P, P, P, P, P, P, P, P, P]),
+        "tts_bb_tree_commit": (I, [C.POINTER(tts_bb_kv_cache), I, I, P, P, C.c_int64, C.c_int64, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -142,7 +152,9 @@ EXPORTED = ("tts_bb_default_config", "tts_bb_create", "tts_bb_free", "tts_bb_pre
             "tts_bb_decode_step_host", "tts_bb_quantizer_create", "tts_bb_quantizer_decode",
             "tts_bb_quantizer_sync", "tts_bb_quantizer_free", "tts_bb_rope_tables", "tts_bb_kv4_append",
             "tts_bb_kv4_read", "tts_bb_kv4_attention_workspace", "tts_bb_kv4_attention", "tts_bb_w4_packed_bytes",
-            "tts_bb_w4_pack", "tts_bb_w4_linear", "tts_bb_token_logprobs_workspace", "tts_bb_token_logprobs")
+            "tts_bb_w4_pack", "tts_bb_w4_linear", "tts_bb_token_logprobs_workspace", "tts_bb_token_logprobs",
+            "tts_bb_tree_attention_workspace", "tts_bb_tree_attention", "tts_bb_tree_verify", "tts_bb_tree_verify_greedy",
+            "tts_bb_tree_commit")
 
 
 def _ptr(x) -> Optional[int]:
@@ -613,3 +625,97 @@ def tts_bb_token_logprobs(R: int, V: int, logits, targets=None, n_top: int = 0, 
         _arg(here, top_ids, "top_ids", _I32, R * n_top), _arg(here, top_logprobs, "top_logprobs", _F32, R * n_top),
         _arg(here, workspace, "workspace", _U8, 0), 0 if workspace is None else workspace.numel(), stream or None)
     return _status(st, "tts_bb_token_logprobs", check)
+
+
+# ---------------------------------------------------------------- speculative decoding operators
+# Device tensors, checked as those of the low-bit operators.
+KV_BLOCK_ELEMS, TREE_MAX_NODES = 131072, 64
+TREE_ERR_PAGE, TREE_ERR_RANGE, TREE_ERR_TREE = 1, 2, 4
+
+
+class KvCache:
+    """A paged bf16 KV cache on the caller's tensors (kept alive): pool bf16 of layers * n_blocks * KV_BLOCK_ELEMS,
+    page_table int32 [n_seqs][blocks_per_seq], err an int32 word for device-side errors, or None."""
+
+    def __init__(self, pool, page_table, err=None, layers: int = 1):
+        self.pool, self.page_table, self.err = pool, page_table, err
+        if page_table.dim() != 2:
+            raise ValueError("page_table: two dimensions are wanted")
+        if layers < 1 or pool.numel() % (layers * KV_BLOCK_ELEMS):
+            raise ValueError(f"pool: {layers} layers of whole blocks are wanted, not {pool.numel()} elements")
+        here = _here()
+        n = pool.numel() // (layers * KV_BLOCK_ELEMS)
+        self.struct = tts_bb_kv_cache(_arg(here, pool, "pool", _BF16, KV_BLOCK_ELEMS), _arg(here, page_table, "page_table", _I32, 1),
+                                      _arg(here, err, "err", _I32, 1), n * KV_BLOCK_ELEMS, layers, n, *page_table.shape)
+        self.ref, self.device, self.layers = C.byref(self.struct), here, layers
+
+    on = Kv4Cache.on
+
+
+def tts_bb_tree_attention_workspace(B: int, N: int, max_len: int) -> int:
+    return lib.tts_bb_tree_attention_workspace(B, N, max_len)
+
+
+def tts_bb_tree_attention(cache: KvCache, layer: int, B: int, N: int, q, k, v, parents, kv_lens, max_len: int, out, workspace=None,
+                          n_nodes=None, seqs=None, stream: int = 0, check: bool = True) -> int:
+    """q: [B * N][2048] and out: [B * N][2048], both fp32 or both bf16; k, v: bf16 [B * N][1024] (rows of q, of k and v
+    may be strided, k and v alike); workspace: a uint8 tensor, or None where none is needed."""
+    if q.dtype != out.dtype:
+        raise TypeError(f"q and out have to be of one type, not {q.dtype} and {out.dtype}")
+    here = _here()
+    qp, q_stride = _rows(here, q, "q", _IO, B * N, 2048)
+    kp, k_stride = _rows(here, k, "k", _BF16, B * N, 1024)
+    vp, v_stride = _rows(here, v, "v", _BF16, B * N, 1024)
+    if k_stride != v_stride:
+        raise ValueError(f"k and v have to be of one row stride, not {k_stride} and {v_stride}")
+    st = lib.tts_bb_tree_attention(
+        cache.on(here), layer, B, N, qp, _IO[q.dtype], q_stride, kp, vp, k_stride, _arg(here, parents, "parents", _I32, B * N),
+        _arg(here, n_nodes, "n_nodes", _I32, B), _arg(here, seqs, "seqs", _I32, B), _arg(here, kv_lens, "kv_lens", _I32, B), max_len,
+        _arg(here, out, "out", _IO, B * N * 2048), _arg(here, workspace, "workspace", _U8, 0),
+        0 if workspace is None else workspace.numel(), stream or None)
+    return _status(st, "tts_bb_tree_attention", check)
+
+
+def tts_bb_tree_verify(B: int, N: int, V: int, tokens, parents, target, u, u_next, n_accepted, path, next_token, draft=None, n_nodes=None,
+                       err=None, stream: int = 0, check: bool = True) -> int:
+    """target, draft: fp32 [B * N][>= V] probabilities (rows may be strided); draft None: drafts that were not drawn."""
+    here = _here()
+    p, p_stride = _rows(here, target, "target", _F32, B * N, V)
+    d, d_stride = (None, V) if draft is None else _rows(here, draft, "draft", _F32, B * N, V)
+    st = lib.tts_bb_tree_verify(
+        B, N, V, _arg(here, tokens, "tokens", _I32, B * N), _arg(here, parents, "parents", _I32, B * N), _arg(here, n_nodes, "n_nodes", _I32, B),
+        p, p_stride, d, d_stride, _arg(here, u, "u", _F32, B * N), _arg(here, u_next, "u_next", _F32, B),
+        _arg(here, n_accepted, "n_accepted", _I32, B), _arg(here, path, "path", _I32, B * N), _arg(here, next_token, "next_token", _I32, B),
+        _arg(here, err, "err", _I32, 1), stream or None)
+    return _status(st, "tts_bb_tree_verify", check)
+
+
+def tts_bb_tree_verify_greedy(B: int, N: int, tokens, parents, target_ids, n_accepted, path, next_token, n_nodes=None, err=None,
+                              stream: int = 0, check: bool = True) -> int:
+    here = _here()
+    st = lib.tts_bb_tree_verify_greedy(
+        B, N, _arg(here, tokens, "tokens", _I32, B * N), _arg(here, parents, "parents", _I32, B * N), _arg(here, n_nodes, "n_nodes", _I32, B),
+        _arg(here, target_ids, "target_ids", _I32, B * N), _arg(here, n_accepted, "n_accepted", _I32, B), _arg(here, path, "path", _I32, B * N),
+        _arg(here, next_token, "next_token", _I32, B), _arg(here, err, "err", _I32, 1), stream or None)
+    return _status(st, "tts_bb_tree_verify_greedy", check)
+
+
+def tts_bb_tree_commit(cache: KvCache, B: int, N: int, k, v, path, n_accepted, kv_lens, seqs=None, stream: int = 0,
+                       check: bool = True) -> int:
+    """k, v: bf16 [layers][B * N][1024], contiguous or (both alike) strided rows and layers of three dimensions."""
+    here, L = _here(), cache.layers
+    at, strides = [], []
+    for x, name in ((k, "k"), (v, "v")):
+        if _BF16[x.dtype] is not None and x.get_device() == here and x.dim() == 3 and x.stride(2) == 1 and x.shape[0] >= L and \
+                x.shape[1] >= B * N and x.shape[2] >= 1024:
+            at.append(x.data_ptr())
+            strides.append((x.stride(1) if B * N > 1 else 1024, x.stride(0) if L > 1 else 0))
+        else:
+            at.append(_arg(here, x, name, _BF16, L * B * N * 1024))
+            strides.append((1024, B * N * 1024 if L > 1 else 0))
+    if strides[0] != strides[1]:
+        raise ValueError(f"k and v have to be of the same strides, not {strides[0]} and {strides[1]}")
+    st = lib.tts_bb_tree_commit(cache.on(here), B, N, *at, *strides[0], _arg(here, path, "path", _I32, B * N),
+                                _arg(here, n_accepted, "n_accepted", _I32, B), _arg(here, seqs, "seqs", _I32, B),
+                                _arg(here, kv_lens, "kv_lens", _I32, B), stream or None)
+    return _status(st, "tts_bb_tree_commit", check)

@@ -1,0 +1,458 @@
+// Verification of a tree of drafted tokens against the target's probabilities, and the accepted path's keys and
+// values into the caches of all layers.
+//
+// Verification. With r_0 = p and Z_0 = 1, a rejected child leaves r_{k+1} = (r_k - Z_k q)^+. Since Z_k q >= 0 and r_k is
+// either 0 or p - c_k q, this is r_{k+1} = (p - c_{k+1} q)^+ with the one number c_{k+1} = c_k + Z_k: no array is kept
+// between rejections, and each costs one pass over the rows p and q that sums r. Children's indices lie above their
+// parent's, so one walk over the nodes in their order meets each accepted node's children in turn.
+//
+// Sums decide which whole number is the answer, so they are carried in 2^-60 as 64-bit whole numbers: exact for
+// probabilities from 2^-37 up (24 bits above 2^-60), cut off at 2^-60 below that, and the same in any order.
+#include <algorithm>
+
+#include "tree.cuh"
+
+#define TTS_API extern "C" __attribute__((visibility("default")))
+
+using namespace ttsbb;
+
+namespace {
+
+typedef unsigned long long u64;
+
+constexpr int THREADS = 512, NWARPS = THREADS / 32;
+constexpr int MAX_CLUSTER = 16;
+
+// a probability's bits, within 0 .. 1 (a NaN counts as 1, or as 0 where its sign is set)
+__device__ __forceinline__ uint32_t prob_bits(float x) { return (uint32_t)min(max(__float_as_int(x), 0), 0x3F800000); }
+// in units of 2^-60: the 24-bit mantissa stands at 2^(e - 150 + 60)
+__device__ __forceinline__ u64 fix60(float x) {
+    const uint32_t b = prob_bits(x), e = b >> 23, m = (b & 0x7FFFFFu) | 0x800000u;
+    return e >= 90 ? (u64)m << (e - 90) : e > 66 ? (u64)(m >> (90 - e)) : 0ull;
+}
+// a * b / 2^s
+__device__ __forceinline__ u64 mul_shift(u64 a, u64 b, int s) { return (__umul64hi(a, b) << (64 - s)) | (a * b >> s); }
+// what c (in 2^-58) times q leaves of p
+__device__ __forceinline__ u64 rest60(u64 p, u64 c, u64 q) {
+    const u64 t = mul_shift(c, q, 58);
+    return p > t ? p - t : 0ull;
+}
+
+__device__ __forceinline__ u64 warp_sum64(u64 v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void store_peer(u64* p, int rank, u64 v) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+
+struct VerifyArgs {
+    const int32_t *tokens, *parents, *n_nodes;
+    const float *target, *draft, *u, *u_next;
+    long long p_stride, q_stride;
+    int32_t *n_accepted, *path, *next, *err;
+    int N, V, ctas, seg;  // blocks of a cluster, ids of a warp
+};
+
+// The nodes of sequence b, 0 where it is padding or out of order (by one warp, lanes hold nodes l and l + 32).
+__device__ __forceinline__ int tree_nodes(const int32_t* n_nodes, int b, int N, int lane, const int (&par)[2], int32_t* err, bool report) {
+    const int n = n_nodes ? n_nodes[b] : N;
+    if (n < 0 || n > N) {
+        if (report && lane == 0) set_err(err, TTS_BB_TREE_ERR_RANGE);
+        return 0;
+    }
+    bool bad = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) bad |= lane + 32 * h < n && (par[h] < -1 || par[h] >= lane + 32 * h);
+    if (__any_sync(0xffffffffu, bad)) {
+        if (report && lane == 0) set_err(err, TTS_BB_TREE_ERR_TREE);
+        return 0;
+    }
+    return n;
+}
+// Count and nodes of the chosen path, by one warp.
+__device__ __forceinline__ void write_path(u64 chosen, int b, int N, int lane, int32_t* n_accepted, int32_t* path) {
+    const int count = __popcll(chosen);
+    if (lane == 0) n_accepted[b] = count;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int j = lane + 32 * h;
+        const u64 below = (1ull << j) - 1;
+        if (j >= N) continue;
+        if (chosen >> j & 1) path[(size_t)b * N + __popcll(chosen & below)] = j;
+        if (j >= count) path[(size_t)b * N + j] = -1;
+    }
+}
+
+enum { WALK_PASS, WALK_LAST };
+
+struct VerifyShared {
+    int par[MAX_NODES], tok[MAX_NODES];
+    float p[MAX_NODES], q[MAX_NODES], u[MAX_NODES];
+    u64 wsum[NWARPS];
+    u64 tot[2][MAX_CLUSTER];  // the blocks' sums of a pass, by its parity
+    u64 chosen, gone;         // accepted nodes; rejected children of the current node (drafts that were not drawn)
+    u64 c;                    // 2^-58
+    int n, cur, event, at;
+};
+
+// grid (ctas, B), a cluster of ctas blocks for each sequence, 512 threads. Block r of a cluster owns the ids
+// [r, r + 1) * NWARPS * seg, warp w of it seg of them.
+template <bool DRAWN>
+__global__ void __launch_bounds__(THREADS) k_tree_verify(VerifyArgs a) {
+    __shared__ VerifyShared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y, rank = blockIdx.x;
+    const bool many = a.ctas > 1;
+    if (many) cluster_arrive();  // waited for before the first word goes to a peer
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 0) {
+        int par[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = lane + 32 * h;
+            par[h] = j < a.N ? a.parents[(size_t)b * a.N + j] : -1;
+            sh.par[j] = par[h];
+        }
+        const int n = tree_nodes(a.n_nodes, b, a.N, lane, par, a.err, rank == 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = lane + 32 * h;
+            if (j >= n) continue;
+            // what the target and the draft of its parent give the node's token
+            const int x = a.tokens[(size_t)b * a.N + j];
+            const bool real = x >= 0 && x < a.V && par[h] >= 0;
+            const size_t row = (size_t)b * a.N + max(par[h], 0);
+            sh.tok[j] = real ? x : -1;
+            sh.u[j] = a.u[(size_t)b * a.N + j];
+            sh.p[j] = real ? __uint_as_float(prob_bits(a.target[row * a.p_stride + x])) : 0.f;
+            if (DRAWN) sh.q[j] = real ? __uint_as_float(prob_bits(a.draft[row * a.q_stride + x])) : 0.f;
+        }
+        if (lane == 0) {
+            sh.n = n;
+            sh.cur = 0;
+            sh.at = 1;
+            sh.chosen = 1;
+            sh.gone = 0;
+            sh.c = 0;
+        }
+    }
+    __syncthreads();
+    if (many) cluster_wait();
+    const int n = sh.n;
+    if (n == 0) {  // for all blocks of the cluster
+        if (rank == 0 && warp == 0) {
+            write_path(0, b, a.N, lane, a.n_accepted, a.path);
+            if (lane == 0) a.next[b] = -1;
+        }
+        return;
+    }
+    const float u_next = a.u_next[b];
+    const int first = (rank * NWARPS + warp) * a.seg, last = min(a.V, first + a.seg);  // ids of this warp
+    u64 Z = 0;
+    bool summed = false;  // the sums in sh are those of the rest as it stands
+    int parity = 0;
+    for (;;) {
+        if (tid == 0) {
+            // Z of the last pass is the mass that the next child is measured by; before the first, 1
+            double mass = DRAWN && sh.c ? (double)Z * 0x1p-60 : 1.0;
+            if (!DRAWN)
+                for (u64 g = sh.gone; g; g &= g - 1) mass -= (double)sh.p[__ffsll(g) - 1];
+            int j = sh.at, event = WALK_LAST;
+            for (; j < n; ++j) {
+                if (sh.par[j] != sh.cur || sh.tok[j] < 0) continue;
+                double r = (double)sh.p[j], price = (double)sh.u[j] * mass;
+                if (DRAWN) {
+                    if (sh.c) r -= (double)sh.c * 0x1p-58 * (double)sh.q[j];
+                    price *= (double)sh.q[j];
+                }
+                bool again = false;  // a token that was rejected here before
+                if (!DRAWN)
+                    for (u64 g = sh.gone; g; g &= g - 1) again |= sh.tok[__ffsll(g) - 1] == sh.tok[j];
+                if (!again && price < r) {
+                    sh.chosen |= 1ull << j;
+                    sh.cur = j;
+                    sh.c = sh.gone = 0;
+                    mass = 1.0;
+                    summed = false;
+                } else if (DRAWN) {
+                    const u64 more = sh.c ? Z >> 2 : 1ull << 58;
+                    sh.c = sh.c + more < sh.c ? ~0ull : sh.c + more;
+                    event = WALK_PASS;
+                    ++j;
+                    break;
+                } else if (!again) {
+                    sh.gone |= 1ull << j;
+                    mass -= (double)sh.p[j];
+                }
+            }
+            sh.at = j;
+            // the path's end: the sums are there where the last pass was of this node's rest
+            sh.event = event == WALK_LAST && summed ? WALK_LAST + 1 : event;
+        }
+        __syncthreads();
+        const int event = sh.event;
+        if (event > WALK_LAST) break;
+        // sums of the rest of node cur
+        const u64 c = sh.c;
+        const size_t row = (size_t)b * a.N + sh.cur;
+        const float* const p = a.target + row * a.p_stride;
+        const float* const q = DRAWN ? a.draft + row * a.q_stride : nullptr;
+        u64 sum = 0;
+        if (!DRAWN || c == 0) {
+#pragma unroll 8
+            for (int x = first + lane; x < last; x += 32) sum += fix60(p[x]);
+        } else if (c == 1ull << 58) {
+#pragma unroll 8
+            for (int x = first + lane; x < last; x += 32) {
+                const u64 f = fix60(p[x]), g = fix60(q[x]);
+                sum += f > g ? f - g : 0ull;
+            }
+        } else {
+#pragma unroll 4
+            for (int x = first + lane; x < last; x += 32) sum += rest60(fix60(p[x]), c, fix60(q[x]));
+        }
+        sum = warp_sum64(sum);
+        if (!DRAWN && lane == 0) {  // less the rejected tokens, each once
+            for (u64 g = sh.gone; g; g &= g - 1) {
+                const int j = __ffsll(g) - 1, x = sh.tok[j];
+                if (x >= first && x < last) sum -= fix60(sh.p[j]);
+            }
+        }
+        if (lane == 0) sh.wsum[warp] = sum;
+        __syncthreads();
+        u64 block = lane < NWARPS ? sh.wsum[lane] : 0ull;
+        block = warp_sum64(block);
+        if (many) {
+            if (tid < a.ctas) store_peer(&sh.tot[parity][rank], tid, block);
+            cluster_arrive();
+            cluster_wait();
+            Z = 0;
+            for (int i = 0; i < a.ctas; ++i) Z += sh.tot[parity][i];
+        } else {
+            if (tid == 0) sh.tot[parity][0] = block;
+            Z = block;
+            __syncthreads();
+        }
+        parity ^= 1;
+        summed = true;
+        if (event == WALK_LAST) break;
+    }
+    // the next token
+    parity ^= 1;
+    const u64 c = sh.c;
+    const size_t row = (size_t)b * a.N + sh.cur;
+    const float* const p = a.target + row * a.p_stride;
+    const float* const q = DRAWN ? a.draft + row * a.q_stride : nullptr;
+    if (rank == 0 && warp == 0) write_path(sh.chosen, b, a.N, lane, a.n_accepted, a.path);
+    if (Z) {
+        u64 t = mul_shift(fix60(u_next), Z, 60);
+        if (t >= Z) t = Z - 1;  // u_next of 1
+        for (int i = 0; i < rank; ++i) {
+            if (t < sh.tot[parity][i]) return;  // in a block before this one
+            t -= sh.tot[parity][i];
+        }
+        for (int i = 0; i < warp; ++i) {
+            if (t < sh.wsum[i]) return;
+            t -= sh.wsum[i];
+        }
+        if (t >= sh.wsum[warp]) return;
+        for (int x0 = first; x0 < last; x0 += 32) {
+            const int x = x0 + lane;
+            u64 r = x < last ? fix60(p[x]) : 0ull;
+            if (DRAWN) {
+                if (c && x < last) r = rest60(r, c, fix60(q[x]));
+            } else {
+                for (u64 g = sh.gone; g; g &= g - 1)
+                    if (sh.tok[__ffsll(g) - 1] == x) r = 0;
+            }
+            u64 upto = r;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 w = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += w;
+            }
+            const uint32_t over = __ballot_sync(0xffffffffu, upto > t);
+            if (over) {
+                if (lane == 0) a.next[b] = x0 + __ffs(over) - 1;
+                return;
+            }
+            t -= __shfl_sync(0xffffffffu, upto, 31);
+        }
+        return;
+    }
+    // nothing is left: the most probable token of p. Keys order by value, then by the lowest id
+    u64 best = 0;
+    for (int x = first + lane; x < last; x += 32) best = max(best, (u64)prob_bits(p[x]) << 32 | (uint32_t)~x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+    __syncthreads();
+    if (lane == 0) sh.wsum[warp] = best;
+    __syncthreads();
+    best = lane < NWARPS ? sh.wsum[lane] : 0ull;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+    if (many) {
+        parity ^= 1;
+        if (tid == 0) store_peer(&sh.tot[parity][rank], 0, best);
+        cluster_arrive();
+        cluster_wait();
+        if (rank != 0) return;
+        for (int i = 0; i < a.ctas; ++i) best = max(best, sh.tot[parity][i]);
+    }
+    if (rank == 0 && tid == 0) a.next[b] = (int)~(uint32_t)best;
+}
+
+// a warp a sequence
+constexpr int GREEDY_WARPS = 4;
+__global__ void __launch_bounds__(GREEDY_WARPS * 32) k_tree_greedy(VerifyArgs a, const int32_t* __restrict__ ids, int B) {
+    pdl_wait();
+    pdl_trigger();
+    const int b = blockIdx.x * GREEDY_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (b >= B) return;
+    int par[2], tok[2], id[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int j = lane + 32 * h;
+        const size_t at = (size_t)b * a.N + j;
+        par[h] = j < a.N ? a.parents[at] : -1;
+        tok[h] = j < a.N ? a.tokens[at] : 0;
+        id[h] = j < a.N ? ids[at] : 0;
+    }
+    const int n = tree_nodes(a.n_nodes, b, a.N, lane, par, a.err, true);
+    u64 chosen = n ? 1 : 0;
+    int cur = 0, want = __shfl_sync(0xffffffffu, id[0], 0);
+    for (int step = 0; step < n; ++step) {  // a path is no longer than the tree
+        uint32_t hit[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) hit[h] = __ballot_sync(0xffffffffu, lane + 32 * h < n && par[h] == cur && tok[h] == want);
+        if (!(hit[0] | hit[1])) break;
+        cur = hit[0] ? __ffs(hit[0]) - 1 : 31 + __ffs(hit[1]);
+        chosen |= 1ull << cur;
+        want = __shfl_sync(0xffffffffu, cur < 32 ? id[0] : id[1], cur & 31);
+    }
+    write_path(chosen, b, a.N, lane, a.n_accepted, a.path);
+    if (lane == 0) a.next[b] = n ? want : -1;
+}
+
+// grid (layers, B), 256 threads: 16 bytes of K or of V each, a token a turn
+struct CommitArgs {
+    const bf16 *k, *v;
+    long long row_stride, layer_stride;
+    const int32_t *path, *n_accepted, *seqs, *kv_lens;
+    int N;
+};
+__global__ void __launch_bounds__(256) k_tree_commit(Pages c, CommitArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int l = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, which = tid >> 7, piece = tid & 127;
+    const int row = row_of(c, a.seqs, b), n = a.n_accepted[b], len = a.kv_lens[b];
+    const bool report = l == 0 && tid == 0;
+    if (row == -1) return;
+    if (row < 0 || n < 0 || n > a.N || len < 0) {
+        if (report) set_err(c.err, TTS_BB_TREE_ERR_RANGE);
+        return;
+    }
+    const bf16* const src = (which ? a.v : a.k) + l * a.layer_stride + piece * 8;
+    bf16* const dst = c.pool + l * c.layer_stride + (size_t)which * (KV_BLOCK / 2) + (size_t)(piece >> 4) * (KVB * HD) + (piece & 15) * 8;
+    const long long room = (long long)c.bps * KVB;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+        const int node = a.path[(size_t)b * a.N + j];
+        const long long pos = (long long)len + j;
+        if (node < 0 || node >= a.N || pos >= room) {
+            if (report) set_err(c.err, pos >= room ? TTS_BB_TREE_ERR_RANGE : TTS_BB_TREE_ERR_TREE);
+            continue;
+        }
+        const int page = page_of(c, row, (int)pos);
+        if (page < 0) {
+            if (report) set_err(c.err, TTS_BB_TREE_ERR_PAGE);
+            continue;
+        }
+        const uint4 x = *reinterpret_cast<const uint4*>(src + ((long long)b * a.N + node) * a.row_stride);
+        *reinterpret_cast<uint4*>(dst + page * KV_BLOCK + (size_t)(pos % KVB) * HD) = x;
+    }
+}
+
+// Blocks of a sequence's cluster: one for each 4096 ids, as many as let all sequences run at once.
+int verify_ctas(int B, int V) {
+    int n = 1;
+    while (n < MAX_CLUSTER && n * 4096 < V && 2 * n * B <= 4 * 152) n *= 2;
+    return n;
+}
+
+}  // namespace
+
+TTS_API tts_bb_status tts_bb_tree_verify(int B, int N, int V, const int32_t* tokens, const int32_t* parents, const int32_t* n_nodes,
+                                         const float* target, int64_t target_stride, const float* draft, int64_t draft_stride,
+                                         const float* u, const float* u_next, int32_t* n_accepted, int32_t* path,
+                                         int32_t* next_token, int32_t* err, void* stream) {
+    if (!tree_ok(B, N) || V < 1 || V > (1 << 30) || !tokens || !parents || !target || target_stride < V ||
+        (draft && draft_stride < V) || !u || !u_next || !n_accepted || !path || !next_token ||
+        !words_aligned(tokens, parents, n_nodes, u, u_next, n_accepted, path, next_token, err, target, draft))
+        return TTS_BB_E_INVALID;
+    if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
+    const int ctas = verify_ctas(B, V);
+    const int seg = (int)(((long long)V + ctas * NWARPS * 32 - 1) / (ctas * NWARPS * 32)) * 32;
+    const VerifyArgs a{tokens, parents, n_nodes, target, draft, u, u_next, target_stride, draft_stride, n_accepted, path, next_token, err,
+                       N, V, ctas, seg};
+    const auto go = [&](auto kernel, SmemState& state) {
+        allow_smem(state, kernel, 0, true);
+        cudaLaunchAttribute at[2];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = ctas;
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(ctas, B);
+        cfg.blockDim = dim3(THREADS);
+        cfg.stream = static_cast<cudaStream_t>(stream);
+        cfg.attrs = at;
+        cfg.numAttrs = ctas > 1 ? 2 : 1;
+        cudaLaunchKernelEx(&cfg, kernel, a);
+    };
+    static SmemState drawn, chosen;
+    if (draft) go(k_tree_verify<true>, drawn);
+    else go(k_tree_verify<false>, chosen);
+    return launched();
+}
+
+TTS_API tts_bb_status tts_bb_tree_verify_greedy(int B, int N, const int32_t* tokens, const int32_t* parents, const int32_t* n_nodes,
+                                                const int32_t* target_ids, int32_t* n_accepted, int32_t* path, int32_t* next_token,
+                                                int32_t* err, void* stream) {
+    if (!tree_ok(B, N) || !tokens || !parents || !target_ids || !n_accepted || !path || !next_token ||
+        !words_aligned(tokens, parents, n_nodes, target_ids, n_accepted, path, next_token, err))
+        return TTS_BB_E_INVALID;
+    if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
+    VerifyArgs a{};
+    a.tokens = tokens;
+    a.parents = parents;
+    a.n_nodes = n_nodes;
+    a.n_accepted = n_accepted;
+    a.path = path;
+    a.next = next_token;
+    a.err = err;
+    a.N = N;
+    launch_pdl(k_tree_greedy, (B + GREEDY_WARPS - 1) / GREEDY_WARPS, GREEDY_WARPS * 32, 0, static_cast<cudaStream_t>(stream), a, target_ids, B);
+    return launched();
+}
+
+TTS_API tts_bb_status tts_bb_tree_commit(const tts_bb_kv_cache* cache, int B, int N, const void* k, const void* v, int64_t row_stride,
+                                         int64_t layer_stride, const int32_t* path, const int32_t* n_accepted, const int32_t* seqs,
+                                         const int32_t* kv_lens, void* stream) {
+    if (!cache_ok(cache) || !tree_ok(B, N) || !k || !v || !aligned16(k) || !aligned16(v) || row_stride < NKV * HD || row_stride % 8 ||
+        (cache->n_layers > 1 && (layer_stride < 0 || layer_stride % 8)) || cache->n_layers > 65535 || !path || !n_accepted || !kv_lens ||
+        (!seqs && B > cache->n_seqs) || !words_aligned(path, n_accepted, seqs, kv_lens))
+        return TTS_BB_E_INVALID;
+    if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
+    const CommitArgs a{static_cast<const bf16*>(k), static_cast<const bf16*>(v), row_stride, cache->n_layers > 1 ? layer_stride : 0, path, n_accepted,
+                       seqs, kv_lens, N};
+    launch_pdl(k_tree_commit, dim3(cache->n_layers, B), 256, 0, static_cast<cudaStream_t>(stream), pages_of(cache, 0), a);
+    return launched();
+}

@@ -632,6 +632,105 @@ tts_bb_status tts_bb_token_logprobs(int R, int V, const void* logits, int type, 
                                     float* logprob, float* entropy, float* lse, int32_t* top_ids, float* top_logprobs,
                                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Speculative decoding operators: a pass over a tree of drafted tokens for each sequence. tts_bb_tree_attention runs the
+ * tree's attention over a paged bf16 cache, tts_bb_tree_verify (or _greedy) finds the path that the target model accepts
+ * and the token behind it, tts_bb_tree_commit appends the path's keys and values to the caches of all layers. Drafted
+ * keys and values stay in the caller's own arrays until then: a rejected token never owns a place of the cache. The
+ * conventions of the low-bit operators hold: the caller's buffers alone, asynchronous on `stream`, no allocation, nothing
+ * kept between calls, capturable into a CUDA graph, TTS_BB_E_INVALID before anything is enqueued.
+ *
+ * A tree has 1 .. N nodes, N <= TTS_BB_TREE_MAX_NODES, B * N <= 65535:
+ *   parents  int32 [B][N]: parents[b][i] is a node below i, or -1: a child of the cached context. Node 0 is the pending token
+ *            (known, its keys not yet cached). Verification starts there: further nodes of parent -1 are never reached
+ *   n_nodes  int32 [B], 0 .. N, or NULL: N each. Nodes behind them are padding, whatever they hold; 0: a padding sequence
+ * A sequence of a parent out of order or of n_nodes out of range is skipped (below) and reported. */
+#define TTS_BB_TREE_MAX_NODES 64
+/* Bits of an error word. */
+enum {
+    TTS_BB_TREE_ERR_PAGE = 1,  /* a page-table entry outside 0..n_blocks-1 was met */
+    TTS_BB_TREE_ERR_RANGE = 2, /* a cache row, a key count, a node count or a position out of range */
+    TTS_BB_TREE_ERR_TREE = 4   /* a parent that is not below its node, or a path's node outside 0..N-1 */
+};
+/* A paged bf16 KV cache of n_layers layers: each a pool of blocks [n_blocks][2][8][64][128] (block: K then V of 64 positions
+ * for the 8 KV heads, as tts_bb_gqa_decode_attention_static reads it), all under one page table. */
+#define TTS_BB_KV_BLOCK_ELEMS 131072
+typedef struct {
+    void* pool;                /* device bf16, 16-byte aligned: layer 0 */
+    const int32_t* page_table; /* device int32 [n_seqs][blocks_per_seq]: block of each 64 positions */
+    int32_t* err;              /* device word, or NULL: the bits of what calls skipped are ORed into it */
+    int64_t layer_stride;      /* elements from a layer's pool to the next, a multiple of 8 (not used for one layer) */
+    int n_layers;
+    int n_blocks;              /* at most 2^20 */
+    int n_seqs;
+    int blocks_per_seq;
+} tts_bb_kv_cache;
+
+/* Grouped-query attention of N tree nodes for each of B sequences: node i sees the first kv_lens[b] cached keys, itself and its
+ * ancestors. Query head h reads KV head h / 2, scale 1 / sqrt(128), softmax and sums in fp32.
+ *   cache, layer  the cache, and which of its layers
+ *   q        fp32 or bf16 (type) [B * N] rows of 2048 (16 heads of 128, normed and rotated), q_stride elements apart
+ *   k, v     bf16 [B * N] rows of 1024 (8 heads of 128, k normed and rotated): the nodes' own, kv_stride elements apart
+ *   out      [B][N][16][128] of the type of q
+ *            all rows of q, k, v, out 16-byte aligned; k, v and q may be parts of wider rows
+ *   seqs     int32 [B], the cache row of each sequence (negative: padding), or NULL: sequence b reads row b
+ *   kv_lens  int32 [B], the sequence's cached keys, 0 .. max_len
+ *   max_len  an upper bound of kv_lens (host), 0 .. 64 * blocks_per_seq, at most 2^30; it sets the split and the workspace,
+ *            a tight one is faster
+ *   workspace at least tts_bb_tree_attention_workspace(B, N, max_len) bytes, 16-byte aligned (NULL where that is 0); written
+ *            before it is read, not shared by calls that overlap
+ * Rows of out of padding and of skipped sequences are left as they were; keys behind a page out of range are left out of the
+ * sums. What masked keys, places behind a sequence's keys and padding nodes hold does not matter, NaN and infinities among it. A value
+ * that is not finite among a row's own keys makes that row's numbers of its column (or the row) not finite. Results do
+ * not depend on the order in which blocks of the launch run. */
+size_t tts_bb_tree_attention_workspace(int B, int N, int max_len);
+tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int layer, int B, int N, const void* q, int type,
+                                    int64_t q_stride, const void* k, const void* v, int64_t kv_stride,
+                                    const int32_t* parents, const int32_t* n_nodes, const int32_t* seqs,
+                                    const int32_t* kv_lens, int max_len, void* out, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* The path of drafted tokens that the target's probabilities accept, by given random numbers, so that the tokens are distributed
+ * as the target's own. At node i (first: node 0) with the target's row p and the draft's row q, the children x in the order of
+ * their index: r = p, Z = 1 at first; x is accepted where u q(x) Z < r(x), and the walk goes on from it. Else r(y) becomes
+ * max(r(y) - Z q(y), 0) for all y, and Z the sum of r. With draft NULL (drafts that were chosen, not drawn, such as the most
+ * probable ones): accepted where u Z < r(x), else r(x) becomes 0 and Z loses what it was. Behind the last accepted node the
+ * next token is the smallest x where the sum of r(0 .. x) exceeds u_next times the sum of all r; where that is 0, the
+ * most probable one of p, the lowest of them.
+ *   tokens   int32 [B][N]; a drafted token outside 0..V-1 is no draw: never accepted, r stays
+ *   target   fp32 [B * N] rows of V probabilities, target_stride elements apart (>= V): row b N + i holds the target's for
+ *            the token behind node i. 0 <= p <= 1, each row's sum near 1 (others: some path of the tree and some next token in
+ *            0..V-1; above 1 and NaN count as 1)
+ *   draft    fp32, the same for the draft model, draft_stride apart: the distribution from which all children of node i were
+ *            drawn, independently of each other; or NULL
+ *   u        fp32 [B][N] in [0, 1): node j's number; u_next fp32 [B]
+ *   n_accepted int32 [B]: nodes of the path, node 0 among them; 0 for padding and skipped sequences
+ *   path     int32 [B][N]: its nodes, -1 behind the last;  next_token int32 [B]: -1 where n_accepted is 0
+ *   err      device word, or NULL
+ * Sums are carried in whole numbers of 2^-60, products in 64 bits or more: the answers are those of exact arithmetic but for ties
+ * that close. V at most 2^30, fp32 and int32 arrays 4-byte aligned. */
+tts_bb_status tts_bb_tree_verify(int B, int N, int V, const int32_t* tokens, const int32_t* parents, const int32_t* n_nodes,
+                                 const float* target, int64_t target_stride, const float* draft, int64_t draft_stride,
+                                 const float* u, const float* u_next, int32_t* n_accepted, int32_t* path,
+                                 int32_t* next_token, int32_t* err, void* stream);
+/* The same for greedy decoding: target_ids int32 [B][N] holds the target's choice behind each node (such as argmax_out); of a
+ * node's children the first of that token is accepted, and next_token is the choice behind the last accepted node. */
+tts_bb_status tts_bb_tree_verify_greedy(int B, int N, const int32_t* tokens, const int32_t* parents, const int32_t* n_nodes,
+                                        const int32_t* target_ids, int32_t* n_accepted, int32_t* path, int32_t* next_token,
+                                        int32_t* err, void* stream);
+
+/* Append the accepted paths to the caches of all layers: node path[b][j] of sequence b becomes position kv_lens[b] + j of its cache
+ * row, for j < n_accepted[b].
+ *   k, v     bf16 [n_layers][B * N] rows of 1024 as tts_bb_tree_attention takes them, rows row_stride and layers layer_stride
+ *            elements apart, every row 16-byte aligned; not a part of the cache
+ *   path, n_accepted  as tts_bb_tree_verify gives them (0: nothing is appended)
+ *   seqs, kv_lens     as in tts_bb_tree_attention. kv_lens is not changed: adding n_accepted to it is the caller's
+ * The rows of one call must differ. Tokens whose position, page or node is out of range are skipped, as is a sequence whose
+ * row, key count or n_accepted is, and reported in cache->err. */
+tts_bb_status tts_bb_tree_commit(const tts_bb_kv_cache* cache, int B, int N, const void* k, const void* v, int64_t row_stride,
+                                 int64_t layer_stride, const int32_t* path, const int32_t* n_accepted, const int32_t* seqs,
+                                 const int32_t* kv_lens, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
