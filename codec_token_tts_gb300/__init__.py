@@ -630,7 +630,7 @@ def tts_bb_token_logprobs(R: int, V: int, logits, targets=None, n_top: int = 0, 
 # ---------------------------------------------------------------- speculative decoding operators
 # Device tensors, checked as those of the low-bit operators.
 KV_BLOCK_ELEMS, TREE_MAX_NODES = 131072, 64
-TREE_ERR_PAGE, TREE_ERR_RANGE, TREE_ERR_TREE = 1, 2, 4
+TREE_ERR_PAGE, TREE_ERR_RANGE, TREE_ERR_TREE, TREE_ERR_TIMEOUT = 1, 2, 4, 8
 
 
 class KvCache:

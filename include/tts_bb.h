@@ -650,7 +650,8 @@ tts_bb_status tts_bb_token_logprobs(int R, int V, const void* logits, int type, 
 enum {
     TTS_BB_TREE_ERR_PAGE = 1,  /* a page-table entry outside 0..n_blocks-1 was met */
     TTS_BB_TREE_ERR_RANGE = 2, /* a cache row, a key count, a node count or a position out of range */
-    TTS_BB_TREE_ERR_TREE = 4   /* a parent that is not below its node, or a path's node outside 0..N-1 */
+    TTS_BB_TREE_ERR_TREE = 4,  /* a parent that is not below its node, or a path's node outside 0..N-1 */
+    TTS_BB_TREE_ERR_TIMEOUT = 8 /* a bounded wait inside a kernel ran out: that call's out is undefined */
 };
 /* A paged bf16 KV cache of n_layers layers: each a pool of blocks [n_blocks][2][8][64][128] (block: K then V of 64 positions
  * for the 8 KV heads, as tts_bb_gqa_decode_attention_static reads it), all under one page table. */
