@@ -1530,6 +1530,19 @@ bool tc_make_map_strided(CUtensorMap* m, const void* base, int rows, int cols, l
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D bf16 tensor [rows][heads][128], rows `stride` elements apart, box [box_rows][2 heads][64], 128-byte swizzle. Not cached.
+bool tc_make_map_heads(CUtensorMap* m, const void* base, int rows, int heads, long long stride, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {256, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 2, (cuuint32_t)box_rows};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool PRECISE>
 static int launch_attn_tc(const CUtensorMap& mkv, const AttnTcArgs& A, int B, cudaStream_t st) {
     constexpr int SMEM = at::Lay<PRECISE>::SMEM;

@@ -63,6 +63,13 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
         "l"(map), "r"(x), "r"(y), "r"(s_addr(bar))
         : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            s_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(s_addr(bar))
+        : "memory");
+}
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,
                                             uint64_t* bar) {
     asm volatile(
@@ -135,5 +142,7 @@ bool tc_make_map_rows(CUtensorMap* m, const void* base, int C, int T, int B, int
 bool tc_make_map_k(CUtensorMap* m, const void* base, int rows, int K, int box_rows, int box_k);
 // Host: 2-D bf16 tensor map [rows][cols], rows `stride` elements apart, box [box_rows][64], 128-byte swizzle.
 bool tc_make_map_strided(CUtensorMap* m, const void* base, int rows, int cols, long long stride, int box_rows);
+// Host: 3-D bf16 tensor map [rows][heads][128], rows `stride` elements apart, box [box_rows][2 heads][64], 128-byte swizzle.
+bool tc_make_map_heads(CUtensorMap* m, const void* base, int rows, int heads, long long stride, int box_rows);
 
 }  // namespace ttsbb

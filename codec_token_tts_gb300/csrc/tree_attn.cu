@@ -33,46 +33,61 @@ constexpr int PAGE_BYTES = KVB * HD * 2;  // K or V of a page and head
 constexpr int PART = HD + 4;              // 128 sums, the reference and the weight, 16-byte rows
 constexpr int SHARES = 152;               // a block an SM
 
-// A share's work: a piece of the tiles of one (sequence, KV head), the pages 0 .. pages - 1 of which the last is the tree.
+// A share's work: a piece of the tiles (a page each) of one (sequence, KV head), the last of which is the tree.
 struct Piece {
     int b, g, row, len, n;  // b < 0: no more
-    int t0, t1, pages;
-    int ok;                 // the tree is in order (known where the piece holds the tree's page)
+    int t0, t1, tiles;
+    int ok;                 // the tree is in order (known where the piece holds the tree)
     int whole, first;
     uint32_t bad[2];        // nodes whose values are not all finite
     u64 seen[MAX_NODES];    // ancestors and self
 };
 
-// bf16: tiles of two pages, queries as they are, weights in two bf16 parts. fp32: tiles of one page, queries and
-// weights in three parts each, which is all of their bits.
+// bf16: queries as they are, weights in two bf16 parts (17 bits, both rounded). fp32: queries and weights in three parts
+// each, which is all of their bits.
 template <bool F32>
 struct Lay {
-    static constexpr int KT = F32 ? 64 : 128, PAGES = KT / KVB, QPARTS = F32 ? 3 : 1, PPARTS = F32 ? 3 : 2;
-    static constexpr int SLOT = KT * HD * 2, SLOTS = F32 ? 7 : 5;
-    static constexpr int Q_BYTES = 128 * HD * 2;
-    static constexpr int RING_OFF = QPARTS * Q_BYTES, END = RING_OFF + SLOTS * SLOT;
+    static constexpr int QPARTS = F32 ? 3 : 1, PPARTS = F32 ? 3 : 2, QBUFS = F32 ? 1 : 2;
+    // regions of TMEM for a tile's scores (64 columns) and then its weights (32 a part), and how far scores run ahead of sums
+    static constexpr int REGIONS = F32 ? 2 : 4, REGION = F32 ? 128 : 64, AHEAD = F32 ? 1 : 2;
 };
-constexpr int SOFT_WARPS = 4, SUM_WARPS = 4, W_LOAD = 8, W_MMA = 9, W_SCHED = 10, WARPS = 11, NT = WARPS * 32;
-constexpr int PIECES = 3;      // descriptors in flight
-constexpr int RING = 4;        // tiles whose factors are kept
-constexpr int TMEM_COLS = 512; // scores / weights of tile t at 128 (t & 1), its sums at 256 + 128 (t & 1)
+// the last two beside the rows that few nodes leave empty
+constexpr int W_SUM = 8, W_REST = 12, W_SCHED = 12, W_SAFE = 13, W_LOAD = 14, W_MMA = 15, WARPS = 16, NT = WARPS * 32;
+// registers of a thread: the launch's 128 are dealt anew
+constexpr int REGS_SOFT = 120, REGS_SUM = 208, REGS_REST = 64;
+static_assert(2 * REGS_SOFT + REGS_SUM + REGS_REST == 4 * 128, "registers of the launch");
+constexpr int PIECES = 4;       // descriptors in flight
+constexpr int RING = 8;         // tiles whose references and weights are kept
+constexpr int MAX_SLOTS = 8;    // of K, and of V
+constexpr int TMEM_COLS = 512;  // the regions, then the sums of tile t at 256 + 128 (t & 1)
 
 struct Shared {
-    u64 full[8], empty[8];      // ring slots
-    u64 s_full[2], p_full[2];   // scores there (and the word of `there`), weights there (4 warps)
-    u64 o_full[2], o_empty[2];  // a tile's sums and factors there (1 + 4), taken (4)
-    u64 q_full, piece_full[PIECES], piece_empty[PIECES], fin;
+    u64 k_full[MAX_SLOTS], k_empty[MAX_SLOTS], v_full[MAX_SLOTS], v_ready[MAX_SLOTS], v_empty[MAX_SLOTS];
+    u64 s_full[4], p_full[4];   // of a region: scores there (products, their issuer), weights there (4 warps)
+    u64 o_full[2], o_empty[2];  // a tile's sums there (products, their issuer), taken (4)
+    u64 m_full[4][2];           // a tile's references of 32 rows there
+    u64 q_full[2], q_empty[2], piece_full[PIECES], piece_empty[PIECES], fin;
     u64 sums[WARPS];
     uint32_t tmem;
     int abort;
     int start[2];
-    int there[8];  // of tile t, at t % 8: a bit for each of its pages that was there
+    int page[16];   // of tile t, at t % 16: its page, -1 where that is out of range (the tree: 0)
     Piece piece[PIECES];
-    float alpha[RING][128], m[RING][128], l[RING][128];
+    float m[RING][128], l[RING][128];
 };
-template <bool F32>
-constexpr int SMEM = Lay<F32>::END + (int)sizeof(Shared);
-static_assert(SMEM<false> <= 232448 && SMEM<true> <= 232448, "shared memory of a block");
+constexpr int SMEM_MAX = 232448;
+// Of dynamic shared memory: the queries of `rows` rows (a multiple of 8), then `slots` pages of K and V, then Shared.
+struct Plan {
+    int rows, k_slots, v_slots;
+    template <bool F32>
+    __host__ __device__ int q_bytes() const { return Lay<F32>::QPARTS * rows * HD * 2; }  // of one buffer
+    template <bool F32>
+    __host__ __device__ int ring() const { return Lay<F32>::QBUFS * q_bytes<F32>(); }
+    template <bool F32>
+    __host__ __device__ int shared() const { return ring<F32>() + (k_slots + v_slots) * PAGE_BYTES; }
+    template <bool F32>
+    __host__ __device__ int bytes() const { return shared<F32>() + (int)sizeof(Shared); }
+};
 
 __device__ __forceinline__ void arrive(u64* bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(s_addr(bar)) : "memory"); }
 __device__ __forceinline__ void arrive_tx(u64* bar, uint32_t bytes) {
@@ -81,12 +96,47 @@ __device__ __forceinline__ void arrive_tx(u64* bar, uint32_t bytes) {
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// D += A B with A (bf16 pairs, a column a pair) in TMEM
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bd, uint32_t idesc, uint32_t acc) {
+// One lane of the warp, the same each time.
+__device__ __forceinline__ bool elect() {
+    uint32_t e;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e != 0;
+}
+// Operand descriptors: the words that do not change (stride 1024 bytes, 128-byte swizzle), and the low ones: the address and, for
+// values (whose dims are two halves PAGE_BYTES / 2 apart), the leading offset.
+constexpr uint32_t DESC_HI = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return saddr >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr) { return saddr >> 4 | (PAGE_BYTES / 2 >> 4) << 16; }
+// D (+)= A B, both in shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-        "r"(a), "l"(bd), "r"(idesc), "r"(acc));
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(DESC_HI), "r"(idesc), "r"((uint32_t)acc));
+}
+// D (+)= A B with A (bf16 pairs, a column a pair) in TMEM
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(DESC_HI), "r"(idesc), "r"((uint32_t)acc));
+}
+__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+        "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+        "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+// A warp's wait, at most WAIT_TRIES tries (each takes some 20 cycles at least, and the hardware holds it for a while where it has to
+// wait): false then, and where another warp has given up.
+constexpr uint32_t WAIT_TRIES = 1u << 22;
+__device__ __forceinline__ bool wait_bounded(u64* bar, uint32_t parity, volatile int* stop) {
+    for (uint32_t n = 0; !__all_sync(0xffffffffu, tc_mbar_try((uint64_t*)bar, parity)); ++n) {
+        if (n >= WAIT_TRIES) *stop = 1;
+        if (__any_sync(0xffffffffu, *stop)) return false;
+    }
+    return true;
 }
 // two floats an instruction
 __device__ __forceinline__ u64 pair(float a, float b) {
@@ -122,7 +172,7 @@ __device__ __forceinline__ bool sequence(const Pages& c, const TreeArgs& a, int 
     }
     return n > 0;
 }
-__host__ __device__ constexpr int tiles_of(int len, int pages_a_tile) { return ((len + KVB - 1) / KVB + pages_a_tile) / pages_a_tile; }
+__host__ __device__ constexpr int tiles_of(int len) { return (len + KVB - 1) / KVB + 1; }
 
 // A warp finds what each node sees; lanes hold nodes l and l + 32. By doubling: what is seen within 2^k steps, and the node
 // 2^k steps up. False where a parent is out of order (taken as -1 then).
@@ -173,14 +223,15 @@ __device__ __forceinline__ void store_row(bf16* to, const float* x, float f) {
                                                        bf16_pair(x[d + 4] * f, x[d + 5] * f), bf16_pair(x[d + 6] * f, x[d + 7] * f));
 }
 
-// grid: the shares, 352 threads. All tiles of all (sequence, KV head) are one line, cut into equal shares. A warp deals the
-// pieces of its share, one loads pages by TMA into a ring of K and V slots (in the order in which the products take them),
-// one issues the products: S = Q K^T of tile t + 1, then O = P V of tile t. Four warps (a thread a row) turn scores into weights,
-// which replace them in TMEM as the A operand of P V; four more add each tile's sums to those in their registers. Every wait is bounded.
+// grid: the shares, 512 threads. All tiles of all (sequence, KV head) are one line, cut into equal shares. Of warps 12 .. 15 one
+// deals the pieces of its share, one loads pages (and bf16 queries) by TMA, one makes values safe to be multiplied by 0, and one
+// issues the products: scores S = Q K^T of tile t + AHEAD, then sums O = P V of tile t. Warps 0 .. 3 turn the scores of even tiles
+// into weights (a thread a row), which replace them in TMEM as the A operand of P V, warps 4 .. 7 those of odd tiles; they hand the
+// running maximum on. Warps 8 .. 11 add each tile's sums to those in their registers. Every wait is bounded.
 template <bool F32>
 __global__ void __launch_bounds__(NT, 1)
     k_tree_attn(const __grid_constant__ CUtensorMap pool_map, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                Pages c, TreeArgs a) {
+                const __grid_constant__ CUtensorMap q_map, Pages c, TreeArgs a, Plan plan) {
     typedef Lay<F32> L;
     typedef std::conditional_t<F32, float, bf16> T;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -192,26 +243,30 @@ __global__ void __launch_bounds__(NT, 1)
         }
         return;
     }
-    Shared& sh = *reinterpret_cast<Shared*>(smem + L::END);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, me = blockIdx.x;
+    unsigned char* const k_ring = smem + plan.ring<F32>();
+    unsigned char* const v_ring = k_ring + plan.k_slots * PAGE_BYTES;
+    Shared& sh = *reinterpret_cast<Shared*>(smem + plan.shared<F32>());
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, me = blockIdx.x;
     volatile int* const stop = &sh.abort;
     if (tid == 0) {
-        for (int i = 0; i < 8; ++i) {
-            tc_mbar_init((uint64_t*)sh.full + i, 1);
-            tc_mbar_init((uint64_t*)sh.empty + i, 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            tc_mbar_init((uint64_t*)sh.s_full + i, 2);
-            tc_mbar_init((uint64_t*)sh.p_full + i, SOFT_WARPS);
-            tc_mbar_init((uint64_t*)sh.o_full + i, 1 + SOFT_WARPS);
-            tc_mbar_init((uint64_t*)sh.o_empty + i, SUM_WARPS);
-        }
-        tc_mbar_init((uint64_t*)&sh.q_full, SOFT_WARPS);
-        for (int i = 0; i < PIECES; ++i) {
-            tc_mbar_init((uint64_t*)sh.piece_full + i, 1);
-            tc_mbar_init((uint64_t*)sh.piece_empty + i, 2 + SOFT_WARPS + SUM_WARPS);
-        }
-        tc_mbar_init((uint64_t*)&sh.fin, 1);
+        const auto init = [](u64* b, int n, int of) {
+            for (int i = 0; i < of; ++i) tc_mbar_init((uint64_t*)b + i, n);
+        };
+        init(sh.k_full, 1, MAX_SLOTS);
+        init(sh.k_empty, 1, MAX_SLOTS);
+        init(sh.v_full, 1, MAX_SLOTS);
+        init(sh.v_ready, 1, MAX_SLOTS);
+        init(sh.v_empty, 1, MAX_SLOTS);
+        init(sh.s_full, 2, 4);
+        init(sh.p_full, 4, 4);
+        init(sh.o_full, 2, 2);
+        init(sh.o_empty, 4, 2);
+        init(&sh.m_full[0][0], 1, 8);
+        init(sh.q_full, F32 ? 8 : 1, 2);
+        init(sh.q_empty, 1, 2);
+        init(sh.piece_full, 1, PIECES);
+        init(sh.piece_empty, 3 + 8 + 4, PIECES);
+        init(&sh.fin, 1, 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -223,11 +278,10 @@ __global__ void __launch_bounds__(NT, 1)
     pdl_wait();  // upstream results are read below
     pdl_trigger();
     // where the share begins: the sequences' tiles, one a thread at a time; the sum of all first, where one turn is not enough
-    long long total = 0, before = 0, first = 0, units = 0;
-    long long share = 0;
+    long long total = 0, before = 0, first = 0, units = 0, share = 0;
     const auto count = [&](int b, bool report) {
         int row, len, n;
-        return b < a.B && sequence(c, a, b, report, row, len, n) ? tiles_of(len, L::PAGES) : 0;
+        return b < a.B && sequence(c, a, b, report, row, len, n) ? tiles_of(len) : 0;
     };
     const auto deal = [&](long long tiles) {
         units = tiles * NKV;
@@ -270,334 +324,401 @@ __global__ void __launch_bounds__(NT, 1)
     __syncthreads();
     tc_after();
     const uint32_t tmem = sh.tmem;
-    const bool any = first < units;
+    const uint32_t U = first < units ? (uint32_t)min(share, units - first) : 0;  // this block's tiles
     bool ok = true;
     const auto wait = [&](u64* bar, uint32_t parity) {  // by whole warps
-        if (ok) ok = __all_sync(0xffffffffu, tc_wait((uint64_t*)bar, parity, stop));
-        if (!ok && lane == 0) *stop = 1;
+        ok = wait_bounded(bar, parity, stop);
         return ok;
     };
-    const auto wait1 = [&](u64* bar, uint32_t parity) {  // by one lane
-        if (ok) ok = tc_wait((uint64_t*)bar, parity, stop);
-        if (!ok) *stop = 1;
-        return ok;
-    };
+    // piece k, once it is there
+    const auto piece_bar = [&](uint32_t k) { return &sh.piece_full[k % PIECES]; };
+    const auto piece_par = [](uint32_t k) { return k / PIECES & 1u; };
 
-    if (warp == W_SCHED) {
-        int b = sh.start[0], at = sh.start[1], known = -1;
-        long long left = any ? min(share, units - first) : 0;
-        u64 seen[2] = {0, 0};
-        bool tree_ok = true, head = true;
-        int row = 0, len = 0, n = 0;
-        if (left > 0) sequence(c, a, b, false, row, len, n);
-        if (!any && lane == 0) a.meta[me] = make_int4(-1, 0, 0, 0);
-        for (int k = 0;; ++k) {
-            const int slot = k % PIECES;
-            if (k >= PIECES && !wait(&sh.piece_empty[slot], (k / PIECES - 1) & 1)) break;
-            Piece& p = sh.piece[slot];
-            if (left <= 0) {
+    if (warp >= W_REST) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
+        if (warp == W_SCHED) {
+            int b = sh.start[0], at = sh.start[1], known = -1;
+            long long left = U;
+            u64 seen[2] = {0, 0};
+            bool tree_ok = true, head = true;
+            int row = 0, len = 0, n = 0;
+            if (left > 0) sequence(c, a, b, false, row, len, n);
+            else if (lane == 0) a.meta[me] = make_int4(-1, 0, 0, 0);
+            for (int k = 0;; ++k) {
+                const int slot = k % PIECES;
+                if (k >= PIECES && !wait(&sh.piece_empty[slot], (uint32_t)(k / PIECES - 1) & 1u)) break;
+                Piece& p = sh.piece[slot];
+                if (left <= 0) {
+                    if (lane == 0) {
+                        p.b = -1;
+                        arrive(&sh.piece_full[slot]);
+                    }
+                    break;
+                }
+                const int nt = tiles_of(len), g = at / nt, t0 = at - g * nt, t1 = (int)min((long long)nt, t0 + left);
+                if (t1 == nt) {
+                    if (known != b) {
+                        tree_ok = ancestors(a.parents + (size_t)b * a.N, n, lane, seen);
+                        known = b;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) p.seen[lane + 32 * h] = seen[h];
+                    if (!tree_ok && lane == 0) set_err(c.err, TTS_BB_TREE_ERR_TREE);
+                }
                 if (lane == 0) {
-                    p.b = -1;
-                    arrive(&sh.piece_full[slot]);
+                    p.b = b;
+                    p.g = g;
+                    p.row = row;
+                    p.len = len;
+                    p.n = n;
+                    p.t0 = t0;
+                    p.t1 = t1;
+                    p.tiles = nt;
+                    p.ok = t1 < nt || tree_ok;
+                    p.whole = t0 == 0 && t1 == nt;
+                    p.first = head;
+                    p.bad[0] = p.bad[1] = 0;
+                    // of the share's first piece: its (sequence, head), nodes, and whether it begins inside of that one; bit 2: in order
+                    if (head) a.meta[me] = make_int4(b * NKV + g, n, (t0 > 0) | p.ok << 2, 0);
                 }
-                break;
-            }
-            const int nt = tiles_of(len, L::PAGES), g = at / nt, t0 = at - g * nt, t1 = (int)min((long long)nt, t0 + left);
-            if (t1 == nt) {
-                if (known != b) {
-                    tree_ok = ancestors(a.parents + (size_t)b * a.N, n, lane, seen);
-                    known = b;
+                __syncwarp();
+                if (lane == 0) arrive(&sh.piece_full[slot]);
+                head = false;
+                left -= t1 - t0;
+                at += t1 - t0;
+                if (at == nt * NKV && left > 0) {
+                    at = 0;
+                    do ++b; while (b < a.B && !sequence(c, a, b, false, row, len, n));
+                    if (b >= a.B) left = 0;
                 }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) p.seen[lane + 32 * h] = seen[h];
-                if (!tree_ok && lane == 0) set_err(c.err, TTS_BB_TREE_ERR_TREE);
             }
-            if (lane == 0) {
-                p.b = b;
-                p.g = g;
-                p.row = row;
-                p.len = len;
-                p.n = n;
-                p.t0 = t0;
-                p.t1 = t1;
-                p.pages = (len + KVB - 1) / KVB + 1;
-                p.ok = t1 < nt || tree_ok;
-                p.whole = t0 == 0 && t1 == nt;
-                p.first = head;
-                p.bad[0] = p.bad[1] = 0;
-                // of the share's first piece: its (sequence, head), nodes, and whether it begins and ends that one; bit 2: in order
-                if (head) a.meta[me] = make_int4(b * NKV + g, n, (t0 > 0) | (t1 == nt) << 1 | p.ok << 2, 0);
-            }
-            __syncwarp();
-            if (lane == 0) arrive(&sh.piece_full[slot]);
-            head = false;
-            left -= t1 - t0;
-            at += t1 - t0;
-            if (at == nt * NKV && left > 0) {
-                at = 0;
-                do ++b; while (b < a.B && !sequence(c, a, b, false, row, len, n));
-                if (b >= a.B) left = 0;
-            }
-        }
-    } else if (warp == W_LOAD) {
-        if (lane == 0) {
-            int slot_at = 0, tile = 0;  // loads so far; the block's tiles whose keys were loaded
-            // which 0: K, 1: V of tile t
-            const auto load = [&](const Piece& p, int t, int which) {
-                const int s = slot_at % L::SLOTS;
-                if (slot_at >= L::SLOTS && !wait1(&sh.empty[s], (slot_at / L::SLOTS - 1) & 1)) return false;
-                int rows[L::PAGES], there = 0;
-#pragma unroll
-                for (int i = 0; i < L::PAGES; ++i) {
-                    const int page = t * L::PAGES + i;
-                    rows[i] = -1;
-                    if (page < p.pages - 1) {
-                        const int at = page_of(c, p.row, page * KVB);
-                        if (at < 0) set_err(c.err, TTS_BB_TREE_ERR_PAGE);
-                        else rows[i] = ((at * 2 + which) * NKV + p.g) * KVB;
-                    } else if (page == p.pages - 1) {
-                        rows[i] = p.b * a.N;
-                    }
-                    there |= (rows[i] >= 0) << i;
-                }
-                if (!which) sh.there[tile++ % 8] = there;  // fewer than 8 tiles are in flight: each takes two slots
-                arrive_tx(&sh.full[s], (uint32_t)__popc(there) * PAGE_BYTES);
-                unsigned char* const to = smem + L::RING_OFF + s * L::SLOT;
-#pragma unroll
-                for (int i = 0; i < L::PAGES; ++i) {
-                    if (rows[i] < 0) continue;
-                    const bool tree = t * L::PAGES + i == p.pages - 1;
-                    const CUtensorMap* map = !tree ? &pool_map : which ? &v_map : &k_map;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        // K: [64 dims of h][keys]; V: [page][64 dims of h][64 keys]
-                        const int off = which ? i * PAGE_BYTES + h * (PAGE_BYTES / 2) : h * (L::SLOT / 2) + i * (PAGE_BYTES / 2);
-                        tma_load_2d(to + off, map, (tree ? p.g * HD : 0) + h * 64, rows[i], (uint64_t*)&sh.full[s]);
-                    }
-                }
-                ++slot_at;
-                return true;
+        } else if (warp == W_LOAD) {
+            int ks = 0, vs = 0;       // slots
+            uint32_t kp = 1, vp = 1;  // parities of what empties them (the first round is empty)
+            uint32_t kk = ~0u, vk = ~0u;
+            int kt = 0, vt = 0, from = 0;
+            int here = 0, next = 0;  // pages of the keys' tiles from + lane and from + 32 + lane
+            const Piece *kq = nullptr, *vq = nullptr;
+            const auto entry = [&](int t) { return t < kq->t1 && t < kq->tiles - 1 ? c.table[(size_t)kq->row * c.bps + t] : 0; };
+            // K (which 0) or V of a tile: a page of the pool, or the tree's own rows
+            const auto fetch = [&](unsigned char* to, u64* bar, const Piece& p, int t, int page, int which) {
+                arrive_tx(bar, page >= 0 ? PAGE_BYTES : 0);
+                if (page < 0) return;
+                const bool tree = t == p.tiles - 1;
+                const CUtensorMap* const map = !tree ? &pool_map : which ? &v_map : &k_map;
+                const int x = tree ? p.g * HD : 0, y = tree ? p.b * a.N : ((page * 2 + which) * NKV + p.g) * KVB;
+                tma_load_2d(to, map, x, y, (uint64_t*)bar);
+                tma_load_2d(to + PAGE_BYTES / 2, map, x + 64, y, (uint64_t*)bar);
             };
-            for (int k = 0; ok; ++k) {
-                const int slot = k % PIECES;
-                if (!wait1(&sh.piece_full[slot], (k / PIECES) & 1)) break;
-                const Piece& p = sh.piece[slot];
-                if (p.b < 0) break;
-                load(p, p.t0, 0);
-                for (int t = p.t0; ok && t < p.t1; ++t) {
-                    if (t + 1 < p.t1 && !load(p, t + 1, 0)) break;
-                    load(p, t, 1);
+            int k_landing = 0, v_landing = 0;
+            for (uint32_t i = 0; ok && i < U + L::AHEAD; ++i) {
+                if (i < U) {
+                    if (!kq || kt == kq->t1) {
+                        ++kk;
+                        if (!wait(piece_bar(kk), piece_par(kk))) break;
+                        kq = &sh.piece[kk % PIECES];
+                        from = kt = kq->t0;
+                        here = entry(from + lane);
+                        next = entry(from + 32 + lane);
+                        if constexpr (!F32) {
+                            const uint32_t qb = kk & 1;
+                            if (kk >= 2 && !wait(&sh.q_empty[qb], ((kk >> 1) - 1) & 1u)) {
+                                --kk;
+                                break;
+                            }
+                            if (lane == 0) {
+                                unsigned char* const to = smem + qb * plan.q_bytes<F32>();
+                                arrive_tx(&sh.q_full[qb], (uint32_t)a.N * 512);
+                                tma_load_3d(to, &q_map, 0, 2 * kq->g, kq->b * a.N, (uint64_t*)&sh.q_full[qb]);
+                                tma_load_3d(to + plan.rows * 128, &q_map, 64, 2 * kq->g, kq->b * a.N, (uint64_t*)&sh.q_full[qb]);
+                            }
+                        }
+                    } else if (kt == from + 32) {
+                        from = kt;
+                        here = next;
+                        next = entry(from + 32 + lane);
+                    }
+                    int page = __shfl_sync(0xffffffffu, here, kt - from);
+                    if (page < 0 || page >= c.n_blocks) {
+                        page = -1;
+                        if (lane == 0) set_err(c.err, TTS_BB_TREE_ERR_PAGE);
+                    }
+                    if (!wait(&sh.k_empty[ks], kp)) break;
+                    if (lane == 0) {
+                        sh.page[i % 16] = page;
+                        fetch(k_ring + ks * PAGE_BYTES, &sh.k_full[ks], *kq, kt, page, 0);
+                    }
+                    ++kt;
+                    ++k_landing;
+                    if (++ks == plan.k_slots) ks = 0, kp ^= 1;
                 }
-                arrive(&sh.piece_empty[slot]);
-            }
-            if (*stop)  // copies in flight land before the block ends
-                for (int j = max(0, slot_at - L::SLOTS); j < slot_at; ++j) {
-                    const unsigned long long t0 = g_time();
-                    while (!tc_mbar_try((uint64_t*)&sh.full[j % L::SLOTS], (j / L::SLOTS) & 1) && g_time() - t0 < TC_TIMEOUT_NS) {
+                if (i >= L::AHEAD) {
+                    if (!vq) {
+                        ++vk;
+                        if (!wait(piece_bar(vk), piece_par(vk))) break;
+                        vq = &sh.piece[vk % PIECES];
+                        vt = vq->t0;
+                    }
+                    if (!wait(&sh.v_empty[vs], vp)) break;
+                    if (lane == 0) fetch(v_ring + vs * PAGE_BYTES, &sh.v_full[vs], *vq, vt, sh.page[(i - L::AHEAD) % 16], 1);
+                    ++v_landing;
+                    if (++vs == plan.v_slots) vs = 0, vp ^= 1;
+                    __syncwarp();
+                    if (++vt == vq->t1) {  // from here on another piece may stand in its place
+                        if (lane == 0) arrive(&sh.piece_empty[vk % PIECES]);
+                        vq = nullptr;
                     }
                 }
-        }
-    } else if (warp == W_MMA) {
-        if (lane == 0) {
+            }
+            if (*stop && lane == 0) {  // copies in flight land before the block ends
+                const auto landed = [&](u64* full, int n, int slots) {
+                    for (int j = max(0, n - slots); j < n; ++j) {
+                        const unsigned long long t0 = g_time();
+                        while (!tc_mbar_try((uint64_t*)&full[j % slots], (uint32_t)(j / slots) & 1u) && g_time() - t0 < TC_TIMEOUT_NS) {
+                        }
+                    }
+                };
+                landed(sh.k_full, k_landing, plan.k_slots);
+                landed(sh.v_full, v_landing, plan.v_slots);
+                if (!F32) landed(sh.q_full, (int)(kk + 1), 2);
+            }
+        } else if (warp == W_MMA) {
             constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(128 >> 4) << 24);
-            constexpr uint32_t IDESC_S = IDESC | ((uint32_t)(L::KT >> 3) << 17), IDESC_PV = IDESC | ((uint32_t)(HD >> 3) << 17) | (1u << 16);
-            const uint32_t q0 = s_addr(smem), ring = s_addr(smem + L::RING_OFF);
-            int slot_at = 0, tile = 0;
-            const auto scores = [&](int j) {  // of the block's tile j
-                const int s = slot_at % L::SLOTS;
-                if (!wait1(&sh.full[s], (slot_at / L::SLOTS) & 1)) return;
-                // the weights of tile j - 2, which the scores replace, were taken by its product
-                if (j >= 2 && !wait1(&sh.o_full[j & 1], ((j - 2) >> 1) & 1)) return;
-                tc_after();
-                const uint32_t k0 = ring + (uint32_t)(s * L::SLOT), d = tmem + (uint32_t)((j & 1) * 128);
-#pragma unroll
-                for (int part = L::QPARTS - 1; part >= 0; --part)
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        at_mma(d, sw128_desc(q0 + (uint32_t)(part * L::Q_BYTES + (kk >> 2) * (L::Q_BYTES / 2) + (kk & 3) * 32)),
-                               sw128_desc(k0 + (uint32_t)((kk >> 2) * (L::SLOT / 2) + (kk & 3) * 32)), IDESC_S, part < L::QPARTS - 1 || kk ? 1u : 0u);
-                arrive(&sh.s_full[j & 1]);
-                at_commit((uint64_t*)&sh.s_full[j & 1]);
-                at_commit((uint64_t*)&sh.empty[s]);
-                ++slot_at;
-            };
-            for (int k = 0; ok; ++k) {
-                const int slot = k % PIECES;
-                if (!wait1(&sh.piece_full[slot], (k / PIECES) & 1)) break;
-                const int nt = sh.piece[slot].b < 0 ? 0 : sh.piece[slot].t1 - sh.piece[slot].t0;
-                if (nt == 0) break;
-                if (!wait1(&sh.q_full, k & 1)) break;
-                scores(tile);
-                for (int t = 0; ok && t < nt; ++t, ++tile) {
-                    if (t + 1 < nt) scores(tile + 1);
-                    if (!ok || !wait1(&sh.p_full[tile & 1], (tile >> 1) & 1)) break;
-                    const int s = slot_at % L::SLOTS;
-                    if (!wait1(&sh.full[s], (slot_at / L::SLOTS) & 1)) break;
-                    if (tile >= 2 && !wait1(&sh.o_empty[tile & 1], ((tile >> 1) - 1) & 1)) break;
+            constexpr uint32_t IDESC_S = IDESC | ((uint32_t)(KVB >> 3) << 17), IDESC_PV = IDESC | ((uint32_t)(HD >> 3) << 17) | (1u << 16);
+            const uint32_t q0 = desc_k(s_addr(smem)), k0 = desc_k(s_addr(k_ring)), v0 = desc_mn(s_addr(v_ring)), half = (uint32_t)plan.rows * 128 >> 4,
+                           q_buf = (uint32_t)plan.q_bytes<F32>() >> 4;
+            const bool leader = elect();
+            uint32_t ks = 0, vs = 0, kp = 0, vp = 0, sk = ~0u, pk = ~0u;  // slots, their parities, pieces of the scores and of the sums
+            int s_left = 0, p_left = 0, pt = 0, p_tiles = 0, p_len = 0, p_n = 0;
+            for (uint32_t i = 0; i < U + L::AHEAD; ++i) {
+                if (i < U) {
+                    if (s_left == 0) {
+                        ++sk;
+                        if (!wait(piece_bar(sk), piece_par(sk))) break;
+                        s_left = sh.piece[sk % PIECES].t1 - sh.piece[sk % PIECES].t0;
+                        if (!wait(&sh.q_full[F32 ? 0 : sk & 1], (F32 ? sk : sk >> 1) & 1u)) break;
+                    }
+                    if (!wait(&sh.k_full[ks], kp)) break;
+                    // the weights in the region were taken by the product of tile i - REGIONS
+                    const uint32_t region = i % L::REGIONS, j = i - L::REGIONS;
+                    if (i >= L::REGIONS && !wait(&sh.o_full[j & 1], (j >> 1) & 1u)) break;
                     tc_after();
-                    const uint32_t v0 = ring + (uint32_t)(s * L::SLOT), w = tmem + (uint32_t)((tile & 1) * 128), d = tmem + 256 + (uint32_t)((tile & 1) * 128);
+                    const uint32_t d = tmem + region * L::REGION, k1 = k0 + ks * (PAGE_BYTES >> 4), q1 = q0 + (F32 ? 0u : (sk & 1) * q_buf);
+                    --s_left;
+                    if (leader) {
 #pragma unroll
-                    for (int part = L::PPARTS - 1; part >= 0; --part)
+                        for (int part = L::QPARTS - 1; part >= 0; --part)
 #pragma unroll
-                        for (int kk = 0; kk < L::KT / 16; ++kk)  // 16 keys a step: 8 columns of weights
-                            mma_ts(d, w + (uint32_t)(part * (L::KT / 2) + kk * 8),
-                                   sw128_desc_mn(v0 + (uint32_t)((kk >> 2) * PAGE_BYTES + (kk & 3) * 2048), PAGE_BYTES / 2, 1024), IDESC_PV,
-                                   part < L::PPARTS - 1 || kk ? 1u : 0u);
-                    at_commit((uint64_t*)&sh.o_full[tile & 1]);
-                    at_commit((uint64_t*)&sh.empty[s]);
-                    ++slot_at;
-                }
-                arrive(&sh.piece_empty[slot]);
-            }
-            if (!ok) *stop = 1;
-            at_commit((uint64_t*)&sh.fin);  // every product has ended
-            const unsigned long long t0 = g_time();
-            while (!tc_mbar_try((uint64_t*)&sh.fin, 0) && g_time() - t0 < TC_TIMEOUT_NS) {
-            }
-        }
-    } else if (warp < SOFT_WARPS) {
-        // ---------------- scores to weights: thread = row
-        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-        const int r = tid;
-        const float cs = 0.08838834764831845f * 1.4426950408889634f;
-        int slot_at = 0, tile = 0;
-        for (int k = 0; ok; ++k) {
-            const int slot = k % PIECES;
-            if (!wait(&sh.piece_full[slot], (k / PIECES) & 1)) break;
-            Piece& p = sh.piece[slot];
-            if (p.b < 0) break;
-            const int nt = p.t1 - p.t0, rows = 2 * p.n;
-            const bool mine = warp * 32 < rows;
-            if (mine) {
-                // queries of this warp's rows; those of the piece before were read by products that have ended
-                const T* const q = static_cast<const T*>(a.q) + (size_t)p.b * a.N * a.q_stride + 2 * p.g * HD;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    constexpr int V = F32 ? 2 : 1;
-                    uint4 x[8][V];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int e = (half * 8 + i) * 32 + lane, qr = warp * 32 + (e >> 4), pc = e & 15;
-#pragma unroll
-                        for (int v = 0; v < V; ++v) x[i][v] = make_uint4(0u, 0u, 0u, 0u);
-                        if (qr < rows) {
-                            const uint4* const src = reinterpret_cast<const uint4*>(q + (qr >> 1) * a.q_stride + (qr & 1) * HD + pc * 8);
-#pragma unroll
-                            for (int v = 0; v < V; ++v) x[i][v] = src[v];
-                        }
+                            for (int kk = 0; kk < 8; ++kk)
+                                mma_ss(d, q1 + (uint32_t)(part * 2 + (kk >> 2)) * half + (kk & 3) * 2, k1 + (uint32_t)((kk >> 2) * (PAGE_BYTES / 2) + (kk & 3) * 32) / 16,
+                                       IDESC_S, part < L::QPARTS - 1 || kk > 0);
+                        arrive(&sh.s_full[region]);
+                        at_commit((uint64_t*)&sh.s_full[region]);
+                        at_commit((uint64_t*)&sh.k_empty[ks]);
+                        if (!F32 && s_left == 0) at_commit((uint64_t*)&sh.q_empty[sk & 1]);
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int e = (half * 8 + i) * 32 + lane, qr = warp * 32 + (e >> 4), pc = e & 15;
-                        unsigned char* const to = smem + (pc >> 3) * (L::Q_BYTES / 2) + sw128_off(qr, pc & 7);
-                        if constexpr (F32) {
-                            float f[8];
-                            uint32_t w[4];
-#pragma unroll
-                            for (int v = 0; v < 2; ++v) {
-                                f[4 * v] = __uint_as_float(x[i][v].x);
-                                f[4 * v + 1] = __uint_as_float(x[i][v].y);
-                                f[4 * v + 2] = __uint_as_float(x[i][v].z);
-                                f[4 * v + 3] = __uint_as_float(x[i][v].w);
-                            }
-#pragma unroll
-                            for (int part = 0; part < 3; ++part) {
-#pragma unroll
-                                for (int u = 0; u < 4; ++u) {
-                                    w[u] = bf16_pair(f[2 * u], f[2 * u + 1]);
-                                    f[2 * u] -= __uint_as_float(w[u] << 16);
-                                    f[2 * u + 1] -= __uint_as_float(w[u] & 0xFFFF0000u);
-                                }
-                                *reinterpret_cast<uint4*>(to + part * L::Q_BYTES) = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        } else {
-                            *reinterpret_cast<uint4*>(to) = x[i][0];
-                        }
-                    }
+                    __syncwarp();
+                    if (++ks == (uint32_t)plan.k_slots) ks = 0, kp ^= 1;
                 }
-                fence_async();
+                if (i >= L::AHEAD) {
+                    const uint32_t u = i - L::AHEAD, region = u % L::REGIONS;
+                    if (p_left == 0) {
+                        ++pk;
+                        if (!wait(piece_bar(pk), piece_par(pk))) break;
+                        const Piece& p = sh.piece[pk % PIECES];
+                        pt = p.t0;
+                        p_left = p.t1 - pt;
+                        p_tiles = p.tiles;
+                        p_len = p.len;
+                        p_n = p.n;
+                    }
+                    // 16 keys a step, of those that there are
+                    const int keys = pt == p_tiles - 1 ? p_n : min(KVB, p_len - pt * KVB), steps = (keys + 15) / 16;
+                    if (!wait(&sh.p_full[region], (u / L::REGIONS) & 1u)) break;
+                    if (!wait(&sh.v_ready[vs], vp)) break;
+                    if (u >= 2 && !wait(&sh.o_empty[u & 1], ((u >> 1) - 1) & 1u)) break;
+                    tc_after();
+                    const uint32_t w = tmem + region * L::REGION, d = tmem + 256 + (u & 1) * 128, v1 = v0 + vs * (PAGE_BYTES >> 4);
+                    ++pt;
+                    --p_left;
+                    if (leader) {
+#pragma unroll
+                        for (int part = L::PPARTS - 1; part >= 0; --part)
+#pragma unroll
+                            for (int kk = 0; kk < KVB / 16; ++kk)  // 8 columns of weights
+                                if (kk < steps) mma_ts(d, w + (uint32_t)(part * (KVB / 2) + kk * 8), v1 + (uint32_t)(kk * 2048 / 16), IDESC_PV, part < L::PPARTS - 1 || kk > 0);
+                        arrive(&sh.o_full[u & 1]);
+                        at_commit((uint64_t*)&sh.o_full[u & 1]);
+                        at_commit((uint64_t*)&sh.v_empty[vs]);
+                        if (p_left == 0) arrive(&sh.piece_empty[pk % PIECES]);
+                    }
+                    __syncwarp();
+                    if (++vs == (uint32_t)plan.v_slots) vs = 0, vp ^= 1;
+                }
+            }
+            if (!ok && lane == 0) *stop = 1;
+            if (leader) {
+                at_commit((uint64_t*)&sh.fin);  // every product has ended
+                const unsigned long long t0 = g_time();
+                while (!tc_mbar_try((uint64_t*)&sh.fin, 0) && g_time() - t0 < TC_TIMEOUT_NS) {
+                }
             }
             __syncwarp();
-            if (lane == 0) arrive(&sh.q_full);
-            float m = -INFINITY, mc = -INFINITY, l = 0.f;  // the largest score, that times cs, the sum of weights
-            for (int t = 0; t < nt; ++t, ++tile) {
-                const int vi = slot_at + (t + 1 < nt ? 2 * t + 2 : 2 * t + 1), vs = vi % L::SLOTS;
-                if (!wait(&sh.s_full[tile & 1], (tile >> 1) & 1)) break;
-                tc_after();
-                // the keys that count, a bit each, and the pages whose values have to be made safe
-                u64 keys[L::PAGES];
-                bool partial = false;
-                const int there = sh.there[tile % 8];
-#pragma unroll
-                for (int i = 0; i < L::PAGES; ++i) {
-                    const int page = (p.t0 + t) * L::PAGES + i, valid = p.len - page * KVB;
-                    keys[i] = !(there >> i & 1) ? 0ull : page == p.pages - 1 ? (r < rows ? p.seen[r >> 1] : 0ull) : valid >= KVB ? ~0ull : (1ull << valid) - 1;
-                    partial |= page >= p.pages - 1 || valid < KVB || !(there >> i & 1);
+        } else if (warp == W_SAFE) {
+            // Values that weights of 0 may meet: rows behind a page's keys (up to a step of 16) and pages that were not there become
+            // zeros, and so does what is not finite among the tree's: it is added to the rows that see it at the end.
+            int t = 0, vs = 0;
+            uint32_t vp = 0, k = ~0u;
+            Piece* p = nullptr;
+            for (uint32_t u = 0; ok && u < U; ++u) {
+                if (!p) {
+                    ++k;
+                    if (!wait(piece_bar(k), piece_par(k))) break;
+                    p = &sh.piece[k % PIECES];
+                    t = p->t0;
                 }
-                if (partial) {
-                    // rows of V that do not count are zeroed, and what is not finite among the tree's (it is added to the rows that see it at
-                    // the end): 0 times it would be NaN. Warp w: keys 16 w .. 16 w + 15 of each page
-                    if (!wait(&sh.full[vs], (vi / L::SLOTS) & 1)) break;
-                    unsigned char* const v0 = smem + L::RING_OFF + vs * L::SLOT;
+                if (!wait(&sh.v_full[vs], vp)) break;
+                const bool tree = t == p->tiles - 1;
+                const int keys = tree ? p->n : min(KVB, p->len - t * KVB), valid = sh.page[u % 16] >= 0 ? keys : 0;
+                if (tree || valid < KVB) {
+                    unsigned char* const v1 = v_ring + vs * PAGE_BYTES;
+                    const auto at = [&](int key, int pc) {
+                        return reinterpret_cast<uint4*>(v1 + (pc >> 3) * (PAGE_BYTES / 2) + sw128_off(key, pc & 7));
+                    };
+                    // 2 keys an instruction
+                    for (int key = valid + (lane >> 4); key < (keys + 15) / 16 * 16; key += 2) *at(key, lane & 15) = make_uint4(0u, 0u, 0u, 0u);
+                    if (tree) {
+                        for (int key0 = lane >> 4; key0 < valid; key0 += 8) {
+                            uint4 x[4];
 #pragma unroll
-                    for (int i = 0; i < L::PAGES; ++i) {
-                        const int page = (p.t0 + t) * L::PAGES + i;
-                        const bool tree = page == p.pages - 1;
-                        const int valid = !(there >> i & 1) ? 0 : tree ? p.n : min(KVB, p.len - page * KVB);
-                        if (valid == KVB && !tree) continue;
+                            for (int i = 0; i < 4; ++i) x[i] = key0 + 2 * i < valid ? *at(key0 + 2 * i, lane & 15) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                        for (int e = lane; e < 256; e += 32) {
-                            const int key = warp * 16 + (e >> 4), pc = e & 15;
-                            uint4* const at = reinterpret_cast<uint4*>(v0 + i * PAGE_BYTES + (pc >> 3) * (PAGE_BYTES / 2) + sw128_off(key, pc & 7));
-                            if (key >= valid) {
-                                *at = make_uint4(0u, 0u, 0u, 0u);
-                            } else if (tree) {
-                                const uint4 x = *at;
-                                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
                                 bool bad = false;
 #pragma unroll
-                                for (int u = 0; u < 4; ++u) {
-                                    if (!finite16(w[u])) { w[u] &= 0xFFFF0000u; bad = true; }
-                                    if (!finite16(w[u] >> 16)) { w[u] &= 0xFFFFu; bad = true; }
+                                for (int h = 0; h < 4; ++h) {
+                                    if (!finite16(w[h])) { w[h] &= 0xFFFF0000u; bad = true; }
+                                    if (!finite16(w[h] >> 16)) { w[h] &= 0xFFFFu; bad = true; }
                                 }
                                 if (bad) {
-                                    *at = make_uint4(w[0], w[1], w[2], w[3]);
-                                    atomicOr(&p.bad[key >> 5], 1u << (key & 31));
+                                    const int key = key0 + 2 * i;
+                                    *at(key, lane & 15) = make_uint4(w[0], w[1], w[2], w[3]);
+                                    atomicOr(&p->bad[key >> 5], 1u << (key & 31));
                                 }
                             }
                         }
                     }
                     fence_async();
                 }
-                float alpha = 1.f;
+                __syncwarp();
+                if (lane == 0) arrive(&sh.v_ready[vs]);
+                if (++vs == plan.v_slots) vs = 0, vp ^= 1;
+                if (++t == p->t1) {
+                    if (lane == 0) arrive(&sh.piece_empty[k % PIECES]);
+                    p = nullptr;
+                }
+            }
+        }
+    } else if (warp < W_SUM) {
+        // ---------------- scores to weights: thread = row; warps 0 .. 3 even tiles, 4 .. 7 odd ones
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
+        const int group = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        const float cs = 0.08838834764831845f * 1.4426950408889634f;
+        uint32_t u0 = 0;
+        for (uint32_t k = 0; ok; ++k) {
+            if (!wait(piece_bar(k), piece_par(k))) break;
+            const Piece& p = sh.piece[k % PIECES];
+            if (p.b < 0) break;
+            const int nt = p.t1 - p.t0, rows = 2 * p.n;
+            if constexpr (F32) {
+                // the queries, a warp 16 rows; those of the piece before were read by products that have ended
+                if (u0 > 0 && !wait(&sh.s_full[(u0 - 1) % L::REGIONS], ((u0 - 1) / L::REGIONS) & 1u)) break;
+                if (warp * 16 < rows) {
+                    const float* const q = static_cast<const float*>(a.q) + (size_t)p.b * a.N * a.q_stride + 2 * p.g * HD;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        float4 x[4][2];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = (half * 4 + i) * 32 + lane, qr = warp * 16 + (e >> 4), pc = e & 15;
+                            x[i][0] = x[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (qr < rows) {
+                                const float4* const src = reinterpret_cast<const float4*>(q + (qr >> 1) * a.q_stride + (qr & 1) * HD + pc * 8);
+                                x[i][0] = src[0];
+                                x[i][1] = src[1];
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = (half * 4 + i) * 32 + lane, qr = warp * 16 + (e >> 4), pc = e & 15;
+                            if (qr >= plan.rows) continue;
+                            unsigned char* const to = smem + (pc >> 3) * plan.rows * 128 + sw128_off(qr, pc & 7);
+                            float f[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+                            uint32_t w[4];
+#pragma unroll
+                            for (int part = 0; part < 3; ++part) {
+#pragma unroll
+                                for (int h = 0; h < 4; ++h) {
+                                    w[h] = bf16_pair(f[2 * h], f[2 * h + 1]);
+                                    f[2 * h] -= __uint_as_float(w[h] << 16);
+                                    f[2 * h + 1] -= __uint_as_float(w[h] & 0xFFFF0000u);
+                                }
+                                *reinterpret_cast<uint4*>(to + part * plan.rows * 256) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                    }
+                    fence_async();
+                }
+                __syncwarp();
+                if (lane == 0) arrive(&sh.q_full[0]);
+            }
+            const bool mine = quarter * 32 < rows;
+            float mc = -INFINITY, l = 0.f;  // of this warp's tiles: the reference, and the sum of weights
+            for (uint32_t u = u0 + ((u0 ^ group) & 1); u < u0 + nt; u += 2) {
+                const int t = p.t0 + (int)(u - u0);
+                const uint32_t at = lanes + (u % L::REGIONS) * L::REGION;
+                if (!wait(&sh.s_full[u % L::REGIONS], (u / L::REGIONS) & 1u)) break;
+                uint32_t s[KVB];
+                float m = -INFINITY;
                 if (mine) {
-                    const uint32_t at = lanes + (uint32_t)((tile & 1) * 128);
-                    uint32_t s[L::KT];
+                    tc_after();
 #pragma unroll
-                    for (int i = 0; i < L::KT; i += 32) tm_ld32_nw(at + i, s + i);
+                    for (int i = 0; i < KVB; i += 32) tm_ld32_nw(at + i, s + i);
                     tm_wait_ld();
-                    if (partial) {
+                    // the keys that count, a bit each
+                    const bool tree = t == p.tiles - 1;
+                    const int valid = p.len - t * KVB;
+                    const bool there = sh.page[u % 16] >= 0;
+                    if (tree || valid < KVB || !there) {
+                        const u64 keys = !there ? 0ull : tree ? (r < rows ? p.seen[r >> 1] : 0ull) : (1ull << valid) - 1;
 #pragma unroll
-                        for (int i = 0; i < L::KT; ++i)
-                            if (!(keys[i >> 6] >> (i & 63) & 1)) s[i] = 0xFF800000u;  // -inf
+                        for (int i = 0; i < KVB; ++i)
+                            if (!((uint32_t)(keys >> (i & 32)) >> (i & 31) & 1)) s[i] = 0xFF800000u;  // -inf
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < L::KT; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    if (top > m) {
-                        alpha = at_ex2(mc - top * cs);
-                        m = top;
-                        mc = top * cs;
-                    }
-                    const float base = m == -INFINITY ? 0.f : mc;
+                    for (int i = 0; i < KVB; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+                    m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                }
+                // the maximum so far, from the warp of the tile before (waited for at a new piece too: no warp is two tiles ahead)
+                if (u > 0) {
+                    if (!wait(&sh.m_full[quarter][(u - 1) & 1], ((u - 1) >> 1) & 1u)) break;
+                    if (u > u0) m = fmaxf(m, sh.m[(u - 1) % RING][r]);
+                }
+                sh.m[u % RING][r] = m;
+                __syncwarp();
+                if (lane == 0) arrive(&sh.m_full[quarter][u & 1]);
+                if (mine) {
+                    const float now = m * cs, base = m == -INFINITY ? 0.f : now;
                     const u64 cs2 = pair(cs, cs), base2 = pair(-base, -base), minus = pair(-1.f, -1.f);
                     u64 sum[2] = {0, 0};
 #pragma unroll
-                    for (int i0 = 0; i0 < L::KT; i0 += 64) {
-                        uint32_t w[L::PPARTS][32];
+                    for (int i0 = 0; i0 < KVB; i0 += 32) {
+                        uint32_t w[L::PPARTS][16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
+                        for (int i = 0; i < 16; ++i) {
                             float x, y;
                             halves(fma2(pair(__uint_as_float(s[i0 + 2 * i]), __uint_as_float(s[i0 + 2 * i + 1])), cs2, base2), x, y);
                             u64 e = pair(at_ex2(x), at_ex2(y));
@@ -611,75 +732,72 @@ __global__ void __launch_bounds__(NT, 1)
                             }
                         }
 #pragma unroll
-                        for (int part = 0; part < L::PPARTS; ++part) tm_st32(at + (uint32_t)(part * (L::KT / 2) + i0 / 2), w[part]);
+                        for (int part = 0; part < L::PPARTS; ++part) tm_st16(at + (uint32_t)(part * (KVB / 2) + i0 / 2), w[part]);
                     }
-                    float x, y, z, u;
+                    float x, y, z, v;
                     halves(sum[0], x, y);
-                    halves(sum[1], z, u);
-                    l = l * alpha + ((x + y) + (z + u));
+                    halves(sum[1], z, v);
+                    l = (l == 0.f ? 0.f : l * at_ex2(mc - base)) + ((x + y) + (z + v));
+                    mc = now;
+                    if (u + 2 >= u0 + nt) sh.l[u % RING][r] = l;
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                }
-                sh.alpha[tile % RING][r] = alpha;
-                if (t + 1 == nt) {
-                    sh.m[tile % RING][r] = m == -INFINITY ? -INFINITY : mc;
-                    sh.l[tile % RING][r] = l;
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0) {
-                    arrive(&sh.p_full[tile & 1]);
-                    arrive(&sh.o_full[tile & 1]);
-                }
+                if (lane == 0) arrive(&sh.p_full[u % L::REGIONS]);
             }
             if (!ok) break;
-            slot_at += 2 * nt;
+            u0 += nt;
             __syncwarp();
-            if (lane == 0) arrive(&sh.piece_empty[slot]);
+            if (lane == 0) arrive(&sh.piece_empty[k % PIECES]);
         }
     } else {
         // ---------------- a row's sums over the tiles: thread = row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SUM));
         const int quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = tmem + 256 + ((uint32_t)(quarter * 32) << 16);
-        int tile = 0;
-        for (int k = 0; ok; ++k) {
-            const int slot = k % PIECES;
-            if (!wait(&sh.piece_full[slot], (k / PIECES) & 1)) break;
-            const Piece& p = sh.piece[slot];
+        const float cs = 0.08838834764831845f * 1.4426950408889634f;
+        uint32_t u = 0;
+        for (uint32_t k = 0; ok; ++k) {
+            if (!wait(piece_bar(k), piece_par(k))) break;
+            const Piece& p = sh.piece[k % PIECES];
             if (p.b < 0) break;
             const int nt = p.t1 - p.t0, rows = 2 * p.n;
             const bool mine = quarter * 32 < rows;
             u64 o[HD / 2];
 #pragma unroll
             for (int i = 0; i < HD / 2; ++i) o[i] = 0;
-            float m = 0.f, l = 0.f;
-            for (int t = 0; t < nt; ++t, ++tile) {
-                if (!wait(&sh.o_full[tile & 1], (tile >> 1) & 1)) break;
-                tc_after();
+            float m = -INFINITY, l = 0.f;  // the reference, times cs
+            for (int t = 0; t < nt; ++t, ++u) {
+                if (!wait(&sh.o_full[u & 1], (u >> 1) & 1u)) break;
                 if (mine) {
-                    const float f = sh.alpha[tile % RING][r];
+                    tc_after();
+                    const float now = sh.m[u % RING][r] * cs, f = t == 0 ? 0.f : now == m ? 1.f : at_ex2(m - now);
                     const u64 f2 = pair(f, f);
+                    const uint32_t at = lanes + (u & 1) * 128;
+                    uint32_t x[2][32];  // the next 32 dims are on their way while these are added
+                    tm_ld32_nw(at, x[0]);
 #pragma unroll
-                    for (int i = 0; i < HD; i += 32) {
-                        uint32_t x[32];
-                        tm_ld32_nw(lanes + (uint32_t)((tile & 1) * 128 + i), x);
+                    for (int i = 0; i < 4; ++i) {
                         tm_wait_ld();
+                        if (i < 3) tm_ld32_nw(at + 32 * (i + 1), x[(i + 1) & 1]);
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            o[i / 2 + j] = fma2(o[i / 2 + j], f2, pair(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])));
+                            o[16 * i + j] = fma2(o[16 * i + j], f2, pair(__uint_as_float(x[i & 1][2 * j]), __uint_as_float(x[i & 1][2 * j + 1])));
                     }
-                    m = sh.m[tile % RING][r];
-                    l = sh.l[tile % RING][r];
+                    if (t + 2 >= nt) l = (t == 0 || l == 0.f ? 0.f : l * f) + sh.l[u % RING][r];  // of even and of odd tiles
+                    m = now;
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0) arrive(&sh.o_empty[tile & 1]);
+                if (lane == 0) arrive(&sh.o_empty[u & 1]);
             }
             if (!ok) break;
             if (r < rows) {
                 float x[HD];
 #pragma unroll
                 for (int i = 0; i < HD / 2; ++i) halves(o[i], x[2 * i], x[2 * i + 1]);
-                const u64 bad = ((u64)p.bad[1] << 32 | p.bad[0]) & (p.bad[0] | p.bad[1] ? p.seen[r >> 1] : 0ull);
+                const u64 bad = p.bad[0] | p.bad[1] ? ((u64)p.bad[1] << 32 | p.bad[0]) & p.seen[r >> 1] : 0ull;
                 for (u64 left = bad; left; left &= left - 1) {  // what was set aside
                     const bf16* const v = a.v + ((size_t)p.b * a.N + __ffsll(left) - 1) * a.kv_stride + p.g * HD;
 #pragma unroll
@@ -698,7 +816,7 @@ __global__ void __launch_bounds__(NT, 1)
                 }
             }
             __syncwarp();
-            if (lane == 0) arrive(&sh.piece_empty[slot]);
+            if (lane == 0) arrive(&sh.piece_empty[k % PIECES]);
         }
     }
     if (!ok && lane == 0) set_err(c.err, TTS_BB_TREE_ERR_TIMEOUT);
@@ -749,16 +867,23 @@ __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
 }
 
 // Blocks of the launch: one an SM, or one a tile where there are fewer.
-int share_count(int B, int max_len, int pages_a_tile) {
-    return (int)std::min<long long>(SHARES, (long long)B * NKV * tiles_of(max_len, pages_a_tile));
-}
+int share_count(int B, int max_len) { return (int)std::min<long long>(SHARES, (long long)B * NKV * tiles_of(max_len)); }
 constexpr size_t META_BYTES = (SHARES * sizeof(int4) + 255) / 256 * 256;
+// As many pages of K and V as fit behind the queries.
+template <bool F32>
+Plan plan_of(int N) {
+    Plan p{(2 * N + 7) / 8 * 8, 0, 0};
+    const int slots = std::min(2 * MAX_SLOTS, (SMEM_MAX - p.bytes<F32>()) / PAGE_BYTES);
+    p.k_slots = slots / 2;
+    p.v_slots = slots - p.k_slots;
+    return p;
+}
 
 }  // namespace
 
 TTS_API size_t tts_bb_tree_attention_workspace(int B, int N, int max_len) {
-    if (!tree_ok(B, N) || max_len < 0 || max_len > (1 << 30)) return 0;
-    return META_BYTES + (size_t)share_count(B, max_len, 1) * 2 * 2 * N * PART * sizeof(float);  // of both types
+    if (!tree_ok(B, N) || max_len < 0 || max_len > (1 << 30) || (long long)B * max_len > (1ll << 40)) return 0;
+    return META_BYTES + (size_t)share_count(B, max_len) * 2 * 2 * N * PART * sizeof(float);
 }
 
 TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int layer, int B, int N, const void* q, int type,
@@ -768,30 +893,41 @@ TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int la
                                             size_t workspace_bytes, void* stream) {
     if (!cache_ok(cache) || layer < 0 || layer >= cache->n_layers || !tree_ok(B, N) || !q || !k || !v || !parents || !kv_lens || !out ||
         (type != TTS_BB_T_F32 && type != TTS_BB_T_BF16) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) ||
-        q_stride < NQ * HD || q_stride % (type == TTS_BB_T_F32 ? 4 : 8) || kv_stride < NKV * HD || kv_stride % 8 || kv_stride > (1ll << 38) ||
-        max_len < 0 || max_len > (1 << 30) || (long long)max_len > (long long)cache->blocks_per_seq * KVB || (!seqs && B > cache->n_seqs) ||
-        !words_aligned(parents, n_nodes, seqs, kv_lens))
+        q_stride < NQ * HD || q_stride % (type == TTS_BB_T_F32 ? 4 : 8) || kv_stride < NKV * HD || kv_stride % 8 ||
+        q_stride > (1ll << 38) || kv_stride > (1ll << 38) || max_len < 0 || max_len > (1 << 30) || (long long)B * max_len > (1ll << 40) ||
+        (long long)max_len > (long long)cache->blocks_per_seq * KVB || (!seqs && B > cache->n_seqs) || !words_aligned(parents, n_nodes, seqs, kv_lens))
         return TTS_BB_E_INVALID;
     if (!workspace || workspace_bytes < tts_bb_tree_attention_workspace(B, N, max_len) || !aligned16(workspace)) return TTS_BB_E_INVALID;
     if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
     const Pages c = pages_of(cache, layer);
-    CUtensorMap pool_map, k_map, v_map;
+    CUtensorMap pool_map, k_map, v_map, q_map;
     if (!tc_make_map_strided(&pool_map, c.pool, c.n_blocks * 2 * NKV * KVB, HD, HD, KVB) ||
-        !tc_make_map_strided(&k_map, k, B * N, NKV * HD, kv_stride, KVB) || !tc_make_map_strided(&v_map, v, B * N, NKV * HD, kv_stride, KVB))
+        !tc_make_map_strided(&k_map, k, B * N, NKV * HD, kv_stride, KVB) || !tc_make_map_strided(&v_map, v, B * N, NKV * HD, kv_stride, KVB) ||
+        (type == TTS_BB_T_BF16 && !tc_make_map_heads(&q_map, q, B * N, NQ, q_stride, N)))
         return TTS_BB_E_CUDA;
+    if (type != TTS_BB_T_BF16) q_map = k_map;  // not used
     const TreeArgs a{q, static_cast<const bf16*>(v), q_stride, kv_stride, parents, n_nodes, seqs, kv_lens, B, N, max_len, out,
                      static_cast<int4*>(workspace), reinterpret_cast<float*>(static_cast<char*>(workspace) + META_BYTES)};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int shares = share_count(B, max_len);
+    bool regs = true;
     const auto go = [&](auto f32) {
         constexpr bool F32 = decltype(f32)::value;
         static SmemState state;
-        allow_smem(state, k_tree_attn<F32>, SMEM<F32>);
-        const int shares = share_count(B, max_len, Lay<F32>::PAGES);
-        launch_pdl(k_tree_attn<F32>, shares, NT, SMEM<F32>, st, pool_map, k_map, v_map, c, a);
-        if (tiles_of(max_len, Lay<F32>::PAGES) > 1)
+        allow_smem(state, k_tree_attn<F32>, SMEM_MAX);
+        // what its warps deal anew has to be there at the launch: they would wait for it
+        static const bool enough = [] {
+            cudaFuncAttributes f{};
+            return cudaFuncGetAttributes(&f, k_tree_attn<F32>) == cudaSuccess && f.numRegs >= 128;
+        }();
+        regs = enough;
+        if (!regs) return;
+        const Plan plan = plan_of<F32>(N);
+        launch_pdl(k_tree_attn<F32>, shares, NT, plan.bytes<F32>(), st, pool_map, k_map, v_map, q_map, c, a, plan);
+        if (tiles_of(max_len) > 1)
             launch_pdl(k_tree_combine<std::conditional_t<F32, float, bf16>>, dim3(shares - 1, (2 * N + 3) / 4), 128, 0, st, a, shares);
     };
     if (type == TTS_BB_T_F32) go(std::true_type{});
     else go(std::false_type{});
-    return launched();
+    return regs ? launched() : TTS_BB_E_CUDA;
 }
