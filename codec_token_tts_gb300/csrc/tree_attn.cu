@@ -26,21 +26,23 @@ struct TreeArgs {
     int B, N, max_len;
     void* out;
     int4* meta;   // [shares]: the first piece of each
-    float* part;  // [shares][2][2 N][PART]
+    float4* part; // [shares][2][PART][128]
 };
 
 constexpr int PAGE_BYTES = KVB * HD * 2;  // K or V of a page and head
-constexpr int PART = HD + 4;              // 128 sums, the reference and the weight, 16-byte rows
+constexpr int PART = HD / 4 + 1;          // a row's 128 sums by four, then its reference and weight: rows side by side
 constexpr int SHARES = 152;               // a block an SM
 
 // A share's work: a piece of the tiles (a page each) of one (sequence, KV head), the last of which is the tree.
 struct Piece {
     int b, g, row, len, n;  // b < 0: no more
     int t0, t1, tiles;
-    int ok;                 // the tree is in order (known where the piece holds the tree)
     int whole, first;
     uint32_t bad[2];        // nodes whose values are not all finite
+    // of pieces that hold the tree, a little later:
+    int ok;                 // the tree is in order
     u64 seen[MAX_NODES];    // ancestors and self
+    int up[MAX_NODES];
 };
 
 // bf16: queries as they are, weights in two bf16 parts (17 bits, both rounded). fp32: queries and weights in three parts
@@ -48,13 +50,17 @@ struct Piece {
 template <bool F32>
 struct Lay {
     static constexpr int QPARTS = F32 ? 3 : 1, PPARTS = F32 ? 3 : 2, QBUFS = F32 ? 1 : 2;
-    // regions of TMEM for a tile's scores (64 columns) and then its weights (32 a part), and how far scores run ahead of sums
+    // regions of TMEM for a tile's scores (64 columns) and then its weights, and how far scores run ahead of sums. Of 32 keys' 32 columns
+    // the first part of their weights takes 16, the second the others; the third stands behind
     static constexpr int REGIONS = F32 ? 2 : 4, REGION = F32 ? 128 : 64, AHEAD = F32 ? 1 : 2;
+    static __device__ __forceinline__ uint32_t part_at(int part, int chunk) { return part < 2 ? chunk * 32 + part * 16 : KVB + chunk * 16; }
+    static constexpr int ROW_PIECES = 32 * (F32 ? 4 : 2) / 16;  // 16-byte pieces of 32 dims of a row of out
+    static __device__ __forceinline__ int stage_at(int row, int pc) { return F32 ? (int)sw128_off(row, pc) : row * 64 + ((pc ^ (row >> 1 & 3)) << 4); }
 };
 // the last two beside the rows that few nodes leave empty
 constexpr int W_SUM = 8, W_REST = 12, W_SCHED = 12, W_SAFE = 13, W_LOAD = 14, W_MMA = 15, WARPS = 16, NT = WARPS * 32;
 // registers of a thread: the launch's 128 are dealt anew
-constexpr int REGS_SOFT = 120, REGS_SUM = 208, REGS_REST = 64;
+constexpr int REGS_SOFT = 112, REGS_SUM = 208, REGS_REST = 80;
 static_assert(2 * REGS_SOFT + REGS_SUM + REGS_REST == 4 * 128, "registers of the launch");
 constexpr int PIECES = 4;       // descriptors in flight
 constexpr int RING = 8;         // tiles whose references and weights are kept
@@ -66,17 +72,18 @@ struct Shared {
     u64 s_full[4], p_full[4];   // of a region: scores there (products, their issuer), weights there (4 warps)
     u64 o_full[2], o_empty[2];  // a tile's sums there (products, their issuer), taken (4)
     u64 m_full[4][2];           // a tile's references of 32 rows there
-    u64 q_full[2], q_empty[2], piece_full[PIECES], piece_empty[PIECES], fin;
-    u64 sums[WARPS];
+    u64 q_full[2], q_empty[2], piece_full[PIECES], seen_full[PIECES], piece_empty[PIECES], fin;
+    uint32_t sums[WARPS];
     uint32_t tmem;
     int abort;
-    int start[2];
+    int start[5];
     int page[16];   // of tile t, at t % 16: its page, -1 where that is out of range (the tree: 0)
     Piece piece[PIECES];
     float m[RING][128], l[RING][128];
 };
 constexpr int SMEM_MAX = 232448;
-// Of dynamic shared memory: the queries of `rows` rows (a multiple of 8), then `slots` pages of K and V, then Shared.
+constexpr int STAGE = 4096;  // of each warp that writes sums
+// Of dynamic shared memory: the queries of `rows` rows (a multiple of 8), then `slots` pages of K and V, the stages, then Shared.
 struct Plan {
     int rows, k_slots, v_slots;
     template <bool F32>
@@ -84,7 +91,9 @@ struct Plan {
     template <bool F32>
     __host__ __device__ int ring() const { return Lay<F32>::QBUFS * q_bytes<F32>(); }
     template <bool F32>
-    __host__ __device__ int shared() const { return ring<F32>() + (k_slots + v_slots) * PAGE_BYTES; }
+    __host__ __device__ int stages() const { return ring<F32>() + (k_slots + v_slots) * PAGE_BYTES; }
+    template <bool F32>
+    __host__ __device__ int shared() const { return stages<F32>() + 4 * STAGE; }
     template <bool F32>
     __host__ __device__ int bytes() const { return shared<F32>() + (int)sizeof(Shared); }
 };
@@ -128,15 +137,37 @@ __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t* r) {
         "r"(r[14]), "r"(r[15])
         : "memory");
 }
-// A warp's wait, at most WAIT_TRIES tries (each takes some 20 cycles at least, and the hardware holds it for a while where it has to
-// wait): false then, and where another warp has given up.
-constexpr uint32_t WAIT_TRIES = 1u << 22;
-__device__ __forceinline__ bool wait_bounded(u64* bar, uint32_t parity, volatile int* stop) {
-    for (uint32_t n = 0; !__all_sync(0xffffffffu, tc_mbar_try((uint64_t*)bar, parity)); ++n) {
-        if (n >= WAIT_TRIES) *stop = 1;
-        if (__any_sync(0xffffffffu, *stop)) return false;
-    }
-    return true;
+// A warp's wait for one to three phases, at most 2^22 rounds of tries (each takes some 20 cycles at least, and the hardware holds a try
+// back for a while where it has to wait): false then, and where another warp has given up.
+#define TREE_TRY(p, bar, par) "mbarrier.try_wait.parity.shared::cta.b64 " p ", [" bar "], " par ";\n"
+#define TREE_RETRY                                                                                                             \
+    "ld.volatile.shared.u32 s, [%1];\nadd.u32 n, n, 1;\nsetp.gt.u32 q, n, 4194304;\n@q st.volatile.shared.u32 [%1], 1;\n" \
+    "setp.eq.u32 q, s, 0;\n@q bra AGAIN;\nTHERE:\nselp.u32 %0, 1, 0, p;\n}"
+__device__ __forceinline__ bool wait_for(int* stop, u64* bar, uint32_t par) {
+    uint32_t ok;
+    asm volatile("{\n.reg .pred p, q;\n.reg .u32 n, s;\nmov.u32 n, 0;\nAGAIN:\n" TREE_TRY("p", "%2", "%3") "@p bra THERE;\n" TREE_RETRY
+                 : "=r"(ok)
+                 : "r"(s_addr(stop)), "r"(s_addr(bar)), "r"(par)
+                 : "memory");
+    return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool wait_for(int* stop, u64* bar, uint32_t par, u64* bar2, uint32_t par2) {
+    uint32_t ok;
+    asm volatile("{\n.reg .pred p, q;\n.reg .u32 n, s;\nmov.u32 n, 0;\nAGAIN:\n" TREE_TRY("p", "%2", "%3") TREE_TRY("q", "%4", "%5")
+                 "and.pred p, p, q;\n@p bra THERE;\n" TREE_RETRY
+                 : "=r"(ok)
+                 : "r"(s_addr(stop)), "r"(s_addr(bar)), "r"(par), "r"(s_addr(bar2)), "r"(par2)
+                 : "memory");
+    return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool wait_for(int* stop, u64* bar, uint32_t par, u64* bar2, uint32_t par2, u64* bar3, uint32_t par3) {
+    uint32_t ok;
+    asm volatile("{\n.reg .pred p, q, r;\n.reg .u32 n, s;\nmov.u32 n, 0;\nAGAIN:\n" TREE_TRY("p", "%2", "%3") TREE_TRY("q", "%4", "%5")
+                 TREE_TRY("r", "%6", "%7") "and.pred p, p, q;\nand.pred p, p, r;\n@p bra THERE;\n" TREE_RETRY
+                 : "=r"(ok)
+                 : "r"(s_addr(stop)), "r"(s_addr(bar)), "r"(par), "r"(s_addr(bar2)), "r"(par2), "r"(s_addr(bar3)), "r"(par3)
+                 : "memory");
+    return __all_sync(0xffffffffu, ok);
 }
 // two floats an instruction
 __device__ __forceinline__ u64 pair(float a, float b) {
@@ -174,54 +205,38 @@ __device__ __forceinline__ bool sequence(const Pages& c, const TreeArgs& a, int 
 }
 __host__ __device__ constexpr int tiles_of(int len) { return (len + KVB - 1) / KVB + 1; }
 
-// A warp finds what each node sees; lanes hold nodes l and l + 32. By doubling: what is seen within 2^k steps, and the node
-// 2^k steps up. False where a parent is out of order (taken as -1 then).
-__device__ __forceinline__ bool ancestors(const int32_t* parents, int n, int lane, u64 (&seen)[2]) {
-    int up[2];
-    bool bad = false;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int j = lane + 32 * h;
-        up[h] = j < n ? parents[j] : -1;
-        if (up[h] < -1 || up[h] >= j) {
-            bad = true;
-            up[h] = -1;
-        }
-        seen[h] = 1ull << j;
+// A warp finds what each node sees, in shared memory. By doubling: what is seen within 2^k steps, and the node 2^k steps up. False
+// where a parent is out of order (taken as -1 then).
+__device__ __forceinline__ bool ancestors(const int32_t* parents, int n, int lane, u64* seen, int* up) {
+    bool bad = false, more = false;
+#pragma unroll 1
+    for (int j = lane; j < MAX_NODES; j += 32) {
+        int u = j < n ? parents[j] : -1;
+        const bool wrong = u < -1 || u >= j;
+        bad |= wrong;
+        if (wrong) u = -1;
+        more |= u >= 0;
+        up[j] = u;
+        seen[j] = 1ull << j;
     }
-    while (__any_sync(0xffffffffu, up[0] >= 0 || up[1] >= 0)) {
-        int next[2];
-        u64 more[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int at = up[h] & 31;
-            const u64 m0 = __shfl_sync(0xffffffffu, seen[0], at), m1 = __shfl_sync(0xffffffffu, seen[1], at);
-            const int u0 = __shfl_sync(0xffffffffu, up[0], at), u1 = __shfl_sync(0xffffffffu, up[1], at);
-            more[h] = up[h] < 0 ? 0 : up[h] < 32 ? m0 : m1;
-            next[h] = up[h] < 0 ? -1 : up[h] < 32 ? u0 : u1;
+    while (__any_sync(0xffffffffu, more)) {
+        more = false;
+#pragma unroll 1
+        for (int j = lane; j < MAX_NODES; j += 32) {
+            __syncwarp();
+            const int u = up[j], v = u < 0 ? -1 : up[u];
+            const u64 m = u < 0 ? 0ull : seen[u];
+            __syncwarp();
+            seen[j] |= m;
+            up[j] = v;
+            more |= v >= 0;
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            seen[h] |= more[h];
-            up[h] = next[h];
-        }
+        __syncwarp();
     }
     return !__any_sync(0xffffffffu, bad);
 }
 
 __device__ __forceinline__ bool finite16(uint32_t half) { return (half & 0x7F80u) != 0x7F80u; }
-
-// a row's 128 numbers to out
-__device__ __forceinline__ void store_row(float* to, const float* x, float f) {
-#pragma unroll
-    for (int d = 0; d < HD; d += 4) *reinterpret_cast<float4*>(to + d) = make_float4(x[d] * f, x[d + 1] * f, x[d + 2] * f, x[d + 3] * f);
-}
-__device__ __forceinline__ void store_row(bf16* to, const float* x, float f) {
-#pragma unroll
-    for (int d = 0; d < HD; d += 8)
-        *reinterpret_cast<uint4*>(to + d) = make_uint4(bf16_pair(x[d] * f, x[d + 1] * f), bf16_pair(x[d + 2] * f, x[d + 3] * f),
-                                                       bf16_pair(x[d + 4] * f, x[d + 5] * f), bf16_pair(x[d + 6] * f, x[d + 7] * f));
-}
 
 // grid: the shares, 512 threads. All tiles of all (sequence, KV head) are one line, cut into equal shares. Of warps 12 .. 15 one
 // deals the pieces of its share, one loads pages (and bf16 queries) by TMA, one makes values safe to be multiplied by 0, and one
@@ -247,16 +262,12 @@ __global__ void __launch_bounds__(NT, 1)
     unsigned char* const v_ring = k_ring + plan.k_slots * PAGE_BYTES;
     Shared& sh = *reinterpret_cast<Shared*>(smem + plan.shared<F32>());
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, me = blockIdx.x;
-    volatile int* const stop = &sh.abort;
-    if (tid == 0) {
-        const auto init = [](u64* b, int n, int of) {
-            for (int i = 0; i < of; ++i) tc_mbar_init((uint64_t*)b + i, n);
+    if (warp == 0) {
+        const auto init = [&](u64* b, int n, int of) {
+            if (lane < of) tc_mbar_init((uint64_t*)b + lane, n);
         };
-        init(sh.k_full, 1, MAX_SLOTS);
-        init(sh.k_empty, 1, MAX_SLOTS);
-        init(sh.v_full, 1, MAX_SLOTS);
-        init(sh.v_ready, 1, MAX_SLOTS);
-        init(sh.v_empty, 1, MAX_SLOTS);
+        init(sh.k_full, 1, 3 * MAX_SLOTS);  // and k_empty, v_full
+        init(sh.v_ready, 1, 2 * MAX_SLOTS);  // and v_empty
         init(sh.s_full, 2, 4);
         init(sh.p_full, 4, 4);
         init(sh.o_full, 2, 2);
@@ -265,6 +276,7 @@ __global__ void __launch_bounds__(NT, 1)
         init(sh.q_full, F32 ? 8 : 1, 2);
         init(sh.q_empty, 1, 2);
         init(sh.piece_full, 1, PIECES);
+        init(sh.seen_full, 1, PIECES);
         init(sh.piece_empty, 3 + 8 + 4, PIECES);
         init(&sh.fin, 1, 1);
         sh.abort = 0;
@@ -278,56 +290,56 @@ __global__ void __launch_bounds__(NT, 1)
     pdl_wait();  // upstream results are read below
     pdl_trigger();
     // where the share begins: the sequences' tiles, one a thread at a time; the sum of all first, where one turn is not enough
-    long long total = 0, before = 0, first = 0, units = 0, share = 0;
-    const auto count = [&](int b, bool report) {
-        int row, len, n;
-        return b < a.B && sequence(c, a, b, report, row, len, n) ? tiles_of(len) : 0;
-    };
-    const auto deal = [&](long long tiles) {
+    uint32_t before = 0, first = 0, units = 0, share = 0;
+    const bool one_turn = a.B <= NT;
+    const auto deal = [&](uint32_t tiles) {
         units = tiles * NKV;
         share = (units + gridDim.x - 1) / gridDim.x;
         first = me * share;
     };
-    const bool one_turn = a.B <= NT;
-    if (!one_turn) {
-        for (int i = tid; i < a.B; i += NT) total += count(i, me == 0);
+#pragma unroll 1
+    for (int turn = one_turn; turn < 2; ++turn) {
+        before = 0;
+#pragma unroll 1
+        for (int i0 = 0; i0 < a.B && (turn == 0 || before * NKV <= first); i0 += NT) {
+            const int i = i0 + tid;
+            int row = 0, len = 0, nodes = 0;
+            const uint32_t n = i < a.B && sequence(c, a, i, turn == one_turn && me == 0, row, len, nodes) ? tiles_of(len) : 0;
+            uint32_t incl = n;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        if (lane == 0) sh.sums[warp] = total;
-        __syncthreads();
-        total = 0;
-        for (int w = 0; w < WARPS; ++w) total += sh.sums[w];
-        deal(total);
-    }
-    for (int i = tid; i - tid < a.B && before * NKV <= first; i += NT) {
-        const int n = count(i, one_turn && me == 0);
-        int incl = n;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t w = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += w;
+            }
+            __syncthreads();
+            if (lane == 31) sh.sums[warp] = incl;
+            __syncthreads();
+            uint32_t of = lane < WARPS ? sh.sums[lane] : 0, upto = of;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int w = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += w;
+            for (int o = 1; o < WARPS; o <<= 1) {
+                const uint32_t w = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += w;
+            }
+            const uint32_t mine = before + __shfl_sync(0xffffffffu, upto - of, warp) + incl - n;
+            before += __shfl_sync(0xffffffffu, upto, WARPS - 1);
+            if (one_turn) deal(before);
+            if (turn && first >= mine * NKV && first < (mine + n) * NKV) {
+                sh.start[0] = i;
+                sh.start[1] = (int)(first - mine * NKV);
+                sh.start[2] = row;
+                sh.start[3] = len;
+                sh.start[4] = nodes;
+            }
         }
-        __syncthreads();
-        if (lane == 31) sh.sums[warp] = incl;
-        __syncthreads();
-        long long mine = before + incl - n;
-        for (int w = 0; w < WARPS; ++w) {
-            if (w < warp) mine += sh.sums[w];
-            before += sh.sums[w];
-        }
-        if (one_turn) deal(before);
-        if (first >= mine * NKV && first < (mine + n) * NKV) {
-            sh.start[0] = i;
-            sh.start[1] = (int)(first - mine * NKV);
-        }
+        if (turn == 0) deal(before);
     }
     __syncthreads();
     tc_after();
     const uint32_t tmem = sh.tmem;
-    const uint32_t U = first < units ? (uint32_t)min(share, units - first) : 0;  // this block's tiles
+    const uint32_t U = first < units ? min(share, units - first) : 0;  // this block's tiles
     bool ok = true;
     const auto wait = [&](u64* bar, uint32_t parity) {  // by whole warps
-        ok = wait_bounded(bar, parity, stop);
+        ok = wait_for(&sh.abort, bar, parity);
         return ok;
     };
     // piece k, once it is there
@@ -337,36 +349,18 @@ __global__ void __launch_bounds__(NT, 1)
     if (warp >= W_REST) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
         if (warp == W_SCHED) {
-            int b = sh.start[0], at = sh.start[1], known = -1;
-            long long left = U;
-            u64 seen[2] = {0, 0};
-            bool tree_ok = true, head = true;
-            int row = 0, len = 0, n = 0;
-            if (left > 0) sequence(c, a, b, false, row, len, n);
-            else if (lane == 0) a.meta[me] = make_int4(-1, 0, 0, 0);
-            for (int k = 0;; ++k) {
+            int b = sh.start[0], at = sh.start[1], row = sh.start[2], len = sh.start[3], n = sh.start[4];
+            uint32_t left = U;
+            bool head = true;
+            if (left == 0 && lane == 0) a.meta[me] = make_int4(-1, 0, 0, 0);
+#pragma unroll 1
+            for (uint32_t k = 0;; ++k) {
                 const int slot = k % PIECES;
-                if (k >= PIECES && !wait(&sh.piece_empty[slot], (uint32_t)(k / PIECES - 1) & 1u)) break;
+                if (k >= PIECES && !wait(&sh.piece_empty[slot], (k / PIECES - 1) & 1u)) break;
                 Piece& p = sh.piece[slot];
-                if (left <= 0) {
-                    if (lane == 0) {
-                        p.b = -1;
-                        arrive(&sh.piece_full[slot]);
-                    }
-                    break;
-                }
-                const int nt = tiles_of(len), g = at / nt, t0 = at - g * nt, t1 = (int)min((long long)nt, t0 + left);
-                if (t1 == nt) {
-                    if (known != b) {
-                        tree_ok = ancestors(a.parents + (size_t)b * a.N, n, lane, seen);
-                        known = b;
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) p.seen[lane + 32 * h] = seen[h];
-                    if (!tree_ok && lane == 0) set_err(c.err, TTS_BB_TREE_ERR_TREE);
-                }
+                const int nt = tiles_of(len), g = at / nt, t0 = at - g * nt, t1 = (int)min((uint32_t)nt, t0 + left);
                 if (lane == 0) {
-                    p.b = b;
+                    p.b = left ? b : -1;
                     p.g = g;
                     p.row = row;
                     p.len = len;
@@ -374,15 +368,23 @@ __global__ void __launch_bounds__(NT, 1)
                     p.t0 = t0;
                     p.t1 = t1;
                     p.tiles = nt;
-                    p.ok = t1 < nt || tree_ok;
                     p.whole = t0 == 0 && t1 == nt;
                     p.first = head;
                     p.bad[0] = p.bad[1] = 0;
-                    // of the share's first piece: its (sequence, head), nodes, and whether it begins inside of that one; bit 2: in order
-                    if (head) a.meta[me] = make_int4(b * NKV + g, n, (t0 > 0) | p.ok << 2, 0);
+                    arrive(&sh.piece_full[slot]);
                 }
-                __syncwarp();
-                if (lane == 0) arrive(&sh.piece_full[slot]);
+                if (left == 0) break;
+                bool tree_ok = true;
+                if (t1 == nt) {
+                    tree_ok = ancestors(a.parents + (size_t)b * a.N, n, lane, p.seen, p.up);
+                    if (!tree_ok && lane == 0) set_err(c.err, TTS_BB_TREE_ERR_TREE);
+                }
+                if (lane == 0) {
+                    p.ok = tree_ok;
+                    arrive(&sh.seen_full[slot]);
+                    // of the share's first piece: its (sequence, head), nodes, and whether it begins inside of that one; bit 2: in order
+                    if (head) a.meta[me] = make_int4(b * NKV + g, n, (t0 > 0) | tree_ok << 2, 0);
+                }
                 head = false;
                 left -= t1 - t0;
                 at += t1 - t0;
@@ -411,6 +413,7 @@ __global__ void __launch_bounds__(NT, 1)
                 tma_load_2d(to + PAGE_BYTES / 2, map, x + 64, y, (uint64_t*)bar);
             };
             int k_landing = 0, v_landing = 0;
+#pragma unroll 1
             for (uint32_t i = 0; ok && i < U + L::AHEAD; ++i) {
                 if (i < U) {
                     if (!kq || kt == kq->t1) {
@@ -470,10 +473,12 @@ __global__ void __launch_bounds__(NT, 1)
                     }
                 }
             }
-            if (*stop && lane == 0) {  // copies in flight land before the block ends
+            if (*(volatile int*)&sh.abort && lane == 0) {  // copies in flight land before the block ends
                 const auto landed = [&](u64* full, int n, int slots) {
+#pragma unroll 1
                     for (int j = max(0, n - slots); j < n; ++j) {
                         const unsigned long long t0 = g_time();
+#pragma unroll 1
                         while (!tc_mbar_try((uint64_t*)&full[j % slots], (uint32_t)(j / slots) & 1u) && g_time() - t0 < TC_TIMEOUT_NS) {
                         }
                     }
@@ -490,6 +495,7 @@ __global__ void __launch_bounds__(NT, 1)
             const bool leader = elect();
             uint32_t ks = 0, vs = 0, kp = 0, vp = 0, sk = ~0u, pk = ~0u;  // slots, their parities, pieces of the scores and of the sums
             int s_left = 0, p_left = 0, pt = 0, p_tiles = 0, p_len = 0, p_n = 0;
+#pragma unroll 1
             for (uint32_t i = 0; i < U + L::AHEAD; ++i) {
                 if (i < U) {
                     if (s_left == 0) {
@@ -498,10 +504,10 @@ __global__ void __launch_bounds__(NT, 1)
                         s_left = sh.piece[sk % PIECES].t1 - sh.piece[sk % PIECES].t0;
                         if (!wait(&sh.q_full[F32 ? 0 : sk & 1], (F32 ? sk : sk >> 1) & 1u)) break;
                     }
-                    if (!wait(&sh.k_full[ks], kp)) break;
-                    // the weights in the region were taken by the product of tile i - REGIONS
+                    // the keys; and the weights in the region were taken by the product of tile i - REGIONS (none: the phase before the first)
                     const uint32_t region = i % L::REGIONS, j = i - L::REGIONS;
-                    if (i >= L::REGIONS && !wait(&sh.o_full[j & 1], (j >> 1) & 1u)) break;
+                    ok = wait_for(&sh.abort, &sh.k_full[ks], kp, &sh.o_full[j & 1], i < L::REGIONS ? 1u : (j >> 1) & 1u);
+                    if (!ok) break;
                     tc_after();
                     const uint32_t d = tmem + region * L::REGION, k1 = k0 + ks * (PAGE_BYTES >> 4), q1 = q0 + (F32 ? 0u : (sk & 1) * q_buf);
                     --s_left;
@@ -534,9 +540,8 @@ __global__ void __launch_bounds__(NT, 1)
                     }
                     // 16 keys a step, of those that there are
                     const int keys = pt == p_tiles - 1 ? p_n : min(KVB, p_len - pt * KVB), steps = (keys + 15) / 16;
-                    if (!wait(&sh.p_full[region], (u / L::REGIONS) & 1u)) break;
-                    if (!wait(&sh.v_ready[vs], vp)) break;
-                    if (u >= 2 && !wait(&sh.o_empty[u & 1], ((u >> 1) - 1) & 1u)) break;
+                    ok = wait_for(&sh.abort, &sh.p_full[region], (u / L::REGIONS) & 1u, &sh.v_ready[vs], vp, &sh.o_empty[u & 1], ((u >> 1) - 1) & 1u);
+                    if (!ok) break;
                     tc_after();
                     const uint32_t w = tmem + region * L::REGION, d = tmem + 256 + (u & 1) * 128, v1 = v0 + vs * (PAGE_BYTES >> 4);
                     ++pt;
@@ -546,7 +551,7 @@ __global__ void __launch_bounds__(NT, 1)
                         for (int part = L::PPARTS - 1; part >= 0; --part)
 #pragma unroll
                             for (int kk = 0; kk < KVB / 16; ++kk)  // 8 columns of weights
-                                if (kk < steps) mma_ts(d, w + (uint32_t)(part * (KVB / 2) + kk * 8), v1 + (uint32_t)(kk * 2048 / 16), IDESC_PV, part < L::PPARTS - 1 || kk > 0);
+                                if (kk < steps) mma_ts(d, w + L::part_at(part, kk >> 1) + (kk & 1) * 8, v1 + (uint32_t)(kk * 2048 / 16), IDESC_PV, part < L::PPARTS - 1 || kk > 0);
                         arrive(&sh.o_full[u & 1]);
                         at_commit((uint64_t*)&sh.o_full[u & 1]);
                         at_commit((uint64_t*)&sh.v_empty[vs]);
@@ -556,10 +561,11 @@ __global__ void __launch_bounds__(NT, 1)
                     if (++vs == (uint32_t)plan.v_slots) vs = 0, vp ^= 1;
                 }
             }
-            if (!ok && lane == 0) *stop = 1;
+            if (!ok && lane == 0) *(volatile int*)&sh.abort = 1;
             if (leader) {
                 at_commit((uint64_t*)&sh.fin);  // every product has ended
                 const unsigned long long t0 = g_time();
+#pragma unroll 1
                 while (!tc_mbar_try((uint64_t*)&sh.fin, 0) && g_time() - t0 < TC_TIMEOUT_NS) {
                 }
             }
@@ -570,6 +576,7 @@ __global__ void __launch_bounds__(NT, 1)
             int t = 0, vs = 0;
             uint32_t vp = 0, k = ~0u;
             Piece* p = nullptr;
+#pragma unroll 1
             for (uint32_t u = 0; ok && u < U; ++u) {
                 if (!p) {
                     ++k;
@@ -586,8 +593,10 @@ __global__ void __launch_bounds__(NT, 1)
                         return reinterpret_cast<uint4*>(v1 + (pc >> 3) * (PAGE_BYTES / 2) + sw128_off(key, pc & 7));
                     };
                     // 2 keys an instruction
+#pragma unroll 1
                     for (int key = valid + (lane >> 4); key < (keys + 15) / 16 * 16; key += 2) *at(key, lane & 15) = make_uint4(0u, 0u, 0u, 0u);
                     if (tree) {
+#pragma unroll 1
                         for (int key0 = lane >> 4; key0 < valid; key0 += 8) {
                             uint4 x[4];
 #pragma unroll
@@ -627,6 +636,7 @@ __global__ void __launch_bounds__(NT, 1)
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const float cs = 0.08838834764831845f * 1.4426950408889634f;
         uint32_t u0 = 0;
+#pragma unroll 1
         for (uint32_t k = 0; ok; ++k) {
             if (!wait(piece_bar(k), piece_par(k))) break;
             const Piece& p = sh.piece[k % PIECES];
@@ -637,7 +647,7 @@ __global__ void __launch_bounds__(NT, 1)
                 if (u0 > 0 && !wait(&sh.s_full[(u0 - 1) % L::REGIONS], ((u0 - 1) / L::REGIONS) & 1u)) break;
                 if (warp * 16 < rows) {
                     const float* const q = static_cast<const float*>(a.q) + (size_t)p.b * a.N * a.q_stride + 2 * p.g * HD;
-#pragma unroll
+#pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
                         float4 x[4][2];
 #pragma unroll
@@ -676,30 +686,41 @@ __global__ void __launch_bounds__(NT, 1)
             }
             const bool mine = quarter * 32 < rows;
             float mc = -INFINITY, l = 0.f;  // of this warp's tiles: the reference, and the sum of weights
+#pragma unroll 1
             for (uint32_t u = u0 + ((u0 ^ group) & 1); u < u0 + nt; u += 2) {
                 const int t = p.t0 + (int)(u - u0);
                 const uint32_t at = lanes + (u % L::REGIONS) * L::REGION;
                 if (!wait(&sh.s_full[u % L::REGIONS], (u / L::REGIONS) & 1u)) break;
-                uint32_t s[KVB];
                 float m = -INFINITY;
+                // the keys that count, a bit each, where not all do
+                const bool tree = t == p.tiles - 1;
+                const int valid = p.len - t * KVB;
+                const bool there = sh.page[u % 16] >= 0, special = tree || valid < KVB || !there;
+                u64 keys = ~0ull;
+                if (special) {
+                    if (tree && !wait(&sh.seen_full[k % PIECES], piece_par(k))) break;
+                    keys = !there ? 0ull : tree ? (r < rows ? p.seen[r >> 1] : 0ull) : (1ull << valid) - 1;
+                }
+                const auto scores = [&](int chunk, uint32_t (&s)[32]) {
+                    tm_ld32_nw(at + chunk * 32, s);
+                    tm_wait_ld();
+                    if (special) {
+                        const uint32_t count = (uint32_t)(keys >> (chunk * 32));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(count >> i & 1)) s[i] = 0xFF800000u;  // -inf
+                    }
+                };
                 if (mine) {
                     tc_after();
-#pragma unroll
-                    for (int i = 0; i < KVB; i += 32) tm_ld32_nw(at + i, s + i);
-                    tm_wait_ld();
-                    // the keys that count, a bit each
-                    const bool tree = t == p.tiles - 1;
-                    const int valid = p.len - t * KVB;
-                    const bool there = sh.page[u % 16] >= 0;
-                    if (tree || valid < KVB || !there) {
-                        const u64 keys = !there ? 0ull : tree ? (r < rows ? p.seen[r >> 1] : 0ull) : (1ull << valid) - 1;
-#pragma unroll
-                        for (int i = 0; i < KVB; ++i)
-                            if (!((uint32_t)(keys >> (i & 32)) >> (i & 31) & 1)) s[i] = 0xFF800000u;  // -inf
-                    }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int chunk = 0; chunk < 2; ++chunk) {
+                        uint32_t s[32];
+                        scores(chunk, s);
 #pragma unroll
-                    for (int i = 0; i < KVB; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+                        for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+                    }
                     m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 }
                 // the maximum so far, from the warp of the tile before (waited for at a new piece too: no warp is two tiles ahead)
@@ -714,13 +735,14 @@ __global__ void __launch_bounds__(NT, 1)
                     const float now = m * cs, base = m == -INFINITY ? 0.f : now;
                     const u64 cs2 = pair(cs, cs), base2 = pair(-base, -base), minus = pair(-1.f, -1.f);
                     u64 sum[2] = {0, 0};
-#pragma unroll
-                    for (int i0 = 0; i0 < KVB; i0 += 32) {
-                        uint32_t w[L::PPARTS][16];
+#pragma unroll 1
+                    for (int chunk = 0; chunk < 2; ++chunk) {
+                        uint32_t s[32], w[L::PPARTS][16];
+                        scores(chunk, s);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float x, y;
-                            halves(fma2(pair(__uint_as_float(s[i0 + 2 * i]), __uint_as_float(s[i0 + 2 * i + 1])), cs2, base2), x, y);
+                            halves(fma2(pair(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cs2, base2), x, y);
                             u64 e = pair(at_ex2(x), at_ex2(y));
                             sum[i & 1] = add2(sum[i & 1], e);
 #pragma unroll
@@ -732,7 +754,7 @@ __global__ void __launch_bounds__(NT, 1)
                             }
                         }
 #pragma unroll
-                        for (int part = 0; part < L::PPARTS; ++part) tm_st16(at + (uint32_t)(part * (KVB / 2) + i0 / 2), w[part]);
+                        for (int part = 0; part < L::PPARTS; ++part) tm_st16(at + L::part_at(part, chunk), w[part]);
                     }
                     float x, y, z, v;
                     halves(sum[0], x, y);
@@ -758,6 +780,7 @@ __global__ void __launch_bounds__(NT, 1)
         const uint32_t lanes = tmem + 256 + ((uint32_t)(quarter * 32) << 16);
         const float cs = 0.08838834764831845f * 1.4426950408889634f;
         uint32_t u = 0;
+#pragma unroll 1
         for (uint32_t k = 0; ok; ++k) {
             if (!wait(piece_bar(k), piece_par(k))) break;
             const Piece& p = sh.piece[k % PIECES];
@@ -768,6 +791,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
             for (int i = 0; i < HD / 2; ++i) o[i] = 0;
             float m = -INFINITY, l = 0.f;  // the reference, times cs
+#pragma unroll 1
             for (int t = 0; t < nt; ++t, ++u) {
                 if (!wait(&sh.o_full[u & 1], (u >> 1) & 1u)) break;
                 if (mine) {
@@ -788,33 +812,88 @@ __global__ void __launch_bounds__(NT, 1)
                     if (t + 2 >= nt) l = (t == 0 || l == 0.f ? 0.f : l * f) + sh.l[u % RING][r];  // of even and of odd tiles
                     m = now;
                 }
+                if (t + 1 == nt) {
+                    // The piece's end. The sums go back into the tile's columns of TMEM and are taken from there 32 dims at a time: a short loop,
+                    // where 128 registers would be written by code that the instruction cache never holds
+                    if (p.t1 == p.tiles && !wait(&sh.seen_full[k % PIECES], piece_par(k))) break;
+                    const bool bad = p.bad[0] | p.bad[1], write = p.whole ? p.ok : true;
+                    T* const to = static_cast<T*>(a.out) + ((size_t)p.b * a.N * NQ + 2 * p.g) * HD;
+                    float4* const part = a.part + ((size_t)me * 2 + !p.first) * PART * 128 + r;
+                    if (mine) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t x[32];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                float y, z;
+                                halves(o[16 * i + j], y, z);
+                                x[2 * j] = __float_as_uint(y);
+                                x[2 * j + 1] = __float_as_uint(z);
+                            }
+                            tm_st32(lanes + (u & 1) * 128 + 32 * i, x);
+                        }
+                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                        const float f = !p.whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                        unsigned char* const stage = smem + plan.stages<F32>() + quarter * STAGE;
+#pragma unroll 1
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t x[32];
+                            tm_ld32_nw(lanes + (u & 1) * 128 + 32 * i, x);
+                            tm_wait_ld();
+                            float y[32];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(x[j]) * f;
+                            if (!p.whole) {
+                                if (r < rows) {  // rows side by side: whole lines
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) part[(8 * i + j) * 128] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                                }
+                            } else if (write) {
+                                // through the warp's stage: whole lines again
+#pragma unroll
+                                for (int j = 0; j < L::ROW_PIECES; ++j) {
+                                    uint4 w;
+                                    if constexpr (F32)
+                                        w = make_uint4(__float_as_uint(y[4 * j]), __float_as_uint(y[4 * j + 1]), __float_as_uint(y[4 * j + 2]), __float_as_uint(y[4 * j + 3]));
+                                    else
+                                        w = make_uint4(bf16_pair(y[8 * j], y[8 * j + 1]), bf16_pair(y[8 * j + 2], y[8 * j + 3]), bf16_pair(y[8 * j + 4], y[8 * j + 5]),
+                                                       bf16_pair(y[8 * j + 6], y[8 * j + 7]));
+                                    *reinterpret_cast<uint4*>(stage + L::stage_at(lane, j)) = w;
+                                }
+                                __syncwarp();
+#pragma unroll
+                                for (int e = lane; e < 32 * L::ROW_PIECES; e += 32) {
+                                    const int in = e / L::ROW_PIECES, pc = e % L::ROW_PIECES, at = quarter * 32 + in;
+                                    if (at < rows)
+                                        *reinterpret_cast<uint4*>(to + ((size_t)(at >> 1) * NQ + (at & 1)) * HD + i * 32 + pc * (16 / (int)sizeof(T))) =
+                                            *reinterpret_cast<const uint4*>(stage + L::stage_at(in, pc));
+                                }
+                                __syncwarp();
+                            }
+                        }
+                        if (!p.whole && r < rows) part[(HD / 4) * 128] = make_float4(m, l, 0.f, 0.f);
+                        if (bad) {  // what was set aside is added to what stands there now
+                            __syncwarp();
+#pragma unroll 1
+                            for (u64 left = r < rows ? ((u64)p.bad[1] << 32 | p.bad[0]) & p.seen[r >> 1] : 0ull; left; left &= left - 1) {
+                                const bf16* const v = a.v + ((size_t)p.b * a.N + __ffsll(left) - 1) * a.kv_stride + p.g * HD;
+#pragma unroll 1
+                                for (int d = 0; d < HD; ++d) {
+                                    const float y = bf2f(v[d]);
+                                    T* const at = to + ((size_t)(r >> 1) * NQ + (r & 1)) * HD + d;
+                                    if (fabsf(y) <= 3.4028235e38f) continue;
+                                    if (!p.whole) reinterpret_cast<float*>(part + (d >> 2) * 128)[d & 3] += y;
+                                    else if (write) *at = (T)((float)*at + y);
+                                }
+                            }
+                        }
+                    }
+                }
                 tc_before();
                 __syncwarp();
                 if (lane == 0) arrive(&sh.o_empty[u & 1]);
             }
             if (!ok) break;
-            if (r < rows) {
-                float x[HD];
-#pragma unroll
-                for (int i = 0; i < HD / 2; ++i) halves(o[i], x[2 * i], x[2 * i + 1]);
-                const u64 bad = p.bad[0] | p.bad[1] ? ((u64)p.bad[1] << 32 | p.bad[0]) & p.seen[r >> 1] : 0ull;
-                for (u64 left = bad; left; left &= left - 1) {  // what was set aside
-                    const bf16* const v = a.v + ((size_t)p.b * a.N + __ffsll(left) - 1) * a.kv_stride + p.g * HD;
-#pragma unroll
-                    for (int d = 0; d < HD; ++d) {
-                        const uint32_t half = *reinterpret_cast<const uint16_t*>(v + d);
-                        if (!finite16(half)) x[d] += __uint_as_float(half << 16);
-                    }
-                }
-                if (p.whole) {
-                    if (p.ok) store_row(static_cast<T*>(a.out) + (((size_t)p.b * a.N + (r >> 1)) * NQ + 2 * p.g + (r & 1)) * HD, x, l == 0.f ? 0.f : 1.f / l);
-                } else {
-                    float* const to = a.part + (((size_t)me * 2 + !p.first) * 2 * a.N + r) * PART;
-                    store_row(to, x, 1.f);
-                    to[HD] = m;
-                    to[HD + 1] = l;
-                }
-            }
             __syncwarp();
             if (lane == 0) arrive(&sh.piece_empty[k % PIECES]);
         }
@@ -828,13 +907,13 @@ __global__ void __launch_bounds__(NT, 1)
     }
 }
 
-// grid (shares - 1, rows / 4), 128 threads: the pieces of the (sequence, KV head) that the end of share blockIdx.x cuts first. A warp a
-// row, a lane 4 of the 128 dims. A share's first piece stands in its place 0, the piece that ends it in place 1.
+// grid (shares - 1, rows / 32, 4), 128 threads: the pieces of the (sequence, KV head) that the end of share blockIdx.x cuts first. A lane
+// a row, a warp 8 of the 128 dims. A share's first piece stands in its place 0, the piece that ends it in place 1.
 template <typename T>
 __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
     pdl_wait();
     pdl_trigger();
-    const int s0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y * 4 + warp;
+    const int s0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y * 32 + lane;
     // the first pieces of this share and of those behind it: at most 20 shares hold parts of one of 8 or more (sequence, head)
     const int4 meta = s0 + lane < shares ? a.meta[s0 + lane] : make_int4(-1, 0, 0, 0);
     const int it = __shfl_sync(0xffffffffu, meta.x, 1);
@@ -846,24 +925,34 @@ __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
     const int n = __shfl_sync(0xffffffffu, meta.y, 1);
     const bool in_order = __shfl_sync(0xffffffffu, meta.z, more) >> 2 & 1;  // the last piece holds the tree
     if (r >= 2 * n || !in_order) return;
-    const auto at = [&](int i) { return a.part + (((size_t)(s0 + i) * 2 + (i == 0 && head != it)) * 2 * a.N + r) * PART; };
-    float M = lane <= more ? at(lane)[HD] : -INFINITY;
-    M = warp_max(M);
+    const auto at = [&](int i) { return a.part + ((size_t)(s0 + i) * 2 + (i == 0 && head != it)) * PART * 128 + r; };
+    float M = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (int i = 0; i <= more; ++i) M = fmaxf(M, at(i)[(HD / 4) * 128].x);
     const float base = M == -INFINITY ? 0.f : M;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 o[2] = {};
+    const int d0 = (blockIdx.z * 4 + warp) * 2;
 #pragma unroll 4
     for (int i = 0; i <= more; ++i) {
-        const float* const p = at(i);
-        const float f = at_ex2(p[HD] - base);
-        const float4 x = *reinterpret_cast<const float4*>(p + lane * 4);
-        l += f * p[HD + 1];
-        o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
+        const float4* const p = at(i);
+        const float4 w = p[(HD / 4) * 128];
+        const float f = at_ex2(w.x - base);
+        l += f * w.y;
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+            const float4 x = p[(d0 + d) * 128];
+            o[d].x += f * x.x; o[d].y += f * x.y; o[d].z += f * x.z; o[d].w += f * x.w;
+        }
     }
     const float f = l == 0.f ? 0.f : 1.f / l;
-    T* const to = static_cast<T*>(a.out) + (((size_t)(it / NKV) * a.N + (r >> 1)) * NQ + 2 * (it % NKV) + (r & 1)) * HD + lane * 4;
-    if constexpr (std::is_same_v<T, float>) *reinterpret_cast<float4*>(to) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-    else *reinterpret_cast<uint2*>(to) = make_uint2(bf16_pair(o.x * f, o.y * f), bf16_pair(o.z * f, o.w * f));
+    T* const to = static_cast<T*>(a.out) + (((size_t)(it / NKV) * a.N + (r >> 1)) * NQ + 2 * (it % NKV) + (r & 1)) * HD + d0 * 4;
+    if constexpr (std::is_same_v<T, float>) {
+#pragma unroll
+        for (int d = 0; d < 2; ++d) *reinterpret_cast<float4*>(to + d * 4) = make_float4(o[d].x * f, o[d].y * f, o[d].z * f, o[d].w * f);
+    } else {
+        *reinterpret_cast<uint4*>(to) = make_uint4(bf16_pair(o[0].x * f, o[0].y * f), bf16_pair(o[0].z * f, o[0].w * f), bf16_pair(o[1].x * f, o[1].y * f),
+                                                   bf16_pair(o[1].z * f, o[1].w * f));
+    }
 }
 
 // Blocks of the launch: one an SM, or one a tile where there are fewer.
@@ -882,8 +971,8 @@ Plan plan_of(int N) {
 }  // namespace
 
 TTS_API size_t tts_bb_tree_attention_workspace(int B, int N, int max_len) {
-    if (!tree_ok(B, N) || max_len < 0 || max_len > (1 << 30) || (long long)B * max_len > (1ll << 40)) return 0;
-    return META_BYTES + (size_t)share_count(B, max_len) * 2 * 2 * N * PART * sizeof(float);
+    if (!tree_ok(B, N) || max_len < 0 || max_len > (1 << 30) || (long long)B * max_len > (1ll << 33)) return 0;
+    return META_BYTES + (size_t)share_count(B, max_len) * 2 * PART * 128 * sizeof(float4);
 }
 
 TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int layer, int B, int N, const void* q, int type,
@@ -894,7 +983,7 @@ TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int la
     if (!cache_ok(cache) || layer < 0 || layer >= cache->n_layers || !tree_ok(B, N) || !q || !k || !v || !parents || !kv_lens || !out ||
         (type != TTS_BB_T_F32 && type != TTS_BB_T_BF16) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) ||
         q_stride < NQ * HD || q_stride % (type == TTS_BB_T_F32 ? 4 : 8) || kv_stride < NKV * HD || kv_stride % 8 ||
-        q_stride > (1ll << 38) || kv_stride > (1ll << 38) || max_len < 0 || max_len > (1 << 30) || (long long)B * max_len > (1ll << 40) ||
+        q_stride > (1ll << 38) || kv_stride > (1ll << 38) || max_len < 0 || max_len > (1 << 30) || (long long)B * max_len > (1ll << 33) ||
         (long long)max_len > (long long)cache->blocks_per_seq * KVB || (!seqs && B > cache->n_seqs) || !words_aligned(parents, n_nodes, seqs, kv_lens))
         return TTS_BB_E_INVALID;
     if (!workspace || workspace_bytes < tts_bb_tree_attention_workspace(B, N, max_len) || !aligned16(workspace)) return TTS_BB_E_INVALID;
@@ -907,7 +996,7 @@ TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int la
         return TTS_BB_E_CUDA;
     if (type != TTS_BB_T_BF16) q_map = k_map;  // not used
     const TreeArgs a{q, static_cast<const bf16*>(v), q_stride, kv_stride, parents, n_nodes, seqs, kv_lens, B, N, max_len, out,
-                     static_cast<int4*>(workspace), reinterpret_cast<float*>(static_cast<char*>(workspace) + META_BYTES)};
+                     static_cast<int4*>(workspace), reinterpret_cast<float4*>(static_cast<char*>(workspace) + META_BYTES)};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int shares = share_count(B, max_len);
     bool regs = true;
@@ -925,7 +1014,7 @@ TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int la
         const Plan plan = plan_of<F32>(N);
         launch_pdl(k_tree_attn<F32>, shares, NT, plan.bytes<F32>(), st, pool_map, k_map, v_map, q_map, c, a, plan);
         if (tiles_of(max_len) > 1)
-            launch_pdl(k_tree_combine<std::conditional_t<F32, float, bf16>>, dim3(shares - 1, (2 * N + 3) / 4), 128, 0, st, a, shares);
+            launch_pdl(k_tree_combine<std::conditional_t<F32, float, bf16>>, dim3(shares - 1, (2 * N + 31) / 32, 4), 128, 0, st, a, shares);
     };
     if (type == TTS_BB_T_F32) go(std::true_type{});
     else go(std::false_type{});
