@@ -1517,15 +1517,15 @@ bool tc_make_map_k(CUtensorMap* m, const void* base, int rows, int K, int box_ro
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 2-D bf16 tensor [rows][cols], rows `stride` elements apart (16-byte multiples), box [box_rows][64], 128-byte swizzle. Not cached.
-bool tc_make_map_strided(CUtensorMap* m, const void* base, int rows, int cols, long long stride, int box_rows) {
+// 3-D bf16 tensor of rows `stride` elements apart of n parts of 64, box [2 parts][box_rows][64], 128-byte swizzle. Not cached.
+bool tc_make_map_parts(CUtensorMap* m, const void* base, int rows, int n, long long stride, int box_rows) {
     auto fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-    const cuuint32_t es[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)n};
+    const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 2};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

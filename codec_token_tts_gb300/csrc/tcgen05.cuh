@@ -140,8 +140,8 @@ bool tc_make_map_rows(CUtensorMap* m, const void* base, int C, int T, int B, int
 // Host: 2-D bf16 tensor map [rows][K], box [box_rows][box_k], box_k 64 (128-byte swizzle) or 32
 // (64-byte swizzle).
 bool tc_make_map_k(CUtensorMap* m, const void* base, int rows, int K, int box_rows, int box_k);
-// Host: 2-D bf16 tensor map [rows][cols], rows `stride` elements apart, box [box_rows][64], 128-byte swizzle.
-bool tc_make_map_strided(CUtensorMap* m, const void* base, int rows, int cols, long long stride, int box_rows);
+// Host: 3-D bf16 tensor map of rows `stride` elements apart of n parts of 64, box [2 parts][box_rows][64], 128-byte swizzle.
+bool tc_make_map_parts(CUtensorMap* m, const void* base, int rows, int n, long long stride, int box_rows);
 // Host: 3-D bf16 tensor map [rows][heads][128], rows `stride` elements apart, box [box_rows][2 heads][64], 128-byte swizzle.
 bool tc_make_map_heads(CUtensorMap* m, const void* base, int rows, int heads, long long stride, int box_rows);
 

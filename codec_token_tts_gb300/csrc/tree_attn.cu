@@ -50,15 +50,17 @@ struct Piece {
 template <bool F32>
 struct Lay {
     static constexpr int QPARTS = F32 ? 3 : 1, PPARTS = F32 ? 3 : 2, QBUFS = F32 ? 1 : 2;
-    // regions of TMEM for a tile's scores (64 columns) and then its weights, and how far scores run ahead of sums. Of 32 keys' 32 columns
-    // the first part of their weights takes 16, the second the others; the third stands behind
+    // Regions of TMEM for a tile's scores (64 columns), where weights replace them: of 32 keys' 32 columns the first part of their
+    // weights takes 16, the second the others; the third stands behind. Values are loaded AHEAD tiles behind keys
     static constexpr int REGIONS = F32 ? 2 : 4, REGION = F32 ? 128 : 64, AHEAD = F32 ? 1 : 2;
     static __device__ __forceinline__ uint32_t part_at(int part, int chunk) { return part < 2 ? chunk * 32 + part * 16 : KVB + chunk * 16; }
     static constexpr int ROW_PIECES = 32 * (F32 ? 4 : 2) / 16;  // 16-byte pieces of 32 dims of a row of out
+    static constexpr int STAGE = 32 * 16 * ROW_PIECES;          // of each warp that writes sums
     static __device__ __forceinline__ int stage_at(int row, int pc) { return F32 ? (int)sw128_off(row, pc) : row * 64 + ((pc ^ (row >> 1 & 3)) << 4); }
 };
 // the last two beside the rows that few nodes leave empty
-constexpr int W_SUM = 8, W_REST = 12, W_SCHED = 12, W_SAFE = 13, W_LOAD = 14, W_MMA = 15, WARPS = 16, NT = WARPS * 32;
+// (the loader in the quarter of warps 2, 6, 10, which few nodes leave empty: 8 x 65537 keys, 31 nodes 326 us, in that of 0 or 1 375)
+constexpr int W_SUM = 8, W_REST = 12, W_SAFE = 12, W_S = 13, W_LOAD = 14, W_PV = 15, WARPS = 16, NT = WARPS * 32;
 // registers of a thread: the launch's 128 are dealt anew
 constexpr int REGS_SOFT = 112, REGS_SUM = 208, REGS_REST = 80;
 static_assert(2 * REGS_SOFT + REGS_SUM + REGS_REST == 4 * 128, "registers of the launch");
@@ -69,10 +71,10 @@ constexpr int TMEM_COLS = 512;  // the regions, then the sums of tile t at 256 +
 
 struct Shared {
     u64 k_full[MAX_SLOTS], k_empty[MAX_SLOTS], v_full[MAX_SLOTS], v_ready[MAX_SLOTS], v_empty[MAX_SLOTS];
-    u64 s_full[4], p_full[4];   // of a region: scores there (products, their issuer), weights there (4 warps)
+    u64 s_full[4], p_full[4], w_empty[4];  // of a region: scores there (products, their issuer), weights there (4 warps), weights taken
     u64 o_full[2], o_empty[2];  // a tile's sums there (products, their issuer), taken (4)
     u64 m_full[4][2];           // a tile's references of 32 rows there
-    u64 q_full[2], q_empty[2], piece_full[PIECES], seen_full[PIECES], piece_empty[PIECES], fin;
+    u64 q_full[2], q_empty[2], piece_full[PIECES], seen_full[PIECES], piece_empty[PIECES], fin[2];
     uint32_t sums[WARPS];
     uint32_t tmem;
     int abort;
@@ -82,8 +84,7 @@ struct Shared {
     float m[RING][128], l[RING][128];
 };
 constexpr int SMEM_MAX = 232448;
-constexpr int STAGE = 4096;  // of each warp that writes sums
-// Of dynamic shared memory: the queries of `rows` rows (a multiple of 8), then `slots` pages of K and V, the stages, then Shared.
+// Of dynamic shared memory: the queries of `rows` rows (a multiple of 8), pages of K and of V, the stages, then Shared.
 struct Plan {
     int rows, k_slots, v_slots;
     template <bool F32>
@@ -93,7 +94,7 @@ struct Plan {
     template <bool F32>
     __host__ __device__ int stages() const { return ring<F32>() + (k_slots + v_slots) * PAGE_BYTES; }
     template <bool F32>
-    __host__ __device__ int shared() const { return stages<F32>() + 4 * STAGE; }
+    __host__ __device__ int shared() const { return stages<F32>() + 4 * Lay<F32>::STAGE; }
     template <bool F32>
     __host__ __device__ int bytes() const { return shared<F32>() + (int)sizeof(Shared); }
 };
@@ -238,11 +239,12 @@ __device__ __forceinline__ bool ancestors(const int32_t* parents, int n, int lan
 
 __device__ __forceinline__ bool finite16(uint32_t half) { return (half & 0x7F80u) != 0x7F80u; }
 
-// grid: the shares, 512 threads. All tiles of all (sequence, KV head) are one line, cut into equal shares. Of warps 12 .. 15 one
-// deals the pieces of its share, one loads pages (and bf16 queries) by TMA, one makes values safe to be multiplied by 0, and one
-// issues the products: scores S = Q K^T of tile t + AHEAD, then sums O = P V of tile t. Warps 0 .. 3 turn the scores of even tiles
-// into weights (a thread a row), which replace them in TMEM as the A operand of P V, warps 4 .. 7 those of odd tiles; they hand the
-// running maximum on. Warps 8 .. 11 add each tile's sums to those in their registers. Every wait is bounded.
+// grid: the shares, 512 threads. All tiles of all (sequence, KV head) are one line, cut into equal shares. Warp 12 deals the pieces of
+// its share and loads pages (and bf16 queries) by TMA, 13 finds the nodes' ancestors and makes values safe to be multiplied by 0, 14 and
+// 15 issue the products: scores S = Q K^T of a tile, and sums O = P V of one before (two warps, since an issuer waits for
+// its products: one took turns at it, and the tensor cores waited meanwhile). Warps 0 .. 7 turn scores into weights (a thread a row),
+// which replace them in TMEM as the A operand of P V; they hand the running maximum on. Warps 8 .. 11 add each tile's sums to those
+// in their registers. Every wait is bounded.
 template <bool F32>
 __global__ void __launch_bounds__(NT, 1)
     k_tree_attn(const __grid_constant__ CUtensorMap pool_map, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
@@ -270,6 +272,7 @@ __global__ void __launch_bounds__(NT, 1)
         init(sh.v_ready, 1, 2 * MAX_SLOTS);  // and v_empty
         init(sh.s_full, 2, 4);
         init(sh.p_full, 4, 4);
+        init(sh.w_empty, 1, 4);
         init(sh.o_full, 2, 2);
         init(sh.o_empty, 4, 2);
         init(&sh.m_full[0][0], 1, 8);
@@ -278,11 +281,11 @@ __global__ void __launch_bounds__(NT, 1)
         init(sh.piece_full, 1, PIECES);
         init(sh.seen_full, 1, PIECES);
         init(sh.piece_empty, 3 + 8 + 4, PIECES);
-        init(&sh.fin, 1, 1);
+        init(sh.fin, 1, 2);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == W_MMA) {
+    if (warp == W_PV) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s_addr(&sh.tmem)), "r"(TMEM_COLS));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
@@ -342,22 +345,37 @@ __global__ void __launch_bounds__(NT, 1)
         ok = wait_for(&sh.abort, bar, parity);
         return ok;
     };
+    constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(128 >> 4) << 24);  // bf16 times bf16 to fp32, 128 rows
+    const auto drain = [&](bool leader) {  // every product that this warp has issued has ended
+        if (leader) {
+            u64* const fin = &sh.fin[warp == W_S];
+            at_commit((uint64_t*)fin);
+            const unsigned long long t0 = g_time();
+#pragma unroll 1
+            while (!tc_mbar_try((uint64_t*)fin, 0) && g_time() - t0 < TC_TIMEOUT_NS) {
+            }
+        }
+        __syncwarp();
+    };
     // piece k, once it is there
     const auto piece_bar = [&](uint32_t k) { return &sh.piece_full[k % PIECES]; };
     const auto piece_par = [](uint32_t k) { return k / PIECES & 1u; };
 
     if (warp >= W_REST) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
-        if (warp == W_SCHED) {
+        if (warp == W_LOAD) {
+            int ks = 0, vs = 0;       // slots
+            uint32_t kp = 1, vp = 1;  // parities of what empties them (the first round is empty)
+            uint32_t kk = ~0u, vk = ~0u;
+            int kt = 0, vt = 0, from = 0;
+            int here = 0, next = 0;  // pages of the keys' tiles from + lane and from + 32 + lane
+            // the sequence, of its 8 heads' tiles the next one, and what of the share has not been dealt
             int b = sh.start[0], at = sh.start[1], row = sh.start[2], len = sh.start[3], n = sh.start[4];
             uint32_t left = U;
-            bool head = true;
-            if (left == 0 && lane == 0) a.meta[me] = make_int4(-1, 0, 0, 0);
-#pragma unroll 1
-            for (uint32_t k = 0;; ++k) {
-                const int slot = k % PIECES;
-                if (k >= PIECES && !wait(&sh.piece_empty[slot], (k / PIECES - 1) & 1u)) break;
-                Piece& p = sh.piece[slot];
+            // the next piece (b < 0 where nothing is left), in its place once every warp is done with the one before
+            const auto deal_piece = [&](uint32_t k) {
+                Piece& p = sh.piece[k % PIECES];
+                if (k >= PIECES && !wait(&sh.piece_empty[k % PIECES], (k / PIECES - 1) & 1u)) return false;
                 const int nt = tiles_of(len), g = at / nt, t0 = at - g * nt, t1 = (int)min((uint32_t)nt, t0 + left);
                 if (lane == 0) {
                     p.b = left ? b : -1;
@@ -369,23 +387,12 @@ __global__ void __launch_bounds__(NT, 1)
                     p.t1 = t1;
                     p.tiles = nt;
                     p.whole = t0 == 0 && t1 == nt;
-                    p.first = head;
+                    p.first = k == 0;
                     p.bad[0] = p.bad[1] = 0;
-                    arrive(&sh.piece_full[slot]);
+                    arrive(piece_bar(k));
                 }
-                if (left == 0) break;
-                bool tree_ok = true;
-                if (t1 == nt) {
-                    tree_ok = ancestors(a.parents + (size_t)b * a.N, n, lane, p.seen, p.up);
-                    if (!tree_ok && lane == 0) set_err(c.err, TTS_BB_TREE_ERR_TREE);
-                }
-                if (lane == 0) {
-                    p.ok = tree_ok;
-                    arrive(&sh.seen_full[slot]);
-                    // of the share's first piece: its (sequence, head), nodes, and whether it begins inside of that one; bit 2: in order
-                    if (head) a.meta[me] = make_int4(b * NKV + g, n, (t0 > 0) | tree_ok << 2, 0);
-                }
-                head = false;
+                __syncwarp();
+                if (left == 0) return true;
                 left -= t1 - t0;
                 at += t1 - t0;
                 if (at == nt * NKV && left > 0) {
@@ -393,24 +400,17 @@ __global__ void __launch_bounds__(NT, 1)
                     do ++b; while (b < a.B && !sequence(c, a, b, false, row, len, n));
                     if (b >= a.B) left = 0;
                 }
-            }
-        } else if (warp == W_LOAD) {
-            int ks = 0, vs = 0;       // slots
-            uint32_t kp = 1, vp = 1;  // parities of what empties them (the first round is empty)
-            uint32_t kk = ~0u, vk = ~0u;
-            int kt = 0, vt = 0, from = 0;
-            int here = 0, next = 0;  // pages of the keys' tiles from + lane and from + 32 + lane
+                return true;
+            };
             const Piece *kq = nullptr, *vq = nullptr;
             const auto entry = [&](int t) { return t < kq->t1 && t < kq->tiles - 1 ? c.table[(size_t)kq->row * c.bps + t] : 0; };
             // K (which 0) or V of a tile: a page of the pool, or the tree's own rows
             const auto fetch = [&](unsigned char* to, u64* bar, const Piece& p, int t, int page, int which) {
-                arrive_tx(bar, page >= 0 ? PAGE_BYTES : 0);
+                arrive_tx(bar, page < 0 ? 0 : PAGE_BYTES);
                 if (page < 0) return;
                 const bool tree = t == p.tiles - 1;
                 const CUtensorMap* const map = !tree ? &pool_map : which ? &v_map : &k_map;
-                const int x = tree ? p.g * HD : 0, y = tree ? p.b * a.N : ((page * 2 + which) * NKV + p.g) * KVB;
-                tma_load_2d(to, map, x, y, (uint64_t*)bar);
-                tma_load_2d(to + PAGE_BYTES / 2, map, x + 64, y, (uint64_t*)bar);
+                tma_load_3d(to, map, 0, tree ? p.b * a.N : ((page * 2 + which) * NKV + p.g) * KVB, tree ? 2 * p.g : 0, (uint64_t*)bar);
             };
             int k_landing = 0, v_landing = 0;
 #pragma unroll 1
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(NT, 1)
                 if (i < U) {
                     if (!kq || kt == kq->t1) {
                         ++kk;
-                        if (!wait(piece_bar(kk), piece_par(kk))) break;
+                        if (!deal_piece(kk)) break;
                         kq = &sh.piece[kk % PIECES];
                         from = kt = kq->t0;
                         here = entry(from + lane);
@@ -457,9 +457,7 @@ __global__ void __launch_bounds__(NT, 1)
                 }
                 if (i >= L::AHEAD) {
                     if (!vq) {
-                        ++vk;
-                        if (!wait(piece_bar(vk), piece_par(vk))) break;
-                        vq = &sh.piece[vk % PIECES];
+                        vq = &sh.piece[++vk % PIECES];
                         vt = vq->t0;
                     }
                     if (!wait(&sh.v_empty[vs], vp)) break;
@@ -473,6 +471,7 @@ __global__ void __launch_bounds__(NT, 1)
                     }
                 }
             }
+            if (ok) ok = deal_piece(kk + 1);  // no more
             if (*(volatile int*)&sh.abort && lane == 0) {  // copies in flight land before the block ends
                 const auto landed = [&](u64* full, int n, int slots) {
 #pragma unroll 1
@@ -487,95 +486,94 @@ __global__ void __launch_bounds__(NT, 1)
                 landed(sh.v_full, v_landing, plan.v_slots);
                 if (!F32) landed(sh.q_full, (int)(kk + 1), 2);
             }
-        } else if (warp == W_MMA) {
-            constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(128 >> 4) << 24);
-            constexpr uint32_t IDESC_S = IDESC | ((uint32_t)(KVB >> 3) << 17), IDESC_PV = IDESC | ((uint32_t)(HD >> 3) << 17) | (1u << 16);
-            const uint32_t q0 = desc_k(s_addr(smem)), k0 = desc_k(s_addr(k_ring)), v0 = desc_mn(s_addr(v_ring)), half = (uint32_t)plan.rows * 128 >> 4,
+        } else if (warp == W_S) {
+            constexpr uint32_t IDESC_S = IDESC | ((uint32_t)(KVB >> 3) << 17);
+            const uint32_t q0 = desc_k(s_addr(smem)), k0 = desc_k(s_addr(k_ring)), half = (uint32_t)plan.rows * 128 >> 4,
                            q_buf = (uint32_t)plan.q_bytes<F32>() >> 4;
             const bool leader = elect();
-            uint32_t ks = 0, vs = 0, kp = 0, vp = 0, sk = ~0u, pk = ~0u;  // slots, their parities, pieces of the scores and of the sums
-            int s_left = 0, p_left = 0, pt = 0, p_tiles = 0, p_len = 0, p_n = 0;
+            uint32_t ks = 0, kp = 0, k = ~0u;  // slot, its parity, piece
+            int left = 0;
 #pragma unroll 1
-            for (uint32_t i = 0; i < U + L::AHEAD; ++i) {
-                if (i < U) {
-                    if (s_left == 0) {
-                        ++sk;
-                        if (!wait(piece_bar(sk), piece_par(sk))) break;
-                        s_left = sh.piece[sk % PIECES].t1 - sh.piece[sk % PIECES].t0;
-                        if (!wait(&sh.q_full[F32 ? 0 : sk & 1], (F32 ? sk : sk >> 1) & 1u)) break;
-                    }
-                    // the keys; and the weights in the region were taken by the product of tile i - REGIONS (none: the phase before the first)
-                    const uint32_t region = i % L::REGIONS, j = i - L::REGIONS;
-                    ok = wait_for(&sh.abort, &sh.k_full[ks], kp, &sh.o_full[j & 1], i < L::REGIONS ? 1u : (j >> 1) & 1u);
-                    if (!ok) break;
-                    tc_after();
-                    const uint32_t d = tmem + region * L::REGION, k1 = k0 + ks * (PAGE_BYTES >> 4), q1 = q0 + (F32 ? 0u : (sk & 1) * q_buf);
-                    --s_left;
-                    if (leader) {
-#pragma unroll
-                        for (int part = L::QPARTS - 1; part >= 0; --part)
-#pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
-                                mma_ss(d, q1 + (uint32_t)(part * 2 + (kk >> 2)) * half + (kk & 3) * 2, k1 + (uint32_t)((kk >> 2) * (PAGE_BYTES / 2) + (kk & 3) * 32) / 16,
-                                       IDESC_S, part < L::QPARTS - 1 || kk > 0);
-                        arrive(&sh.s_full[region]);
-                        at_commit((uint64_t*)&sh.s_full[region]);
-                        at_commit((uint64_t*)&sh.k_empty[ks]);
-                        if (!F32 && s_left == 0) at_commit((uint64_t*)&sh.q_empty[sk & 1]);
-                    }
-                    __syncwarp();
-                    if (++ks == (uint32_t)plan.k_slots) ks = 0, kp ^= 1;
+            for (uint32_t u = 0; u < U; ++u) {
+                if (left == 0) {
+                    ++k;
+                    if (!wait(piece_bar(k), piece_par(k))) break;
+                    left = sh.piece[k % PIECES].t1 - sh.piece[k % PIECES].t0;
+                    if (!wait(&sh.q_full[F32 ? 0 : k & 1], (F32 ? k : k >> 1) & 1u)) break;
                 }
-                if (i >= L::AHEAD) {
-                    const uint32_t u = i - L::AHEAD, region = u % L::REGIONS;
-                    if (p_left == 0) {
-                        ++pk;
-                        if (!wait(piece_bar(pk), piece_par(pk))) break;
-                        const Piece& p = sh.piece[pk % PIECES];
-                        pt = p.t0;
-                        p_left = p.t1 - pt;
-                        p_tiles = p.tiles;
-                        p_len = p.len;
-                        p_n = p.n;
-                    }
-                    // 16 keys a step, of those that there are
-                    const int keys = pt == p_tiles - 1 ? p_n : min(KVB, p_len - pt * KVB), steps = (keys + 15) / 16;
-                    ok = wait_for(&sh.abort, &sh.p_full[region], (u / L::REGIONS) & 1u, &sh.v_ready[vs], vp, &sh.o_empty[u & 1], ((u >> 1) - 1) & 1u);
-                    if (!ok) break;
-                    tc_after();
-                    const uint32_t w = tmem + region * L::REGION, d = tmem + 256 + (u & 1) * 128, v1 = v0 + vs * (PAGE_BYTES >> 4);
-                    ++pt;
-                    --p_left;
-                    if (leader) {
+                // the keys; and the weights that tile u - REGIONS left in the region were taken (of none: the phase before the first)
+                const uint32_t region = u % L::REGIONS;
+                ok = wait_for(&sh.abort, &sh.k_full[ks], kp, &sh.w_empty[region], (u / L::REGIONS - 1) & 1u);
+                if (!ok) break;
+                tc_after();
+                const uint32_t d = tmem + region * L::REGION, k1 = k0 + ks * (PAGE_BYTES >> 4), q1 = q0 + (F32 ? 0u : (k & 1) * q_buf);
+                --left;
+                if (leader) {
 #pragma unroll
-                        for (int part = L::PPARTS - 1; part >= 0; --part)
+                    for (int part = L::QPARTS - 1; part >= 0; --part)
 #pragma unroll
-                            for (int kk = 0; kk < KVB / 16; ++kk)  // 8 columns of weights
-                                if (kk < steps) mma_ts(d, w + L::part_at(part, kk >> 1) + (kk & 1) * 8, v1 + (uint32_t)(kk * 2048 / 16), IDESC_PV, part < L::PPARTS - 1 || kk > 0);
-                        arrive(&sh.o_full[u & 1]);
-                        at_commit((uint64_t*)&sh.o_full[u & 1]);
-                        at_commit((uint64_t*)&sh.v_empty[vs]);
-                        if (p_left == 0) arrive(&sh.piece_empty[pk % PIECES]);
-                    }
-                    __syncwarp();
-                    if (++vs == (uint32_t)plan.v_slots) vs = 0, vp ^= 1;
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_ss(d, q1 + (uint32_t)(part * 2 + (kk >> 2)) * half + (kk & 3) * 2, k1 + (uint32_t)((kk >> 2) * (PAGE_BYTES / 2) + (kk & 3) * 32) / 16,
+                                   IDESC_S, part < L::QPARTS - 1 || kk > 0);
+                    arrive(&sh.s_full[region]);
+                    at_commit((uint64_t*)&sh.s_full[region]);
+                    at_commit((uint64_t*)&sh.k_empty[ks]);
+                    if (!F32 && left == 0) at_commit((uint64_t*)&sh.q_empty[k & 1]);
                 }
+                __syncwarp();
+                if (++ks == (uint32_t)plan.k_slots) ks = 0, kp ^= 1;
             }
-            if (!ok && lane == 0) *(volatile int*)&sh.abort = 1;
-            if (leader) {
-                at_commit((uint64_t*)&sh.fin);  // every product has ended
-                const unsigned long long t0 = g_time();
+            drain(leader);
+        } else if (warp == W_PV) {
+            constexpr uint32_t IDESC_PV = IDESC | ((uint32_t)(HD >> 3) << 17) | (1u << 16);
+            const uint32_t v0 = desc_mn(s_addr(v_ring));
+            const bool leader = elect();
+            uint32_t vs = 0, vp = 0, k = ~0u;  // slot, its parity, piece
+            int left = 0, t = 0, tiles = 0, len = 0, n = 0;
 #pragma unroll 1
-                while (!tc_mbar_try((uint64_t*)&sh.fin, 0) && g_time() - t0 < TC_TIMEOUT_NS) {
+            for (uint32_t u = 0; u < U; ++u) {
+                if (left == 0) {
+                    ++k;
+                    if (!wait(piece_bar(k), piece_par(k))) break;
+                    const Piece& p = sh.piece[k % PIECES];
+                    t = p.t0;
+                    left = p.t1 - t;
+                    tiles = p.tiles;
+                    len = p.len;
+                    n = p.n;
                 }
+                // 16 keys a step of the products, of those that there are
+                const int keys = t == tiles - 1 ? n : min(KVB, len - t * KVB), steps = (keys + 15) / 16;
+                const uint32_t region = u % L::REGIONS;
+                ok = wait_for(&sh.abort, &sh.p_full[region], (u / L::REGIONS) & 1u, &sh.v_ready[vs], vp, &sh.o_empty[u & 1], ((u >> 1) - 1) & 1u);
+                if (!ok) break;
+                tc_after();
+                const uint32_t w = tmem + region * L::REGION, d = tmem + 256 + (u & 1) * 128, v1 = v0 + vs * (PAGE_BYTES >> 4);
+                ++t;
+                --left;
+                if (leader) {
+#pragma unroll
+                    for (int part = L::PPARTS - 1; part >= 0; --part)
+#pragma unroll
+                        for (int kk = 0; kk < KVB / 16; ++kk)  // 8 columns of weights
+                            if (kk < steps) mma_ts(d, w + L::part_at(part, kk >> 1) + (kk & 1) * 8, v1 + (uint32_t)(kk * 2048 / 16), IDESC_PV, part < L::PPARTS - 1 || kk > 0);
+                    arrive(&sh.o_full[u & 1]);
+                    at_commit((uint64_t*)&sh.o_full[u & 1]);
+                    at_commit((uint64_t*)&sh.v_empty[vs]);
+                    at_commit((uint64_t*)&sh.w_empty[region]);
+                    if (left == 0) arrive(&sh.piece_empty[k % PIECES]);
+                }
+                __syncwarp();
+                if (++vs == (uint32_t)plan.v_slots) vs = 0, vp ^= 1;
             }
-            __syncwarp();
+            drain(leader);
         } else if (warp == W_SAFE) {
             // Values that weights of 0 may meet: rows behind a page's keys (up to a step of 16) and pages that were not there become
             // zeros, and so does what is not finite among the tree's: it is added to the rows that see it at the end.
             int t = 0, vs = 0;
             uint32_t vp = 0, k = ~0u;
             Piece* p = nullptr;
+            if (U == 0 && lane == 0) a.meta[me] = make_int4(-1, 0, 0, 0);
 #pragma unroll 1
             for (uint32_t u = 0; ok && u < U; ++u) {
                 if (!p) {
@@ -583,6 +581,18 @@ __global__ void __launch_bounds__(NT, 1)
                     if (!wait(piece_bar(k), piece_par(k))) break;
                     p = &sh.piece[k % PIECES];
                     t = p->t0;
+                    bool tree_ok = true;
+                    if (p->t1 == p->tiles) {
+                        tree_ok = ancestors(a.parents + (size_t)p->b * a.N, p->n, lane, p->seen, p->up);
+                        if (!tree_ok && lane == 0) set_err(c.err, TTS_BB_TREE_ERR_TREE);
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        p->ok = tree_ok;
+                        arrive(&sh.seen_full[k % PIECES]);
+                        // of the share's first piece: its (sequence, head), nodes, and whether it begins inside of that one; bit 2: in order
+                        if (k == 0) a.meta[me] = make_int4(p->b * NKV + p->g, p->n, (t > 0) | tree_ok << 2, 0);
+                    }
                 }
                 if (!wait(&sh.v_full[vs], vp)) break;
                 const bool tree = t == p->tiles - 1;
@@ -603,18 +613,19 @@ __global__ void __launch_bounds__(NT, 1)
                             for (int i = 0; i < 4; ++i) x[i] = key0 + 2 * i < valid ? *at(key0 + 2 * i, lane & 15) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                                bool bad = false;
+                                // an exponent of all ones carries into the bit above it
+                                uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, over = 0;
+#pragma unroll
+                                for (int h = 0; h < 4; ++h) over |= (w[h] & 0x7F807F80u) + 0x00800080u;
+                                if (!(over & 0x80008000u)) continue;
 #pragma unroll
                                 for (int h = 0; h < 4; ++h) {
-                                    if (!finite16(w[h])) { w[h] &= 0xFFFF0000u; bad = true; }
-                                    if (!finite16(w[h] >> 16)) { w[h] &= 0xFFFFu; bad = true; }
+                                    if (!finite16(w[h])) w[h] &= 0xFFFF0000u;
+                                    if (!finite16(w[h] >> 16)) w[h] &= 0xFFFFu;
                                 }
-                                if (bad) {
-                                    const int key = key0 + 2 * i;
-                                    *at(key, lane & 15) = make_uint4(w[0], w[1], w[2], w[3]);
-                                    atomicOr(&p->bad[key >> 5], 1u << (key & 31));
-                                }
+                                const int key = key0 + 2 * i;
+                                *at(key, lane & 15) = make_uint4(w[0], w[1], w[2], w[3]);
+                                atomicOr(&p->bad[key >> 5], 1u << (key & 31));
                             }
                         }
                     }
@@ -630,12 +641,12 @@ __global__ void __launch_bounds__(NT, 1)
             }
         }
     } else if (warp < W_SUM) {
-        // ---------------- scores to weights: thread = row; warps 0 .. 3 even tiles, 4 .. 7 odd ones
+        // ---------------- scores to weights: thread = row; warps 0 .. 3 the share's even tiles, 4 .. 7 the odd ones
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
         const int group = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const float cs = 0.08838834764831845f * 1.4426950408889634f;
-        uint32_t u0 = 0;
+        uint32_t u0 = 0;  // tiles before the piece
 #pragma unroll 1
         for (uint32_t k = 0; ok; ++k) {
             if (!wait(piece_bar(k), piece_par(k))) break;
@@ -687,10 +698,10 @@ __global__ void __launch_bounds__(NT, 1)
             const bool mine = quarter * 32 < rows;
             float mc = -INFINITY, l = 0.f;  // of this warp's tiles: the reference, and the sum of weights
 #pragma unroll 1
-            for (uint32_t u = u0 + ((u0 ^ group) & 1); u < u0 + nt; u += 2) {
-                const int t = p.t0 + (int)(u - u0);
-                const uint32_t at = lanes + (u % L::REGIONS) * L::REGION;
-                if (!wait(&sh.s_full[u % L::REGIONS], (u / L::REGIONS) & 1u)) break;
+            for (int j = (int)(u0 ^ group) & 1; j < nt; j += 2) {
+                const int t = p.t0 + j;
+                const uint32_t u = u0 + j, region = u % L::REGIONS, at = lanes + region * L::REGION;
+                if (!wait(&sh.s_full[region], (u / L::REGIONS) & 1u)) break;
                 float m = -INFINITY;
                 // the keys that count, a bit each, where not all do
                 const bool tree = t == p.tiles - 1;
@@ -761,12 +772,12 @@ __global__ void __launch_bounds__(NT, 1)
                     halves(sum[1], z, v);
                     l = (l == 0.f ? 0.f : l * at_ex2(mc - base)) + ((x + y) + (z + v));
                     mc = now;
-                    if (u + 2 >= u0 + nt) sh.l[u % RING][r] = l;
+                    if (j + 2 >= nt) sh.l[u % RING][r] = l;
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0) arrive(&sh.p_full[u % L::REGIONS]);
+                if (lane == 0) arrive(&sh.p_full[region]);
             }
             if (!ok) break;
             u0 += nt;
@@ -834,7 +845,7 @@ __global__ void __launch_bounds__(NT, 1)
                         }
                         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                         const float f = !p.whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-                        unsigned char* const stage = smem + plan.stages<F32>() + quarter * STAGE;
+                        unsigned char* const stage = smem + plan.stages<F32>() + quarter * L::STAGE;
 #pragma unroll 1
                         for (int i = 0; i < 4; ++i) {
                             uint32_t x[32];
@@ -901,7 +912,7 @@ __global__ void __launch_bounds__(NT, 1)
     if (!ok && lane == 0) set_err(c.err, TTS_BB_TREE_ERR_TIMEOUT);
     tc_before();
     __syncthreads();
-    if (warp == W_MMA) {
+    if (warp == W_PV) {
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS));
     }
@@ -962,9 +973,9 @@ constexpr size_t META_BYTES = (SHARES * sizeof(int4) + 255) / 256 * 256;
 template <bool F32>
 Plan plan_of(int N) {
     Plan p{(2 * N + 7) / 8 * 8, 0, 0};
-    const int slots = std::min(2 * MAX_SLOTS, (SMEM_MAX - p.bytes<F32>()) / PAGE_BYTES);
-    p.k_slots = slots / 2;
-    p.v_slots = slots - p.k_slots;
+    const int pages = (SMEM_MAX - p.bytes<F32>()) / PAGE_BYTES;
+    p.k_slots = std::min(MAX_SLOTS, pages / 2);
+    p.v_slots = std::min(MAX_SLOTS, pages - p.k_slots);
     return p;
 }
 
@@ -990,8 +1001,8 @@ TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int la
     if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
     const Pages c = pages_of(cache, layer);
     CUtensorMap pool_map, k_map, v_map, q_map;
-    if (!tc_make_map_strided(&pool_map, c.pool, c.n_blocks * 2 * NKV * KVB, HD, HD, KVB) ||
-        !tc_make_map_strided(&k_map, k, B * N, NKV * HD, kv_stride, KVB) || !tc_make_map_strided(&v_map, v, B * N, NKV * HD, kv_stride, KVB) ||
+    if (!tc_make_map_parts(&pool_map, c.pool, c.n_blocks * 2 * NKV * KVB, 2, HD, KVB) ||
+        !tc_make_map_parts(&k_map, k, B * N, 2 * NKV, kv_stride, KVB) || !tc_make_map_parts(&v_map, v, B * N, 2 * NKV, kv_stride, KVB) ||
         (type == TTS_BB_T_BF16 && !tc_make_map_heads(&q_map, q, B * N, NQ, q_stride, N)))
         return TTS_BB_E_CUDA;
     if (type != TTS_BB_T_BF16) q_map = k_map;  // not used
