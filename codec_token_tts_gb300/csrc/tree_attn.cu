@@ -54,9 +54,7 @@ struct Lay {
     // weights takes 16, the second the others; the third stands behind. Values are loaded AHEAD tiles behind keys
     static constexpr int REGIONS = F32 ? 2 : 4, REGION = F32 ? 128 : 64, AHEAD = F32 ? 1 : 2;
     static __device__ __forceinline__ uint32_t part_at(int part, int chunk) { return part < 2 ? chunk * 32 + part * 16 : KVB + chunk * 16; }
-    static constexpr int ROW_PIECES = 32 * (F32 ? 4 : 2) / 16;  // 16-byte pieces of 32 dims of a row of out
-    static constexpr int STAGE = 32 * 16 * ROW_PIECES;          // of each warp that writes sums
-    static __device__ __forceinline__ int stage_at(int row, int pc) { return F32 ? (int)sw128_off(row, pc) : row * 64 + ((pc ^ (row >> 1 & 3)) << 4); }
+    static constexpr int STAGE = F32 ? 4096 : 0;  // of each warp that writes sums: 32 rows of 128 bytes
 };
 // the last two beside the rows that few nodes leave empty
 // (the loader in the quarter of warps 2, 6, 10, which few nodes leave empty: 8 x 65537 keys, 31 nodes 326 us, in that of 0 or 1 375)
@@ -606,24 +604,35 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll 1
                     for (int key = valid + (lane >> 4); key < (keys + 15) / 16 * 16; key += 2) *at(key, lane & 15) = make_uint4(0u, 0u, 0u, 0u);
                     if (tree) {
-#pragma unroll 1
-                        for (int key0 = lane >> 4; key0 < valid; key0 += 8) {
+                        // 0 times what is finite is 0, and NaN else; the rows behind are zeros by now
+                        __syncwarp();
+                        const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+                        __nv_bfloat162 sum[4] = {zero, zero, zero, zero};
+#pragma unroll 2
+                        for (int key0 = lane >> 4; key0 < (valid + 15) / 16 * 16; key0 += 8) {
                             uint4 x[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) x[i] = key0 + 2 * i < valid ? *at(key0 + 2 * i, lane & 15) : make_uint4(0u, 0u, 0u, 0u);
+                            for (int i = 0; i < 4; ++i) x[i] = *at(key0 + 2 * i, lane & 15);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                // an exponent of all ones carries into the bit above it
-                                uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, over = 0;
+                                const __nv_bfloat162* const y = reinterpret_cast<const __nv_bfloat162*>(&x[i]);
 #pragma unroll
-                                for (int h = 0; h < 4; ++h) over |= (w[h] & 0x7F807F80u) + 0x00800080u;
-                                if (!(over & 0x80008000u)) continue;
+                                for (int h = 0; h < 4; ++h) sum[h] = __hfma2(y[h], zero, sum[h]);
+                            }
+                        }
+                        const __nv_bfloat162 all = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
+                        if (__any_sync(0xffffffffu, __hisnan(__low2bfloat16(all)) || __hisnan(__high2bfloat16(all)))) {
+#pragma unroll 1
+                            for (int key = lane >> 4; key < valid; key += 2) {
+                                const uint4 x = *at(key, lane & 15);
+                                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                                bool bad = false;
 #pragma unroll
                                 for (int h = 0; h < 4; ++h) {
-                                    if (!finite16(w[h])) w[h] &= 0xFFFF0000u;
-                                    if (!finite16(w[h] >> 16)) w[h] &= 0xFFFFu;
+                                    if (!finite16(w[h])) { w[h] &= 0xFFFF0000u; bad = true; }
+                                    if (!finite16(w[h] >> 16)) { w[h] &= 0xFFFFu; bad = true; }
                                 }
-                                const int key = key0 + 2 * i;
+                                if (!bad) continue;
                                 *at(key, lane & 15) = make_uint4(w[0], w[1], w[2], w[3]);
                                 atomicOr(&p->bad[key >> 5], 1u << (key & 31));
                             }
@@ -823,88 +832,72 @@ __global__ void __launch_bounds__(NT, 1)
                     if (t + 2 >= nt) l = (t == 0 || l == 0.f ? 0.f : l * f) + sh.l[u % RING][r];  // of even and of odd tiles
                     m = now;
                 }
-                if (t + 1 == nt) {
-                    // The piece's end. The sums go back into the tile's columns of TMEM and are taken from there 32 dims at a time: a short loop,
-                    // where 128 registers would be written by code that the instruction cache never holds
-                    if (p.t1 == p.tiles && !wait(&sh.seen_full[k % PIECES], piece_par(k))) break;
-                    const bool bad = p.bad[0] | p.bad[1], write = p.whole ? p.ok : true;
-                    T* const to = static_cast<T*>(a.out) + ((size_t)p.b * a.N * NQ + 2 * p.g) * HD;
-                    float4* const part = a.part + ((size_t)me * 2 + !p.first) * PART * 128 + r;
-                    if (mine) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t x[32];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                float y, z;
-                                halves(o[16 * i + j], y, z);
-                                x[2 * j] = __float_as_uint(y);
-                                x[2 * j + 1] = __float_as_uint(z);
-                            }
-                            tm_st32(lanes + (u & 1) * 128 + 32 * i, x);
-                        }
-                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                        const float f = !p.whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-                        unsigned char* const stage = smem + plan.stages<F32>() + quarter * L::STAGE;
-#pragma unroll 1
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t x[32];
-                            tm_ld32_nw(lanes + (u & 1) * 128 + 32 * i, x);
-                            tm_wait_ld();
-                            float y[32];
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(x[j]) * f;
-                            if (!p.whole) {
-                                if (r < rows) {  // rows side by side: whole lines
-#pragma unroll
-                                    for (int j = 0; j < 8; ++j) part[(8 * i + j) * 128] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-                                }
-                            } else if (write) {
-                                // through the warp's stage: whole lines again
-#pragma unroll
-                                for (int j = 0; j < L::ROW_PIECES; ++j) {
-                                    uint4 w;
-                                    if constexpr (F32)
-                                        w = make_uint4(__float_as_uint(y[4 * j]), __float_as_uint(y[4 * j + 1]), __float_as_uint(y[4 * j + 2]), __float_as_uint(y[4 * j + 3]));
-                                    else
-                                        w = make_uint4(bf16_pair(y[8 * j], y[8 * j + 1]), bf16_pair(y[8 * j + 2], y[8 * j + 3]), bf16_pair(y[8 * j + 4], y[8 * j + 5]),
-                                                       bf16_pair(y[8 * j + 6], y[8 * j + 7]));
-                                    *reinterpret_cast<uint4*>(stage + L::stage_at(lane, j)) = w;
-                                }
-                                __syncwarp();
-#pragma unroll
-                                for (int e = lane; e < 32 * L::ROW_PIECES; e += 32) {
-                                    const int in = e / L::ROW_PIECES, pc = e % L::ROW_PIECES, at = quarter * 32 + in;
-                                    if (at < rows)
-                                        *reinterpret_cast<uint4*>(to + ((size_t)(at >> 1) * NQ + (at & 1)) * HD + i * 32 + pc * (16 / (int)sizeof(T))) =
-                                            *reinterpret_cast<const uint4*>(stage + L::stage_at(in, pc));
-                                }
-                                __syncwarp();
-                            }
-                        }
-                        if (!p.whole && r < rows) part[(HD / 4) * 128] = make_float4(m, l, 0.f, 0.f);
-                        if (bad) {  // what was set aside is added to what stands there now
-                            __syncwarp();
-#pragma unroll 1
-                            for (u64 left = r < rows ? ((u64)p.bad[1] << 32 | p.bad[0]) & p.seen[r >> 1] : 0ull; left; left &= left - 1) {
-                                const bf16* const v = a.v + ((size_t)p.b * a.N + __ffsll(left) - 1) * a.kv_stride + p.g * HD;
-#pragma unroll 1
-                                for (int d = 0; d < HD; ++d) {
-                                    const float y = bf2f(v[d]);
-                                    T* const at = to + ((size_t)(r >> 1) * NQ + (r & 1)) * HD + d;
-                                    if (fabsf(y) <= 3.4028235e38f) continue;
-                                    if (!p.whole) reinterpret_cast<float*>(part + (d >> 2) * 128)[d & 3] += y;
-                                    else if (write) *at = (T)((float)*at + y);
-                                }
-                            }
-                        }
-                    }
-                }
                 tc_before();
                 __syncwarp();
                 if (lane == 0) arrive(&sh.o_empty[u & 1]);
             }
             if (!ok) break;
+            // the piece's end: code that runs this seldom comes from beyond the instruction cache, so it is kept short
+            if (p.t1 == p.tiles && !wait(&sh.seen_full[k % PIECES], piece_par(k))) break;
+            if (mine) {
+                T* const to = static_cast<T*>(a.out) + ((size_t)p.b * a.N * NQ + 2 * p.g) * HD;
+                T* const row = to + ((size_t)(r >> 1) * NQ + (r & 1)) * HD;
+                float4* const part = a.part + ((size_t)me * 2 + !p.first) * PART * 128 + r;
+                const auto four = [&](int i) {
+                    float4 x;
+                    halves(o[2 * i], x.x, x.y);
+                    halves(o[2 * i + 1], x.z, x.w);
+                    return x;
+                };
+                if (!p.whole) {
+                    if (r < rows) {  // rows side by side: whole lines
+#pragma unroll
+                        for (int i = 0; i < HD / 4; ++i) part[i * 128] = four(i);
+                        part[(HD / 4) * 128] = make_float4(m, l, 0.f, 0.f);
+                    }
+                } else if (p.ok) {
+                    const float f = l == 0.f ? 0.f : 1.f / l;
+                    const u64 f2 = pair(f, f), none = pair(-0.f, -0.f);
+#pragma unroll
+                    for (int i = 0; i < HD / 2; ++i) o[i] = fma2(o[i], f2, none);
+                    if constexpr (F32) {
+                        // 128 bytes of each row at a time through the warp's stage: whole lines (straight from the lanes, which hold a row each, 32
+                        // lines an instruction)
+                        unsigned char* const stage = smem + plan.stages<F32>() + quarter * L::STAGE;
+#pragma unroll
+                        for (int d0 = 0; d0 < HD; d0 += 32) {
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(stage + sw128_off(lane, i)) = four(d0 / 4 + i);
+                            __syncwarp();
+#pragma unroll 1
+                            for (int at = quarter * 32 + (lane >> 3); at < min(rows, quarter * 32 + 32); at += 4)
+                                *reinterpret_cast<float4*>(to + ((size_t)(at >> 1) * NQ + (at & 1)) * HD + d0 + (lane & 7) * 4) =
+                                    *reinterpret_cast<const float4*>(stage + sw128_off(at & 31, lane & 7));
+                        }
+                    } else if (r < rows) {
+#pragma unroll
+                        for (int i = 0; i < HD / 8; ++i) {
+                            const float4 x = four(2 * i), y = four(2 * i + 1);
+                            *reinterpret_cast<uint4*>(row + i * 8) = make_uint4(bf16_pair(x.x, x.y), bf16_pair(x.z, x.w), bf16_pair(y.x, y.y), bf16_pair(y.z, y.w));
+                        }
+                    }
+                }
+                if (p.bad[0] | p.bad[1]) {  // what was set aside is added to what stands there now
+                    __syncwarp();
+#pragma unroll 1
+                    for (u64 left = r < rows ? ((u64)p.bad[1] << 32 | p.bad[0]) & p.seen[r >> 1] : 0ull; left; left &= left - 1) {
+                        const bf16* const v = a.v + ((size_t)p.b * a.N + __ffsll(left) - 1) * a.kv_stride + p.g * HD;
+#pragma unroll 1
+                        for (int d = 0; d < HD; ++d) {
+                            const float y = bf2f(v[d]);
+                            if (fabsf(y) <= 3.4028235e38f) continue;
+                            if (!p.whole) reinterpret_cast<float*>(part + (d >> 2) * 128)[d & 3] += y;
+                            else if (p.ok) row[d] = (T)((float)row[d] + y);
+                        }
+                    }
+                }
+            }
             __syncwarp();
             if (lane == 0) arrive(&sh.piece_empty[k % PIECES]);
         }
@@ -938,21 +931,33 @@ __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
     if (r >= 2 * n || !in_order) return;
     const auto at = [&](int i) { return a.part + ((size_t)(s0 + i) * 2 + (i == 0 && head != it)) * PART * 128 + r; };
     float M = -INFINITY, l = 0.f;
-#pragma unroll 4
-    for (int i = 0; i <= more; ++i) M = fmaxf(M, at(i)[(HD / 4) * 128].x);
-    const float base = M == -INFINITY ? 0.f : M;
     float4 o[2] = {};
     const int d0 = (blockIdx.z * 4 + warp) * 2;
-#pragma unroll 4
-    for (int i = 0; i <= more; ++i) {
-        const float4* const p = at(i);
-        const float4 w = p[(HD / 4) * 128];
-        const float f = at_ex2(w.x - base);
-        l += f * w.y;
+#pragma unroll 1
+    for (int i0 = 0; i0 <= more; i0 += 8) {  // eight pieces at once
+        float4 w[8], x[8][2];
+        float top = M;
 #pragma unroll
-        for (int d = 0; d < 2; ++d) {
-            const float4 x = p[(d0 + d) * 128];
-            o[d].x += f * x.x; o[d].y += f * x.y; o[d].z += f * x.z; o[d].w += f * x.w;
+        for (int i = 0; i < 8; ++i) {
+            const float4* const p = at(min(i0 + i, more));
+            w[i] = p[(HD / 4) * 128];
+            x[i][0] = p[d0 * 128];
+            x[i][1] = p[(d0 + 1) * 128];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, w[i].x);
+        const float base = top == -INFINITY ? 0.f : top, f0 = at_ex2(M - base);
+        M = top;
+        l *= f0;
+#pragma unroll
+        for (int d = 0; d < 2; ++d) { o[d].x *= f0; o[d].y *= f0; o[d].z *= f0; o[d].w *= f0; }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i0 + i > more) break;
+            const float f = at_ex2(w[i].x - base);
+            l += f * w[i].y;
+#pragma unroll
+            for (int d = 0; d < 2; ++d) { o[d].x += f * x[i][d].x; o[d].y += f * x[i][d].y; o[d].z += f * x[i][d].z; o[d].w += f * x[i][d].w; }
         }
     }
     const float f = l == 0.f ? 0.f : 1.f / l;
