@@ -6,8 +6,10 @@
 // between rejections, and each costs one pass over the rows p and q that sums r. Children's indices lie above their
 // parent's, so one walk over the nodes in their order meets each accepted node's children in turn.
 //
-// Sums decide which whole number is the answer, so they are carried in 2^-60 as 64-bit whole numbers: exact for
-// probabilities from 2^-37 up (24 bits above 2^-60), cut off at 2^-60 below that, and the same in any order.
+// Sums decide which whole number is the answer, so they have to hold far more bits than a float. A thread adds its ids' rests in pairs of
+// floats (the sum, and what its roundings left; two ids an instruction), some 2^-46 of the sum; between threads they are whole numbers of
+// 2^-60, whose order does not matter. The ids around the answer are then gone through in whole numbers of 2^-60 alone: exact for
+// probabilities from 2^-37 up (24 bits above 2^-60), cut off at 2^-60 below that.
 #include <algorithm>
 
 #include "tree.cuh"
@@ -21,14 +23,15 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int THREADS = 512, NWARPS = THREADS / 32;
-constexpr int MAX_CLUSTER = 16;
+constexpr int MAX_CLUSTER = 16, BLOCKS_SM = 2;
 
 // a probability's bits, within 0 .. 1 (a NaN counts as 1, or as 0 where its sign is set)
 __device__ __forceinline__ uint32_t prob_bits(float x) { return (uint32_t)min(max(__float_as_int(x), 0), 0x3F800000); }
-// in units of 2^-60: the 24-bit mantissa stands at 2^(e - 150 + 60)
+// in units of 2^-60: the mantissa of 1 has its bit 60, that of others stands 127 - exponent lower
 __device__ __forceinline__ u64 fix60(float x) {
-    const uint32_t b = prob_bits(x), e = b >> 23, m = (b & 0x7FFFFFu) | 0x800000u;
-    return e >= 90 ? (u64)m << (e - 90) : e > 66 ? (u64)(m >> (90 - e)) : 0ull;
+    const uint32_t b = prob_bits(x), s = 127 - (b >> 23);
+    const u64 m = (u64)((b << 5 & 0x0FFFFFFFu) | 0x10000000u) << 32;
+    return s < 64 ? m >> s : 0ull;
 }
 // a * b / 2^s
 __device__ __forceinline__ u64 mul_shift(u64 a, u64 b, int s) { return (__umul64hi(a, b) << (64 - s)) | (a * b >> s); }
@@ -36,6 +39,99 @@ __device__ __forceinline__ u64 mul_shift(u64 a, u64 b, int s) { return (__umul64
 __device__ __forceinline__ u64 rest60(u64 p, u64 c, u64 q) {
     const u64 t = mul_shift(c, q, 58);
     return p > t ? p - t : 0ull;
+}
+
+// a pair of floats in units of 2^-60 (0 below 0 or where it is not a number, 8 at most)
+__device__ __forceinline__ u64 pair60(float s, float rest) {
+    const auto fix = [](float x) {  // 0 <= x < 16
+        const uint32_t b = __float_as_uint(x), e = b >> 23;
+        const u64 m = (b & 0x7FFFFFu) | 0x800000u;
+        return e >= 90 ? m << (e - 90) : e > 66 ? m >> (90 - e) : 0ull;
+    };
+    if (!(s > 0.f)) return 0ull;
+    const u64 a = fix(fminf(s, 8.f)), d = fix(fminf(fabsf(rest), 1.f));
+    return rest < 0.f ? (a > d ? a - d : 0ull) : a + d;
+}
+// two floats an instruction
+__device__ __forceinline__ u64 both(float a, float b) {
+    u64 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void halves(u64 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+    u64 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+    u64 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+    u64 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ u64 sub2(u64 a, u64 b) { return fma2(b, both(-1.f, -1.f), a); }
+// (s, rest) += x and the small y: the rounding of s + x goes to rest (Knuth's two-sum)
+__device__ __forceinline__ void gather2(u64& s, u64& rest, u64 x, u64 y) {
+    const u64 t = add2(s, x), z = sub2(t, s);
+    rest = add2(rest, add2(add2(sub2(s, sub2(t, z)), sub2(x, z)), y));
+    s = t;
+}
+// p - q of two ids where that is above 0: what rounds off p - min(p, q) is exact too
+__device__ __forceinline__ void rest2(u64& s, u64& rest, float p0, float p1, float q0, float q1) {
+    const u64 p = both(p0, p1), q = both(fminf(p0, q0), fminf(p1, q1)), d = sub2(p, q);
+    gather2(s, rest, d, sub2(sub2(p, d), q));
+}
+// p - c q, c = (hi, lo)
+__device__ __forceinline__ void rest2(u64& s, u64& rest, float p0, float p1, float q0, float q1, u64 hi, u64 lo) {
+    const u64 q = both(q0, q1), h = mul2(hi, q);
+    float h0, h1, l0, l1;
+    halves(h, h0, h1);
+    halves(fma2(lo, q, fma2(hi, q, mul2(h, both(-1.f, -1.f)))), l0, l1);  // what h rounded off, and lo q
+    if (p0 <= h0) { h0 = p0; l0 = 0.f; }
+    if (p1 <= h1) { h1 = p1; l1 = 0.f; }
+    const u64 p = both(p0, p1), b = both(h0, h1), d = sub2(p, b);
+    gather2(s, rest, d, sub2(sub2(sub2(p, d), b), both(l0, l1)));
+}
+// ids x .. x + 3 of a row of V, 0 for those outside
+__device__ __forceinline__ float4 four(const float* row, int x, int V) {
+    return make_float4(x >= 0 && x < V ? row[x] : 0.f, x >= -1 && x < V - 1 ? row[x + 1] : 0.f, x >= -2 && x < V - 2 ? row[x + 2] : 0.f,
+                       x < V - 3 ? row[x + 3] : 0.f);
+}
+// f(x, p[x .. x + 3], q[x .. x + 3]) for a lane's ids of first .. last - 1, whole and aligned where `vec` (q may be null)
+template <typename F>
+__device__ __forceinline__ void for_ids(const float* p, const float* q, int first, int last, int V, int lane, bool vec, F f) {
+    int x = first + lane * 4;
+    const auto guarded = [&] { f(x, four(p, x, V), q ? four(q, x, V) : make_float4(0.f, 0.f, 0.f, 0.f)); };
+    if (vec) {
+        if (first < 0) {
+            guarded();
+            x += 128;
+        }
+        const int end = min(last, V) - 4;
+#pragma unroll 4
+        for (; x <= end; x += 128)
+            f(x, *reinterpret_cast<const float4*>(p + x), q ? *reinterpret_cast<const float4*>(q + x) : make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+#pragma unroll 1
+    for (; x < last && x < V; x += 128) guarded();
+}
+// a whole number of 2^-s as a pair of floats
+__device__ __forceinline__ void pair_of(u64 v, float unit, float& hi, float& lo) {
+    hi = __ull2float_rn(v);
+    lo = (float)(long long)(v - __float2ull_rz(hi)) * unit;
+    hi *= unit;
+}
+// Whether u q Z < p - c q, for pairs of floats Z and c (48 bits; exact where Z is 1 and c is 0).
+__device__ __forceinline__ bool accepts(float u, float q, float zh, float zl, float p, float ch, float cl) {
+    const float a = u * q, a1 = fmaf(u, q, -a), b = a * zh, b1 = fmaf(a, zh, -b) + fmaf(a, zl, a1 * zh);
+    const float h = ch * q, l = fmaf(ch, q, -h) + cl * q;
+    const float t = p - h, z = t - p, e = (p - (t - z)) - (h + z) - l;  // t + e = p - c q
+    return (b - t) + (b1 - e) < 0.f;
 }
 
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
@@ -98,13 +194,15 @@ struct VerifyShared {
     u64 tot[2][MAX_CLUSTER];  // the blocks' sums of a pass, by its parity
     u64 chosen, gone;         // accepted nodes; rejected children of the current node (drafts that were not drawn)
     u64 c;                    // 2^-58
-    int n, cur, event, at;
+    float hi, lo;             // c
+    int found;                // the last id that is left where the whole numbers end before the sum does
+    int n, cur, event;
 };
 
 // grid (ctas, B), a cluster of ctas blocks for each sequence, 512 threads. Block r of a cluster owns the ids
 // [r, r + 1) * NWARPS * seg, warp w of it seg of them.
 template <bool DRAWN>
-__global__ void __launch_bounds__(THREADS) k_tree_verify(VerifyArgs a) {
+__global__ void __launch_bounds__(THREADS, BLOCKS_SM) k_tree_verify(VerifyArgs a) {
     __shared__ VerifyShared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y, rank = blockIdx.x;
     const bool many = a.ctas > 1;
@@ -134,66 +232,79 @@ __global__ void __launch_bounds__(THREADS) k_tree_verify(VerifyArgs a) {
             if (DRAWN) sh.q[j] = real ? __uint_as_float(prob_bits(a.draft[row * a.q_stride + x])) : 0.f;
         }
         if (lane == 0) {
+            if (rank == 0) a.next[b] = n ? 0 : -1;  // some id, whatever the numbers are
             sh.n = n;
-            sh.cur = 0;
-            sh.at = 1;
-            sh.chosen = 1;
-            sh.gone = 0;
-            sh.c = 0;
         }
     }
     __syncthreads();
     if (many) cluster_wait();
     const int n = sh.n;
     if (n == 0) {  // for all blocks of the cluster
-        if (rank == 0 && warp == 0) {
-            write_path(0, b, a.N, lane, a.n_accepted, a.path);
-            if (lane == 0) a.next[b] = -1;
-        }
+        if (rank == 0 && warp == 0) write_path(0, b, a.N, lane, a.n_accepted, a.path);
         return;
     }
     const float u_next = a.u_next[b];
-    const int first = (rank * NWARPS + warp) * a.seg, last = min(a.V, first + a.seg);  // ids of this warp
+    const int at0 = (rank * NWARPS + warp) * a.seg;  // ids of this warp, but for the row's alignment
     u64 Z = 0;
-    bool summed = false;  // the sums in sh are those of the rest as it stands
     int parity = 0;
+    // the walk's state, in warp 0: the nodes that have not been looked at, the children among them that may be accepted
+    u64 chosen = 1, gone = 0, ahead = ~1ull, c58 = 0;
+    int cur = 0;
+    bool summed = false;  // the block's sums are those of node cur's rest as it stands
+    const bool able[2] = {lane < n && sh.tok[lane] >= 0, lane + 32 < n && sh.tok[lane + 32] >= 0};
+    const int parent[2] = {lane < n ? sh.par[lane] : -1, lane + 32 < n ? sh.par[lane + 32] : -1};
     for (;;) {
-        if (tid == 0) {
-            // Z of the last pass is the mass that the next child is measured by; before the first, 1
-            double mass = DRAWN && sh.c ? (double)Z * 0x1p-60 : 1.0;
-            if (!DRAWN)
-                for (u64 g = sh.gone; g; g &= g - 1) mass -= (double)sh.p[__ffsll(g) - 1];
-            int j = sh.at, event = WALK_LAST;
-            for (; j < n; ++j) {
-                if (sh.par[j] != sh.cur || sh.tok[j] < 0) continue;
-                double r = (double)sh.p[j], price = (double)sh.u[j] * mass;
-                if (DRAWN) {
-                    if (sh.c) r -= (double)sh.c * 0x1p-58 * (double)sh.q[j];
-                    price *= (double)sh.q[j];
-                }
+        if (warp == 0) {
+            // the mass that the next child is measured by: Z of the pass before, 1 less the rejected ones, or 1
+            float zh = 1.f, zl = 0.f, ch = 0.f, cl = 0.f;
+            if (DRAWN && c58) {
+                pair_of(Z, 0x1p-60f, zh, zl);
+                pair_of(c58, 0x1p-58f, ch, cl);
+            }
+            int event = WALK_LAST;
+            u64 mass = 1ull << 60;
+            for (;;) {
+                u64 kids = (u64)__ballot_sync(0xffffffffu, able[1] && parent[1] == cur) << 32 | __ballot_sync(0xffffffffu, able[0] && parent[0] == cur);
+                kids &= ahead;
+                if (!kids) break;
+                const int j = __ffsll(kids) - 1;
+                ahead = ~0ull << j << 1;
+                const float p = sh.p[j];
                 bool again = false;  // a token that was rejected here before
-                if (!DRAWN)
-                    for (u64 g = sh.gone; g; g &= g - 1) again |= sh.tok[__ffsll(g) - 1] == sh.tok[j];
-                if (!again && price < r) {
-                    sh.chosen |= 1ull << j;
-                    sh.cur = j;
-                    sh.c = sh.gone = 0;
-                    mass = 1.0;
+                if (!DRAWN) {
+#pragma unroll 1
+                    for (u64 g = gone; g; g &= g - 1) again |= sh.tok[__ffsll(g) - 1] == sh.tok[j];
+                }
+                if (!again && accepts(sh.u[j], DRAWN ? sh.q[j] : 1.f, zh, zl, p, ch, cl)) {
+                    chosen |= 1ull << j;
+                    cur = j;
+                    c58 = gone = 0;
+                    mass = 1ull << 60;
+                    zh = 1.f;
+                    zl = ch = cl = 0.f;
                     summed = false;
                 } else if (DRAWN) {
-                    const u64 more = sh.c ? Z >> 2 : 1ull << 58;
-                    sh.c = sh.c + more < sh.c ? ~0ull : sh.c + more;
+                    const u64 more = c58 ? Z >> 2 : 1ull << 58;
+                    c58 = c58 + more < c58 ? ~0ull : c58 + more;
                     event = WALK_PASS;
-                    ++j;
                     break;
                 } else if (!again) {
-                    sh.gone |= 1ull << j;
-                    mass -= (double)sh.p[j];
+                    gone |= 1ull << j;
+                    mass -= min(mass, fix60(p));
+                    pair_of(mass, 0x1p-60f, zh, zl);
                 }
             }
-            sh.at = j;
             // the path's end: the sums are there where the last pass was of this node's rest
-            sh.event = event == WALK_LAST && summed ? WALK_LAST + 1 : event;
+            if (event == WALK_LAST && summed) event = WALK_LAST + 1;
+            summed = true;
+            if (lane == 0) {
+                pair_of(c58, 0x1p-58f, sh.hi, sh.lo);
+                sh.c = c58;
+                sh.chosen = chosen;
+                sh.gone = gone;
+                sh.cur = cur;
+                sh.event = event;
+            }
         }
         __syncthreads();
         const int event = sh.event;
@@ -203,25 +314,36 @@ __global__ void __launch_bounds__(THREADS) k_tree_verify(VerifyArgs a) {
         const size_t row = (size_t)b * a.N + sh.cur;
         const float* const p = a.target + row * a.p_stride;
         const float* const q = DRAWN ? a.draft + row * a.q_stride : nullptr;
-        u64 sum = 0;
+        // ids from a whole 16 bytes of both rows on
+        const bool vec = !DRAWN || (((uintptr_t)p ^ (uintptr_t)q) & 15) == 0;
+        const int first = at0 - (vec ? (int)((uintptr_t)p >> 2 & 3) : 0), last = first + a.seg;
+        u64 s = 0, rest = 0;
         if (!DRAWN || c == 0) {
-#pragma unroll 8
-            for (int x = first + lane; x < last; x += 32) sum += fix60(p[x]);
+            for_ids(p, nullptr, first, last, a.V, lane, vec, [&](int, float4 f, float4) {
+                gather2(s, rest, both(f.x, f.y), 0ull);
+                gather2(s, rest, both(f.z, f.w), 0ull);
+            });
         } else if (c == 1ull << 58) {
-#pragma unroll 8
-            for (int x = first + lane; x < last; x += 32) {
-                const u64 f = fix60(p[x]), g = fix60(q[x]);
-                sum += f > g ? f - g : 0ull;
-            }
+            for_ids(p, q, first, last, a.V, lane, vec, [&](int, float4 f, float4 g) {
+                rest2(s, rest, f.x, f.y, g.x, g.y);
+                rest2(s, rest, f.z, f.w, g.z, g.w);
+            });
         } else {
-#pragma unroll 4
-            for (int x = first + lane; x < last; x += 32) sum += rest60(fix60(p[x]), c, fix60(q[x]));
+            const u64 hi = both(sh.hi, sh.hi), lo = both(sh.lo, sh.lo);
+            for_ids(p, q, first, last, a.V, lane, vec, [&](int, float4 f, float4 g) {
+                rest2(s, rest, f.x, f.y, g.x, g.y, hi, lo);
+                rest2(s, rest, f.z, f.w, g.z, g.w, hi, lo);
+            });
         }
+        float s0, s1, r0, r1;
+        halves(s, s0, s1);
+        halves(rest, r0, r1);
+        u64 sum = pair60(s0, r0) + pair60(s1, r1);
         sum = warp_sum64(sum);
         if (!DRAWN && lane == 0) {  // less the rejected tokens, each once
             for (u64 g = sh.gone; g; g &= g - 1) {
                 const int j = __ffsll(g) - 1, x = sh.tok[j];
-                if (x >= first && x < last) sum -= fix60(sh.p[j]);
+                if (x >= first && x < last) sum -= min(sum, fix60(sh.p[j]));
             }
         }
         if (lane == 0) sh.wsum[warp] = sum;
@@ -240,7 +362,6 @@ __global__ void __launch_bounds__(THREADS) k_tree_verify(VerifyArgs a) {
             __syncthreads();
         }
         parity ^= 1;
-        summed = true;
         if (event == WALK_LAST) break;
     }
     // the next token
@@ -257,38 +378,72 @@ __global__ void __launch_bounds__(THREADS) k_tree_verify(VerifyArgs a) {
             if (t < sh.tot[parity][i]) return;  // in a block before this one
             t -= sh.tot[parity][i];
         }
-        for (int i = 0; i < warp; ++i) {
-            if (t < sh.wsum[i]) return;
-            t -= sh.wsum[i];
+        // in this block: the warp whose ids it lies among, which all warps search together, 4 ids a thread at a time
+        u64 upto = lane < NWARPS ? sh.wsum[lane] : 0ull;
+        const u64 own = upto;
+#pragma unroll
+        for (int o = 1; o < NWARPS; o <<= 1) {
+            const u64 w = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += w;
         }
-        if (t >= sh.wsum[warp]) return;
-        for (int x0 = first; x0 < last; x0 += 32) {
-            const int x = x0 + lane;
-            u64 r = x < last ? fix60(p[x]) : 0ull;
-            if (DRAWN) {
-                if (c && x < last) r = rest60(r, c, fix60(q[x]));
-            } else {
-                for (u64 g = sh.gone; g; g &= g - 1)
-                    if (sh.tok[__ffsll(g) - 1] == x) r = 0;
+        const uint32_t over = __ballot_sync(0xffffffffu, lane < NWARPS && upto > t);
+        if (!over) return;  // in a block behind this one
+        const bool vec = !DRAWN || (((uintptr_t)p ^ (uintptr_t)q) & 15) == 0;
+        const int in = __ffs(over) - 1, from = (rank * NWARPS + in) * a.seg - (vec ? (int)((uintptr_t)p >> 2 & 3) : 0), to = min(a.V, from + a.seg);
+        t -= __shfl_sync(0xffffffffu, upto - own, in);
+        int seen = max(from, 0);  // of this thread's ids the last one that is left
+        for (int x0 = from; x0 < to; x0 += THREADS * 4) {
+            u64 r[4], mine = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int x = x0 + tid * 4 + i;
+                r[i] = x >= 0 && x < to ? fix60(p[x]) : 0ull;
+                if (DRAWN) {
+                    if (c && x >= 0 && x < to) r[i] = rest60(r[i], c, fix60(q[x]));
+                } else {
+                    for (u64 g = sh.gone; g; g &= g - 1)
+                        if (sh.tok[__ffsll(g) - 1] == x) r[i] = 0;
+                }
+                if (r[i]) seen = x;
+                mine += r[i];
             }
-            u64 upto = r;
+            u64 incl = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const u64 w = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += w;
+                const u64 w = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += w;
             }
-            const uint32_t over = __ballot_sync(0xffffffffu, upto > t);
-            if (over) {
-                if (lane == 0) a.next[b] = x0 + __ffs(over) - 1;
-                return;
+            __syncthreads();
+            if (lane == 31) sh.wsum[warp] = incl;
+            __syncthreads();
+            u64 all = lane < NWARPS ? sh.wsum[lane] : 0ull;
+            const u64 before_me = all;
+#pragma unroll
+            for (int o = 1; o < NWARPS; o <<= 1) {
+                const u64 w = __shfl_up_sync(0xffffffffu, all, o);
+                if (lane >= o) all += w;
             }
-            t -= __shfl_sync(0xffffffffu, upto, 31);
+            u64 at = __shfl_sync(0xffffffffu, all - before_me, warp) + incl - mine;
+            const u64 total = __shfl_sync(0xffffffffu, all, NWARPS - 1);
+            if (t >= at && t < at + mine) {
+                int i = 0;
+                while (t >= at + r[i]) at += r[i++];
+                a.next[b] = x0 + tid * 4 + i;
+            }
+            if (t < total) return;
+            t -= total;
         }
+        // the floats' sum ends 2^-46 behind the whole numbers': the last id
+        if (tid == 0) sh.found = 0;
+        __syncthreads();
+        atomicMax(&sh.found, seen);
+        __syncthreads();
+        if (tid == 0) a.next[b] = sh.found;
         return;
     }
     // nothing is left: the most probable token of p. Keys order by value, then by the lowest id
     u64 best = 0;
-    for (int x = first + lane; x < last; x += 32) best = max(best, (u64)prob_bits(p[x]) << 32 | (uint32_t)~x);
+    for (int x = at0 + lane; x < min(a.V, at0 + a.seg); x += 32) best = max(best, (u64)prob_bits(p[x]) << 32 | (uint32_t)~x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
     __syncthreads();
@@ -379,10 +534,11 @@ __global__ void __launch_bounds__(256) k_tree_commit(Pages c, CommitArgs a) {
     }
 }
 
-// Blocks of a sequence's cluster: one for each 4096 ids, as many as let all sequences run at once.
+// Blocks of a sequence's cluster: one for each 4096 ids, while all sequences' blocks run in two turns. 64 x 151676, 12 nodes: by 8 blocks
+// a sequence 36 us, 4 (one turn) 38, 16 (four) 59.
 int verify_ctas(int B, int V) {
     int n = 1;
-    while (n < MAX_CLUSTER && n * 4096 < V && 2 * n * B <= 4 * 152) n *= 2;
+    while (n < MAX_CLUSTER && n * 4096 < V && 2 * n * B <= 2 * BLOCKS_SM * 152) n *= 2;
     return n;
 }
 
@@ -398,7 +554,7 @@ TTS_API tts_bb_status tts_bb_tree_verify(int B, int N, int V, const int32_t* tok
         return TTS_BB_E_INVALID;
     if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
     const int ctas = verify_ctas(B, V);
-    const int seg = (int)(((long long)V + ctas * NWARPS * 32 - 1) / (ctas * NWARPS * 32)) * 32;
+    const int seg = (int)((V + 3ll + ctas * NWARPS * 128 - 1) / (ctas * NWARPS * 128)) * 128;  // and 3 ids that alignment skips
     const VerifyArgs a{tokens, parents, n_nodes, target, draft, u, u_next, target_stride, draft_stride, n_accepted, path, next_token, err,
                        N, V, ctas, seg};
     const auto go = [&](auto kernel, SmemState& state) {

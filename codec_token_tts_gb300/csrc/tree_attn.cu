@@ -24,6 +24,7 @@ struct TreeArgs {
     long long q_stride, kv_stride;
     const int32_t *parents, *n_nodes, *seqs, *kv_lens;
     int B, N, max_len;
+    int one;      // 1: a block a (sequence, KV head), none is cut
     void* out;
     int4* meta;   // [shares]: the first piece of each
     float4* part; // [shares][2][PART][128]
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(NT, 1)
         if (threadIdx.x == 0) {
             set_err(c.err, TTS_BB_TREE_ERR_TIMEOUT);
             pdl_wait();
-            a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+            if (!a.one) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
         }
         return;
     }
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(NT, 1)
         for (int i0 = 0; i0 < a.B && (turn == 0 || before * NKV <= first); i0 += NT) {
             const int i = i0 + tid;
             int row = 0, len = 0, nodes = 0;
-            const uint32_t n = i < a.B && sequence(c, a, i, turn == one_turn && me == 0, row, len, nodes) ? tiles_of(len) : 0;
+            const uint32_t n = i < a.B && sequence(c, a, i, turn == one_turn && me == 0, row, len, nodes) ? a.one ? 1 : tiles_of(len) : 0;
             uint32_t incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(NT, 1)
             if (one_turn) deal(before);
             if (turn && first >= mine * NKV && first < (mine + n) * NKV) {
                 sh.start[0] = i;
-                sh.start[1] = (int)(first - mine * NKV);
+                sh.start[1] = (int)(first - mine * NKV) * (a.one ? tiles_of(len) : 1);
                 sh.start[2] = row;
                 sh.start[3] = len;
                 sh.start[4] = nodes;
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(NT, 1)
     __syncthreads();
     tc_after();
     const uint32_t tmem = sh.tmem;
-    const uint32_t U = first < units ? min(share, units - first) : 0;  // this block's tiles
+    const uint32_t U = first >= units ? 0 : a.one ? tiles_of(sh.start[3]) : min(share, units - first);  // this block's tiles
     bool ok = true;
     const auto wait = [&](u64* bar, uint32_t parity) {  // by whole warps
         ok = wait_for(&sh.abort, bar, parity);
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(NT, 1)
             int t = 0, vs = 0;
             uint32_t vp = 0, k = ~0u;
             Piece* p = nullptr;
-            if (U == 0 && lane == 0) a.meta[me] = make_int4(-1, 0, 0, 0);
+            if (U == 0 && lane == 0 && !a.one) a.meta[me] = make_int4(-1, 0, 0, 0);
 #pragma unroll 1
             for (uint32_t u = 0; ok && u < U; ++u) {
                 if (!p) {
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(NT, 1)
                         p->ok = tree_ok;
                         arrive(&sh.seen_full[k % PIECES]);
                         // of the share's first piece: its (sequence, head), nodes, and whether it begins inside of that one; bit 2: in order
-                        if (k == 0) a.meta[me] = make_int4(p->b * NKV + p->g, p->n, (t > 0) | tree_ok << 2, 0);
+                        if (k == 0 && !a.one) a.meta[me] = make_int4(p->b * NKV + p->g, p->n, (t > 0) | tree_ok << 2, 0);
                     }
                 }
                 if (!wait(&sh.v_full[vs], vp)) break;
@@ -971,8 +972,13 @@ __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
     }
 }
 
-// Blocks of the launch: one an SM, or one a tile where there are fewer.
-int share_count(int B, int max_len) { return (int)std::min<long long>(SHARES, (long long)B * NKV * tiles_of(max_len)); }
+// Blocks of the launch: one an SM, or one a tile where there are fewer; few and short sequences are not cut, which saves the launch that
+// merges.
+constexpr int ONE_TILES = 8;
+bool one_block(int B, int max_len) { return B * NKV <= SHARES && tiles_of(max_len) <= ONE_TILES; }
+int share_count(int B, int max_len) {
+    return one_block(B, max_len) ? B * NKV : (int)std::min<long long>(SHARES, (long long)B * NKV * tiles_of(max_len));
+}
 constexpr size_t META_BYTES = (SHARES * sizeof(int4) + 255) / 256 * 256;
 // As many pages of K and V as fit behind the queries.
 template <bool F32>
@@ -988,7 +994,7 @@ Plan plan_of(int N) {
 
 TTS_API size_t tts_bb_tree_attention_workspace(int B, int N, int max_len) {
     if (!tree_ok(B, N) || max_len < 0 || max_len > (1 << 30) || (long long)B * max_len > (1ll << 33)) return 0;
-    return META_BYTES + (size_t)share_count(B, max_len) * 2 * PART * 128 * sizeof(float4);
+    return one_block(B, max_len) ? 0 : META_BYTES + (size_t)share_count(B, max_len) * 2 * PART * 128 * sizeof(float4);
 }
 
 TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int layer, int B, int N, const void* q, int type,
@@ -1002,7 +1008,8 @@ TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int la
         q_stride > (1ll << 38) || kv_stride > (1ll << 38) || max_len < 0 || max_len > (1 << 30) || (long long)B * max_len > (1ll << 33) ||
         (long long)max_len > (long long)cache->blocks_per_seq * KVB || (!seqs && B > cache->n_seqs) || !words_aligned(parents, n_nodes, seqs, kv_lens))
         return TTS_BB_E_INVALID;
-    if (!workspace || workspace_bytes < tts_bb_tree_attention_workspace(B, N, max_len) || !aligned16(workspace)) return TTS_BB_E_INVALID;
+    const size_t need = tts_bb_tree_attention_workspace(B, N, max_len);
+    if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return TTS_BB_E_INVALID;
     if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
     const Pages c = pages_of(cache, layer);
     CUtensorMap pool_map, k_map, v_map, q_map;
@@ -1011,7 +1018,7 @@ TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int la
         (type == TTS_BB_T_BF16 && !tc_make_map_heads(&q_map, q, B * N, NQ, q_stride, N)))
         return TTS_BB_E_CUDA;
     if (type != TTS_BB_T_BF16) q_map = k_map;  // not used
-    const TreeArgs a{q, static_cast<const bf16*>(v), q_stride, kv_stride, parents, n_nodes, seqs, kv_lens, B, N, max_len, out,
+    const TreeArgs a{q, static_cast<const bf16*>(v), q_stride, kv_stride, parents, n_nodes, seqs, kv_lens, B, N, max_len, one_block(B, max_len), out,
                      static_cast<int4*>(workspace), reinterpret_cast<float4*>(static_cast<char*>(workspace) + META_BYTES)};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int shares = share_count(B, max_len);
@@ -1029,7 +1036,7 @@ TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int la
         if (!regs) return;
         const Plan plan = plan_of<F32>(N);
         launch_pdl(k_tree_attn<F32>, shares, NT, plan.bytes<F32>(), st, pool_map, k_map, v_map, q_map, c, a, plan);
-        if (tiles_of(max_len) > 1)
+        if (!a.one && tiles_of(max_len) > 1)
             launch_pdl(k_tree_combine<std::conditional_t<F32, float, bf16>>, dim3(shares - 1, (2 * N + 31) / 32, 4), 128, 0, st, a, shares);
     };
     if (type == TTS_BB_T_F32) go(std::true_type{});

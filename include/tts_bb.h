@@ -700,16 +700,16 @@ tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int layer, int
  * most probable one of p, the lowest of them.
  *   tokens   int32 [B][N]; a drafted token outside 0..V-1 is no draw: never accepted, r stays
  *   target   fp32 [B * N] rows of V probabilities, target_stride elements apart (>= V): row b N + i holds the target's for
- *            the token behind node i. 0 <= p <= 1, each row's sum near 1 (others: some path of the tree and some next token in
- *            0..V-1; above 1 and NaN count as 1)
+ *            the token behind node i. 0 <= p <= 1, each row's sum near 1 (others, NaN among them: some path of the tree and some
+ *            next token in 0..V-1)
  *   draft    fp32, the same for the draft model, draft_stride apart: the distribution from which all children of node i were
  *            drawn, independently of each other; or NULL
  *   u        fp32 [B][N] in [0, 1): node j's number; u_next fp32 [B]
  *   n_accepted int32 [B]: nodes of the path, node 0 among them; 0 for padding and skipped sequences
  *   path     int32 [B][N]: its nodes, -1 behind the last;  next_token int32 [B]: -1 where n_accepted is 0
  *   err      device word, or NULL
- * Sums are carried in whole numbers of 2^-60, products in 64 bits or more: the answers are those of exact arithmetic but for ties
- * that close. V at most 2^30, fp32 and int32 arrays 4-byte aligned. */
+ * Sums and products carry 46 bits or more: the answers are those of exact arithmetic but where a number lies that close to
+ * a border. V at most 2^30, fp32 and int32 arrays 4-byte aligned. */
 tts_bb_status tts_bb_tree_verify(int B, int N, int V, const int32_t* tokens, const int32_t* parents, const int32_t* n_nodes,
                                  const float* target, int64_t target_stride, const float* draft, int64_t draft_stride,
                                  const float* u, const float* u_next, int32_t* n_accepted, int32_t* path,
