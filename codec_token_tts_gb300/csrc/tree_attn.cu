@@ -722,27 +722,26 @@ __global__ void __launch_bounds__(NT, 1)
                     if (tree && !wait(&sh.seen_full[k % PIECES], piece_par(k))) break;
                     keys = !there ? 0ull : tree ? (r < rows ? p.seen[r >> 1] : 0ull) : (1ull << valid) - 1;
                 }
-                const auto scores = [&](int chunk, uint32_t (&s)[32]) {
-                    tm_ld32_nw(at + chunk * 32, s);
-                    tm_wait_ld();
-                    if (special) {
-                        const uint32_t count = (uint32_t)(keys >> (chunk * 32));
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!(count >> i & 1)) s[i] = 0xFF800000u;  // -inf
-                    }
-                };
                 if (mine) {
                     tc_after();
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
                     for (int chunk = 0; chunk < 2; ++chunk) {
                         uint32_t s[32];
-                        scores(chunk, s);
+                        tm_ld32_nw(at + chunk * 32, s);
+                        tm_wait_ld();
+                        if (special) {  // and back: what follows is the same for all tiles
+                            const uint32_t count = (uint32_t)(keys >> (chunk * 32));
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(count >> i & 1)) s[i] = 0xFF800000u;  // -inf
+                            tm_st32(at + chunk * 32, s);
+                        }
 #pragma unroll
                         for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
                     }
                     m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 }
                 // the maximum so far, from the warp of the tile before (waited for at a new piece too: no warp is two tiles ahead)
                 if (u > 0) {
@@ -759,7 +758,8 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll 1
                     for (int chunk = 0; chunk < 2; ++chunk) {
                         uint32_t s[32], w[L::PPARTS][16];
-                        scores(chunk, s);
+                        tm_ld32_nw(at + chunk * 32, s);
+                        tm_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float x, y;
