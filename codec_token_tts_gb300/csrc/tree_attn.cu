@@ -51,10 +51,14 @@ struct Piece {
 template <bool F32>
 struct Lay {
     static constexpr int QPARTS = F32 ? 3 : 1, PPARTS = F32 ? 3 : 2, QBUFS = F32 ? 1 : 2;
-    // Regions of TMEM for a tile's scores (64 columns), where weights replace them: of 32 keys' 32 columns the first part of their
-    // weights takes 16, the second the others; the third stands behind. Values are loaded AHEAD tiles behind keys
-    static constexpr int REGIONS = F32 ? 2 : 4, REGION = F32 ? 128 : 64, AHEAD = F32 ? 1 : 2;
-    static __device__ __forceinline__ uint32_t part_at(int part, int chunk) { return part < 2 ? chunk * 32 + part * 16 : KVB + chunk * 16; }
+    // Regions of 64 columns of TMEM for a tile's scores, where weights replace them: of 32 keys' 32 columns the first part of their weights
+    // takes 16, the second the others. The third part of tile t has 32 columns of its own by t & 1, behind three regions (two regions of
+    // 96, which need no wait for them: 2500 cycles a tile, 3 regions 2100). Values are loaded AHEAD tiles behind keys
+    static constexpr int REGIONS = F32 ? 3 : 4, AHEAD = 2;
+    // the column of a part of 32 keys' weights of tile u
+    static __device__ __forceinline__ uint32_t part_at(uint32_t u, int part, int chunk) {
+        return part < 2 ? u % REGIONS * KVB + chunk * 32 + part * 16 : 192 + (u & 1) * 32 + chunk * 16;
+    }
     static constexpr int STAGE = F32 ? 4096 : 0;  // of each warp that writes sums: 32 rows of 128 bytes
 };
 // the last two beside the rows that few nodes leave empty
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(NT, 1)
                 ok = wait_for(&sh.abort, &sh.k_full[ks], kp, &sh.w_empty[region], (u / L::REGIONS - 1) & 1u);
                 if (!ok) break;
                 tc_after();
-                const uint32_t d = tmem + region * L::REGION, k1 = k0 + ks * (PAGE_BYTES >> 4), q1 = q0 + (F32 ? 0u : (k & 1) * q_buf);
+                const uint32_t d = tmem + region * KVB, k1 = k0 + ks * (PAGE_BYTES >> 4), q1 = q0 + (F32 ? 0u : (k & 1) * q_buf);
                 --left;
                 if (leader) {
 #pragma unroll
@@ -547,7 +551,7 @@ __global__ void __launch_bounds__(NT, 1)
                 ok = wait_for(&sh.abort, &sh.p_full[region], (u / L::REGIONS) & 1u, &sh.v_ready[vs], vp, &sh.o_empty[u & 1], ((u >> 1) - 1) & 1u);
                 if (!ok) break;
                 tc_after();
-                const uint32_t w = tmem + region * L::REGION, d = tmem + 256 + (u & 1) * 128, v1 = v0 + vs * (PAGE_BYTES >> 4);
+                const uint32_t d = tmem + 256 + (u & 1) * 128, v1 = v0 + vs * (PAGE_BYTES >> 4);
                 ++t;
                 --left;
                 if (leader) {
@@ -555,7 +559,7 @@ __global__ void __launch_bounds__(NT, 1)
                     for (int part = L::PPARTS - 1; part >= 0; --part)
 #pragma unroll
                         for (int kk = 0; kk < KVB / 16; ++kk)  // 8 columns of weights
-                            if (kk < steps) mma_ts(d, w + L::part_at(part, kk >> 1) + (kk & 1) * 8, v1 + (uint32_t)(kk * 2048 / 16), IDESC_PV, part < L::PPARTS - 1 || kk > 0);
+                            if (kk < steps) mma_ts(d, tmem + L::part_at(u, part, kk >> 1) + (kk & 1) * 8, v1 + (uint32_t)(kk * 2048 / 16), IDESC_PV, part < L::PPARTS - 1 || kk > 0);
                     arrive(&sh.o_full[u & 1]);
                     at_commit((uint64_t*)&sh.o_full[u & 1]);
                     at_commit((uint64_t*)&sh.v_empty[vs]);
@@ -710,7 +714,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll 1
             for (int j = (int)(u0 ^ group) & 1; j < nt; j += 2) {
                 const int t = p.t0 + j;
-                const uint32_t u = u0 + j, region = u % L::REGIONS, at = lanes + region * L::REGION;
+                const uint32_t u = u0 + j, region = u % L::REGIONS, at = lanes + region * KVB;
                 if (!wait(&sh.s_full[region], (u / L::REGIONS) & 1u)) break;
                 float m = -INFINITY;
                 // the keys that count, a bit each, where not all do
@@ -755,6 +759,8 @@ __global__ void __launch_bounds__(NT, 1)
                     const float now = m * cs, base = m == -INFINITY ? 0.f : now;
                     const u64 cs2 = pair(cs, cs), base2 = pair(-base, -base), minus = pair(-1.f, -1.f);
                     u64 sum[2] = {0, 0};
+                    // the third parts' columns were taken by the product of this group's tile before
+                    if (F32 && u >= 2 && !wait(&sh.w_empty[(u - 2) % L::REGIONS], ((u - 2) / L::REGIONS) & 1u)) break;
 #pragma unroll 1
                     for (int chunk = 0; chunk < 2; ++chunk) {
                         uint32_t s[32], w[L::PPARTS][16];
@@ -775,7 +781,7 @@ __global__ void __launch_bounds__(NT, 1)
                             }
                         }
 #pragma unroll
-                        for (int part = 0; part < L::PPARTS; ++part) tm_st16(at + L::part_at(part, chunk), w[part]);
+                        for (int part = 0; part < L::PPARTS; ++part) tm_st16(lanes + L::part_at(u, part, chunk), w[part]);
                     }
                     float x, y, z, v;
                     halves(sum[0], x, y);
