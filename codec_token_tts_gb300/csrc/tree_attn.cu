@@ -32,7 +32,7 @@ struct TreeArgs {
 
 constexpr int PAGE_BYTES = KVB * HD * 2;  // K or V of a page and head
 constexpr int PART = HD / 4 + 1;          // a row's 128 sums by four, then its reference and weight: rows side by side
-constexpr int SHARES = 152;               // a block an SM
+constexpr int SHARES = 152 / NKV;         // times 8 blocks: one an SM
 
 // A share's work: a piece of the tiles (a page each) of one (sequence, KV head), the last of which is the tree.
 struct Piece {
@@ -242,7 +242,8 @@ __device__ __forceinline__ bool ancestors(const int32_t* parents, int n, int lan
 
 __device__ __forceinline__ bool finite16(uint32_t half) { return (half & 0x7F80u) != 0x7F80u; }
 
-// grid: the shares, 512 threads. All tiles of all (sequence, KV head) are one line, cut into equal shares. Warp 12 deals the pieces of
+// grid: 8 blocks a share, 512 threads. The tiles of all sequences are one line, cut into equal shares, and the 8 KV heads walk it side
+// by side, a block each: what they read at a time lies together. Warp 12 deals the pieces of
 // its share and loads pages (and bf16 queries) by TMA, 13 finds the nodes' ancestors and makes values safe to be multiplied by 0, 14 and
 // 15 issue the products: scores S = Q K^T of a tile, and sums O = P V of one before (two warps, since an issuer waits for
 // its products: one took turns at it, and the tensor cores waited meanwhile). Warps 0 .. 7 turn scores into weights (a thread a row),
@@ -298,16 +299,17 @@ __global__ void __launch_bounds__(NT, 1)
     // where the share begins: the sequences' tiles, one a thread at a time; the sum of all first, where one turn is not enough
     uint32_t before = 0, first = 0, units = 0, share = 0;
     const bool one_turn = a.B <= NT;
+    const uint32_t shares = gridDim.x / NKV;
     const auto deal = [&](uint32_t tiles) {
-        units = tiles * NKV;
-        share = (units + gridDim.x - 1) / gridDim.x;
-        first = me * share;
+        units = tiles;
+        share = (units + shares - 1) / shares;
+        first = me / NKV * share;
     };
 #pragma unroll 1
     for (int turn = one_turn; turn < 2; ++turn) {
         before = 0;
 #pragma unroll 1
-        for (int i0 = 0; i0 < a.B && (turn == 0 || before * NKV <= first); i0 += NT) {
+        for (int i0 = 0; i0 < a.B && (turn == 0 || before <= first); i0 += NT) {
             const int i = i0 + tid;
             int row = 0, len = 0, nodes = 0;
             const uint32_t n = i < a.B && sequence(c, a, i, turn == one_turn && me == 0, row, len, nodes) ? a.one ? 1 : tiles_of(len) : 0;
@@ -329,9 +331,9 @@ __global__ void __launch_bounds__(NT, 1)
             const uint32_t mine = before + __shfl_sync(0xffffffffu, upto - of, warp) + incl - n;
             before += __shfl_sync(0xffffffffu, upto, WARPS - 1);
             if (one_turn) deal(before);
-            if (turn && first >= mine * NKV && first < (mine + n) * NKV) {
+            if (turn && first >= mine && first < mine + n) {
                 sh.start[0] = i;
-                sh.start[1] = (int)(first - mine * NKV) * (a.one ? tiles_of(len) : 1);
+                sh.start[1] = (int)(first - mine);
                 sh.start[2] = row;
                 sh.start[3] = len;
                 sh.start[4] = nodes;
@@ -372,17 +374,17 @@ __global__ void __launch_bounds__(NT, 1)
             uint32_t kk = ~0u, vk = ~0u;
             int kt = 0, vt = 0, from = 0;
             int here = 0, next = 0;  // pages of the keys' tiles from + lane and from + 32 + lane
-            // the sequence, of its 8 heads' tiles the next one, and what of the share has not been dealt
+            // the sequence, its next tile, and what of the share has not been dealt
             int b = sh.start[0], at = sh.start[1], row = sh.start[2], len = sh.start[3], n = sh.start[4];
             uint32_t left = U;
             // the next piece (b < 0 where nothing is left), in its place once every warp is done with the one before
             const auto deal_piece = [&](uint32_t k) {
                 Piece& p = sh.piece[k % PIECES];
                 if (k >= PIECES && !wait(&sh.piece_empty[k % PIECES], (k / PIECES - 1) & 1u)) return false;
-                const int nt = tiles_of(len), g = at / nt, t0 = at - g * nt, t1 = (int)min((uint32_t)nt, t0 + left);
+                const int nt = tiles_of(len), t0 = at, t1 = (int)min((uint32_t)nt, t0 + left);
                 if (lane == 0) {
                     p.b = left ? b : -1;
-                    p.g = g;
+                    p.g = me % NKV;
                     p.row = row;
                     p.len = len;
                     p.n = n;
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(NT, 1)
                 if (left == 0) return true;
                 left -= t1 - t0;
                 at += t1 - t0;
-                if (at == nt * NKV && left > 0) {
+                if (at == nt && left > 0) {
                     at = 0;
                     do ++b; while (b < a.B && !sequence(c, a, b, false, row, len, n));
                     if (b >= a.B) left = 0;
@@ -593,8 +595,8 @@ __global__ void __launch_bounds__(NT, 1)
                     if (lane == 0) {
                         p->ok = tree_ok;
                         arrive(&sh.seen_full[k % PIECES]);
-                        // of the share's first piece: its (sequence, head), nodes, and whether it begins inside of that one; bit 2: in order
-                        if (k == 0 && !a.one) a.meta[me] = make_int4(p->b * NKV + p->g, p->n, (t > 0) | tree_ok << 2, 0);
+                        // of the share's first piece: its sequence, nodes, and whether it begins inside of that; bit 2: in order
+                        if (k == 0 && !a.one) a.meta[me] = make_int4(p->b, p->n, (t > 0) | tree_ok << 2, 0);
                     }
                 }
                 if (!wait(&sh.v_full[vs], vp)) break;
@@ -918,15 +920,15 @@ __global__ void __launch_bounds__(NT, 1)
     }
 }
 
-// grid (shares - 1, rows / 32, 4), 128 threads: the pieces of the (sequence, KV head) that the end of share blockIdx.x cuts first. A lane
+// grid (8 (shares - 1), rows / 32, 4), 128 threads: the pieces of the (sequence, KV head) that the end of a share cuts first. A lane
 // a row, a warp 8 of the 128 dims. A share's first piece stands in its place 0, the piece that ends it in place 1.
 template <typename T>
 __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
     pdl_wait();
     pdl_trigger();
-    const int s0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y * 32 + lane;
-    // the first pieces of this share and of those behind it: at most 20 shares hold parts of one of 8 or more (sequence, head)
-    const int4 meta = s0 + lane < shares ? a.meta[s0 + lane] : make_int4(-1, 0, 0, 0);
+    const int s0 = blockIdx.x / NKV, g = blockIdx.x % NKV, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y * 32 + lane;
+    // the first pieces of this share and of those behind it: fewer than 32
+    const int4 meta = s0 + lane < shares ? a.meta[(s0 + lane) * NKV + g] : make_int4(-1, 0, 0, 0);
     const int it = __shfl_sync(0xffffffffu, meta.x, 1);
     const uint32_t goes_on = __ballot_sync(0xffffffffu, lane > 0 && meta.x == it && (meta.z & 1));
     if (it < 0 || !(goes_on & 2)) return;  // the share behind begins with a new one
@@ -936,7 +938,7 @@ __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
     const int n = __shfl_sync(0xffffffffu, meta.y, 1);
     const bool in_order = __shfl_sync(0xffffffffu, meta.z, more) >> 2 & 1;  // the last piece holds the tree
     if (r >= 2 * n || !in_order) return;
-    const auto at = [&](int i) { return a.part + ((size_t)(s0 + i) * 2 + (i == 0 && head != it)) * PART * 128 + r; };
+    const auto at = [&](int i) { return a.part + ((size_t)((s0 + i) * NKV + g) * 2 + (i == 0 && head != it)) * PART * 128 + r; };
     float M = -INFINITY, l = 0.f;
     float4 o[2] = {};
     const int d0 = (blockIdx.z * 4 + warp) * 2;
@@ -968,7 +970,7 @@ __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
         }
     }
     const float f = l == 0.f ? 0.f : 1.f / l;
-    T* const to = static_cast<T*>(a.out) + (((size_t)(it / NKV) * a.N + (r >> 1)) * NQ + 2 * (it % NKV) + (r & 1)) * HD + d0 * 4;
+    T* const to = static_cast<T*>(a.out) + (((size_t)it * a.N + (r >> 1)) * NQ + 2 * g + (r & 1)) * HD + d0 * 4;
     if constexpr (std::is_same_v<T, float>) {
 #pragma unroll
         for (int d = 0; d < 2; ++d) *reinterpret_cast<float4*>(to + d * 4) = make_float4(o[d].x * f, o[d].y * f, o[d].z * f, o[d].w * f);
@@ -978,14 +980,12 @@ __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
     }
 }
 
-// Blocks of the launch: one an SM, or one a tile where there are fewer; few and short sequences are not cut, which saves the launch that
-// merges.
+// Shares of the launch: 8 blocks each, one an SM in all, or a tile a share where there are fewer; few and short sequences are not cut,
+// which saves the launch that merges: 1 x 333 keys 9.5 us (and 3 of the host's), in shares 10.1; 1 x 1000 15.5 and 14.2.
 constexpr int ONE_TILES = 8;
-bool one_block(int B, int max_len) { return B * NKV <= SHARES && tiles_of(max_len) <= ONE_TILES; }
-int share_count(int B, int max_len) {
-    return one_block(B, max_len) ? B * NKV : (int)std::min<long long>(SHARES, (long long)B * NKV * tiles_of(max_len));
-}
-constexpr size_t META_BYTES = (SHARES * sizeof(int4) + 255) / 256 * 256;
+bool one_block(int B, int max_len) { return B <= SHARES && tiles_of(max_len) <= ONE_TILES; }
+int share_count(int B, int max_len) { return one_block(B, max_len) ? B : (int)std::min<long long>(SHARES, (long long)B * tiles_of(max_len)); }
+constexpr size_t META_BYTES = (SHARES * NKV * sizeof(int4) + 255) / 256 * 256;
 // As many pages of K and V as fit behind the queries.
 template <bool F32>
 Plan plan_of(int N) {
@@ -1000,7 +1000,7 @@ Plan plan_of(int N) {
 
 TTS_API size_t tts_bb_tree_attention_workspace(int B, int N, int max_len) {
     if (!tree_ok(B, N) || max_len < 0 || max_len > (1 << 30) || (long long)B * max_len > (1ll << 33)) return 0;
-    return one_block(B, max_len) ? 0 : META_BYTES + (size_t)share_count(B, max_len) * 2 * PART * 128 * sizeof(float4);
+    return one_block(B, max_len) ? 0 : META_BYTES + (size_t)share_count(B, max_len) * NKV * 2 * PART * 128 * sizeof(float4);
 }
 
 TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int layer, int B, int N, const void* q, int type,
@@ -1041,9 +1041,9 @@ TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int la
         regs = enough;
         if (!regs) return;
         const Plan plan = plan_of<F32>(N);
-        launch_pdl(k_tree_attn<F32>, shares, NT, plan.bytes<F32>(), st, pool_map, k_map, v_map, q_map, c, a, plan);
-        if (!a.one && tiles_of(max_len) > 1)
-            launch_pdl(k_tree_combine<std::conditional_t<F32, float, bf16>>, dim3(shares - 1, (2 * N + 31) / 32, 4), 128, 0, st, a, shares);
+        launch_pdl(k_tree_attn<F32>, shares * NKV, NT, plan.bytes<F32>(), st, pool_map, k_map, v_map, q_map, c, a, plan);
+        if (shares > 1 && !a.one && tiles_of(max_len) > 1)
+            launch_pdl(k_tree_combine<std::conditional_t<F32, float, bf16>>, dim3((shares - 1) * NKV, (2 * N + 31) / 32, 4), 128, 0, st, a, shares);
     };
     if (type == TTS_BB_T_F32) go(std::true_type{});
     else go(std::false_type{});
