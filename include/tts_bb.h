@@ -676,14 +676,14 @@ typedef struct {
  *            all rows of q, k, v, out 16-byte aligned; k, v and q may be parts of wider rows
  *   seqs     int32 [B], the cache row of each sequence (negative: padding), or NULL: sequence b reads row b
  *   kv_lens  int32 [B], the sequence's cached keys, 0 .. max_len
- *   max_len  an upper bound of kv_lens (host), 0 .. 64 * blocks_per_seq, at most 2^30; it sets the split and the workspace,
- *            a tight one is faster
- *   workspace at least tts_bb_tree_attention_workspace(B, N, max_len) bytes, 16-byte aligned (NULL where that is 0); written
- *            before it is read, not shared by calls that overlap
- * Rows of out of padding and of skipped sequences are left as they were; keys behind a page out of range are left out of the
- * sums. What masked keys, places behind a sequence's keys and padding nodes hold does not matter, NaN and infinities among it. A value
- * that is not finite among a row's own keys makes that row's numbers of its column (or the row) not finite. Results do
- * not depend on the order in which blocks of the launch run. */
+ *   max_len  an upper bound of kv_lens (host), 0 .. 64 * blocks_per_seq, at most 2^30, B * max_len at most 2^33; it sets the
+ *            split and the workspace, a tight one is faster
+ *   workspace at least tts_bb_tree_attention_workspace(B, N, max_len) bytes (20.6 MB at most), 16-byte aligned (NULL where that
+ *            is 0); written before it is read, not shared by calls that overlap
+ * out and the workspace overlap no input. Rows of out of padding and of skipped sequences are left as they were; keys behind a page out
+ * of range are left out of the sums. What masked keys, places behind a sequence's keys and padding nodes hold does not matter, NaN and
+ * infinities among it. Where the formula gives NaN or an infinity the number is one of the two; queries and keys of magnitudes up
+ * to 1e18 and values up to 1e30 leave fp32 room for the sums. Results do not depend on the order in which blocks of the launch run. */
 size_t tts_bb_tree_attention_workspace(int B, int N, int max_len);
 tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int layer, int B, int N, const void* q, int type,
                                     int64_t q_stride, const void* k, const void* v, int64_t kv_stride,

@@ -136,6 +136,39 @@ def test_attention_of_many_sequences(io):
 
 
 @IO
+def test_attention_of_more_sequences_than_threads(io):
+    """Lengths are summed in several turns of a block; every seventh sequence is padding or out of range."""
+    rng = np.random.default_rng(51)
+    B = 1100
+    c = Case(52, [int(n) for n in rng.integers(0, 3, B) * rng.integers(1, 70, B)], 2, io, nodes=[int(n) for n in rng.integers(0, 3, B)])
+    seqs = np.arange(B)
+    seqs[::7] = np.where(np.arange(0, B, 7) % 2, -1, B)
+    out = c.run(seqs=seqs, max_len=200 if c.bps * BLK >= 200 else c.bps * BLK)
+    some = set(range(0, B, 7))
+    c.check(out, skip=some)
+    assert int(c.err) == tb().TREE_ERR_RANGE
+
+
+@IO
+def test_attention_and_commit_beyond_4_gigabytes(io):
+    """Blocks whose bytes start above 2^32, of a pool whose other blocks are NaN."""
+    c = Case(53, [100, 700], 5, io)
+    far = 17000
+    pool = torch.full((1, far + c.n_blocks, 2, NKV, BLK, HD), NAN, dtype=torch.bfloat16, device="cuda")
+    pool[:, far:] = c.pool
+    c.pool, c.table, c.n_blocks = pool, c.table + far, far + c.n_blocks
+    c.check(c.run())
+    m = tb()
+    cache = m.KvCache(pool, dev(c.table[:, -1:]), c.err)
+    x = torch.randn(2 * 5, 1024, device="cuda").bfloat16()
+    m.tts_bb_tree_commit(cache, 2, 5, x, x, ints([[0, 3, -1, -1, -1], [4, -1, -1, -1, -1]]), ints([2, 1]), ints([62, 0]), stream=stream())
+    for b, pos, row in ((0, 62, 0), (0, 63, 3), (1, 0, 9)):
+        got = pool[0, int(c.table[b, -1]), :, :, pos].reshape(2, -1)
+        assert torch.equal(got[0], x[row]) and torch.equal(got[1], x[row])
+    assert int(c.err) == 0
+
+
+@IO
 def test_attention_split_over_a_long_cache(io):
     c = Case(7, [20000, 7], 3, io)
     c.check(c.run())
@@ -378,6 +411,24 @@ def test_verify_keeps_the_targets_distribution(drawn):
     assert (np.abs(counts - T * p) <= 5 * np.sqrt(T * p * (1 - p))).all(), (counts / T, p)
 
 
+def test_verify_rows_of_every_alignment():
+    """Rows that start at each of the four places of 16 bytes, the draft's like the target's or not."""
+    m = tb()
+    t = Trees(6, 12, 5, 5003, True)
+    want = t.run()
+    for dp in range(4):
+        for dq in (dp, (dp + 1) % 4):
+            def at(x, off):
+                buf = torch.full((t.B * t.N, t.V + 5), NAN, device="cuda")
+                buf[:, off : off + t.V] = dev(x)
+                return buf[:, off : off + t.V]
+            count, nxt = (torch.zeros(t.B, dtype=torch.int32, device="cuda") for _ in range(2))
+            path = torch.zeros(t.B, t.N, dtype=torch.int32, device="cuda")
+            m.tts_bb_tree_verify(t.B, t.N, t.V, ints(t.tokens), ints(t.parents), at(t.p, dp), dev(t.u), dev(t.un), count, path, nxt, draft=at(t.q, dq),
+                                 stream=stream())
+            assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip((count, path, nxt), want))
+
+
 def test_verify_borders():
     """Numbers of 0 and next to 1, mass at one id, nothing left, equal rows, tokens out of range, the same token twice."""
     N, V = 4, 40
@@ -443,6 +494,39 @@ def test_verify_reports_what_it_skips(drawn):
     t.check()
     a, b = t.run(), t.run(nodes=False)
     assert all(np.array_equal(x, y) for x, y in zip(a, b))
+
+
+@DRAWN
+def test_verify_in_a_graph_and_two_at_once(drawn):
+    m = tb()
+    t = Trees(8, 20, 8, 9000, drawn)
+    want = t.run()
+    a = [ints(t.tokens), ints(t.parents), dev(t.p), dev(t.u), dev(t.un)]
+    q = dev(t.q) if drawn else None
+    outs = [[torch.zeros(t.B, dtype=torch.int32, device="cuda"), torch.zeros(t.B, t.N, dtype=torch.int32, device="cuda"),
+             torch.zeros(t.B, dtype=torch.int32, device="cuda")] for _ in range(2)]
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    call = lambda o, st: m.tts_bb_tree_verify(t.B, t.N, t.V, *a, *o, draft=q, stream=st)
+    for _ in range(5):
+        for o, s in zip(outs, sides):
+            call(o, s.cuda_stream)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(np.array_equal(x.cpu().numpy(), y) for x, y in zip(o, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(sides[0]), torch.cuda.graph(g, stream=sides[0]):
+        call(outs[0], torch.cuda.current_stream().cuda_stream)
+    for x in outs[0]:
+        x.fill_(-9)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(np.array_equal(x.cpu().numpy(), y) for x, y in zip(outs[0], want))
+    t.u = np.random.default_rng(9).random(t.u.shape).astype(np.float32)
+    a[3].copy_(dev(t.u))
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(np.array_equal(x.cpu().numpy(), y) for x, y in zip(outs[0], t.run()))
 
 
 @pytest.mark.parametrize("B, N", [(1, 1), (3, 64), (130, 33), (1000, 6)])

@@ -36,8 +36,14 @@ def test_attention_refuses():
         max_len=[-1, 129, 2**31 - 1], out=[None, P + 4]))
     refused(m.lib.tts_bb_tree_attention, {**good, "type": 1}, dict(q_stride=[2052]))
     assert m.lib.tts_bb_tree_attention(*{**good, "seqs": P, "B": 1024, "N": 64, "n": 2**62}.values()) == -1  # B * N = 65536
-    if m.tts_bb_tree_attention_workspace(2, 5, 128):
-        refused(m.lib.tts_bb_tree_attention, good, dict(ws=[None, P + 8], n=[need - 1, 0]))
+    # short sequences need no workspace, long ones do
+    assert m.tts_bb_tree_attention_workspace(2, 5, 128) == 0
+    need = m.tts_bb_tree_attention_workspace(2, 5, 6400)
+    assert 0 < need < 2**25
+    long = {**good, "cache": cache(m, blocks_per_seq=100), "max_len": 6400, "n": need}
+    refused(m.lib.tts_bb_tree_attention, long, dict(ws=[None, P + 8], n=[need - 1, 0]))
+    big = {**good, "cache": cache(m, blocks_per_seq=2**25), "seqs": P, "B": 9, "N": 1, "max_len": 2**30, "n": 2**62}
+    assert m.lib.tts_bb_tree_attention(*big.values()) == -1 and m.tts_bb_tree_attention_workspace(9, 1, 2**30) == 0  # B * max_len above 2^33
     for args in ((0, 1, 1), (1, 0, 1), (1, 65, 1), (1, 1, -1), (1, 1, 2**30 + 1), (1024, 64, 64), (2**31 - 1, 64, 64)):
         assert m.tts_bb_tree_attention_workspace(*args) == 0
 
