@@ -3,7 +3,11 @@
 // The two query heads of a KV head and up to 64 nodes are the 128 rows of a tile of the tensor cores: row 2 i + h is node i's
 // head 2 g + h. A sequence's keys are its cache pages of 64 and, behind them, one page of the tree's own keys, masked by
 // each node's ancestors. Sums: out = sum_j 2^(c s_j - m) v_j / sum_j 2^(c s_j - m), c = log2 e / sqrt 128, with the running
-// maximum m of the tiles so far.
+// maximum m of the tiles so far. Scores, softmax and sums are fp32; each tile's sums are added to those before in registers, since the
+// tensor cores' own accumulation cuts off what it shifts out.
+//
+// Each key's 512 bytes a KV head are read once and meet up to 128 rows: 256 products a byte at most, which needs tcgen05, and stays
+// bound by memory. The least that a call reads is the cache: see k_tree_attn for what is reached.
 #include <algorithm>
 #include <type_traits>
 
@@ -26,8 +30,8 @@ struct TreeArgs {
     int B, N, max_len;
     int one;      // 1: a block a (sequence, KV head), none is cut
     void* out;
-    int4* meta;   // [shares]: the first piece of each
-    float4* part; // [shares][2][PART][128]
+    int4* meta;   // [blocks]: the first piece of each
+    float4* part; // [blocks][2][PART][128]
 };
 
 constexpr int PAGE_BYTES = KVB * HD * 2;  // K or V of a page and head
@@ -61,8 +65,8 @@ struct Lay {
     }
     static constexpr int STAGE = F32 ? 4096 : 0;  // of each warp that writes sums: 32 rows of 128 bytes
 };
-// the last two beside the rows that few nodes leave empty
-// (the loader in the quarter of warps 2, 6, 10, which few nodes leave empty: 8 x 65537 keys, 31 nodes 326 us, in that of 0 or 1 375)
+// Warps of single tasks: the loader and the issuer of sums beside the rows that trees of up to 32 nodes leave empty (warps of one index modulo
+// 4 share a scheduler, and 0 and 1 are busy then): 8 x 65537 keys, 31 nodes 326 us, with the loader beside warp 0 or 1 375.
 constexpr int W_SUM = 8, W_REST = 12, W_SAFE = 12, W_S = 13, W_LOAD = 14, W_PV = 15, WARPS = 16, NT = WARPS * 32;
 // registers of a thread: the launch's 128 are dealt anew
 constexpr int REGS_SOFT = 112, REGS_SUM = 208, REGS_REST = 80;
@@ -243,12 +247,17 @@ __device__ __forceinline__ bool ancestors(const int32_t* parents, int n, int lan
 __device__ __forceinline__ bool finite16(uint32_t half) { return (half & 0x7F80u) != 0x7F80u; }
 
 // grid: 8 blocks a share, 512 threads. The tiles of all sequences are one line, cut into equal shares, and the 8 KV heads walk it side
-// by side, a block each: what they read at a time lies together. Warp 12 deals the pieces of
-// its share and loads pages (and bf16 queries) by TMA, 13 finds the nodes' ancestors and makes values safe to be multiplied by 0, 14 and
-// 15 issue the products: scores S = Q K^T of a tile, and sums O = P V of one before (two warps, since an issuer waits for
-// its products: one took turns at it, and the tensor cores waited meanwhile). Warps 0 .. 7 turn scores into weights (a thread a row),
-// which replace them in TMEM as the A operand of P V; they hand the running maximum on. Warps 8 .. 11 add each tile's sums to those
-// in their registers. Every wait is bounded.
+// by side, a block each: what they read at a time lies together (64 x 200..2000 keys, 64 nodes: 74 us; heads one after the other 81). Warp
+// 14 deals the pieces of its share and loads pages (and bf16 queries) by TMA, 12 finds the nodes' ancestors and makes values safe to be
+// multiplied by 0, 13 issues the scores S = Q K^T and 15 the sums O = P V (two warps, since an issuer waits for its products: one took
+// turns, and the tensor cores waited meanwhile: 90 us for 97). Warps 0 .. 7 turn scores into weights (a thread a row, even and odd
+// tiles by four each), which replace them in TMEM as the A operand of P V; they hand the running maximum on. Warps 8 .. 11 add each
+// tile's sums to those in their registers. Every wait is bounded.
+//
+// Measured: 8 x 65537 keys, 31 nodes 312 us, 6.9 TB/s: memory. 64 x 200..2000 keys, 64 nodes 75 us, 4.5 TB/s: 5 us until the first
+// scores (one third of it instructions that come from L2), some 1500 cycles a tile where memory needs 1390, 3 us at the end of each
+// piece and of the launch, 3 for the launch that merges. fp32, 8 x 16384 keys, 64 nodes 136 us: the tensor cores (24 products of 128 x 64 x 16 for the
+// scores of a tile, 12 of 128 x 128 x 16 for its sums, 2100 cycles).
 template <bool F32>
 __global__ void __launch_bounds__(NT, 1)
     k_tree_attn(const __grid_constant__ CUtensorMap pool_map, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
