@@ -86,7 +86,7 @@ struct Shared {
     uint32_t tmem;
     int abort;
     int start[5];
-    int page[16];   // of tile t, at t % 16: its page, -1 where that is out of range (the tree: 0)
+    int page[16];   // of tile t, at t % 16: -1 where its page is out of range
     Piece piece[PIECES];
     float m[RING][128], l[RING][128];
 };
@@ -254,8 +254,8 @@ __device__ __forceinline__ bool finite16(uint32_t half) { return (half & 0x7F80u
 // tiles by four each), which replace them in TMEM as the A operand of P V; they hand the running maximum on. Warps 8 .. 11 add each
 // tile's sums to those in their registers. Every wait is bounded.
 //
-// Measured: 8 x 65537 keys, 31 nodes 312 us, 6.9 TB/s: memory. 64 x 200..2000 keys, 64 nodes 75 us, 4.5 TB/s: 5 us until the first
-// scores (one third of it instructions that come from L2), some 1500 cycles a tile where memory needs 1390, 3 us at the end of each
+// Measured: 8 x 65537 keys, 31 nodes 312 us, 6.9 TB/s: memory. 64 x 200..2000 keys, 64 nodes 73 us, 4.7 TB/s: 5 us until the first
+// scores (one third of it instructions that come from L2), some 1400 cycles a tile, which memory needs too, 3 us at the end of each
 // piece and of the launch, 3 for the launch that merges. fp32, 8 x 16384 keys, 64 nodes 136 us: the tensor cores (24 products of 128 x 64 x 16 for the
 // scores of a tile, 12 of 128 x 128 x 16 for its sums, 2100 cycles).
 template <bool F32>
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(NT, 1)
         init(sh.q_empty, 1, 2);
         init(sh.piece_full, 1, PIECES);
         init(sh.seen_full, 1, PIECES);
-        init(sh.piece_empty, 3 + 8 + 4, PIECES);
+        init(sh.piece_empty, 2 + 8 + 4, PIECES);
         init(sh.fin, 1, 2);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -380,9 +380,7 @@ __global__ void __launch_bounds__(NT, 1)
         if (warp == W_LOAD) {
             int ks = 0, vs = 0;       // slots
             uint32_t kp = 1, vp = 1;  // parities of what empties them (the first round is empty)
-            uint32_t kk = ~0u, vk = ~0u;
-            int kt = 0, vt = 0, from = 0;
-            int here = 0, next = 0;  // pages of the keys' tiles from + lane and from + 32 + lane
+            uint32_t kk = ~0u;
             // the sequence, its next tile, and what of the share has not been dealt
             int b = sh.start[0], at = sh.start[1], row = sh.start[2], len = sh.start[3], n = sh.start[4];
             uint32_t left = U;
@@ -416,26 +414,36 @@ __global__ void __launch_bounds__(NT, 1)
                 }
                 return true;
             };
-            const Piece *kq = nullptr, *vq = nullptr;
-            const auto entry = [&](int t) { return t < kq->t1 && t < kq->tiles - 1 ? c.table[(size_t)kq->row * c.bps + t] : 0; };
-            // K (which 0) or V of a tile: a page of the pool, or the tree's own rows
-            const auto fetch = [&](unsigned char* to, u64* bar, const Piece& p, int t, int page, int which) {
-                arrive_tx(bar, page < 0 ? 0 : PAGE_BYTES);
-                if (page < 0) return;
-                const bool tree = t == p.tiles - 1;
-                const CUtensorMap* const map = !tree ? &pool_map : which ? &v_map : &k_map;
-                tma_load_3d(to, map, 0, tree ? p.b * a.N : ((page * 2 + which) * NKV + p.g) * KVB, tree ? 2 * p.g : 0, (uint64_t*)bar);
+            // of the piece whose keys are loaded: its tiles (all, and its next and last here), its sequence, row and keys
+            int tiles = 0, kt = 0, t1 = 0, from = 0, pb = 0, prow = 0;
+            const int g = me % NKV;
+            const auto entry = [&](int t) { return t < t1 && t < tiles - 1 ? c.table[(size_t)prow * c.bps + t] : 0; };
+            // the first row of a tile's keys in what holds them, the pool or the tree's own; -1 where its page is out of range
+            const auto rows_at = [&](int t, int page) {
+                if (t == tiles - 1) return pb * a.N;
+                if (page >= 0 && page < c.n_blocks) return (page * 2 * NKV + g) * KVB;
+                set_err(c.err, TTS_BB_TREE_ERR_PAGE);
+                return -1;
             };
+            int here = 0, next = 0;  // that of the tiles from + lane, and the pages of the tiles from + 32 + lane
+            // Keys are loaded a tile a round, and the values of AHEAD rounds ago: where these are. The round is short, since this warp's
+            // instructions were what bounded a tile before: 8 x 65537 keys from L2, 64 nodes 282 us, with two waits and the piece read
+            // from shared memory for keys and for values 325.
+            int y[L::AHEAD + 1] = {};
+            bool tree[L::AHEAD + 1] = {};
             int k_landing = 0, v_landing = 0;
 #pragma unroll 1
             for (uint32_t i = 0; ok && i < U + L::AHEAD; ++i) {
-                if (i < U) {
-                    if (!kq || kt == kq->t1) {
+                // both at once: an empty slot for the keys, and one for the values (behind the last keys, and before the first values,
+                // of one that nothing is loaded to)
+                const bool k_turn = i < U, v_turn = i >= L::AHEAD;
+                if (k_turn) {
+                    if (kt == t1) {
                         ++kk;
                         if (!deal_piece(kk)) break;
-                        kq = &sh.piece[kk % PIECES];
-                        from = kt = kq->t0;
-                        here = entry(from + lane);
+                        const Piece& p = sh.piece[kk % PIECES];
+                        tiles = p.tiles, from = kt = p.t0, t1 = p.t1, pb = p.b, prow = p.row;
+                        here = rows_at(from + lane, entry(from + lane));
                         next = entry(from + 32 + lane);
                         if constexpr (!F32) {
                             const uint32_t qb = kk & 1;
@@ -446,43 +454,44 @@ __global__ void __launch_bounds__(NT, 1)
                             if (lane == 0) {
                                 unsigned char* const to = smem + qb * plan.q_bytes<F32>();
                                 arrive_tx(&sh.q_full[qb], (uint32_t)a.N * 512);
-                                tma_load_3d(to, &q_map, 0, 2 * kq->g, kq->b * a.N, (uint64_t*)&sh.q_full[qb]);
-                                tma_load_3d(to + plan.rows * 128, &q_map, 64, 2 * kq->g, kq->b * a.N, (uint64_t*)&sh.q_full[qb]);
+                                tma_load_3d(to, &q_map, 0, 2 * g, pb * a.N, (uint64_t*)&sh.q_full[qb]);
+                                tma_load_3d(to + plan.rows * 128, &q_map, 64, 2 * g, pb * a.N, (uint64_t*)&sh.q_full[qb]);
                             }
                         }
                     } else if (kt == from + 32) {
                         from = kt;
-                        here = next;
+                        here = rows_at(from + lane, next);
                         next = entry(from + 32 + lane);
                     }
-                    int page = __shfl_sync(0xffffffffu, here, kt - from);
-                    if (page < 0 || page >= c.n_blocks) {
-                        page = -1;
-                        if (lane == 0) set_err(c.err, TTS_BB_TREE_ERR_PAGE);
+                }
+#pragma unroll
+                for (int j = L::AHEAD; j > 0; --j) y[j] = y[j - 1], tree[j] = tree[j - 1];
+                y[0] = __shfl_sync(0xffffffffu, here, kt - from);
+                tree[0] = kt == tiles - 1;
+                ok = wait_for(&sh.abort, &sh.k_empty[ks], kp, &sh.v_empty[vs], vp);
+                if (!ok) break;
+                if (lane == 0) {
+                    // K (which 0) or V of a tile
+                    const auto fetch = [&](unsigned char* to, u64* bar, int j, int which) {
+                        arrive_tx(bar, y[j] < 0 ? 0 : PAGE_BYTES);
+                        if (y[j] >= 0)
+                            tma_load_3d(to, !tree[j] ? &pool_map : which ? &v_map : &k_map, 0, y[j] + (tree[j] ? 0 : which * NKV * KVB),
+                                        tree[j] ? 2 * g : 0, (uint64_t*)bar);
+                    };
+                    if (k_turn) {
+                        sh.page[i % 16] = y[0];
+                        fetch(k_ring + ks * PAGE_BYTES, &sh.k_full[ks], 0, 0);
                     }
-                    if (!wait(&sh.k_empty[ks], kp)) break;
-                    if (lane == 0) {
-                        sh.page[i % 16] = page;
-                        fetch(k_ring + ks * PAGE_BYTES, &sh.k_full[ks], *kq, kt, page, 0);
-                    }
+                    if (v_turn) fetch(v_ring + vs * PAGE_BYTES, &sh.v_full[vs], L::AHEAD, 1);
+                }
+                if (k_turn) {
                     ++kt;
                     ++k_landing;
                     if (++ks == plan.k_slots) ks = 0, kp ^= 1;
                 }
-                if (i >= L::AHEAD) {
-                    if (!vq) {
-                        vq = &sh.piece[++vk % PIECES];
-                        vt = vq->t0;
-                    }
-                    if (!wait(&sh.v_empty[vs], vp)) break;
-                    if (lane == 0) fetch(v_ring + vs * PAGE_BYTES, &sh.v_full[vs], *vq, vt, sh.page[(i - L::AHEAD) % 16], 1);
+                if (v_turn) {
                     ++v_landing;
                     if (++vs == plan.v_slots) vs = 0, vp ^= 1;
-                    __syncwarp();
-                    if (++vt == vq->t1) {  // from here on another piece may stand in its place
-                        if (lane == 0) arrive(&sh.piece_empty[vk % PIECES]);
-                        vq = nullptr;
-                    }
                 }
             }
             if (ok) ok = deal_piece(kk + 1);  // no more
