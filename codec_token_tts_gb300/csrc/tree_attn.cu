@@ -3,8 +3,8 @@
 // The two query heads of a KV head and up to 64 nodes are the 128 rows of a tile of the tensor cores: row 2 i + h is node i's
 // head 2 g + h. A sequence's keys are its cache pages of 64 and, behind them, one page of the tree's own keys, masked by
 // each node's ancestors. Sums: out = sum_j 2^(c s_j - m) v_j / sum_j 2^(c s_j - m), c = log2 e / sqrt 128, with the running
-// maximum m of the tiles so far. Scores, softmax and sums are fp32; each tile's sums are added to those before in registers, since the
-// tensor cores' own accumulation cuts off what it shifts out.
+// maximum m of the tiles so far (bf16: within a factor of 4 of it). Scores, softmax and sums are fp32; the sums of a tile (bf16: of two) are
+// added to those before in registers, since the tensor cores' own accumulation cuts off what it shifts out.
 //
 // Each key's 512 bytes a KV head are read once and meet up to 128 rows: 256 products a byte at most, which needs tcgen05, and stays
 // bound by memory. The least that a call reads is the cache: see k_tree_attn for what is reached.
@@ -59,6 +59,12 @@ struct Lay {
     // takes 16, the second the others. The third part of tile t has 32 columns of its own by t & 1, behind three regions (two regions of
     // 96, which need no wait for them: 2500 cycles a tile, 3 regions 2100). Values are loaded AHEAD tiles behind keys
     static constexpr int REGIONS = F32 ? 3 : 4, AHEAD = 2;
+    // Tiles whose sums the tensor cores add up where no row's reference rises between them, before warps 8 .. 11 take them: with one of
+    // two buffers a tile, products that end late and the taking of their sums bounded a tile (8 x 65537 keys, 31 nodes, from L2: 272 us,
+    // of pairs 253).
+    // So that references rise seldom, one lags up to 2^SLACK behind the maximum: weights reach 4 then.
+    static constexpr int GROUP = F32 ? 1 : 2;
+    static constexpr float SLACK = F32 ? 0.f : 2.f;
     // the column of a part of 32 keys' weights of tile u
     static __device__ __forceinline__ uint32_t part_at(uint32_t u, int part, int chunk) {
         return part < 2 ? u % REGIONS * KVB + chunk * 32 + part * 16 : 192 + (u & 1) * 32 + chunk * 16;
@@ -79,13 +85,15 @@ constexpr int TMEM_COLS = 512;  // the regions, then the sums of tile t at 256 +
 struct Shared {
     u64 k_full[MAX_SLOTS], k_empty[MAX_SLOTS], v_full[MAX_SLOTS], v_ready[MAX_SLOTS], v_empty[MAX_SLOTS];
     u64 s_full[4], p_full[4], w_empty[4];  // of a region: scores there (products, their issuer), weights there (4 warps), weights taken
-    u64 o_full[2], o_empty[2];  // a tile's sums there (products, their issuer), taken (4)
+    u64 o_full[2], o_empty[2];  // one or two tiles' sums there (products, their issuer), taken (4)
     u64 m_full[4][2];           // a tile's references of 32 rows there
     u64 q_full[2], q_empty[2], piece_full[PIECES], seen_full[PIECES], piece_empty[PIECES], fin[2];
     uint32_t sums[WARPS];
     uint32_t tmem;
     int abort;
     int start[5];
+    int last[2];    // of the tiles whose sums a buffer holds
+    unsigned char rose[4][4];  // of a region's weights and 32 rows: whether a reference rose
     int page[16];   // of tile t, at t % 16: -1 where its page is out of range
     Piece piece[PIECES];
     float m[RING][128], l[RING][128];
@@ -251,10 +259,10 @@ __device__ __forceinline__ bool finite16(uint32_t half) { return (half & 0x7F80u
 // 14 deals the pieces of its share and loads pages (and bf16 queries) by TMA, 12 finds the nodes' ancestors and makes values safe to be
 // multiplied by 0, 13 issues the scores S = Q K^T and 15 the sums O = P V (two warps, since an issuer waits for its products: one took
 // turns, and the tensor cores waited meanwhile: 90 us for 97). Warps 0 .. 7 turn scores into weights (a thread a row, even and odd
-// tiles by four each), which replace them in TMEM as the A operand of P V; they hand the running maximum on. Warps 8 .. 11 add each
-// tile's sums to those in their registers. Every wait is bounded.
+// tiles by four each), which replace them in TMEM as the A operand of P V; they hand the running maximum on. Warps 8 .. 11 add
+// the tiles' sums to those in their registers. Every wait is bounded.
 //
-// Measured: 8 x 65537 keys, 31 nodes 312 us, 6.9 TB/s: memory. 64 x 200..2000 keys, 64 nodes 73 us, 4.7 TB/s: 5 us until the first
+// Measured: 8 x 65537 keys, 31 nodes 313 us, 6.9 TB/s: memory. 64 x 200..2000 keys, 64 nodes 73 us, 4.7 TB/s: 5 us until the first
 // scores (one third of it instructions that come from L2), some 1400 cycles a tile, which memory needs too, 3 us at the end of each
 // piece and of the launch, 3 for the launch that merges. fp32, 8 x 16384 keys, 64 nodes 136 us: the tensor cores (24 products of 128 x 64 x 16 for the
 // scores of a tile, 12 of 128 x 128 x 16 for its sums, 2100 cycles).
@@ -552,7 +560,17 @@ __global__ void __launch_bounds__(NT, 1)
             const uint32_t v0 = desc_mn(s_addr(v_ring));
             const bool leader = elect();
             uint32_t vs = 0, vp = 0, k = ~0u;  // slot, its parity, piece
-            int left = 0, t = 0, tiles = 0, len = 0, n = 0;
+            uint32_t o = 0;                    // the buffer's turn
+            int left = 0, t = 0, tiles = 0, len = 0, n = 0, held = 0;  // tiles in it
+            const auto close = [&](uint32_t last) {
+                if (leader) {
+                    sh.last[o & 1] = (int)last;
+                    arrive(&sh.o_full[o & 1]);
+                    at_commit((uint64_t*)&sh.o_full[o & 1]);
+                }
+                ++o;
+                held = 0;
+            };
 #pragma unroll 1
             for (uint32_t u = 0; u < U; ++u) {
                 if (left == 0) {
@@ -568,10 +586,21 @@ __global__ void __launch_bounds__(NT, 1)
                 // 16 keys a step of the products, of those that there are
                 const int keys = t == tiles - 1 ? n : min(KVB, len - t * KVB), steps = (keys + 15) / 16;
                 const uint32_t region = u % L::REGIONS;
-                ok = wait_for(&sh.abort, &sh.p_full[region], (u / L::REGIONS) & 1u, &sh.v_ready[vs], vp, &sh.o_empty[u & 1], ((u >> 1) - 1) & 1u);
+                if (L::GROUP > 1 && held) {
+                    ok = wait_for(&sh.abort, &sh.p_full[region], (u / L::REGIONS) & 1u, &sh.v_ready[vs], vp);
+                    if (!ok) break;
+                    if (*reinterpret_cast<const volatile uint32_t*>(sh.rose[region])) {
+                        __syncwarp();
+                        close(u - 1);
+                        ok = wait(&sh.o_empty[o & 1], ((o >> 1) - 1) & 1u);
+                    }
+                } else {
+                    ok = wait_for(&sh.abort, &sh.p_full[region], (u / L::REGIONS) & 1u, &sh.v_ready[vs], vp, &sh.o_empty[o & 1], ((o >> 1) - 1) & 1u);
+                }
                 if (!ok) break;
                 tc_after();
-                const uint32_t d = tmem + 256 + (u & 1) * 128, v1 = v0 + vs * (PAGE_BYTES >> 4);
+                const bool adds = held > 0;
+                const uint32_t d = tmem + 256 + (o & 1) * 128, v1 = v0 + vs * (PAGE_BYTES >> 4);
                 ++t;
                 --left;
                 if (leader) {
@@ -579,13 +608,12 @@ __global__ void __launch_bounds__(NT, 1)
                     for (int part = L::PPARTS - 1; part >= 0; --part)
 #pragma unroll
                         for (int kk = 0; kk < KVB / 16; ++kk)  // 8 columns of weights
-                            if (kk < steps) mma_ts(d, tmem + L::part_at(u, part, kk >> 1) + (kk & 1) * 8, v1 + (uint32_t)(kk * 2048 / 16), IDESC_PV, part < L::PPARTS - 1 || kk > 0);
-                    arrive(&sh.o_full[u & 1]);
-                    at_commit((uint64_t*)&sh.o_full[u & 1]);
+                            if (kk < steps) mma_ts(d, tmem + L::part_at(u, part, kk >> 1) + (kk & 1) * 8, v1 + (uint32_t)(kk * 2048 / 16), IDESC_PV, adds || part < L::PPARTS - 1 || kk > 0);
                     at_commit((uint64_t*)&sh.v_empty[vs]);
                     at_commit((uint64_t*)&sh.w_empty[region]);
                     if (left == 0) arrive(&sh.piece_empty[k % PIECES]);
                 }
+                if (++held == L::GROUP || left == 0) close(u);
                 __syncwarp();
                 if (++vs == (uint32_t)plan.v_slots) vs = 0, vp ^= 1;
             }
@@ -737,6 +765,7 @@ __global__ void __launch_bounds__(NT, 1)
                 const uint32_t u = u0 + j, region = u % L::REGIONS, at = lanes + region * KVB;
                 if (!wait(&sh.s_full[region], (u / L::REGIONS) & 1u)) break;
                 float m = -INFINITY;
+                bool rose = false;
                 // the keys that count, a bit each, where not all do
                 const bool tree = t == p.tiles - 1;
                 const int valid = p.len - t * KVB;
@@ -770,7 +799,15 @@ __global__ void __launch_bounds__(NT, 1)
                 // the maximum so far, from the warp of the tile before (waited for at a new piece too: no warp is two tiles ahead)
                 if (u > 0) {
                     if (!wait(&sh.m_full[quarter][(u - 1) & 1], ((u - 1) >> 1) & 1u)) break;
-                    if (u > u0) m = fmaxf(m, sh.m[(u - 1) % RING][r]);
+                    if (u > u0) {
+                        const float before = sh.m[(u - 1) % RING][r];
+                        if ((m - before) * cs > L::SLACK) rose = r < rows;
+                        else m = before;
+                    }
+                }
+                if constexpr (L::GROUP > 1) {
+                    rose = __any_sync(0xffffffffu, rose);
+                    if (lane == 0) sh.rose[region][quarter] = rose;
                 }
                 sh.m[u % RING][r] = m;
                 __syncwarp();
@@ -826,7 +863,7 @@ __global__ void __launch_bounds__(NT, 1)
         const int quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = tmem + 256 + ((uint32_t)(quarter * 32) << 16);
         const float cs = 0.08838834764831845f * 1.4426950408889634f;
-        uint32_t u = 0;
+        uint32_t u = 0, turn = 0;
 #pragma unroll 1
         for (uint32_t k = 0; ok; ++k) {
             if (!wait(piece_bar(k), piece_par(k))) break;
@@ -839,13 +876,18 @@ __global__ void __launch_bounds__(NT, 1)
             for (int i = 0; i < HD / 2; ++i) o[i] = 0;
             float m = -INFINITY, l = 0.f;  // the reference, times cs
 #pragma unroll 1
-            for (int t = 0; t < nt; ++t, ++u) {
-                if (!wait(&sh.o_full[u & 1], (u >> 1) & 1u)) break;
+            for (int t = 0; t < nt; ++t, ++u, ++turn) {
+                if (!wait(&sh.o_full[turn & 1], (turn >> 1) & 1u)) break;
+                // the buffer's tiles: from one on, to t
+                const bool first = t == 0;
+                const int more = sh.last[turn & 1] - (int)u;
+                t += more;
+                u += more;
                 if (mine) {
                     tc_after();
-                    const float now = sh.m[u % RING][r] * cs, f = t == 0 ? 0.f : now == m ? 1.f : at_ex2(m - now);
+                    const float now = sh.m[u % RING][r] * cs, f = first ? 0.f : now == m ? 1.f : at_ex2(m - now);
                     const u64 f2 = pair(f, f);
-                    const uint32_t at = lanes + (u & 1) * 128;
+                    const uint32_t at = lanes + (turn & 1) * 128;
                     uint32_t x[2][32];  // the next 32 dims are on their way while these are added
                     tm_ld32_nw(at, x[0]);
 #pragma unroll
@@ -856,12 +898,15 @@ __global__ void __launch_bounds__(NT, 1)
                         for (int j = 0; j < 16; ++j)
                             o[16 * i + j] = fma2(o[16 * i + j], f2, pair(__uint_as_float(x[i & 1][2 * j]), __uint_as_float(x[i & 1][2 * j + 1])));
                     }
-                    if (t + 2 >= nt) l = (t == 0 || l == 0.f ? 0.f : l * f) + sh.l[u % RING][r];  // of even and of odd tiles
+                    if (t + 2 >= nt) {  // of even and of odd tiles
+                        l = (first || l == 0.f ? 0.f : l * f) + sh.l[u % RING][r];
+                        if (more && t + 1 == nt) l += sh.l[(u - 1) % RING][r];
+                    }
                     m = now;
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0) arrive(&sh.o_empty[u & 1]);
+                if (lane == 0) arrive(&sh.o_empty[turn & 1]);
             }
             if (!ok) break;
             // the piece's end: code that runs this seldom comes from beyond the instruction cache, so it is kept short

@@ -280,6 +280,27 @@ def test_attention_of_large_and_small_scores(io):
 
 
 @IO
+@pytest.mark.parametrize("step", ["little", "much", "either", "once"])
+@pytest.mark.parametrize("who", ["all", "last"])
+def test_attention_of_scores_that_rise_from_page_to_page(io, step, who):
+    """By less than the reference may lag, by more, up and down, and once: for all nodes, or for the last one alone."""
+    c = Case(26, [64 * 21 + 20, 64 * 5, 64 * 2 + 1], 33, io)
+    rng = np.random.default_rng(27)
+    for b, n in enumerate(c.lens):
+        page = np.arange(n) // BLK
+        rise = {"little": 0.6 * page, "much": 3.0 * page, "either": rng.choice([-4.0, 0.0, 0.9, 4.0], page[-1] + 1)[page], "once": 9.0 * (page == page[-1] - 1)}[step]
+        x = dev(rise * np.sqrt(HD) / 8).bfloat16()
+        at = dev(c.table[b]).long()[dev(page)]
+        c.pool[0, at, 0, :, dev(np.arange(n) % BLK), 0] = x[:, None]
+        c.k[b][:, :, 0] = x.double().cpu().numpy()[:, None]
+    q = c.q.view(3, 33, NQ, HD)
+    q[:, :, :, 0] = 0.0
+    q[:, 0 if who == "all" else 32 :, 0::3, 0] = 8.0
+    q[:, 0 if who == "all" else 32 :, 1::3, 0] = -8.0
+    c.check(c.run())
+
+
+@IO
 def test_attention_is_the_same_every_time_and_in_a_graph(io):
     """Bitwise, on another stream, in a captured graph that is replayed on other inputs, and two calls at once."""
     c = Case(24, [900, 40, 333], 7, io)
