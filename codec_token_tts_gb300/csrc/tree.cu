@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(128) k_tree_commit(Pages c, CommitArgs a) {
 #pragma unroll
         for (int i = 0; i < COMMIT; ++i) {
             if (page[i] < 0) continue;
-            bf16* const at = to + page[i] * KV_BLOCK + (size_t)((len + j0 + i) % KVB) * HD;
+            bf16* const at = to + page[i] * KV_BLOCK + (size_t)(((unsigned)len + j0 + i) % KVB) * HD;
             *reinterpret_cast<uint4*>(at) = x[i][0];
             *reinterpret_cast<uint4*>(at + KV_BLOCK / 2) = x[i][1];
         }

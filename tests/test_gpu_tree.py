@@ -617,3 +617,21 @@ def test_commit_writes_the_paths_and_nothing_else(L, B, N, strided):
     m.tts_bb_tree_commit(cache, B, N, k, v, ints(path), ints(count), ints(lens), seqs=ints(seqs), stream=stream())
     assert torch.equal(pool.view(torch.int16), want.view(torch.int16))
     assert int(err) == flags
+
+
+def test_commit_at_positions_beyond_31_bits():
+    """A row whose table is that long (of pages that all but the last two are one): K and V from position 2^31 - 3 on."""
+    m = tb()
+    bps, N = 2 ** 25 + 1, 6
+    pool = torch.randn(4, 2, NKV, BLK, HD, device="cuda").bfloat16()
+    table = torch.zeros(1, bps, dtype=torch.int32, device="cuda")
+    table[0, -2], table[0, -1] = 2, 1
+    k, v = (torch.randn(1, N, 1024, device="cuda").bfloat16() for _ in range(2))
+    want = pool.clone()
+    for j in range(N):
+        for w, x in ((0, k), (1, v)):
+            want[2 if j < 3 else 1, w, :, (61 + j) % BLK] = x[0, j].reshape(NKV, HD)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m.tts_bb_tree_commit(m.KvCache(pool, table, err), 1, N, k, v, ints(np.arange(N)), ints([N]), ints([2 ** 31 - 3]), stream=stream())
+    assert torch.equal(pool.view(torch.int16), want.view(torch.int16))
+    assert int(err) == 0
