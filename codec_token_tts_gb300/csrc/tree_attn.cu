@@ -994,11 +994,12 @@ __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
     const int4 meta = s0 + lane < shares ? a.meta[(s0 + lane) * NKV + g] : make_int4(-1, 0, 0, 0);
     const int it = __shfl_sync(0xffffffffu, meta.x, 1);
     const uint32_t goes_on = __ballot_sync(0xffffffffu, lane > 0 && meta.x == it && (meta.z & 1));
-    if (it < 0 || !(goes_on & 2)) return;  // the share behind begins with a new one
+    // (and after a wait that ran out a place may hold anything)
+    if (it < 0 || it >= a.B || !(goes_on & 2)) return;  // the share behind begins with a new one
     const int head = __shfl_sync(0xffffffffu, meta.x, 0), inside = __shfl_sync(0xffffffffu, meta.z, 0) & 1;
     if (head == it && inside) return;  // begun before this share
     const int more = __ffs(~(goes_on >> 1)) - 1;  // shares behind this one
-    const int n = __shfl_sync(0xffffffffu, meta.y, 1);
+    const int n = min(__shfl_sync(0xffffffffu, meta.y, 1), a.N);
     const bool in_order = __shfl_sync(0xffffffffu, meta.z, more) >> 2 & 1;  // the last piece holds the tree
     if (r >= 2 * n || !in_order) return;
     const auto at = [&](int i) { return a.part + ((size_t)((s0 + i) * NKV + g) * 2 + (i == 0 && head != it)) * PART * 128 + r; };
