@@ -48,9 +48,11 @@ __device__ __forceinline__ u64 pair60(float s, float rest) {
         const u64 m = (b & 0x7FFFFFu) | 0x800000u;
         return e >= 90 ? m << (e - 90) : e > 66 ? m >> (90 - e) : 0ull;
     };
-    if (!(s > 0.f)) return 0ull;
-    const u64 a = fix(fminf(s, 8.f)), d = fix(fminf(fabsf(rest), 1.f));
-    return rest < 0.f ? (a > d ? a - d : 0ull) : a + d;
+    // s may be 0 beside a rest, or below it
+    const float t = s + rest, z = t - s, y = (s - (t - z)) + (rest - z);
+    if (!(t > 0.f)) return 0ull;
+    const u64 a = fix(fminf(t, 8.f)), d = fix(fminf(fabsf(y), 1.f));
+    return y < 0.f ? (a > d ? a - d : 0ull) : a + d;
 }
 // two floats an instruction
 __device__ __forceinline__ u64 both(float a, float b) {
@@ -86,16 +88,18 @@ __device__ __forceinline__ void rest2(u64& s, u64& rest, float p0, float p1, flo
     const u64 p = both(p0, p1), q = both(fminf(p0, q0), fminf(p1, q1)), d = sub2(p, q);
     gather2(s, rest, d, sub2(sub2(p, d), q));
 }
-// p - c q, c = (hi, lo)
+// p - c q where that is above 0, c = (hi, lo): the sign is that of the sum, since c q may lie to either side of what it rounds to
 __device__ __forceinline__ void rest2(u64& s, u64& rest, float p0, float p1, float q0, float q1, u64 hi, u64 lo) {
-    const u64 q = both(q0, q1), h = mul2(hi, q);
-    float h0, h1, l0, l1;
-    halves(h, h0, h1);
-    halves(fma2(lo, q, fma2(hi, q, mul2(h, both(-1.f, -1.f)))), l0, l1);  // what h rounded off, and lo q
-    if (p0 <= h0) { h0 = p0; l0 = 0.f; }
-    if (p1 <= h1) { h1 = p1; l1 = 0.f; }
-    const u64 p = both(p0, p1), b = both(h0, h1), d = sub2(p, b);
-    gather2(s, rest, d, sub2(sub2(sub2(p, d), b), both(l0, l1)));
+    const u64 p = both(p0, p1), q = both(q0, q1), h = mul2(hi, q);
+    const u64 l = fma2(lo, q, fma2(hi, q, mul2(h, both(-1.f, -1.f))));  // what h rounded off, and lo q
+    const u64 d = sub2(p, h), e = sub2(sub2(sub2(p, d), h), l);
+    float t0, t1, d0, d1, e0, e1;
+    halves(add2(d, e), t0, t1);
+    halves(d, d0, d1);
+    halves(e, e0, e1);
+    if (t0 <= 0.f) d0 = e0 = 0.f;
+    if (t1 <= 0.f) d1 = e1 = 0.f;
+    gather2(s, rest, both(d0, d1), both(e0, e1));
 }
 // ids x .. x + 3 of a row of V, 0 for those outside
 __device__ __forceinline__ float4 four(const float* row, int x, int V) {

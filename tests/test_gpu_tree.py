@@ -1,4 +1,6 @@
 """Attention of trees of drafted tokens, their verification and their commit, against the plain forms in 64 bits."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 
@@ -484,6 +486,44 @@ def test_verify_borders():
     t.check(skip=())
     t.q = None
     t.check()
+
+
+def rounded_case(seed):
+    """Rows p, q of 8 ids, a token x and a number u. Behind two rejections of id 0 the rest is (p - c q)^+ with c = 1 + sum (p - q)^+. Id 1's p is
+    what c q rounds to in fp32, and above c q: u lies above the border of x for the sum of all rests, below it for the sum without id 1's."""
+    rng = np.random.default_rng(seed)
+    rests = lambda p, q, c: [max(x - c * y, 0) for x, y in zip(p, q)]
+    while True:
+        q = rng.dirichlet(np.full(8, 4.0)).astype(np.float32)
+        p = (q * (1 + 0.02 * rng.standard_normal(8))).astype(np.float32)
+        p[0] = q[0] * np.float32(0.9)
+        P, Q = [Fraction(float(x)) for x in p], [Fraction(float(x)) for x in q]
+        for _ in range(30):  # c moves with id 1's p
+            c = 1 + sum(rests(P, Q, 1))
+            same = p[1] == np.float32(float(c * Q[1]))
+            if same:
+                break
+            p[1] = np.float32(float(c * Q[1]))
+            P[1] = Fraction(float(p[1]))
+        if not same or P[1] <= c * Q[1]:
+            continue
+        r = rests(P, Q, c)
+        for x in range(2, 8):
+            low, high = (r[x] / (Q[x] * z) for z in (sum(r), sum(r) - r[1]))
+            u = np.float32(float((low + high) / 2))
+            if r[x] > 0 and u < 1 and low * (1 + Fraction(1, 2 ** 40)) < Fraction(float(u)) < high * (1 - Fraction(1, 2 ** 40)):
+                return p, q, x, u
+
+
+def test_verify_counts_a_rest_below_the_rounding_of_its_product():
+    t = Trees(2, 4, 4, 8, True)
+    t.parents = np.tile(np.array([[-1, 0, 0, 0]], np.int32), (4, 1))
+    t.u[:, 1:3] = 1 - 2.0 ** -10
+    for b in range(4):
+        t.p[4 * b], t.q[4 * b], x, t.u[b, 3] = rounded_case(b)
+        t.tokens[b] = [0, 0, 0, x]
+    count, path, nxt = t.run()
+    assert list(count) == [1, 1, 1, 1]
 
 
 @DRAWN
