@@ -65,7 +65,7 @@ class Case:
             at = slice(b * N, b * N + n)
             self.qw[at, :2048] = dev(1.5 * rng.standard_normal((n, 2048))).to(dt)
             self.kvw[at, 2048:] = dev(rng.standard_normal((n, 2048))).bfloat16()
-        self.q, self.tk, self.tv = self.qw[:, :2048], self.kvw[:, 2048:3072], self.kvw[:, 3072:]
+        self.q, (self.tk, self.tv) = self.qw[:, :2048], self.kvw[:, 2048:].split(1024, 1)
         self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
         self.layers = layers
 
