@@ -22,8 +22,10 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int THREADS = 512, NWARPS = THREADS / 32;
-constexpr int MAX_CLUSTER = 16, BLOCKS_SM = 2;
+constexpr int MAX_CLUSTER = 16, THREADS_SM = 1024;
+// Ids that one block takes; below that it has fewer threads, whose barriers cost less and of which more sequences' are at work at a time
+// (64 x 2048, chosen drafts, 25 nodes: 7.2 us, by 512 threads 7.9; 1000 x 2048, drawn, 6 nodes: 16.3 and 25.7; 700 x 30000: 61 and 55).
+constexpr int BLOCK_IDS = 4096, THREADS = 512, THREADS_SMALL = 256;
 
 // a probability's bits, within 0 .. 1 (a NaN counts as 1, or as 0 where its sign is set)
 __device__ __forceinline__ uint32_t prob_bits(float x) { return (uint32_t)min(max(__float_as_int(x), 0), 0x3F800000); }
@@ -194,7 +196,7 @@ enum { WALK_PASS, WALK_LAST };
 struct VerifyShared {
     int par[MAX_NODES], tok[MAX_NODES];
     float p[MAX_NODES], q[MAX_NODES], u[MAX_NODES];
-    u64 wsum[NWARPS];
+    u64 wsum[THREADS / 32];
     u64 tot[2][MAX_CLUSTER];  // the blocks' sums of a pass, by its parity
     u64 chosen, gone;         // accepted nodes; rejected children of the current node (drafts that were not drawn)
     u64 c;                    // 2^-58
@@ -203,10 +205,11 @@ struct VerifyShared {
     int n, cur, event;
 };
 
-// grid (ctas, B), a cluster of ctas blocks for each sequence, 512 threads. Block r of a cluster owns the ids
+// grid (ctas, B), a cluster of ctas blocks for each sequence. Block r of a cluster owns the ids
 // [r, r + 1) * NWARPS * seg, warp w of it seg of them.
-template <bool DRAWN>
-__global__ void __launch_bounds__(THREADS, BLOCKS_SM) k_tree_verify(VerifyArgs a) {
+template <bool DRAWN, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS_SM / THREADS) k_tree_verify(VerifyArgs a) {
+    constexpr int NWARPS = THREADS / 32;
     __shared__ VerifyShared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y, rank = blockIdx.x;
     const bool many = a.ctas > 1;
@@ -556,11 +559,11 @@ __global__ void __launch_bounds__(128) k_tree_commit(Pages c, CommitArgs a) {
     }
 }
 
-// Blocks of a sequence's cluster: one for each 4096 ids, while all sequences' blocks run in two turns. 64 x 151676, 12 nodes: by 8 blocks
+// Blocks of a sequence's cluster: one for each BLOCK_IDS, while all sequences' blocks run in two turns. 64 x 151676, 12 nodes: by 8 blocks
 // a sequence 36 us, 4 (one turn) 38, 16 (four) 59.
 int verify_ctas(int B, int V) {
     int n = 1;
-    while (n < MAX_CLUSTER && n * 4096 < V && 2 * n * B <= 2 * BLOCKS_SM * 152) n *= 2;
+    while (n < MAX_CLUSTER && n * BLOCK_IDS < V && 2 * n * B <= 2 * (THREADS_SM / THREADS) * 152) n *= 2;
     return n;
 }
 
@@ -576,7 +579,9 @@ TTS_API tts_bb_status tts_bb_tree_verify(int B, int N, int V, const int32_t* tok
         return TTS_BB_E_INVALID;
     if (cudaPeekAtLastError() != cudaSuccess) return TTS_BB_E_CUDA;
     const int ctas = verify_ctas(B, V);
-    const int seg = (int)((V + 3ll + ctas * NWARPS * 128 - 1) / (ctas * NWARPS * 128)) * 128;  // and 3 ids that alignment skips
+    const bool large = V > BLOCK_IDS;
+    const int threads = large ? THREADS : THREADS_SMALL, turn = ctas * threads * 4;  // ids at a time
+    const int seg = (int)((V + 3ll + turn - 1) / turn) * 128;  // and 3 ids that alignment skips
     const VerifyArgs a{tokens, parents, n_nodes, target, draft, u, u_next, target_stride, draft_stride, n_accepted, path, next_token, err,
                        N, V, ctas, seg};
     const auto go = [&](auto kernel, SmemState& state) {
@@ -589,15 +594,15 @@ TTS_API tts_bb_status tts_bb_tree_verify(int B, int N, int V, const int32_t* tok
         at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(ctas, B);
-        cfg.blockDim = dim3(THREADS);
+        cfg.blockDim = dim3(threads);
         cfg.stream = static_cast<cudaStream_t>(stream);
         cfg.attrs = at;
         cfg.numAttrs = ctas > 1 ? 2 : 1;
         cudaLaunchKernelEx(&cfg, kernel, a);
     };
-    static SmemState drawn, chosen;
-    if (draft) go(k_tree_verify<true>, drawn);
-    else go(k_tree_verify<false>, chosen);
+    static SmemState states[4];
+    if (large) draft ? go(k_tree_verify<true, THREADS>, states[0]) : go(k_tree_verify<false, THREADS>, states[1]);
+    else draft ? go(k_tree_verify<true, THREADS_SMALL>, states[2]) : go(k_tree_verify<false, THREADS_SMALL>, states[3]);
     return launched();
 }
 
