@@ -216,13 +216,17 @@ __global__ void __launch_bounds__(THREADS, THREADS_SM / THREADS) k_tree_verify(V
     if (many) cluster_arrive();  // waited for before the first word goes to a peer
     pdl_wait();
     pdl_trigger();
+    const float u_next = a.u_next[b];
     if (warp == 0) {
-        int par[2];
+        int par[2], tok[2];
+        float u[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h) {  // one wait for all
             const int j = lane + 32 * h;
-            par[h] = j < a.N ? a.parents[(size_t)b * a.N + j] : -1;
-            sh.par[j] = par[h];
+            const size_t at = (size_t)b * a.N + j;
+            par[h] = j < a.N ? a.parents[at] : -1;
+            tok[h] = j < a.N ? a.tokens[at] : -1;
+            u[h] = j < a.N ? a.u[at] : 0.f;
         }
         const int n = tree_nodes(a.n_nodes, b, a.N, lane, par, a.err, rank == 0);
 #pragma unroll
@@ -230,11 +234,12 @@ __global__ void __launch_bounds__(THREADS, THREADS_SM / THREADS) k_tree_verify(V
             const int j = lane + 32 * h;
             if (j >= n) continue;
             // what the target and the draft of its parent give the node's token
-            const int x = a.tokens[(size_t)b * a.N + j];
+            const int x = tok[h];
             const bool real = x >= 0 && x < a.V && par[h] >= 0;
             const size_t row = (size_t)b * a.N + max(par[h], 0);
+            sh.par[j] = par[h];
             sh.tok[j] = real ? x : -1;
-            sh.u[j] = a.u[(size_t)b * a.N + j];
+            sh.u[j] = u[h];
             sh.p[j] = real ? __uint_as_float(prob_bits(a.target[row * a.p_stride + x])) : 0.f;
             if (DRAWN) sh.q[j] = real ? __uint_as_float(prob_bits(a.draft[row * a.q_stride + x])) : 0.f;
         }
@@ -250,7 +255,6 @@ __global__ void __launch_bounds__(THREADS, THREADS_SM / THREADS) k_tree_verify(V
         if (rank == 0 && warp == 0) write_path(0, b, a.N, lane, a.n_accepted, a.path);
         return;
     }
-    const float u_next = a.u_next[b];
     const int at0 = (rank * NWARPS + warp) * a.seg;  // ids of this warp, but for the row's alignment
     u64 Z = 0;
     int parity = 0;
