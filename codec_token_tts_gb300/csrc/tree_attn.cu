@@ -28,7 +28,6 @@ struct TreeArgs {
     long long q_stride, kv_stride;
     const int32_t *parents, *n_nodes, *seqs, *kv_lens;
     int B, N, max_len;
-    int one;      // 1: a block a (sequence, KV head), none is cut
     void* out;
     int4* meta;   // [blocks]: the first piece of each
     float4* part; // [blocks][2][PART][128]
@@ -266,7 +265,9 @@ __device__ __forceinline__ bool finite16(uint32_t half) { return (half & 0x7F80u
 // scores (one third of it instructions that come from L2), some 1400 cycles a tile, which memory needs too, 3 us at the end of each
 // piece and of the launch, 3 for the launch that merges. fp32, 8 x 16384 keys, 64 nodes 136 us: the tensor cores (24 products of 128 x 64 x 16 for the
 // scores of a tile, 12 of 128 x 128 x 16 for its sums, 2100 cycles).
-template <bool F32>
+//
+// ONE: a share is a sequence, and none is cut.
+template <bool F32, bool ONE>
 __global__ void __launch_bounds__(NT, 1)
     k_tree_attn(const __grid_constant__ CUtensorMap pool_map, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                 const __grid_constant__ CUtensorMap q_map, Pages c, TreeArgs a, Plan plan) {
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(NT, 1)
         if (threadIdx.x == 0) {
             set_err(c.err, TTS_BB_TREE_ERR_TIMEOUT);
             pdl_wait();
-            if (!a.one) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+            if (!ONE) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
         }
         return;
     }
@@ -322,46 +323,59 @@ __global__ void __launch_bounds__(NT, 1)
         share = (units + shares - 1) / shares;
         first = me / NKV * share;
     };
-#pragma unroll 1
-    for (int turn = one_turn; turn < 2; ++turn) {
-        before = 0;
-#pragma unroll 1
-        for (int i0 = 0; i0 < a.B && (turn == 0 || before <= first); i0 += NT) {
-            const int i = i0 + tid;
+    if constexpr (ONE) {  // a sequence a share: no deal
+        if (tid == 0) {
+            const int b = me / NKV;
             int row = 0, len = 0, nodes = 0;
-            const uint32_t n = i < a.B && sequence(c, a, i, turn == one_turn && me == 0, row, len, nodes) ? a.one ? 1 : tiles_of(len) : 0;
-            uint32_t incl = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t w = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += w;
-            }
-            __syncthreads();
-            if (lane == 31) sh.sums[warp] = incl;
-            __syncthreads();
-            uint32_t of = lane < WARPS ? sh.sums[lane] : 0, upto = of;
-#pragma unroll
-            for (int o = 1; o < WARPS; o <<= 1) {
-                const uint32_t w = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += w;
-            }
-            const uint32_t mine = before + __shfl_sync(0xffffffffu, upto - of, warp) + incl - n;
-            before += __shfl_sync(0xffffffffu, upto, WARPS - 1);
-            if (one_turn) deal(before);
-            if (turn && first >= mine && first < mine + n) {
-                sh.start[0] = i;
-                sh.start[1] = (int)(first - mine);
-                sh.start[2] = row;
-                sh.start[3] = len;
-                sh.start[4] = nodes;
-            }
+            const bool any = sequence(c, a, b, me % NKV == 0, row, len, nodes);
+            sh.start[0] = b;
+            sh.start[1] = 0;
+            sh.start[2] = row;
+            sh.start[3] = any ? len : -1;
+            sh.start[4] = nodes;
         }
-        if (turn == 0) deal(before);
+    } else {
+#pragma unroll 1
+        for (int turn = one_turn; turn < 2; ++turn) {
+            before = 0;
+#pragma unroll 1
+            for (int i0 = 0; i0 < a.B && (turn == 0 || before <= first); i0 += NT) {
+                const int i = i0 + tid;
+                int row = 0, len = 0, nodes = 0;
+                const uint32_t n = i < a.B && sequence(c, a, i, turn == one_turn && me == 0, row, len, nodes) ? tiles_of(len) : 0;
+                uint32_t incl = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t w = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += w;
+                }
+                __syncthreads();
+                if (lane == 31) sh.sums[warp] = incl;
+                __syncthreads();
+                uint32_t of = lane < WARPS ? sh.sums[lane] : 0, upto = of;
+#pragma unroll
+                for (int o = 1; o < WARPS; o <<= 1) {
+                    const uint32_t w = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += w;
+                }
+                const uint32_t mine = before + __shfl_sync(0xffffffffu, upto - of, warp) + incl - n;
+                before += __shfl_sync(0xffffffffu, upto, WARPS - 1);
+                if (one_turn) deal(before);
+                if (turn && first >= mine && first < mine + n) {
+                    sh.start[0] = i;
+                    sh.start[1] = (int)(first - mine);
+                    sh.start[2] = row;
+                    sh.start[3] = len;
+                    sh.start[4] = nodes;
+                }
+            }
+            if (turn == 0) deal(before);
+        }
     }
     __syncthreads();
     tc_after();
     const uint32_t tmem = sh.tmem;
-    const uint32_t U = first >= units ? 0 : a.one ? tiles_of(sh.start[3]) : min(share, units - first);  // this block's tiles
+    const uint32_t U = ONE ? (sh.start[3] < 0 ? 0 : tiles_of(sh.start[3])) : first >= units ? 0 : min(share, units - first);  // this block's tiles
     bool ok = true;
     const auto wait = [&](u64* bar, uint32_t parity) {  // by whole warps
         ok = wait_for(&sh.abort, bar, parity);
@@ -624,7 +638,7 @@ __global__ void __launch_bounds__(NT, 1)
             int t = 0, vs = 0;
             uint32_t vp = 0, k = ~0u;
             Piece* p = nullptr;
-            if (U == 0 && lane == 0 && !a.one) a.meta[me] = make_int4(-1, 0, 0, 0);
+            if (U == 0 && lane == 0 && !ONE) a.meta[me] = make_int4(-1, 0, 0, 0);
 #pragma unroll 1
             for (uint32_t u = 0; ok && u < U; ++u) {
                 if (!p) {
@@ -642,7 +656,7 @@ __global__ void __launch_bounds__(NT, 1)
                         p->ok = tree_ok;
                         arrive(&sh.seen_full[k % PIECES]);
                         // of the share's first piece: its sequence, nodes, and whether it begins inside of that; bit 2: in order
-                        if (k == 0 && !a.one) a.meta[me] = make_int4(p->b, p->n, (t > 0) | tree_ok << 2, 0);
+                        if (k == 0 && !ONE) a.meta[me] = make_int4(p->b, p->n, (t > 0) | tree_ok << 2, 0);
                     }
                 }
                 if (!wait(&sh.v_full[vs], vp)) break;
@@ -921,7 +935,7 @@ __global__ void __launch_bounds__(NT, 1)
                     halves(o[2 * i + 1], x.z, x.w);
                     return x;
                 };
-                if (!p.whole) {
+                if (!ONE && !p.whole) {
                     if (r < rows) {  // rows side by side: whole lines
 #pragma unroll
                         for (int i = 0; i < HD / 4; ++i) part[i * 128] = four(i);
@@ -964,7 +978,7 @@ __global__ void __launch_bounds__(NT, 1)
                         for (int d = 0; d < HD; ++d) {
                             const float y = bf2f(v[d]);
                             if (fabsf(y) <= 3.4028235e38f) continue;
-                            if (!p.whole) reinterpret_cast<float*>(part + (d >> 2) * 128)[d & 3] += y;
+                            if (!ONE && !p.whole) reinterpret_cast<float*>(part + (d >> 2) * 128)[d & 3] += y;
                             else if (p.ok) row[d] = (T)((float)row[d] + y);
                         }
                     }
@@ -1045,7 +1059,7 @@ __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
 }
 
 // Shares of the launch: 8 blocks each, one an SM in all, or a tile a share where there are fewer; few and short sequences are not cut,
-// which saves the launch that merges: 1 x 333 keys 9.5 us (and 3 of the host's), in shares 10.1; 1 x 1000 15.5 and 14.2.
+// which saves the deal and the launch that merges: 1 x 333 keys 8.3 us (and 3 of the host's), in shares 10.1; 1 x 1000 15.5 and 14.2.
 constexpr int ONE_TILES = 8;
 bool one_block(int B, int max_len) { return B <= SHARES && tiles_of(max_len) <= ONE_TILES; }
 int share_count(int B, int max_len) { return one_block(B, max_len) ? B : (int)std::min<long long>(SHARES, (long long)B * tiles_of(max_len)); }
@@ -1088,28 +1102,29 @@ TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int la
         (type == TTS_BB_T_BF16 && !tc_make_map_heads(&q_map, q, B * N, NQ, q_stride, N)))
         return TTS_BB_E_CUDA;
     if (type != TTS_BB_T_BF16) q_map = k_map;  // not used
-    const TreeArgs a{q, static_cast<const bf16*>(v), q_stride, kv_stride, parents, n_nodes, seqs, kv_lens, B, N, max_len, one_block(B, max_len), out,
+    const TreeArgs a{q, static_cast<const bf16*>(v), q_stride, kv_stride, parents, n_nodes, seqs, kv_lens, B, N, max_len, out,
                      static_cast<int4*>(workspace), reinterpret_cast<float4*>(static_cast<char*>(workspace) + META_BYTES)};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int shares = share_count(B, max_len);
     bool regs = true;
-    const auto go = [&](auto f32) {
-        constexpr bool F32 = decltype(f32)::value;
+    const bool one = one_block(B, max_len);
+    const auto go = [&](auto f32, auto single) {
+        constexpr bool F32 = decltype(f32)::value, ONE = decltype(single)::value;
         static SmemState state;
-        allow_smem(state, k_tree_attn<F32>, SMEM_MAX);
+        allow_smem(state, k_tree_attn<F32, ONE>, SMEM_MAX);
         // what its warps deal anew has to be there at the launch: they would wait for it
         static const bool enough = [] {
             cudaFuncAttributes f{};
-            return cudaFuncGetAttributes(&f, k_tree_attn<F32>) == cudaSuccess && f.numRegs >= 128;
+            return cudaFuncGetAttributes(&f, k_tree_attn<F32, ONE>) == cudaSuccess && f.numRegs >= 128;
         }();
         regs = enough;
         if (!regs) return;
         const Plan plan = plan_of<F32>(N);
-        launch_pdl(k_tree_attn<F32>, shares * NKV, NT, plan.bytes<F32>(), st, pool_map, k_map, v_map, q_map, c, a, plan);
-        if (shares > 1 && !a.one && tiles_of(max_len) > 1)
+        launch_pdl(k_tree_attn<F32, ONE>, shares * NKV, NT, plan.bytes<F32>(), st, pool_map, k_map, v_map, q_map, c, a, plan);
+        if (!ONE && shares > 1 && tiles_of(max_len) > 1)
             launch_pdl(k_tree_combine<std::conditional_t<F32, float, bf16>>, dim3((shares - 1) * NKV, (2 * N + 31) / 32, 4), 128, 0, st, a, shares);
     };
-    if (type == TTS_BB_T_F32) go(std::true_type{});
-    else go(std::false_type{});
+    if (type == TTS_BB_T_F32) one ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+    else one ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
     return regs ? launched() : TTS_BB_E_CUDA;
 }
