@@ -1058,11 +1058,16 @@ __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
     }
 }
 
-// Shares of the launch: 8 blocks each, one an SM in all, or a tile a share where there are fewer; few and short sequences are not cut,
-// which saves the deal and the launch that merges: 1 x 333 keys 8.3 us (and 3 of the host's), in shares 10.1; 1 x 1000 15.5 and 14.2.
-constexpr int ONE_TILES = 8;
-bool one_block(int B, int max_len) { return B <= SHARES && tiles_of(max_len) <= ONE_TILES; }
-int share_count(int B, int max_len) { return one_block(B, max_len) ? B : (int)std::min<long long>(SHARES, (long long)B * tiles_of(max_len)); }
+// Shares of the launch: 8 blocks each, one an SM in all, or a tile a share where there are fewer. Few and short sequences are not cut, which
+// saves the deal and the launch that merges, as long as what a cut would take from the longest is worth fewer than 10 tiles (fp32: 5). bf16, 6
+// nodes: 1 x 333 keys 8.3 us (and 3 of the host's), in shares 8.9; 1 x 1200 14.9 and 11.9; 19 x 120..1200 15.5 and 18.3. fp32, 25 nodes: 1 x
+// 100 9.2 and 9.3, 1 x 320 12.1 and 10.3, 12 x 64..640 18.0 and 19.7. Up to 20 tiles: where only one sequence is long, it bounds all.
+constexpr int ONE_TILES = 20;
+bool one_block(int B, int max_len, bool f32) {
+    const int t = tiles_of(max_len);
+    return B <= SHARES && t <= ONE_TILES && t * (SHARES - B) <= SHARES * (f32 ? 5 : 10);
+}
+int share_count(int B, int max_len) { return (int)std::min<long long>(SHARES, (long long)B * tiles_of(max_len)); }
 constexpr size_t META_BYTES = (SHARES * NKV * sizeof(int4) + 255) / 256 * 256;
 // As many pages of K and V as fit behind the queries.
 template <bool F32>
@@ -1078,7 +1083,8 @@ Plan plan_of(int N) {
 
 TTS_API size_t tts_bb_tree_attention_workspace(int B, int N, int max_len) {
     if (!tree_ok(B, N) || max_len < 0 || max_len > (1 << 30) || (long long)B * max_len > (1ll << 33)) return 0;
-    return one_block(B, max_len) ? 0 : META_BYTES + (size_t)share_count(B, max_len) * NKV * 2 * PART * 128 * sizeof(float4);
+    // (what bf16 calls cut, fp32 calls cut too)
+    return one_block(B, max_len, true) ? 0 : META_BYTES + (size_t)share_count(B, max_len) * NKV * 2 * PART * 128 * sizeof(float4);
 }
 
 TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int layer, int B, int N, const void* q, int type,
@@ -1105,9 +1111,8 @@ TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int la
     const TreeArgs a{q, static_cast<const bf16*>(v), q_stride, kv_stride, parents, n_nodes, seqs, kv_lens, B, N, max_len, out,
                      static_cast<int4*>(workspace), reinterpret_cast<float4*>(static_cast<char*>(workspace) + META_BYTES)};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int shares = share_count(B, max_len);
     bool regs = true;
-    const bool one = one_block(B, max_len);
+    const bool one = one_block(B, max_len, type == TTS_BB_T_F32);
     const auto go = [&](auto f32, auto single) {
         constexpr bool F32 = decltype(f32)::value, ONE = decltype(single)::value;
         static SmemState state;
@@ -1120,6 +1125,7 @@ TTS_API tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int la
         regs = enough;
         if (!regs) return;
         const Plan plan = plan_of<F32>(N);
+        const int shares = ONE ? B : share_count(B, max_len);
         launch_pdl(k_tree_attn<F32, ONE>, shares * NKV, NT, plan.bytes<F32>(), st, pool_map, k_map, v_map, q_map, c, a, plan);
         if (!ONE && shares > 1 && tiles_of(max_len) > 1)
             launch_pdl(k_tree_combine<std::conditional_t<F32, float, bf16>>, dim3((shares - 1) * NKV, (2 * N + 31) / 32, 4), 128, 0, st, a, shares);

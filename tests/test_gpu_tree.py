@@ -138,6 +138,18 @@ def test_attention_of_many_sequences(io):
 
 
 @IO
+@pytest.mark.parametrize("B, longest", [(1, 256), (1, 257), (1, 576), (1, 577), (4, 320), (4, 641), (4, 769), (12, 641), (19, 1216), (19, 1217), (20, 65)])
+def test_attention_of_few_sequences_whole_and_cut(io, B, longest):
+    """On both sides of what decides whether a sequence is cut; one of no keys, padding, and a longest one last."""
+    lens = [int(x) for x in np.random.default_rng(B + longest).integers(0, longest + 1, B)]
+    lens[-1] = longest
+    if B > 2:
+        lens[1] = 0
+    c = Case(40 + B, lens, 5, io, rows=[-1 if B > 3 and b == 2 else b for b in range(B)])
+    c.check(c.run(seqs=c.rows), skip=[2] if B > 3 else ())
+
+
+@IO
 def test_attention_of_more_sequences_than_threads(io):
     """Lengths are summed in several turns of a block; every seventh sequence is padding or out of range."""
     rng = np.random.default_rng(51)
