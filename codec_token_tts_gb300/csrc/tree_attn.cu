@@ -46,7 +46,6 @@ struct Piece {
     // of pieces that hold the tree, a little later:
     int ok;                 // the tree is in order
     u64 seen[MAX_NODES];    // ancestors and self
-    int up[MAX_NODES];
 };
 
 // bf16: queries as they are, weights in two bf16 parts (17 bits, both rounded). fp32: queries and weights in three parts
@@ -73,8 +72,8 @@ struct Lay {
 // Warps of single tasks: the loader and the issuer of sums beside the rows that trees of up to 32 nodes leave empty (warps of one index modulo
 // 4 share a scheduler, and 0 and 1 are busy then): 8 x 65537 keys, 31 nodes 326 us, with the loader beside warp 0 or 1 375.
 constexpr int W_SUM = 8, W_REST = 12, W_SAFE = 12, W_S = 13, W_LOAD = 14, W_PV = 15, WARPS = 16, NT = WARPS * 32;
-// registers of a thread: the launch's 128 are dealt anew
-constexpr int REGS_SOFT = 112, REGS_SUM = 208, REGS_REST = 80;
+// registers of a thread: the launch's 128 are dealt anew (208 for the sums and 80 for the rest: fp32 spills, 16 x 200..2000 keys 33.6 us, now 33.0)
+constexpr int REGS_SOFT = 112, REGS_SUM = 200, REGS_REST = 88;
 static_assert(2 * REGS_SOFT + REGS_SUM + REGS_REST == 4 * 128, "registers of the launch");
 constexpr int PIECES = 4;       // descriptors in flight
 constexpr int RING = 8;         // tiles whose references and weights are kept
@@ -220,48 +219,61 @@ __device__ __forceinline__ bool sequence(const Pages& c, const TreeArgs& a, int 
 }
 __host__ __device__ constexpr int tiles_of(int len) { return (len + KVB - 1) / KVB + 1; }
 
-// A warp finds what each node sees, in shared memory. By doubling: what is seen within 2^k steps, and the node 2^k steps up. False
-// where a parent is out of order (taken as -1 then).
-__device__ __forceinline__ bool ancestors(const int32_t* parents, int n, int lane, u64* seen, int* up) {
-    bool bad = false, more = false;
-#pragma unroll 1
-    for (int j = lane; j < MAX_NODES; j += 32) {
-        int u = j < n ? parents[j] : -1;
-        const bool wrong = u < -1 || u >= j;
-        bad |= wrong;
-        if (wrong) u = -1;
-        more |= u >= 0;
-        up[j] = u;
-        seen[j] = 1ull << j;
-    }
-    while (__any_sync(0xffffffffu, more)) {
-        more = false;
-#pragma unroll 1
-        for (int j = lane; j < MAX_NODES; j += 32) {
-            __syncwarp();
-            const int u = up[j], v = u < 0 ? -1 : up[u];
-            const u64 m = u < 0 ? 0ull : seen[u];
-            __syncwarp();
-            seen[j] |= m;
-            up[j] = v;
-            more |= v >= 0;
+// What each node sees, by doubling: what is seen within 2^k steps, and the node 2^k steps up. Nodes lane and lane + 32 of a warp. 200 x 3..30
+// keys, 64 nodes: 54 us, through shared memory 63.
+struct Line {
+    u64 seen[2];
+    int up[2];
+    bool in_order;  // or a parent was not (taken as -1)
+
+    __device__ __forceinline__ void begin(const int32_t* parents, int n, int lane) {
+        in_order = true;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = lane + 32 * h;
+            up[h] = j < n ? parents[j] : -1;
+            seen[h] = 1ull << j;
         }
-        __syncwarp();
     }
-    return !__any_sync(0xffffffffu, bad);
-}
+    // one round; whether there are more
+    __device__ __forceinline__ bool step(int lane) {
+        bool bad = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool wrong = up[h] < -1 || up[h] >= lane + 32 * h;
+            bad |= wrong;
+            if (wrong) up[h] = -1;
+        }
+        in_order &= !__any_sync(0xffffffffu, bad);
+        u64 more[2];
+        int above[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const u64 s0 = __shfl_sync(0xffffffffu, seen[0], up[h] & 31), s1 = __shfl_sync(0xffffffffu, seen[1], up[h] & 31);
+            const int v0 = __shfl_sync(0xffffffffu, up[0], up[h] & 31), v1 = __shfl_sync(0xffffffffu, up[1], up[h] & 31);
+            more[h] = up[h] < 0 ? 0ull : up[h] < 32 ? s0 : s1;
+            above[h] = up[h] < 0 ? -1 : up[h] < 32 ? v0 : v1;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            seen[h] |= more[h];
+            up[h] = above[h];
+        }
+        return __any_sync(0xffffffffu, up[0] >= 0 || up[1] >= 0);
+    }
+};
 
 __device__ __forceinline__ bool finite16(uint32_t half) { return (half & 0x7F80u) != 0x7F80u; }
 
 // grid: 8 blocks a share, 512 threads. The tiles of all sequences are one line, cut into equal shares, and the 8 KV heads walk it side
-// by side, a block each: what they read at a time lies together (64 x 200..2000 keys, 64 nodes: 74 us; heads one after the other 81). Warp
+// by side, a block each: what they read at a time lies together (64 x 200..2000 keys, 64 nodes: 74 us then; heads one after the other 81). Warp
 // 14 deals the pieces of its share and loads pages (and bf16 queries) by TMA, 12 finds the nodes' ancestors and makes values safe to be
 // multiplied by 0, 13 issues the scores S = Q K^T and 15 the sums O = P V (two warps, since an issuer waits for its products: one took
 // turns, and the tensor cores waited meanwhile: 90 us for 97). Warps 0 .. 7 turn scores into weights (a thread a row, even and odd
 // tiles by four each), which replace them in TMEM as the A operand of P V; they hand the running maximum on. Warps 8 .. 11 add
 // the tiles' sums to those in their registers. Every wait is bounded.
 //
-// Measured: 8 x 65537 keys, 31 nodes 313 us, 6.9 TB/s: memory. 64 x 200..2000 keys, 64 nodes 73 us, 4.7 TB/s: 5 us until the first
+// Measured: 8 x 65537 keys, 31 nodes 313 us, 6.9 TB/s: memory. 64 x 200..2000 keys, 64 nodes 71 us, 4.8 TB/s: 5 us until the first
 // scores (one third of it instructions that come from L2), some 1400 cycles a tile, which memory needs too, 3 us at the end of each
 // piece and of the launch, 3 for the launch that merges. fp32, 8 x 16384 keys, 64 nodes 136 us: the tensor cores (24 products of 128 x 64 x 16 for the
 // scores of a tile, 12 of 128 x 128 x 16 for its sums, 2100 cycles).
@@ -647,8 +659,14 @@ __global__ void __launch_bounds__(NT, 1)
                     p = &sh.piece[k % PIECES];
                     t = p->t0;
                     bool tree_ok = true;
-                    if (p->t1 == p->tiles) {
-                        tree_ok = ancestors(a.parents + (size_t)p->b * a.N, p->n, lane, p->seen, p->up);
+                    if (p->t1 == p->tiles) {  // the tiles' values wait meanwhile, so all of it stays in registers
+                        Line line;
+                        line.begin(a.parents + (size_t)p->b * a.N, p->n, lane);
+                        while (line.step(lane)) {
+                        }
+                        p->seen[lane] = line.seen[0];
+                        p->seen[lane + 32] = line.seen[1];
+                        tree_ok = line.in_order;
                         if (!tree_ok && lane == 0) set_err(c.err, TTS_BB_TREE_ERR_TREE);
                     }
                     __syncwarp();
