@@ -37,8 +37,10 @@ __device__ __forceinline__ u64 fix60(float x) {
 }
 // a * b / 2^s
 __device__ __forceinline__ u64 mul_shift(u64 a, u64 b, int s) { return (__umul64hi(a, b) << (64 - s)) | (a * b >> s); }
-// what c (in 2^-58) times q leaves of p
+// what c (in 2^-58) times q leaves of p: nothing where the product is 16 or more, which is beyond 64 bits (c grows by up to 1 with each of
+// up to 63 rejections, and q may be 1)
 __device__ __forceinline__ u64 rest60(u64 p, u64 c, u64 q) {
+    if (__umul64hi(c, q) >> 58) return 0ull;
     const u64 t = mul_shift(c, q, 58);
     return p > t ? p - t : 0ull;
 }

@@ -538,6 +538,34 @@ def test_verify_counts_a_rest_below_the_rounding_of_its_product():
     assert list(count) == [1, 1, 1, 1]
 
 
+@pytest.mark.parametrize("V", [2, 70, 5000])
+@pytest.mark.parametrize("top", [1.0, 0.98])
+def test_verify_of_stars_whose_draft_repeats_one_token(V, top):
+    """17 to 63 children of the root, all (but for one at the end) of the token that the draft gives `top`, all rejected: c, the sum of
+    what the rejections leave, passes 16 (and with that what 64 bits hold of c q in 2^-60) and 32."""
+    N, likely, nexts = 64, (0.06, 0.3, 0.45), (0.0, 0.004, 0.01, 0.05, 0.4)
+    todo = [(p0, n, un) for p0 in likely for n in range(18, N + 1) for un in nexts]
+    t = Trees(1, len(todo), N, 2, True)
+    rng = np.random.default_rng(V)
+    t.V = V
+    t.parents[:] = [-1] + [0] * (N - 1)
+    t.nodes = [n for _, n, _ in todo]
+    t.tokens[:] = 0
+    t.u[:] = 0.9
+    t.un = np.array([un for _, _, un in todo], np.float32)
+    others = rng.dirichlet(np.ones(V - 1), len(todo))
+    root = np.arange(len(todo)) * N
+    t.p, t.q = (np.zeros((len(todo) * N, V), np.float32) for _ in range(2))
+    t.p[root, 0] = [p0 for p0, _, _ in todo]
+    t.p[root, 1:] = (1 - np.array([[p0] for p0, _, _ in todo])) * others
+    t.q[root, 0] = top
+    t.q[root, 1:] = (1 - top) / (V - 1)
+    for b, n in enumerate(t.nodes):
+        if b % 3 == 0:
+            t.tokens[b, n - 1] = V - 1
+    assert len(t.check(least=1e-7)) > 0.9 * len(todo)
+
+
 @DRAWN
 def test_verify_with_values_that_are_no_probabilities(drawn):
     """NaN, infinities, negative and large values: some path and some token, and no other sequence's changes."""
