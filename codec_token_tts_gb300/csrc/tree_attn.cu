@@ -2,7 +2,7 @@
 //
 // The two query heads of a KV head and up to 64 nodes are the 128 rows of a tile of the tensor cores: row 2 i + h is node i's
 // head 2 g + h. A sequence's keys are its cache pages of 64 and, behind them, one page of the tree's own keys, masked by
-// each node's ancestors. Sums: out = sum_j 2^(c s_j - m) v_j / sum_j 2^(c s_j - m), c = log2 e / sqrt 128, with the running
+// each node's ancestors. Sums: out = sum_j 2^(c (s_j - m)) v_j / sum_j 2^(c (s_j - m)), c = log2 e / sqrt 128, with the running
 // maximum m of the tiles so far (bf16: within a factor of 4 of it). Scores, softmax and sums are fp32; the sums of a tile (bf16: of two) are
 // added to those before in registers, since the tensor cores' own accumulation cuts off what it shifts out.
 //
@@ -36,6 +36,10 @@ struct TreeArgs {
 constexpr int PAGE_BYTES = KVB * HD * 2;  // K or V of a page and head
 constexpr int PART = HD / 4 + 1;          // a row's 128 sums by four, then its reference and weight: rows side by side
 constexpr int SHARES = 152 / NKV;         // times 8 blocks: one an SM
+
+// Exponents of 2 are (score - reference) CS, the difference first: in score CS - reference CS the rounding of the second product, up to 2^-25 of
+// it, would be the exponent of the largest weight, which beyond 2^31 is 0 or infinite.
+constexpr float CS = 0.08838834764831845f * 1.4426950408889634f;
 
 // A share's work: a piece of the tiles (a page each) of one (sequence, KV head), the last of which is the tree.
 struct Piece {
@@ -198,6 +202,11 @@ __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
 __device__ __forceinline__ u64 add2(u64 a, u64 b) {
     u64 d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+    u64 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
@@ -739,7 +748,6 @@ __global__ void __launch_bounds__(NT, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
         const int group = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-        const float cs = 0.08838834764831845f * 1.4426950408889634f;
         uint32_t u0 = 0;  // tiles before the piece
 #pragma unroll 1
         for (uint32_t k = 0; ok; ++k) {
@@ -790,7 +798,7 @@ __global__ void __launch_bounds__(NT, 1)
                 if (lane == 0) arrive(&sh.q_full[0]);
             }
             const bool mine = quarter * 32 < rows;
-            float mc = -INFINITY, l = 0.f;  // of this warp's tiles: the reference, and the sum of weights
+            float before = -INFINITY, l = 0.f;  // of this warp's tiles: the reference, and the sum of weights
 #pragma unroll 1
             for (int j = (int)(u0 ^ group) & 1; j < nt; j += 2) {
                 const int t = p.t0 + j;
@@ -832,9 +840,9 @@ __global__ void __launch_bounds__(NT, 1)
                 if (u > 0) {
                     if (!wait(&sh.m_full[quarter][(u - 1) & 1], ((u - 1) >> 1) & 1u)) break;
                     if (u > u0) {
-                        const float before = sh.m[(u - 1) % RING][r];
-                        if ((m - before) * cs > L::SLACK) rose = r < rows;
-                        else m = before;
+                        const float other = sh.m[(u - 1) % RING][r];
+                        if ((m - other) * CS > L::SLACK) rose = r < rows;
+                        else m = other;
                     }
                 }
                 if constexpr (L::GROUP > 1) {
@@ -845,8 +853,8 @@ __global__ void __launch_bounds__(NT, 1)
                 __syncwarp();
                 if (lane == 0) arrive(&sh.m_full[quarter][u & 1]);
                 if (mine) {
-                    const float now = m * cs, base = m == -INFINITY ? 0.f : now;
-                    const u64 cs2 = pair(cs, cs), base2 = pair(-base, -base), minus = pair(-1.f, -1.f);
+                    const float base = m == -INFINITY ? 0.f : m;
+                    const u64 cs2 = pair(CS, CS), base2 = pair(-base, -base), minus = pair(-1.f, -1.f);
                     u64 sum[2] = {0, 0};
                     // the third parts' columns were taken by the product of this group's tile before
                     if (F32 && u >= 2 && !wait(&sh.w_empty[(u - 2) % L::REGIONS], ((u - 2) / L::REGIONS) & 1u)) break;
@@ -858,7 +866,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float x, y;
-                            halves(fma2(pair(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cs2, base2), x, y);
+                            halves(mul2(add2(pair(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), base2), cs2), x, y);
                             u64 e = pair(at_ex2(x), at_ex2(y));
                             sum[i & 1] = add2(sum[i & 1], e);
 #pragma unroll
@@ -875,8 +883,8 @@ __global__ void __launch_bounds__(NT, 1)
                     float x, y, z, v;
                     halves(sum[0], x, y);
                     halves(sum[1], z, v);
-                    l = (l == 0.f ? 0.f : l * at_ex2(mc - base)) + ((x + y) + (z + v));
-                    mc = now;
+                    l = (l == 0.f ? 0.f : l * at_ex2((before - base) * CS)) + ((x + y) + (z + v));
+                    before = m;
                     if (j + 2 >= nt) sh.l[u % RING][r] = l;
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 }
@@ -894,7 +902,6 @@ __global__ void __launch_bounds__(NT, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SUM));
         const int quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = tmem + 256 + ((uint32_t)(quarter * 32) << 16);
-        const float cs = 0.08838834764831845f * 1.4426950408889634f;
         uint32_t u = 0, turn = 0;
 #pragma unroll 1
         for (uint32_t k = 0; ok; ++k) {
@@ -906,7 +913,7 @@ __global__ void __launch_bounds__(NT, 1)
             u64 o[HD / 2];
 #pragma unroll
             for (int i = 0; i < HD / 2; ++i) o[i] = 0;
-            float m = -INFINITY, l = 0.f;  // the reference, times cs
+            float m = -INFINITY, l = 0.f;  // the reference
 #pragma unroll 1
             for (int t = 0; t < nt; ++t, ++u, ++turn) {
                 if (!wait(&sh.o_full[turn & 1], (turn >> 1) & 1u)) break;
@@ -917,7 +924,7 @@ __global__ void __launch_bounds__(NT, 1)
                 u += more;
                 if (mine) {
                     tc_after();
-                    const float now = sh.m[u % RING][r] * cs, f = first ? 0.f : now == m ? 1.f : at_ex2(m - now);
+                    const float now = sh.m[u % RING][r], f = first ? 0.f : now == m ? 1.f : at_ex2((m - now) * CS);
                     const u64 f2 = pair(f, f);
                     const uint32_t at = lanes + (turn & 1) * 128;
                     uint32_t x[2][32];  // the next 32 dims are on their way while these are added
@@ -1051,7 +1058,7 @@ __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, w[i].x);
-        const float base = top == -INFINITY ? 0.f : top, f0 = at_ex2(M - base);
+        const float base = top == -INFINITY ? 0.f : top, f0 = at_ex2((M - base) * CS);
         M = top;
         l *= f0;
 #pragma unroll
@@ -1059,7 +1066,7 @@ __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (i0 + i > more) break;
-            const float f = at_ex2(w[i].x - base);
+            const float f = at_ex2((w[i].x - base) * CS);
             l += f * w[i].y;
 #pragma unroll
             for (int d = 0; d < 2; ++d) { o[d].x += f * x[i][d].x; o[d].y += f * x[i][d].y; o[d].z += f * x[i][d].z; o[d].w += f * x[i][d].w; }

@@ -294,6 +294,35 @@ def test_attention_of_large_and_small_scores(io):
 
 
 @IO
+@pytest.mark.parametrize("N, lens", [(5, [100, 7]), (33, [5000, 130])])
+@pytest.mark.parametrize("size", [13, 15, 17, 30, 59])
+@pytest.mark.parametrize("shape", ["equal", "rising", "falling", "mixed"])
+def test_attention_of_scores_far_from_zero(io, N, lens, size, shape):
+    """Queries and keys of 2^size: scores of which the greatest take all, equally, whole sequences and cut ones. Keys are 2^size times one of
+    few numbers of 8 bits, so equal keys' scores are equal and others' 2^18 apart at least."""
+    c = Case(28, lens, N, io)
+    rng = np.random.default_rng(size)
+    pages = -(-max(lens) // BLK)
+    of_page = {"equal": np.full(pages, 77), "rising": np.arange(pages) + 5, "falling": 120 - np.arange(pages), "mixed": rng.integers(0, 128, pages)}[shape]
+    f = lambda i: 2.0 ** size * (1 + np.asarray(i) / 128)
+    for b, n in enumerate(c.lens):
+        page = np.arange(n) // BLK
+        x = f(of_page[page])
+        c.pool[0, dev(c.table[b]).long()[dev(page)], 0, :, dev(np.arange(n) % BLK)] = dev(x).bfloat16()[:, None, None]
+        c.k[b][:] = x[:, None, None]
+    q, tk = c.q.view(len(lens), N, NQ, HD), c.tk.view(len(lens), N, NKV, HD)
+    q[:] = 2.0 ** size * (1 + 2.0 ** (-20 if io == "float32" else -6))
+    q[:, :, 1::2] *= -1
+    tk[:] = dev(f(np.full((len(lens), N), 77) if shape == "equal" else rng.integers(0, 128, (len(lens), N)))).bfloat16()[:, :, None, None]
+    got = c.run().double().cpu().numpy().reshape(len(lens), N, NQ, HD)
+    for b, n in enumerate(lens):
+        w, mag, _ = c.want(b)
+        # the exponentials of 0 and the sums; bf16: weights in two parts, the result rounded
+        tol = mag * (2 * 2.0 ** -21 + (n + N + 32) * U) + (mag * 2.0 ** -15 + np.abs(w) * 2.0 ** -8 if io == "bfloat16" else 0)
+        assert (np.abs(got[b] - w) <= tol).all(), (b, np.abs(got[b] - w).max())
+
+
+@IO
 @pytest.mark.parametrize("step", ["little", "much", "either", "once"])
 @pytest.mark.parametrize("who", ["all", "last"])
 def test_attention_of_scores_that_rise_from_page_to_page(io, step, who):
