@@ -7,9 +7,10 @@
 // parent's, so one walk over the nodes in their order meets each accepted node's children in turn.
 //
 // Sums decide which whole number is the answer, so they have to hold far more bits than a float. A thread adds its ids' rests in pairs of
-// floats (the sum, and what its roundings left; two ids an instruction), some 2^-46 of the sum; between threads they are whole numbers of
-// 2^-60, whose order does not matter. The ids around the answer are then gone through in whole numbers of 2^-60 alone: exact for
-// probabilities from 2^-37 up (24 bits above 2^-60), cut off at 2^-60 below that.
+// floats (the sum, and what its roundings left; two ids an instruction: 2^-48 of the sum and less, of the tens of ids that a thread has of
+// 151676); between threads they are whole numbers of 2^-60, whose order does not matter. Up to 16384 threads' halves are cut off there,
+// so a sum is off by 2^-46 of the row's 1 at most, however little is left, and c by that for each rejection. The ids around the answer are
+// then gone through in whole numbers of 2^-60 alone: exact for probabilities from 2^-37 up (24 bits above 2^-60), cut off at 2^-60 below that.
 #include <algorithm>
 
 #include "tree.cuh"

@@ -6,7 +6,7 @@ import pytest
 
 from tests.gpu_util import tb
 from tests.lowbit_util import U, attention_tol
-from tests.tree_util import BLK, BLOCK, HD, NKV, NQ, random_tree, tree_attention, verify, verify_greedy
+from tests.tree_util import BLK, BLOCK, HD, NKV, NQ, random_tree, tree_attention, verify, verify_exactly, verify_greedy
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -593,6 +593,35 @@ def test_verify_of_stars_whose_draft_repeats_one_token(V, top):
         if b % 3 == 0:
             t.tokens[b, n - 1] = V - 1
     assert len(t.check(least=1e-7)) > 0.9 * len(todo)
+
+
+@pytest.mark.parametrize("V, steps", [(64, 1), (64, 40), (1500, 3), (5003, 60)])
+def test_verify_of_a_draft_next_to_the_target(V, steps):
+    """Rows that differ by a few steps of fp32: what the first rejection of a node leaves is of the size of 2^-24, and the rejections and
+    the next token behind it are of that. Masses are held to some 2^-46 for each rejection (seven here), whatever their size."""
+    B, N = 24, 20
+    t = Trees(V + steps, B, N, V, True, sharp=1.0)
+    rng = np.random.default_rng(V)
+    t.parents[:] = [-1] + [0] * 7 + [1] * 3 + [2] * 3 + [3, 4, 5, 6, 7, 7]
+    t.p[:: N] = np.where(rng.random((B, V)) < 0.02, t.p[:: N] * np.float32(1 + 2.0 ** -20), t.p[:: N])
+    off = rng.integers(-steps, steps + 1, t.p.shape) * np.spacing(t.p)
+    t.q = (t.p + off).astype(np.float32)
+    below = 1 - 2.0 ** -24
+    for b in range(B):  # the root's first child is rejected: its draft lies above the target; a third of the trees end there, behind seven such
+        above = np.nonzero(t.q[b * N] * below >= t.p[b * N].astype(np.float64))[0]
+        t.tokens[b, 1:8] = rng.choice(above, 7) if b % 3 == 0 else rng.integers(0, V, 7)
+        t.tokens[b, 1], t.u[b, 1] = rng.choice(above), below
+    count, path, nxt = t.run()
+    seen, rejected = 0, 0
+    for b in range(B):
+        at = slice(b * N, (b + 1) * N)
+        want, token, near = verify_exactly(t.tokens[b], t.parents[b], t.p[at], t.q[at], t.u[b], t.un[b])
+        if near < 8 * 2.0 ** -46:
+            continue
+        assert count[b] == len(want) and list(path[b]) == want + [-1] * (N - len(want)) and nxt[b] == token, b
+        seen += 1
+        rejected += len(want) == 1
+    assert seen > 0.8 * B and rejected >= 6
 
 
 @DRAWN

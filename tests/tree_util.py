@@ -1,4 +1,6 @@
 """Plain 64-bit forms of the speculative decoding operators (numpy), shared by their tests."""
+from fractions import Fraction
+
 import numpy as np
 
 NQ, NKV, HD, BLK = 16, 8, 128, 64
@@ -73,6 +75,42 @@ def verify(tokens, parents, p, q, u, u_next):
     else:
         token = int(np.argmax(p[node]))
     return path, token, near
+
+
+def verify_exactly(tokens, parents, p, q, u, u_next):
+    """As verify for drawn drafts, of fp32 numbers, without roundings: the distance is that of two masses, of the 1 of a row."""
+    whole = lambda x: int(Fraction(float(x)) * 2 ** 160)  # fp32 numbers from 2^-136 up are whole numbers of 2^-160
+    n, path, node, near = len(tokens), [], 0, 1.0
+    while True:
+        path.append(node)
+        P, Q = [whole(x) for x in p[node]], [whole(x) for x in q[node]]
+        # r is in units of 2^-(160 + e), c of 2^-e, mass of 2^-m
+        r, mass, m, c, e = P, 1, 0, 0, 0
+        found = None
+        for j in range(node + 1, n):
+            if parents[j] != node:
+                continue
+            x = int(tokens[j])
+            gap = (whole(u[j]) * Q[x] * mass << e) - (r[x] << 160 + m)
+            near = min(near, abs(Fraction(gap, 1 << 320 + m + e)))
+            if gap < 0:
+                found = j
+                break
+            c, e = (c << m - e) + mass, m
+            r = [max((a << e) - c * b, 0) for a, b in zip(P, Q)]
+            mass, m = sum(r), 160 + e
+        if found is None:
+            break
+        node = found
+    k, total, cum, token = whole(u_next), sum(r), 0, None
+    for x, y in enumerate(r):
+        cum += y
+        gap = (cum << 160) - k * total
+        if y:
+            near = min(near, abs(Fraction(gap, 1 << 320 + e)))
+        if token is None and gap > 0:
+            token = x
+    return path, P.index(max(P)) if token is None else token, float(near)
 
 
 def verify_greedy(tokens, parents, ids):
