@@ -17,11 +17,6 @@ struct Pages {
     long long layer_stride;
     int n_blocks, n_seqs, bps;
 };
-// The block that holds position pos (below 64 * bps) of a cache row, -1 where the table's entry is out of range.
-__device__ __forceinline__ int page_of(const Pages& c, int row, int pos) {
-    const int p = c.table[(size_t)row * c.bps + pos / KVB];
-    return p >= 0 && p < c.n_blocks ? p : -1;
-}
 // The cache row of sequence b: -1 padding, -2 out of range.
 __device__ __forceinline__ int row_of(const Pages& c, const int32_t* seqs, int b) {
     const int r = seqs ? seqs[b] : b;
