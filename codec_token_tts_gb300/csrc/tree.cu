@@ -566,8 +566,10 @@ __global__ void __launch_bounds__(128) k_tree_commit(Pages c, CommitArgs a) {
     }
 }
 
-// Blocks of a sequence's cluster: one for each BLOCK_IDS, while all sequences' blocks run in two turns. 64 x 151676, 12 nodes: by 8 blocks
-// a sequence 36 us, 4 (one turn) 38, 16 (four) 59.
+// Blocks of a sequence's cluster: one for each BLOCK_IDS, while all sequences' blocks run in two turns, so that what a walk's end leaves free
+// is taken. Drawn drafts of 151676 ids, 64 x 12 nodes: 39.7 us, in one turn (4 blocks a sequence) 44.7, in four (16) 54.9; 128 x 6 nodes 55,
+// 71 and 61. Walks of a pass or two, and shorter rows, would rather have one turn: chosen drafts, 64 x 12 nodes 23.1 us, 17.1 and 39.4;
+// drawn, 32 x 12 nodes 32.2, 28.2 and 32.1; 64 x 12 nodes of 30000 ids 23.4, 17.9 and 23.4.
 int verify_ctas(int B, int V) {
     int n = 1;
     while (n < MAX_CLUSTER && n * BLOCK_IDS < V && 2 * n * B <= 2 * (THREADS_SM / THREADS) * 152) n *= 2;

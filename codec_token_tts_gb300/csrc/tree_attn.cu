@@ -38,7 +38,8 @@ constexpr int PART = HD / 4 + 1;          // a row's 128 sums by four, then its 
 constexpr int SHARES = 152 / NKV;         // times 8 blocks: one an SM
 
 // Exponents of 2 are (score - reference) CS, the difference first: in score CS - reference CS the rounding of the second product, up to 2^-25 of
-// it, would be the exponent of the largest weight, which beyond 2^31 is 0 or infinite.
+// it, would be the exponent of the largest weight, which beyond 2^31 is 0 or infinite. One instruction more for two weights: 1 x 333 keys, 6
+// nodes 8.5 us for 8.3, 8 x 65537, 31 nodes 255 for 250 from L2 and 309 for 309 from memory.
 constexpr float CS = 0.08838834764831845f * 1.4426950408889634f;
 
 // A share's work: a piece of the tiles (a page each) of one (sequence, KV head), the last of which is the tree.
@@ -62,8 +63,8 @@ struct Lay {
     // 96, which need no wait for them: 2500 cycles a tile, 3 regions 2100). Values are loaded AHEAD tiles behind keys
     static constexpr int REGIONS = F32 ? 3 : 4, AHEAD = 2;
     // Tiles whose sums the tensor cores add up where no row's reference rises between them, before warps 8 .. 11 take them: with one of
-    // two buffers a tile, products that end late and the taking of their sums bounded a tile (8 x 65537 keys, 31 nodes, from L2: 272 us,
-    // of pairs 253).
+    // two buffers a tile, products that end late and the taking of their sums bounded a tile (8 x 65537 keys, 31 nodes, from L2: 272 us, of
+    // pairs 253; 255 since weights take the difference first).
     // So that references rise seldom, one lags up to 2^SLACK behind the maximum: weights reach 4 then.
     static constexpr int GROUP = F32 ? 1 : 2;
     static constexpr float SLACK = F32 ? 0.f : 2.f;
@@ -282,9 +283,9 @@ __device__ __forceinline__ bool finite16(uint32_t half) { return (half & 0x7F80u
 // tiles by four each), which replace them in TMEM as the A operand of P V; they hand the running maximum on. Warps 8 .. 11 add
 // the tiles' sums to those in their registers. Every wait is bounded.
 //
-// Measured: 8 x 65537 keys, 31 nodes 313 us, 6.9 TB/s: memory. 64 x 200..2000 keys, 64 nodes 71 us, 4.8 TB/s: 5 us until the first
+// Measured: 8 x 65537 keys, 31 nodes 309 us, 7.0 TB/s: memory. 64 x 200..2000 keys, 64 nodes 71 us, 4.8 TB/s: 5 us until the first
 // scores (one third of it instructions that come from L2), some 1400 cycles a tile, which memory needs too, 3 us at the end of each
-// piece and of the launch, 3 for the launch that merges. fp32, 8 x 16384 keys, 64 nodes 136 us: the tensor cores (24 products of 128 x 64 x 16 for the
+// piece and of the launch, 7 for the launch that merges (8 x 16384 keys, 31 nodes: 5). fp32, 8 x 16384 keys, 64 nodes 134 us: the tensor cores (24 products of 128 x 64 x 16 for the
 // scores of a tile, 12 of 128 x 128 x 16 for its sums, 2100 cycles).
 //
 // ONE: a share is a sequence, and none is cut.
@@ -1085,8 +1086,9 @@ __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
 
 // Shares of the launch: 8 blocks each, one an SM in all, or a tile a share where there are fewer. Few and short sequences are not cut, which
 // saves the deal and the launch that merges, as long as what a cut would take from the longest is worth fewer than 10 tiles (fp32: 5). bf16, 6
-// nodes: 1 x 333 keys 8.3 us (and 3 of the host's), in shares 8.9; 1 x 1200 14.9 and 11.9; 19 x 120..1200 15.5 and 18.3. fp32, 25 nodes: 1 x
-// 100 9.2 and 9.3, 1 x 320 12.1 and 10.3, 12 x 64..640 18.0 and 19.7. Up to 20 tiles: where only one sequence is long, it bounds all.
+// nodes: 1 x 333 keys 8.5 us (and 3 of the host's less), in shares 9.4; 1 x 600 10.6 and 10.8; 1 x 1200 15.6 and 11.5; 19 x 120..1200 16.5 and
+// 18.7. fp32, 25 nodes: 1 x 100 9.5 and 9.4, 1 x 320 12.4 and 10.4, 12 x 64..640 18.1 and 19.9. Up to 20 tiles: where only one sequence is
+// long, it bounds all.
 constexpr int ONE_TILES = 20;
 bool one_block(int B, int max_len, bool f32) {
     const int t = tiles_of(max_len);

@@ -710,7 +710,8 @@ tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int layer, int
  *   err      device word, or NULL
  * Masses are held to some 2^-46 of the 1 of a row for each rejected child of a node, whatever their own size (rows beyond 2^24 ids: to
  * a few bits fewer): the answers are those of exact arithmetic but where two masses lie that close to each other. What rejections
- * by a draft next to the target leave may itself be of the size of 2^-25. V at most 2^30, fp32 and int32 arrays 4-byte aligned. */
+ * by a draft next to the target leave may itself be of the size of 2^-25. V at most 2^30, fp32 and int32 arrays 4-byte aligned. Rows of
+ * target and draft that begin at different places of 16 bytes are read an id at a time: 64 x 151676 ids, 12 nodes 45 us instead of 40. */
 tts_bb_status tts_bb_tree_verify(int B, int N, int V, const int32_t* tokens, const int32_t* parents, const int32_t* n_nodes,
                                  const float* target, int64_t target_stride, const float* draft, int64_t draft_stride,
                                  const float* u, const float* u_next, int32_t* n_accepted, int32_t* path,
