@@ -968,7 +968,7 @@ __global__ void __launch_bounds__(NT, 1)
                         part[(HD / 4) * 128] = make_float4(m, l, 0.f, 0.f);
                     }
                 } else if (p.ok) {
-                    const float f = l == 0.f ? 0.f : 1.f / l;
+                    const float f = 1.f / l;  // l is 0 where all scores are -inf: NaN, as the formula's
                     const u64 f2 = pair(f, f), none = pair(-0.f, -0.f);
 #pragma unroll
                     for (int i = 0; i < HD / 2; ++i) o[i] = fma2(o[i], f2, none);
@@ -1073,7 +1073,7 @@ __global__ void __launch_bounds__(128) k_tree_combine(TreeArgs a, int shares) {
             for (int d = 0; d < 2; ++d) { o[d].x += f * x[i][d].x; o[d].y += f * x[i][d].y; o[d].z += f * x[i][d].z; o[d].w += f * x[i][d].w; }
         }
     }
-    const float f = l == 0.f ? 0.f : 1.f / l;
+    const float f = 1.f / l;
     T* const to = static_cast<T*>(a.out) + (((size_t)it * a.N + (r >> 1)) * NQ + 2 * g + (r & 1)) * HD + d0 * 4;
     if constexpr (std::is_same_v<T, float>) {
 #pragma unroll

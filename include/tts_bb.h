@@ -683,7 +683,8 @@ typedef struct {
  * out and the workspace overlap no input. Rows of out of padding and of skipped sequences are left as they were; keys behind a page out
  * of range are left out of the sums. What masked keys, places behind a sequence's keys and padding nodes hold does not matter, NaN and
  * infinities among it. Where the formula gives NaN or an infinity the number is one of the two; queries and keys of magnitudes up
- * to 1e18 and values up to 1e28 leave fp32 room for scores and sums. Results do not depend on the order in which blocks of the launch run. */
+ * to 1e18 and values up to 1e28 leave fp32 room for scores and sums; an infinite key that a node sees gives bf16 queries what
+ * the formula gives, fp32 ones that or NaN. Results do not depend on the order in which blocks of the launch run. */
 size_t tts_bb_tree_attention_workspace(int B, int N, int max_len);
 tts_bb_status tts_bb_tree_attention(const tts_bb_kv_cache* cache, int layer, int B, int N, const void* q, int type,
                                     int64_t q_stride, const void* k, const void* v, int64_t kv_stride,

@@ -294,6 +294,24 @@ def test_attention_of_large_and_small_scores(io):
 
 
 @IO
+@pytest.mark.parametrize("n", [70, 3000])
+def test_attention_of_infinite_keys(io, n):
+    """Scores of -inf: no weight beside others, NaN where a node sees nothing else. fp32 queries meet infinite keys in parts, whose signs may differ: or NaN."""
+    c = Case(29, [n], 4, io, parents=[[-1, 0, 1, -1]])
+    c.q.abs_()
+    c.pool[0, dev(c.table[0]).long()[torch.arange(n, device="cuda") // BLK], 0, :, torch.arange(n, device="cuda") % BLK, 0] = -np.inf
+    c.k[0][:, :, 0] = -np.inf
+    c.tk.view(4, NKV, HD)[3, :, 0] = -np.inf
+    out = c.run().double().cpu().numpy().reshape(4, NQ, HD)
+    assert np.isnan(out[3]).all()
+    w, mag, _ = c.want(0)
+    assert np.isnan(w[3]).all()
+    # scores of 128 products whose magnitudes add up to 200 at most, in fp32; bf16: weights in two parts, the result rounded
+    near = np.abs(out - w) <= mag * (2 * 136 * 200 * U / np.sqrt(HD) + 2.0 ** -15) + np.abs(w) * 2.0 ** -8
+    assert (near | (np.isnan(out).all(-1, keepdims=True) & (io == "float32")))[:3].all()
+
+
+@IO
 @pytest.mark.parametrize("N, lens", [(5, [100, 7]), (33, [5000, 130])])
 @pytest.mark.parametrize("size", [13, 15, 17, 30, 59])
 @pytest.mark.parametrize("shape", ["equal", "rising", "falling", "mixed"])
